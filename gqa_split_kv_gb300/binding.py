@@ -27,6 +27,15 @@ __all__ = [
     "decode_attn_int8_contig",
     "decode_attn_int8_paged",
     "decode_combine",
+    "rope_inv_freq",
+    "rope_apply",
+    "kv_write_contig",
+    "kv_write_paged",
+    "kv_write_int8_contig",
+    "kv_write_int8_paged",
+    "kv_read_paged",
+    "kv_read_int8_contig",
+    "kv_read_int8_paged",
     "device_error",
     "selftest_bounded_wait",
     "counters_len",
@@ -91,6 +100,21 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.decode_plan_pieces.restype = i
     lib.decode_max_batch.argtypes = [i, i, i, i, i, i]
     lib.decode_max_batch.restype = i
+    ll, d = ctypes.c_longlong, ctypes.c_double
+    rope = [vp, i, i, i, f]  # inv_freq, rot_offset, rot_dim, interleaved, magnitude
+    for name, args in {
+        "rope_inv_freq": [vp, i, d, i, d, d, d, d],
+        "rope_apply": [vp, vp, vp, vp, ll, i, i, i, i, i, f, i, i, ll, ll, ll, ll, vp],
+        "kv_write_contig": [vp, vp, ll, ll, vp, i, i, i, i, i, *rope, vp, vp, vp],
+        "kv_write_paged": [vp, vp, ll, ll, vp, vp, i, i, i, i, i, i, i, i, *rope, vp, vp, vp],
+        "kv_write_int8_contig": [vp, vp, ll, ll, vp, i, i, i, i, i, *rope, vp, vp, vp, vp, vp],
+        "kv_write_int8_paged": [vp, vp, ll, ll, vp, vp, i, i, i, i, i, i, i, i, *rope, vp, vp, vp, vp, vp],
+        "kv_read_paged": [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
+        "kv_read_int8_contig": [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp],
+        "kv_read_int8_paged": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
+    }.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
     if path is None:
         _lib = lib
     return lib
@@ -412,6 +436,262 @@ def decode_combine(part_acc, part_ml, out=None, stream=None):
     st = load().decode_combine(_ptr(part_acc), _ptr(part_ml), B, Hq, D, S, _ptr(out), _stream(stream))
     _check("decode_combine", st)
     return out
+
+
+# ---------------------------------------------------------------- rotary positions and caches
+
+_ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                  original_ctx: float = 4096, low_turns: float = 1.0, high_turns: float = 32.0, device=None):
+    """Radians a position of each of the rot_dim / 2 rotated pairs: a float64 tensor on device (default: the
+    current CUDA device) for rope_apply and kv_write_*.  scaling "plain", "linear", "base" or "by_parts"
+    (include/decode_attn.h, da_rope_scaling)."""
+    import numpy as np
+    import torch
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling: expected one of {sorted(_ROPE_SCALING)}, got {scaling!r}")
+    w = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    _check("rope_inv_freq", load().rope_inv_freq(w.ctypes.data, int(rot_dim), float(base), _ROPE_SCALING[scaling],
+                                                 float(factor), float(original_ctx), float(low_turns),
+                                                 float(high_turns)))
+    return torch.from_numpy(w).to("cuda" if device is None else device)
+
+
+def _here(*tensors):
+    """The current device's index; every tensor (None: skipped) must be on it."""
+    import torch
+    at = {t.get_device() for t in tensors if t is not None}
+    if -1 in at or at != {torch.cuda.current_device()}:
+        raise ValueError("expected every tensor on the current CUDA device, got "
+                         f"{[str(t.device) for t in tensors if t is not None]}")
+    return at.pop()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _shape(t, name, *want):
+    """t's shape: every entry of want that is not None must match."""
+    if t.dim() != len(want) or any(w is not None and w != n for w, n in zip(want, t.shape)):
+        raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in want)}, "
+                         f"got {tuple(t.shape)}")
+
+
+def _plain(t, name, dtype, *want):
+    """A contiguous tensor of this type and shape."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor, got {t.dtype}, strides {t.stride()}")
+    _shape(t, name, *want)
+
+
+def _token_stride(t, name, lead: int):
+    """Elements from one token to the next of t [.., H, D] (lead leading dims that are one run of tokens); the
+    elements of a head are consecutive."""
+    st, sh = t.stride(), t.shape
+    ok = st[-1] == 1 or sh[-1] == 1
+    if lead == 2 and sh[0] > 1 and sh[1] > 0:
+        if sh[1] > 1 and st[0] != sh[1] * st[1]:
+            ok = False
+        step = st[1] if sh[1] > 1 else st[0]
+    else:
+        step = st[lead - 1]
+    if not ok:
+        raise ValueError(f"{name}: tokens must be equally far apart and a head's elements consecutive, "
+                         f"got strides {st} of shape {tuple(sh)}")
+    return step
+
+
+def rope_apply(x, positions, inv_freq, offset: int = 0, interleaved: bool = False, magnitude: float = 1.0,
+               backward: bool = False, out=None, stream=None):
+    """Rotary positions: x [T, H, D] or [B, T, H, D] (bf16, fp16 or fp32; tokens and heads may be strided),
+    positions int32 [T] or [B, T], inv_freq float64 [rot / 2] (rope_inv_freq).  Elements [offset, offset + rot)
+    of every head are rotated, pairs (j, j + rot / 2) or, interleaved, (2j, 2j + 1); with backward, the gradient
+    of that.  out: x itself (in place) or a tensor of x's shape.  Returns out."""
+    import torch
+    dtype = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(x.dtype)
+    if dtype is None or x.dim() not in (3, 4):
+        raise ValueError(f"x: expected bf16, fp16 or fp32 [T, H, D] or [B, T, H, D], got {x.dtype} {tuple(x.shape)}")
+    _plain(positions, "positions", torch.int32, *x.shape[:-2])
+    _plain(inv_freq, "inv_freq", torch.float64, None)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
+    lead = x.dim() - 2
+    H, D = x.shape[-2:]
+    xt, ot = _token_stride(x, "x", lead), _token_stride(out, "out", lead)
+    dev = _here(x, positions, inv_freq, out)
+    _check("rope_apply", load().rope_apply(
+        x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), positions.numel(), H, D, offset,
+        2 * inv_freq.shape[0], int(interleaved), magnitude, int(backward), dtype, xt, x.stride(-2), ot,
+        out.stride(-2), _raw_stream(stream, dev)))
+    return out
+
+
+def _rope_args(inv_freq, offset, interleaved, magnitude):
+    import torch
+    if inv_freq is None:
+        return None, 0, 0, 0, 1.0
+    _plain(inv_freq, "inv_freq", torch.float64, None)
+    return inv_freq.data_ptr(), offset, 2 * inv_freq.shape[0], int(interleaved), magnitude
+
+
+def _new_tokens(k_new, v_new, v):
+    """Checks the new tokens [B, q_len, Hkv, D] (v_new None with v None); returns their token strides."""
+    import torch
+    if (v_new is None) != (v is None):
+        raise ValueError("v_new and v: both tensors, or both None to write keys only")
+    strides = []
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        if t is None:
+            strides.append(0)
+            continue
+        if t.dtype != torch.bfloat16 or t.dim() != 4:
+            raise ValueError(f"{name}: expected bf16 [B, q_len, Hkv, D], got {t.dtype} {tuple(t.shape)}")
+        if t.shape[2] > 1 and t.stride(2) != t.shape[3]:
+            raise ValueError(f"{name}: a token's heads must be consecutive, got strides {t.stride()}")
+        _shape(t, name, *k_new.shape)
+        step = _token_stride(t, name, 2)
+        strides.append(step if t.shape[0] * t.shape[1] > 1 else t.shape[2] * t.shape[3])
+    return strides
+
+
+def _check_cache(k, v, k_scale, v_scale, seq_lens, B, H, D, page_table):
+    """Checks a cache against the call's batch and heads; returns (rows of a slab, page-table columns)."""
+    import torch
+    dtype = torch.bfloat16 if k_scale is None else torch.int8
+    slabs, slab = k.shape[:2] if k.dim() == 4 else (None, None)
+    if page_table is None:
+        slabs = B
+    else:
+        _plain(page_table, "page_table", torch.int32, B, None)
+    for t, s, name in ((k, k_scale, "k"), (v, v_scale, "v")):
+        if t is None:
+            continue
+        _plain(t, name, dtype, slabs, slab, H, D)
+        if dtype == torch.int8:
+            if s is None:
+                raise ValueError(f"{name}: an int8 cache needs its scales")
+            _plain(s, f"{name}_scale", torch.float32, slabs, H, slab)
+    if seq_lens is not None:
+        _plain(seq_lens, "seq_lens", torch.int32, B)
+    elif page_table is not None:
+        raise ValueError("seq_lens: a paged cache needs them")
+    return slab, None if page_table is None else page_table.shape[1]
+
+
+def _kv_write(fn, k_new, v_new, k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, inv_freq, offset,
+              interleaved, magnitude, stream):
+    ks, vs = _new_tokens(k_new, v_new, v)
+    B, n, H, D = k_new.shape
+    slab, cols = _check_cache(k, v, k_scale, v_scale, seq_lens, B, H, D, page_table)
+    dev = _here(k_new, v_new, k, v, k_scale, v_scale, page_table, seq_lens, inv_freq)
+    where = (slab,) if page_table is None else (slab, cols, k.shape[0], int(max_seq_len))
+    table = () if page_table is None else (page_table.data_ptr(),)
+    scales = () if k_scale is None else (k_scale.data_ptr(), _addr(v_scale))
+    _check(fn, getattr(load(), fn)(k_new.data_ptr(), _addr(v_new), ks, vs, *table, _addr(seq_lens), B, n, H, D, *where,
+                                   *_rope_args(inv_freq, offset, interleaved, magnitude), k.data_ptr(), _addr(v),
+                                   *scales, _raw_stream(stream, dev)))
+
+
+def kv_write_contig(k_new, v_new, k, v, seq_lens=None, inv_freq=None, offset: int = 0, interleaved: bool = False,
+                    magnitude: float = 1.0, stream=None):
+    """Writes the last q_len tokens of every sequence, k_new/v_new bf16 [B, q_len, Hkv, D], into the bf16 cache k/v
+    [B, max_ctx, Hkv, D]; seq_lens int32 [B] (with the new tokens) or None.  inv_freq: rotate the keys at their
+    positions first (rope_apply).  v_new and v may both be None (keys only)."""
+    _kv_write("kv_write_contig", k_new, v_new, k, v, None, None, None, seq_lens, 0, inv_freq, offset, interleaved,
+              magnitude, stream)
+
+
+def kv_write_paged(k_new, v_new, k_pool, v_pool, page_table, seq_lens, max_seq_len: int, inv_freq=None,
+                   offset: int = 0, interleaved: bool = False, magnitude: float = 1.0, stream=None):
+    """kv_write_contig into page pools [num_pages, page_size, Hkv, D]; page_table int32 [B, max_pages]."""
+    _kv_write("kv_write_paged", k_new, v_new, k_pool, v_pool, None, None, page_table, seq_lens, max_seq_len, inv_freq,
+              offset, interleaved, magnitude, stream)
+
+
+def kv_write_int8_contig(k_new, v_new, k_i8, v_i8, k_scale, v_scale, seq_lens=None, inv_freq=None, offset: int = 0,
+                         interleaved: bool = False, magnitude: float = 1.0, stream=None):
+    """kv_write_contig into an int8 cache: k_i8/v_i8 int8 [B, max_ctx, Hkv, D], k_scale/v_scale fp32
+    [B, Hkv, max_ctx]; every (token, head) row is quantised by its largest magnitude."""
+    if k_scale is None:
+        raise ValueError("k: an int8 cache needs its scales")
+    _kv_write("kv_write_int8_contig", k_new, v_new, k_i8, v_i8, k_scale, v_scale, None, seq_lens, 0, inv_freq, offset,
+              interleaved, magnitude, stream)
+
+
+def kv_write_int8_paged(k_new, v_new, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens,
+                        max_seq_len: int, inv_freq=None, offset: int = 0, interleaved: bool = False,
+                        magnitude: float = 1.0, stream=None):
+    """kv_write_int8_contig into page pools; scale pools fp32 [num_pages, Hkv, page_size]."""
+    if k_scale_pool is None:
+        raise ValueError("k: an int8 cache needs its scales")
+    _kv_write("kv_write_int8_paged", k_new, v_new, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table,
+              seq_lens, max_seq_len, inv_freq, offset, interleaved, magnitude, stream)
+
+
+def _kv_read(fn, k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, n_tokens, starts, k_out, v_out, stream):
+    import torch
+    if k.dim() != 4:
+        raise ValueError(f"k: expected 4 dims, got {tuple(k.shape)}")
+    B = k.shape[0] if page_table is None else page_table.shape[0]
+    H, D = k.shape[2:]
+    n = int(n_tokens)
+    slab, cols = _check_cache(k, v, k_scale, v_scale, seq_lens, B, H, D, page_table)
+    if starts is not None:
+        _plain(starts, "starts", torch.int32, B)
+    if k_out is None:
+        k_out = torch.zeros((B, n, H, D), dtype=torch.bfloat16, device=k.device)
+    if v_out is None and v is not None:
+        v_out = torch.zeros((B, n, H, D), dtype=torch.bfloat16, device=k.device)
+    _plain(k_out, "k_out", torch.bfloat16, B, n, H, D)
+    if v is None:
+        if v_out is not None:
+            raise ValueError("v_out: no v to read")
+    else:
+        _plain(v_out, "v_out", torch.bfloat16, B, n, H, D)
+    dev = _here(k, v, k_scale, v_scale, page_table, seq_lens, starts, k_out, v_out)
+    where = (slab,) if page_table is None else (slab, cols, k.shape[0], int(max_seq_len))
+    table = () if page_table is None else (page_table.data_ptr(),)
+    scales = () if k_scale is None else (k_scale.data_ptr(), _addr(v_scale))
+    _check(fn, getattr(load(), fn)(k.data_ptr(), _addr(v), *scales, *table, _addr(starts), _addr(seq_lens), B, n, H, D,
+                                   *where, k_out.data_ptr(), _addr(v_out), _raw_stream(stream, dev)))
+    return k_out, v_out
+
+
+def kv_read_paged(k_pool, v_pool, page_table, seq_lens, max_seq_len: int, n_tokens: int, starts=None, k_out=None,
+                  v_out=None, stream=None):
+    """Tokens [starts[b], starts[b] + n_tokens) (starts int32 [B]; None: 0) of every sequence of a paged bf16 cache
+    as contiguous bf16 [B, n_tokens, Hkv, D]: (k_out, v_out), v_out None with v_pool None.  Rows past a sequence
+    are left as they were (zeros in outputs made here)."""
+    return _kv_read("kv_read_paged", k_pool, v_pool, None, None, page_table, seq_lens, max_seq_len, n_tokens, starts,
+                    k_out, v_out, stream)
+
+
+def kv_read_int8_contig(k_i8, v_i8, k_scale, v_scale, seq_lens, n_tokens: int, starts=None, k_out=None, v_out=None,
+                        stream=None):
+    """kv_read_paged of a contiguous int8 cache (seq_lens may be None): value = int8 * scale, rounded to bf16."""
+    if k_scale is None:
+        raise ValueError("k: an int8 cache needs its scales")
+    return _kv_read("kv_read_int8_contig", k_i8, v_i8, k_scale, v_scale, None, seq_lens, 0, n_tokens, starts, k_out,
+                    v_out, stream)
+
+
+def kv_read_int8_paged(k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens, max_seq_len: int,
+                       n_tokens: int, starts=None, k_out=None, v_out=None, stream=None):
+    """kv_read_paged of an int8 cache: value = int8 * scale, rounded to bf16."""
+    if k_scale_pool is None:
+        raise ValueError("k: an int8 cache needs its scales")
+    return _kv_read("kv_read_int8_paged", k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens,
+                    max_seq_len, n_tokens, starts, k_out, v_out, stream)
 
 
 def selftest_bounded_wait(timeout_ns: int, stream=None) -> None:

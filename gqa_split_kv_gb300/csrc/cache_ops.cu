@@ -1,0 +1,698 @@
+// Entry points around the caches (declared in include/decode_attn.h): rotary
+// positions, writing new tokens into a cache (bf16 or quantised to int8) and reading a
+// cache back as contiguous bf16.  All three move bytes: HBM (or, for a decode step's
+// few tokens, the launch) bounds them, so every kernel is one pass with 16-byte
+// accesses and the arithmetic between the load and the store.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/decode_attn.h"
+#include "device_error.cuh"
+#include "host_util.cuh"
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace da {
+
+int take_cache_error_word(unsigned int* flags) { return take_unit_error_word(flags); }
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRot = 2048;       // rotated elements of a head (cosines and sines sit in shared memory)
+constexpr int kRopeSmem = 32 * 1024;
+
+// ---------------------------------------------------------------- rope_apply
+
+struct RopeApplyParams {
+  RopeParams r;
+  const void* x;
+  void* out;
+  const int* positions;
+  long long tokens;
+  int H, D;
+  long long xt, xh, ot, oh;  // strides in elements
+  int copy;                  // out is not x: elements outside the rotated part are copied
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T>
+union Chunk {  // 16 bytes
+  uint4 raw;
+  T v[16 / sizeof(T)];
+};
+
+// One CTA a token at a time: its rot / 2 cosines and sines go to shared memory once
+// and serve every head.  VECTOR: all offsets and strides are whole 16-byte chunks; an
+// item is a chunk (interleaved: whole pairs; a copy) or the two chunks that hold the
+// halves of the same pairs.  Otherwise an item is one pair or one copied element.
+template <typename T, bool VECTOR>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p) {
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  const int np = p.r.rot / 2;
+  unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
+  float2* cs = reinterpret_cast<float2*>(step + np);
+  for (int j = threadIdx.x; j < np; j += kThreads) step[j] = rope_turn_step(p.r.inv_freq[j]);
+  constexpr int V = VECTOR ? 16 / (int)sizeof(T) : 1;
+  // items of one head: the rotated ones first, then the copies
+  const int nrot = VECTOR && p.r.interleaved ? p.r.rot / V : np / V;
+  const int ncopy = p.copy ? (p.D - p.r.rot) / V : 0;
+  const int per_head = nrot + ncopy;
+  const int lo = p.r.offset / V;  // copied items before the rotated part
+  for (long long t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    const int pos = __ldg(p.positions + t);
+    __syncthreads();  // step is written; the last token's cosines are read
+    for (int j = threadIdx.x; j < np; j += kThreads) cs[j] = rope_cos_sin(step[j], pos, p.r);
+    __syncthreads();
+    const T* x = static_cast<const T*>(p.x) + t * p.xt;
+    T* out = static_cast<T*>(p.out) + t * p.ot;
+    for (int e = threadIdx.x; e < p.H * per_head; e += kThreads) {
+      const int h = e / per_head, k = e - h * per_head;
+      const T* xh = x + h * p.xh;
+      T* oh = out + h * p.oh;
+      if (k >= nrot) {
+        const int c = k - nrot;
+        const int at = (c < lo ? c : c + p.r.rot / V) * V;
+        if constexpr (VECTOR)
+          *reinterpret_cast<uint4*>(oh + at) = *reinterpret_cast<const uint4*>(xh + at);
+        else
+          oh[at] = xh[at];
+        continue;
+      }
+      if constexpr (VECTOR) {
+        if (p.r.interleaved) {
+          const int at = p.r.offset + k * V;
+          Chunk<T> a;
+          a.raw = *reinterpret_cast<const uint4*>(xh + at);
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const float2 w = cs[k * (V / 2) + i / 2];
+            const float u = to_f32(a.v[i]), v = to_f32(a.v[i + 1]);
+            a.v[i] = from_f32<T>(u * w.x - v * w.y);
+            a.v[i + 1] = from_f32<T>(u * w.y + v * w.x);
+          }
+          *reinterpret_cast<uint4*>(oh + at) = a.raw;
+        } else {
+          const int at = p.r.offset + k * V;
+          Chunk<T> a, b;
+          a.raw = *reinterpret_cast<const uint4*>(xh + at);
+          b.raw = *reinterpret_cast<const uint4*>(xh + at + np);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float2 w = cs[k * V + i];
+            const float u = to_f32(a.v[i]), v = to_f32(b.v[i]);
+            a.v[i] = from_f32<T>(u * w.x - v * w.y);
+            b.v[i] = from_f32<T>(u * w.y + v * w.x);
+          }
+          *reinterpret_cast<uint4*>(oh + at) = a.raw;
+          *reinterpret_cast<uint4*>(oh + at + np) = b.raw;
+        }
+      } else {
+        const int at = p.r.offset + (p.r.interleaved ? 2 * k : k), bt = at + (p.r.interleaved ? 1 : np);
+        const float2 w = cs[k];
+        const float u = to_f32(xh[at]), v = to_f32(xh[bt]);
+        oh[at] = from_f32<T>(u * w.x - v * w.y);
+        oh[bt] = from_f32<T>(u * w.y + v * w.x);
+      }
+    }
+  }
+}
+
+template <typename T>
+int launch_rope(const RopeApplyParams& p, int sms, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int half = p.r.interleaved ? p.r.rot : p.r.rot / 2;
+  const bool vec = aligned(p.x, 16) && aligned(p.out, 16) && p.D % V == 0 && p.r.offset % V == 0 && half % V == 0 &&
+                   p.r.rot % V == 0 && p.xt % V == 0 && p.xh % V == 0 && p.ot % V == 0 && p.oh % V == 0;
+  const size_t smem = (size_t)(p.r.rot / 2) * 16;
+  const long long cap = 8LL * sms;  // 2048 threads an SM
+  const unsigned grid = (unsigned)(p.tokens < cap ? p.tokens : cap);
+  if (vec)
+    rope_kernel<T, true><<<grid, kThreads, smem, st>>>(p);
+  else
+    rope_kernel<T, false><<<grid, kThreads, smem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int rope_check(const double* inv_freq, int head_dim, int offset, int rot, int interleaved, float magnitude) {
+  if (!inv_freq || !aligned(inv_freq, 8) || rot < 2 || rot % 2 || offset < 0 || (long long)offset + rot > head_dim ||
+      (interleaved != 0 && interleaved != 1) || !std::isfinite(magnitude))
+    return DA_ERR_INVALID_ARG;
+  return rot > kMaxRot ? DA_ERR_UNSUPPORTED : DA_OK;
+}
+
+// [T, H, D] with these strides: whether two (token, head) rows can share an element.
+bool rows_apart(long long T, long long H, long long D, long long st, long long sh) {
+  if (T <= 1) st = 0;
+  if (H <= 1) sh = 0;
+  const bool th = (H <= 1 || sh >= D) && (T <= 1 || st >= (H - 1) * sh + D);
+  const bool ht = (T <= 1 || st >= D) && (H <= 1 || sh >= (T - 1) * st + D);
+  return th || ht;
+}
+
+// ---------------------------------------------------------------- the caches
+
+struct CacheParams {
+  RopeParams r;
+  const void *k_new, *v_new;  // write: the new tokens; read: the outputs
+  void *k_out, *v_out;
+  void *k, *v;                // the cache
+  float *ks, *vs;             // int8: its scales, [B or pages, Hkv, max_ctx or page_size]
+  const int *seq_lens, *starts, *page_table;
+  long long k_stride, v_stride;  // write: elements between new tokens
+  int B, n, Hkv, D;           // n: tokens a sequence of this call
+  int cap;                    // tokens a sequence has room for
+  int slab;                   // rows of one batch entry or page: max_ctx or page_size
+  int max_pages, num_pages;
+  int tb;                     // tokens a CTA takes at a time
+  int lanes;                  // write: lanes a row (a power of two)
+};
+
+// The cache row (in tokens) of sequence b's position t, or -1 when its page is not in
+// the pool (flagged); slab_index and in_slab address its scale.
+template <bool PAGED>
+__device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int t, long long& slab_index,
+                                               int& in_slab) {
+  if (!PAGED) {
+    slab_index = b;
+    in_slab = t;
+  } else {
+    const int col = t / p.slab;
+    const int page = __ldg(p.page_table + (size_t)b * p.max_pages + col);
+    if ((unsigned)page >= (unsigned)p.num_pages) {
+      atomicOr(&g_error_word, 4u);
+      return -1;
+    }
+    slab_index = page;
+    in_slab = t - col * p.slab;
+  }
+  return slab_index * p.slab + in_slab;
+}
+
+__device__ __forceinline__ void unpack8(uint4 w, float (&f)[8]) {
+  f[0] = bf16lo_to_f32(w.x);
+  f[1] = bf16hi_to_f32(w.x);
+  f[2] = bf16lo_to_f32(w.y);
+  f[3] = bf16hi_to_f32(w.y);
+  f[4] = bf16lo_to_f32(w.z);
+  f[5] = bf16hi_to_f32(w.z);
+  f[6] = bf16lo_to_f32(w.w);
+  f[7] = bf16hi_to_f32(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
+// A CTA takes tb new tokens at a time.  A row (token, tensor, head) of D elements has
+// `lanes` lanes of one warp, CPL chunks of 8 elements each.  K rows are rotated in fp32
+// on the way (a half-layout lane also loads the chunk with the other halves of its
+// pairs: an L1 hit) and int8 rows quantised from that fp32 value, so a key is rounded
+// once.  The row's maximum is a shuffle over its lanes.
+template <bool PAGED, bool INT8, int CPL>
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p) {
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  const int np = p.r.inv_freq ? p.r.rot / 2 : 0;
+  unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
+  float2* cs = reinterpret_cast<float2*>(step + np);  // [tb][np]
+  for (int j = threadIdx.x; j < np; j += kThreads) step[j] = rope_turn_step(p.r.inv_freq[j]);
+  const long long total = (long long)p.B * p.n;
+  const int rows_per_token = p.Hkv * (p.v ? 2 : 1);
+  const int rows = p.tb * rows_per_token;
+  const int nchunk = p.D / 8, gl = threadIdx.x & (p.lanes - 1);
+  // position of new token g = b n + i: L_b - n + i
+  auto position = [&](long long g, int& b) -> long long {
+    b = (int)(g / p.n);
+    const int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
+    return (long long)L - p.n + (g - (long long)b * p.n);
+  };
+  for (long long g0 = (long long)blockIdx.x * p.tb; g0 < total; g0 += (long long)gridDim.x * p.tb) {
+    if (np) {
+      __syncthreads();
+      for (int e = threadIdx.x; e < p.tb * np; e += kThreads) {
+        const long long g = g0 + e / np;
+        if (g < total) {
+          int b;
+          cs[e] = rope_cos_sin(step[e % np], (int)position(g, b), p.r);
+        }
+      }
+      __syncthreads();
+    }
+    // every lane of a warp runs the same number of rounds (the shuffles need them all)
+    const int per_round = kThreads / p.lanes;
+    for (int r0 = 0; r0 < rows; r0 += per_round) {
+      const int row = r0 + threadIdx.x / p.lanes;
+      const int ti = row / rows_per_token, in_token = row - ti * rows_per_token;
+      const bool is_v = in_token >= p.Hkv;
+      const int h = is_v ? in_token - p.Hkv : in_token;
+      const long long g = g0 + ti;
+      long long slab = 0, dst = -1;
+      int in_slab = 0;
+      if (row < rows && g < total) {
+        int b;
+        const long long pos = position(g, b);
+        if (pos >= p.cap) {
+          atomicOr(&g_error_word, 8u);
+        } else if (pos >= 0) {
+          dst = cache_row<PAGED>(p, b, (int)pos, slab, in_slab);
+        }
+      }
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) +
+                                 (dst < 0 ? 0 : g * (is_v ? p.v_stride : p.k_stride) + (long long)h * p.D);
+      float x[CPL][8];
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        const int ch = gl + c * p.lanes;
+        if (dst >= 0 && ch < nchunk) {
+          unpack8(__ldg(reinterpret_cast<const uint4*>(src) + ch), x[c]);
+          const int at = ch * 8 - p.r.offset;  // within the rotated part
+          if (np && !is_v && at >= 0 && at < p.r.rot) {
+            const float2* w = cs + ti * np;
+            if (p.r.interleaved) {
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                const float2 a = w[(at + i) / 2];
+                const float u = x[c][i], v = x[c][i + 1];
+                x[c][i] = u * a.x - v * a.y;
+                x[c][i + 1] = u * a.y + v * a.x;
+              }
+            } else {
+              const bool second = at >= np;
+              const int j = second ? at - np : at;
+              float o[8];  // the other halves of these pairs
+              unpack8(__ldg(reinterpret_cast<const uint4*>(src + p.r.offset + (second ? j : j + np))), o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 a = w[j + i];
+                x[c][i] = second ? o[i] * a.y + x[c][i] * a.x : x[c][i] * a.x - o[i] * a.y;
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] = 0.f;
+        }
+      }
+      if constexpr (INT8) {
+        // largest magnitude; a NaN anywhere makes it NaN (fmaxf would drop it), so the
+        // row's scale and everything read back from it are NaN
+        float top = 0.f;
+        bool nan = false;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            top = fmaxf(top, fabsf(x[c][i]));
+            nan |= x[c][i] != x[c][i];
+          }
+        if (nan) top = __int_as_float(0x7f800000);
+        for (int o = p.lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool finite = top < __int_as_float(0x7f800000);
+        // 127 2^-126 and less would leave a scale below the normal numbers: floor it
+        float scale = top > 0.f ? fmaxf(__fdiv_rn(top, 127.f), 1.17549435e-38f) : 1.f;
+        if (!finite) scale = __int_as_float(0x7fffffff);
+        if (dst >= 0) {
+          int8_t* q = static_cast<int8_t*>(is_v ? p.v : p.k) + (dst * p.Hkv + h) * p.D;
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) {
+            const int ch = gl + c * p.lanes;
+            if (ch >= nchunk) continue;
+            uint32_t w[2] = {0u, 0u};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int v = finite ? max(-127, min(127, __float2int_rn(__fdiv_rn(x[c][i], scale)))) : 0;
+              w[i / 4] |= (uint32_t)(v & 255) << (8 * (i % 4));
+            }
+            *reinterpret_cast<uint2*>(q + ch * 8) = make_uint2(w[0], w[1]);
+          }
+          if (gl == 0) (is_v ? p.vs : p.ks)[(slab * p.Hkv + h) * p.slab + in_slab] = scale;
+        }
+      } else if (dst >= 0) {
+        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) + (dst * p.Hkv + h) * p.D;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          const int ch = gl + c * p.lanes;
+          if (ch < nchunk) *reinterpret_cast<uint4*>(q + ch * 8) = pack8(x[c]);
+        }
+      }
+    }
+  }
+}
+
+// A CTA reads tb consecutive tokens of one sequence, 16 elements a thread and step.
+template <bool PAGED, bool INT8>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) {
+  const int nblk = (p.n + p.tb - 1) / p.tb;
+  const int b = blockIdx.x / nblk, i0 = (blockIdx.x - b * nblk) * p.tb;
+  int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
+  L = min(L, p.cap);
+  const int start = p.starts ? __ldg(p.starts + b) : 0;
+  constexpr int E = INT8 ? 16 : 8;  // elements of a 16-byte load
+  const int per_row = p.Hkv * p.D / E, per_head = p.D / E;
+  const int ntok = min(p.tb, p.n - i0);
+  for (int e = threadIdx.x; e < ntok * per_row; e += kThreads) {
+    const int ti = e / per_row, c = e - ti * per_row;
+    const long long t = (long long)start + i0 + ti;
+    if (t < 0 || t >= L) continue;
+    long long slab;
+    int in_slab;
+    const long long row = cache_row<PAGED>(p, b, (int)t, slab, in_slab);
+    if (row < 0) continue;
+    const size_t dst = ((size_t)b * p.n + i0 + ti) * per_row + c;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      void* out = kv ? p.v_out : p.k_out;
+      if (kv && !out) break;
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(kv ? p.v : p.k) + row * per_row + c);
+      if constexpr (!INT8) {
+        reinterpret_cast<uint4*>(out)[dst] = w;
+      } else {
+        const float s = __ldg((kv ? p.vs : p.ks) + (slab * p.Hkv + c / per_head) * p.slab + in_slab);
+        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[2 * i] = pack_bf16x2((float)(int8_t)(q[i]) * s, (float)(int8_t)(q[i] >> 8) * s);
+          o[2 * i + 1] = pack_bf16x2((float)(int8_t)(q[i] >> 16) * s, (float)(int8_t)(q[i] >> 24) * s);
+        }
+        uint4* d = reinterpret_cast<uint4*>(out) + 2 * dst;
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+  }
+}
+
+int check_cache(const CacheParams& p, bool paged, bool int8, long long cap) {
+  if (p.B < 0 || p.n < 0 || p.Hkv <= 0 || p.D <= 0 || cap < 0) return DA_ERR_INVALID_ARG;
+  if (p.D % (int8 ? 16 : 8) || p.D > 1024 || p.Hkv > 1024 || cap > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  if (paged && (p.slab <= 0 || p.max_pages < 0 || p.num_pages < 0)) return DA_ERR_INVALID_ARG;
+  if ((long long)p.B * p.n > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+int check_cache_pointers(const CacheParams& p, bool paged, bool int8) {
+  if (!p.k || !aligned(p.k, 16) || !aligned(p.v, 16)) return DA_ERR_INVALID_ARG;
+  if (int8 && (!p.ks || !aligned(p.ks, 4) || (p.v && (!p.vs || !aligned(p.vs, 4))))) return DA_ERR_INVALID_ARG;
+  if (paged && (!p.page_table || !p.seq_lens || !aligned(p.page_table, 4))) return DA_ERR_INVALID_ARG;
+  if (!aligned(p.seq_lens, 4) || !aligned(p.starts, 4)) return DA_ERR_INVALID_ARG;
+  return DA_OK;
+}
+
+template <bool PAGED, bool INT8>
+int launch_write(CacheParams& p, int sms, cudaStream_t st) {
+  const int nchunk = p.D / 8;
+  p.lanes = 1;
+  while (p.lanes < nchunk && p.lanes < 32) p.lanes *= 2;
+  const int rows = p.Hkv * (p.v ? 2 : 1), np = p.r.inv_freq ? p.r.rot / 2 : 0;
+  // enough tokens that every lane has a row, as long as their cosines fit
+  p.tb = kThreads / (rows * p.lanes);
+  const int room = np ? kRopeSmem / (8 * np) - 1 : 16;
+  p.tb = p.tb > 16 ? 16 : p.tb;
+  p.tb = p.tb > room ? room : p.tb;
+  p.tb = p.tb < 1 ? 1 : p.tb;
+  const long long blocks = ((long long)p.B * p.n + p.tb - 1) / p.tb, cap = 8LL * sms;
+  const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
+  const size_t smem = (size_t)np * 8 * (1 + p.tb);
+  if (nchunk <= 32)
+    kv_write_kernel<PAGED, INT8, 1><<<grid, kThreads, smem, st>>>(p);
+  else
+    kv_write_kernel<PAGED, INT8, 4><<<grid, kThreads, smem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int write_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t st) {
+  if (int e = check_cache(p, paged, int8, cap)) return e;
+  p.cap = (int)cap;
+  if (p.r.inv_freq) {
+    if (int e = rope_check(p.r.inv_freq, p.D, p.r.offset, p.r.rot, p.r.interleaved, p.r.magnitude)) return e;
+    if (p.r.offset % 8 || p.r.rot % 16) return DA_ERR_UNSUPPORTED;  // whole chunks of 8, in either layout
+  }
+  if (p.B == 0 || p.n == 0) return DA_OK;
+  const long long width = (long long)p.Hkv * p.D;
+  if (!p.k_new || !aligned(p.k_new, 16) || !p.v_new != !p.v || !aligned(p.v_new, 16)) return DA_ERR_INVALID_ARG;
+  if (p.k_stride < width || p.k_stride % 8 || (p.v && (p.v_stride < width || p.v_stride % 8)))
+    return DA_ERR_INVALID_ARG;
+  if (int e = check_cache_pointers(p, paged, int8)) return e;
+  int dev, sms, optin;
+  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
+  if (paged) return int8 ? launch_write<true, true>(p, sms, st) : launch_write<true, false>(p, sms, st);
+  return int8 ? launch_write<false, true>(p, sms, st) : launch_write<false, false>(p, sms, st);
+}
+
+int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t st) {
+  if (int e = check_cache(p, paged, int8, cap)) return e;
+  p.cap = (int)cap;
+  if (p.B == 0 || p.n == 0) return DA_OK;
+  if (!p.k_out || !aligned(p.k_out, 16) || !p.v_out != !p.v || !aligned(p.v_out, 16)) return DA_ERR_INVALID_ARG;
+  if (int e = check_cache_pointers(p, paged, int8)) return e;
+  // about 8 loads of 16 bytes a thread
+  const int per_row = p.Hkv * p.D / (int8 ? 16 : 8);
+  const int tb = kThreads * 4 / per_row;
+  p.tb = tb < 1 ? 1 : tb > 64 ? 64 : tb;
+  const long long grid = (long long)p.B * ((p.n + p.tb - 1) / p.tb);
+  if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  if (paged && int8)
+    kv_read_kernel<true, true><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  else if (paged)
+    kv_read_kernel<true, false><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  else
+    kv_read_kernel<false, true><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+long long paged_cap(int page_size, int max_pages, int max_seq_len) {
+  if (max_seq_len < 0 || page_size <= 0 || max_pages < 0) return -1;
+  const long long room = (long long)max_pages * page_size;
+  return room < max_seq_len ? room : max_seq_len;
+}
+
+}  // namespace
+}  // namespace da
+
+using namespace da;
+
+extern "C" int rope_inv_freq(double* inv_freq, int rot_dim, double base, int scaling, double factor,
+                             double original_ctx, double low_turns, double high_turns) {
+  const double two_pi = 6.283185307179586476925;
+  if (!inv_freq || rot_dim < 2 || rot_dim % 2 || !(base > 1.0) || !std::isfinite(base)) return DA_ERR_INVALID_ARG;
+  if (scaling < DA_ROPE_PLAIN || scaling > DA_ROPE_BY_PARTS) return DA_ERR_UNSUPPORTED;
+  if (scaling != DA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return DA_ERR_INVALID_ARG;
+  if (scaling == DA_ROPE_BASE && rot_dim == 2) return DA_ERR_INVALID_ARG;  // one pair, of frequency 1 under any base
+  if (scaling == DA_ROPE_BY_PARTS && (!(original_ctx > 0) || !std::isfinite(original_ctx) || !(low_turns >= 0) ||
+                                      !(high_turns > low_turns) || !std::isfinite(high_turns)))
+    return DA_ERR_INVALID_ARG;
+  if (scaling == DA_ROPE_BASE) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double w = std::pow(base, -2.0 * j / rot_dim);
+    if (scaling == DA_ROPE_LINEAR) w /= factor;
+    if (scaling == DA_ROPE_BY_PARTS) {
+      const double turns = original_ctx * w / two_pi;
+      double keep = (turns - low_turns) / (high_turns - low_turns);
+      keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
+      w = w * keep + w / factor * (1.0 - keep);
+    }
+    inv_freq[j] = w;
+  }
+  return DA_OK;
+}
+
+extern "C" int rope_apply(const void* x, void* out, const int* positions, const double* inv_freq, long long tokens,
+                          int num_heads, int head_dim, int rot_offset, int rot_dim, int interleaved, float magnitude,
+                          int backward, int dtype, long long x_token_stride, long long x_head_stride,
+                          long long out_token_stride, long long out_head_stride, void* stream) {
+  if (tokens < 0 || num_heads <= 0 || head_dim <= 0) return DA_ERR_INVALID_ARG;
+  if (dtype < DA_BF16 || dtype > DA_F32) return DA_ERR_UNSUPPORTED;
+  if (int e = rope_check(inv_freq, head_dim, rot_offset, rot_dim, interleaved, magnitude)) return e;
+  if ((long long)num_heads * head_dim > 0x3fffffffLL) return DA_ERR_UNSUPPORTED;
+  if (tokens == 0) return DA_OK;
+  const int size = dtype == DA_F32 ? 4 : 2;
+  if (!x || !out || !positions || !aligned(x, size) || !aligned(out, size) || !aligned(positions, 4))
+    return DA_ERR_INVALID_ARG;
+  const long long far = 1LL << 40;  // strides whose products with the sizes stay in 64 bits
+  if (tokens > 0x7fffffffLL || x_token_stride < 0 || x_head_stride < 0 || x_token_stride > far ||
+      x_head_stride > far || out_token_stride < 0 || out_head_stride < 0 || out_token_stride > far ||
+      out_head_stride > far)
+    return DA_ERR_INVALID_ARG;
+  if (!rows_apart(tokens, num_heads, head_dim, out_token_stride, out_head_stride)) return DA_ERR_INVALID_ARG;
+  const bool same = x == out;
+  if (same) {
+    if ((tokens > 1 && x_token_stride != out_token_stride) || (num_heads > 1 && x_head_stride != out_head_stride))
+      return DA_ERR_INVALID_ARG;
+  } else {
+    // a partly overlapping output would be read after it is written
+    const uintptr_t xb = reinterpret_cast<uintptr_t>(x), ob = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t xn = ((tokens - 1) * x_token_stride + (num_heads - 1) * x_head_stride + head_dim) * size;
+    const uintptr_t on = ((tokens - 1) * out_token_stride + (num_heads - 1) * out_head_stride + head_dim) * size;
+    if (xb < ob + on && ob < xb + xn) return DA_ERR_INVALID_ARG;
+  }
+  int dev, sms, optin;
+  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
+  RopeApplyParams p;
+  p.r = {inv_freq, rot_offset, rot_dim, interleaved, magnitude, backward ? -1.f : 1.f};
+  p.x = x;
+  p.out = out;
+  p.positions = positions;
+  p.tokens = tokens;
+  p.H = num_heads;
+  p.D = head_dim;
+  p.xt = x_token_stride;
+  p.xh = x_head_stride;
+  p.ot = out_token_stride;
+  p.oh = out_head_stride;
+  p.copy = !same;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == DA_BF16 ? launch_rope<__nv_bfloat16>(p, sms, st)
+         : dtype == DA_F16 ? launch_rope<__half>(p, sms, st) : launch_rope<float>(p, sms, st);
+}
+
+namespace {
+
+CacheParams write_params(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                         const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim,
+                         const double* inv_freq, int rot_offset, int rot_dim, int interleaved, float magnitude,
+                         void* k, void* v, float* ks, float* vs) {
+  CacheParams p = {};
+  p.r = {inv_freq, rot_offset, rot_dim, interleaved, magnitude, 1.f};
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.seq_lens = seq_lens;
+  p.B = batch;
+  p.n = q_len;
+  p.Hkv = num_kv_heads;
+  p.D = head_dim;
+  p.k = k;
+  p.v = v;
+  p.ks = ks;
+  p.vs = vs;
+  return p;
+}
+
+CacheParams read_params(const void* k, const void* v, const float* ks, const float* vs, const int* starts,
+                        const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim, void* k_out,
+                        void* v_out) {
+  CacheParams p = {};
+  p.k = const_cast<void*>(k);
+  p.v = const_cast<void*>(v);
+  p.ks = const_cast<float*>(ks);
+  p.vs = const_cast<float*>(vs);
+  p.starts = starts;
+  p.seq_lens = seq_lens;
+  p.B = batch;
+  p.n = n_tokens;
+  p.Hkv = num_kv_heads;
+  p.D = head_dim;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  return p;
+}
+
+void set_pages(CacheParams& p, const int* page_table, int page_size, int max_pages, int num_pages) {
+  p.page_table = page_table;
+  p.slab = page_size;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+}
+
+}  // namespace
+
+extern "C" int kv_write_contig(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                               const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim, int max_ctx,
+                               const double* inv_freq, int rot_offset, int rot_dim, int interleaved, float magnitude,
+                               void* k, void* v, void* stream) {
+  CacheParams p = write_params(k_new, v_new, k_stride, v_stride, seq_lens, batch, q_len, num_kv_heads, head_dim,
+                               inv_freq, rot_offset, rot_dim, interleaved, magnitude, k, v, nullptr, nullptr);
+  p.slab = max_ctx;
+  return write_call(false, false, p, max_ctx, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kv_write_paged(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                              const int* page_table, const int* seq_lens, int batch, int q_len, int num_kv_heads,
+                              int head_dim, int page_size, int max_pages_per_seq, int num_pages, int max_seq_len,
+                              const double* inv_freq, int rot_offset, int rot_dim, int interleaved, float magnitude,
+                              void* k_pool, void* v_pool, void* stream) {
+  CacheParams p = write_params(k_new, v_new, k_stride, v_stride, seq_lens, batch, q_len, num_kv_heads, head_dim,
+                               inv_freq, rot_offset, rot_dim, interleaved, magnitude, k_pool, v_pool, nullptr, nullptr);
+  set_pages(p, page_table, page_size, max_pages_per_seq, num_pages);
+  return write_call(true, false, p, paged_cap(page_size, max_pages_per_seq, max_seq_len),
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kv_write_int8_contig(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                                    const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim,
+                                    int max_ctx, const double* inv_freq, int rot_offset, int rot_dim, int interleaved,
+                                    float magnitude, void* k_i8, void* v_i8, float* k_scale, float* v_scale,
+                                    void* stream) {
+  CacheParams p = write_params(k_new, v_new, k_stride, v_stride, seq_lens, batch, q_len, num_kv_heads, head_dim,
+                               inv_freq, rot_offset, rot_dim, interleaved, magnitude, k_i8, v_i8, k_scale, v_scale);
+  p.slab = max_ctx;
+  return write_call(false, true, p, max_ctx, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kv_write_int8_paged(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                                   const int* page_table, const int* seq_lens, int batch, int q_len, int num_kv_heads,
+                                   int head_dim, int page_size, int max_pages_per_seq, int num_pages, int max_seq_len,
+                                   const double* inv_freq, int rot_offset, int rot_dim, int interleaved,
+                                   float magnitude, void* k_pool_i8, void* v_pool_i8, float* k_scale_pool,
+                                   float* v_scale_pool, void* stream) {
+  CacheParams p =
+      write_params(k_new, v_new, k_stride, v_stride, seq_lens, batch, q_len, num_kv_heads, head_dim, inv_freq,
+                   rot_offset, rot_dim, interleaved, magnitude, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool);
+  set_pages(p, page_table, page_size, max_pages_per_seq, num_pages);
+  return write_call(true, true, p, paged_cap(page_size, max_pages_per_seq, max_seq_len),
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kv_read_int8_contig(const void* k_i8, const void* v_i8, const float* k_scale, const float* v_scale,
+                                   const int* starts, const int* seq_lens, int batch, int n_tokens, int num_kv_heads,
+                                   int head_dim, int max_ctx, void* k_out, void* v_out, void* stream) {
+  CacheParams p = read_params(k_i8, v_i8, k_scale, v_scale, starts, seq_lens, batch, n_tokens, num_kv_heads, head_dim,
+                              k_out, v_out);
+  p.slab = max_ctx;
+  return read_call(false, true, p, max_ctx, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kv_read_paged(const void* k_pool, const void* v_pool, const int* page_table, const int* starts,
+                             const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
+                             int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
+                             void* v_out, void* stream) {
+  CacheParams p = read_params(k_pool, v_pool, nullptr, nullptr, starts, seq_lens, batch, n_tokens, num_kv_heads,
+                              head_dim, k_out, v_out);
+  set_pages(p, page_table, page_size, max_pages_per_seq, num_pages);
+  return read_call(true, false, p, paged_cap(page_size, max_pages_per_seq, max_seq_len),
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kv_read_int8_paged(const void* k_pool_i8, const void* v_pool_i8, const float* k_scale_pool,
+                                  const float* v_scale_pool, const int* page_table, const int* starts,
+                                  const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
+                                  int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
+                                  void* v_out, void* stream) {
+  CacheParams p = read_params(k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, starts, seq_lens, batch, n_tokens,
+                              num_kv_heads, head_dim, k_out, v_out);
+  set_pages(p, page_table, page_size, max_pages_per_seq, num_pages);
+  return read_call(true, true, p, paged_cap(page_size, max_pages_per_seq, max_seq_len),
+                   reinterpret_cast<cudaStream_t>(stream));
+}

@@ -20,20 +20,12 @@
 
 #include "../../include/decode_attn.h"
 #include "combine_kernel.cuh"
+#include "host_util.cuh"
 #include "split_kernel.cuh"
 
 namespace da {
 namespace {
 
-constexpr int kMaxDevices = 64;
-constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;  // 2 s per bounded wait
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-std::mutex g_mu;
-EncodeTiledFn g_encode = nullptr;
 std::atomic<unsigned int> g_epoch{0};
 
 // A fresh non-zero tag for the per-segment counters of one call.
@@ -41,57 +33,6 @@ unsigned int next_epoch() {
   unsigned int e = ++g_epoch;
   while (e == 0) e = ++g_epoch;
   return e;
-}
-int g_num_sms[kMaxDevices] = {0};
-int g_smem_optin[kMaxDevices] = {0};
-
-int current_device(int* dev) { return cudaGetDevice(dev) == cudaSuccess ? DA_OK : DA_ERR_CUDA; }
-
-int device_info(int dev, int* sms, int* smem_optin) {
-  if (dev < 0 || dev >= kMaxDevices) return DA_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (g_num_sms[dev] == 0) {
-    int s = 0, m = 0;
-    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&m, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return DA_ERR_CUDA;
-    }
-    g_num_sms[dev] = s;
-    g_smem_optin[dev] = m;
-  }
-  *sms = g_num_sms[dev];
-  *smem_optin = g_smem_optin[dev];
-  return DA_OK;
-}
-
-int get_encoder(EncodeTiledFn* fn) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_encode) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || p == nullptr) {
-      cudaGetLastError();
-      return DA_ERR_CUDA;
-    }
-    g_encode = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  *fn = g_encode;
-  return DA_OK;
-}
-
-// Tiled map; dims/box innermost first, strides in bytes for dims 1..rank-1.
-int encode_map_t(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swz, const void* base, int rank,
-                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-  EncodeTiledFn enc;
-  if (int st = get_encoder(&enc)) return st;
-  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = enc(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? DA_OK : DA_ERR_INVALID_ARG;
 }
 
 // Tiled bf16 map with the swizzle the kernels read (128-byte rows, 64-byte at D = 32).
@@ -101,8 +42,6 @@ int encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dim
                       head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, base, rank, dims,
                       strides, box);
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int sub_width(int D) { return D >= 64 ? 64 : 32; }
 // int8 tiles: bytes per swizzle row and the swizzle the kernels read
@@ -794,17 +733,8 @@ extern "C" int decode_device_error(void* stream, unsigned int* flags) {
     return DA_ERR_CUDA;
   }
   unsigned int w = 0;
-  if (cudaMemcpyFromSymbol(&w, g_error_word, sizeof(w)) != cudaSuccess) {
-    cudaGetLastError();
+  if (da::take_unit_error_word(&w) || da::take_cache_error_word(&w))
     return DA_ERR_CUDA;
-  }
-  if (w) {
-    const unsigned int zero = 0;
-    if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess) {
-      cudaGetLastError();
-      return DA_ERR_CUDA;
-    }
-  }
   *flags = w;
   return w ? DA_ERR_TIMEOUT : DA_OK;
 }

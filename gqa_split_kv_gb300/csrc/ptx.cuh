@@ -85,6 +85,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of ROWB-byte rows under
+// the TMA swizzle of that width (128 or 64 bytes).
+template <int ROWB>
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+  const uint32_t off = (uint32_t)(row * ROWB + chunk * 16);
+  return ROWB == 128 ? off ^ (((off >> 7) & 7u) << 4) : off ^ (((off >> 7) & 3u) << 4);
+}
+
 // ---------------------------------------------------------------- warp MMA
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {

@@ -39,16 +39,11 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "device_error.cuh"
 #include "plan.cuh"
 #include "ptx.cuh"
 
 namespace da {
-
-// Device error word (bit 0: a bounded wait ran out; bit 1: a segment counter
-// update gave up; bit 2: a page-table entry outside [0, num_pages)).  The
-// library is one translation unit, so the definition lives here; the host reads
-// and clears it through decode_device_error().
-__device__ unsigned int g_error_word = 0;
 
 struct SplitParams {
   CUtensorMap tm_k;   // K cache / pool (bf16, or int8 values)
@@ -160,31 +155,6 @@ struct SplitGeo {
   static_assert(NPROD <= STAGES && NPROD + STAGES + LA <= RING, "producer warps and rings");
   static_assert(smem_bytes(64) <= 227 * 1024, "shared memory budget");
 };
-
-template <int ROWB>
-__device__ __forceinline__ uint32_t swz(int row, int chunk) {
-  const uint32_t off = (uint32_t)(row * ROWB + chunk * 16);
-  return ROWB == 128 ? off ^ (((off >> 7) & 7u) << 4) : off ^ (((off >> 7) & 3u) << 4);
-}
-
-// Bounded mbarrier wait.  Gives up after timeout_ns: sets the device error word
-// and the CTA's abort flag, after which every later wait returns at once, so
-// all warps still reach the same named barriers and the CTA exits.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             unsigned long long timeout_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (*abort_flag) return false;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > timeout_ns) {
-      atomicOr(&g_error_word, 1u);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");

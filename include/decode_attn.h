@@ -335,6 +335,119 @@ int prefill_attn_paged(const void* q, const void* k_pool, const void* v_pool, co
                        int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, float scale, void* out,
                        void* stream);
 
+/*
+ * Rotary positions.
+ *
+ * Pair j of a head, j < rot_dim / 2, is turned by position * inv_freq[j] radians:
+ *
+ *     a' = magnitude (a cos - b sin),   b' = magnitude (a sin + b cos)
+ *
+ * (a, b) are elements rot_offset + (2j, 2j + 1) of the head when interleaved is 1, or
+ * rot_offset + (j, j + rot_dim / 2) when it is 0; the rest of the head is unchanged.
+ * inv_freq is a float64 array on the device, finite; angles are exact to 2e-7 radians
+ * + position * inv_freq * 2^-52 at any 32-bit position, negative ones included, and the
+ * rotation runs in fp32 with one rounding to the tensor's type.
+ */
+typedef enum { DA_BF16 = 0, DA_F16 = 1, DA_F32 = 2 } da_dtype;
+typedef enum {
+  DA_ROPE_PLAIN = 0,    /* w_j = base^(-2j / rot_dim) */
+  DA_ROPE_LINEAR = 1,   /* w_j / factor: positions squeezed into the original context */
+  DA_ROPE_BASE = 2,     /* base * factor^(rot_dim / (rot_dim - 2)): the slowest pair stretched by
+                           factor, the fastest kept */
+  DA_ROPE_BY_PARTS = 3  /* pairs of more than high_turns turns over original_ctx positions kept, of
+                           fewer than low_turns divided by factor, in between mixed linearly */
+} da_rope_scaling;
+
+/*
+ * rope_inv_freq — the frequencies of a rotary embedding (host only, pure): writes
+ * rot_dim / 2 values to inv_freq (HOST memory).  base > 1; factor >= 1 (unused when
+ * plain); original_ctx > 0 and 0 <= low_turns < high_turns (by parts only).
+ */
+int rope_inv_freq(double* inv_freq, int rot_dim, double base, int scaling, double factor, double original_ctx,
+                  double low_turns, double high_turns);
+
+/*
+ * rope_apply — rotates the heads of tokens, or the gradient through them.
+ *  x, out     [tokens, num_heads, head_dim] of dtype, elements of a head consecutive, with the
+ *             given strides (in elements).  Rows of out may not share elements.  out may be x itself
+ *             with the same strides (in place), and may not overlap it otherwise.  16-byte
+ *             accesses are used when pointers, strides, rot_offset and the rotated part allow.
+ *  positions  int32 [tokens]
+ *  backward   0: out = magnitude R x; otherwise its gradient, out = magnitude R^T x.
+ *  rot_dim    even, rot_offset + rot_dim <= head_dim, at most 2048
+ */
+int rope_apply(const void* x, void* out, const int* positions, const double* inv_freq, long long tokens,
+               int num_heads, int head_dim, int rot_offset, int rot_dim, int interleaved, float magnitude,
+               int backward, int dtype, long long x_token_stride, long long x_head_stride,
+               long long out_token_stride, long long out_head_stride, void* stream);
+
+/*
+ * kv_write_contig / kv_write_paged / kv_write_int8_contig / kv_write_int8_paged — write
+ * the last q_len tokens of every sequence into the cache that the attention calls read.
+ * As for prefill_attn_*, seq_lens counts a sequence's tokens with the new ones, so new
+ * token i of sequence b is position L_b - q_len + i.  Positions below 0 are skipped (a
+ * padded batch: a sequence of L_b < q_len tokens brings only the last L_b of its rows).
+ * A position at or past the capacity (max_ctx, or min(max_seq_len, max_pages_per_seq *
+ * page_size)) is not written and sets bit 3 of the device error word; one whose page-table
+ * entry lies outside [0, num_pages) is not written and sets bit 2.  Nothing else in the
+ * cache changes.  Sequences whose new tokens fall on the same cache row race.
+ *  k_new, v_new  bf16 [batch, q_len, num_kv_heads, head_dim], k_stride / v_stride elements
+ *                from one token to the next (a multiple of 8, at least num_kv_heads *
+ *                head_dim: a slice of a fused projection will do); 16-byte aligned
+ *  inv_freq      NULL, or the frequencies by which keys are rotated first, as in rope_apply,
+ *                at their positions (rot_offset a multiple of 8, rot_dim of 16); in fp32,
+ *                without a rounding in between
+ *  v_new, v      both NULL: only keys are written (a latent cache, num_kv_heads 1)
+ *  bf16 caches   as decode_attn_contig / _paged read them (latent_attn_*: num_kv_heads 1,
+ *                head_dim latent_dim + 64); head_dim a multiple of 8 up to 1024
+ *  int8 caches   as decode_attn_int8_* read them: scale = max|x| / 127 over the row's
+ *                head_dim elements (1 for a row of zeros, and no smaller than the smallest normal
+ *                float), value = x / scale rounded to nearest even; head_dim a multiple of 16.
+ *                A row with an infinity or a NaN gets a NaN scale and zeros.
+ *  seq_lens      int32 [batch] on the device (contiguous: may be NULL, every sequence
+ *                max_ctx tokens)
+ */
+int kv_write_contig(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                    const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim, int max_ctx,
+                    const double* inv_freq, int rot_offset, int rot_dim, int interleaved, float magnitude,
+                    void* k, void* v, void* stream);
+int kv_write_paged(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                   const int* page_table, const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim,
+                   int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, const double* inv_freq,
+                   int rot_offset, int rot_dim, int interleaved, float magnitude, void* k_pool, void* v_pool,
+                   void* stream);
+int kv_write_int8_contig(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                         const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim, int max_ctx,
+                         const double* inv_freq, int rot_offset, int rot_dim, int interleaved, float magnitude,
+                         void* k_i8, void* v_i8, float* k_scale, float* v_scale, void* stream);
+int kv_write_int8_paged(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                        const int* page_table, const int* seq_lens, int batch, int q_len, int num_kv_heads,
+                        int head_dim, int page_size, int max_pages_per_seq, int num_pages, int max_seq_len,
+                        const double* inv_freq, int rot_offset, int rot_dim, int interleaved, float magnitude,
+                        void* k_pool_i8, void* v_pool_i8, float* k_scale_pool, float* v_scale_pool, void* stream);
+
+/*
+ * kv_read_paged / kv_read_int8_contig / kv_read_int8_paged — a cache's tokens as
+ * contiguous bf16 (an int8 cache for prefill_attn_contig, the pages of a latent cache
+ * for its expansion).  Output row i of sequence b is position starts[b] + i, widened as
+ * int8 * scale in fp32 and rounded once; rows whose position is negative or at or past
+ * L_b, and rows of a page-table entry outside [0, num_pages) (which sets bit 2 of the
+ * device error word), are left as they were.
+ *  k_out, v_out  bf16 [batch, n_tokens, num_kv_heads, head_dim] (v_out NULL with v NULL)
+ *  starts        int32 [batch] on the device, or NULL (0)
+ *  seq_lens      int32 [batch], clamped to the capacity; contiguous: may be NULL (max_ctx)
+ */
+int kv_read_paged(const void* k_pool, const void* v_pool, const int* page_table, const int* starts,
+                  const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim, int page_size,
+                  int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out, void* v_out, void* stream);
+int kv_read_int8_contig(const void* k_i8, const void* v_i8, const float* k_scale, const float* v_scale,
+                        const int* starts, const int* seq_lens, int batch, int n_tokens, int num_kv_heads,
+                        int head_dim, int max_ctx, void* k_out, void* v_out, void* stream);
+int kv_read_int8_paged(const void* k_pool_i8, const void* v_pool_i8, const float* k_scale_pool,
+                       const float* v_scale_pool, const int* page_table, const int* starts, const int* seq_lens,
+                       int batch, int n_tokens, int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq,
+                       int num_pages, int max_seq_len, void* k_out, void* v_out, void* stream);
+
 /* Human-readable name of a da_status value (static string). */
 const char* decode_status_string(int status);
 
@@ -345,7 +458,8 @@ const char* decode_status_string(int status);
  * read by decode_attn_paged / decode_attn_multi_paged / decode_attn_int8_paged was
  * outside [0, num_pages)
  * (that box was read from page 0 instead, so the affected rows are wrong but no
- * copy leaves the pool).  Returns DA_OK when flags == 0, DA_ERR_TIMEOUT otherwise,
+ * copy leaves the pool; kv_write_* and kv_read_* skip such rows), bit 3 a token at or
+ * past the cache's capacity that kv_write_* did not write.  Returns DA_OK when flags == 0, DA_ERR_TIMEOUT otherwise,
  * or DA_ERR_CUDA.
  */
 int decode_device_error(void* stream, unsigned int* flags);
