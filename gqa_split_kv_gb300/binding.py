@@ -36,6 +36,10 @@ __all__ = [
     "kv_read_paged",
     "kv_read_int8_contig",
     "kv_read_int8_paged",
+    "latent_attn_contig",
+    "latent_attn_paged",
+    "latent_workspace",
+    "latent_max_batch",
     "device_error",
     "selftest_bounded_wait",
     "counters_len",
@@ -112,9 +116,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "kv_read_paged": [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
         "kv_read_int8_contig": [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp],
         "kv_read_int8_paged": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
+        "latent_attn_contig": [vp, vp, vp, i, i, i, i, i, f, vp, ll, vp, vp],
+        "latent_attn_paged": [vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, ll, vp, vp],
+        "latent_workspace_bytes": [i, i, i, i, i],
+        "latent_max_batch": [i, i, i],
     }.items():
         getattr(lib, name).argtypes = args
-        getattr(lib, name).restype = i
+        getattr(lib, name).restype = ll if name == "latent_workspace_bytes" else i
     if path is None:
         _lib = lib
     return lib
@@ -692,6 +700,73 @@ def kv_read_int8_paged(k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_ta
         raise ValueError("k: an int8 cache needs its scales")
     return _kv_read("kv_read_int8_paged", k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens,
                     max_seq_len, n_tokens, starts, k_out, v_out, stream)
+
+
+# ---------------------------------------------------------------- latent attention
+
+LATENT_ROPE = 64  # elements of a cached row past its latent: the rotated part that all heads share
+
+
+def latent_max_batch(num_heads: int, latent_dim: int, q_len: int = 1) -> int:
+    """Largest batch latent_attn_* accepts for this shape (host only)."""
+    m = load().latent_max_batch(q_len, num_heads, latent_dim)
+    if m < 0:
+        raise DecodeAttnError("latent_max_batch", -m)
+    return m
+
+
+def latent_workspace(batch: int, num_heads: int, latent_dim: int, q_len: int = 1):
+    """A workspace for latent_attn_* calls of this shape on the current CUDA device (uint8).  A program may keep
+    one; calls that share it must not overlap on the GPU."""
+    import torch
+    n = load().latent_workspace_bytes(batch, q_len, num_heads, latent_dim, 0)
+    if n < 0:
+        raise DecodeAttnError("latent_workspace_bytes", -n)
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def _latent(fn, q, cache, page_table, seq_lens, max_seq_len, scale, workspace, out, stream):
+    import torch
+    bf16 = torch.bfloat16
+    _plain(q, "q", bf16, None, None, None, None)
+    B, n, H, W = q.shape
+    R = W - LATENT_ROPE
+    _plain(cache, "cache", bf16, B if page_table is None else None, None, W)
+    if page_table is not None:
+        _plain(page_table, "page_table", torch.int32, B, None)
+    if seq_lens is not None:
+        _plain(seq_lens, "seq_lens", torch.int32, B)
+    elif page_table is not None:
+        raise ValueError("seq_lens: a paged cache needs them")
+    if out is None:
+        out = torch.empty((B, n, H, max(R, 0)), dtype=bf16, device=q.device)
+    _plain(out, "out", bf16, B, n, H, R)
+    dev = _here(q, cache, page_table, seq_lens, workspace, out)
+    if workspace is None:
+        workspace = latent_workspace(B, H, R, n)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    slabs, slab = cache.shape[:2]
+    where = (slab,) if page_table is None else (slab, page_table.shape[1], slabs, int(max_seq_len))
+    table = () if page_table is None else (page_table.data_ptr(),)
+    _check(fn, getattr(load(), fn)(q.data_ptr(), cache.data_ptr(), *table, _addr(seq_lens), B, n, H, R, *where, scale,
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
+                                   _raw_stream(stream, dev)))
+    return out
+
+
+def latent_attn_contig(q, cache, seq_lens=None, *, scale: float, workspace=None, out=None, stream=None):
+    """Attention over one shared latent vector a token (absorbed form): q bf16 [B, q_len, H, R + 64] (the last q_len
+    tokens, causal among themselves), cache bf16 [B, max_ctx, R + 64], R in {128, 256, 512}; seq_lens int32 [B] or
+    None.  scale is the head's own (one over the root of its width before absorption).  workspace: as made by
+    latent_workspace (None: made here).  Returns out bf16 [B, q_len, H, R]."""
+    return _latent("latent_attn_contig", q, cache, None, seq_lens, 0, scale, workspace, out, stream)
+
+
+def latent_attn_paged(q, pool, page_table, seq_lens, max_seq_len: int, *, scale: float, workspace=None, out=None,
+                      stream=None):
+    """latent_attn_contig over a page pool [num_pages, page_size, R + 64]; page_table int32 [B, max_pages]."""
+    return _latent("latent_attn_paged", q, pool, page_table, seq_lens, max_seq_len, scale, workspace, out, stream)
 
 
 def selftest_bounded_wait(timeout_ns: int, stream=None) -> None:

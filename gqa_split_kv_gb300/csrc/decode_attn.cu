@@ -733,7 +733,7 @@ extern "C" int decode_device_error(void* stream, unsigned int* flags) {
     return DA_ERR_CUDA;
   }
   unsigned int w = 0;
-  if (da::take_unit_error_word(&w) || da::take_cache_error_word(&w))
+  if (da::take_unit_error_word(&w) || da::take_cache_error_word(&w) || da::take_latent_error_word(&w))
     return DA_ERR_CUDA;
   *flags = w;
   return w ? DA_ERR_TIMEOUT : DA_OK;

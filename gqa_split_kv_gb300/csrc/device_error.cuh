@@ -56,5 +56,6 @@ static int take_unit_error_word(unsigned int* flags) {
 
 // The words of the other units (each defined in its unit).
 int take_cache_error_word(unsigned int* flags);
+int take_latent_error_word(unsigned int* flags);
 
 }  // namespace da

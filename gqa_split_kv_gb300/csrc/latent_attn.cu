@@ -1,0 +1,222 @@
+// Entry points of latent attention (declared in include/decode_attn.h): the absorbed
+// form over a contiguous or paged latent cache.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "../../include/decode_attn.h"
+#include "device_error.cuh"
+#include "host_util.cuh"
+#include "latent_kernel.cuh"
+
+namespace da {
+
+int take_latent_error_word(unsigned int* flags) { return take_unit_error_word(flags); }
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Rows of a tile: the smallest built size that holds them all, else tiles of 64.
+int latent_tile_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <typename K>
+int allow_smem(K kern, int bytes, bool (&done)[kMaxDevices], int dev) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (done[dev]) return DA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+      cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_UNSUPPORTED;
+  }
+  done[dev] = true;
+  return DA_OK;
+}
+
+template <int R, int N, bool PAGED>
+int launch_latent(const LatentParams& prm, int sms, int dev, cudaStream_t st) {
+  using Gm = LatentGeo<R, N>;
+  static bool split_done[kMaxDevices] = {false}, combine_done[kMaxDevices] = {false};
+  if (prm.B > Gm::MAX_BATCH) return DA_ERR_UNSUPPORTED;
+  if (int e = allow_smem(latent_kernel<R, N, PAGED>, 227 * 1024, split_done, dev)) return e;
+  if (int e = allow_smem(latent_combine_kernel<R>, 227 * 1024, combine_done, dev)) return e;
+  // one CTA a range, and no more ranges than the line has units
+  const long long units =
+      ((long long)prm.B * prm.U * ((prm.max_len + kBlockTokens - 1) / kBlockTokens + 3 + kLatentGap)) / kRangeQuantum + 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(prm.ranges < units ? prm.ranges : units));
+  cfg.blockDim = dim3(Gm::NTHREADS);
+  cfg.dynamicSmemBytes = (size_t)Gm::smem_bytes(prm.B);
+  cfg.stream = st;
+  if (cudaLaunchKernelEx(&cfg, latent_kernel<R, N, PAGED>, prm) != cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_CUDA;
+  }
+  const LatentCombineParams c = {prm.part_acc, prm.part_ml, prm.out, prm.seq_lens, prm.B,
+                                 prm.rows,     prm.U,       N,       prm.ranges,   prm.max_len};
+  // items go a warp at a time; the few rows of long runs a CTA at a time
+  const long long items = (long long)prm.B * prm.rows * (R / 128);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(items < 2LL * sms ? items : 2LL * sms));
+  cfg.blockDim = dim3(512);
+  cfg.dynamicSmemBytes = (size_t)(16 * 32 * 16 + (2 * prm.B + 2) * 4);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, latent_combine_kernel<R>, c) != cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_CUDA;
+  }
+  return DA_OK;
+}
+
+template <int R>
+int launch_latent_rows(const LatentParams& prm, int N, bool paged, int sms, int dev, cudaStream_t st) {
+  if (N == 16)
+    return paged ? launch_latent<R, 16, true>(prm, sms, dev, st) : launch_latent<R, 16, false>(prm, sms, dev, st);
+  if (N == 32)
+    return paged ? launch_latent<R, 32, true>(prm, sms, dev, st) : launch_latent<R, 32, false>(prm, sms, dev, st);
+  return paged ? launch_latent<R, 64, true>(prm, sms, dev, st) : launch_latent<R, 64, false>(prm, sms, dev, st);
+}
+
+template <int R>
+int latent_batch_limit(int N) {
+  return N == 16 ? LatentGeo<R, 16>::MAX_BATCH : N == 32 ? LatentGeo<R, 32>::MAX_BATCH : LatentGeo<R, 64>::MAX_BATCH;
+}
+
+int latent_shape(int batch, int q_len, int num_heads, int latent_dim) {
+  if (batch < 0 || q_len < 1 || q_len > DA_MAX_QLEN || num_heads < 1) return DA_ERR_INVALID_ARG;
+  if (latent_dim != 128 && latent_dim != 256 && latent_dim != 512) return DA_ERR_UNSUPPORTED;
+  if (num_heads > DA_MAX_LATENT_HEADS) return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+long long latent_part_rows(int rows, int sms) { return 2LL * sms * latent_tile_rows(rows); }
+
+int latent_call(bool paged, const void* q, const void* cache, const int* page_table, const int* seq_lens, int B,
+                int q_len, int H, int R, long long max_len, int page_size, int max_pages, int num_pages, float scale,
+                void* workspace, long long workspace_bytes, void* out, cudaStream_t st) {
+  if (int e = latent_shape(B, q_len, H, R)) return e;
+  if (!std::isfinite(scale)) return DA_ERR_INVALID_ARG;
+  if (max_len > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  if (B == 0) return DA_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4)) return DA_ERR_INVALID_ARG;
+  const int rows = H * q_len, N = latent_tile_rows(rows), W = R + 64;
+  if (max_len == 0 || (paged && num_pages == 0)) {
+    if (cudaMemsetAsync(out, 0, (size_t)B * rows * R * 2, st) != cudaSuccess) {
+      cudaGetLastError();
+      return DA_ERR_CUDA;
+    }
+    return DA_OK;
+  }
+  if (!cache || !aligned(cache, 16)) return DA_ERR_INVALID_ARG;
+  const int limit = R == 128 ? latent_batch_limit<128>(N) : R == 256 ? latent_batch_limit<256>(N)
+                                                                     : latent_batch_limit<512>(N);
+  if (B > limit) return DA_ERR_UNSUPPORTED;
+  int dev, sms, optin;
+  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
+  if (!workspace || workspace_bytes < latent_part_rows(rows, sms) * (R * 4 + 8)) return DA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DA_ERR_INVALID_ARG;
+
+  LatentParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.U = (rows + N - 1) / N;
+  // the plan counts line positions in 32 bits
+  if ((long long)B * prm.U * ((max_len + kBlockTokens - 1) / kBlockTokens + 3 + kLatentGap) >= (1LL << 30))
+    return DA_ERR_UNSUPPORTED;
+  {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(W / 64), (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)W * 2, 128, (cuuint64_t)rows * W * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)N, (cuuint32_t)(W / 64), 1};
+    if (int e = encode_map_t(&prm.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, q, 4, dims,
+                             strides, box))
+      return e;
+  }
+  // boxes of R rows of one page, the largest of 64, 32 and 16 that divides it; a box of two
+  // columns has them 64 tokens apart only where it has all 64
+  const int box_shift = !paged || page_size % 64 == 0 ? 2 : page_size % 32 == 0 ? 1 : 0;
+  {
+    const cuuint64_t slab = (cuuint64_t)(paged ? page_size : max_len);
+    const cuuint64_t dims[4] = {64, slab, (cuuint64_t)(W / 64), (cuuint64_t)(paged ? num_pages : B)};
+    const cuuint64_t strides[3] = {(cuuint64_t)W * 2, 128, slab * W * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(16 << box_shift), (cuuint32_t)(box_shift == 2 ? 2 : 1), 1};
+    const cuuint32_t box1[4] = {64, (cuuint32_t)(16 << box_shift), 1, 1};
+    if (int e = encode_map_t(&prm.tm_unit, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, cache, 4,
+                             dims, strides, box))
+      return e;
+    if (int e = encode_map_t(&prm.tm_pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, cache, 4, dims,
+                             strides, box1))
+      return e;
+  }
+  prm.seq_lens = seq_lens;
+  prm.page_table = page_table;
+  prm.part_acc = static_cast<float*>(workspace);
+  prm.part_ml = reinterpret_cast<float2*>(prm.part_acc + latent_part_rows(rows, sms) * R);
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.B = B;
+  prm.H = H;
+  prm.q_len = q_len;
+  prm.rows = rows;
+  prm.ranges = sms;
+  prm.max_len = (int)max_len;
+  prm.page_size = page_size;
+  prm.max_pages = max_pages;
+  prm.num_pages = num_pages;
+  prm.box_shift = box_shift;
+  prm.page_shift = paged && (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
+  prm.scale_log2 = scale * kLog2e;
+  prm.timeout_ns = kWaitTimeoutNs;
+  switch (R) {
+    case 128: return launch_latent_rows<128>(prm, N, paged, sms, dev, st);
+    case 256: return launch_latent_rows<256>(prm, N, paged, sms, dev, st);
+    default: return launch_latent_rows<512>(prm, N, paged, sms, dev, st);
+  }
+}
+
+}  // namespace
+}  // namespace da
+
+using namespace da;
+
+extern "C" long long latent_workspace_bytes(int batch, int q_len, int num_heads, int latent_dim, int num_sms) {
+  if (int e = latent_shape(batch, q_len, num_heads, latent_dim)) return -e;
+  int dev, sms = num_sms, optin;
+  if (sms <= 0 && (current_device(&dev) || device_info(dev, &sms, &optin))) return -DA_ERR_CUDA;
+  return latent_part_rows(num_heads * q_len, sms) * (latent_dim * 4 + 8);
+}
+
+extern "C" int latent_max_batch(int q_len, int num_heads, int latent_dim) {
+  if (int e = latent_shape(1, q_len, num_heads, latent_dim)) return -e;
+  const int N = latent_tile_rows(num_heads * q_len);
+  return latent_dim == 128 ? latent_batch_limit<128>(N) : latent_dim == 256 ? latent_batch_limit<256>(N)
+                                                                            : latent_batch_limit<512>(N);
+}
+
+extern "C" int latent_attn_contig(const void* q, const void* cache, const int* seq_lens, int batch, int q_len,
+                                  int num_heads, int latent_dim, int max_ctx, float scale, void* workspace,
+                                  long long workspace_bytes, void* out, void* stream) {
+  if (max_ctx < 0) return DA_ERR_INVALID_ARG;
+  return latent_call(false, q, cache, nullptr, seq_lens, batch, q_len, num_heads, latent_dim, max_ctx, 0, 0, 0, scale,
+                     workspace, workspace_bytes, out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int latent_attn_paged(const void* q, const void* pool, const int* page_table, const int* seq_lens,
+                                 int batch, int q_len, int num_heads, int latent_dim, int page_size,
+                                 int max_pages_per_seq, int num_pages, int max_seq_len, float scale, void* workspace,
+                                 long long workspace_bytes, void* out, void* stream) {
+  if (page_size <= 0 || max_pages_per_seq < 0 || num_pages < 0 || max_seq_len < 0) return DA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0) return DA_ERR_UNSUPPORTED;
+  if (batch > 0 && (!seq_lens || !page_table || !aligned(page_table, 4))) return DA_ERR_INVALID_ARG;
+  long long cap = (long long)max_pages_per_seq * page_size;
+  if (cap > max_seq_len) cap = max_seq_len;
+  return latent_call(true, q, pool, page_table, seq_lens, batch, q_len, num_heads, latent_dim, cap, page_size,
+                     max_pages_per_seq, num_pages, scale, workspace, workspace_bytes, out,
+                     reinterpret_cast<cudaStream_t>(stream));
+}

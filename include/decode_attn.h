@@ -448,6 +448,50 @@ int kv_read_int8_paged(const void* k_pool_i8, const void* v_pool_i8, const float
                        int batch, int n_tokens, int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq,
                        int num_pages, int max_seq_len, void* k_out, void* v_out, void* stream);
 
+/*
+ * latent_attn_contig / latent_attn_paged — attention over a cache of one shared latent
+ * vector a token, in its absorbed form: the up-projections of keys and values are folded
+ * into the queries and the output, so every head attends to the cached vector itself.
+ * With c_t the cached row of latent_dim + 64 elements (the latent, then the rotated part
+ * that all heads share), for query token i (of the last q_len tokens, as in
+ * decode_attn_multi_*: it sees the first L_b - q_len + 1 + i cached tokens) and head h:
+ *
+ *     s_t = scale * <q[b,i,h,:], c_t>,   out[b,i,h,:] = sum_t softmax(s)_t * c_t[0 : latent_dim]
+ *
+ * A query that sees no token gives zeros.
+ *  q          bf16 [batch, q_len, num_heads, latent_dim + 64], token-major
+ *  cache      bf16 [batch, max_ctx, latent_dim + 64], or a pool [num_pages, page_size,
+ *             latent_dim + 64] with page_table int32 [batch, max_pages_per_seq] (page_size a
+ *             multiple of 16; kv_write_* with num_kv_heads 1 and no values writes either).  Rows at
+ *             positions below L_b are finite; what lies past them is never used.
+ *  seq_lens   int32 [batch], clamped to the capacity (contiguous: may be NULL, max_ctx)
+ *  out        bf16 [batch, q_len, num_heads, latent_dim]
+ *  workspace  latent_workspace_bytes(...) bytes, 16-byte aligned, of any content; calls that share
+ *             it must not overlap on the GPU (two captured graphs included)
+ *  latent_dim 128, 256 or 512; num_heads up to DA_MAX_LATENT_HEADS; 1 <= q_len <= DA_MAX_QLEN;
+ *             batch up to latent_max_batch(...).  scale: finite.
+ * Softmax in fp32, weights rounded to bf16 for the product with the latents and summed as
+ * rounded, fp32 accumulation, one rounding of the output.  Results are bitwise reproducible.
+ * Page-table entries outside [0, num_pages) set bit 2 of the device error word and read
+ * page 0 instead.  DA_ERR_WORKSPACE: the workspace is missing or too small.
+ */
+#define DA_MAX_LATENT_HEADS 256
+int latent_attn_contig(const void* q, const void* cache, const int* seq_lens, int batch, int q_len, int num_heads,
+                       int latent_dim, int max_ctx, float scale, void* workspace, long long workspace_bytes,
+                       void* out, void* stream);
+int latent_attn_paged(const void* q, const void* pool, const int* page_table, const int* seq_lens, int batch,
+                      int q_len, int num_heads, int latent_dim, int page_size, int max_pages_per_seq, int num_pages,
+                      int max_seq_len, float scale, void* workspace, long long workspace_bytes, void* out,
+                      void* stream);
+
+/*
+ * latent_workspace_bytes — the workspace of a latent_attn_* call on a device of num_sms
+ * SMs (<= 0: the current device); latent_max_batch — the largest batch it accepts (host
+ * only, pure).  Negative da_status for shapes outside those above.
+ */
+long long latent_workspace_bytes(int batch, int q_len, int num_heads, int latent_dim, int num_sms);
+int latent_max_batch(int q_len, int num_heads, int latent_dim);
+
 /* Human-readable name of a da_status value (static string). */
 const char* decode_status_string(int status);
 
