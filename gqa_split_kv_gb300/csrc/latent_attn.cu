@@ -43,7 +43,8 @@ template <int R, int N, bool PAGED>
 int launch_latent(const LatentParams& prm, int sms, int dev, cudaStream_t st) {
   using Gm = LatentGeo<R, N>;
   static bool split_done[kMaxDevices] = {false}, combine_done[kMaxDevices] = {false};
-  if (prm.B > Gm::MAX_BATCH) return DA_ERR_UNSUPPORTED;
+  const long long items = (long long)prm.B * prm.rows * (R / 128);  // of the combine kernel
+  if (prm.B > Gm::MAX_BATCH || items > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   if (int e = allow_smem(latent_kernel<R, N, PAGED>, 227 * 1024, split_done, dev)) return e;
   if (int e = allow_smem(latent_combine_kernel<R>, 227 * 1024, combine_done, dev)) return e;
   // one CTA a range, and no more ranges than the line has units
@@ -52,7 +53,7 @@ int launch_latent(const LatentParams& prm, int sms, int dev, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(prm.ranges < units ? prm.ranges : units));
   cfg.blockDim = dim3(Gm::NTHREADS);
-  cfg.dynamicSmemBytes = (size_t)Gm::smem_bytes(prm.B);
+  cfg.dynamicSmemBytes = (size_t)Gm::SMEM;
   cfg.stream = st;
   if (cudaLaunchKernelEx(&cfg, latent_kernel<R, N, PAGED>, prm) != cudaSuccess) {
     cudaGetLastError();
@@ -60,14 +61,13 @@ int launch_latent(const LatentParams& prm, int sms, int dev, cudaStream_t st) {
   }
   const LatentCombineParams c = {prm.part_acc, prm.part_ml, prm.out, prm.seq_lens, prm.B,
                                  prm.rows,     prm.U,       N,       prm.ranges,   prm.max_len};
-  // items go a warp at a time; the few rows of long runs a CTA at a time
-  const long long items = (long long)prm.B * prm.rows * (R / 128);
+  // items go a warp at a time, those of long runs a CTA at a time
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(items < 2LL * sms ? items : 2LL * sms));
-  cfg.blockDim = dim3(512);
-  cfg.dynamicSmemBytes = (size_t)(16 * 32 * 16 + (2 * prm.B + 2) * 4);
+  cfg.blockDim = dim3(LatentCombineGeo::NTHREADS);
+  cfg.dynamicSmemBytes = (size_t)LatentCombineGeo::smem_bytes(prm.ranges, prm.B);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, latent_combine_kernel<R>, c) != cudaSuccess) {
@@ -100,6 +100,12 @@ int latent_shape(int batch, int q_len, int num_heads, int latent_dim) {
 
 long long latent_part_rows(int rows, int sms) { return 2LL * sms * latent_tile_rows(rows); }
 
+// partials, their (m, l), and the list of pieces
+long long latent_workspace(int B, int rows, int R, int sms) {
+  const int N = latent_tile_rows(rows);
+  return latent_part_rows(rows, sms) * (R * 4 + 8) + (sms + (long long)B * ((rows + N - 1) / N)) * 16;
+}
+
 int latent_call(bool paged, const void* q, const void* cache, const int* page_table, const int* seq_lens, int B,
                 int q_len, int H, int R, long long max_len, int page_size, int max_pages, int num_pages, float scale,
                 void* workspace, long long workspace_bytes, void* out, cudaStream_t st) {
@@ -122,7 +128,7 @@ int latent_call(bool paged, const void* q, const void* cache, const int* page_ta
   if (B > limit) return DA_ERR_UNSUPPORTED;
   int dev, sms, optin;
   if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
-  if (!workspace || workspace_bytes < latent_part_rows(rows, sms) * (R * 4 + 8)) return DA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < latent_workspace(B, rows, R, sms)) return DA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return DA_ERR_INVALID_ARG;
 
   LatentParams prm;
@@ -159,6 +165,7 @@ int latent_call(bool paged, const void* q, const void* cache, const int* page_ta
   prm.page_table = page_table;
   prm.part_acc = static_cast<float*>(workspace);
   prm.part_ml = reinterpret_cast<float2*>(prm.part_acc + latent_part_rows(rows, sms) * R);
+  prm.pieces = reinterpret_cast<int4*>(prm.part_ml + latent_part_rows(rows, sms));
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.B = B;
   prm.H = H;
@@ -189,7 +196,7 @@ extern "C" long long latent_workspace_bytes(int batch, int q_len, int num_heads,
   if (int e = latent_shape(batch, q_len, num_heads, latent_dim)) return -e;
   int dev, sms = num_sms, optin;
   if (sms <= 0 && (current_device(&dev) || device_info(dev, &sms, &optin))) return -DA_ERR_CUDA;
-  return latent_part_rows(num_heads * q_len, sms) * (latent_dim * 4 + 8);
+  return latent_workspace(batch, num_heads * q_len, latent_dim, sms);
 }
 
 extern "C" int latent_max_batch(int q_len, int num_heads, int latent_dim) {

@@ -20,8 +20,12 @@
 // (144 KB) could not be double-buffered.
 //
 // A tile is R / 128 units of 16 KB ([2][64 tokens][64 elements], 128-byte swizzle) and
-// the rotated part (8 KB) in a ring of its own; a unit is freed by its own P^T product, so
-// the ring need not hold two whole tiles.
+// the rotated part (8 KB) in a ring of its own; a unit is freed by its own P^T product.  The
+// ring has to hold two whole tiles: with one unit less (7 at N = 64) the last unit of a
+// tile waits for the first product of the tile before it, and a tile takes that
+// latency (0.8 us) and a load's (1.5 us) instead of half of it (2.3 us a tile, where HBM
+// needs 1.7).  So at N = 64, R = 512 the plan's arrays share the ring's memory, each
+// CTA's pieces are listed once, and P^T has one buffer.
 //
 // Softmax.  S comes back as the fragment of a 16 x 8 warp MMA: thread t of warp w holds
 // tokens 16 w + t / 4 and 8 further on, N / 4 rows of each; P^T is stored with transposing
@@ -39,7 +43,7 @@
 // Warps: 0 and 3 issue the copies (Q and even units; odd units and the rotated part), 1
 // the S products, 2 the O products (one thread issues an MMA every 45 cycles; at N = 64 the
 // two kinds take 32 and 48 on the tensor cores, so one thread for both would be the
-// limit), 4..7 softmax and epilogue.  Waits are bounded as in prefill_tc.cuh.
+// limit), from 4 on softmax and epilogue, a warpgroup per 32 rows.  Waits are bounded as in prefill_tc.cuh.
 #pragma once
 
 #include <cuda.h>
@@ -62,6 +66,7 @@ struct LatentParams {
   const int* page_table;
   float* part_acc;      // [2 ranges][N][R]
   float2* part_ml;      // [2 ranges][N], m in log2 units
+  int4* pieces;         // [ranges + B U]: the ranges' pieces past the first LatentGeo::PCAP
   __nv_bfloat16* out;   // [B][rows][R]
   int B, H, q_len, rows, U;
   int ranges;           // ranges the line is cut into (at most)
@@ -92,6 +97,12 @@ __device__ __forceinline__ Plan latent_plan(int B, int U, int ranges, const int*
 // first segment may have begun before it, its last may go on after it.
 __host__ __device__ __forceinline__ int latent_slot(int r0, int j) { return j == 0 ? 2 * r0 + 1 : 2 * (r0 + j); }
 
+// A piece as the warps of a CTA read it: (sequence, first token, last token + 1, row tile
+// and partial slot + 1, 0 for a segment of one piece).
+__device__ __forceinline__ int4 latent_piece(const Piece& pc, int r) {
+  return make_int4(pc.b, pc.t0, pc.t1, pc.u | (pc.npieces == 1 ? 0 : (latent_slot(r - pc.j, pc.j) + 1) << 8));
+}
+
 template <int R, int N>
 struct LatentGeo {
   static constexpr int T = 64;               // tokens a tile
@@ -100,38 +111,42 @@ struct LatentGeo {
   static constexpr int UNIT = 2 * T * 128, PE = T * 128;
   static constexpr int Q_BYTES = NC * N * 128, P_BYTES = N * 128;
   static constexpr int NPE = 2;
+  // P^T has two buffers but where the second would cost the ring its second whole tile
+  static constexpr int NP = R == 512 && N == 64 ? 1 : 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_PE = OFF_P + 2 * P_BYTES;
+  static constexpr int OFF_PE = OFF_P + NP * P_BYTES;
   static constexpr int OFF_U = OFF_PE + NPE * PE;
-  static constexpr int SCRATCH = 2048;       // barriers, reductions
-  static constexpr int PLAN_ROOM = 8192;     // at least: batches of 1023
-  static constexpr int NUNIT_FIT = (227 * 1024 - 1024 - OFF_U - SCRATCH - PLAN_ROOM) / UNIT;
+  static constexpr int SCRATCH = 2048;       // barriers, reductions, the first pieces
+  static constexpr int NUNIT_FIT = (227 * 1024 - 1024 - OFF_U - SCRATCH) / UNIT;
   static constexpr int NUNIT = NUNIT_FIT < 12 ? NUNIT_FIT : 12;
   static constexpr int OFF_SCR = OFF_U + NUNIT * UNIT;
   // barriers
   static constexpr int B_UFULL = 0, B_UEMPTY = NUNIT, B_PEFULL = 2 * NUNIT, B_PEEMPTY = B_PEFULL + NPE,
                        B_QFULL = B_PEEMPTY + NPE, B_QEMPTY = B_QFULL + 1, B_S = B_QEMPTY + 1, B_P = B_S + 2,
                        B_PV = B_P + 2, B_OFREE = B_PV + 2, B_FIN = B_OFREE + 1, NBAR = B_FIN + 2;
-  static constexpr int OFF_MISC = OFF_SCR + NBAR * 8;          // tensor memory base, abort flag
-  static constexpr int OFF_RED = (OFF_MISC + 16 + 15) / 16 * 16;  // [4][N] floats
+  static constexpr int OFF_MISC = OFF_SCR + NBAR * 8;          // tensor memory base, abort flag, pieces
+  static constexpr int PCAP = 8;                               // pieces kept in shared memory
+  static constexpr int OFF_PC = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr int OFF_RED = OFF_PC + PCAP * 16;           // [4][N] floats
   static constexpr int OFF_COL = OFF_RED + 4 * N * 4;          // [N] floats: factors of O's columns
   static constexpr int OFF_COLM = OFF_COL + N * 4;             // [N] floats: maxima at a piece's end
-  static constexpr int OFF_PLAN = OFF_SCR + SCRATCH;
-  static constexpr int smem_bytes(int B) { return OFF_PLAN + (2 * B + 2) * 4 + 1024; }
-  static constexpr int MAX_BATCH = ((227 * 1024 - 1024 - OFF_PLAN) / 4 - 2) / 2;
+  static constexpr int SMEM = OFF_SCR + SCRATCH + 1024;
+  // the plan's arrays lie in the ring until the first copy goes out
+  static constexpr int MAX_BATCH = (NUNIT * UNIT / 4 - 2) / 2;
   static constexpr int TCOL_S = NU * N;      // O block i at i N, then two S buffers
   static constexpr int TCOLS = (NU + 2) * N;
   static constexpr uint32_t TMEM_COLS = TCOLS <= 64 ? 64u : TCOLS <= 128 ? 128u : TCOLS <= 256 ? 256u : 512u;
-  static constexpr int NTHREADS = 256;
-  static_assert(OFF_COLM + N * 4 <= OFF_PLAN, "scratch");
+  static constexpr int NWG = N >= 32 ? 2 : 1;  // softmax warpgroups, N / NWG rows each
+  static constexpr int NTHREADS = 128 + 128 * NWG;
+  static_assert(OFF_COLM + N * 4 <= OFF_SCR + SCRATCH, "scratch");
   static_assert(R % 128 == 0 && N % 16 == 0 && TCOLS <= 512, "tensor memory");
-  static_assert(NUNIT >= NU + 1, "the ring holds a tile and the next one's first unit");
-  static_assert(smem_bytes(1023) <= 227 * 1024, "shared memory");
+  static_assert(NUNIT >= 2 * NU, "the ring holds two tiles");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 template <int R, int N, bool PAGED>
-__global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ LatentParams p) {
+__global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(const __grid_constant__ LatentParams p) {
   using Gm = LatentGeo<R, N>;
   constexpr int T = Gm::T, NU = Gm::NU;
   extern __shared__ uint8_t smem_raw[];
@@ -141,8 +156,6 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
   const uint32_t sbase = raw + pad;
   auto bar = [&](int i) -> uint32_t { return sbase + Gm::OFF_SCR + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 4);
-  int* lens = reinterpret_cast<int*>(smem + Gm::OFF_PLAN);
-  int* P = lens + p.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -158,11 +171,11 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
     mbar_init(bar(Gm::B_QEMPTY), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Gm::B_S + i), 1);
-      mbar_init(bar(Gm::B_P + i), 128);
+      mbar_init(bar(Gm::B_P + i), 128 * Gm::NWG);
       mbar_init(bar(Gm::B_PV + i), 1);
       mbar_init(bar(Gm::B_FIN + i), 1);
     }
-    mbar_init(bar(Gm::B_OFREE), 128);
+    mbar_init(bar(Gm::B_OFREE), 128 * Gm::NWG);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tm_q);
@@ -173,17 +186,55 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
     tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  build_plan_arrays(p.seq_lens, p.B, p.max_len, kLatentGap, lens, P, 0, Gm::NTHREADS);
-  const Plan pl = latent_plan(p.B, p.U, p.ranges, P);
+  {
+    // this CTA's range of the line and its pieces
+    int* lens = reinterpret_cast<int*>(smem + Gm::OFF_U);
+    int* P = lens + p.B;
+    build_plan_arrays(p.seq_lens, p.B, p.max_len, kLatentGap, lens, P, 0, Gm::NTHREADS);
+    if (threadIdx.x == 0) {
+      const Plan pl = latent_plan(p.B, p.U, p.ranges, P);
+      const int r = blockIdx.x;
+      int count = 0, x = r * pl.q, xe = min(x + pl.q, pl.NB), first = -1;
+      while (r < pl.ranges && x < xe) {
+        Piece pc;
+        x = piece_at(pl, lens, P, p.B, x, xe, r, pc);
+        // a range's list begins after the ranges and segments before it
+        if (first < 0) first = r + pc.u * p.B + pc.b;
+        if (pc.t1 == pc.t0) continue;  // only a gap
+        const int4 e = latent_piece(pc, r);
+        if (count < Gm::PCAP)
+          reinterpret_cast<int4*>(smem + Gm::OFF_PC)[count] = e;
+        else
+          p.pieces[first + count] = e;
+        ++count;
+      }
+      *reinterpret_cast<int*>(smem + Gm::OFF_MISC + 8) = count;
+      *reinterpret_cast<int*>(smem + Gm::OFF_MISC + 12) = first;
+    }
+  }
+  fence_proxy_async_smem();  // the ring's next writes are copies
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MISC);
+  const int npieces = *reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 8);
+  const int4* more = p.pieces + *reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 12);
   pdl_launch_dependents();
 
-  PieceWalker walk;
-  walk.init(blockIdx.x, gridDim.x);
-  Piece pc;
+  struct {
+    int b, t0, t1, u, slot;
+  } pc;
+  // piece i of this CTA
+  auto take = [&](int i) {
+    if (i >= npieces) return false;
+    const int4 e = i < Gm::PCAP ? reinterpret_cast<const int4*>(smem + Gm::OFF_PC)[i] : more[i];
+    pc.b = e.x;
+    pc.t0 = e.y;
+    pc.t1 = e.z;
+    pc.u = e.w & 255;
+    pc.slot = (e.w >> 8) - 1;  // -1: the segment's only piece
+    return true;
+  };
   int n = 0;      // tiles so far (over all pieces)
   int piece = 0;  // pieces so far
   auto wait = [&](int b, int phase) { return wait_bounded(bar(b), (uint32_t)(phase & 1), abort_flag, p.timeout_ns); };
@@ -197,7 +248,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
       const bool second = warp == 3;
       bool ok = true;
       const int rsh = p.box_shift;
-      while (ok && walk.next(pl, lens, P, p.B, true, pc)) {
+      while (ok && take(piece)) {
         if (!second) {
           if (piece > 0 && !(ok = wait(Gm::B_QEMPTY, piece - 1))) break;
           mbar_arrive_expect_tx(bar(Gm::B_QFULL), Gm::Q_BYTES);
@@ -243,15 +294,15 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
                                 page[i]);
             }
           };
+          if (second) {
+            const int slot = n % Gm::NPE, fill = n / Gm::NPE;
+            if (fill > 0 && !(ok = wait(Gm::B_PEEMPTY + slot, fill - 1))) break;
+            load(&p.tm_pe, sbase + Gm::OFF_PE + slot * Gm::PE, bar(Gm::B_PEFULL + slot), 2 * NU, 1);
+          }
           for (int k = second ? 1 : 0; k < NU; k += 2) {
             const int m = n * NU + k, slot = m % Gm::NUNIT, fill = m / Gm::NUNIT;
             if (fill > 0 && !(ok = wait(Gm::B_UEMPTY + slot, fill - 1))) break;
             load(&p.tm_unit, sbase + Gm::OFF_U + slot * Gm::UNIT, bar(Gm::B_UFULL + slot), 2 * k, 2);
-          }
-          if (second && ok) {
-            const int slot = n % Gm::NPE, fill = n / Gm::NPE;
-            if (fill > 0 && !(ok = wait(Gm::B_PEEMPTY + slot, fill - 1))) break;
-            load(&p.tm_pe, sbase + Gm::OFF_PE + slot * Gm::PE, bar(Gm::B_PEFULL + slot), 2 * NU, 1);
           }
           if (!ok) break;
         }
@@ -278,7 +329,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
     // ---- S^T of every tile
     constexpr uint32_t id_s = tc_idesc_bf16(64, N, false, false);
     bool ok = true, issued = false;
-    while (ok && walk.next(pl, lens, P, p.B, true, pc)) {
+    while (ok && take(piece)) {
       ok = wait_all(Gm::B_QFULL, piece);
       for (int t = pc.t0; t < pc.t1 && ok; t += T, ++n) {
         const int sb = n & 1;
@@ -286,6 +337,19 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
         if (n >= 2 && !(ok = wait_all(Gm::B_P + sb, (n >> 1) - 1))) break;
         const int valid = pc.t1 - t;  // tokens of this tile, if below T
         const uint32_t d = tmem + Gm::TCOL_S + sb * N;
+        // the rotated part first: the last unit to land then has 8 products left
+        const int slot_pe = n % Gm::NPE;
+        if (!(ok = wait_all(Gm::B_PEFULL + slot_pe, n / Gm::NPE))) break;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t da = tc_sdesc(sbase + Gm::OFF_PE + slot_pe * Gm::PE, 16, 1024, kTcSwizzle128B);
+          const uint64_t db = tc_sdesc(sbase + Gm::OFF_Q + 2 * NU * N * 128, 16, 1024, kTcSwizzle128B);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tc_mma_ss(d, da + i * 2, db + i * 2, id_s, i > 0);
+          tc_commit(bar(Gm::B_PEEMPTY + slot_pe));
+        }
+        issued = true;
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
           const int m = n * NU + k, slot = m % Gm::NUNIT;
@@ -308,24 +372,15 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               tc_mma_ss(d, da + (i / 4) * (T * 128 / 16) + (i % 4) * 2, db + (i / 4) * (N * 128 / 16) + (i % 4) * 2,
-                        id_s, k > 0 || i > 0);
+                        id_s, true);
           }
           __syncwarp();
         }
         if (!ok) break;
-        const int slot = n % Gm::NPE;
-        if (!(ok = wait_all(Gm::B_PEFULL + slot, n / Gm::NPE))) break;
         if (lane == 0) {
-          tc_fence_after();
-          const uint64_t da = tc_sdesc(sbase + Gm::OFF_PE + slot * Gm::PE, 16, 1024, kTcSwizzle128B);
-          const uint64_t db = tc_sdesc(sbase + Gm::OFF_Q + 2 * NU * N * 128, 16, 1024, kTcSwizzle128B);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tc_mma_ss(d, da + i * 2, db + i * 2, id_s, true);
-          tc_commit(bar(Gm::B_PEEMPTY + slot));
           tc_commit(bar(Gm::B_S + sb));
           if (t + T >= pc.t1) tc_commit(bar(Gm::B_QEMPTY));
         }
-        issued = true;
         __syncwarp();
       }
       ++piece;
@@ -341,7 +396,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
     // ---- O^T += C^T P^T of every tile
     constexpr uint32_t id_o = tc_idesc_bf16(128, N, true, false);
     bool ok = true, issued = false;
-    while (ok && walk.next(pl, lens, P, p.B, true, pc)) {
+    while (ok && take(piece)) {
       // the epilogue has read the last piece's O
       if (piece > 0) ok = wait_all(Gm::B_OFREE, piece - 1);
       for (int t = pc.t0; t < pc.t1 && ok; t += T, ++n) {
@@ -349,7 +404,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
         if (!(ok = wait_all(Gm::B_P + sb, n >> 1))) break;
         if (lane == 0) {
           tc_fence_after();
-          const uint64_t db = tc_sdesc(sbase + Gm::OFF_P + sb * Gm::P_BYTES, 16, 1024, kTcSwizzle128B);
+          const uint64_t db = tc_sdesc(sbase + Gm::OFF_P + (n % Gm::NP) * Gm::P_BYTES, 16, 1024, kTcSwizzle128B);
 #pragma unroll
           for (int k = 0; k < NU; ++k) {
             const int slot = (n * NU + k) % Gm::NUNIT;
@@ -374,23 +429,25 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
     }
     __syncwarp();
   } else {
-    // ---- softmax and epilogue: 4 warps, 128 threads that meet on named barrier 1.  A wait
-    // that gives up only marks the thread; the next vote takes all of them out together.
-    constexpr int NG = N / 8;  // column groups of 8 rows
-    const int w = warp & 3;
+    // ---- softmax and epilogue: each warpgroup has NR rows (columns of S^T and O^T) of its
+    // own, so its 128 threads meet on their own named barrier.  A wait that gives up only
+    // marks the thread; the next vote takes the warpgroup out together.
+    constexpr int NR = N / Gm::NWG;
+    constexpr int NG = NR / 8;  // column groups of 8 rows
+    const int w = warp & 3, wg = (warp >> 2) - 1, cb = wg * NR, mb = 1 + wg;
     const uint32_t lane_addr = (uint32_t)(32 * w) << 16;
-    float* red = reinterpret_cast<float*>(smem + Gm::OFF_RED);
-    float* colv = reinterpret_cast<float*>(smem + Gm::OFF_COL);
-    float* colm = reinterpret_cast<float*>(smem + Gm::OFF_COLM);  // (a slow warp may still rescale by colv)
+    float* red = reinterpret_cast<float*>(smem + Gm::OFF_RED) + cb;
+    float* colv = reinterpret_cast<float*>(smem + Gm::OFF_COL) + cb;
+    float* colm = reinterpret_cast<float*>(smem + Gm::OFF_COLM) + cb;  // (a slow warp may still rescale by colv)
     const float kNegInf = -__int_as_float(0x7f800000);
-    const int c2 = 2 * (lane & 3);  // this thread's rows: 8 g + c2 and the next
+    const int c2 = 2 * (lane & 3);  // this thread's rows: cb + 8 g + c2 and the next
     // where its stmatrix lane writes within P: row 8 (lane / 16) + lane % 8 of a pair of groups,
     // 16-byte chunk 2 w + (lane / 8) % 2 of tokens
     const int st_row = 8 * (lane >> 4) + (lane & 7);
     const uint32_t st_off = (uint32_t)(st_row * 128 + (((2 * w + ((lane >> 3) & 1)) ^ (st_row & 7)) << 4));
     bool ok = true;
-    while (walk.next(pl, lens, P, p.B, true, pc)) {
-      const int L = lens[pc.b];
+    while (take(piece)) {
+      const int L = max(0, min(p.seq_lens ? __ldg(p.seq_lens + pc.b) : p.max_len, p.max_len));
       float m[2 * NG], l[2 * NG];
 #pragma unroll
       for (int i = 0; i < 2 * NG; ++i) {
@@ -408,7 +465,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
           uint32_t r[4 * NG];
 #pragma unroll
           for (int g = 0; g < NG; g += 2)
-            tmem_ld_frag16(tmem + lane_addr + Gm::TCOL_S + sb * N + 8 * g,
+            tmem_ld_frag16(tmem + lane_addr + Gm::TCOL_S + sb * N + cb + 8 * g,
                            *reinterpret_cast<uint32_t(*)[8]>(r + 4 * g));
           tmem_ld_wait();
 #pragma unroll
@@ -424,7 +481,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
           for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int lim = min(L, L - p.q_len + 1 + (pc.u * N + 8 * g + c2 + e) / p.H);
+              const int lim = min(L, L - p.q_len + 1 + (pc.u * N + cb + 8 * g + c2 + e) / p.H);
               x[4 * g + e] = tok < lim ? x[4 * g + e] : kNegInf;
               x[4 * g + 2 + e] = tok + 8 < lim ? x[4 * g + 2 + e] : kNegInf;
             }
@@ -433,8 +490,8 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 2 * NG; ++i)
           past |= fmaxf(x[4 * (i / 2) + i % 2], x[4 * (i / 2) + 2 + i % 2]) > m[i] + 24.f;
-        if (named_bar_any(1, 128, past)) {
-          if (named_bar_any(1, 128, !ok)) {
+        if (named_bar_any(mb, 128, past)) {
+          if (named_bar_any(mb, 128, !ok)) {
             stop = true;
             break;
           }
@@ -447,7 +504,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             if (lane < 4) red[w * N + 8 * (i / 2) + c2 + i % 2] = mx;
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(mb, 128);
 #pragma unroll
           for (int i = 0; i < 2 * NG; ++i) {
             const int c = 8 * (i / 2) + c2 + i % 2;
@@ -457,7 +514,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
             l[i] *= a;
             if (w == 0 && lane < 4) colv[c] = a;
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(mb, 128);
           if (t > pc.t0) {
             // O holds the tiles before this one, once the last of their products is done
             ok = wait(Gm::B_PV + ((n - 1) & 1), (n - 1) >> 1);
@@ -465,21 +522,23 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
-              for (int c0 = 0; c0 < NU * N; c0 += 16) {
+              for (int e = 0; e < NU * NR; e += 16) {
+                const int c0 = e % NR;
+                const uint32_t at = tmem + lane_addr + (e / NR) * N + cb + c0;
                 uint32_t o[16];
-                tmem_ld16(tmem + lane_addr + c0, o);
+                tmem_ld16(at, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * colv[c0 % N + i]);
-                tmem_st16(tmem + lane_addr + c0, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * colv[c0 + i]);
+                tmem_st16(at, o);
               }
               tmem_st_wait();
             }
           }
         }
-        // P^T of this tile; its buffer was last read by the product of tile n - 2
-        if (n >= 2) {
-          ok = wait(Gm::B_PV + sb, (n >> 1) - 1) && ok;
+        // P^T of this tile; its buffer was last read by the product of tile n - NP
+        if (n >= Gm::NP) {
+          ok = wait(Gm::B_PV + ((n - Gm::NP) & 1), (n - Gm::NP) >> 1) && ok;
           ok = __all_sync(0xffffffffu, ok);
         }
 #pragma unroll
@@ -497,7 +556,7 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
               l[i + 1] += bf16hi_to_f32(v);
               pk[2 * h + half] = v;
             }
-          stsm_x4_t(sbase + Gm::OFF_P + sb * Gm::P_BYTES + g * 1024 + st_off, pk[0], pk[1], pk[2], pk[3]);
+          stsm_x4_t(sbase + Gm::OFF_P + (n % Gm::NP) * Gm::P_BYTES + (cb / 8 + g) * 1024 + st_off, pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -518,30 +577,30 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
         }
       }
       ok = wait(Gm::B_PV + ((n - 1) & 1), (n - 1) >> 1) && ok;
-      if (named_bar_any(1, 128, !ok)) break;
+      if (named_bar_any(mb, 128, !ok)) break;
       tc_fence_after();
-      const int row0 = pc.u * N;
-      const int live = min(N, p.rows - row0);  // rows of this tile
-      const bool whole = pc.npieces == 1;
+      const int row0 = pc.u * N + cb;
+      const int live = min(NR, p.rows - row0);  // rows of this warpgroup, if any
+      const int slot = pc.slot;
+      const bool whole = slot < 0;
       // (the meeting above made red and colm visible to all four warps)
-      const int ctid = threadIdx.x - 128;
+      const int ctid = threadIdx.x & 127;
       float lsum = 0.f;
-      if (ctid < N) lsum = (red[ctid] + red[N + ctid]) + (red[2 * N + ctid] + red[3 * N + ctid]);
-      const int slot = latent_slot(walk.r - pc.j, pc.j);
-      if (!whole && ctid < live) p.part_ml[(size_t)slot * N + ctid] = make_float2(colm[ctid], lsum);
-      if (ctid < N) colv[ctid] = whole ? (lsum > 0.f || lsum != lsum ? 1.f / lsum : 0.f) : 1.f;
-      named_bar_sync(1, 128);
+      if (ctid < NR) lsum = (red[ctid] + red[N + ctid]) + (red[2 * N + ctid] + red[3 * N + ctid]);
+      if (!whole && ctid < live) p.part_ml[(size_t)slot * N + cb + ctid] = make_float2(colm[ctid], lsum);
+      if (ctid < NR) colv[ctid] = whole ? (lsum > 0.f || lsum != lsum ? 1.f / lsum : 0.f) : 1.f;
+      named_bar_sync(mb, 128);
 #pragma unroll 1
       for (int k = 0; k < NU; ++k) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < N; c0 += 16) {
+        for (int c0 = 0; c0 < NR; c0 += 16) {
           if (c0 >= live) break;
           uint32_t o[16];
-          tmem_ld16(tmem + lane_addr + k * N + c0, o);
+          tmem_ld16(tmem + lane_addr + k * N + cb + c0, o);
           tmem_ld_wait();
           const int d = k * 128 + 32 * w + lane;  // this lane's latent
           if (!whole) {
-            float* dst = p.part_acc + ((size_t)slot * N + c0) * R + d;
+            float* dst = p.part_acc + ((size_t)slot * N + cb + c0) * R + d;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (c0 + i < live) dst[(size_t)i * R] = __uint_as_float(o[i]);
@@ -573,10 +632,13 @@ __global__ void __launch_bounds__(256, 1) latent_kernel(const __grid_constant__ 
 }
 
 // Merge of the partials: for each row, M = max_j m_j over slots with l_j > 0, w_j =
-// 2^(m_j - M), out = sum_j w_j acc_j / sum_j w_j l_j, in ascending j.  An item is 128
-// latents of a row.  Rows of up to 8 pieces are a warp's work with every load in
-// flight; longer runs take the whole CTA, 16 warps of slots whose sums are added in
-// order.  Rows of empty sequences are zeroed.
+// 2^(m_j - M), out = sum_j w_j acc_j / sum_j w_j l_j.  An item is 128 latents of a row, a
+// float4 a lane.  Rows of up to 32 pieces are a warp's work with 8 loads in flight,
+// summed in ascending j.  A segment of more pieces fills more than 30 ranges, so there
+// are few of them: warp 0 lists them in order, and each of their items takes a CTA, 16
+// warps of slots (10 loads a thread in flight: 160 slots at once) whose sums are added in
+// order.  Rows of empty sequences are zeroed.  All
+// of the plan's work comes before the wait for the split kernel.
 struct LatentCombineParams {
   const float* part_acc;
   const float2* part_ml;
@@ -585,115 +647,124 @@ struct LatentCombineParams {
   int B, rows, U, N, ranges, max_len;
 };
 
+struct LatentCombineGeo {
+  static constexpr int NTHREADS = 512, W = NTHREADS / 32, KB = 8, SHORT = 32;
+  // shared: lane sums, weights of a long run, the list of long segments, the plan
+  static constexpr int OFF_WTS = W * 32 * 16;
+  __host__ __device__ static constexpr int off_list(int ranges) { return OFF_WTS + (ranges + 1 + 3) / 4 * 16; }
+  __host__ __device__ static constexpr int off_plan(int ranges) { return off_list(ranges) + (ranges / (SHORT - 1) + 2 + 3) / 4 * 16; }
+  static constexpr int smem_bytes(int ranges, int B) { return off_plan(ranges) + (2 * B + 2) * 4; }
+};
+
 template <int R>
-__global__ void __launch_bounds__(512) latent_combine_kernel(const LatentCombineParams p) {
+__global__ void __launch_bounds__(512, 2) latent_combine_kernel(const LatentCombineParams p) {
+  using Cg = LatentCombineGeo;
   extern __shared__ __align__(16) uint8_t csm[];
-  float4* lane_sum = reinterpret_cast<float4*>(csm);  // [16][32]
-  int* lens = reinterpret_cast<int*>(csm + 16 * 32 * 16);
+  float4* lane_sum = reinterpret_cast<float4*>(csm);               // [W][32]
+  float* wts = reinterpret_cast<float*>(csm + Cg::OFF_WTS);        // [ranges], then the sum
+  int* list = reinterpret_cast<int*>(csm + Cg::off_list(p.ranges));
+  int* lens = reinterpret_cast<int*>(csm + Cg::off_plan(p.ranges));
   int* P = lens + p.B;
   constexpr int NCH = R / 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float kNegInf = -__int_as_float(0x7f800000);
-  build_plan_arrays(p.seq_lens, p.B, p.max_len, kLatentGap, lens, P, 0, 512);
+  build_plan_arrays(p.seq_lens, p.B, p.max_len, kLatentGap, lens, P, 0, Cg::NTHREADS);
   const Plan pl = latent_plan(p.B, p.U, p.ranges, P);
-  const int nb_max = P[p.B + 1];
-  const bool long_runs = nb_max > 0 && (nb_max - 1) / pl.q + 2 > 8;
+  if (warp == 0) {
+    int count = 0;
+    const int nb_max = P[p.B + 1];
+    if (nb_max > 0 && (nb_max - 1) / pl.q + 2 > Cg::SHORT) {
+      for (int s0 = 0; s0 < p.B * p.U; s0 += 32) {
+        const int seg = s0 + lane;
+        const bool is_long = seg < p.B * p.U && segment_pieces(pl, lens, P, p.B, seg / p.U, seg % p.U) > Cg::SHORT;
+        const unsigned m = __ballot_sync(0xffffffffu, is_long);
+        if (is_long) list[1 + count + __popc(m & ((1u << lane) - 1))] = seg;
+        count += __popc(m);
+      }
+    }
+    if (lane == 0) list[0] = count;
+  }
+  __syncthreads();
   pdl_wait_primary();
 
-  const long long items = (long long)p.B * p.rows * NCH;
-  // an item's row, its segment's pieces and first range
-  auto locate = [&](long long item, long long& row, int& col, int& n, int& r0) {
-    row = item / NCH;
-    const int b = (int)(row / p.rows), in_seq = (int)(row - (long long)b * p.rows);
-    const int u = in_seq / p.N;
-    col = in_seq - u * p.N;
-    n = segment_pieces(pl, lens, P, p.B, b, u);
-    r0 = n > 0 ? (u * P[p.B] + P[b] + pl.gap) / pl.q : 0;
-  };
+  auto first_range = [&](int b, int u) { return (u * P[p.B] + P[b] + pl.gap) / pl.q; };
   auto acc_at = [&](int r0, int j, int col, int ch) {
     return reinterpret_cast<const float4*>(p.part_acc + ((size_t)latent_slot(r0, j) * p.N + col) * R + ch * 128) + lane;
   };
-  auto put = [&](long long row, int ch, float4 s, float den) {
-    const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
+  auto ml_at = [&](int r0, int j, int col) { return __ldcg(p.part_ml + (size_t)latent_slot(r0, j) * p.N + col); };
+  auto is_live = [](float l) { return l > 0.f || l != l; };
+  auto put = [&](int b, int row, int ch, float4 s, float den) {
+    const float inv = is_live(den) ? 1.f / den : 0.f;
     uint2 o;
     o.x = pack_bf16x2(s.x * inv, s.y * inv);
     o.y = pack_bf16x2(s.z * inv, s.w * inv);
-    reinterpret_cast<uint2*>(p.out + row * R + ch * 128)[lane] = o;
+    reinterpret_cast<uint2*>(p.out + ((size_t)b * p.rows + row) * R + ch * 128)[lane] = o;
   };
-  for (long long item = (long long)blockIdx.x * 16 + warp; item < items; item += (long long)gridDim.x * 16) {
-    long long row;
-    int col, n, r0;
-    locate(item, row, col, n, r0);
-    if (n == 1 || n > 8) continue;
-    const int ch = (int)(item % NCH);
-    float4 a[8];
+  // ---- long segments
+  const int nlong = list[0], per_seg = p.N * NCH;
+  for (int item = blockIdx.x; item < nlong * per_seg; item += gridDim.x) {
+    const int seg = list[1 + item / per_seg], in_seg = item % per_seg;
+    const int b = seg / p.U, u = seg % p.U, col = in_seg / NCH, ch = in_seg % NCH;
+    const int row = u * p.N + col;
+    if (row >= p.rows) continue;
+    const int n = segment_pieces(pl, lens, P, p.B, b, u), r0 = first_range(b, u);
+    constexpr int KB = 10;
+    float4 a[KB];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = j < n ? __ldcg(acc_at(r0, j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float2 ml = lane < n ? __ldcg(p.part_ml + (size_t)latent_slot(r0, lane) * p.N + col)
-                               : make_float2(kNegInf, 0.f);
-    const bool live = ml.y > 0.f || ml.y != ml.y;
-    float M = live ? ml.x : kNegInf;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float wgt = live ? exp2_approx(ml.x - M) : 0.f;
-    float den = 0.f;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, wgt, j), lj = __shfl_sync(0xffffffffu, ml.y, j);
-      if (j < n && wj != 0.f) {
-        den += wj * lj;
-        s.x += wj * a[j].x;
-        s.y += wj * a[j].y;
-        s.z += wj * a[j].z;
-        s.w += wj * a[j].w;
-      }
-    }
-    put(row, ch, s, den);
-  }
-  if (!long_runs) return;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    long long row;
-    int col, n, r0;
-    locate(item, row, col, n, r0);
-    if (n <= 8) continue;
-    const int ch = (int)(item % NCH);
-    float4 a[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = warp + 16 * k;
+    for (int k = 0; k < KB; ++k) {
+      const int j = warp + Cg::W * k;
       a[k] = j < n ? __ldcg(acc_at(r0, j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // every warp takes the row's maximum and sum itself
-    float M = kNegInf;
-    for (int j = lane; j < n; j += 32) {
-      const float2 ml = __ldcg(p.part_ml + (size_t)latent_slot(r0, j) * p.N + col);
-      if (ml.y > 0.f || ml.y != ml.y) M = fmaxf(M, ml.x);
-    }
+    if (warp == 0) {  // the weights, while the loads are in flight
+      constexpr int KM = 5;  // 160 slots at a time
+      float2 v[KM];
+      float M = kNegInf;
+      for (int j0 = 0; j0 < n; j0 += 32 * KM) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float den = 0.f;
-    for (int j = lane; j < n; j += 32) {
-      const float2 ml = __ldcg(p.part_ml + (size_t)latent_slot(r0, j) * p.N + col);
-      if (ml.y > 0.f || ml.y != ml.y) den += exp2_approx(ml.x - M) * ml.y;
-    }
+        for (int k = 0; k < KM; ++k) {
+          const int j = j0 + lane + 32 * k;
+          v[k] = j < n ? ml_at(r0, j, col) : make_float2(kNegInf, 0.f);
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        for (int k = 0; k < KM; ++k)
+          if (is_live(v[k].y)) M = fmaxf(M, v[k].x);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      float den = 0.f;
+      for (int j0 = 0; j0 < n; j0 += 32 * KM) {
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+          const int j = j0 + lane + 32 * k;
+          if (n > 32 * KM) v[k] = j < n ? ml_at(r0, j, col) : make_float2(kNegInf, 0.f);
+          const float wj = is_live(v[k].y) ? exp2_approx(v[k].x - M) : 0.f;
+          if (j < n) wts[j] = wj;
+          if (wj != 0.f) den += wj * v[k].y;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      if (lane == 0) wts[p.ranges] = den;
+    }
+    __syncthreads();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = warp; j0 < n; j0 += 64) {
+    for (int j0 = warp; j0 < n; j0 += KB * Cg::W) {
+      if (j0 != warp) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = j0 + 16 * k;
-        if (j0 != warp) a[k] = j < n ? __ldcg(acc_at(r0, j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < n) {
-          const float2 ml = __ldcg(p.part_ml + (size_t)latent_slot(r0, j) * p.N + col);
-          const float wj = ml.y > 0.f || ml.y != ml.y ? exp2_approx(ml.x - M) : 0.f;
-          if (wj != 0.f) {
-            s.x += wj * a[k].x;
-            s.y += wj * a[k].y;
-            s.z += wj * a[k].z;
-            s.w += wj * a[k].w;
-          }
+        for (int k = 0; k < KB; ++k) {
+          const int j = j0 + Cg::W * k;
+          a[k] = j < n ? __ldcg(acc_at(r0, j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const int j = j0 + Cg::W * k;
+        const float wj = j < n ? wts[j] : 0.f;
+        if (wj != 0.f) {
+          s.x += wj * a[k].x;
+          s.y += wj * a[k].y;
+          s.z += wj * a[k].z;
+          s.w += wj * a[k].w;
         }
       }
     }
@@ -701,16 +772,57 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const LatentCombine
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-      for (int k = 1; k < 16; ++k) {
+      for (int k = 1; k < Cg::W; ++k) {
         const float4 v = lane_sum[k * 32 + lane];
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
         s.w += v.w;
       }
-      put(row, ch, s, den);
+      put(b, row, ch, s, wts[p.ranges]);
     }
     __syncthreads();
+  }
+  // ---- short segments and empty sequences
+  const unsigned items = (unsigned)p.B * p.rows * NCH;
+  for (unsigned item = blockIdx.x * Cg::W + warp; item < items; item += gridDim.x * Cg::W) {
+    const int ch = item % NCH, grow = item / NCH;
+    const int b = grow / p.rows, row = grow - b * p.rows;
+    const int u = row / p.N, col = row - u * p.N;
+    const int n = segment_pieces(pl, lens, P, p.B, b, u);
+    if (n == 1 || n > Cg::SHORT) continue;
+    const int r0 = n > 0 ? first_range(b, u) : 0;
+    float4 a[Cg::KB];
+#pragma unroll
+    for (int j = 0; j < Cg::KB; ++j)
+      a[j] = j < n ? __ldcg(acc_at(r0, j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float2 ml = lane < n ? ml_at(r0, lane, col) : make_float2(kNegInf, 0.f);
+    const bool live = is_live(ml.y);
+    float M = live ? ml.x : kNegInf;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float wgt = live ? exp2_approx(ml.x - M) : 0.f;
+    float den = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < n; j0 += Cg::KB) {
+      if (j0 > 0) {
+#pragma unroll
+        for (int j = 0; j < Cg::KB; ++j)
+          a[j] = j0 + j < n ? __ldcg(acc_at(r0, j0 + j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < Cg::KB; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, wgt, j0 + j), lj = __shfl_sync(0xffffffffu, ml.y, j0 + j);
+        if (j0 + j < n && wj != 0.f) {
+          den += wj * lj;
+          s.x += wj * a[j].x;
+          s.y += wj * a[j].y;
+          s.z += wj * a[j].z;
+          s.w += wj * a[j].w;
+        }
+      }
+    }
+    put(b, row, ch, s, den);
   }
 }
 

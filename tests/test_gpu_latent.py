@@ -164,15 +164,17 @@ def test_many_sequences(H):
 
 
 def test_batch_limit_and_workspace_refusals():
-    n = binding.latent_max_batch(64, 512)
-    c = make(10, [3] * n, 1, 64, 512, 3)
-    check(run(c), c, "batch limit", sequences=[0, n // 2, n - 1])
-    q = torch.zeros(n + 1, 1, 64, 576, device="cuda", dtype=torch.bfloat16)
+    n = binding.latent_max_batch(1, 128)
+    lens = np.full(n, 3, np.int32)
+    lens[::3] = 0
+    c = make(10, lens, 1, 1, 128, 3)
+    check(run(c), c, "batch limit", sequences=[0, 1, 2, n // 2, n - 2, n - 1])
+    q = torch.zeros(n + 1, 1, 1, 192, device="cuda", dtype=torch.bfloat16)
     with pytest.raises(binding.DecodeAttnError):
-        binding.latent_attn_contig(q, torch.zeros(n + 1, 4, 576, device="cuda", dtype=torch.bfloat16), scale=1.0)
-    small = binding.latent_workspace(4, 64, 512)[:-16]
+        binding.latent_attn_contig(q, torch.zeros(n + 1, 4, 192, device="cuda", dtype=torch.bfloat16), scale=1.0)
+    small = binding.latent_workspace(4, 1, 128)[:-16]
     with pytest.raises(binding.DecodeAttnError):
-        binding.latent_attn_contig(q[:4], torch.zeros(4, 4, 576, device="cuda", dtype=torch.bfloat16), scale=1.0,
+        binding.latent_attn_contig(q[:4], torch.zeros(4, 4, 192, device="cuda", dtype=torch.bfloat16), scale=1.0,
                                    workspace=small)
 
 
