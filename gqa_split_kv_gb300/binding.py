@@ -467,37 +467,40 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "plain", f
     return torch.from_numpy(w).to("cuda" if device is None else device)
 
 
-def _here(*tensors):
-    """The current device's index; every tensor (None: skipped) must be on it."""
-    import torch
-    at = {t.get_device() for t in tensors if t is not None}
-    if -1 in at or at != {torch.cuda.current_device()}:
-        raise ValueError("expected every tensor on the current CUDA device, got "
-                         f"{[str(t.device) for t in tensors if t is not None]}")
-    return at.pop()
+# The checks below run on every call, and a decode step's kernels take a few
+# microseconds: torch is looked up once, and a tensor that is as it should be costs four
+# attribute reads.
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _plain(t, name, dtype, shape, dev):
+    """t must be a contiguous tensor of this type and shape on CUDA device dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+
+
+def _on_current(dev: int):
+    """The library launches on the current device: the tensors' device dev must be that one."""
+    if dev < 0 or dev != _torch._C._cuda_getDevice():
+        raise ValueError("expected tensors on the current CUDA device, got them on "
+                         + (f"cuda:{dev}" if dev >= 0 else "the CPU"))
 
 
 def _raw_stream(stream, dev: int) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _shape(t, name, *want):
-    """t's shape: every entry of want that is not None must match."""
-    if t.dim() != len(want) or any(w is not None and w != n for w, n in zip(want, t.shape)):
-        raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in want)}, "
-                         f"got {tuple(t.shape)}")
-
-
-def _plain(t, name, dtype, *want):
-    """A contiguous tensor of this type and shape."""
-    if t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor, got {t.dtype}, strides {t.stride()}")
-    _shape(t, name, *want)
 
 
 def _token_stride(t, name, lead: int):
@@ -523,91 +526,118 @@ def rope_apply(x, positions, inv_freq, offset: int = 0, interleaved: bool = Fals
     positions int32 [T] or [B, T], inv_freq float64 [rot / 2] (rope_inv_freq).  Elements [offset, offset + rot)
     of every head are rotated, pairs (j, j + rot / 2) or, interleaved, (2j, 2j + 1); with backward, the gradient
     of that.  out: x itself (in place) or a tensor of x's shape.  Returns out."""
-    import torch
-    dtype = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(x.dtype)
-    if dtype is None or x.dim() not in (3, 4):
-        raise ValueError(f"x: expected bf16, fp16 or fp32 [T, H, D] or [B, T, H, D], got {x.dtype} {tuple(x.shape)}")
-    _plain(positions, "positions", torch.int32, *x.shape[:-2])
-    _plain(inv_freq, "inv_freq", torch.float64, None)
+    torch = _torch or _t()
+    xd = x.dtype
+    dtype = 0 if xd is torch.bfloat16 else 1 if xd is torch.float16 else 2 if xd is torch.float32 else None
+    shape = x.shape
+    lead = len(shape) - 2
+    if dtype is None or lead not in (1, 2):
+        raise ValueError(f"x: expected bf16, fp16 or fp32 [T, H, D] or [B, T, H, D], got {xd} {tuple(shape)}")
+    dev = x.get_device()
+    _plain(positions, "positions", torch.int32, shape[:-2], dev)
+    rot = inv_freq.shape
+    _plain(inv_freq, "inv_freq", torch.float64, (rot[0] if rot else 0,), dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.dtype != x.dtype or out.shape != x.shape:
-        raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
-    lead = x.dim() - 2
-    H, D = x.shape[-2:]
+        out = torch.empty(shape, dtype=xd, device=x.device)
+    elif out.dtype is not xd or out.shape != shape or out.get_device() != dev:
+        raise ValueError(f"out: expected {xd} {tuple(shape)} on cuda:{dev}, got {out.dtype} {tuple(out.shape)} on "
+                         f"{out.device}")
     xt, ot = _token_stride(x, "x", lead), _token_stride(out, "out", lead)
-    dev = _here(x, positions, inv_freq, out)
-    _check("rope_apply", load().rope_apply(
-        x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), positions.numel(), H, D, offset,
-        2 * inv_freq.shape[0], int(interleaved), magnitude, int(backward), dtype, xt, x.stride(-2), ot,
-        out.stride(-2), _raw_stream(stream, dev)))
+    _on_current(dev)
+    st = (_lib or load()).rope_apply(
+        x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), positions.numel(), shape[-2],
+        shape[-1], offset, 2 * rot[0], 1 if interleaved else 0, magnitude, 1 if backward else 0, dtype, xt,
+        x.stride(-2), ot, out.stride(-2), _raw_stream(stream, dev))
+    if st:
+        raise DecodeAttnError("rope_apply", st)
     return out
 
 
-def _rope_args(inv_freq, offset, interleaved, magnitude):
-    import torch
+def _rope_args(inv_freq, offset, interleaved, magnitude, dev):
     if inv_freq is None:
         return None, 0, 0, 0, 1.0
-    _plain(inv_freq, "inv_freq", torch.float64, None)
-    return inv_freq.data_ptr(), offset, 2 * inv_freq.shape[0], int(interleaved), magnitude
+    n = inv_freq.shape
+    _plain(inv_freq, "inv_freq", _torch.float64, (n[0] if n else 0,), dev)
+    return inv_freq.data_ptr(), offset, 2 * n[0], 1 if interleaved else 0, magnitude
 
 
-def _new_tokens(k_new, v_new, v):
-    """Checks the new tokens [B, q_len, Hkv, D] (v_new None with v None); returns their token strides."""
-    import torch
-    if (v_new is None) != (v is None):
-        raise ValueError("v_new and v: both tensors, or both None to write keys only")
-    strides = []
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        if t is None:
-            strides.append(0)
-            continue
-        if t.dtype != torch.bfloat16 or t.dim() != 4:
-            raise ValueError(f"{name}: expected bf16 [B, q_len, Hkv, D], got {t.dtype} {tuple(t.shape)}")
-        if t.shape[2] > 1 and t.stride(2) != t.shape[3]:
-            raise ValueError(f"{name}: a token's heads must be consecutive, got strides {t.stride()}")
-        _shape(t, name, *k_new.shape)
-        step = _token_stride(t, name, 2)
-        strides.append(step if t.shape[0] * t.shape[1] > 1 else t.shape[2] * t.shape[3])
-    return strides
+def _new_tokens(t, name, shape, dev):
+    """The token stride of new tokens [B, q_len, Hkv, D], a token's heads consecutive."""
+    if t.dtype is not _torch.bfloat16 or t.shape != shape or len(shape) != 4 or t.get_device() != dev:
+        raise ValueError(f"{name}: expected bf16 [B, q_len, Hkv, D], here {tuple(shape)}, on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    B, n, H, D = shape
+    if t.is_contiguous():
+        return H * D
+    if H > 1 and t.stride(2) != D:
+        raise ValueError(f"{name}: a token's heads must be consecutive, got strides {t.stride()}")
+    return _token_stride(t, name, 2) if B * n > 1 else H * D
 
 
-def _check_cache(k, v, k_scale, v_scale, seq_lens, B, H, D, page_table):
-    """Checks a cache against the call's batch and heads; returns (rows of a slab, page-table columns)."""
-    import torch
-    dtype = torch.bfloat16 if k_scale is None else torch.int8
-    slabs, slab = k.shape[:2] if k.dim() == 4 else (None, None)
+def _check_cache(k, v, k_scale, v_scale, page_table, seq_lens, B, H, D, dev):
+    """Checks a cache against the call's batch and heads; returns the size arguments that follow head_dim."""
+    torch = _torch
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"k: expected 4 dims, got {tuple(shape)}")
+    slabs, slab = shape[0], shape[1]
     if page_table is None:
-        slabs = B
+        slabs, where = B, (slab,)
     else:
-        _plain(page_table, "page_table", torch.int32, B, None)
-    for t, s, name in ((k, k_scale, "k"), (v, v_scale, "v")):
-        if t is None:
-            continue
-        _plain(t, name, dtype, slabs, slab, H, D)
-        if dtype == torch.int8:
-            if s is None:
-                raise ValueError(f"{name}: an int8 cache needs its scales")
-            _plain(s, f"{name}_scale", torch.float32, slabs, H, slab)
+        pt = page_table.shape
+        cols = pt[1] if len(pt) == 2 else 0
+        _plain(page_table, "page_table", torch.int32, (B, cols), dev)
+        where = (slab, cols, slabs)
+        if seq_lens is None:
+            raise ValueError("seq_lens: a paged cache needs them")
     if seq_lens is not None:
-        _plain(seq_lens, "seq_lens", torch.int32, B)
-    elif page_table is not None:
-        raise ValueError("seq_lens: a paged cache needs them")
-    return slab, None if page_table is None else page_table.shape[1]
+        _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    want = (slabs, slab, H, D)
+    if k_scale is None:
+        _plain(k, "k", torch.bfloat16, want, dev)
+        if v is not None:
+            _plain(v, "v", torch.bfloat16, want, dev)
+    else:
+        _plain(k, "k", torch.int8, want, dev)
+        _plain(k_scale, "k_scale", torch.float32, (slabs, H, slab), dev)
+        if v is not None:
+            if v_scale is None:
+                raise ValueError("v: an int8 cache needs its scales")
+            _plain(v, "v", torch.int8, want, dev)
+            _plain(v_scale, "v_scale", torch.float32, (slabs, H, slab), dev)
+    return where
 
 
 def _kv_write(fn, k_new, v_new, k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, inv_freq, offset,
               interleaved, magnitude, stream):
-    ks, vs = _new_tokens(k_new, v_new, v)
-    B, n, H, D = k_new.shape
-    slab, cols = _check_cache(k, v, k_scale, v_scale, seq_lens, B, H, D, page_table)
-    dev = _here(k_new, v_new, k, v, k_scale, v_scale, page_table, seq_lens, inv_freq)
-    where = (slab,) if page_table is None else (slab, cols, k.shape[0], int(max_seq_len))
-    table = () if page_table is None else (page_table.data_ptr(),)
-    scales = () if k_scale is None else (k_scale.data_ptr(), _addr(v_scale))
-    _check(fn, getattr(load(), fn)(k_new.data_ptr(), _addr(v_new), ks, vs, *table, _addr(seq_lens), B, n, H, D, *where,
-                                   *_rope_args(inv_freq, offset, interleaved, magnitude), k.data_ptr(), _addr(v),
-                                   *scales, _raw_stream(stream, dev)))
+    _t()
+    dev = k_new.get_device()
+    shape = k_new.shape
+    ks = _new_tokens(k_new, "k_new", shape, dev)
+    if v_new is None:
+        vs = 0
+        if v is not None:
+            raise ValueError("v_new and v: both tensors, or both None to write keys only")
+    else:
+        vs = _new_tokens(v_new, "v_new", shape, dev)
+        if v is None:
+            raise ValueError("v_new and v: both tensors, or both None to write keys only")
+    B, n, H, D = shape
+    where = _check_cache(k, v, k_scale, v_scale, page_table, seq_lens, B, H, D, dev)
+    rope = _rope_args(inv_freq, offset, interleaved, magnitude, dev)
+    _on_current(dev)
+    call = getattr(_lib or load(), fn)
+    if page_table is None:
+        head = (k_new.data_ptr(), _addr(v_new), ks, vs, _addr(seq_lens), B, n, H, D, *where, *rope)
+    else:
+        head = (k_new.data_ptr(), _addr(v_new), ks, vs, page_table.data_ptr(), seq_lens.data_ptr(), B, n, H, D, *where,
+                max_seq_len, *rope)
+    if k_scale is None:
+        st = call(*head, k.data_ptr(), _addr(v), _raw_stream(stream, dev))
+    else:
+        st = call(*head, k.data_ptr(), _addr(v), k_scale.data_ptr(), _addr(v_scale), _raw_stream(stream, dev))
+    if st:
+        raise DecodeAttnError(fn, st)
 
 
 def kv_write_contig(k_new, v_new, k, v, seq_lens=None, inv_freq=None, offset: int = 0, interleaved: bool = False,
@@ -646,32 +676,39 @@ def kv_write_int8_paged(k_new, v_new, k_pool_i8, v_pool_i8, k_scale_pool, v_scal
               seq_lens, max_seq_len, inv_freq, offset, interleaved, magnitude, stream)
 
 
-def _kv_read(fn, k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, n_tokens, starts, k_out, v_out, stream):
-    import torch
-    if k.dim() != 4:
-        raise ValueError(f"k: expected 4 dims, got {tuple(k.shape)}")
-    B = k.shape[0] if page_table is None else page_table.shape[0]
-    H, D = k.shape[2:]
-    n = int(n_tokens)
-    slab, cols = _check_cache(k, v, k_scale, v_scale, seq_lens, B, H, D, page_table)
+def _kv_read(fn, k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, n, starts, k_out, v_out, stream):
+    torch = _t()
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"k: expected 4 dims, got {tuple(shape)}")
+    dev = k.get_device()
+    B = shape[0] if page_table is None else page_table.shape[0]
+    H, D = shape[2], shape[3]
+    where = _check_cache(k, v, k_scale, v_scale, page_table, seq_lens, B, H, D, dev)
     if starts is not None:
-        _plain(starts, "starts", torch.int32, B)
+        _plain(starts, "starts", torch.int32, (B,), dev)
+    want = (B, n, H, D)
     if k_out is None:
-        k_out = torch.zeros((B, n, H, D), dtype=torch.bfloat16, device=k.device)
-    if v_out is None and v is not None:
-        v_out = torch.zeros((B, n, H, D), dtype=torch.bfloat16, device=k.device)
-    _plain(k_out, "k_out", torch.bfloat16, B, n, H, D)
+        k_out = torch.zeros(want, dtype=torch.bfloat16, device=k.device)
+    else:
+        _plain(k_out, "k_out", torch.bfloat16, want, dev)
     if v is None:
         if v_out is not None:
             raise ValueError("v_out: no v to read")
+    elif v_out is None:
+        v_out = torch.zeros(want, dtype=torch.bfloat16, device=k.device)
     else:
-        _plain(v_out, "v_out", torch.bfloat16, B, n, H, D)
-    dev = _here(k, v, k_scale, v_scale, page_table, seq_lens, starts, k_out, v_out)
-    where = (slab,) if page_table is None else (slab, cols, k.shape[0], int(max_seq_len))
-    table = () if page_table is None else (page_table.data_ptr(),)
+        _plain(v_out, "v_out", torch.bfloat16, want, dev)
+    _on_current(dev)
     scales = () if k_scale is None else (k_scale.data_ptr(), _addr(v_scale))
-    _check(fn, getattr(load(), fn)(k.data_ptr(), _addr(v), *scales, *table, _addr(starts), _addr(seq_lens), B, n, H, D,
-                                   *where, k_out.data_ptr(), _addr(v_out), _raw_stream(stream, dev)))
+    if page_table is None:
+        place = (_addr(starts), _addr(seq_lens), B, n, H, D, *where)
+    else:
+        place = (page_table.data_ptr(), _addr(starts), seq_lens.data_ptr(), B, n, H, D, *where, max_seq_len)
+    st = getattr(_lib or load(), fn)(k.data_ptr(), _addr(v), *scales, *place, k_out.data_ptr(), _addr(v_out),
+                                     _raw_stream(stream, dev))
+    if st:
+        raise DecodeAttnError(fn, st)
     return k_out, v_out
 
 
@@ -718,7 +755,7 @@ def latent_max_batch(num_heads: int, latent_dim: int, q_len: int = 1) -> int:
 def latent_workspace(batch: int, num_heads: int, latent_dim: int, q_len: int = 1):
     """A workspace for latent_attn_* calls of this shape on the current CUDA device (uint8).  A program may keep
     one; calls that share it must not overlap on the GPU."""
-    import torch
+    torch = _t()
     n = load().latent_workspace_bytes(batch, q_len, num_heads, latent_dim, 0)
     if n < 0:
         raise DecodeAttnError("latent_workspace_bytes", -n)
@@ -726,32 +763,41 @@ def latent_workspace(batch: int, num_heads: int, latent_dim: int, q_len: int = 1
 
 
 def _latent(fn, q, cache, page_table, seq_lens, max_seq_len, scale, workspace, out, stream):
-    import torch
+    torch = _t()
     bf16 = torch.bfloat16
-    _plain(q, "q", bf16, None, None, None, None)
-    B, n, H, W = q.shape
+    shape, cs = q.shape, cache.shape
+    if len(shape) != 4 or len(cs) != 3:
+        raise ValueError(f"q, cache: expected 4 and 3 dims, got {tuple(shape)} and {tuple(cs)}")
+    B, n, H, W = shape
     R = W - LATENT_ROPE
-    _plain(cache, "cache", bf16, B if page_table is None else None, None, W)
+    dev = q.get_device()
+    _plain(q, "q", bf16, shape, dev)
+    _plain(cache, "cache", bf16, (B if page_table is None else cs[0], cs[1], W), dev)
     if page_table is not None:
-        _plain(page_table, "page_table", torch.int32, B, None)
+        pt = page_table.shape
+        _plain(page_table, "page_table", torch.int32, (B, pt[1] if len(pt) == 2 else 0), dev)
+        if seq_lens is None:
+            raise ValueError("seq_lens: a paged cache needs them")
     if seq_lens is not None:
-        _plain(seq_lens, "seq_lens", torch.int32, B)
-    elif page_table is not None:
-        raise ValueError("seq_lens: a paged cache needs them")
+        _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
     if out is None:
         out = torch.empty((B, n, H, max(R, 0)), dtype=bf16, device=q.device)
-    _plain(out, "out", bf16, B, n, H, R)
-    dev = _here(q, cache, page_table, seq_lens, workspace, out)
+    else:
+        _plain(out, "out", bf16, (B, n, H, R), dev)
+    _on_current(dev)
     if workspace is None:
         workspace = latent_workspace(B, H, R, n)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace: expected a contiguous tensor")
-    slabs, slab = cache.shape[:2]
-    where = (slab,) if page_table is None else (slab, page_table.shape[1], slabs, int(max_seq_len))
-    table = () if page_table is None else (page_table.data_ptr(),)
-    _check(fn, getattr(load(), fn)(q.data_ptr(), cache.data_ptr(), *table, _addr(seq_lens), B, n, H, R, *where, scale,
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
-                                   _raw_stream(stream, dev)))
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
+    size = workspace.numel() * workspace.element_size()
+    if page_table is None:
+        place = (_addr(seq_lens), B, n, H, R, cs[1])
+    else:
+        place = (page_table.data_ptr(), seq_lens.data_ptr(), B, n, H, R, cs[1], pt[1], cs[0], max_seq_len)
+    st = getattr(_lib or load(), fn)(q.data_ptr(), cache.data_ptr(), *place, scale, workspace.data_ptr(), size,
+                                     out.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        raise DecodeAttnError(fn, st)
     return out
 
 
