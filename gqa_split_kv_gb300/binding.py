@@ -38,6 +38,7 @@ __all__ = [
     "kv_read_int8_paged",
     "latent_attn_contig",
     "latent_attn_paged",
+    "latent_prefill_contig",
     "latent_workspace",
     "latent_max_batch",
     "device_error",
@@ -118,6 +119,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "kv_read_int8_paged": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
         "latent_attn_contig": [vp, vp, vp, i, i, i, i, i, f, vp, ll, vp, vp],
         "latent_attn_paged": [vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, ll, vp, vp],
+        "latent_prefill_contig": [vp, vp, vp, vp, vp, i, i, i, i, i, ll, ll, ll, f, vp, vp],
         "latent_workspace_bytes": [i, i, i, i, i],
         "latent_max_batch": [i, i, i],
     }.items():
@@ -813,6 +815,59 @@ def latent_attn_paged(q, pool, page_table, seq_lens, max_seq_len: int, *, scale:
                       stream=None):
     """latent_attn_contig over a page pool [num_pages, page_size, R + 64]; page_table int32 [B, max_pages]."""
     return _latent("latent_attn_paged", q, pool, page_table, seq_lens, max_seq_len, scale, workspace, out, stream)
+
+
+def _cache_strides(t, name, want, dev):
+    """(token, head) strides of keys or values [B, ctx, H, D] (or [B, ctx, D]): a head's elements consecutive, batch
+    entries ctx tokens apart.  Strides that no element is reached by are taken as dense."""
+    if t.dtype is not _torch.bfloat16 or t.shape != want or t.get_device() != dev:
+        raise ValueError(f"{name}: expected bf16 {tuple(want)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    st = t.stride()
+    B, ctx = want[0], want[1]
+    H, D = (want[2], want[3]) if len(want) == 4 else (1, want[2])
+    head = st[2] if H > 1 else D
+    dense = -(-((H - 1) * head + D) // 8) * 8
+    step = st[1] if ctx > 1 else st[0] if B > 1 and ctx == 1 else dense
+    if ctx and D and (st[-1] != 1 or (B > 1 and st[0] != ctx * step)):
+        raise ValueError(f"{name}: a head's elements must be consecutive and batch entries max_ctx tokens apart, got "
+                         f"strides {st}")
+    return step, head
+
+
+def latent_prefill_contig(q, k_nope, k_rope, v, seq_lens=None, *, scale: float, out=None, stream=None):
+    """Causal prefill of the last q_len tokens over keys and values expanded from latent vectors: q bf16
+    [B, q_len, H, D + 64] (token-major), k_nope and v bf16 [B, max_ctx, H, D] (D 64 or 128; equally strided, e.g.
+    the halves of one expansion), k_rope bf16 [B, max_ctx, 64], shared by the heads (tokens may be strided, e.g. the
+    last columns of a latent cache); seq_lens int32 [B] or None.  Returns out bf16 [B, q_len, H, D]."""
+    torch = _t()
+    bf16 = torch.bfloat16
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q: expected 4 dims, got {tuple(shape)}")
+    B, n, H, W = shape
+    D = W - LATENT_ROPE
+    dev = q.get_device()
+    _plain(q, "q", bf16, shape, dev)
+    ctx = k_nope.shape[1] if k_nope.dim() == 4 else 0
+    kts, khs = _cache_strides(k_nope, "k_nope", (B, ctx, H, D), dev)
+    vts, vhs = _cache_strides(v, "v", (B, ctx, H, D), dev)
+    pts, _ = _cache_strides(k_rope, "k_rope", (B, ctx, LATENT_ROPE), dev)
+    if (kts, khs) != (vts, vhs):
+        raise ValueError(f"v: expected the strides of k_nope, got {v.stride()} and {k_nope.stride()}")
+    if seq_lens is not None:
+        _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((B, n, H, max(D, 0)), dtype=bf16, device=q.device)
+    else:
+        _plain(out, "out", bf16, (B, n, H, D), dev)
+    _on_current(dev)
+    st = (_lib or load()).latent_prefill_contig(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
+                                                _addr(seq_lens), B, n, H, D, ctx, kts, khs, pts, scale, out.data_ptr(),
+                                                _raw_stream(stream, dev))
+    if st:
+        raise DecodeAttnError("latent_prefill_contig", st)
+    return out
 
 
 def selftest_bounded_wait(timeout_ns: int, stream=None) -> None:

@@ -1,5 +1,6 @@
 // Entry points of latent attention (declared in include/decode_attn.h): the absorbed
-// form over a contiguous or paged latent cache.
+// form over a contiguous or paged latent cache, and the prefill over expanded keys and
+// values.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -13,6 +14,7 @@
 #include "device_error.cuh"
 #include "host_util.cuh"
 #include "latent_kernel.cuh"
+#include "latent_prefill.cuh"
 
 namespace da {
 
@@ -187,6 +189,57 @@ int latent_call(bool paged, const void* q, const void* cache, const int* page_ta
   }
 }
 
+template <int D>
+int launch_latent_prefill(LatentPrefillParams& prm, const void* k, const void* k_rope, const void* v,
+                          long long token_stride, long long head_stride, long long rope_stride, int dev,
+                          cudaStream_t st) {
+  using Gm = LatentPrefillGeo<D>;
+  static bool done[kMaxDevices] = {false}, fits[kMaxDevices] = {false};
+  if (int e = allow_smem(latent_prefill_kernel<D>, Gm::SMEM, done, dev)) return e;
+  {
+    // the softmax warpgroups raise their registers out of what the launch gave the CTA; a
+    // build whose per-thread count is below the split would wait for ever, so it is refused
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!fits[dev]) {
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, latent_prefill_kernel<D>) != cudaSuccess) {
+        cudaGetLastError();
+        return DA_ERR_CUDA;
+      }
+      if (fa.numRegs * Gm::NTHREADS < Gm::REG_POOL_NEEDED) return DA_ERR_UNSUPPORTED;
+      fits[dev] = true;
+    }
+  }
+  const cuuint64_t L = (cuuint64_t)prm.max_len, H = (cuuint64_t)prm.H, B = (cuuint64_t)prm.B;
+  const cuuint64_t ts = (cuuint64_t)token_stride * 2, hs = (cuuint64_t)head_stride * 2;
+  const cuuint64_t dims[5] = {64, L, D / 64, H, B}, strides[4] = {ts, 128, hs, ts * L};
+  const cuuint32_t box_k[5] = {64, 128, 1, 1, 1}, box_v[5] = {64, (cuuint32_t)Gm::VKEYS, D / 64, 1, 1};
+  const cuuint64_t dims_pe[3] = {64, L, B}, strides_pe[2] = {(cuuint64_t)rope_stride * 2, (cuuint64_t)rope_stride * 2 * L};
+  const cuuint32_t box_pe[3] = {64, 128, 1};
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (int e = encode_map_t(&prm.tm_k, bf16, sw, k, 5, dims, strides, box_k)) return e;
+  if (int e = encode_map_t(&prm.tm_v, bf16, sw, v, 5, dims, strides, box_v)) return e;
+  if (int e = encode_map_t(&prm.tm_pe, bf16, sw, k_rope, 3, dims_pe, strides_pe, box_pe)) return e;
+  {
+    // launch groups of (b, h) units whose K/V fit in about 48 MB of L2 together
+    const long long unit_bytes = 4LL * D * prm.max_len, units = (long long)prm.B * prm.H;
+    long long g = (48LL << 20) / unit_bytes;
+    g = g < 1 ? 1 : g;
+    prm.grp = (int)(g < units ? g : units);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)prm.nqb * prm.B * prm.H));
+  cfg.blockDim = dim3(Gm::NTHREADS);
+  cfg.dynamicSmemBytes = (size_t)Gm::SMEM;
+  cfg.stream = st;
+  if (cudaLaunchKernelEx(&cfg, latent_prefill_kernel<D>, prm) != cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_CUDA;
+  }
+  return DA_OK;
+}
+
 }  // namespace
 }  // namespace da
 
@@ -226,4 +279,48 @@ extern "C" int latent_attn_paged(const void* q, const void* pool, const int* pag
   return latent_call(true, q, pool, page_table, seq_lens, batch, q_len, num_heads, latent_dim, cap, page_size,
                      max_pages_per_seq, num_pages, scale, workspace, workspace_bytes, out,
                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                                     const int* seq_lens, int batch, int q_len, int num_heads, int head_dim,
+                                     int max_ctx, long long kv_token_stride, long long kv_head_stride,
+                                     long long rope_token_stride, float scale, void* out, void* stream) {
+  if (batch < 0 || q_len < 0 || num_heads < 1 || max_ctx < 0 || !std::isfinite(scale)) return DA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return DA_ERR_UNSUPPORTED;
+  if (batch == 0 || q_len == 0) return DA_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4)) return DA_ERR_INVALID_ARG;
+  const int BQ = LatentPrefillGeo<128>::BQ;
+  const long long nqb = ((long long)q_len + BQ - 1) / BQ;
+  if (nqb * batch > 0x7fffffffLL / num_heads) return DA_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (max_ctx == 0) {
+    if (cudaMemsetAsync(out, 0, (size_t)batch * q_len * num_heads * head_dim * 2, st) != cudaSuccess) {
+      cudaGetLastError();
+      return DA_ERR_CUDA;
+    }
+    return DA_OK;
+  }
+  if (!k_nope || !k_rope || !v || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16))
+    return DA_ERR_INVALID_ARG;
+  if (kv_head_stride < head_dim || kv_head_stride % 8 || kv_token_stride % 8 ||
+      kv_token_stride < (num_heads - 1) * kv_head_stride + head_dim || rope_token_stride < 64 || rope_token_stride % 8)
+    return DA_ERR_INVALID_ARG;
+  int dev, sms, optin;
+  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
+  LatentPrefillParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.seq_lens = seq_lens;
+  prm.B = batch;
+  prm.q_len = q_len;
+  prm.H = num_heads;
+  prm.nqb = (int)nqb;
+  prm.max_len = max_ctx;
+  prm.scale_log2 = scale * kLog2e;
+  prm.timeout_ns = kWaitTimeoutNs;
+  return head_dim == 64 ? launch_latent_prefill<64>(prm, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
+                                                    rope_token_stride, dev, st)
+                        : launch_latent_prefill<128>(prm, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
+                                                     rope_token_stride, dev, st);
 }

@@ -1,0 +1,405 @@
+// Causal prefill over keys and values expanded from latent vectors (the expanded form
+// of latent attention), on the 5th-generation tensor cores.
+//
+// Head h's key at token t is [k_nope[t, h], k_rope[t]]: D elements of its own and 64
+// rotated ones that all heads share, read from one place.  Values have D elements.
+//   S = q[0:D] k_nope^T + q[D:D+64] k_rope^T,  O = softmax(scale S) v
+// Operations 2 (2 D + 64) a (row, visible key), bytes of K and V once a query block: a
+// dense contraction, bound by the tensor cores and, beside them, by one exponential a
+// (row, key): with 320 products a weight at D = 128 the two take about the same time.
+//
+// The engine is prefill_tc.cuh's with two query tiles: a CTA owns 256 query tokens of one
+// head, tile A and tile B of 128 rows (tensor memory lanes); S_A, S_B (128 columns), O_A,
+// O_B (D) fill tensor memory; each tile has a softmax warpgroup, one thread a row, and
+// while one works the tensor cores run the other's products:
+//   P_A V_j, S_A = Q_A K_{j+1}^T, P_B V_j, S_B = Q_B K_{j+1}^T.
+// What differs is the shared memory.  The queries take 96 KB at D = 128, so K and V come
+// through one ring of 16 KB granules, each freed by its own last product: K_j is D / 64 + 1
+// granules of 128 keys x 64 elements (the last one the shared part), V_j granules of 64
+// keys x 128 elements (D = 128) or 128 x 64.  Five a tile at D = 128 and eight in the ring:
+// P_B V_j frees two that K_{j+2} takes, 1290 cycles of products before it is used.  A ring
+// of whole tiles would hold one and a half of 128 keys, and tiles of 64 keys take 48
+// instead of 32 cycles an MMA.
+#pragma once
+
+#include <cstdint>
+
+#include "device_error.cuh"
+#include "ptx.cuh"
+#include "tc05.cuh"
+
+namespace da {
+
+struct LatentPrefillParams {
+  CUtensorMap tm_k;   // [B][H][D / 64][tokens][64], boxes of 128 tokens and one column
+  CUtensorMap tm_v;   // the same, boxes of VKEYS tokens and every column
+  CUtensorMap tm_pe;  // [B][tokens][64], boxes of 128 tokens
+  const __nv_bfloat16* q;  // [B, q_len, H, D + 64]
+  __nv_bfloat16* out;      // [B, q_len, H, D]
+  const int* seq_lens;     // [B] or null (every sequence max_len tokens)
+  int B, q_len, H, nqb;
+  int grp;                 // (sequence, head) units per launch group (their K/V fit in L2 together)
+  int max_len;
+  float scale_log2;
+  unsigned long long timeout_ns;
+};
+
+template <int D>
+struct LatentPrefillGeo {
+  static constexpr int M = 128, BK = 128, NQT = 2;  // rows a query tile, keys a tile
+  static constexpr int BQ = NQT * M;                // query tokens a CTA
+  static constexpr int W = D + 64;                  // elements of a query
+  static constexpr int NKG = W / 64;                // K granules a tile
+  static constexpr int G = 16384;                   // bytes a granule
+  static constexpr int VKEYS = G / (2 * D);         // keys of a V granule
+  static constexpr int NVG = BK / VKEYS;
+  static constexpr int PER = NKG + NVG;             // granules a tile
+  static constexpr int QT_BYTES = M * W * 2;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_G = NQT * QT_BYTES;
+  static constexpr int NG_FIT = (227 * 1024 - 1024 - 1024 - OFF_G) / G;
+  static constexpr int NG = NG_FIT < 12 ? NG_FIT : 12;
+  static constexpr int OFF_BAR = OFF_G + NG * G;
+  static constexpr int BAR_FULL = 0, BAR_EMPTY = NG, BAR_S = 2 * NG, BAR_P = BAR_S + 2, BAR_O = BAR_P + 2,
+                       BAR_FIN = BAR_O + 2, NBAR = BAR_FIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory base, abort flag
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr int TCOL_O = 2 * BK;             // S of tile t at t BK, O at TCOL_O + t D
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr int NTHREADS = 128 + 128 * NQT;
+  // registers after the split: producers and MMA issue, softmax
+  static constexpr int REG_LOW = 56, REG_HIGH = 216;
+  static constexpr int REG_POOL_NEEDED = 128 * REG_LOW + 128 * NQT * REG_HIGH;
+  static_assert(NG >= PER + NVG && SMEM <= 227 * 1024, "the ring holds a tile's K and two of V");
+  static_assert(TCOL_O + NQT * D <= 512, "tensor memory");
+};
+
+template <int N>
+__device__ __forceinline__ void latent_setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void latent_setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D>
+__global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
+    latent_prefill_kernel(const __grid_constant__ LatentPrefillParams p) {
+  using Gm = LatentPrefillGeo<D>;
+  constexpr int BK = Gm::BK, M = Gm::M;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  auto bar = [&](int i) -> uint32_t { return sbase + Gm::OFF_BAR + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float kNegInf = -__int_as_float(0x7f800000);
+
+  // work unit: groups of grp (b, h) units, latest query blocks first
+  const int nbh = p.B * p.H;
+  const long long per_grp = (long long)p.nqb * p.grp;
+  const int gi = (int)(blockIdx.x / per_grp);
+  const int gsz = min(p.grp, nbh - gi * p.grp);
+  const int in_g = (int)(blockIdx.x - gi * per_grp);
+  const int qb = p.nqb - 1 - in_g / gsz;
+  const int bh = gi * p.grp + in_g % gsz;
+  const int b = bh / p.H, h = bh % p.H;
+  int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len;
+  L = L < 0 ? 0 : (L > p.max_len ? p.max_len : L);
+  const int q0 = qb * Gm::BQ;
+  const int nq = min(Gm::BQ, p.q_len - q0);
+  const int nqt = nq > M ? 2 : 1;                     // query tiles with rows
+  const int base = L - p.q_len;                       // position of query token 0
+  const int kv_end = max(0, min(L, base + q0 + nq));  // keys some row sees
+  const int ntiles = (kv_end + BK - 1) / BK;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Gm::NG; ++i) {
+      mbar_init(bar(Gm::BAR_FULL + i), 1);
+      mbar_init(bar(Gm::BAR_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Gm::BAR_S + i), 1);
+      mbar_init(bar(Gm::BAR_P + i), 128);
+      mbar_init(bar(Gm::BAR_O + i), 1);
+    }
+    mbar_init(bar(Gm::BAR_FIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+    prefetch_tensormap(&p.tm_pe);
+  }
+  if (warp == 1) {
+    tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // query rows, [W / 64][M][64] per tile with the 128-byte swizzle; zero past the block
+  for (int e = threadIdx.x; e < nqt * M * (Gm::W / 8); e += Gm::NTHREADS) {
+    const int rr = e / (Gm::W / 8), ch = e % (Gm::W / 8);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (rr < nq)
+      v = __ldg(reinterpret_cast<const uint4*>(p.q + (((size_t)b * p.q_len + q0 + rr) * p.H + h) * Gm::W) + ch);
+    const int t = rr / M, r = rr % M;
+    *reinterpret_cast<uint4*>(smem + Gm::OFF_Q + t * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(r, ch % 8)) = v;
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MISC);
+  auto wait = [&](int i, int phase) { return wait_bounded(bar(i), (uint32_t)(phase & 1), abort_flag, p.timeout_ns); };
+  // granule g of tile j: K columns 0 .. NKG - 1, then V
+  auto slot_of = [&](int j, int g) { return (j * Gm::PER + g) % Gm::NG; };
+  auto fill_of = [&](int j, int g) { return (j * Gm::PER + g) / Gm::NG; };
+  auto addr_of = [&](int j, int g) { return sbase + Gm::OFF_G + (uint32_t)(slot_of(j, g) * Gm::G); };
+
+  if (warp < 4) {
+    // ---- first warpgroup: every warp gives registers up at the same instruction
+    latent_setmaxnreg_dec<Gm::REG_LOW>();
+    if (warp == 0) {
+      // ---- producer: granules in the order the products use them.  The wait for the free of
+      // granule m - NG is by its slot's phase, whose next one needs granule m.
+      if (lane == 0) {
+        bool ok = true;
+        int last = -1;
+        for (int j = 0; j < ntiles && ok; ++j) {
+          const int t = j * BK;
+#pragma unroll 1
+          for (int g = 0; g < Gm::PER; ++g) {
+            const int fill = fill_of(j, g), slot = slot_of(j, g);
+            if (fill > 0 && !(ok = wait(Gm::BAR_EMPTY + slot, fill - 1))) break;
+            const uint32_t full = bar(Gm::BAR_FULL + slot);
+            mbar_arrive_expect_tx(full, Gm::G);
+            if (g < Gm::NKG - 1)
+              tma_load_5d(addr_of(j, g), &p.tm_k, full, 0, t, g, h, b);
+            else if (g == Gm::NKG - 1)
+              tma_load_3d(addr_of(j, g), &p.tm_pe, full, 0, t, b);
+            else
+              tma_load_5d(addr_of(j, g), &p.tm_v, full, 0, t + (g - Gm::NKG) * Gm::VKEYS, 0, h, b);
+            last = j * Gm::PER + g;
+          }
+        }
+        if (*abort_flag) {  // copies in flight land before the CTA exits
+          const uint64_t t0 = globaltimer_ns();
+          for (int m = last; m >= 0 && m > last - Gm::NG; --m)
+            while (!mbar_try_wait(bar(Gm::BAR_FULL + m % Gm::NG), (uint32_t)((m / Gm::NG) & 1)) &&
+                   globaltimer_ns() - t0 < p.timeout_ns) {
+            }
+        }
+      }
+    } else if (warp == 1) {
+      // ---- MMA issue (lane 0); the warp zeroes V rows past the keys of the last tile
+      constexpr uint32_t id_s = tc_idesc_bf16(M, BK, false, false);
+      constexpr uint32_t id_o = tc_idesc_bf16(M, D, false, true);
+      auto wait_all = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)) != 0; };
+      auto wait_granule = [&](int j, int g) { return wait_all(Gm::BAR_FULL + slot_of(j, g), fill_of(j, g)); };
+      // S_t = Q_t K_j^T, each granule once it is there; freed after the last query tile
+      auto issue_qk = [&](int t, int j) {
+#pragma unroll
+        for (int g = 0; g < Gm::NKG; ++g) {
+          if (!wait_granule(j, g)) return false;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t da = tc_sdesc(sbase + Gm::OFF_Q + t * Gm::QT_BYTES + g * (M * 128), 16, 1024, kTcSwizzle128B);
+            const uint64_t db = tc_sdesc(addr_of(j, g), 16, 1024, kTcSwizzle128B);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc_mma_ss(tmem + t * BK, da + 2 * i, db + 2 * i, id_s, g > 0 || i > 0);
+            if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, g)));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) tc_commit(bar(Gm::BAR_S + t));
+        __syncwarp();
+        return true;
+      };
+      // O_t += P_t V_j with P_t from the S buffer
+      auto issue_pv = [&](int t, int j) {
+#pragma unroll
+        for (int g = 0; g < Gm::NVG; ++g) {
+          if (!wait_granule(j, Gm::NKG + g)) return false;
+          const int k0 = j * BK + g * Gm::VKEYS;
+          if (t == 0 && k0 + Gm::VKEYS > kv_end) {
+            // rows at or past kv_end may hold anything (0 * NaN would poison O): zero them
+            const int r0 = max(0, kv_end - k0);
+            uint8_t* vs = smem + Gm::OFF_G + slot_of(j, Gm::NKG + g) * Gm::G;
+            for (int e = r0 * 8 + lane; e < Gm::VKEYS * 8; e += 32)
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<uint4*>(vs + c * (Gm::VKEYS * 128) + swz<128>(e / 8, e % 8)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t db = tc_sdesc(addr_of(j, Gm::NKG + g), Gm::VKEYS * 128, 1024, kTcSwizzle128B);
+#pragma unroll
+            for (int i = 0; i < Gm::VKEYS / 16; ++i)
+              tc_mma_ts(tmem + Gm::TCOL_O + t * D, tmem + t * BK + 8 * (g * (Gm::VKEYS / 16) + i), db + i * 128, id_o,
+                        j > 0 || g > 0 || i > 0);
+            if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, Gm::NKG + g)));
+          }
+          __syncwarp();
+        }
+        return true;
+      };
+      bool ok = true;
+      for (int t = 0; t < nqt && ok && ntiles > 0; ++t) ok = issue_qk(t, 0);
+      for (int j = 0; j < ntiles && ok; ++j)
+        for (int t = 0; t < nqt && ok; ++t) {
+          ok = wait_all(Gm::BAR_P + t, j);
+          if (!ok) break;
+          ok = issue_pv(t, j);
+          if (!ok) break;
+          if (j + 1 < ntiles) {
+            ok = issue_qk(t, j + 1);
+          } else {
+            if (lane == 0) tc_commit(bar(Gm::BAR_O + t));
+            __syncwarp();
+          }
+        }
+      // before the tensor memory is freed, every MMA issued must have completed
+      if (lane == 0 && ntiles > 0) {
+        tc_commit(bar(Gm::BAR_FIN));
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar(Gm::BAR_FIN), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+        }
+      }
+      __syncwarp();
+    }  // warps 2 and 3: idle
+  } else {
+    // ---- softmax and epilogue of query tile qt: one thread per row (tensor memory lane)
+    latent_setmaxnreg_inc<Gm::REG_HIGH>();
+    const int qt = (warp >> 2) - 1;
+    const int row = lane + 32 * (warp & 3);
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    const int tok = qt * M + row;  // this row's token within the block
+    const bool has_row = tok < nq;
+    const int lim = has_row ? max(0, min(L, base + q0 + tok + 1)) : 0;  // keys this row sees
+    const int lim_first = max(0, min(L, base + q0 + qt * M + 1));       // keys every row of the tile sees
+    const uint32_t o_addr = tmem + lane_addr + Gm::TCOL_O + qt * D;
+    const uint32_t s_addr = tmem + lane_addr + qt * BK;
+    const bool fold = p.scale_log2 > 0.f;  // a positive scale goes into the exponent's fma
+    const float sc = fold ? p.scale_log2 : 1.f;
+    float m = kNegInf, l = 0.f;
+    bool ok = true;
+    if (qt < nqt) {
+      for (int j = 0; j < ntiles; ++j) {
+        ok = __all_sync(0xffffffffu, wait(Gm::BAR_S + qt, j));
+        if (!ok) break;
+        tc_fence_after();
+        float x[BK];
+        {
+          uint32_t r[BK];
+#pragma unroll
+          for (int c0 = 0; c0 < BK; c0 += 32) tmem_ld32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(r + c0));
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < BK; ++i) x[i] = fold ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * p.scale_log2;
+        }
+        if (j * BK + BK > lim_first) {
+#pragma unroll
+          for (int i = 0; i < BK; ++i) x[i] = j * BK + i < lim ? x[i] : kNegInf;
+        }
+        // P = exp2(x sc - mu) as bf16 pairs over the first half of the S buffer; the sum of the weights
+        auto weights = [&](float mu) {
+          float sk[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sk[k] = 0.f;
+#pragma unroll
+          for (int c0 = 0; c0 < BK / 2; c0 += 32) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float e0 = exp2_approx(fmaf(x[2 * (c0 + i)], sc, -mu));
+              const float e1 = exp2_approx(fmaf(x[2 * (c0 + i) + 1], sc, -mu));
+              sk[i & 7] += e0 + e1;
+              pk[i] = pack_bf16x2(e0, e1);
+            }
+            tmem_st32(s_addr + c0, pk);
+          }
+          return ((sk[0] + sk[1]) + (sk[2] + sk[3])) + ((sk[4] + sk[5]) + (sk[6] + sk[7]));
+        };
+        // The weights are first taken against the current m; only a row that has seen no key
+        // yet, or whose weights sum past 2^14, takes its maximum and raises m to it.  The
+        // stores in weights() are the whole warp's, so every call is warp-uniform.
+        const bool have = __any_sync(0xffffffffu, m != kNegInf);
+        float sum = 0.f;
+        if (have) sum = weights(m == kNegInf ? 0.f : m);
+        const bool need = m == kNegInf || !(sum <= 16384.f);
+        float mx = kNegInf;
+        if (need) {
+          float mk[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mk[k] = x[k];
+#pragma unroll
+          for (int i = 8; i < BK; ++i) mk[i & 7] = fmaxf(mk[i & 7], x[i]);
+          mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
+          mx = fold ? mx * p.scale_log2 : mx;
+        }
+        const bool raise = need && mx > m;
+        const float m_new = raise ? mx : m;
+        const float alpha = raise ? exp2_approx(m - m_new) : 1.f;  // 0 while m is still -inf
+        if (__any_sync(0xffffffffu, raise && m != kNegInf) && j > 0) {
+          // S of tile j was issued after P V of tile j - 1 by the same thread, and its commit
+          // covers every MMA before it: O is complete
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(o_addr + c0, o);
+          }
+          tmem_st_wait();
+        }
+        m = m_new;
+        if (!have || __any_sync(0xffffffffu, raise)) sum = weights(m == kNegInf ? 0.f : m);
+        l = l * alpha + sum;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(Gm::BAR_P + qt));
+      }
+      // ---- normalise and write the tile's rows (a row that saw nothing: zeros)
+      if (ok && ntiles > 0) ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + qt, 0));
+      if (ok) {
+        tc_fence_after();
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        __nv_bfloat16* dst = p.out + (((size_t)b * p.q_len + q0 + tok) * p.H + h) * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t r[32];
+          if (ntiles > 0) {
+            tmem_ld32(o_addr + c0, r);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+          }
+          if (has_row) {
+            uint4* o = reinterpret_cast<uint4*>(dst + c0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = make_uint4(pack_bf16x2(__uint_as_float(r[8 * k + 0]) * inv, __uint_as_float(r[8 * k + 1]) * inv),
+                                pack_bf16x2(__uint_as_float(r[8 * k + 2]) * inv, __uint_as_float(r[8 * k + 3]) * inv),
+                                pack_bf16x2(__uint_as_float(r[8 * k + 4]) * inv, __uint_as_float(r[8 * k + 5]) * inv),
+                                pack_bf16x2(__uint_as_float(r[8 * k + 6]) * inv, __uint_as_float(r[8 * k + 7]) * inv));
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Gm::TMEM_COLS);
+  }
+}
+
+}  // namespace da

@@ -492,6 +492,27 @@ int latent_attn_paged(const void* q, const void* pool, const int* page_table, co
 long long latent_workspace_bytes(int batch, int q_len, int num_heads, int latent_dim, int num_sms);
 int latent_max_batch(int q_len, int num_heads, int latent_dim);
 
+/*
+ * latent_prefill_contig — causal prefill of the last q_len tokens over keys and values
+ * expanded from the latent vectors (the expanded form, for many query tokens: fewer
+ * operations a key than the absorbed one).  Head h's key at token t is [k_nope[b,t,h,:],
+ * k_rope[b,t,:]]; causality, lengths and empty rows as for prefill_attn_contig.
+ *  q          bf16 [batch, q_len, num_heads, head_dim + 64], token-major
+ *  k_nope, v  bf16 [batch, max_ctx, num_heads, head_dim] with the given strides in elements, the
+ *             same for both (multiples of 8; a batch entry is max_ctx tokens): one product may
+ *             expand a token's keys and values side by side
+ *  k_rope     bf16 [batch, max_ctx, 64] with rope_token_stride elements between tokens (a multiple
+ *             of 8): the last 64 columns of a latent cache will do
+ *  out        bf16 [batch, q_len, num_heads, head_dim]
+ *  head_dim   64 or 128; seq_lens int32 [batch] clamped to [0, max_ctx], or NULL (max_ctx).
+ * Keys and values at positions below L_b are finite; what lies past them is never used.
+ * Numerics as for prefill_attn_*; no workspace.
+ */
+int latent_prefill_contig(const void* q, const void* k_nope, const void* k_rope, const void* v, const int* seq_lens,
+                          int batch, int q_len, int num_heads, int head_dim, int max_ctx,
+                          long long kv_token_stride, long long kv_head_stride, long long rope_token_stride,
+                          float scale, void* out, void* stream);
+
 /* Human-readable name of a da_status value (static string). */
 const char* decode_status_string(int status);
 
