@@ -190,7 +190,7 @@ int latent_call(bool paged, const void* q, const void* cache, const int* page_ta
 }
 
 template <int D>
-int launch_latent_prefill(LatentPrefillParams& prm, const void* k, const void* k_rope, const void* v,
+int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k, const void* k_rope, const void* v,
                           long long token_stride, long long head_stride, long long rope_stride, int dev,
                           cudaStream_t st) {
   using Gm = LatentPrefillGeo<D>;
@@ -218,6 +218,11 @@ int launch_latent_prefill(LatentPrefillParams& prm, const void* k, const void* k
   const cuuint32_t box_pe[3] = {64, 128, 1};
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const cuuint64_t qw = Gm::W * 2;
+  const cuuint64_t dims_q[5] = {64, (cuuint64_t)prm.q_len, Gm::W / 64, H, B};
+  const cuuint64_t strides_q[4] = {qw * H, 128, qw, qw * H * (cuuint64_t)prm.q_len};
+  const cuuint32_t box_q[5] = {64, Gm::M, Gm::W / 64, 1, 1};
+  if (int e = encode_map_t(&prm.tm_q, bf16, sw, q, 5, dims_q, strides_q, box_q)) return e;
   if (int e = encode_map_t(&prm.tm_k, bf16, sw, k, 5, dims, strides, box_k)) return e;
   if (int e = encode_map_t(&prm.tm_v, bf16, sw, v, 5, dims, strides, box_v)) return e;
   if (int e = encode_map_t(&prm.tm_pe, bf16, sw, k_rope, 3, dims_pe, strides_pe, box_pe)) return e;
@@ -309,7 +314,6 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
   if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
   LatentPrefillParams prm;
   std::memset(&prm, 0, sizeof(prm));
-  prm.q = static_cast<const __nv_bfloat16*>(q);
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.seq_lens = seq_lens;
   prm.B = batch;
@@ -319,8 +323,8 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
   prm.max_len = max_ctx;
   prm.scale_log2 = scale * kLog2e;
   prm.timeout_ns = kWaitTimeoutNs;
-  return head_dim == 64 ? launch_latent_prefill<64>(prm, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
+  return head_dim == 64 ? launch_latent_prefill<64>(prm, q, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
                                                     rope_token_stride, dev, st)
-                        : launch_latent_prefill<128>(prm, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
+                        : launch_latent_prefill<128>(prm, q, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
                                                      rope_token_stride, dev, st);
 }

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
         // the rotated part first: the last unit to land then has 8 products left
         const int slot_pe = n % Gm::NPE;
         if (!(ok = wait_all(Gm::B_PEFULL + slot_pe, n / Gm::NPE))) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
           const uint64_t da = tc_sdesc(sbase + Gm::OFF_PE + slot_pe * Gm::PE, 16, 1024, kTcSwizzle128B);
           const uint64_t db = tc_sdesc(sbase + Gm::OFF_Q + 2 * NU * N * 128, 16, 1024, kTcSwizzle128B);
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) {
+          if (elect_one()) {
             tc_fence_after();
             const uint64_t da = tc_sdesc(unit, 16, 1024, kTcSwizzle128B);
             const uint64_t db = tc_sdesc(sbase + Gm::OFF_Q + 2 * k * N * 128, 16, 1024, kTcSwizzle128B);
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
           __syncwarp();
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_commit(bar(Gm::B_S + sb));
           if (t + T >= pc.t1) tc_commit(bar(Gm::B_QEMPTY));
         }
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
       }
       ++piece;
     }
-    if (lane == 0 && (issued || !ok)) {  // everything issued completes before the tensor memory goes
+    if ((issued || !ok) && elect_one()) {  // everything issued completes before the tensor memory goes
       tc_commit(bar(Gm::B_FIN));
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(bar(Gm::B_FIN), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
       for (int t = pc.t0; t < pc.t1 && ok; t += T, ++n) {
         const int sb = n & 1;
         if (!(ok = wait_all(Gm::B_P + sb, n >> 1))) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
           const uint64_t db = tc_sdesc(sbase + Gm::OFF_P + (n % Gm::NP) * Gm::P_BYTES, 16, 1024, kTcSwizzle128B);
 #pragma unroll
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
       }
       ++piece;
     }
-    if (lane == 0 && issued) {
+    if (issued && elect_one()) {
       tc_commit(bar(Gm::B_FIN + 1));
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(bar(Gm::B_FIN + 1), 0) && globaltimer_ns() - t0 < p.timeout_ns) {

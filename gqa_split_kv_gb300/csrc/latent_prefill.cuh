@@ -31,10 +31,10 @@
 namespace da {
 
 struct LatentPrefillParams {
+  CUtensorMap tm_q;   // [B][H][W / 64][q_len][64], boxes of 128 tokens and every column
   CUtensorMap tm_k;   // [B][H][D / 64][tokens][64], boxes of 128 tokens and one column
   CUtensorMap tm_v;   // the same, boxes of VKEYS tokens and every column
   CUtensorMap tm_pe;  // [B][tokens][64], boxes of 128 tokens
-  const __nv_bfloat16* q;  // [B, q_len, H, D + 64]
   __nv_bfloat16* out;      // [B, q_len, H, D]
   const int* seq_lens;     // [B] or null (every sequence max_len tokens)
   int B, q_len, H, nqb;
@@ -61,7 +61,7 @@ struct LatentPrefillGeo {
   static constexpr int NG = NG_FIT < 12 ? NG_FIT : 12;
   static constexpr int OFF_BAR = OFF_G + NG * G;
   static constexpr int BAR_FULL = 0, BAR_EMPTY = NG, BAR_S = 2 * NG, BAR_P = BAR_S + 2, BAR_O = BAR_P + 2,
-                       BAR_FIN = BAR_O + 2, NBAR = BAR_FIN + 1;
+                       BAR_Q = BAR_O + 2, BAR_FIN = BAR_Q + 2, NBAR = BAR_FIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory base, abort flag
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int TCOL_O = 2 * BK;             // S of tile t at t BK, O at TCOL_O + t D
@@ -125,10 +125,12 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       mbar_init(bar(Gm::BAR_S + i), 1);
       mbar_init(bar(Gm::BAR_P + i), 128);
       mbar_init(bar(Gm::BAR_O + i), 1);
+      mbar_init(bar(Gm::BAR_Q + i), 1);
     }
     mbar_init(bar(Gm::BAR_FIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
+    prefetch_tensormap(&p.tm_q);
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
     prefetch_tensormap(&p.tm_pe);
@@ -137,16 +139,6 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  // query rows, [W / 64][M][64] per tile with the 128-byte swizzle; zero past the block
-  for (int e = threadIdx.x; e < nqt * M * (Gm::W / 8); e += Gm::NTHREADS) {
-    const int rr = e / (Gm::W / 8), ch = e % (Gm::W / 8);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (rr < nq)
-      v = __ldg(reinterpret_cast<const uint4*>(p.q + (((size_t)b * p.q_len + q0 + rr) * p.H + h) * Gm::W) + ch);
-    const int t = rr / M, r = rr % M;
-    *reinterpret_cast<uint4*>(smem + Gm::OFF_Q + t * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(r, ch % 8)) = v;
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -166,6 +158,11 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       if (lane == 0) {
         bool ok = true;
         int last = -1;
+        // query tiles, [W / 64][M][64] each; zeros past q_len
+        for (int t = 0; t < nqt && ntiles > 0; ++t) {
+          mbar_arrive_expect_tx(bar(Gm::BAR_Q + t), Gm::QT_BYTES);
+          tma_load_5d(sbase + Gm::OFF_Q + t * Gm::QT_BYTES, &p.tm_q, bar(Gm::BAR_Q + t), 0, q0 + t * M, 0, h, b);
+        }
         for (int j = 0; j < ntiles && ok; ++j) {
           const int t = j * BK;
 #pragma unroll 1
@@ -185,6 +182,9 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         }
         if (*abort_flag) {  // copies in flight land before the CTA exits
           const uint64_t t0 = globaltimer_ns();
+          for (int t = 0; t < nqt && ntiles > 0; ++t)
+            while (!mbar_try_wait(bar(Gm::BAR_Q + t), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+            }
           for (int m = last; m >= 0 && m > last - Gm::NG; --m)
             while (!mbar_try_wait(bar(Gm::BAR_FULL + m % Gm::NG), (uint32_t)((m / Gm::NG) & 1)) &&
                    globaltimer_ns() - t0 < p.timeout_ns) {
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         }
       }
     } else if (warp == 1) {
-      // ---- MMA issue (lane 0); the warp zeroes V rows past the keys of the last tile
+      // ---- MMA issue (one lane); the warp zeroes V rows past the keys of the last tile
       constexpr uint32_t id_s = tc_idesc_bf16(M, BK, false, false);
       constexpr uint32_t id_o = tc_idesc_bf16(M, D, false, true);
       auto wait_all = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)) != 0; };
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
 #pragma unroll
         for (int g = 0; g < Gm::NKG; ++g) {
           if (!wait_granule(j, g)) return false;
-          if (lane == 0) {
+          if (elect_one()) {
             tc_fence_after();
             const uint64_t da = tc_sdesc(sbase + Gm::OFF_Q + t * Gm::QT_BYTES + g * (M * 128), 16, 1024, kTcSwizzle128B);
             const uint64_t db = tc_sdesc(addr_of(j, g), 16, 1024, kTcSwizzle128B);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           }
           __syncwarp();
         }
-        if (lane == 0) tc_commit(bar(Gm::BAR_S + t));
+        if (elect_one()) tc_commit(bar(Gm::BAR_S + t));
         __syncwarp();
         return true;
       };
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) {
+          if (elect_one()) {
             tc_fence_after();
             const uint64_t db = tc_sdesc(addr_of(j, Gm::NKG + g), Gm::VKEYS * 128, 1024, kTcSwizzle128B);
 #pragma unroll
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         return true;
       };
       bool ok = true;
-      for (int t = 0; t < nqt && ok && ntiles > 0; ++t) ok = issue_qk(t, 0);
+      for (int t = 0; t < nqt && ok && ntiles > 0; ++t) ok = wait_all(Gm::BAR_Q + t, 0) && issue_qk(t, 0);
       for (int j = 0; j < ntiles && ok; ++j)
         for (int t = 0; t < nqt && ok; ++t) {
           ok = wait_all(Gm::BAR_P + t, j);
@@ -258,12 +258,12 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           if (j + 1 < ntiles) {
             ok = issue_qk(t, j + 1);
           } else {
-            if (lane == 0) tc_commit(bar(Gm::BAR_O + t));
+            if (elect_one()) tc_commit(bar(Gm::BAR_O + t));
             __syncwarp();
           }
         }
       // before the tensor memory is freed, every MMA issued must have completed
-      if (lane == 0 && ntiles > 0) {
+      if (ntiles > 0 && elect_one()) {
         tc_commit(bar(Gm::BAR_FIN));
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(bar(Gm::BAR_FIN), 0) && globaltimer_ns() - t0 < p.timeout_ns) {

@@ -56,6 +56,17 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 
 // ---------------------------------------------------------------- MMA
 
+// True in one lane of the warp, the same one every time; the whole warp executes it.  An
+// MMA's operands are uniform registers: behind this branch the compiler knows that one
+// thread runs and computes them there, and an MMA issues every 23 cycles; behind lane ==
+// 0 it moves each operand across, and one issues every 45 (measured, M = 64, N = 16), 52
+// or more with descriptors computed in between.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc]; issued by one thread.
 __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           bool accumulate) {
