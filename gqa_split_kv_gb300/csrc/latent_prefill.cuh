@@ -196,72 +196,99 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       constexpr uint32_t id_s = tc_idesc_bf16(M, BK, false, false);
       constexpr uint32_t id_o = tc_idesc_bf16(M, D, false, true);
       auto wait_all = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)) != 0; };
-      auto wait_granule = [&](int j, int g) { return wait_all(Gm::BAR_FULL + slot_of(j, g), fill_of(j, g)); };
-      // S_t = Q_t K_j^T, each granule once it is there; freed after the last query tile
+      // granules [g0, g1) of tile j have landed (query tile A waits for both)
+      auto landed = [&](int j, int g0, int g1) {
+        bool there = true;
+        for (int g = g0; g < g1; ++g) there = wait(Gm::BAR_FULL + slot_of(j, g), fill_of(j, g)) && there;
+        return __all_sync(0xffffffffu, there) != 0;
+      };
+      // one thread: S_t = Q_t K_j^T; the granules are freed after the last query tile
       auto issue_qk = [&](int t, int j) {
 #pragma unroll
         for (int g = 0; g < Gm::NKG; ++g) {
-          if (!wait_granule(j, g)) return false;
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t da = tc_sdesc(sbase + Gm::OFF_Q + t * Gm::QT_BYTES + g * (M * 128), 16, 1024, kTcSwizzle128B);
-            const uint64_t db = tc_sdesc(addr_of(j, g), 16, 1024, kTcSwizzle128B);
+          const uint64_t da = tc_sdesc(sbase + Gm::OFF_Q + t * Gm::QT_BYTES + g * (M * 128), 16, 1024, kTcSwizzle128B);
+          const uint64_t db = tc_sdesc(addr_of(j, g), 16, 1024, kTcSwizzle128B);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tc_mma_ss(tmem + t * BK, da + 2 * i, db + 2 * i, id_s, g > 0 || i > 0);
-            if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, g)));
-          }
-          __syncwarp();
+          for (int i = 0; i < 4; ++i) tc_mma_ss(tmem + t * BK, da + 2 * i, db + 2 * i, id_s, g > 0 || i > 0);
+          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, g)));
         }
-        if (elect_one()) tc_commit(bar(Gm::BAR_S + t));
-        __syncwarp();
-        return true;
+        tc_commit(bar(Gm::BAR_S + t));
       };
-      // O_t += P_t V_j with P_t from the S buffer
+      // one thread: O_t += P_t V_j with P_t from the S buffer
       auto issue_pv = [&](int t, int j) {
 #pragma unroll
         for (int g = 0; g < Gm::NVG; ++g) {
-          if (!wait_granule(j, Gm::NKG + g)) return false;
-          const int k0 = j * BK + g * Gm::VKEYS;
-          if (t == 0 && k0 + Gm::VKEYS > kv_end) {
-            // rows at or past kv_end may hold anything (0 * NaN would poison O): zero them
-            const int r0 = max(0, kv_end - k0);
-            uint8_t* vs = smem + Gm::OFF_G + slot_of(j, Gm::NKG + g) * Gm::G;
-            for (int e = r0 * 8 + lane; e < Gm::VKEYS * 8; e += 32)
+          const uint64_t db = tc_sdesc(addr_of(j, Gm::NKG + g), Gm::VKEYS * 128, 1024, kTcSwizzle128B);
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                *reinterpret_cast<uint4*>(vs + c * (Gm::VKEYS * 128) + swz<128>(e / 8, e % 8)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (elect_one()) {
+          for (int i = 0; i < Gm::VKEYS / 16; ++i)
+            tc_mma_ts(tmem + Gm::TCOL_O + t * D, tmem + t * BK + 8 * (g * (Gm::VKEYS / 16) + i), db + i * 128, id_o,
+                      j > 0 || g > 0 || i > 0);
+          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, Gm::NKG + g)));
+        }
+      };
+      // V rows at or past kv_end may hold anything (0 * NaN would poison O): zero them
+      auto zero_tail = [&](int j) {
+        for (int g = 0; g < Gm::NVG; ++g) {
+          const int r0 = max(0, kv_end - (j * BK + g * Gm::VKEYS));
+          uint8_t* vs = smem + Gm::OFF_G + slot_of(j, Gm::NKG + g) * Gm::G;
+          for (int e = r0 * 8 + lane; e < Gm::VKEYS * 8; e += 32)
+            for (int c = 0; c < D / 64; ++c)
+              *reinterpret_cast<uint4*>(vs + c * (Gm::VKEYS * 128) + swz<128>(e / 8, e % 8)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      bool ok = ntiles > 0 && wait_all(Gm::BAR_Q, 0) && landed(0, 0, Gm::NKG);
+      if (ok) {
+        if (elect_one()) {
+          tc_fence_after();
+          issue_qk(0, 0);
+        }
+        __syncwarp();
+        if (nqt == 2) {
+          ok = wait_all(Gm::BAR_Q + 1, 0);
+          if (ok && elect_one()) {
             tc_fence_after();
-            const uint64_t db = tc_sdesc(addr_of(j, Gm::NKG + g), Gm::VKEYS * 128, 1024, kTcSwizzle128B);
-#pragma unroll
-            for (int i = 0; i < Gm::VKEYS / 16; ++i)
-              tc_mma_ts(tmem + Gm::TCOL_O + t * D, tmem + t * BK + 8 * (g * (Gm::VKEYS / 16) + i), db + i * 128, id_o,
-                        j > 0 || g > 0 || i > 0);
-            if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, Gm::NKG + g)));
+            issue_qk(1, 0);
           }
           __syncwarp();
         }
-        return true;
-      };
-      bool ok = true;
-      for (int t = 0; t < nqt && ok && ntiles > 0; ++t) ok = wait_all(Gm::BAR_Q + t, 0) && issue_qk(t, 0);
-      for (int j = 0; j < ntiles && ok; ++j)
-        for (int t = 0; t < nqt && ok; ++t) {
-          ok = wait_all(Gm::BAR_P + t, j);
-          if (!ok) break;
-          ok = issue_pv(t, j);
-          if (!ok) break;
-          if (j + 1 < ntiles) {
-            ok = issue_qk(t, j + 1);
-          } else {
-            if (elect_one()) tc_commit(bar(Gm::BAR_O + t));
-            __syncwarp();
-          }
+      }
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const bool more = j + 1 < ntiles;
+        // A: P_A V_j, then S_A of tile j + 1 once its keys are there
+        ok = landed(j, Gm::NKG, Gm::PER);
+        if (!ok) break;
+        if (!more) zero_tail(j);
+        if (!(ok = wait_all(Gm::BAR_P, j))) break;
+        if (elect_one()) {
+          tc_fence_after();
+          issue_pv(0, j);
+          if (!more) tc_commit(bar(Gm::BAR_O));
         }
+        __syncwarp();
+        if (more) {
+          if (!(ok = landed(j + 1, 0, Gm::NKG))) break;
+          if (elect_one()) {
+            tc_fence_after();
+            issue_qk(0, j + 1);
+          }
+          __syncwarp();
+        }
+        if (nqt == 2) {  // B: the same tiles
+          if (!(ok = wait_all(Gm::BAR_P + 1, j))) break;
+          if (elect_one()) {
+            tc_fence_after();
+            issue_pv(1, j);
+            if (more)
+              issue_qk(1, j + 1);
+            else
+              tc_commit(bar(Gm::BAR_O + 1));
+          }
+          __syncwarp();
+        }
+      }
       // before the tensor memory is freed, every MMA issued must have completed
       if (ntiles > 0 && elect_one()) {
         tc_commit(bar(Gm::BAR_FIN));
