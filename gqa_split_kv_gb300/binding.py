@@ -469,57 +469,28 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "plain", f
     return torch.from_numpy(w).to("cuda" if device is None else device)
 
 
-# The checks below run on every call, and a decode step's kernels take a few
-# microseconds: torch is looked up once, and a tensor that is as it should be costs four
-# attribute reads.
-_torch = None
+_ext_module = None
 
 
-def _t():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
+def _ext():
+    """The extension that marshals the calls below (csrc/binding_ext.cpp, built with the library)."""
+    global _ext_module
+    if _ext_module is None:
+        import torch  # noqa: F401  (the extension uses its libraries)
+        load()
+        try:
+            from . import _binding_ext
+        except ImportError as e:
+            raise RuntimeError("the binding's extension is not built; run gqa_split_kv_gb300.build.build()") from e
+        _binding_ext.open(LIB, DecodeAttnError)
+        _ext_module = _binding_ext
+    return _ext_module
 
 
-def _plain(t, name, dtype, shape, dev):
-    """t must be a contiguous tensor of this type and shape on CUDA device dev."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got "
-                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-
-
-def _on_current(dev: int):
-    """The library launches on the current device: the tensors' device dev must be that one."""
-    if dev < 0 or dev != _torch._C._cuda_getDevice():
-        raise ValueError("expected tensors on the current CUDA device, got them on "
-                         + (f"cuda:{dev}" if dev >= 0 else "the CPU"))
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _token_stride(t, name, lead: int):
-    """Elements from one token to the next of t [.., H, D] (lead leading dims that are one run of tokens); the
-    elements of a head are consecutive."""
-    st, sh = t.stride(), t.shape
-    ok = st[-1] == 1 or sh[-1] == 1
-    if lead == 2 and sh[0] > 1 and sh[1] > 0:
-        if sh[1] > 1 and st[0] != sh[1] * st[1]:
-            ok = False
-        step = st[1] if sh[1] > 1 else st[0]
-    else:
-        step = st[lead - 1]
-    if not ok:
-        raise ValueError(f"{name}: tokens must be equally far apart and a head's elements consecutive, "
-                         f"got strides {st} of shape {tuple(sh)}")
-    return step
+def _int8(k_scale):
+    if k_scale is None:
+        raise ValueError("k: an int8 cache needs its scales")
+    return k_scale
 
 
 def rope_apply(x, positions, inv_freq, offset: int = 0, interleaved: bool = False, magnitude: float = 1.0,
@@ -528,118 +499,8 @@ def rope_apply(x, positions, inv_freq, offset: int = 0, interleaved: bool = Fals
     positions int32 [T] or [B, T], inv_freq float64 [rot / 2] (rope_inv_freq).  Elements [offset, offset + rot)
     of every head are rotated, pairs (j, j + rot / 2) or, interleaved, (2j, 2j + 1); with backward, the gradient
     of that.  out: x itself (in place) or a tensor of x's shape.  Returns out."""
-    torch = _torch or _t()
-    xd = x.dtype
-    dtype = 0 if xd is torch.bfloat16 else 1 if xd is torch.float16 else 2 if xd is torch.float32 else None
-    shape = x.shape
-    lead = len(shape) - 2
-    if dtype is None or lead not in (1, 2):
-        raise ValueError(f"x: expected bf16, fp16 or fp32 [T, H, D] or [B, T, H, D], got {xd} {tuple(shape)}")
-    dev = x.get_device()
-    _plain(positions, "positions", torch.int32, shape[:-2], dev)
-    rot = inv_freq.shape
-    _plain(inv_freq, "inv_freq", torch.float64, (rot[0] if rot else 0,), dev)
-    if out is None:
-        out = torch.empty(shape, dtype=xd, device=x.device)
-    elif out.dtype is not xd or out.shape != shape or out.get_device() != dev:
-        raise ValueError(f"out: expected {xd} {tuple(shape)} on cuda:{dev}, got {out.dtype} {tuple(out.shape)} on "
-                         f"{out.device}")
-    xt, ot = _token_stride(x, "x", lead), _token_stride(out, "out", lead)
-    _on_current(dev)
-    st = (_lib or load()).rope_apply(
-        x.data_ptr(), out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), positions.numel(), shape[-2],
-        shape[-1], offset, 2 * rot[0], 1 if interleaved else 0, magnitude, 1 if backward else 0, dtype, xt,
-        x.stride(-2), ot, out.stride(-2), _raw_stream(stream, dev))
-    if st:
-        raise DecodeAttnError("rope_apply", st)
-    return out
-
-
-def _rope_args(inv_freq, offset, interleaved, magnitude, dev):
-    if inv_freq is None:
-        return None, 0, 0, 0, 1.0
-    n = inv_freq.shape
-    _plain(inv_freq, "inv_freq", _torch.float64, (n[0] if n else 0,), dev)
-    return inv_freq.data_ptr(), offset, 2 * n[0], 1 if interleaved else 0, magnitude
-
-
-def _new_tokens(t, name, shape, dev):
-    """The token stride of new tokens [B, q_len, Hkv, D], a token's heads consecutive."""
-    if t.dtype is not _torch.bfloat16 or t.shape != shape or len(shape) != 4 or t.get_device() != dev:
-        raise ValueError(f"{name}: expected bf16 [B, q_len, Hkv, D], here {tuple(shape)}, on cuda:{dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    B, n, H, D = shape
-    if t.is_contiguous():
-        return H * D
-    if H > 1 and t.stride(2) != D:
-        raise ValueError(f"{name}: a token's heads must be consecutive, got strides {t.stride()}")
-    return _token_stride(t, name, 2) if B * n > 1 else H * D
-
-
-def _check_cache(k, v, k_scale, v_scale, page_table, seq_lens, B, H, D, dev):
-    """Checks a cache against the call's batch and heads; returns the size arguments that follow head_dim."""
-    torch = _torch
-    shape = k.shape
-    if len(shape) != 4:
-        raise ValueError(f"k: expected 4 dims, got {tuple(shape)}")
-    slabs, slab = shape[0], shape[1]
-    if page_table is None:
-        slabs, where = B, (slab,)
-    else:
-        pt = page_table.shape
-        cols = pt[1] if len(pt) == 2 else 0
-        _plain(page_table, "page_table", torch.int32, (B, cols), dev)
-        where = (slab, cols, slabs)
-        if seq_lens is None:
-            raise ValueError("seq_lens: a paged cache needs them")
-    if seq_lens is not None:
-        _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    want = (slabs, slab, H, D)
-    if k_scale is None:
-        _plain(k, "k", torch.bfloat16, want, dev)
-        if v is not None:
-            _plain(v, "v", torch.bfloat16, want, dev)
-    else:
-        _plain(k, "k", torch.int8, want, dev)
-        _plain(k_scale, "k_scale", torch.float32, (slabs, H, slab), dev)
-        if v is not None:
-            if v_scale is None:
-                raise ValueError("v: an int8 cache needs its scales")
-            _plain(v, "v", torch.int8, want, dev)
-            _plain(v_scale, "v_scale", torch.float32, (slabs, H, slab), dev)
-    return where
-
-
-def _kv_write(fn, k_new, v_new, k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, inv_freq, offset,
-              interleaved, magnitude, stream):
-    _t()
-    dev = k_new.get_device()
-    shape = k_new.shape
-    ks = _new_tokens(k_new, "k_new", shape, dev)
-    if v_new is None:
-        vs = 0
-        if v is not None:
-            raise ValueError("v_new and v: both tensors, or both None to write keys only")
-    else:
-        vs = _new_tokens(v_new, "v_new", shape, dev)
-        if v is None:
-            raise ValueError("v_new and v: both tensors, or both None to write keys only")
-    B, n, H, D = shape
-    where = _check_cache(k, v, k_scale, v_scale, page_table, seq_lens, B, H, D, dev)
-    rope = _rope_args(inv_freq, offset, interleaved, magnitude, dev)
-    _on_current(dev)
-    call = getattr(_lib or load(), fn)
-    if page_table is None:
-        head = (k_new.data_ptr(), _addr(v_new), ks, vs, _addr(seq_lens), B, n, H, D, *where, *rope)
-    else:
-        head = (k_new.data_ptr(), _addr(v_new), ks, vs, page_table.data_ptr(), seq_lens.data_ptr(), B, n, H, D, *where,
-                max_seq_len, *rope)
-    if k_scale is None:
-        st = call(*head, k.data_ptr(), _addr(v), _raw_stream(stream, dev))
-    else:
-        st = call(*head, k.data_ptr(), _addr(v), k_scale.data_ptr(), _addr(v_scale), _raw_stream(stream, dev))
-    if st:
-        raise DecodeAttnError(fn, st)
+    return (_ext_module or _ext()).rope_apply(x, positions, inv_freq, offset, interleaved, magnitude, backward, out,
+                                              stream)
 
 
 def kv_write_contig(k_new, v_new, k, v, seq_lens=None, inv_freq=None, offset: int = 0, interleaved: bool = False,
@@ -647,71 +508,31 @@ def kv_write_contig(k_new, v_new, k, v, seq_lens=None, inv_freq=None, offset: in
     """Writes the last q_len tokens of every sequence, k_new/v_new bf16 [B, q_len, Hkv, D], into the bf16 cache k/v
     [B, max_ctx, Hkv, D]; seq_lens int32 [B] (with the new tokens) or None.  inv_freq: rotate the keys at their
     positions first (rope_apply).  v_new and v may both be None (keys only)."""
-    _kv_write("kv_write_contig", k_new, v_new, k, v, None, None, None, seq_lens, 0, inv_freq, offset, interleaved,
-              magnitude, stream)
+    (_ext_module or _ext()).kv_write(k_new, v_new, k, v, None, None, None, seq_lens, 0, inv_freq, offset, interleaved,
+                                     magnitude, stream)
 
 
 def kv_write_paged(k_new, v_new, k_pool, v_pool, page_table, seq_lens, max_seq_len: int, inv_freq=None,
                    offset: int = 0, interleaved: bool = False, magnitude: float = 1.0, stream=None):
     """kv_write_contig into page pools [num_pages, page_size, Hkv, D]; page_table int32 [B, max_pages]."""
-    _kv_write("kv_write_paged", k_new, v_new, k_pool, v_pool, None, None, page_table, seq_lens, max_seq_len, inv_freq,
-              offset, interleaved, magnitude, stream)
+    (_ext_module or _ext()).kv_write(k_new, v_new, k_pool, v_pool, None, None, page_table, seq_lens, max_seq_len,
+                                     inv_freq, offset, interleaved, magnitude, stream)
 
 
 def kv_write_int8_contig(k_new, v_new, k_i8, v_i8, k_scale, v_scale, seq_lens=None, inv_freq=None, offset: int = 0,
                          interleaved: bool = False, magnitude: float = 1.0, stream=None):
     """kv_write_contig into an int8 cache: k_i8/v_i8 int8 [B, max_ctx, Hkv, D], k_scale/v_scale fp32
     [B, Hkv, max_ctx]; every (token, head) row is quantised by its largest magnitude."""
-    if k_scale is None:
-        raise ValueError("k: an int8 cache needs its scales")
-    _kv_write("kv_write_int8_contig", k_new, v_new, k_i8, v_i8, k_scale, v_scale, None, seq_lens, 0, inv_freq, offset,
-              interleaved, magnitude, stream)
+    (_ext_module or _ext()).kv_write(k_new, v_new, k_i8, v_i8, _int8(k_scale), v_scale, None, seq_lens, 0, inv_freq,
+                                     offset, interleaved, magnitude, stream)
 
 
 def kv_write_int8_paged(k_new, v_new, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens,
                         max_seq_len: int, inv_freq=None, offset: int = 0, interleaved: bool = False,
                         magnitude: float = 1.0, stream=None):
     """kv_write_int8_contig into page pools; scale pools fp32 [num_pages, Hkv, page_size]."""
-    if k_scale_pool is None:
-        raise ValueError("k: an int8 cache needs its scales")
-    _kv_write("kv_write_int8_paged", k_new, v_new, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table,
-              seq_lens, max_seq_len, inv_freq, offset, interleaved, magnitude, stream)
-
-
-def _kv_read(fn, k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, n, starts, k_out, v_out, stream):
-    torch = _t()
-    shape = k.shape
-    if len(shape) != 4:
-        raise ValueError(f"k: expected 4 dims, got {tuple(shape)}")
-    dev = k.get_device()
-    B = shape[0] if page_table is None else page_table.shape[0]
-    H, D = shape[2], shape[3]
-    where = _check_cache(k, v, k_scale, v_scale, page_table, seq_lens, B, H, D, dev)
-    if starts is not None:
-        _plain(starts, "starts", torch.int32, (B,), dev)
-    want = (B, n, H, D)
-    if k_out is None:
-        k_out = torch.zeros(want, dtype=torch.bfloat16, device=k.device)
-    else:
-        _plain(k_out, "k_out", torch.bfloat16, want, dev)
-    if v is None:
-        if v_out is not None:
-            raise ValueError("v_out: no v to read")
-    elif v_out is None:
-        v_out = torch.zeros(want, dtype=torch.bfloat16, device=k.device)
-    else:
-        _plain(v_out, "v_out", torch.bfloat16, want, dev)
-    _on_current(dev)
-    scales = () if k_scale is None else (k_scale.data_ptr(), _addr(v_scale))
-    if page_table is None:
-        place = (_addr(starts), _addr(seq_lens), B, n, H, D, *where)
-    else:
-        place = (page_table.data_ptr(), _addr(starts), seq_lens.data_ptr(), B, n, H, D, *where, max_seq_len)
-    st = getattr(_lib or load(), fn)(k.data_ptr(), _addr(v), *scales, *place, k_out.data_ptr(), _addr(v_out),
-                                     _raw_stream(stream, dev))
-    if st:
-        raise DecodeAttnError(fn, st)
-    return k_out, v_out
+    (_ext_module or _ext()).kv_write(k_new, v_new, k_pool_i8, v_pool_i8, _int8(k_scale_pool), v_scale_pool, page_table,
+                                     seq_lens, max_seq_len, inv_freq, offset, interleaved, magnitude, stream)
 
 
 def kv_read_paged(k_pool, v_pool, page_table, seq_lens, max_seq_len: int, n_tokens: int, starts=None, k_out=None,
@@ -719,26 +540,22 @@ def kv_read_paged(k_pool, v_pool, page_table, seq_lens, max_seq_len: int, n_toke
     """Tokens [starts[b], starts[b] + n_tokens) (starts int32 [B]; None: 0) of every sequence of a paged bf16 cache
     as contiguous bf16 [B, n_tokens, Hkv, D]: (k_out, v_out), v_out None with v_pool None.  Rows past a sequence
     are left as they were (zeros in outputs made here)."""
-    return _kv_read("kv_read_paged", k_pool, v_pool, None, None, page_table, seq_lens, max_seq_len, n_tokens, starts,
-                    k_out, v_out, stream)
+    return (_ext_module or _ext()).kv_read(k_pool, v_pool, None, None, page_table, seq_lens, max_seq_len, n_tokens,
+                                           starts, k_out, v_out, stream)
 
 
 def kv_read_int8_contig(k_i8, v_i8, k_scale, v_scale, seq_lens, n_tokens: int, starts=None, k_out=None, v_out=None,
                         stream=None):
     """kv_read_paged of a contiguous int8 cache (seq_lens may be None): value = int8 * scale, rounded to bf16."""
-    if k_scale is None:
-        raise ValueError("k: an int8 cache needs its scales")
-    return _kv_read("kv_read_int8_contig", k_i8, v_i8, k_scale, v_scale, None, seq_lens, 0, n_tokens, starts, k_out,
-                    v_out, stream)
+    return (_ext_module or _ext()).kv_read(k_i8, v_i8, _int8(k_scale), v_scale, None, seq_lens, 0, n_tokens, starts,
+                                           k_out, v_out, stream)
 
 
 def kv_read_int8_paged(k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens, max_seq_len: int,
                        n_tokens: int, starts=None, k_out=None, v_out=None, stream=None):
     """kv_read_paged of an int8 cache: value = int8 * scale, rounded to bf16."""
-    if k_scale_pool is None:
-        raise ValueError("k: an int8 cache needs its scales")
-    return _kv_read("kv_read_int8_paged", k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens,
-                    max_seq_len, n_tokens, starts, k_out, v_out, stream)
+    return (_ext_module or _ext()).kv_read(k_pool_i8, v_pool_i8, _int8(k_scale_pool), v_scale_pool, page_table, seq_lens,
+                                           max_seq_len, n_tokens, starts, k_out, v_out, stream)
 
 
 # ---------------------------------------------------------------- latent attention
@@ -757,50 +574,11 @@ def latent_max_batch(num_heads: int, latent_dim: int, q_len: int = 1) -> int:
 def latent_workspace(batch: int, num_heads: int, latent_dim: int, q_len: int = 1):
     """A workspace for latent_attn_* calls of this shape on the current CUDA device (uint8).  A program may keep
     one; calls that share it must not overlap on the GPU."""
-    torch = _t()
+    import torch
     n = load().latent_workspace_bytes(batch, q_len, num_heads, latent_dim, 0)
     if n < 0:
         raise DecodeAttnError("latent_workspace_bytes", -n)
     return torch.empty(n, dtype=torch.uint8, device="cuda")
-
-
-def _latent(fn, q, cache, page_table, seq_lens, max_seq_len, scale, workspace, out, stream):
-    torch = _t()
-    bf16 = torch.bfloat16
-    shape, cs = q.shape, cache.shape
-    if len(shape) != 4 or len(cs) != 3:
-        raise ValueError(f"q, cache: expected 4 and 3 dims, got {tuple(shape)} and {tuple(cs)}")
-    B, n, H, W = shape
-    R = W - LATENT_ROPE
-    dev = q.get_device()
-    _plain(q, "q", bf16, shape, dev)
-    _plain(cache, "cache", bf16, (B if page_table is None else cs[0], cs[1], W), dev)
-    if page_table is not None:
-        pt = page_table.shape
-        _plain(page_table, "page_table", torch.int32, (B, pt[1] if len(pt) == 2 else 0), dev)
-        if seq_lens is None:
-            raise ValueError("seq_lens: a paged cache needs them")
-    if seq_lens is not None:
-        _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    if out is None:
-        out = torch.empty((B, n, H, max(R, 0)), dtype=bf16, device=q.device)
-    else:
-        _plain(out, "out", bf16, (B, n, H, R), dev)
-    _on_current(dev)
-    if workspace is None:
-        workspace = latent_workspace(B, H, R, n)
-    elif not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
-    size = workspace.numel() * workspace.element_size()
-    if page_table is None:
-        place = (_addr(seq_lens), B, n, H, R, cs[1])
-    else:
-        place = (page_table.data_ptr(), seq_lens.data_ptr(), B, n, H, R, cs[1], pt[1], cs[0], max_seq_len)
-    st = getattr(_lib or load(), fn)(q.data_ptr(), cache.data_ptr(), *place, scale, workspace.data_ptr(), size,
-                                     out.data_ptr(), _raw_stream(stream, dev))
-    if st:
-        raise DecodeAttnError(fn, st)
-    return out
 
 
 def latent_attn_contig(q, cache, seq_lens=None, *, scale: float, workspace=None, out=None, stream=None):
@@ -808,31 +586,13 @@ def latent_attn_contig(q, cache, seq_lens=None, *, scale: float, workspace=None,
     tokens, causal among themselves), cache bf16 [B, max_ctx, R + 64], R in {128, 256, 512}; seq_lens int32 [B] or
     None.  scale is the head's own (one over the root of its width before absorption).  workspace: as made by
     latent_workspace (None: made here).  Returns out bf16 [B, q_len, H, R]."""
-    return _latent("latent_attn_contig", q, cache, None, seq_lens, 0, scale, workspace, out, stream)
+    return (_ext_module or _ext()).latent_attn(q, cache, None, seq_lens, 0, scale, workspace, out, stream)
 
 
 def latent_attn_paged(q, pool, page_table, seq_lens, max_seq_len: int, *, scale: float, workspace=None, out=None,
                       stream=None):
     """latent_attn_contig over a page pool [num_pages, page_size, R + 64]; page_table int32 [B, max_pages]."""
-    return _latent("latent_attn_paged", q, pool, page_table, seq_lens, max_seq_len, scale, workspace, out, stream)
-
-
-def _cache_strides(t, name, want, dev):
-    """(token, head) strides of keys or values [B, ctx, H, D] (or [B, ctx, D]): a head's elements consecutive, batch
-    entries ctx tokens apart.  Strides that no element is reached by are taken as dense."""
-    if t.dtype is not _torch.bfloat16 or t.shape != want or t.get_device() != dev:
-        raise ValueError(f"{name}: expected bf16 {tuple(want)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
-    st = t.stride()
-    B, ctx = want[0], want[1]
-    H, D = (want[2], want[3]) if len(want) == 4 else (1, want[2])
-    head = st[2] if H > 1 else D
-    dense = -(-((H - 1) * head + D) // 8) * 8
-    step = st[1] if ctx > 1 else st[0] if B > 1 and ctx == 1 else dense
-    if ctx and D and (st[-1] != 1 or (B > 1 and st[0] != ctx * step)):
-        raise ValueError(f"{name}: a head's elements must be consecutive and batch entries max_ctx tokens apart, got "
-                         f"strides {st}")
-    return step, head
+    return (_ext_module or _ext()).latent_attn(q, pool, page_table, seq_lens, max_seq_len, scale, workspace, out, stream)
 
 
 def latent_prefill_contig(q, k_nope, k_rope, v, seq_lens=None, *, scale: float, out=None, stream=None):
@@ -840,34 +600,7 @@ def latent_prefill_contig(q, k_nope, k_rope, v, seq_lens=None, *, scale: float, 
     [B, q_len, H, D + 64] (token-major), k_nope and v bf16 [B, max_ctx, H, D] (D 64 or 128; equally strided, e.g.
     the halves of one expansion), k_rope bf16 [B, max_ctx, 64], shared by the heads (tokens may be strided, e.g. the
     last columns of a latent cache); seq_lens int32 [B] or None.  Returns out bf16 [B, q_len, H, D]."""
-    torch = _t()
-    bf16 = torch.bfloat16
-    shape = q.shape
-    if len(shape) != 4:
-        raise ValueError(f"q: expected 4 dims, got {tuple(shape)}")
-    B, n, H, W = shape
-    D = W - LATENT_ROPE
-    dev = q.get_device()
-    _plain(q, "q", bf16, shape, dev)
-    ctx = k_nope.shape[1] if k_nope.dim() == 4 else 0
-    kts, khs = _cache_strides(k_nope, "k_nope", (B, ctx, H, D), dev)
-    vts, vhs = _cache_strides(v, "v", (B, ctx, H, D), dev)
-    pts, _ = _cache_strides(k_rope, "k_rope", (B, ctx, LATENT_ROPE), dev)
-    if (kts, khs) != (vts, vhs):
-        raise ValueError(f"v: expected the strides of k_nope, got {v.stride()} and {k_nope.stride()}")
-    if seq_lens is not None:
-        _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    if out is None:
-        out = torch.empty((B, n, H, max(D, 0)), dtype=bf16, device=q.device)
-    else:
-        _plain(out, "out", bf16, (B, n, H, D), dev)
-    _on_current(dev)
-    st = (_lib or load()).latent_prefill_contig(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
-                                                _addr(seq_lens), B, n, H, D, ctx, kts, khs, pts, scale, out.data_ptr(),
-                                                _raw_stream(stream, dev))
-    if st:
-        raise DecodeAttnError("latent_prefill_contig", st)
-    return out
+    return (_ext_module or _ext()).latent_prefill(q, k_nope, k_rope, v, seq_lens, scale, out, stream)
 
 
 def selftest_bounded_wait(timeout_ns: int, stream=None) -> None:

@@ -1,10 +1,13 @@
-"""Builds libdecode_attn.so in-tree with nvcc for sm_103a (no CMake; its units compile side by side)."""
+"""Builds libdecode_attn.so in-tree with nvcc for sm_103a, and the binding's CPython extension with the host compiler
+(no CMake; the units compile side by side)."""
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,6 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdecode_attn.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("decode_attn.cu", "latent_attn.cu", "cache_ops.cu")]
+EXT = os.path.join(PKG, "_binding_ext" + sysconfig.get_config_var("EXT_SUFFIX"))
+EXT_SOURCE = os.path.join(CSRC, "binding_ext.cpp")
 HEADERS = [os.path.join(ROOT, "include", "decode_attn.h")] + [
     os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cuh", ".h"))
 ]
@@ -35,11 +40,22 @@ def link_command(out: str, objects) -> list:
             *objects]
 
 
+def ext_command(out: str) -> list:
+    """Compiles the binding's extension against the installed PyTorch (found without importing it)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(torch, "lib")
+    return [os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-std=c++17", "-O2", *("-I" + i for i in include),
+            EXT_SOURCE, "-o", out, "-L" + lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", "-ldl"]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in SOURCES + HEADERS)
+    def newer(out, sources):
+        return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in sources)
+    return newer(LIB, SOURCES + HEADERS) and newer(EXT, [EXT_SOURCE, HEADERS[0]])
 
 
 def _run(cmd: list):
@@ -52,18 +68,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     with tempfile.TemporaryDirectory() as tmpdir:
         objects = [os.path.join(tmpdir, os.path.basename(src) + ".o") for src in SOURCES]
-        with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
-            done = list(pool.map(_run, map(nvcc_command, objects, SOURCES)))
+        ext = os.path.join(tmpdir, "ext.so")
+        commands = [*map(nvcc_command, objects, SOURCES), ext_command(ext)]
+        with concurrent.futures.ThreadPoolExecutor(len(commands)) as pool:
+            done = list(pool.map(_run, commands))
         if all(res.returncode == 0 for res in done):
-            tmp = LIB + ".tmp"
-            done.append(_run(link_command(tmp, objects)))
+            done.append(_run(link_command(os.path.join(tmpdir, "lib.so"), objects)))
+        if all(res.returncode == 0 for res in done):
+            for made, out in ((os.path.join(tmpdir, "lib.so"), LIB), (ext, EXT)):
+                shutil.copy(made, out + ".tmp")
+                os.replace(out + ".tmp", out)
     for res in done:
         if verbose or res.returncode != 0:
             print(" ".join(res.args))
             print(res.stdout + res.stderr)
     if any(res.returncode != 0 for res in done):
         raise RuntimeError("nvcc failed building libdecode_attn.so")
-    os.replace(tmp, LIB)
     return LIB
 
 
