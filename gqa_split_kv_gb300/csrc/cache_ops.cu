@@ -9,6 +9,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/decode_attn.h"
 #include "device_error.cuh"
@@ -56,83 +57,179 @@ __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v);
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
 
+// A 16-byte chunk to and from fp32, two 16-bit elements an instruction.
 template <typename T>
-union Chunk {  // 16 bytes
-  uint4 raw;
-  T v[16 / sizeof(T)];
+struct Chunk;
+template <>
+struct Chunk<float> {
+  static __device__ __forceinline__ void unpack(uint4 w, float (&f)[4]) {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
 };
+template <>
+struct Chunk<__nv_bfloat16> {
+  static __device__ __forceinline__ void unpack(uint4 w, float (&f)[8]) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16lo_to_f32(q[i]);
+      f[2 * i + 1] = bf16hi_to_f32(q[i]);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Chunk<__half> {
+  static __device__ __forceinline__ void unpack(uint4 w, float (&f)[8]) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = f16lo_to_f32(q[i]);
+      f[2 * i + 1] = f16hi_to_f32(q[i]);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                      pack_f16x2(f[6], f[7]));
+  }
+};
+
+// The cosines and sines of pairs j .. j + n - 1 (j even: two pairs a read).
+template <int N>
+__device__ __forceinline__ void load_cs(const float2* cs, int j, float2 (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + j + i);
+    w[i] = make_float2(c.x, c.y);
+    w[i + 1] = make_float2(c.z, c.w);
+  }
+}
+
+// Rotates the pairs (a[i], b[i]), or the pairs of neighbours in a.
+template <int V>
+__device__ __forceinline__ void rotate_half(float (&a)[V], float (&b)[V], const float2* cs, int j) {
+  float2 w[V];
+  load_cs(cs, j, w);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float f = a[i], g = b[i];
+    a[i] = f * w[i].x - g * w[i].y;
+    b[i] = f * w[i].y + g * w[i].x;
+  }
+}
+template <int V>
+__device__ __forceinline__ void rotate_neighbours(float (&a)[V], const float2* cs, int j) {
+  float2 w[V / 2];
+  load_cs(cs, j, w);
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    const float f = a[i], g = a[i + 1];
+    a[i] = f * w[i / 2].x - g * w[i / 2].y;
+    a[i + 1] = f * w[i / 2].y + g * w[i / 2].x;
+  }
+}
 
 // One CTA a token at a time: its rot / 2 cosines and sines go to shared memory once
 // and serve every head.  VECTOR: all offsets and strides are whole 16-byte chunks; an
 // item is a chunk (interleaved: whole pairs; a copy) or the two chunks that hold the
 // halves of the same pairs.  Otherwise an item is one pair or one copied element.
+//
+// Bound by HBM (read and write once).  A thread's loads of the first U items go out
+// before the position is known: with them after the cosines, a token takes two memory
+// latencies and the sines in a row (4096 tokens x 32 heads x 128: 22.5 us; floor 10).
 template <typename T, bool VECTOR>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p) {
   extern __shared__ __align__(16) uint8_t rope_smem[];
   const int np = p.r.rot / 2;
   unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
-  float2* cs = reinterpret_cast<float2*>(step + np);
+  float2* cs = reinterpret_cast<float2*>(step + (np + 1) / 2 * 2);  // 16-byte aligned
   for (int j = threadIdx.x; j < np; j += kThreads) step[j] = rope_turn_step(p.r.inv_freq[j]);
   constexpr int V = VECTOR ? 16 / (int)sizeof(T) : 1;
+  constexpr int U = 2;  // items a thread has in flight
   // items of one head: the rotated ones first, then the copies
   const int nrot = VECTOR && p.r.interleaved ? p.r.rot / V : np / V;
   const int ncopy = p.copy ? (p.D - p.r.rot) / V : 0;
-  const int per_head = nrot + ncopy;
+  const int per_head = nrot + ncopy, items = p.H * per_head;
   const int lo = p.r.offset / V;  // copied items before the rotated part
+  // this thread's first item is the same of every token; kThreads items on is (dh, dk) on
+  const int h0 = threadIdx.x / per_head, k0 = threadIdx.x - h0 * per_head;
+  const int dh = kThreads / per_head, dk = kThreads - dh * per_head;
+  const int second = VECTOR || !p.r.interleaved ? np : 1;  // from a pair's first half to its second
+  const bool two = !(VECTOR && p.r.interleaved);           // the halves are loaded apart
+  // an item's element (of the first of its two chunks or elements)
+  auto place = [&](int k) {
+    if (k < nrot) return VECTOR || !p.r.interleaved ? p.r.offset + k * V : p.r.offset + 2 * k;
+    const int c = k - nrot;
+    return (c < lo ? c : c + p.r.rot / V) * V;
+  };
+  using Item = typename std::conditional<VECTOR, uint4, T>::type;
   for (long long t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     const int pos = __ldg(p.positions + t);
-    __syncthreads();  // step is written; the last token's cosines are read
-    for (int j = threadIdx.x; j < np; j += kThreads) cs[j] = rope_cos_sin(step[j], pos, p.r);
-    __syncthreads();
     const T* x = static_cast<const T*>(p.x) + t * p.xt;
     T* out = static_cast<T*>(p.out) + t * p.ot;
-    for (int e = threadIdx.x; e < p.H * per_head; e += kThreads) {
-      const int h = e / per_head, k = e - h * per_head;
-      const T* xh = x + h * p.xh;
-      T* oh = out + h * p.oh;
-      if (k >= nrot) {
-        const int c = k - nrot;
-        const int at = (c < lo ? c : c + p.r.rot / V) * V;
-        if constexpr (VECTOR)
-          *reinterpret_cast<uint4*>(oh + at) = *reinterpret_cast<const uint4*>(xh + at);
-        else
-          oh[at] = xh[at];
-        continue;
-      }
-      if constexpr (VECTOR) {
-        if (p.r.interleaved) {
-          const int at = p.r.offset + k * V;
-          Chunk<T> a;
-          a.raw = *reinterpret_cast<const uint4*>(xh + at);
+    int h = h0, k = k0;
+    for (int e0 = 0; e0 < items; e0 += U * kThreads) {
+      Item a[U], b[U];
+      int at[U];
+      bool rotates[U];
+      long long oh[U];
 #pragma unroll
-          for (int i = 0; i < V; i += 2) {
-            const float2 w = cs[k * (V / 2) + i / 2];
-            const float u = to_f32(a.v[i]), v = to_f32(a.v[i + 1]);
-            a.v[i] = from_f32<T>(u * w.x - v * w.y);
-            a.v[i + 1] = from_f32<T>(u * w.y + v * w.x);
-          }
-          *reinterpret_cast<uint4*>(oh + at) = a.raw;
-        } else {
-          const int at = p.r.offset + k * V;
-          Chunk<T> a, b;
-          a.raw = *reinterpret_cast<const uint4*>(xh + at);
-          b.raw = *reinterpret_cast<const uint4*>(xh + at + np);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float2 w = cs[k * V + i];
-            const float u = to_f32(a.v[i]), v = to_f32(b.v[i]);
-            a.v[i] = from_f32<T>(u * w.x - v * w.y);
-            b.v[i] = from_f32<T>(u * w.y + v * w.x);
-          }
-          *reinterpret_cast<uint4*>(oh + at) = a.raw;
-          *reinterpret_cast<uint4*>(oh + at + np) = b.raw;
+      for (int u = 0; u < U; ++u) {
+        rotates[u] = k < nrot && h < p.H;
+        at[u] = h < p.H ? place(k) : -1;
+        oh[u] = h * p.oh;
+        if (h < p.H) {
+          const T* src = x + h * p.xh + at[u];
+          a[u] = *reinterpret_cast<const Item*>(src);
+          if (rotates[u] && two) b[u] = *reinterpret_cast<const Item*>(src + second);
         }
-      } else {
-        const int at = p.r.offset + (p.r.interleaved ? 2 * k : k), bt = at + (p.r.interleaved ? 1 : np);
-        const float2 w = cs[k];
-        const float u = to_f32(xh[at]), v = to_f32(xh[bt]);
-        oh[at] = from_f32<T>(u * w.x - v * w.y);
-        oh[bt] = from_f32<T>(u * w.y + v * w.x);
+        k += dk;
+        h += dh;
+        if (k >= per_head) {
+          k -= per_head;
+          ++h;
+        }
+      }
+      if (e0 == 0) {      // the token's cosines
+        __syncthreads();  // step is written; the last token's cosines are read
+        for (int j = threadIdx.x; j < np; j += kThreads) cs[j] = rope_cos_sin(step[j], pos, p.r);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (at[u] < 0) continue;
+        T* o = out + oh[u] + at[u];
+        if (rotates[u]) {
+          if constexpr (VECTOR) {
+            const int j = at[u] - p.r.offset;
+            float f[V], g[V];
+            Chunk<T>::unpack(a[u], f);
+            if (two) {
+              Chunk<T>::unpack(b[u], g);
+              rotate_half(f, g, cs, j);
+              b[u] = Chunk<T>::pack(g);
+            } else {
+              rotate_neighbours(f, cs, j / 2);
+            }
+            a[u] = Chunk<T>::pack(f);
+          } else {
+            const float2 w = cs[p.r.interleaved ? (at[u] - p.r.offset) / 2 : at[u] - p.r.offset];
+            const float f = to_f32(a[u]), g = to_f32(b[u]);
+            a[u] = from_f32<T>(f * w.x - g * w.y);
+            b[u] = from_f32<T>(f * w.y + g * w.x);
+          }
+          if (two) *reinterpret_cast<Item*>(o + second) = b[u];
+        }
+        *reinterpret_cast<Item*>(o) = a[u];
       }
     }
   }
@@ -144,7 +241,7 @@ int launch_rope(const RopeApplyParams& p, int sms, cudaStream_t st) {
   const int half = p.r.interleaved ? p.r.rot : p.r.rot / 2;
   const bool vec = aligned(p.x, 16) && aligned(p.out, 16) && p.D % V == 0 && p.r.offset % V == 0 && half % V == 0 &&
                    p.r.rot % V == 0 && p.xt % V == 0 && p.xh % V == 0 && p.ot % V == 0 && p.oh % V == 0;
-  const size_t smem = (size_t)(p.r.rot / 2) * 16;
+  const size_t smem = (size_t)(p.r.rot / 2 + 1) * 16;
   const long long cap = 8LL * sms;  // 2048 threads an SM
   const unsigned grid = (unsigned)(p.tokens < cap ? p.tokens : cap);
   if (vec)
@@ -209,55 +306,30 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
   return slab_index * p.slab + in_slab;
 }
 
-__device__ __forceinline__ void unpack8(uint4 w, float (&f)[8]) {
-  f[0] = bf16lo_to_f32(w.x);
-  f[1] = bf16hi_to_f32(w.x);
-  f[2] = bf16lo_to_f32(w.y);
-  f[3] = bf16hi_to_f32(w.y);
-  f[4] = bf16lo_to_f32(w.z);
-  f[5] = bf16hi_to_f32(w.z);
-  f[6] = bf16lo_to_f32(w.w);
-  f[7] = bf16hi_to_f32(w.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
 // A CTA takes tb new tokens at a time.  A row (token, tensor, head) of D elements has
 // `lanes` lanes of one warp, CPL chunks of 8 elements each.  K rows are rotated in fp32
 // on the way (a half-layout lane also loads the chunk with the other halves of its
 // pairs: an L1 hit) and int8 rows quantised from that fp32 value, so a key is rounded
-// once.  The row's maximum is a shuffle over its lanes.
+// once.  The row's maximum is a shuffle over its lanes.  Bound by HBM for a chunk and by
+// latency for a step: the rows' loads, the length, the page and the cosines overlap.
 template <bool PAGED, bool INT8, int CPL>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p) {
   extern __shared__ __align__(16) uint8_t rope_smem[];
   const int np = p.r.inv_freq ? p.r.rot / 2 : 0;
   unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
-  float2* cs = reinterpret_cast<float2*>(step + np);  // [tb][np]
+  float2* cs = reinterpret_cast<float2*>(step + np);  // [tb][np] (np a multiple of 8)
   for (int j = threadIdx.x; j < np; j += kThreads) step[j] = rope_turn_step(p.r.inv_freq[j]);
-  const long long total = (long long)p.B * p.n;
+  const unsigned total = (unsigned)p.B * (unsigned)p.n;  // below 2^31
   const int rows_per_token = p.Hkv * (p.v ? 2 : 1);
   const int rows = p.tb * rows_per_token;
   const int nchunk = p.D / 8, gl = threadIdx.x & (p.lanes - 1);
   // position of new token g = b n + i: L_b - n + i
-  auto position = [&](long long g, int& b) -> long long {
-    b = (int)(g / p.n);
+  auto position = [&](unsigned g, int& b) -> long long {
+    b = (int)(g / (unsigned)p.n);
     const int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
-    return (long long)L - p.n + (g - (long long)b * p.n);
+    return (long long)L - p.n + (int)(g - (unsigned)b * (unsigned)p.n);
   };
-  for (long long g0 = (long long)blockIdx.x * p.tb; g0 < total; g0 += (long long)gridDim.x * p.tb) {
-    if (np) {
-      __syncthreads();
-      for (int e = threadIdx.x; e < p.tb * np; e += kThreads) {
-        const long long g = g0 + e / np;
-        if (g < total) {
-          int b;
-          cs[e] = rope_cos_sin(step[e % np], (int)position(g, b), p.r);
-        }
-      }
-      __syncthreads();
-    }
+  for (unsigned g0 = blockIdx.x * p.tb; g0 < total; g0 += gridDim.x * p.tb) {
     // every lane of a warp runs the same number of rounds (the shuffles need them all)
     const int per_round = kThreads / p.lanes;
     for (int r0 = 0; r0 < rows; r0 += per_round) {
@@ -265,10 +337,27 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
       const int ti = row / rows_per_token, in_token = row - ti * rows_per_token;
       const bool is_v = in_token >= p.Hkv;
       const int h = is_v ? in_token - p.Hkv : in_token;
-      const long long g = g0 + ti;
+      const unsigned g = g0 + ti;
+      const bool there = row < rows && g < total;
       long long slab = 0, dst = -1;
       int in_slab = 0;
-      if (row < rows && g < total) {
+      // the row's elements do not depend on its place, so their loads go out first
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) +
+                                 (there ? g * (is_v ? p.v_stride : p.k_stride) + (long long)h * p.D : 0);
+      const bool rotates = np && !is_v;
+      uint4 raw[CPL], other[CPL];
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        const int ch = gl + c * p.lanes;
+        raw[c] = other[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (there && ch < nchunk) {
+          raw[c] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
+          const int at = ch * 8 - p.r.offset;  // within the rotated part
+          if (rotates && !p.r.interleaved && at >= 0 && at < p.r.rot)  // the other halves of these pairs
+            other[c] = __ldg(reinterpret_cast<const uint4*>(src + p.r.offset + (at >= np ? at - np : at + np)));
+        }
+      }
+      if (there) {
         int b;
         const long long pos = position(g, b);
         if (pos >= p.cap) {
@@ -277,59 +366,51 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
           dst = cache_row<PAGED>(p, b, (int)pos, slab, in_slab);
         }
       }
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) +
-                                 (dst < 0 ? 0 : g * (is_v ? p.v_stride : p.k_stride) + (long long)h * p.D);
+      if (np && r0 == 0) {  // the round's tokens' cosines
+        __syncthreads();    // step is written; the last ones are read
+        for (int e = threadIdx.x; e < p.tb * np; e += kThreads) {
+          const unsigned gt = g0 + e / np;
+          int b;
+          if (gt < total) cs[e] = rope_cos_sin(step[e % np], (int)position(gt, b), p.r);
+        }
+        __syncthreads();
+      }
       float x[CPL][8];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
-        const int ch = gl + c * p.lanes;
-        if (dst >= 0 && ch < nchunk) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(src) + ch), x[c]);
-          const int at = ch * 8 - p.r.offset;  // within the rotated part
-          if (np && !is_v && at >= 0 && at < p.r.rot) {
-            const float2* w = cs + ti * np;
-            if (p.r.interleaved) {
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                const float2 a = w[(at + i) / 2];
-                const float u = x[c][i], v = x[c][i + 1];
-                x[c][i] = u * a.x - v * a.y;
-                x[c][i + 1] = u * a.y + v * a.x;
-              }
-            } else {
-              const bool second = at >= np;
-              const int j = second ? at - np : at;
-              float o[8];  // the other halves of these pairs
-              unpack8(__ldg(reinterpret_cast<const uint4*>(src + p.r.offset + (second ? j : j + np))), o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 a = w[j + i];
-                x[c][i] = second ? o[i] * a.y + x[c][i] * a.x : x[c][i] * a.x - o[i] * a.y;
-              }
-            }
+        Chunk<__nv_bfloat16>::unpack(raw[c], x[c]);
+        const int at = (gl + c * p.lanes) * 8 - p.r.offset;
+        if (rotates && there && at >= 0 && at < p.r.rot) {
+          const float2* w = cs + ti * np;
+          if (p.r.interleaved) {
+            rotate_neighbours(x[c], w, at / 2);
+          } else {
+            float o[8];
+            Chunk<__nv_bfloat16>::unpack(other[c], o);
+            if (at >= np)
+              rotate_half(o, x[c], w, at - np);
+            else
+              rotate_half(x[c], o, w, at);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] = 0.f;
         }
       }
       if constexpr (INT8) {
-        // largest magnitude; a NaN anywhere makes it NaN (fmaxf would drop it), so the
-        // row's scale and everything read back from it are NaN
-        float top = 0.f;
-        bool nan = false;
+        // The largest magnitude by its bits, whose order is that of the magnitudes, with
+        // infinity and the NaNs above them: a row with any of those gets a NaN scale and zeros.
+        unsigned bits = 0;
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            top = fmaxf(top, fabsf(x[c][i]));
-            nan |= x[c][i] != x[c][i];
-          }
-        if (nan) top = __int_as_float(0x7f800000);
-        for (int o = p.lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool finite = top < __int_as_float(0x7f800000);
+          for (int i = 0; i < 8; ++i) bits = max(bits, __float_as_uint(x[c][i]) & 0x7fffffffu);
+        for (int o = p.lanes / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+        const bool finite = bits < 0x7f800000u;
+        const float top = __uint_as_float(bits);
         // 127 2^-126 and less would leave a scale below the normal numbers: floor it
-        float scale = top > 0.f ? fmaxf(__fdiv_rn(top, 127.f), 1.17549435e-38f) : 1.f;
+        float scale = bits ? fmaxf(__fdiv_rn(top, 127.f), 1.17549435e-38f) : 1.f;
+        // x / scale, rounded as a division is: a quotient from the rounded reciprocal and one
+        // correction by its remainder (Markstein); adding 1.5 2^23 leaves the nearest integer,
+        // ties to even, in the low bits, and no quotient passes 127 by half a step
+        const float inv = __frcp_rn(scale);
         if (!finite) scale = __int_as_float(0x7fffffff);
         if (dst >= 0) {
           int8_t* q = static_cast<int8_t*>(is_v ? p.v : p.k) + (dst * p.Hkv + h) * p.D;
@@ -337,13 +418,17 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
           for (int c = 0; c < CPL; ++c) {
             const int ch = gl + c * p.lanes;
             if (ch >= nchunk) continue;
-            uint32_t w[2] = {0u, 0u};
+            uint32_t n[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int v = finite ? max(-127, min(127, __float2int_rn(__fdiv_rn(x[c][i], scale)))) : 0;
-              w[i / 4] |= (uint32_t)(v & 255) << (8 * (i % 4));
+              const float r = x[c][i] * inv;
+              n[i] = __float_as_uint(fmaf(fmaf(-r, scale, x[c][i]), inv, r) + 12582912.f);
             }
-            *reinterpret_cast<uint2*>(q + ch * 8) = make_uint2(w[0], w[1]);
+            uint2 w;
+            w.x = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+            w.y = __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410);
+            if (!finite) w = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(q + ch * 8) = w;
           }
           if (gl == 0) (is_v ? p.vs : p.ks)[(slab * p.Hkv + h) * p.slab + in_slab] = scale;
         }
@@ -352,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
           const int ch = gl + c * p.lanes;
-          if (ch < nchunk) *reinterpret_cast<uint4*>(q + ch * 8) = pack8(x[c]);
+          if (ch < nchunk) *reinterpret_cast<uint4*>(q + ch * 8) = Chunk<__nv_bfloat16>::pack(x[c]);
         }
       }
     }

@@ -67,7 +67,7 @@ int launch_latent(const LatentParams& prm, int sms, int dev, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(items < 2LL * sms ? items : 2LL * sms));
+  cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
   cfg.blockDim = dim3(LatentCombineGeo::NTHREADS);
   cfg.dynamicSmemBytes = (size_t)LatentCombineGeo::smem_bytes(prm.ranges, prm.B);
   cfg.attrs = attr;

@@ -50,6 +50,7 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "device_error.cuh"
 #include "plan.cuh"
@@ -633,8 +634,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
 
 // Merge of the partials: for each row, M = max_j m_j over slots with l_j > 0, w_j =
 // 2^(m_j - M), out = sum_j w_j acc_j / sum_j w_j l_j.  An item is 128 latents of a row, a
-// float4 a lane.  Rows of up to 32 pieces are a warp's work with 8 loads in flight,
-// summed in ascending j.  A segment of more pieces fills more than 30 ranges, so there
+// float4 a lane.  Rows of up to 32 pieces are a warp's work, summed in ascending j.  A segment of more pieces fills more than 30 ranges, so there
 // are few of them: warp 0 lists them in order, and each of their items takes a CTA, 16
 // warps of slots (10 loads a thread in flight: 160 slots at once) whose sums are added in
 // order.  Rows of empty sequences are zeroed.  All
@@ -648,7 +648,7 @@ struct LatentCombineParams {
 };
 
 struct LatentCombineGeo {
-  static constexpr int NTHREADS = 512, W = NTHREADS / 32, KB = 8, SHORT = 32;
+  static constexpr int NTHREADS = 512, W = NTHREADS / 32, SHORT = 32;
   // shared: lane sums, weights of a long run, the list of long segments, the plan
   static constexpr int OFF_WTS = W * 32 * 16;
   __host__ __device__ static constexpr int off_list(int ranges) { return OFF_WTS + (ranges + 1 + 3) / 4 * 16; }
@@ -657,7 +657,7 @@ struct LatentCombineGeo {
 };
 
 template <int R>
-__global__ void __launch_bounds__(512, 2) latent_combine_kernel(const LatentCombineParams p) {
+__global__ void __launch_bounds__(512, 1) latent_combine_kernel(const LatentCombineParams p) {
   using Cg = LatentCombineGeo;
   extern __shared__ __align__(16) uint8_t csm[];
   float4* lane_sum = reinterpret_cast<float4*>(csm);               // [W][32]
@@ -783,47 +783,62 @@ __global__ void __launch_bounds__(512, 2) latent_combine_kernel(const LatentComb
     }
     __syncthreads();
   }
-  // ---- short segments and empty sequences
-  const unsigned items = (unsigned)p.B * p.rows * NCH;
-  for (unsigned item = blockIdx.x * Cg::W + warp; item < items; item += gridDim.x * Cg::W) {
-    const int ch = item % NCH, grow = item / NCH;
-    const int b = grow / p.rows, row = grow - b * p.rows;
-    const int u = row / p.N, col = row - u * p.N;
-    const int n = segment_pieces(pl, lens, P, p.B, b, u);
-    if (n == 1 || n > Cg::SHORT) continue;
-    const int r0 = n > 0 ? first_range(b, u) : 0;
-    float4 a[Cg::KB];
+  // ---- short segments and empty sequences: CPI chunks of a row are a warp's work, 16 loads a
+  // lane in flight.  Whole rows when there are rows enough for every warp, else chunks.
+  auto merge_short = [&](auto cpi) {
+    constexpr int CPI = decltype(cpi)::value, PARTS = NCH / CPI, KB = 16 / CPI;
+    const unsigned items = (unsigned)p.B * p.rows * PARTS;
+    for (unsigned item = blockIdx.x * Cg::W + warp; item < items; item += gridDim.x * Cg::W) {
+      const int ch = item % PARTS * CPI, grow = item / PARTS;
+      const int b = grow / p.rows, row = grow - b * p.rows;
+      const int u = row / p.N, col = row - u * p.N;
+      const int n = segment_pieces(pl, lens, P, p.B, b, u);
+      if (n == 1 || n > Cg::SHORT) continue;
+      const int r0 = n > 0 ? first_range(b, u) : 0;
+      float4 a[KB][CPI];
+      auto fetch = [&](int j0) {
 #pragma unroll
-    for (int j = 0; j < Cg::KB; ++j)
-      a[j] = j < n ? __ldcg(acc_at(r0, j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float2 ml = lane < n ? ml_at(r0, lane, col) : make_float2(kNegInf, 0.f);
-    const bool live = is_live(ml.y);
-    float M = live ? ml.x : kNegInf;
+        for (int j = 0; j < KB; ++j)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float wgt = live ? exp2_approx(ml.x - M) : 0.f;
-    float den = 0.f;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < n; j0 += Cg::KB) {
-      if (j0 > 0) {
+          for (int c = 0; c < CPI; ++c)
+            a[j][c] = j0 + j < n ? __ldcg(acc_at(r0, j0 + j, col, ch + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+      fetch(0);
+      const float2 ml = lane < n ? ml_at(r0, lane, col) : make_float2(kNegInf, 0.f);
+      const bool live = is_live(ml.y);
+      float M = live ? ml.x : kNegInf;
 #pragma unroll
-        for (int j = 0; j < Cg::KB; ++j)
-          a[j] = j0 + j < n ? __ldcg(acc_at(r0, j0 + j, col, ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float wgt = live ? exp2_approx(ml.x - M) : 0.f;
+      float den = 0.f;
+      float4 s[CPI];
 #pragma unroll
-      for (int j = 0; j < Cg::KB; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, wgt, j0 + j), lj = __shfl_sync(0xffffffffu, ml.y, j0 + j);
-        if (j0 + j < n && wj != 0.f) {
-          den += wj * lj;
-          s.x += wj * a[j].x;
-          s.y += wj * a[j].y;
-          s.z += wj * a[j].z;
-          s.w += wj * a[j].w;
+      for (int c = 0; c < CPI; ++c) s[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j0 = 0; j0 < n; j0 += KB) {
+        if (j0 > 0) fetch(j0);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, wgt, (j0 + j) & 31), lj = __shfl_sync(0xffffffffu, ml.y, (j0 + j) & 31);
+          if (j0 + j < n && wj != 0.f) {
+            den += wj * lj;
+#pragma unroll
+            for (int c = 0; c < CPI; ++c) {
+              s[c].x += wj * a[j][c].x;
+              s[c].y += wj * a[j][c].y;
+              s[c].z += wj * a[j][c].z;
+              s[c].w += wj * a[j][c].w;
+            }
+          }
         }
       }
+#pragma unroll
+      for (int c = 0; c < CPI; ++c) put(b, row, ch + c, s[c], den);
     }
-    put(b, row, ch, s, den);
-  }
+  };
+  if ((unsigned)p.B * p.rows >= gridDim.x * Cg::W)
+    merge_short(std::integral_constant<int, NCH>{});
+  else
+    merge_short(std::integral_constant<int, 1>{});
 }
 
 }  // namespace da
