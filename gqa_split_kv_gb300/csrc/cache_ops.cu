@@ -311,14 +311,16 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
 // on the way (a half-layout lane also loads the chunk with the other halves of its
 // pairs: an L1 hit) and int8 rows quantised from that fp32 value, so a key is rounded
 // once.  The row's maximum is a shuffle over its lanes.  Bound by HBM for a chunk and by
-// latency for a step: the rows' loads, the length, the page and the cosines overlap.
+// latency for a step: the first rows' loads go out before the lengths, pages and cosines,
+// which are looked up once a token.
+constexpr int kMaxTokens = 16;  // tokens a CTA takes at a time, at most
 template <bool PAGED, bool INT8, int CPL>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p) {
   extern __shared__ __align__(16) uint8_t rope_smem[];
+  __shared__ long long tok_row[kMaxTokens], tok_scale[kMaxTokens];  // cache row, or -1; its first head's scale
   const int np = p.r.inv_freq ? p.r.rot / 2 : 0;
   unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
   float2* cs = reinterpret_cast<float2*>(step + np);  // [tb][np] (np a multiple of 8)
-  for (int j = threadIdx.x; j < np; j += kThreads) step[j] = rope_turn_step(p.r.inv_freq[j]);
   const unsigned total = (unsigned)p.B * (unsigned)p.n;  // below 2^31
   const int rows_per_token = p.Hkv * (p.v ? 2 : 1);
   const int rows = p.tb * rows_per_token;
@@ -329,9 +331,10 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
     const int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
     return (long long)L - p.n + (int)(g - (unsigned)b * (unsigned)p.n);
   };
+  bool first = true;
+  // every lane of a warp runs the same number of rounds (the shuffles need them all)
+  const int per_round = kThreads / p.lanes;
   for (unsigned g0 = blockIdx.x * p.tb; g0 < total; g0 += gridDim.x * p.tb) {
-    // every lane of a warp runs the same number of rounds (the shuffles need them all)
-    const int per_round = kThreads / p.lanes;
     for (int r0 = 0; r0 < rows; r0 += per_round) {
       const int row = r0 + threadIdx.x / p.lanes;
       const int ti = row / rows_per_token, in_token = row - ti * rows_per_token;
@@ -339,12 +342,12 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
       const int h = is_v ? in_token - p.Hkv : in_token;
       const unsigned g = g0 + ti;
       const bool there = row < rows && g < total;
-      long long slab = 0, dst = -1;
-      int in_slab = 0;
       // the row's elements do not depend on its place, so their loads go out first
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) +
                                  (there ? g * (is_v ? p.v_stride : p.k_stride) + (long long)h * p.D : 0);
       const bool rotates = np && !is_v;
+      // the halves of a pair are one lane's two chunks (a fully rotated head of 2 chunks a lane)
+      const bool paired = CPL == 2 && !p.r.interleaved && np == 8 * p.lanes && p.r.offset == 0;
       uint4 raw[CPL], other[CPL];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
@@ -353,32 +356,41 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
         if (there && ch < nchunk) {
           raw[c] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
           const int at = ch * 8 - p.r.offset;  // within the rotated part
-          if (rotates && !p.r.interleaved && at >= 0 && at < p.r.rot)  // the other halves of these pairs
+          if (rotates && !p.r.interleaved && !paired && at >= 0 && at < p.r.rot)  // the other halves of these pairs
             other[c] = __ldg(reinterpret_cast<const uint4*>(src + p.r.offset + (at >= np ? at - np : at + np)));
         }
       }
-      if (there) {
-        int b;
-        const long long pos = position(g, b);
-        if (pos >= p.cap) {
-          atomicOr(&g_error_word, 8u);
-        } else if (pos >= 0) {
-          dst = cache_row<PAGED>(p, b, (int)pos, slab, in_slab);
+      if (r0 == 0) {  // the tokens' places and cosines
+        if (first)
+          for (int j = threadIdx.x; j < np; j += kThreads) step[j] = rope_turn_step(p.r.inv_freq[j]);
+        first = false;
+        __syncthreads();  // step is written; the last tokens' cosines and places are read
+        const int helper = (int)kThreads - 1 - (int)threadIdx.x;  // the last threads have the fewest cosines
+        if (helper < p.tb) {
+          long long slab = 0, place = -1;
+          int in_slab = 0, b;
+          if (g0 + helper < total) {
+            const long long pos = position(g0 + helper, b);
+            if (pos >= p.cap)
+              atomicOr(&g_error_word, 8u);
+            else if (pos >= 0)
+              place = cache_row<PAGED>(p, b, (int)pos, slab, in_slab);
+          }
+          tok_row[helper] = place;
+          tok_scale[helper] = slab * p.Hkv * p.slab + in_slab;
         }
-      }
-      if (np && r0 == 0) {  // the round's tokens' cosines
-        __syncthreads();    // step is written; the last ones are read
-        for (int e = threadIdx.x; e < p.tb * np; e += kThreads) {
-          const unsigned gt = g0 + e / np;
+        for (int e = threadIdx.x, i = e / max(np, 1); e < p.tb * np; e += kThreads, i = e / np) {
           int b;
-          if (gt < total) cs[e] = rope_cos_sin(step[e % np], (int)position(gt, b), p.r);
+          if (g0 + i < total) cs[e] = rope_cos_sin(step[e - i * np], (int)position(g0 + i, b), p.r);
         }
         __syncthreads();
       }
+      const long long dst = there ? tok_row[ti] : -1;
       float x[CPL][8];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
         Chunk<__nv_bfloat16>::unpack(raw[c], x[c]);
+        if (paired) continue;
         const int at = (gl + c * p.lanes) * 8 - p.r.offset;
         if (rotates && there && at >= 0 && at < p.r.rot) {
           const float2* w = cs + ti * np;
@@ -394,6 +406,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
           }
         }
       }
+      if (CPL == 2 && paired && rotates && there) rotate_half(x[0], x[CPL - 1], cs + ti * np, gl * 8);
       if constexpr (INT8) {
         // The largest magnitude by its bits, whose order is that of the magnitudes, with
         // infinity and the NaNs above them: a row with any of those gets a NaN scale and zeros.
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
             if (!finite) w = make_uint2(0u, 0u);
             *reinterpret_cast<uint2*>(q + ch * 8) = w;
           }
-          if (gl == 0) (is_v ? p.vs : p.ks)[(slab * p.Hkv + h) * p.slab + in_slab] = scale;
+          if (gl == 0) (is_v ? p.vs : p.ks)[tok_scale[ti] + (long long)h * p.slab] = scale;
         }
       } else if (dst >= 0) {
         __nv_bfloat16* q = static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) + (dst * p.Hkv + h) * p.D;
@@ -506,21 +519,30 @@ int check_cache_pointers(const CacheParams& p, bool paged, bool int8) {
 
 template <bool PAGED, bool INT8>
 int launch_write(CacheParams& p, int sms, cudaStream_t st) {
+  // two chunks a lane where tokens abound (fewer lanes share a row's fixed work: 4096 tokens
+  // x 8 heads x 128 written and read back, 28.8 -> 25.3 us), one for a step's few (more
+  // loads at once)
   const int nchunk = p.D / 8;
+  const int cpl = nchunk > 64 ? 4 : nchunk > 32 || (nchunk > 1 && (long long)p.B * p.n >= 8LL * sms) ? 2 : 1;
   p.lanes = 1;
-  while (p.lanes < nchunk && p.lanes < 32) p.lanes *= 2;
+  while (p.lanes * cpl < nchunk && p.lanes < 32) p.lanes *= 2;
   const int rows = p.Hkv * (p.v ? 2 : 1), np = p.r.inv_freq ? p.r.rot / 2 : 0;
-  // enough tokens that every lane has a row, as long as their cosines fit
+  // enough tokens that every lane has a row, four rounds of them where tokens abound (the
+  // cosines then take every thread), as long as the cosines fit
+  const long long total = (long long)p.B * p.n;
   p.tb = kThreads / (rows * p.lanes);
-  const int room = np ? kRopeSmem / (8 * np) - 1 : 16;
-  p.tb = p.tb > 16 ? 16 : p.tb;
-  p.tb = p.tb > room ? room : p.tb;
   p.tb = p.tb < 1 ? 1 : p.tb;
-  const long long blocks = ((long long)p.B * p.n + p.tb - 1) / p.tb, cap = 8LL * sms;
+  while (p.tb < 4 && total >= 12LL * sms * p.tb) p.tb *= 2;
+  const int room = np ? kRopeSmem / (8 * np) - 1 : kMaxTokens;
+  p.tb = p.tb > kMaxTokens ? kMaxTokens : p.tb;
+  p.tb = p.tb > room ? room : p.tb;
+  const long long blocks = (total + p.tb - 1) / p.tb, cap = 8LL * sms;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const size_t smem = (size_t)np * 8 * (1 + p.tb);
-  if (nchunk <= 32)
+  if (cpl == 1)
     kv_write_kernel<PAGED, INT8, 1><<<grid, kThreads, smem, st>>>(p);
+  else if (cpl == 2)
+    kv_write_kernel<PAGED, INT8, 2><<<grid, kThreads, smem, st>>>(p);
   else
     kv_write_kernel<PAGED, INT8, 4><<<grid, kThreads, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
@@ -551,10 +573,15 @@ int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t
   if (p.B == 0 || p.n == 0) return DA_OK;
   if (!p.k_out || !aligned(p.k_out, 16) || !p.v_out != !p.v || !aligned(p.v_out, 16)) return DA_ERR_INVALID_ARG;
   if (int e = check_cache_pointers(p, paged, int8)) return e;
-  // about 8 loads of 16 bytes a thread
+  int dev, sms, optin;
+  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
+  // about 4 loads of 16 bytes a thread and tensor, fewer while that leaves SMs without their
+  // 2048 threads (4096 tokens x 8 heads x 128 from int8: 11 us at 4, 256 CTAs)
   const int per_row = p.Hkv * p.D / (int8 ? 16 : 8);
-  const int tb = kThreads * 4 / per_row;
-  p.tb = tb < 1 ? 1 : tb > 64 ? 64 : tb;
+  int tb = kThreads * 4 / per_row;
+  tb = tb < 1 ? 1 : tb > 64 ? 64 : tb;
+  while (tb > 1 && tb * per_row > kThreads && (long long)p.B * ((p.n + tb - 1) / tb) < 8LL * sms) tb = (tb + 1) / 2;
+  p.tb = tb;
   const long long grid = (long long)p.B * ((p.n + p.tb - 1) / p.tb);
   if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   if (paged && int8)
@@ -609,7 +636,7 @@ extern "C" int rope_apply(const void* x, void* out, const int* positions, const 
   if (tokens < 0 || num_heads <= 0 || head_dim <= 0) return DA_ERR_INVALID_ARG;
   if (dtype < DA_BF16 || dtype > DA_F32) return DA_ERR_UNSUPPORTED;
   if (int e = rope_check(inv_freq, head_dim, rot_offset, rot_dim, interleaved, magnitude)) return e;
-  if ((long long)num_heads * head_dim > 0x3fffffffLL) return DA_ERR_UNSUPPORTED;
+  if ((long long)num_heads * head_dim > 0x1fffffffLL) return DA_ERR_UNSUPPORTED;
   if (tokens == 0) return DA_OK;
   const int size = dtype == DA_F32 ? 4 : 2;
   if (!x || !out || !positions || !aligned(x, size) || !aligned(out, size) || !aligned(positions, 4))

@@ -258,6 +258,23 @@ def test_write_rotates_keys(int8, interleaved, D, rot, offset):
 
 
 @pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("H,D,rot,offset,interleaved", [
+    (2, 128, 128, 0, False),   # a pair's halves in one lane's two chunks
+    (2, 128, 128, 0, True), (2, 128, 64, 64, False), (1, 64, 64, 0, False), (3, 96, 96, 0, False), (1, 512, 512, 0, False),
+    (1, 320, 64, 256, False), (4, 16, 16, 0, False)])
+def test_write_many_tokens(int8, H, D, rot, offset, interleaved):
+    """Enough tokens that a CTA takes several and a lane two chunks."""
+    lens = [700, 650, 20, 900]
+    c = write_case(D + H, len(lens), 640, H, D, lens, 912, 16, int8)
+    w = freqs(rot)
+    got, scales = run_write(c, w, offset=offset, interleaved=interleaved)
+    check_write(c, got, scales, w, offset, interleaved)
+    got, scales = run_write(c)
+    check_write(c, got, scales)
+    assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("int8", [False, True])
 def test_write_keys_only(int8):
     c = write_case(3, 3, 4, 1, 576, [4, 30, 64], 64, 16, int8, keys_only=True)
     got, scales = run_write(c)
