@@ -119,12 +119,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "kv_read_int8_paged": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
         "latent_attn_contig": [vp, vp, vp, i, i, i, i, i, f, vp, ll, vp, vp],
         "latent_attn_paged": [vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, ll, vp, vp],
-        "latent_prefill_contig": [vp, vp, vp, vp, vp, i, i, i, i, i, ll, ll, ll, f, vp, vp],
+        "latent_prefill_contig": [vp, vp, vp, vp, vp, i, i, i, i, i, ll, ll, ll, f, vp, ll, vp, vp],
+        "latent_prefill_workspace_bytes": [i, i, i, i, i, i],
         "latent_workspace_bytes": [i, i, i, i, i],
         "latent_max_batch": [i, i, i],
     }.items():
         getattr(lib, name).argtypes = args
-        getattr(lib, name).restype = ll if name == "latent_workspace_bytes" else i
+        getattr(lib, name).restype = ll if name.endswith("_bytes") else i
     if path is None:
         _lib = lib
     return lib

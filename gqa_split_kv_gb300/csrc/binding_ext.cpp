@@ -59,6 +59,7 @@ struct Library {
   decltype(&::latent_attn_paged) latent_attn_paged = nullptr;
   decltype(&::latent_workspace_bytes) latent_workspace_bytes = nullptr;
   decltype(&::latent_prefill_contig) latent_prefill_contig = nullptr;
+  decltype(&::latent_prefill_workspace_bytes) latent_prefill_workspace_bytes = nullptr;
 };
 Library g_lib;
 PyObject* g_error = nullptr;  // DecodeAttnError
@@ -499,10 +500,14 @@ PyObject* latent_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     on_current(dev);
     Stream st(a[7], dev);
     const Tensor out = given ? *given : at::empty(dims(B, n, H, D), q.options());
+    Tensor work;
+    const long long bytes = g_lib.latent_prefill_workspace_bytes(B, n, H, (int)D, small(ctx, "k_nope"), 0);
+    if (bytes < 0) throw Failed{"latent_prefill_contig", (int)-bytes};
+    if (bytes > 0) work = at::empty(dims(bytes), q.options().dtype(at::kByte));
     call("latent_prefill_contig", [&] {
       return g_lib.latent_prefill_contig(ptr(q), ptr(k), ptr(pe), ptr(v), ptr<int>(lens), B, n, H, (int)D,
-                                         small(ctx, "k_nope"), kst.first, kst.second, pst.first, scale, ptr(out),
-                                         st.raw);
+                                         small(ctx, "k_nope"), kst.first, kst.second, pst.first, scale,
+                                         bytes > 0 ? ptr(work) : nullptr, bytes, ptr(out), st.raw);
     });
     return given ? same(a[6]) : THPVariable_Wrap(out);
   });
@@ -542,6 +547,7 @@ PyObject* open(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   FIND(latent_attn_paged)
   FIND(latent_workspace_bytes)
   FIND(latent_prefill_contig)
+  FIND(latent_prefill_workspace_bytes)
 #undef FIND
   g_lib = l;
   Py_INCREF(a[1]);

@@ -189,6 +189,25 @@ int latent_call(bool paged, const void* q, const void* cache, const int* page_ta
   }
 }
 
+// How a prefill's keys are cut: where all CTAs of two parts a block still run at once, into
+// as many parts as do, of 4 key tiles at least.  A second round of parts costs what the
+// cut saves: 128 blocks of up to 21 tiles (4 sequences, 16 heads, 500 new tokens) take
+// 51.2 us whole and 47 to 54 us in parts of 11 to 8, by the sequences' order.
+void prefill_parts(long long units, int max_ctx, int sms, int* parts, int* part_tiles) {
+  const long long tiles = ((long long)max_ctx + 127) / 128;
+  long long n = units > 0 ? sms / units : 1;
+  n = n > (tiles + 3) / 4 ? (tiles + 3) / 4 : n;
+  n = n < 1 ? 1 : n;
+  *parts = (int)n;
+  *part_tiles = n == 1 ? 0x7fffffff / 256 : (int)((tiles + n - 1) / n);
+}
+
+long long prefill_workspace(long long units, int max_ctx, int D, int sms) {
+  int parts, part_tiles;
+  prefill_parts(units, max_ctx, sms, &parts, &part_tiles);
+  return parts == 1 ? 0 : units * parts * LatentPrefillGeo<128>::BQ * (D + 2) * 4;
+}
+
 template <int D>
 int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k, const void* k_rope, const void* v,
                           long long token_stride, long long head_stride, long long rope_stride, int dev,
@@ -227,18 +246,35 @@ int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k
   if (int e = encode_map_t(&prm.tm_v, bf16, sw, v, 5, dims, strides, box_v)) return e;
   if (int e = encode_map_t(&prm.tm_pe, bf16, sw, k_rope, 3, dims_pe, strides_pe, box_pe)) return e;
   {
-    // launch groups of (b, h) units whose K/V fit in about 48 MB of L2 together
+    // launch groups of (b, h) units whose K/V fit in about 96 MB of L2 together: the longest
+    // query blocks of a group start first, so a second group's would start last (32 heads x
+    // 4096 tokens: 160 us in groups of 24, 142 in one)
     const long long unit_bytes = 4LL * D * prm.max_len, units = (long long)prm.B * prm.H;
-    long long g = (48LL << 20) / unit_bytes;
+    long long g = (96LL << 20) / unit_bytes;
     g = g < 1 ? 1 : g;
     prm.grp = (int)(g < units ? g : units);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)prm.nqb * prm.B * prm.H));
+  const long long units = (long long)prm.nqb * prm.B * prm.H;
+  if (units * prm.parts > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  cfg.gridDim = dim3((unsigned)(units * prm.parts));
   cfg.blockDim = dim3(Gm::NTHREADS);
   cfg.dynamicSmemBytes = (size_t)Gm::SMEM;
   cfg.stream = st;
   if (cudaLaunchKernelEx(&cfg, latent_prefill_kernel<D>, prm) != cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_CUDA;
+  }
+  if (prm.parts == 1) return DA_OK;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(units * (Gm::BQ / 32)));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, latent_prefill_merge<D>, prm) != cudaSuccess) {
     cudaGetLastError();
     return DA_ERR_CUDA;
   }
@@ -289,11 +325,13 @@ extern "C" int latent_attn_paged(const void* q, const void* pool, const int* pag
 extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const void* k_rope, const void* v,
                                      const int* seq_lens, int batch, int q_len, int num_heads, int head_dim,
                                      int max_ctx, long long kv_token_stride, long long kv_head_stride,
-                                     long long rope_token_stride, float scale, void* out, void* stream) {
+                                     long long rope_token_stride, float scale, void* workspace,
+                                     long long workspace_bytes, void* out, void* stream) {
   if (batch < 0 || q_len < 0 || num_heads < 1 || max_ctx < 0 || !std::isfinite(scale)) return DA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return DA_ERR_UNSUPPORTED;
   if (batch == 0 || q_len == 0) return DA_OK;
-  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4)) return DA_ERR_INVALID_ARG;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(workspace, 16))
+    return DA_ERR_INVALID_ARG;
   const int BQ = LatentPrefillGeo<128>::BQ;
   const long long nqb = ((long long)q_len + BQ - 1) / BQ;
   if (nqb * batch > 0x7fffffffLL / num_heads) return DA_ERR_UNSUPPORTED;
@@ -323,8 +361,29 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
   prm.max_len = max_ctx;
   prm.scale_log2 = scale * kLog2e;
   prm.timeout_ns = kWaitTimeoutNs;
+  const long long units = nqb * batch * num_heads;
+  prm.parts = 1;
+  prm.part_tiles = 0x7fffffff / 256;
+  if (workspace) {
+    if (workspace_bytes < prefill_workspace(units, max_ctx, head_dim, sms)) return DA_ERR_WORKSPACE;
+    prefill_parts(units, max_ctx, sms, &prm.parts, &prm.part_tiles);
+    prm.part_acc = static_cast<float*>(workspace);
+    prm.part_ml = reinterpret_cast<float2*>(prm.part_acc + units * prm.parts * BQ * head_dim);
+  }
   return head_dim == 64 ? launch_latent_prefill<64>(prm, q, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
                                                     rope_token_stride, dev, st)
                         : launch_latent_prefill<128>(prm, q, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
                                                      rope_token_stride, dev, st);
+}
+
+extern "C" long long latent_prefill_workspace_bytes(int batch, int q_len, int num_heads, int head_dim, int max_ctx,
+                                                    int num_sms) {
+  if (batch < 0 || q_len < 0 || num_heads < 1 || max_ctx < 0) return -DA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return -DA_ERR_UNSUPPORTED;
+  int dev, sms = num_sms, optin;
+  if (sms <= 0 && (current_device(&dev) || device_info(dev, &sms, &optin))) return -DA_ERR_CUDA;
+  const int BQ = LatentPrefillGeo<128>::BQ;
+  const long long nqb = ((long long)q_len + BQ - 1) / BQ;
+  if (nqb * batch > 0x7fffffffLL / num_heads) return -DA_ERR_UNSUPPORTED;
+  return prefill_workspace(nqb * batch * num_heads, max_ctx, head_dim, sms);
 }

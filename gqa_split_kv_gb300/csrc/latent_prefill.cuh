@@ -20,6 +20,14 @@
 // P_B V_j frees two that K_{j+2} takes, 1290 cycles of products before it is used.  A ring
 // of whole tiles would hold one and a half of 128 keys, and tiles of 64 keys take 48
 // instead of 32 cycles an MMA.
+//
+// A few query blocks (a chunk after a long prefix, few heads) leave most SMs idle.  Then a
+// block's key tiles are cut into up to `parts` equal parts of at most `part_tiles`, each a
+// CTA's, which leaves (O, m, l) unnormalised in fp32; latent_prefill_merge joins them.  A
+// block of one part is written at once.
+//
+// Measured: a 4096-token prompt, 32 heads, D = 128: a tile of both query tiles takes 1.9
+// us, 1.7 of them 40 MMAs at the clock that the card holds under them (1.5 GHz).
 #pragma once
 
 #include <cstdint>
@@ -37,6 +45,9 @@ struct LatentPrefillParams {
   CUtensorMap tm_pe;  // [B][tokens][64], boxes of 128 tokens
   __nv_bfloat16* out;      // [B, q_len, H, D]
   const int* seq_lens;     // [B] or null (every sequence max_len tokens)
+  float* part_acc;         // [unit][part][D][256]: parts' O (with more than one part)
+  float2* part_ml;         // [unit][part][256], m in log2 units
+  int parts, part_tiles;   // parts a unit's keys may have, key tiles a part
   int B, q_len, H, nqb;
   int grp;                 // (sequence, head) units per launch group (their K/V fit in L2 together)
   int max_len;
@@ -98,12 +109,14 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float kNegInf = -__int_as_float(0x7f800000);
 
-  // work unit: groups of grp (b, h) units, latest query blocks first
+  // work unit: groups of grp (b, h) units, latest query blocks (the longest) first; a unit's
+  // parts together
   const int nbh = p.B * p.H;
+  const int part = blockIdx.x % p.parts, unit = blockIdx.x / p.parts;
   const long long per_grp = (long long)p.nqb * p.grp;
-  const int gi = (int)(blockIdx.x / per_grp);
+  const int gi = (int)(unit / per_grp);
   const int gsz = min(p.grp, nbh - gi * p.grp);
-  const int in_g = (int)(blockIdx.x - gi * per_grp);
+  const int in_g = (int)(unit - gi * per_grp);
   const int qb = p.nqb - 1 - in_g / gsz;
   const int bh = gi * p.grp + in_g % gsz;
   const int b = bh / p.H, h = bh % p.H;
@@ -114,7 +127,13 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
   const int nqt = nq > M ? 2 : 1;                     // query tiles with rows
   const int base = L - p.q_len;                       // position of query token 0
   const int kv_end = max(0, min(L, base + q0 + nq));  // keys some row sees
-  const int ntiles = (kv_end + BK - 1) / BK;
+  const int all_tiles = (kv_end + BK - 1) / BK;
+  // equal parts of at most part_tiles; this one's tiles
+  const int nparts = max(1, (all_tiles + p.part_tiles - 1) / p.part_tiles);
+  if (part >= nparts) return;
+  const int j0 = (int)((long long)all_tiles * part / nparts);
+  const int ntiles = (int)((long long)all_tiles * (part + 1) / nparts) - j0;
+  const bool whole = nparts == 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Gm::NG; ++i) {
@@ -164,7 +183,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           tma_load_5d(sbase + Gm::OFF_Q + t * Gm::QT_BYTES, &p.tm_q, bar(Gm::BAR_Q + t), 0, q0 + t * M, 0, h, b);
         }
         for (int j = 0; j < ntiles && ok; ++j) {
-          const int t = j * BK;
+          const int t = (j0 + j) * BK;
 #pragma unroll 1
           for (int g = 0; g < Gm::PER; ++g) {
             const int fill = fill_of(j, g), slot = slot_of(j, g);
@@ -229,7 +248,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       // V rows at or past kv_end may hold anything (0 * NaN would poison O): zero them
       auto zero_tail = [&](int j) {
         for (int g = 0; g < Gm::NVG; ++g) {
-          const int r0 = max(0, kv_end - (j * BK + g * Gm::VKEYS));
+          const int r0 = max(0, kv_end - ((j0 + j) * BK + g * Gm::VKEYS));
           uint8_t* vs = smem + Gm::OFF_G + slot_of(j, Gm::NKG + g) * Gm::G;
           for (int e = r0 * 8 + lane; e < Gm::VKEYS * 8; e += 32)
             for (int c = 0; c < D / 64; ++c)
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         // A: P_A V_j, then S_A of tile j + 1 once its keys are there
         ok = landed(j, Gm::NKG, Gm::PER);
         if (!ok) break;
-        if (!more) zero_tail(j);
+        if ((j0 + j + 1) * BK > kv_end) zero_tail(j);
         if (!(ok = wait_all(Gm::BAR_P, j))) break;
         if (elect_one()) {
           tc_fence_after();
@@ -326,30 +345,37 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           for (int c0 = 0; c0 < BK; c0 += 32) tmem_ld32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(r + c0));
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < BK; ++i) x[i] = fold ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * p.scale_log2;
+          for (int i = 0; i < BK; ++i) x[i] = __uint_as_float(r[i]);
         }
-        if (j * BK + BK > lim_first) {
+        if (!fold) {
 #pragma unroll
-          for (int i = 0; i < BK; ++i) x[i] = j * BK + i < lim ? x[i] : kNegInf;
+          for (int i = 0; i < BK; ++i) x[i] *= p.scale_log2;
+        }
+        if ((j0 + j + 1) * BK > lim_first) {
+          const int left = lim - (j0 + j) * BK;  // keys of this tile that the row sees
+#pragma unroll
+          for (int i = 0; i < BK; ++i) x[i] = i < left ? x[i] : kNegInf;
         }
         // P = exp2(x sc - mu) as bf16 pairs over the first half of the S buffer; the sum of the weights
         auto weights = [&](float mu) {
-          float sk[8];
+          float2 sk[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sk[k] = 0.f;
+          for (int k = 0; k < 4; ++k) sk[k] = make_float2(0.f, 0.f);
+          const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
 #pragma unroll
           for (int c0 = 0; c0 < BK / 2; c0 += 32) {
             uint32_t pk[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float e0 = exp2_approx(fmaf(x[2 * (c0 + i)], sc, -mu));
-              const float e1 = exp2_approx(fmaf(x[2 * (c0 + i) + 1], sc, -mu));
-              sk[i & 7] += e0 + e1;
-              pk[i] = pack_bf16x2(e0, e1);
+              const float2 y = fma_f32x2(make_float2(x[2 * (c0 + i)], x[2 * (c0 + i) + 1]), sc2, mu2);
+              const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              sk[i & 3] = add_f32x2(sk[i & 3], e);
+              pk[i] = pack_bf16x2(e.x, e.y);
             }
             tmem_st32(s_addr + c0, pk);
           }
-          return ((sk[0] + sk[1]) + (sk[2] + sk[3])) + ((sk[4] + sk[5]) + (sk[6] + sk[7]));
+          const float2 t = add_f32x2(add_f32x2(sk[0], sk[1]), add_f32x2(sk[2], sk[3]));
+          return t.x + t.y;
         };
         // The weights are first taken against the current m; only a row that has seen no key
         // yet, or whose weights sum past 2^14, takes its maximum and raises m to it.  The
@@ -396,10 +422,24 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       if (ok && ntiles > 0) ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + qt, 0));
       if (ok) {
         tc_fence_after();
+        if (!whole) {
+          // the part as it is, [D][256]: 32 lanes store 32 rows of a column
+          const size_t slot = ((size_t)bh * p.nqb + qb) * p.parts + part;
+          float* acc = p.part_acc + slot * D * Gm::BQ + tok;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32(o_addr + c0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[(size_t)(c0 + i) * Gm::BQ] = __uint_as_float(r[i]);
+          }
+          p.part_ml[slot * Gm::BQ + tok] = make_float2(m, l);
+        }
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         __nv_bfloat16* dst = p.out + (((size_t)b * p.q_len + q0 + tok) * p.H + h) * D;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = 0; c0 < D && whole; c0 += 32) {
           uint32_t r[32];
           if (ntiles > 0) {
             tmem_ld32(o_addr + c0, r);
@@ -427,6 +467,55 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, Gm::TMEM_COLS);
   }
+}
+
+// Joins the parts of the blocks that have more than one: out = sum_j w_j O_j / sum_j w_j
+// l_j, w_j = 2^(m_j - max m), in ascending j.  A CTA takes 32 rows of a block, a warp D /
+// 8 columns of them, a lane a row.
+template <int D>
+__global__ void __launch_bounds__(256) latent_prefill_merge(const LatentPrefillParams p) {
+  using Gm = LatentPrefillGeo<D>;
+  constexpr int C = D / 8;  // columns a warp
+  const int unit = blockIdx.x / (Gm::BQ / 32), row = (blockIdx.x % (Gm::BQ / 32)) * 32 + (threadIdx.x & 31);
+  const int bh = unit / p.nqb, qb = unit - bh * p.nqb, b = bh / p.H, h = bh - b * p.H;
+  int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len;
+  L = L < 0 ? 0 : (L > p.max_len ? p.max_len : L);
+  const int q0 = qb * Gm::BQ, nq = min(Gm::BQ, p.q_len - q0);
+  const int kv_end = max(0, min(L, L - p.q_len + q0 + nq));
+  const int n = ((kv_end + Gm::BK - 1) / Gm::BK + p.part_tiles - 1) / p.part_tiles;
+  pdl_wait_primary();
+  if (n <= 1 || row >= nq) return;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  const size_t slot0 = (size_t)unit * p.parts;
+  float M = kNegInf;
+  for (int j = 0; j < n; ++j) {
+    const float2 ml = __ldcg(p.part_ml + (slot0 + j) * Gm::BQ + row);
+    if (ml.y > 0.f || ml.y != ml.y) M = fmaxf(M, ml.x);
+  }
+  float s[C], den = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) s[c] = 0.f;
+  const int c0 = (threadIdx.x >> 5) * C;
+  for (int j = 0; j < n; ++j) {
+    const float* acc = p.part_acc + ((slot0 + j) * D + c0) * Gm::BQ + row;
+    float a[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) a[c] = __ldcg(acc + c * Gm::BQ);
+    const float2 ml = __ldcg(p.part_ml + (slot0 + j) * Gm::BQ + row);
+    const float w = ml.y > 0.f || ml.y != ml.y ? exp2_approx(ml.x - M) : 0.f;
+    if (w != 0.f) {
+      den += w * ml.y;
+#pragma unroll
+      for (int c = 0; c < C; ++c) s[c] += w * a[c];
+    }
+  }
+  const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
+  uint4* o = reinterpret_cast<uint4*>(p.out + (((size_t)b * p.q_len + q0 + row) * p.H + h) * D + c0);
+#pragma unroll
+  for (int k = 0; k < C / 8; ++k)
+    o[k] = make_uint4(pack_bf16x2(s[8 * k] * inv, s[8 * k + 1] * inv), pack_bf16x2(s[8 * k + 2] * inv, s[8 * k + 3] * inv),
+                      pack_bf16x2(s[8 * k + 4] * inv, s[8 * k + 5] * inv),
+                      pack_bf16x2(s[8 * k + 6] * inv, s[8 * k + 7] * inv));
 }
 
 }  // namespace da

@@ -505,13 +505,23 @@ int latent_max_batch(int q_len, int num_heads, int latent_dim);
  *             of 8): the last 64 columns of a latent cache will do
  *  out        bf16 [batch, q_len, num_heads, head_dim]
  *  head_dim   64 or 128; seq_lens int32 [batch] clamped to [0, max_ctx], or NULL (max_ctx).
+ *  workspace  NULL, or latent_prefill_workspace_bytes(...) bytes, 16-byte aligned, of any content:
+ *             with it, the keys of few query blocks are split over CTAs and joined in fp32.  Calls
+ *             that share it must not overlap on the GPU (two captured graphs included).
  * Keys and values at positions below L_b are finite; what lies past them is never used.
- * Numerics as for prefill_attn_*; no workspace.
+ * Numerics as for prefill_attn_*.  DA_ERR_WORKSPACE: a workspace that is too small.
  */
 int latent_prefill_contig(const void* q, const void* k_nope, const void* k_rope, const void* v, const int* seq_lens,
                           int batch, int q_len, int num_heads, int head_dim, int max_ctx,
                           long long kv_token_stride, long long kv_head_stride, long long rope_token_stride,
-                          float scale, void* out, void* stream);
+                          float scale, void* workspace, long long workspace_bytes, void* out, void* stream);
+
+/*
+ * latent_prefill_workspace_bytes — the workspace with which latent_prefill_contig splits
+ * keys on a device of num_sms SMs (<= 0: the current device); 0 where it would not (host
+ * only, pure).  Negative da_status for shapes outside those above.
+ */
+long long latent_prefill_workspace_bytes(int batch, int q_len, int num_heads, int head_dim, int max_ctx, int num_sms);
 
 /* Human-readable name of a da_status value (static string). */
 const char* decode_status_string(int status);

@@ -83,6 +83,19 @@ def test_long_context_and_lengths(D):
     assert np.array_equal(run(c, lens_null=True), run(c))
 
 
+@pytest.mark.parametrize("D,H,q_len", [(128, 2, 200), (64, 3, 1), (128, 1, 600)])
+def test_keys_split_over_parts(D, H, q_len):
+    """Few blocks over many key tiles: parts that end within a block's causal border, sequences of one part beside
+    sequences of many, empty ones, rows that see nothing of a part."""
+    ctx = 2600
+    lens = [2600, 511, 513, 0, 1, 2049, q_len // 2 + 1]
+    assert binding.load().latent_prefill_workspace_bytes(len(lens), q_len, H, D, ctx, 0) > 0
+    c = make(D + q_len, lens, q_len, H, D, ctx)
+    first = run(c)
+    check(first, c, "parts")
+    assert np.array_equal(run(c), first)
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 0.6])
 def test_any_scale(scale):
     c = make(9, [400, 200], 200, 2, 128, 400)

@@ -97,19 +97,33 @@ def test_workspace_and_batch_queries(clib):
     assert clib.latent_max_batch(0, 1, 128) == -1
 
 
-def prefill(clib, q=A, k=A, pe=A, v=A, lens=A, B=2, n=4, H=4, D=128, ctx=64, ts=512, hs=128, ps=64, scale=0.1, out=A):
-    return clib.latent_prefill_contig(q, k, pe, v, lens, B, n, H, D, ctx, ts, hs, ps, ctypes.c_float(scale), out, None)
+def prefill(clib, q=A, k=A, pe=A, v=A, lens=A, B=2, n=4, H=4, D=128, ctx=64, ts=512, hs=128, ps=64, scale=0.1, out=A,
+            ws=None, size=0):
+    return clib.latent_prefill_contig(q, k, pe, v, lens, B, n, H, D, ctx, ts, hs, ps, ctypes.c_float(scale), ws, size, out,
+                                      None)
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), 1), (dict(n=-1), 1), (dict(H=0), 1), (dict(D=96), 2), (dict(D=256), 2), (dict(ctx=-1), 1),
     (dict(scale=float("nan")), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(pe=None), 1), (dict(v=None), 1),
     (dict(out=None), 1), (dict(q=A + 8), 1), (dict(k=A + 8), 1), (dict(pe=A + 4), 1), (dict(v=A + 2), 1),
-    (dict(out=A + 8), 1), (dict(lens=A + 1), 1), (dict(hs=64), 1), (dict(hs=132, ts=1024), 1), (dict(ts=500), 1),
+    (dict(out=A + 8), 1), (dict(lens=A + 1), 1), (dict(ws=A + 8), 1), (dict(hs=64), 1), (dict(hs=132, ts=1024), 1), (dict(ts=500), 1),
     (dict(ts=516), 1), (dict(ps=32), 1), (dict(ps=68), 1), (dict(B=1 << 20, n=1 << 20), 2), (dict(B=0), 0), (dict(n=0), 0),
 ])
 def test_prefill_refusals(clib, kw, want):
     assert prefill(clib, **kw) == want
+
+
+def test_prefill_workspace(clib):
+    size = clib.latent_prefill_workspace_bytes
+    assert size(1, 4096, 64, 128, 4096, 152) == 0          # 1024 blocks fill the card
+    assert size(4, 500, 16, 128, 3000, 152) == 0           # 128 blocks: two parts each would not run at once
+    assert size(1, 256, 16, 128, 512, 152) == 0            # 4 tiles are one part
+    # 32 blocks: 4 parts each run at once, of 24 tiles
+    assert size(4, 200, 8, 128, 3000, 152) == 32 * 4 * 256 * (128 + 2) * 4
+    assert size(1, 1, 1, 64, 100000, 152) == 152 * 256 * (64 + 2) * 4  # one block: the whole card
+    assert size(1, 1, 1, 64, 1000, 152) == 2 * 256 * (64 + 2) * 4      # 8 tiles: two parts of 4
+    assert size(0, 5, 4, 128, 3000, 152) == 0 and size(1, 5, 4, 96, 3000, 152) == -2 and size(-1, 5, 4, 64, 1, 152) == -1
 
 
 def test_binding_refuses_mismatched_tensors():
