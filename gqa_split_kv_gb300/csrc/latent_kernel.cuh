@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
     mbar_init(bar(Gm::B_QEMPTY), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Gm::B_S + i), 1);
-      mbar_init(bar(Gm::B_P + i), 128 * Gm::NWG);
+      mbar_init(bar(Gm::B_P + i), 4 * Gm::NWG);  // one arrival a warp
       mbar_init(bar(Gm::B_PV + i), 1);
       mbar_init(bar(Gm::B_FIN + i), 1);
     }
-    mbar_init(bar(Gm::B_OFREE), 128 * Gm::NWG);
+    mbar_init(bar(Gm::B_OFREE), 4 * Gm::NWG);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tm_q);
@@ -561,7 +561,8 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(Gm::B_P + sb));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Gm::B_P + sb));
       }
       if (stop) break;
       // ---- the piece's sums: over 8 lanes, then over the warps in order
@@ -620,7 +621,8 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
         }
       }
       tc_fence_before();
-      mbar_arrive(bar(Gm::B_OFREE));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Gm::B_OFREE));
       ++piece;
     }
   }

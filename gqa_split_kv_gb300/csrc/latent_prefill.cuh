@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Gm::BAR_S + i), 1);
-      mbar_init(bar(Gm::BAR_P + i), 128);
+      mbar_init(bar(Gm::BAR_P + i), 4);  // one arrival a warp
       mbar_init(bar(Gm::BAR_O + i), 1);
       mbar_init(bar(Gm::BAR_Q + i), 1);
     }
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         l = l * alpha + sum;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar(Gm::BAR_P + qt));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Gm::BAR_P + qt));
       }
       // ---- normalise and write the tile's rows (a row that saw nothing: zeros)
       if (ok && ntiles > 0) ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + qt, 0));
