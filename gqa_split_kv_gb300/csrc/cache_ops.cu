@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p)
   const int np = p.r.rot / 2;
   unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
   float2* cs = reinterpret_cast<float2*>(step + (np + 1) / 2 * 2);  // 16-byte aligned
+  pdl_launch_dependents();
+  pdl_wait_primary();
   for (int j = threadIdx.x; j < np; j += kThreads) step[j] = rope_turn_step(p.r.inv_freq[j]);
   constexpr int V = VECTOR ? 16 / (int)sizeof(T) : 1;
   constexpr int U = 2;  // items a thread has in flight
@@ -244,11 +246,8 @@ int launch_rope(const RopeApplyParams& p, int sms, cudaStream_t st) {
   const size_t smem = (size_t)(p.r.rot / 2 + 1) * 16;
   const long long cap = 8LL * sms;  // 2048 threads an SM
   const unsigned grid = (unsigned)(p.tokens < cap ? p.tokens : cap);
-  if (vec)
-    rope_kernel<T, true><<<grid, kThreads, smem, st>>>(p);
-  else
-    rope_kernel<T, false><<<grid, kThreads, smem, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return vec ? launch_dependent(rope_kernel<T, true>, grid, kThreads, smem, st, p)
+             : launch_dependent(rope_kernel<T, false>, grid, kThreads, smem, st, p);
 }
 
 int rope_check(const double* inv_freq, int head_dim, int offset, int rot, int interleaved, float magnitude) {
@@ -331,6 +330,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
     const int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
     return (long long)L - p.n + (int)(g - (unsigned)b * (unsigned)p.n);
   };
+  pdl_launch_dependents();
+  pdl_wait_primary();
   bool first = true;
   // every lane of a warp runs the same number of rounds (the shuffles need them all)
   const int per_round = kThreads / p.lanes;
@@ -462,6 +463,8 @@ template <bool PAGED, bool INT8>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) {
   const int nblk = (p.n + p.tb - 1) / p.tb;
   const int b = blockIdx.x / nblk, i0 = (blockIdx.x - b * nblk) * p.tb;
+  pdl_launch_dependents();
+  pdl_wait_primary();
   int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
   L = min(L, p.cap);
   const int start = p.starts ? __ldg(p.starts + b) : 0;
@@ -539,13 +542,9 @@ int launch_write(CacheParams& p, int sms, cudaStream_t st) {
   const long long blocks = (total + p.tb - 1) / p.tb, cap = 8LL * sms;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const size_t smem = (size_t)np * 8 * (1 + p.tb);
-  if (cpl == 1)
-    kv_write_kernel<PAGED, INT8, 1><<<grid, kThreads, smem, st>>>(p);
-  else if (cpl == 2)
-    kv_write_kernel<PAGED, INT8, 2><<<grid, kThreads, smem, st>>>(p);
-  else
-    kv_write_kernel<PAGED, INT8, 4><<<grid, kThreads, smem, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  if (cpl == 1) return launch_dependent(kv_write_kernel<PAGED, INT8, 1>, grid, kThreads, smem, st, p);
+  if (cpl == 2) return launch_dependent(kv_write_kernel<PAGED, INT8, 2>, grid, kThreads, smem, st, p);
+  return launch_dependent(kv_write_kernel<PAGED, INT8, 4>, grid, kThreads, smem, st, p);
 }
 
 int write_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t st) {
@@ -584,13 +583,9 @@ int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t
   p.tb = tb;
   const long long grid = (long long)p.B * ((p.n + p.tb - 1) / p.tb);
   if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
-  if (paged && int8)
-    kv_read_kernel<true, true><<<(unsigned)grid, kThreads, 0, st>>>(p);
-  else if (paged)
-    kv_read_kernel<true, false><<<(unsigned)grid, kThreads, 0, st>>>(p);
-  else
-    kv_read_kernel<false, true><<<(unsigned)grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  if (paged && int8) return launch_dependent(kv_read_kernel<true, true>, (unsigned)grid, kThreads, 0, st, p);
+  if (paged) return launch_dependent(kv_read_kernel<true, false>, (unsigned)grid, kThreads, 0, st, p);
+  return launch_dependent(kv_read_kernel<false, true>, (unsigned)grid, kThreads, 0, st, p);
 }
 
 long long paged_cap(int page_size, int max_pages, int max_seq_len) {

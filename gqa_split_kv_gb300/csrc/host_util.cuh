@@ -77,5 +77,27 @@ int encode_map_t(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle sw
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Launches kern as a programmatic dependent of what precedes it in the stream: its CTAs may
+// start while that drains, so every kernel launched here waits for it (griddepcontrol.wait)
+// before it touches memory.
+template <typename P>
+int launch_dependent(void (*kern)(P), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const P& prm) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, prm) != cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_CUDA;
+  }
+  return DA_OK;
+}
+
 }  // namespace
 }  // namespace da

@@ -52,31 +52,14 @@ int launch_latent(const LatentParams& prm, int sms, int dev, cudaStream_t st) {
   // one CTA a range, and no more ranges than the line has units
   const long long units =
       ((long long)prm.B * prm.U * ((prm.max_len + kBlockTokens - 1) / kBlockTokens + 3 + kLatentGap)) / kRangeQuantum + 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(prm.ranges < units ? prm.ranges : units));
-  cfg.blockDim = dim3(Gm::NTHREADS);
-  cfg.dynamicSmemBytes = (size_t)Gm::SMEM;
-  cfg.stream = st;
-  if (cudaLaunchKernelEx(&cfg, latent_kernel<R, N, PAGED>, prm) != cudaSuccess) {
-    cudaGetLastError();
-    return DA_ERR_CUDA;
-  }
+  if (int e = launch_dependent(latent_kernel<R, N, PAGED>, (unsigned)(prm.ranges < units ? prm.ranges : units),
+                               Gm::NTHREADS, (size_t)Gm::SMEM, st, prm))
+    return e;
   const LatentCombineParams c = {prm.part_acc, prm.part_ml, prm.out, prm.seq_lens, prm.B,
                                  prm.rows,     prm.U,       N,       prm.ranges,   prm.max_len};
   // items go a warp at a time, those of long runs a CTA at a time
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
-  cfg.blockDim = dim3(LatentCombineGeo::NTHREADS);
-  cfg.dynamicSmemBytes = (size_t)LatentCombineGeo::smem_bytes(prm.ranges, prm.B);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, latent_combine_kernel<R>, c) != cudaSuccess) {
-    cudaGetLastError();
-    return DA_ERR_CUDA;
-  }
-  return DA_OK;
+  return launch_dependent(latent_combine_kernel<R>, (unsigned)(items < sms ? items : sms), LatentCombineGeo::NTHREADS,
+                          (size_t)LatentCombineGeo::smem_bytes(prm.ranges, prm.B), st, c);
 }
 
 template <int R>
@@ -254,31 +237,13 @@ int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k
     g = g < 1 ? 1 : g;
     prm.grp = (int)(g < units ? g : units);
   }
-  cudaLaunchConfig_t cfg = {};
   const long long units = (long long)prm.nqb * prm.B * prm.H;
   if (units * prm.parts > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
-  cfg.gridDim = dim3((unsigned)(units * prm.parts));
-  cfg.blockDim = dim3(Gm::NTHREADS);
-  cfg.dynamicSmemBytes = (size_t)Gm::SMEM;
-  cfg.stream = st;
-  if (cudaLaunchKernelEx(&cfg, latent_prefill_kernel<D>, prm) != cudaSuccess) {
-    cudaGetLastError();
-    return DA_ERR_CUDA;
-  }
+  if (int e = launch_dependent(latent_prefill_kernel<D>, (unsigned)(units * prm.parts), Gm::NTHREADS,
+                               (size_t)Gm::SMEM, st, prm))
+    return e;
   if (prm.parts == 1) return DA_OK;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(units * (Gm::BQ / 32)));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, latent_prefill_merge<D>, prm) != cudaSuccess) {
-    cudaGetLastError();
-    return DA_ERR_CUDA;
-  }
-  return DA_OK;
+  return launch_dependent(latent_prefill_merge<D>, (unsigned)(units * (Gm::BQ / 32)), 256, 0, st, prm);
 }
 
 }  // namespace

@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
     tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
     tmem_relinquish();
   }
+  pdl_wait_primary();  // (what precedes this call in the stream)
   {
     // this CTA's range of the line and its pieces
     int* lens = reinterpret_cast<int*>(smem + Gm::OFF_U);
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MISC);
   const int npieces = *reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 8);
   const int4* more = p.pieces + *reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 12);
-  pdl_launch_dependents();
+  pdl_launch_dependents();  // (after this CTA's own wait: the combine kernel reads seq_lens at once)
 
   struct {
     int b, t0, t1, u, slot;
@@ -640,7 +641,8 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
 // are few of them: warp 0 lists them in order, and each of their items takes a CTA, 16
 // warps of slots (10 loads a thread in flight: 160 slots at once) whose sums are added in
 // order.  Rows of empty sequences are zeroed.  All
-// of the plan's work comes before the wait for the split kernel.
+// of the plan's work comes before the wait for the split kernel, whose CTAs let this one
+// start only after their own wait: seq_lens is as they read it.
 struct LatentCombineParams {
   const float* part_acc;
   const float2* part_ml;
@@ -670,6 +672,7 @@ __global__ void __launch_bounds__(512, 1) latent_combine_kernel(const LatentComb
   constexpr int NCH = R / 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float kNegInf = -__int_as_float(0x7f800000);
+  pdl_launch_dependents();
   build_plan_arrays(p.seq_lens, p.B, p.max_len, kLatentGap, lens, P, 0, Cg::NTHREADS);
   const Plan pl = latent_plan(p.B, p.U, p.ranges, P);
   if (warp == 0) {

@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
   const int qb = p.nqb - 1 - in_g / gsz;
   const int bh = gi * p.grp + in_g % gsz;
   const int b = bh / p.H, h = bh % p.H;
+  pdl_wait_primary();  // (what precedes this call in the stream)
+  pdl_launch_dependents();
   int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len;
   L = L < 0 ? 0 : (L > p.max_len ? p.max_len : L);
   const int q0 = qb * Gm::BQ;
@@ -479,12 +481,13 @@ __global__ void __launch_bounds__(256) latent_prefill_merge(const LatentPrefillP
   constexpr int C = D / 8;  // columns a warp
   const int unit = blockIdx.x / (Gm::BQ / 32), row = (blockIdx.x % (Gm::BQ / 32)) * 32 + (threadIdx.x & 31);
   const int bh = unit / p.nqb, qb = unit - bh * p.nqb, b = bh / p.H, h = bh - b * p.H;
+  pdl_wait_primary();
+  pdl_launch_dependents();
   int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len;
   L = L < 0 ? 0 : (L > p.max_len ? p.max_len : L);
   const int q0 = qb * Gm::BQ, nq = min(Gm::BQ, p.q_len - q0);
   const int kv_end = max(0, min(L, L - p.q_len + q0 + nq));
   const int n = ((kv_end + Gm::BK - 1) / Gm::BK + p.part_tiles - 1) / p.part_tiles;
-  pdl_wait_primary();
   if (n <= 1 || row >= nq) return;
   const float kNegInf = -__int_as_float(0x7f800000);
   const size_t slot0 = (size_t)unit * p.parts;

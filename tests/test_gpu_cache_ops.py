@@ -448,3 +448,51 @@ def test_a_step_in_a_row_captured_and_on_another_stream():
         qn = feed(lens0 + more)
         graph.replay()
         check(qn, lens0 + more, f"replayed {more}")
+
+
+@pytest.mark.parametrize("tokens", [3, 2500])
+def test_calls_in_a_row_see_each_other(tokens):
+    """Every kernel may start while the one before it drains: dependent calls queued without a pause, torch's
+    own kernels among them, give what the same calls give one at a time."""
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    H, D, R, ps = 2, 64, 128, 16
+    pages = -(-tokens // ps)
+    w, w64 = binding.rope_inv_freq(D), binding.rope_inv_freq(64)
+    table = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)[None]
+    start = torch.randn(1, tokens, H, D, generator=gen, device="cuda").to(torch.bfloat16)
+    qs = torch.randn(1, 1, 8, R + 64, generator=gen, device="cuda").to(torch.bfloat16)
+
+    def chain(pause):
+        x, lens = start.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+        pos = torch.zeros(1, tokens, dtype=torch.int32, device="cuda")
+        pool = [torch.zeros(pages, ps, H, D, dtype=torch.int8, device="cuda") for _ in "kv"]
+        scale = [torch.zeros(pages, H, ps, device="cuda") for _ in "kv"]
+        latent = torch.zeros(pages, ps, R + 64, dtype=torch.bfloat16, device="cuda")
+        seen = []
+        for i in range(12):
+            pos.fill_(i * 1000).add_(torch.arange(tokens, device="cuda", dtype=torch.int32))
+            lens.fill_(tokens)
+            pause()
+            binding.rope_apply(x, pos, w, out=x)
+            pause()
+            binding.kv_write_int8_paged(x, x, *pool, *scale, table, lens, tokens, inv_freq=w)
+            pause()
+            k, v = binding.kv_read_int8_paged(*pool, *scale, table, lens, tokens, tokens)
+            pause()
+            binding.rope_apply(k, pos, w, backward=True, out=x)
+            pause()
+            row = torch.cat((x.flatten(2), v.flatten(2)[..., :64]), -1)[:, :, None]
+            binding.kv_write_paged(row, None, latent[:, :, None], None, table, lens, tokens, inv_freq=w64, offset=R)
+            pause()
+            out = binding.latent_attn_paged(qs, latent, table, lens, tokens, scale=0.1)
+            pause()
+            x.mul_(1.0 + out.float().mean().clamp(-0.1, 0.1).to(torch.bfloat16))
+            lens.zero_()  # after the calls that read it
+            seen.append(x.clone())
+        torch.cuda.synchronize()
+        return torch.stack(seen)
+
+    slow = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        assert torch.equal(chain(lambda: None), slow)
+    assert binding.device_error() == 0
