@@ -179,6 +179,7 @@ int64_t token_stride(const Tensor& t, const char* name, int lead) {
   return step;
 }
 
+// The C ABI call, without the GIL: f neither throws nor touches Python.
 template <typename F>
 void call(const char* fn, F f) {
   int st;
@@ -246,11 +247,11 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor out = given ? *given : at::empty(shape, x.options());
     const int64_t oh = given ? out.strides()[lead] : D, xh = x.strides()[lead];
     const int off = small(a[3], "offset"), il = truth(a[4]), back = truth(a[6]);
+    const int Hi = small(H, "x"), Di = small(D, "x"), roti = small(2 * rot, "inv_freq");
     const float mag = real(a[5]);
     call("rope_apply", [&] {
-      return g_lib.rope_apply(ptr(x), ptr(out), ptr<int>(positions), ptr<double>(w), positions.numel(), small(H, "x"),
-                              small(D, "x"), off, small(2 * rot, "inv_freq"), il, mag, back, dtype, xt, xh, ot, oh,
-                              st.raw);
+      return g_lib.rope_apply(ptr(x), ptr(out), ptr<int>(positions), ptr<double>(w), positions.numel(), Hi, Di, off,
+                              roti, il, mag, back, dtype, xt, xh, ot, oh, st.raw);
     });
     return given ? same(a[7]) : THPVariable_Wrap(out);
   });
@@ -443,12 +444,13 @@ PyObject* latent_attn(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     }
     const Tensor& w = ws ? *ws : work;
     const long long size = (long long)w.nbytes();
-    const int slab = small(cache.size(1), "cache"), slabs = small(cache.size(0), "cache");
+    const int slab = small(cache.size(1), "cache"), slabs = small(cache.size(0), "cache"),
+              columns = small(cols, "page_table");
     if (table) {
       const int cap = small(a[4], "max_seq_len");
       call(fn, [&] {
         return g_lib.latent_attn_paged(ptr(q), ptr(cache), ptr<int>(table), ptr<int>(lens), B, n, H, (int)R, slab,
-                                       small(cols, "page_table"), slabs, cap, scale, ptr(w), size, ptr(out), st.raw);
+                                       columns, slabs, cap, scale, ptr(w), size, ptr(out), st.raw);
       });
     } else {
       call(fn, [&] {
@@ -497,16 +499,17 @@ PyObject* latent_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (lens) plain(*lens, "seq_lens", at::kInt, dims(B), dev);
     if (given) plain(*given, "out", at::kBFloat16, dims(B, n, H, D), dev);
     const float scale = real(a[5]);
+    const int ctxi = small(ctx, "k_nope");
     on_current(dev);
     Stream st(a[7], dev);
     const Tensor out = given ? *given : at::empty(dims(B, n, H, D), q.options());
     Tensor work;
-    const long long bytes = g_lib.latent_prefill_workspace_bytes(B, n, H, (int)D, small(ctx, "k_nope"), 0);
+    const long long bytes = g_lib.latent_prefill_workspace_bytes(B, n, H, (int)D, ctxi, 0);
     if (bytes < 0) throw Failed{"latent_prefill_contig", (int)-bytes};
     if (bytes > 0) work = at::empty(dims(bytes), q.options().dtype(at::kByte));
     call("latent_prefill_contig", [&] {
       return g_lib.latent_prefill_contig(ptr(q), ptr(k), ptr(pe), ptr(v), ptr<int>(lens), B, n, H, (int)D,
-                                         small(ctx, "k_nope"), kst.first, kst.second, pst.first, scale,
+                                         ctxi, kst.first, kst.second, pst.first, scale,
                                          bytes > 0 ? ptr(work) : nullptr, bytes, ptr(out), st.raw);
     });
     return given ? same(a[6]) : THPVariable_Wrap(out);

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
   unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
   float2* cs = reinterpret_cast<float2*>(step + np);  // [tb][np] (np a multiple of 8)
   const unsigned total = (unsigned)p.B * (unsigned)p.n;  // below 2^31
-  const int rows_per_token = p.Hkv * (p.v ? 2 : 1);
+  const int rows_per_token = p.Hkv * (p.v_new ? 2 : 1);
   const int rows = p.tb * rows_per_token;
   const int nchunk = p.D / 8, gl = threadIdx.x & (p.lanes - 1);
   // position of new token g = b n + i: L_b - n + i
@@ -512,9 +512,20 @@ int check_cache(const CacheParams& p, bool paged, bool int8, long long cap) {
   return DA_OK;
 }
 
-int check_cache_pointers(const CacheParams& p, bool paged, bool int8) {
-  if (!p.k || !aligned(p.k, 16) || !aligned(p.v, 16)) return DA_ERR_INVALID_ARG;
-  if (int8 && (!p.ks || !aligned(p.ks, 4) || (p.v && (!p.vs || !aligned(p.vs, 4))))) return DA_ERR_INVALID_ARG;
+// Bytes of one tensor of the cache, and of its scales.
+long long cache_bytes(const CacheParams& p, bool paged, bool int8) {
+  return (long long)(paged ? p.num_pages : p.B) * p.slab * p.Hkv * p.D * (int8 ? 1 : 2);
+}
+long long scale_bytes(const CacheParams& p, bool paged) {
+  return (long long)(paged ? p.num_pages : p.B) * p.slab * p.Hkv * 4;
+}
+
+int check_cache_pointers(const CacheParams& p, bool paged, bool int8, bool has_v) {
+  const bool rows = p.cap > 0 && (!paged || p.num_pages > 0);  // a cache of none may be null
+  if (rows && (!p.k || !p.v != !has_v)) return DA_ERR_INVALID_ARG;
+  if (!aligned(p.k, 16) || !aligned(p.v, 16)) return DA_ERR_INVALID_ARG;
+  if (int8 && rows && (!p.ks || (has_v && !p.vs))) return DA_ERR_INVALID_ARG;
+  if (!aligned(p.ks, 4) || !aligned(p.vs, 4)) return DA_ERR_INVALID_ARG;
   if (paged && (!p.page_table || !p.seq_lens || !aligned(p.page_table, 4))) return DA_ERR_INVALID_ARG;
   if (!aligned(p.seq_lens, 4) || !aligned(p.starts, 4)) return DA_ERR_INVALID_ARG;
   return DA_OK;
@@ -529,7 +540,7 @@ int launch_write(CacheParams& p, int sms, cudaStream_t st) {
   const int cpl = nchunk > 64 ? 4 : nchunk > 32 || (nchunk > 1 && (long long)p.B * p.n >= 8LL * sms) ? 2 : 1;
   p.lanes = 1;
   while (p.lanes * cpl < nchunk && p.lanes < 32) p.lanes *= 2;
-  const int rows = p.Hkv * (p.v ? 2 : 1), np = p.r.inv_freq ? p.r.rot / 2 : 0;
+  const int rows = p.Hkv * (p.v_new ? 2 : 1), np = p.r.inv_freq ? p.r.rot / 2 : 0;
   // enough tokens that every lane has a row, four rounds of them where tokens abound (the
   // cosines then take every thread), as long as the cosines fit
   const long long total = (long long)p.B * p.n;
@@ -556,10 +567,26 @@ int write_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_
   }
   if (p.B == 0 || p.n == 0) return DA_OK;
   const long long width = (long long)p.Hkv * p.D;
-  if (!p.k_new || !aligned(p.k_new, 16) || !p.v_new != !p.v || !aligned(p.v_new, 16)) return DA_ERR_INVALID_ARG;
-  if (p.k_stride < width || p.k_stride % 8 || (p.v && (p.v_stride < width || p.v_stride % 8)))
+  const bool has_v = p.v_new != nullptr;
+  if (!p.k_new || !aligned(p.k_new, 16) || !aligned(p.v_new, 16)) return DA_ERR_INVALID_ARG;
+  const long long far = 1LL << 40;  // strides whose products with the sizes stay in 64 bits
+  if (p.k_stride < width || p.k_stride % 8 || p.k_stride > far ||
+      (has_v && (p.v_stride < width || p.v_stride % 8 || p.v_stride > far)))
     return DA_ERR_INVALID_ARG;
-  if (int e = check_cache_pointers(p, paged, int8)) return e;
+  if (!has_v && p.v) return DA_ERR_INVALID_ARG;
+  if (int e = check_cache_pointers(p, paged, int8, has_v)) return e;
+  {
+    // nothing that is written may be read by the same call, nor written twice
+    const long long tokens = (long long)p.B * p.n - 1, kn = (tokens * p.k_stride + width) * 2,
+                    vn = (tokens * p.v_stride + width) * 2, cn = cache_bytes(p, paged, int8), sn = scale_bytes(p, paged);
+    const void* dst[4] = {p.k, p.v, p.ks, p.vs};
+    const long long bytes[4] = {cn, cn, sn, sn};
+    for (int i = 0; i < 4; ++i) {
+      if (overlap(p.k_new, kn, dst[i], bytes[i]) || overlap(p.v_new, vn, dst[i], bytes[i])) return DA_ERR_INVALID_ARG;
+      for (int j = 0; j < i; ++j)
+        if (overlap(dst[j], bytes[j], dst[i], bytes[i])) return DA_ERR_INVALID_ARG;
+    }
+  }
   int dev, sms, optin;
   if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
   if (paged) return int8 ? launch_write<true, true>(p, sms, st) : launch_write<true, false>(p, sms, st);
@@ -570,8 +597,19 @@ int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t
   if (int e = check_cache(p, paged, int8, cap)) return e;
   p.cap = (int)cap;
   if (p.B == 0 || p.n == 0) return DA_OK;
-  if (!p.k_out || !aligned(p.k_out, 16) || !p.v_out != !p.v || !aligned(p.v_out, 16)) return DA_ERR_INVALID_ARG;
-  if (int e = check_cache_pointers(p, paged, int8)) return e;
+  const bool has_v = p.v_out != nullptr;
+  if (!p.k_out || !aligned(p.k_out, 16) || !aligned(p.v_out, 16) || (!has_v && p.v)) return DA_ERR_INVALID_ARG;
+  if (int e = check_cache_pointers(p, paged, int8, has_v)) return e;
+  if (p.cap == 0 || (paged && p.num_pages == 0)) return DA_OK;  // every row is past its sequence
+  {
+    const long long on = (long long)p.B * p.n * p.Hkv * p.D * 2, cn = cache_bytes(p, paged, int8),
+                    sn = scale_bytes(p, paged);
+    const void *out[2] = {p.k_out, p.v_out}, *src[4] = {p.k, p.v, p.ks, p.vs};
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 4; ++j)
+        if (overlap(out[i], on, src[j], j < 2 ? cn : sn)) return DA_ERR_INVALID_ARG;
+    if (overlap(out[0], on, out[1], on)) return DA_ERR_INVALID_ARG;
+  }
   int dev, sms, optin;
   if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
   // about 4 loads of 16 bytes a thread and tensor, fewer while that leaves SMs without their
@@ -648,10 +686,9 @@ extern "C" int rope_apply(const void* x, void* out, const int* positions, const 
       return DA_ERR_INVALID_ARG;
   } else {
     // a partly overlapping output would be read after it is written
-    const uintptr_t xb = reinterpret_cast<uintptr_t>(x), ob = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t xn = ((tokens - 1) * x_token_stride + (num_heads - 1) * x_head_stride + head_dim) * size;
-    const uintptr_t on = ((tokens - 1) * out_token_stride + (num_heads - 1) * out_head_stride + head_dim) * size;
-    if (xb < ob + on && ob < xb + xn) return DA_ERR_INVALID_ARG;
+    const long long xn = ((tokens - 1) * x_token_stride + (num_heads - 1) * x_head_stride + head_dim) * size;
+    const long long on = ((tokens - 1) * out_token_stride + (num_heads - 1) * out_head_stride + head_dim) * size;
+    if (overlap(x, xn, out, on)) return DA_ERR_INVALID_ARG;
   }
   int dev, sms, optin;
   if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;

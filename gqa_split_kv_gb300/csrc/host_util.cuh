@@ -77,6 +77,12 @@ int encode_map_t(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle sw
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Whether [a, a + an) and [b, b + bn) share a byte (null pointers: no).
+bool overlap(const void* a, long long an, const void* b, long long bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
 // Launches kern as a programmatic dependent of what precedes it in the stream: its CTAs may
 // start while that drains, so every kernel launched here waits for it (griddepcontrol.wait)
 // before it touches memory.

@@ -390,7 +390,8 @@ int rope_apply(const void* x, void* out, const int* positions, const double* inv
  * A position at or past the capacity (max_ctx, or min(max_seq_len, max_pages_per_seq *
  * page_size)) is not written and sets bit 3 of the device error word; one whose page-table
  * entry lies outside [0, num_pages) is not written and sets bit 2.  Nothing else in the
- * cache changes.  Sequences whose new tokens fall on the same cache row race.
+ * cache changes.  Sequences whose new tokens fall on the same cache row race; new tokens
+ * and caches that overlap are refused.
  *  k_new, v_new  bf16 [batch, q_len, num_kv_heads, head_dim], k_stride / v_stride elements
  *                from one token to the next (a multiple of 8, at least num_kv_heads *
  *                head_dim: a slice of a fused projection will do); 16-byte aligned

@@ -9,7 +9,8 @@ import pytest
 from oracle import cache_ops as oc
 from gqa_split_kv_gb300 import build as build_mod
 
-A = 0x10000  # an aligned address that refused calls never read
+A = 0x10000  # aligned addresses, far apart, that refused calls never read
+K, V, SK, SV = (A + (i << 40) for i in range(1, 5))
 NAN = float("nan")
 
 
@@ -120,7 +121,7 @@ def test_rope_refusals(clib, kw, want):
 
 
 def write(clib, paged=True, int8=True, k_new=A, v_new=A, ks=256, vs=256, table=A, lens=A, B=2, n=1, H=2, D=64, ps=16,
-          maxp=4, npages=8, maxlen=64, w=None, off=0, rot=0, il=0, mag=1.0, k=A, v=A, sk=A, sv=A):
+          maxp=4, npages=8, maxlen=64, w=None, off=0, rot=0, il=0, mag=1.0, k=K, v=V, sk=SK, sv=SV):
     where = (ps, maxp, npages, maxlen) if paged else (maxlen,)
     fn = getattr(clib, "kv_write" + ("_int8" if int8 else "") + ("_paged" if paged else "_contig"))
     return fn(k_new, v_new, ks, vs, *((table,) if paged else ()), lens, B, n, H, D, *where, w, off, rot, il, mag, k, v,
@@ -131,12 +132,14 @@ def write(clib, paged=True, int8=True, k_new=A, v_new=A, ks=256, vs=256, table=A
     (dict(B=-1), 1), (dict(n=-1), 1), (dict(H=0), 1), (dict(D=0), 1), (dict(D=24), 2), (dict(D=20, int8=False), 2),
     (dict(D=1040), 2), (dict(H=2000), 2), (dict(ps=0), 1), (dict(maxp=-1), 1), (dict(npages=-1), 1),
     (dict(maxlen=-1), 1), (dict(maxlen=-1, paged=False), 1), (dict(k_new=None), 1), (dict(k_new=A + 8), 1),
-    (dict(v_new=None), 1), (dict(v=None), 1), (dict(k=None), 1), (dict(k=A + 8), 1), (dict(sk=None), 1),
+    (dict(v_new=None), 1), (dict(v=None), 1), (dict(k=None), 1), (dict(k=K + 8), 1), (dict(sk=None), 1),
     (dict(sv=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(ks=100), 1), (dict(ks=260), 1),
     (dict(vs=64), 1), (dict(w=A, rot=64, off=8), 1), (dict(w=A, rot=24), 2), (dict(w=A, rot=32, off=4), 2),
     (dict(w=A + 4, rot=32), 1), (dict(w=A, rot=0), 1), (dict(w=A, rot=32, il=5), 1), (dict(w=A, rot=32, mag=NAN), 1),
     (dict(B=70000, n=70000), 2), (dict(maxp=1 << 30, ps=64, maxlen=2**31 - 1), None),
-    (dict(B=0), 0), (dict(n=0), 0),
+    (dict(B=0), 0), (dict(n=0), 0), (dict(ks=1 << 41), 1),
+    (dict(k=A), 1), (dict(v=A + 64), 1), (dict(sk=A), 1), (dict(v_new=SV + 16), 1),  # new tokens in the cache
+    (dict(v=K), 1), (dict(sv=V), 1), (dict(sk=SV + 4), 1),                          # the cache's tensors share bytes
 ])
 def test_write_refusals(clib, kw, want):
     if want is None:  # a long cap is the smaller of the two: fine up to 2^31 - 1 (refused here for its null table)
@@ -145,8 +148,8 @@ def test_write_refusals(clib, kw, want):
         assert write(clib, **kw) == want
 
 
-def read(clib, paged=True, int8=True, k=A, v=A, sk=A, sv=A, table=A, starts=None, lens=A, B=2, n=4, H=2, D=64, ps=16,
-         maxp=4, npages=8, maxlen=64, ko=A, vo=A):
+def read(clib, paged=True, int8=True, k=K, v=V, sk=SK, sv=SV, table=A, starts=None, lens=A, B=2, n=4, H=2, D=64, ps=16,
+         maxp=4, npages=8, maxlen=64, ko=A, vo=A + (1 << 30)):
     where = (ps, maxp, npages, maxlen) if paged else (maxlen,)
     fn = getattr(clib, "kv_read" + ("_int8" if int8 else "") + ("_paged" if paged else "_contig"))
     return fn(k, v, *((sk, sv) if int8 else ()), *((table,) if paged else ()), starts, lens, B, n, H, D, *where, ko, vo,
@@ -158,7 +161,8 @@ def read(clib, paged=True, int8=True, k=A, v=A, sk=A, sv=A, table=A, starts=None
     (dict(ko=None), 1), (dict(vo=None), 1), (dict(v=None), 1), (dict(ko=A + 8), 1), (dict(vo=A + 4), 1),
     (dict(sk=None), 1), (dict(sv=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(starts=A + 2), 1),
     (dict(ps=-16), 1), (dict(npages=-1), 1), (dict(maxlen=-1), 1), (dict(paged=False, maxlen=-1), 1),
-    (dict(B=0), 0), (dict(n=0), 0),
+    (dict(B=0), 0), (dict(n=0), 0), (dict(ko=K), 1), (dict(vo=SV + 16), 1), (dict(vo=A), 1),  # outputs in the cache
+    (dict(npages=0, k=None, v=None, sk=None, sv=None), 0), (dict(maxlen=0, k=None, v=None, sk=None, sv=None), 0),
 ])
 def test_read_refusals(clib, kw, want):
     assert read(clib, **kw) == want

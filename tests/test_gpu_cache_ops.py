@@ -496,3 +496,103 @@ def test_calls_in_a_row_see_each_other(tokens):
     for _ in range(5):
         assert torch.equal(chain(lambda: None), slow)
     assert binding.device_error() == 0
+
+
+def test_offsets_past_32_bits():
+    """A pool of over 2^32 bytes and 2^31 elements: its last pages written, attended to and read; heads far apart."""
+    W, ps, pages = 576, 64, 66000  # 2.4e9 elements, 4.9 GB
+    pool = torch.zeros(pages, ps, W, device="cuda", dtype=torch.bfloat16)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    L = 150
+    rows = torch.randn(1, L, 1, W, generator=gen, device="cuda").to(torch.bfloat16)
+    table = torch.tensor([[pages - 1, pages - 3, pages - 2]], dtype=torch.int32, device="cuda")
+    lens = dev_i32(np.array([L]))
+    binding.kv_write_paged(rows, None, pool[:, :, None], None, table, lens, 192)
+    back, _ = binding.kv_read_paged(pool[:, :, None], None, table, lens, 192, L)
+    assert torch.equal(back, rows)
+    q = torch.randn(1, 1, 16, W, generator=gen, device="cuda").to(torch.bfloat16)
+    small = binding.latent_attn_contig(q, rows[:, :, 0].contiguous(), scale=0.05)
+    assert torch.equal(binding.latent_attn_paged(q, pool, table, lens, 192, scale=0.05), small)
+    assert int((pool.view(torch.int16)[: pages - 3] != 0).sum()) == 0
+    k8 = pool.view(torch.int8).view(pages, ps, 2, W)  # the same memory as an int8 pool
+    scale = torch.zeros(pages, 2, ps, device="cuda")
+    new = torch.randn(1, L, 2, W, generator=gen, device="cuda").to(torch.bfloat16)
+    binding.kv_write_int8_paged(new, None, k8, None, scale, None, table, lens, 192)
+    back, _ = binding.kv_read_int8_paged(k8, None, scale, None, table, lens, 192, L)
+    near, near_scale = torch.zeros(1, 192, 2, W, device="cuda", dtype=torch.int8), torch.zeros(1, 2, 192, device="cuda")
+    binding.kv_write_int8_contig(new, None, near, None, near_scale, None, lens)
+    want, _ = binding.kv_read_int8_contig(near, None, near_scale, None, lens, L)
+    assert torch.equal(back, want) and bool(want.any())
+    x = pool.view(-1)
+    far = torch.as_strided(x, (2, 2, 64), (2 ** 30 + 2 ** 29, 2 ** 29, 1))
+    far.copy_(torch.randn(2, 2, 64, generator=gen, device="cuda"))
+    pos, w = dev_i32(np.array([5, 1000])), binding.rope_inv_freq(64)
+    want = binding.rope_apply(far.contiguous(), pos, w)
+    binding.rope_apply(far, pos, w, out=far)
+    assert torch.equal(far, want)
+
+
+def test_empty_caches():
+    """A cache of no pages or no tokens: nothing is read, a written token is flagged."""
+    bf16, z = torch.bfloat16, dev_i32(np.array([0, 0]))
+    pool, table = torch.zeros(0, 16, 2, 64, device="cuda", dtype=bf16), torch.zeros(2, 3, device="cuda", dtype=torch.int32)
+    k, v = binding.kv_read_paged(pool, pool.clone(), table, dev_i32(np.array([5, 0])), 48, 4)
+    assert not k.any() and not v.any() and binding.device_error() == 0
+    new = torch.ones(2, 1, 2, 64, device="cuda", dtype=bf16)
+    binding.kv_write_paged(new, new, pool, pool.clone(), table, z, 48)  # lengths 0: nothing to write
+    assert binding.device_error() == 0
+    binding.kv_write_paged(new, new, pool, pool.clone(), table, dev_i32(np.array([1, 0])), 48)
+    assert binding.device_error() == 4
+    cache = torch.zeros(2, 0, 2, 64, device="cuda", dtype=bf16)
+    binding.kv_write_contig(new, new, cache, cache.clone(), dev_i32(np.array([1, 0])))
+    assert binding.device_error() == 8
+    q = torch.ones(2, 1, 4, 192, device="cuda", dtype=bf16)
+    assert not binding.latent_attn_contig(q, torch.zeros(2, 0, 192, device="cuda", dtype=bf16), scale=1.0).any()
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+from gqa_split_kv_gb300 import binding
+bf16 = torch.bfloat16
+gen = torch.Generator(device="cuda").manual_seed(3)
+x = torch.randn(8, 2, 64, generator=gen, device="cuda").to(bf16)
+pos = torch.arange(8, device="cuda", dtype=torch.int32)
+w = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).cuda()
+new = torch.randn(2, 4, 2, 64, generator=gen, device="cuda").to(bf16)
+k = torch.zeros(2, 8, 2, 64, device="cuda", dtype=torch.int8)
+ks = torch.zeros(2, 2, 8, device="cuda")
+lens = torch.tensor([4, 8], device="cuda", dtype=torch.int32)
+q = torch.randn(2, 1, 4, 192, generator=gen, device="cuda").to(bf16)
+cache = torch.randn(2, 8, 192, generator=gen, device="cuda").to(bf16)
+qe = torch.randn(2, 3, 2, 128, generator=gen, device="cuda").to(bf16)
+kv = torch.randn(2, 600, 2, 128, generator=gen, device="cuda").to(bf16)
+pe = torch.randn(2, 600, 64, generator=gen, device="cuda").to(bf16)
+
+def calls():
+    a = binding.rope_apply(x, pos, w)
+    v, vs = k.clone(), ks.clone()
+    binding.kv_write_int8_contig(new, new, k, v, ks, vs, lens, inv_freq=w)
+    b, c = binding.kv_read_int8_contig(k, v, ks, vs, lens, 8)
+    d = binding.latent_attn_contig(q, cache, lens, scale=0.1)
+    e = binding.latent_prefill_contig(qe, kv[..., :64], pe, kv[..., 64:], scale=0.1)
+    return a, b, c, d, e
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+for g, r in zip(got, calls()):
+    assert torch.equal(g, r)
+assert binding.device_error() == 0
+print("first calls captured")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "first calls captured" in res.stdout, res.stdout + res.stderr

@@ -8,7 +8,8 @@ import pytest
 from oracle import latent_attention as ol
 from gqa_split_kv_gb300 import build as build_mod
 
-A = 0x10000  # an aligned address that refused calls never read
+A = 0x10000  # aligned addresses, far apart, that refused calls never read
+K, V, PE, WS, OUT = (A + (i << 44) for i in range(1, 6))
 
 
 @pytest.fixture(scope="module")
@@ -65,8 +66,8 @@ def test_causal_and_pages():
 
 # ---------------------------------------------------------------- refusals
 
-def attn(clib, paged=False, q=A, cache=A, table=A, lens=A, B=2, n=1, H=16, R=512, ctx=64, ps=16, maxp=4, npages=8,
-         maxlen=64, scale=0.1, ws=A, size=1 << 40, out=A):
+def attn(clib, paged=False, q=A, cache=K, table=A, lens=A, B=2, n=1, H=16, R=512, ctx=64, ps=16, maxp=4, npages=8,
+         maxlen=64, scale=0.1, ws=WS, size=1 << 40, out=OUT):
     f = ctypes.c_float(scale)
     if paged:
         return clib.latent_attn_paged(q, cache, table, lens, B, n, H, R, ps, maxp, npages, maxlen, f, ws, size, out, None)
@@ -76,8 +77,8 @@ def attn(clib, paged=False, q=A, cache=A, table=A, lens=A, B=2, n=1, H=16, R=512
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), 1), (dict(n=0), 1), (dict(n=17), 1), (dict(H=0), 1), (dict(H=257), 2), (dict(R=64), 2),
     (dict(R=384), 2), (dict(ctx=-1), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
-    (dict(q=None), 1), (dict(out=None), 1), (dict(q=A + 8), 1), (dict(out=A + 2), 1), (dict(cache=None), 1),
-    (dict(cache=A + 8), 1), (dict(lens=A + 2), 1), (dict(B=1 << 20), 2), (dict(B=0), 0),
+    (dict(q=None), 1), (dict(out=None), 1), (dict(q=A + 8), 1), (dict(out=OUT + 2), 1), (dict(cache=None), 1),
+    (dict(cache=K + 8), 1), (dict(lens=A + 2), 1), (dict(B=1 << 20), 2), (dict(B=0), 0),
     (dict(paged=True, ps=0), 1), (dict(paged=True, ps=24), 2), (dict(paged=True, ps=8), 2),
     (dict(paged=True, maxp=-1), 1), (dict(paged=True, npages=-1), 1), (dict(paged=True, maxlen=-1), 1),
     (dict(paged=True, table=None), 1), (dict(paged=True, lens=None), 1), (dict(paged=True, table=A + 2), 1),
@@ -97,7 +98,7 @@ def test_workspace_and_batch_queries(clib):
     assert clib.latent_max_batch(0, 1, 128) == -1
 
 
-def prefill(clib, q=A, k=A, pe=A, v=A, lens=A, B=2, n=4, H=4, D=128, ctx=64, ts=512, hs=128, ps=64, scale=0.1, out=A,
+def prefill(clib, q=A, k=K, pe=PE, v=V, lens=A, B=2, n=4, H=4, D=128, ctx=64, ts=512, hs=128, ps=64, scale=0.1, out=OUT,
             ws=None, size=0):
     return clib.latent_prefill_contig(q, k, pe, v, lens, B, n, H, D, ctx, ts, hs, ps, ctypes.c_float(scale), ws, size, out,
                                       None)
@@ -106,8 +107,9 @@ def prefill(clib, q=A, k=A, pe=A, v=A, lens=A, B=2, n=4, H=4, D=128, ctx=64, ts=
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), 1), (dict(n=-1), 1), (dict(H=0), 1), (dict(D=96), 2), (dict(D=256), 2), (dict(ctx=-1), 1),
     (dict(scale=float("nan")), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(pe=None), 1), (dict(v=None), 1),
-    (dict(out=None), 1), (dict(q=A + 8), 1), (dict(k=A + 8), 1), (dict(pe=A + 4), 1), (dict(v=A + 2), 1),
-    (dict(out=A + 8), 1), (dict(lens=A + 1), 1), (dict(ws=A + 8), 1), (dict(hs=64), 1), (dict(hs=132, ts=1024), 1), (dict(ts=500), 1),
+    (dict(out=None), 1), (dict(q=A + 8), 1), (dict(k=K + 8), 1), (dict(pe=PE + 4), 1), (dict(v=V + 2), 1),
+    (dict(out=OUT + 8), 1), (dict(lens=A + 1), 1), (dict(ws=WS + 8), 1), (dict(ts=1 << 41), 1),
+    (dict(out=A), 1), (dict(out=V + 16), 1), (dict(out=PE), 1), (dict(ws=K, size=64), 1), (dict(ws=OUT, size=64), 1), (dict(hs=64), 1), (dict(hs=132, ts=1024), 1), (dict(ts=500), 1),
     (dict(ts=516), 1), (dict(ps=32), 1), (dict(ps=68), 1), (dict(B=1 << 20, n=1 << 20), 2), (dict(B=0), 0), (dict(n=0), 0),
 ])
 def test_prefill_refusals(clib, kw, want):
