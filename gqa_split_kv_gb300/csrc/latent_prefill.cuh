@@ -136,6 +136,9 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
   const int j0 = (int)((long long)all_tiles * part / nparts);
   const int ntiles = (int)((long long)all_tiles * (part + 1) / nparts) - j0;
   const bool whole = nparts == 1;
+  // query tile A's rows see up to 128 keys less than B's: its tiles of this part
+  const int end_a = max(0, min(L, base + q0 + min(nq, M)));
+  const int ntiles_a = max(0, min(ntiles, (end_a + BK - 1) / BK - j0));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Gm::NG; ++i) {
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       };
       bool ok = ntiles > 0 && wait_all(Gm::BAR_Q, 0) && landed(0, 0, Gm::NKG);
       if (ok) {
-        if (elect_one()) {
+        if (ntiles_a > 0 && elect_one()) {
           tc_fence_after();
           issue_qk(0, 0);
         }
@@ -282,16 +285,18 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         ok = landed(j, Gm::NKG, Gm::PER);
         if (!ok) break;
         if ((j0 + j + 1) * BK > kv_end) zero_tail(j);
-        if (!(ok = wait_all(Gm::BAR_P, j))) break;
-        if (elect_one()) {
-          tc_fence_after();
-          issue_pv(0, j);
-          if (!more) tc_commit(bar(Gm::BAR_O));
+        if (j < ntiles_a) {
+          if (!(ok = wait_all(Gm::BAR_P, j))) break;
+          if (elect_one()) {
+            tc_fence_after();
+            issue_pv(0, j);
+            if (j + 1 == ntiles_a) tc_commit(bar(Gm::BAR_O));
+          }
+          __syncwarp();
         }
-        __syncwarp();
         if (more) {
           if (!(ok = landed(j + 1, 0, Gm::NKG))) break;
-          if (elect_one()) {
+          if (j + 1 < ntiles_a && elect_one()) {
             tc_fence_after();
             issue_qk(0, j + 1);
           }
@@ -323,6 +328,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     // ---- softmax and epilogue of query tile qt: one thread per row (tensor memory lane)
     latent_setmaxnreg_inc<Gm::REG_HIGH>();
     const int qt = (warp >> 2) - 1;
+    const int nt = qt == 0 ? ntiles_a : ntiles;  // this query tile's key tiles
     const int row = lane + 32 * (warp & 3);
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const int tok = qt * M + row;  // this row's token within the block
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     float m = kNegInf, l = 0.f;
     bool ok = true;
     if (qt < nqt) {
-      for (int j = 0; j < ntiles; ++j) {
+      for (int j = 0; j < nt; ++j) {
         ok = __all_sync(0xffffffffu, wait(Gm::BAR_S + qt, j));
         if (!ok) break;
         tc_fence_after();
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         if (lane == 0) mbar_arrive(bar(Gm::BAR_P + qt));
       }
       // ---- normalise and write the tile's rows (a row that saw nothing: zeros)
-      if (ok && ntiles > 0) ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + qt, 0));
+      if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + qt, 0));
       if (ok) {
         tc_fence_after();
         if (!whole) {
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           const size_t slot = ((size_t)bh * p.nqb + qb) * p.parts + part;
           float* acc = p.part_acc + slot * D * Gm::BQ + tok;
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
+          for (int c0 = 0; c0 < D && nt > 0; c0 += 32) {  // (l is 0 with no tile, and nothing else read)
             uint32_t r[32];
             tmem_ld32(o_addr + c0, r);
             tmem_ld_wait();
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
 #pragma unroll 1
         for (int c0 = 0; c0 < D && whole; c0 += 32) {
           uint32_t r[32];
-          if (ntiles > 0) {
+          if (nt > 0) {
             tmem_ld32(o_addr + c0, r);
             tmem_ld_wait();
           } else {
