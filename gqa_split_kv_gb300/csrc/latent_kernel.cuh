@@ -23,8 +23,8 @@
 // the rotated part (8 KB) in a ring of its own; a unit is freed by its own P^T product.  The
 // ring has to hold two whole tiles: with one unit less (7 at N = 64) the last unit of a
 // tile waits for the first product of the tile before it, and a tile takes that
-// latency (0.8 us) and a load's (1.5 us) instead of half of it (2.3 us a tile, where HBM
-// needs 1.7).  So at N = 64, R = 512 the plan's arrays share the ring's memory, each
+// latency (0.8 us) and a load's (1.5 us) instead of half of it: 2.27 us a tile with 7 units,
+// 1.96 with 8.  So at N = 64, R = 512 the plan's arrays share the ring's memory, each
 // CTA's pieces are listed once, and P^T has one buffer.
 //
 // Softmax.  S comes back as the fragment of a 16 x 8 warp MMA: thread t of warp w holds
@@ -41,9 +41,21 @@
 // 512), whatever the batch; latent_combine_kernel merges them.
 //
 // Warps: 0 and 3 issue the copies (Q and even units; odd units and the rotated part), 1
-// the S products, 2 the O products (one thread issues an MMA every 45 cycles; at N = 64 the
-// two kinds take 32 and 48 on the tensor cores, so one thread for both would be the
-// limit), from 4 on softmax and epilogue, a warpgroup per 32 rows.  Waits are bounded as in prefill_tc.cuh.
+// the S products, 2 the O products, from 4 on softmax and epilogue, a warpgroup per 32
+// rows.  The issuing lane is chosen by elect.sync: behind a lane compare the compiler
+// guards every MMA, 45 cycles each, behind elect.sync 23, which at N <= 32 is less than the
+// tensor core takes (batch below: 57.8 -> 47.9 us).  Waits are bounded as in prefill_tc.cuh.
+//
+// Bound and measured (bf16, R = 512).  16 sequences up to 8192 tokens, 128 heads: 46.7
+// us, where HBM needs 12.3 and the tensor cores 9.6; 64 sequences of 1 to 32768 tokens, 64
+// heads: 64.7 us, HBM 36.0; one sequence of 4096 tokens, 16 heads: 10.7 us.  A tile of 64
+// rows takes 1.85 us: the round through its two ring slots (load 1.5 us, S 0.6, softmax
+// 0.5, O 0.4, overlapping by units), not HBM (85 MB of it are read once, by the other row
+// tile from L2), with the tensor cores 35% busy.  Around the tiles: 5 us to the first
+// tile's products (launch, plan, Q and the first load), 2.4 us for the partials, and the merge,
+// 5 to 8 us, whose 22 MB come from L2.  Tried and dropped: prefetching 4 tiles ahead into
+// L2 (2.5 us a tile), and pairs of CTAs that share a tile by multicast (1.65 us a tile but 2
+// us more at the start and end: 49.4 against 49.2 us).
 #pragma once
 
 #include <cuda.h>

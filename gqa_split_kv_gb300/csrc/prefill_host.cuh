@@ -1,6 +1,6 @@
 // Host side of the causal prefill entry points (declared in include/decode_attn.h):
 // argument checks, TMA maps of the caller's cache and the launch of the prefill
-// kernel.  Part of the library's single translation unit (included at the end of
+// kernel.  Part of decode_attn.cu's translation unit (included at the end of
 // decode_attn.cu, after its helpers).
 #pragma once
 
