@@ -46,14 +46,14 @@
 // guards every MMA, 45 cycles each, behind elect.sync 23, which at N <= 32 is less than the
 // tensor core takes (batch below: 57.8 -> 47.9 us).  Waits are bounded as in prefill_tc.cuh.
 //
-// Bound and measured (bf16, R = 512).  16 sequences up to 8192 tokens, 128 heads: 46.7
+// Bound and measured (bf16, R = 512).  16 sequences up to 8192 tokens, 128 heads: 42.9
 // us, where HBM needs 12.3 and the tensor cores 9.6; 64 sequences of 1 to 32768 tokens, 64
 // heads: 64.7 us, HBM 36.0; one sequence of 4096 tokens, 16 heads: 10.7 us.  A tile of 64
 // rows takes 1.85 us: the round through its two ring slots (load 1.5 us, S 0.6, softmax
 // 0.5, O 0.4, overlapping by units), not HBM (85 MB of it are read once, by the other row
 // tile from L2), with the tensor cores 35% busy.  Around the tiles: 5 us to the first
 // tile's products (launch, plan, Q and the first load), 2.4 us for the partials, and the merge,
-// 5 to 8 us, whose 22 MB come from L2.  Tried and dropped: prefetching 4 tiles ahead into
+// 3 to 6 us, whose 22 MB come from L2.  Tried and dropped: prefetching 4 tiles ahead into
 // L2 (2.5 us a tile), and pairs of CTAs that share a tile by multicast (1.65 us a tile but 2
 // us more at the start and end: 49.4 against 49.2 us).
 #pragma once
@@ -801,7 +801,9 @@ __global__ void __launch_bounds__(512, 1) latent_combine_kernel(const LatentComb
     __syncthreads();
   }
   // ---- short segments and empty sequences: CPI chunks of a row are a warp's work, 16 loads a
-  // lane in flight.  Whole rows when there are rows enough for every warp, else chunks.
+  // lane in flight.  Whole rows when there are about enough for every warp, else chunks: a
+  // row's fixed work (divisions, shuffles) is an item's (2048 rows on 2432 warps, 5 pieces
+  // each: the call 42.9 us with whole rows, 46.7 with chunks).
   auto merge_short = [&](auto cpi) {
     constexpr int CPI = decltype(cpi)::value, PARTS = NCH / CPI, KB = 16 / CPI;
     const unsigned items = (unsigned)p.B * p.rows * PARTS;
@@ -852,7 +854,7 @@ __global__ void __launch_bounds__(512, 1) latent_combine_kernel(const LatentComb
       for (int c = 0; c < CPI; ++c) put(b, row, ch + c, s[c], den);
     }
   };
-  if ((unsigned)p.B * p.rows >= gridDim.x * Cg::W)
+  if ((unsigned)p.B * p.rows * 4 >= gridDim.x * Cg::W * 3)
     merge_short(std::integral_constant<int, NCH>{});
   else
     merge_short(std::integral_constant<int, 1>{});
