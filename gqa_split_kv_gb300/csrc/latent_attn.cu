@@ -201,8 +201,8 @@ long long prefill_workspace(long long units, int max_ctx, int D, int sms) {
 
 template <int D>
 int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k, const void* k_rope, const void* v,
-                          long long token_stride, long long head_stride, long long rope_stride, int dev,
-                          cudaStream_t st) {
+                          long long token_stride, long long head_stride, long long rope_stride, int sms,
+                          int dev, cudaStream_t st) {
   using Gm = LatentPrefillGeo<D>;
   static bool done[kMaxDevices] = {false}, fits[kMaxDevices] = {false};
   if (int e = allow_smem(latent_prefill_kernel<D>, Gm::SMEM, done, dev)) return e;
@@ -247,6 +247,7 @@ int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k
   }
   const long long units = (long long)prm.nqb * prm.B * prm.H;
   if (units * prm.parts > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  prm.more = units * prm.parts > sms;  // one CTA an SM
   if (int e = launch_dependent(latent_prefill_kernel<D>, (unsigned)(units * prm.parts), Gm::NTHREADS,
                                (size_t)Gm::SMEM, st, prm))
     return e;
@@ -357,9 +358,9 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
     prm.part_ml = reinterpret_cast<float2*>(prm.part_acc + units * prm.parts * BQ * head_dim);
   }
   return head_dim == 64 ? launch_latent_prefill<64>(prm, q, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
-                                                    rope_token_stride, dev, st)
+                                                    rope_token_stride, sms, dev, st)
                         : launch_latent_prefill<128>(prm, q, k_nope, k_rope, v, kv_token_stride, kv_head_stride,
-                                                     rope_token_stride, dev, st);
+                                                     rope_token_stride, sms, dev, st);
 }
 
 extern "C" long long latent_prefill_workspace_bytes(int batch, int q_len, int num_heads, int head_dim, int max_ctx,

@@ -26,12 +26,22 @@
 // CTA's, which leaves (O, m, l) unnormalised in fp32; latent_prefill_merge joins them.  A
 // block of one part is written at once.
 //
+// More blocks than SMs: a CTA that has issued its last loads asks for the index of one that
+// has not started (clusterlaunchcontrol) and goes on with it, so the next block's queries and
+// keys load and its first scores are taken while the last one's output is written.  The launch order,
+// longest blocks first, and so the balance, stay the hardware's: 4096-token prompt, 32 heads,
+// D = 128: 131.5 us, 144.8 with a CTA a block.
+//
+// Registers: the issuing warps need 120; with 72 the spills between MMAs cost 8% (141.9
+// us), and the softmax warps need no more than 192.
+//
 // Bound by the tensor cores at the clock that the card holds under them (1.5 GHz), where a
-// tile of both query tiles takes 1.9 us, 1.7 of them its 40 MMAs.  A 4096-token prompt, 32
-// heads, D = 128: 138.5 us, the operations under the mask 87.3 at the measured peak; the
-// rest is the clock, the masked halves of diagonal tiles (3%), and 4 us at each CTA's start
-// and end, three to four CTAs an SM.  4 sequences of 500 new tokens up to 3000, 16 heads: 48.9 us, floor 13.6: 128
-// query blocks on 152 SMs, and the longest is the call's time.
+// tile of both query tiles takes 1.9 us, 1.7 of them its 40 MMAs: the prompt above is 131.5 us,
+// the operations under the mask 87.3 at the measured peak; the rest is the clock, the masked
+// halves of diagonal tiles (3%) and the start and end.  4 sequences of 500 new tokens up to 3000, 16 heads:
+// 48.2 us, floor 13.6: 128 query blocks on 152 SMs, and the longest is the call's time.
+// Tried and dropped there: all blocks on one line, cut into equal ranges (46.8 us; the merge of 37 MB
+// of pieces takes most of what the balance gives, and a prompt takes 151).
 #pragma once
 
 #include <cstdint>
@@ -52,6 +62,7 @@ struct LatentPrefillParams {
   float* part_acc;         // [unit][part][D][256]: parts' O (with more than one part)
   float2* part_ml;         // [unit][part][256], m in log2 units
   int parts, part_tiles;   // parts a unit's keys may have, key tiles a part
+  int more;                // not every CTA runs at once: CTAs take over others' indices
   int B, q_len, H, nqb;
   int grp;                 // (sequence, head) units per launch group (their K/V fit in L2 together)
   int max_len;
@@ -76,14 +87,17 @@ struct LatentPrefillGeo {
   static constexpr int NG = NG_FIT < 12 ? NG_FIT : 12;
   static constexpr int OFF_BAR = OFF_G + NG * G;
   static constexpr int BAR_FULL = 0, BAR_EMPTY = NG, BAR_S = 2 * NG, BAR_P = BAR_S + 2, BAR_O = BAR_P + 2,
-                       BAR_Q = BAR_O + 2, BAR_FIN = BAR_Q + 2, NBAR = BAR_FIN + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory base, abort flag
+                       BAR_Q = BAR_O + 2, BAR_QE = BAR_Q + 2, BAR_NEXT = BAR_QE + 2, BAR_READ = BAR_NEXT + 2, BAR_ANSWER = BAR_READ + 2,
+                       BAR_FIN = BAR_ANSWER + 1, NBAR = BAR_FIN + 1;
+  static constexpr int OFF_ANSWER = OFF_BAR + (NBAR + 1) / 2 * 16;  // to the request for a next index
+  static constexpr int OFF_PIECE = OFF_ANSWER + 16;                 // this piece and the next
+  static constexpr int OFF_MISC = OFF_PIECE + 2 * 48;               // tensor memory base, abort flag
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int TCOL_O = 2 * BK;             // S of tile t at t BK, O at TCOL_O + t D
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int NTHREADS = 128 + 128 * NQT;
   // registers after the split: producers and MMA issue, softmax
-  static constexpr int REG_LOW = 56, REG_HIGH = 216;
+  static constexpr int REG_LOW = 120, REG_HIGH = 192;
   static constexpr int REG_POOL_NEEDED = 128 * REG_LOW + 128 * NQT * REG_HIGH;
   static_assert(NG >= PER + NVG && SMEM <= 227 * 1024, "the ring holds a tile's K and two of V");
   static_assert(TCOL_O + NQT * D <= 512, "tensor memory");
@@ -96,6 +110,79 @@ __device__ __forceinline__ void latent_setmaxnreg_dec() {
 template <int N>
 __device__ __forceinline__ void latent_setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A CTA's work of one index: tiles [j0, j0 + n) of query block qb of (b, h).  Groups of grp
+// (b, h) pairs, latest query blocks (the longest) first; a unit's parts together.
+struct PrefillPiece {
+  int b, h, qb;
+  int L, nq, base, kv_end;  // length, rows, position of query token 0, keys some row sees
+  int j0, n, n_a;           // n_a: of the n tiles, those that query tile A's rows see some of
+  int slot;                 // of the part; -1: the whole block
+  int any;                  // 0: no part of this index; -1: no more pieces
+  __device__ __forceinline__ void set(const LatentPrefillParams& p, int index) volatile {
+    constexpr int BQ = 256, BK = 128;
+    if (index < 0) {
+      any = -1;
+      return;
+    }
+    const int part = index % p.parts, unit = index / p.parts;
+    const int nbh = p.B * p.H;
+    const long long per_grp = (long long)p.nqb * p.grp;
+    const int gi = (int)(unit / per_grp);
+    const int gsz = min(p.grp, nbh - gi * p.grp);
+    const int in_g = (int)(unit - gi * per_grp);
+    const int bh = gi * p.grp + in_g % gsz;
+    const int qb_ = p.nqb - 1 - in_g / gsz, b_ = bh / p.H;
+    int len = p.seq_lens ? __ldg(p.seq_lens + b_) : p.max_len;
+    len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
+    const int rows = min(BQ, p.q_len - qb_ * BQ), first = len - p.q_len;
+    const int end = max(0, min(len, first + qb_ * BQ + rows)), tiles = (end + BK - 1) / BK;
+    // equal parts of at most part_tiles
+    const int nparts = max(1, (tiles + p.part_tiles - 1) / p.part_tiles);
+    const int from = part < nparts ? (int)((long long)tiles * part / nparts) : 0;
+    const int count = part < nparts ? (int)((long long)tiles * (part + 1) / nparts) - from : 0;
+    const int end_a = max(0, min(len, first + qb_ * BQ + min(rows, BQ / 2)));
+    b = b_;
+    h = bh - b_ * p.H;
+    qb = qb_;
+    L = len;
+    nq = rows;
+    base = first;
+    kv_end = end;
+    j0 = from;
+    n = count;
+    n_a = max(0, min(count, (end_a + BK - 1) / BK - from));
+    slot = nparts == 1 ? -1 : (bh * p.nqb + qb_) * p.parts + part;
+    any = part < nparts;
+  }
+};
+
+// A CTA that has finished its own index goes on with one that has not started: it asks the
+// launch hardware to cancel a waiting CTA and takes that one's index.
+__device__ __forceinline__ void request_next(uint32_t answer, uint32_t mbar) {
+  mbar_arrive_expect_tx(mbar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(mbar)
+               : "memory");
+}
+// The index of the cancelled CTA (a grid of one dimension), or -1: none was waiting.
+__device__ __forceinline__ int next_index(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n\t"
+      ".reg .b128 a;\n\t"
+      ".reg .pred p;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t"
+      "}"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
 }
 
 template <int D>
@@ -113,37 +200,8 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float kNegInf = -__int_as_float(0x7f800000);
 
-  // work unit: groups of grp (b, h) units, latest query blocks (the longest) first; a unit's
-  // parts together
-  const int nbh = p.B * p.H;
-  const int part = blockIdx.x % p.parts, unit = blockIdx.x / p.parts;
-  const long long per_grp = (long long)p.nqb * p.grp;
-  const int gi = (int)(unit / per_grp);
-  const int gsz = min(p.grp, nbh - gi * p.grp);
-  const int in_g = (int)(unit - gi * per_grp);
-  const int qb = p.nqb - 1 - in_g / gsz;
-  const int bh = gi * p.grp + in_g % gsz;
-  const int b = bh / p.H, h = bh % p.H;
   pdl_wait_primary();  // (what precedes this call in the stream)
   pdl_launch_dependents();
-  int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len;
-  L = L < 0 ? 0 : (L > p.max_len ? p.max_len : L);
-  const int q0 = qb * Gm::BQ;
-  const int nq = min(Gm::BQ, p.q_len - q0);
-  const int nqt = nq > M ? 2 : 1;                     // query tiles with rows
-  const int base = L - p.q_len;                       // position of query token 0
-  const int kv_end = max(0, min(L, base + q0 + nq));  // keys some row sees
-  const int all_tiles = (kv_end + BK - 1) / BK;
-  // equal parts of at most part_tiles; this one's tiles
-  const int nparts = max(1, (all_tiles + p.part_tiles - 1) / p.part_tiles);
-  if (part >= nparts) return;
-  const int j0 = (int)((long long)all_tiles * part / nparts);
-  const int ntiles = (int)((long long)all_tiles * (part + 1) / nparts) - j0;
-  const bool whole = nparts == 1;
-  // query tile A's rows see up to 128 keys less than B's: its tiles of this part
-  const int end_a = max(0, min(L, base + q0 + min(nq, M)));
-  const int ntiles_a = max(0, min(ntiles, (end_a + BK - 1) / BK - j0));
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < Gm::NG; ++i) {
       mbar_init(bar(Gm::BAR_FULL + i), 1);
@@ -154,7 +212,13 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       mbar_init(bar(Gm::BAR_P + i), 4);  // one arrival a warp
       mbar_init(bar(Gm::BAR_O + i), 1);
       mbar_init(bar(Gm::BAR_Q + i), 1);
+      mbar_init(bar(Gm::BAR_QE + i), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Gm::BAR_NEXT + i), 1);
+      mbar_init(bar(Gm::BAR_READ + i), 1 + 4 * Gm::NQT);  // the issuing warp's and the softmax warps'
+    }
+    mbar_init(bar(Gm::BAR_ANSWER), 1);
     mbar_init(bar(Gm::BAR_FIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -167,12 +231,23 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
     tmem_relinquish();
   }
+  if (threadIdx.x == 64) reinterpret_cast<volatile PrefillPiece*>(smem + Gm::OFF_PIECE)->set(p, blockIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MISC);
   auto wait = [&](int i, int phase) { return wait_bounded(bar(i), (uint32_t)(phase & 1), abort_flag, p.timeout_ns); };
-  // granule g of tile j: K columns 0 .. NKG - 1, then V
+  // The pieces a CTA works through: its own index's, then those of the indices it takes over.
+  // Piece k lies in buffer k & 1; the producer writes piece k + 1 there when every role has
+  // left piece k - 1.
+  volatile PrefillPiece* pieces = reinterpret_cast<volatile PrefillPiece*>(smem + Gm::OFF_PIECE);
+  auto leave = [&](int k) {  // whole warps: piece k is done; true when there is another
+    __syncwarp();
+    if (!p.more) return false;
+    if (lane == 0) mbar_arrive(bar(Gm::BAR_READ + (k & 1)));
+    return __all_sync(0xffffffffu, wait(Gm::BAR_NEXT + ((k + 1) & 1), k >> 1)) && pieces[(k + 1) & 1].any >= 0;
+  };
+  // granule g of the CTA's tile j (counted over its pieces): K columns 0 .. NKG - 1, then V
   auto slot_of = [&](int j, int g) { return (j * Gm::PER + g) % Gm::NG; };
   auto fill_of = [&](int j, int g) { return (j * Gm::PER + g) / Gm::NG; };
   auto addr_of = [&](int j, int g) { return sbase + Gm::OFF_G + (uint32_t)(slot_of(j, g) * Gm::G); };
@@ -185,33 +260,59 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       // granule m - NG is by its slot's phase, whose next one needs granule m.
       if (lane == 0) {
         bool ok = true;
-        int last = -1;
-        // query tiles, [W / 64][M][64] each; zeros past q_len
-        for (int t = 0; t < nqt && ntiles > 0; ++t) {
-          mbar_arrive_expect_tx(bar(Gm::BAR_Q + t), Gm::QT_BYTES);
-          tma_load_5d(sbase + Gm::OFF_Q + t * Gm::QT_BYTES, &p.tm_q, bar(Gm::BAR_Q + t), 0, q0 + t * M, 0, h, b);
-        }
-        for (int j = 0; j < ntiles && ok; ++j) {
-          const int t = (j0 + j) * BK;
-#pragma unroll 1
-          for (int g = 0; g < Gm::PER; ++g) {
-            const int fill = fill_of(j, g), slot = slot_of(j, g);
-            if (fill > 0 && !(ok = wait(Gm::BAR_EMPTY + slot, fill - 1))) break;
-            const uint32_t full = bar(Gm::BAR_FULL + slot);
-            mbar_arrive_expect_tx(full, Gm::G);
-            if (g < Gm::NKG - 1)
-              tma_load_5d(addr_of(j, g), &p.tm_k, full, 0, t, g, h, b);
-            else if (g == Gm::NKG - 1)
-              tma_load_3d(addr_of(j, g), &p.tm_pe, full, 0, t, b);
-            else
-              tma_load_5d(addr_of(j, g), &p.tm_v, full, 0, t + (g - Gm::NKG) * Gm::VKEYS, 0, h, b);
-            last = j * Gm::PER + g;
+        int last = -1, tiles = 0, fills[2] = {0, 0};  // of the pieces before
+        bool waiting = false;  // for a request's answer
+        int k = 0;
+        do {
+          volatile PrefillPiece& pc = pieces[k & 1];
+          const int b = pc.b, h = pc.h, n = pc.n, nqt = pc.nq > M ? 2 : 1, q0 = pc.qb * Gm::BQ, j0 = pc.j0;
+          // query tiles, [W / 64][M][64] each; zeros past q_len
+          for (int t = 0; t < nqt && n > 0; ++t) {
+            if (fills[t] > 0 && !(ok = wait(Gm::BAR_QE + t, fills[t] - 1))) break;
+            ++fills[t];
+            mbar_arrive_expect_tx(bar(Gm::BAR_Q + t), Gm::QT_BYTES);
+            tma_load_5d(sbase + Gm::OFF_Q + t * Gm::QT_BYTES, &p.tm_q, bar(Gm::BAR_Q + t), 0, q0 + t * M, 0, h, b);
           }
-        }
+          for (int j = 0; j < n && ok; ++j) {
+            const int t = (j0 + j) * BK;
+#pragma unroll 1
+            for (int g = 0; g < Gm::PER; ++g) {
+              const int fill = fill_of(tiles + j, g), slot = slot_of(tiles + j, g);
+              if (fill > 0 && !(ok = wait(Gm::BAR_EMPTY + slot, fill - 1))) break;
+              const uint32_t full = bar(Gm::BAR_FULL + slot);
+              mbar_arrive_expect_tx(full, Gm::G);
+              if (g < Gm::NKG - 1)
+                tma_load_5d(addr_of(tiles + j, g), &p.tm_k, full, 0, t, g, h, b);
+              else if (g == Gm::NKG - 1)
+                tma_load_3d(addr_of(tiles + j, g), &p.tm_pe, full, 0, t, b);
+              else
+                tma_load_5d(addr_of(tiles + j, g), &p.tm_v, full, 0, t + (g - Gm::NKG) * Gm::VKEYS, 0, h, b);
+              last = (tiles + j) * Gm::PER + g;
+            }
+          }
+          tiles += n;
+          if (!ok || !p.more) break;
+          // asked only now, with this piece's loads issued: a CTA that asks at its start takes
+          // over indices whose SM is about to be free
+          const uint32_t answer = sbase + Gm::OFF_ANSWER;
+          request_next(answer, bar(Gm::BAR_ANSWER));
+          waiting = true;
+          if (!(ok = wait(Gm::BAR_ANSWER, k))) break;
+          waiting = false;
+          if (k > 0 && !(ok = wait(Gm::BAR_READ + ((k + 1) & 1), (k - 1) >> 1))) break;
+          ++k;
+          pieces[k & 1].set(p, next_index(answer));
+          fence_proxy_async_smem();  // the answer is read before another is asked for
+          mbar_arrive(bar(Gm::BAR_NEXT + (k & 1)));
+        } while (pieces[k & 1].any >= 0);
         if (*abort_flag) {  // copies in flight land before the CTA exits
           const uint64_t t0 = globaltimer_ns();
-          for (int t = 0; t < nqt && ntiles > 0; ++t)
-            while (!mbar_try_wait(bar(Gm::BAR_Q + t), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+          while (waiting && !mbar_try_wait(bar(Gm::BAR_ANSWER), (uint32_t)(k & 1)) &&
+                 globaltimer_ns() - t0 < p.timeout_ns) {
+          }
+          for (int t = 0; t < 2; ++t)
+            while (fills[t] > 0 && !mbar_try_wait(bar(Gm::BAR_Q + t), (uint32_t)((fills[t] - 1) & 1)) &&
+                   globaltimer_ns() - t0 < p.timeout_ns) {
             }
           for (int m = last; m >= 0 && m > last - Gm::NG; --m)
             while (!mbar_try_wait(bar(Gm::BAR_FULL + m % Gm::NG), (uint32_t)((m / Gm::NG) & 1)) &&
@@ -223,42 +324,45 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
       // ---- MMA issue (one lane); the warp zeroes V rows past the keys of the last tile
       constexpr uint32_t id_s = tc_idesc_bf16(M, BK, false, false);
       constexpr uint32_t id_o = tc_idesc_bf16(M, D, false, true);
+      int nqt = 1, tiles = 0, kv_end = 0, j0 = 0;  // query tiles with rows; tiles of the pieces before
       auto wait_all = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)) != 0; };
       // granules [g0, g1) of tile j have landed (query tile A waits for both)
       auto landed = [&](int j, int g0, int g1) {
         bool there = true;
-        for (int g = g0; g < g1; ++g) there = wait(Gm::BAR_FULL + slot_of(j, g), fill_of(j, g)) && there;
+        for (int g = g0; g < g1; ++g) there = wait(Gm::BAR_FULL + slot_of(tiles + j, g), fill_of(tiles + j, g)) && there;
         return __all_sync(0xffffffffu, there) != 0;
       };
-      // one thread: S_t = Q_t K_j^T; the granules are freed after the last query tile
-      auto issue_qk = [&](int t, int j) {
+      // one thread: S_t = Q_t K_j^T; the granules are freed after the last query tile, the
+      // queries after the piece's last tile
+      auto issue_qk = [&](int t, int j, bool last) {
 #pragma unroll
         for (int g = 0; g < Gm::NKG; ++g) {
           const uint64_t da = tc_sdesc(sbase + Gm::OFF_Q + t * Gm::QT_BYTES + g * (M * 128), 16, 1024, kTcSwizzle128B);
-          const uint64_t db = tc_sdesc(addr_of(j, g), 16, 1024, kTcSwizzle128B);
+          const uint64_t db = tc_sdesc(addr_of(tiles + j, g), 16, 1024, kTcSwizzle128B);
 #pragma unroll
           for (int i = 0; i < 4; ++i) tc_mma_ss(tmem + t * BK, da + 2 * i, db + 2 * i, id_s, g > 0 || i > 0);
-          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, g)));
+          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(tiles + j, g)));
         }
         tc_commit(bar(Gm::BAR_S + t));
+        if (last) tc_commit(bar(Gm::BAR_QE + t));
       };
       // one thread: O_t += P_t V_j with P_t from the S buffer
       auto issue_pv = [&](int t, int j) {
 #pragma unroll
         for (int g = 0; g < Gm::NVG; ++g) {
-          const uint64_t db = tc_sdesc(addr_of(j, Gm::NKG + g), Gm::VKEYS * 128, 1024, kTcSwizzle128B);
+          const uint64_t db = tc_sdesc(addr_of(tiles + j, Gm::NKG + g), Gm::VKEYS * 128, 1024, kTcSwizzle128B);
 #pragma unroll
           for (int i = 0; i < Gm::VKEYS / 16; ++i)
             tc_mma_ts(tmem + Gm::TCOL_O + t * D, tmem + t * BK + 8 * (g * (Gm::VKEYS / 16) + i), db + i * 128, id_o,
                       j > 0 || g > 0 || i > 0);
-          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, Gm::NKG + g)));
+          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(tiles + j, Gm::NKG + g)));
         }
       };
       // V rows at or past kv_end may hold anything (0 * NaN would poison O): zero them
       auto zero_tail = [&](int j) {
         for (int g = 0; g < Gm::NVG; ++g) {
           const int r0 = max(0, kv_end - ((j0 + j) * BK + g * Gm::VKEYS));
-          uint8_t* vs = smem + Gm::OFF_G + slot_of(j, Gm::NKG + g) * Gm::G;
+          uint8_t* vs = smem + Gm::OFF_G + slot_of(tiles + j, Gm::NKG + g) * Gm::G;
           for (int e = r0 * 8 + lane; e < Gm::VKEYS * 8; e += 32)
             for (int c = 0; c < D / 64; ++c)
               *reinterpret_cast<uint4*>(vs + c * (Gm::VKEYS * 128) + swz<128>(e / 8, e % 8)) =
@@ -267,60 +371,74 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
-      bool ok = ntiles > 0 && wait_all(Gm::BAR_Q, 0) && landed(0, 0, Gm::NKG);
-      if (ok) {
-        if (ntiles_a > 0 && elect_one()) {
+      bool ok = true;
+      int fills[2] = {0, 0}, done[2] = {0, 0};  // pieces and key tiles of each query tile so far
+      int k = 0;
+      do {
+        volatile PrefillPiece& pc = pieces[k & 1];
+        if (pc.n == 0) continue;
+        const int ntiles = pc.n, ntiles_a = pc.n_a;
+        nqt = pc.nq > M ? 2 : 1;
+        kv_end = pc.kv_end;
+        j0 = pc.j0;
+        ok = wait_all(Gm::BAR_Q, fills[0]++) && landed(0, 0, Gm::NKG);
+        if (!ok) break;
+        if (elect_one()) {
           tc_fence_after();
-          issue_qk(0, 0);
+          if (ntiles_a > 0)
+            issue_qk(0, 0, ntiles_a == 1);
+          else
+            tc_commit(bar(Gm::BAR_QE));
         }
         __syncwarp();
         if (nqt == 2) {
-          ok = wait_all(Gm::BAR_Q + 1, 0);
-          if (ok && elect_one()) {
-            tc_fence_after();
-            issue_qk(1, 0);
-          }
-          __syncwarp();
-        }
-      }
-      for (int j = 0; j < ntiles && ok; ++j) {
-        const bool more = j + 1 < ntiles;
-        // A: P_A V_j, then S_A of tile j + 1 once its keys are there
-        ok = landed(j, Gm::NKG, Gm::PER);
-        if (!ok) break;
-        if ((j0 + j + 1) * BK > kv_end) zero_tail(j);
-        if (j < ntiles_a) {
-          if (!(ok = wait_all(Gm::BAR_P, j))) break;
+          if (!(ok = wait_all(Gm::BAR_Q + 1, fills[1]++))) break;
           if (elect_one()) {
             tc_fence_after();
-            issue_pv(0, j);
-            if (j + 1 == ntiles_a) tc_commit(bar(Gm::BAR_O));
+            issue_qk(1, 0, ntiles == 1);
           }
           __syncwarp();
         }
-        if (more) {
-          if (!(ok = landed(j + 1, 0, Gm::NKG))) break;
-          if (j + 1 < ntiles_a && elect_one()) {
-            tc_fence_after();
-            issue_qk(0, j + 1);
+        for (int j = 0; j < ntiles && ok; ++j) {
+          const bool more = j + 1 < ntiles;
+          // A: P_A V_j, then S_A of tile j + 1 once its keys are there
+          ok = landed(j, Gm::NKG, Gm::PER);
+          if (!ok) break;
+          if ((j0 + j + 1) * BK > kv_end) zero_tail(j);
+          if (j < ntiles_a) {
+            if (!(ok = wait_all(Gm::BAR_P, done[0]++))) break;
+            if (elect_one()) {
+              tc_fence_after();
+              issue_pv(0, j);
+              if (j + 1 == ntiles_a) tc_commit(bar(Gm::BAR_O));
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        if (nqt == 2) {  // B: the same tiles
-          if (!(ok = wait_all(Gm::BAR_P + 1, j))) break;
-          if (elect_one()) {
-            tc_fence_after();
-            issue_pv(1, j);
-            if (more)
-              issue_qk(1, j + 1);
-            else
-              tc_commit(bar(Gm::BAR_O + 1));
+          if (more) {
+            if (!(ok = landed(j + 1, 0, Gm::NKG))) break;
+            if (j + 1 < ntiles_a && elect_one()) {
+              tc_fence_after();
+              issue_qk(0, j + 1, j + 2 == ntiles_a);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (nqt == 2) {  // B: the same tiles
+            if (!(ok = wait_all(Gm::BAR_P + 1, done[1]++))) break;
+            if (elect_one()) {
+              tc_fence_after();
+              issue_pv(1, j);
+              if (more)
+                issue_qk(1, j + 1, j + 2 == ntiles);
+              else
+                tc_commit(bar(Gm::BAR_O + 1));
+            }
+            __syncwarp();
+          }
         }
-      }
+        tiles += ntiles;
+      } while (ok && leave(k++));
       // before the tensor memory is freed, every MMA issued must have completed
-      if (ntiles > 0 && elect_one()) {
+      if (fills[0] > 0 && elect_one()) {
         tc_commit(bar(Gm::BAR_FIN));
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(bar(Gm::BAR_FIN), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
@@ -332,22 +450,26 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     // ---- softmax and epilogue of query tile qt: one thread per row (tensor memory lane)
     latent_setmaxnreg_inc<Gm::REG_HIGH>();
     const int qt = (warp >> 2) - 1;
-    const int nt = qt == 0 ? ntiles_a : ntiles;  // this query tile's key tiles
     const int row = lane + 32 * (warp & 3);
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-    const int tok = qt * M + row;  // this row's token within the block
-    const bool has_row = tok < nq;
-    const int lim = has_row ? max(0, min(L, base + q0 + tok + 1)) : 0;  // keys this row sees
-    const int lim_first = max(0, min(L, base + q0 + qt * M + 1));       // keys every row of the tile sees
     const uint32_t o_addr = tmem + lane_addr + Gm::TCOL_O + qt * D;
     const uint32_t s_addr = tmem + lane_addr + qt * BK;
+    const int tok = qt * M + row;               // this row's token within the block
     const bool fold = p.scale_log2 > 0.f;  // a positive scale goes into the exponent's fma
     const float sc = fold ? p.scale_log2 : 1.f;
-    float m = kNegInf, l = 0.f;
     bool ok = true;
-    if (qt < nqt) {
+    int done = 0, ends = 0;  // key tiles, and pieces that had some, so far
+    int k = 0;
+    do {
+      volatile PrefillPiece& pc = pieces[k & 1];
+      if (!pc.any || (qt > 0 && pc.nq <= M)) continue;  // no rows
+      const int j0 = pc.j0, q0 = pc.qb * Gm::BQ;
+      const int nt = qt == 0 ? pc.n_a : pc.n;           // this query tile's key tiles
+      const int lim = tok < pc.nq ? max(0, min(pc.L, pc.base + q0 + tok + 1)) : 0;  // keys this row sees
+      const int lim_first = max(0, min(pc.L, pc.base + q0 + qt * M + 1));       // keys every row of the tile sees
+      float m = kNegInf, l = 0.f;
       for (int j = 0; j < nt; ++j) {
-        ok = __all_sync(0xffffffffu, wait(Gm::BAR_S + qt, j));
+        ok = __all_sync(0xffffffffu, wait(Gm::BAR_S + qt, done++));
         if (!ok) break;
         tc_fence_after();
         float x[BK];
@@ -432,12 +554,13 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
         if (lane == 0) mbar_arrive(bar(Gm::BAR_P + qt));
       }
       // ---- normalise and write the tile's rows (a row that saw nothing: zeros)
-      if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + qt, 0));
+      if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + qt, ends++));
       if (ok) {
         tc_fence_after();
+        const bool has_row = tok < pc.nq, whole = pc.slot < 0;
         if (!whole) {
           // the part as it is, [D][256]: 32 lanes store 32 rows of a column
-          const size_t slot = ((size_t)bh * p.nqb + qb) * p.parts + part;
+          const size_t slot = (size_t)pc.slot;
           float* acc = p.part_acc + slot * D * Gm::BQ + tok;
 #pragma unroll 1
           for (int c0 = 0; c0 < D && nt > 0; c0 += 32) {  // (l is 0 with no tile, and nothing else read)
@@ -450,7 +573,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           p.part_ml[slot * Gm::BQ + tok] = make_float2(m, l);
         }
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        __nv_bfloat16* dst = p.out + (((size_t)b * p.q_len + q0 + tok) * p.H + h) * D;
+        __nv_bfloat16* dst = p.out + (((size_t)pc.b * p.q_len + pc.qb * Gm::BQ + tok) * p.H + pc.h) * D;
 #pragma unroll 1
         for (int c0 = 0; c0 < D && whole; c0 += 32) {
           uint32_t r[32];
@@ -472,7 +595,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           }
         }
       }
-    }
+    } while (ok && leave(k++));
   }
   tc_fence_before();
   __syncthreads();

@@ -96,6 +96,28 @@ def test_keys_split_over_parts(D, H, q_len):
     assert np.array_equal(run(c), first)
 
 
+@pytest.mark.parametrize("D,H,q_len,lens", [(128, 24, 520, [520, 77, 0, 600]), (64, 40, 300, [300, 0, 512, 130, 700]),
+                                            (128, 200, 1, [1, 129]), (64, 320, 3, [2])])
+def test_more_blocks_than_multiprocessors(D, H, q_len, lens):
+    """CTAs that go on with other CTAs' blocks: blocks of one row tile after two, of one key tile, of none."""
+    assert len(lens) * H * -(-q_len // 256) > 152
+    c = make(D + H, lens, q_len, H, D, max(lens) + 5)
+    first = run(c)
+    check(first, c, "blocks")
+    args = (dev_bf16(c["q"]), dev_bf16(c["k"]), dev_bf16(c["pe"]), dev_bf16(c["v"]), dev_i32(c["lens"]))
+    outs = [torch.full((*args[0].shape[:3], D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):  # calls in a row: one's last blocks beside the next one's first
+        for out in outs[:3]:
+            binding.latent_prefill_contig(*args, scale=c["scale"], out=out)
+    graph.replay()
+    binding.latent_prefill_contig(*args, scale=c["scale"], out=outs[3])
+    torch.cuda.synchronize()
+    assert binding.device_error() == 0
+    for out in outs:
+        assert np.array_equal(host_bits(out), first)
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 0.6])
 def test_any_scale(scale):
     c = make(9, [400, 200], 200, 2, 128, 400)
