@@ -307,6 +307,13 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
   return slab_index * p.slab + in_slab;
 }
 
+// The larger one; NaN when either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // A CTA takes tb new tokens at a time.  A row (token, tensor, head) of D elements has
 // `lanes` lanes of one warp, CPL chunks of 8 elements each.  K rows are rotated in fp32
 // on the way (a half-layout lane also loads the chunk with the other halves of its
@@ -318,10 +325,11 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
 // them here: 33 instructions an element, a third of them the cosines and the rows' fixed
 // work, and 1.7 rounds of CTAs).
 constexpr int kMaxTokens = 16;  // tokens a CTA takes at a time, at most
-template <bool PAGED, bool INT8, int CPL>
+template <bool PAGED, bool INT8, int CPL, bool PAIRED>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p) {
   extern __shared__ __align__(16) uint8_t rope_smem[];
-  __shared__ long long tok_row[kMaxTokens], tok_scale[kMaxTokens];  // cache row, or -1; its first head's scale
+  // where a token's first head begins in the cache, or -1; its first head's scale
+  __shared__ long long tok_at[kMaxTokens], tok_scale[kMaxTokens];
   const int np = p.r.inv_freq ? p.r.rot / 2 : 0;
   unsigned long long* step = reinterpret_cast<unsigned long long*>(rope_smem);
   float2* cs = reinterpret_cast<float2*>(step + np);  // [tb][np] (np a multiple of 8)
@@ -338,22 +346,28 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
   pdl_launch_dependents();
   pdl_wait_primary();
   bool first = true;
-  // every lane of a warp runs the same number of rounds (the shuffles need them all)
+  // every lane of a warp runs the same number of rounds (the shuffles need them all); a
+  // thread's rows and cosines are the same of every tb tokens, and the next ones a fixed step on
   const int per_round = kThreads / p.lanes;
+  const int row0 = threadIdx.x / p.lanes, ti0 = row0 / rows_per_token, in0 = row0 - ti0 * rows_per_token;
+  const int dti = per_round / rows_per_token, din = per_round - dti * rows_per_token;
+  const int ci0 = np ? threadIdx.x / np : 0, cj0 = threadIdx.x - ci0 * np;
+  const int dci = np ? kThreads / np : 0, dcj = kThreads - dci * np;
   for (unsigned g0 = blockIdx.x * p.tb; g0 < total; g0 += gridDim.x * p.tb) {
-    for (int r0 = 0; r0 < rows; r0 += per_round) {
-      const int row = r0 + threadIdx.x / p.lanes;
-      const int ti = row / rows_per_token, in_token = row - ti * rows_per_token;
+    int ti = ti0, in_token = in0;
+    for (int r0 = 0; r0 < rows; r0 += per_round, ti += dti, in_token += din) {
+      if (in_token >= rows_per_token) {
+        in_token -= rows_per_token;
+        ++ti;
+      }
       const bool is_v = in_token >= p.Hkv;
       const int h = is_v ? in_token - p.Hkv : in_token;
       const unsigned g = g0 + ti;
-      const bool there = row < rows && g < total;
+      const bool there = ti < p.tb && g < total;
       // the row's elements do not depend on its place, so their loads go out first
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) +
-                                 (there ? g * (is_v ? p.v_stride : p.k_stride) + (long long)h * p.D : 0);
+                                 (there ? g * (is_v ? p.v_stride : p.k_stride) + h * p.D : 0);
       const bool rotates = np && !is_v;
-      // the halves of a pair are one lane's two chunks (a fully rotated head of 2 chunks a lane)
-      const bool paired = CPL == 2 && !p.r.interleaved && np == 8 * p.lanes && p.r.offset == 0;
       uint4 raw[CPL], other[CPL];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
         if (there && ch < nchunk) {
           raw[c] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
           const int at = ch * 8 - p.r.offset;  // within the rotated part
-          if (rotates && !p.r.interleaved && !paired && at >= 0 && at < p.r.rot)  // the other halves of these pairs
+          if (!PAIRED && rotates && !p.r.interleaved && at >= 0 && at < p.r.rot)  // the other halves of these pairs
             other[c] = __ldg(reinterpret_cast<const uint4*>(src + p.r.offset + (at >= np ? at - np : at + np)));
         }
       }
@@ -382,21 +396,25 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
             else if (pos >= 0)
               place = cache_row<PAGED>(p, b, (int)pos, slab, in_slab);
           }
-          tok_row[helper] = place;
+          tok_at[helper] = place < 0 ? -1 : place * p.Hkv * p.D;
           tok_scale[helper] = slab * p.Hkv * p.slab + in_slab;
         }
-        for (int e = threadIdx.x, i = e / max(np, 1); e < p.tb * np; e += kThreads, i = e / np) {
+        for (int i = ci0, j = cj0; i < p.tb && np; i += dci, j += dcj) {
+          if (j >= np) {
+            j -= np;
+            if (++i >= p.tb) break;
+          }
           int b;
-          if (g0 + i < total) cs[e] = rope_cos_sin(step[e - i * np], (int)position(g0 + i, b), p.r);
+          if (g0 + i < total) cs[i * np + j] = rope_cos_sin(step[j], (int)position(g0 + i, b), p.r);
         }
         __syncthreads();
       }
-      const long long dst = there ? tok_row[ti] : -1;
+      const long long dst = there ? tok_at[ti] : -1;
       float x[CPL][8];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
         Chunk<__nv_bfloat16>::unpack(raw[c], x[c]);
-        if (paired) continue;
+        if (PAIRED) continue;
         const int at = (gl + c * p.lanes) * 8 - p.r.offset;
         if (rotates && there && at >= 0 && at < p.r.rot) {
           const float2* w = cs + ti * np;
@@ -412,18 +430,19 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
           }
         }
       }
-      if (CPL == 2 && paired && rotates && there) rotate_half(x[0], x[CPL - 1], cs + ti * np, gl * 8);
+      if (PAIRED && rotates && there) rotate_half(x[0], x[CPL - 1], cs + ti * np, gl * 8);
       if constexpr (INT8) {
-        // The largest magnitude by its bits, whose order is that of the magnitudes, with
+        // The largest magnitude, then by its bits, whose order is that of the magnitudes, with
         // infinity and the NaNs above them: a row with any of those gets a NaN scale and zeros.
-        unsigned bits = 0;
+        float top = 0.f;
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) bits = max(bits, __float_as_uint(x[c][i]) & 0x7fffffffu);
+          for (int i = 0; i < 8; ++i) top = max_or_nan(top, fabsf(x[c][i]));
+        unsigned bits = __float_as_uint(top) & 0x7fffffffu;
         for (int o = p.lanes / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
         const bool finite = bits < 0x7f800000u;
-        const float top = __uint_as_float(bits);
+        top = __uint_as_float(bits);
         // 127 2^-126 and less would leave a scale below the normal numbers: floor it
         float scale = bits ? fmaxf(__fdiv_rn(top, 127.f), 1.17549435e-38f) : 1.f;
         // x / scale, rounded as a division is: a quotient from the rounded reciprocal and one
@@ -432,7 +451,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
         const float inv = __frcp_rn(scale);
         if (!finite) scale = __int_as_float(0x7fffffff);
         if (dst >= 0) {
-          int8_t* q = static_cast<int8_t*>(is_v ? p.v : p.k) + (dst * p.Hkv + h) * p.D;
+          int8_t* q = static_cast<int8_t*>(is_v ? p.v : p.k) + dst + h * p.D;
 #pragma unroll
           for (int c = 0; c < CPL; ++c) {
             const int ch = gl + c * p.lanes;
@@ -452,11 +471,11 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
           if (gl == 0) (is_v ? p.vs : p.ks)[tok_scale[ti] + (long long)h * p.slab] = scale;
         }
       } else if (dst >= 0) {
-        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) + (dst * p.Hkv + h) * p.D;
+        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) + dst + h * p.D;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
           const int ch = gl + c * p.lanes;
-          if (ch < nchunk) *reinterpret_cast<uint4*>(q + ch * 8) = Chunk<__nv_bfloat16>::pack(x[c]);
+          if (ch < nchunk) *reinterpret_cast<uint4*>(q + ch * 8) = rotates ? Chunk<__nv_bfloat16>::pack(x[c]) : raw[c];
         }
       }
     }
@@ -561,9 +580,12 @@ int launch_write(CacheParams& p, int sms, cudaStream_t st) {
   const long long blocks = (total + p.tb - 1) / p.tb, cap = 8LL * sms;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const size_t smem = (size_t)np * 8 * (1 + p.tb);
-  if (cpl == 1) return launch_dependent(kv_write_kernel<PAGED, INT8, 1>, grid, kThreads, smem, st, p);
-  if (cpl == 2) return launch_dependent(kv_write_kernel<PAGED, INT8, 2>, grid, kThreads, smem, st, p);
-  return launch_dependent(kv_write_kernel<PAGED, INT8, 4>, grid, kThreads, smem, st, p);
+  // no rotation, or the halves of every pair are one lane's two chunks
+  const bool paired = cpl == 2 && (np == 0 || (!p.r.interleaved && np == 8 * p.lanes && p.r.offset == 0));
+  if (paired) return launch_dependent(kv_write_kernel<PAGED, INT8, 2, true>, grid, kThreads, smem, st, p);
+  if (cpl == 1) return launch_dependent(kv_write_kernel<PAGED, INT8, 1, false>, grid, kThreads, smem, st, p);
+  if (cpl == 2) return launch_dependent(kv_write_kernel<PAGED, INT8, 2, false>, grid, kThreads, smem, st, p);
+  return launch_dependent(kv_write_kernel<PAGED, INT8, 4, false>, grid, kThreads, smem, st, p);
 }
 
 int write_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t st) {
