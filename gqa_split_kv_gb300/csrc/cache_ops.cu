@@ -321,9 +321,9 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
 // once.  The row's maximum is a shuffle over its lanes.  Bound by HBM for a chunk and by
 // latency for a step: the first rows' loads go out before the lengths, pages and cosines,
 // which are looked up once a token.  A decode step of 64 sequences (8 heads x 128, int8 pages)
-// with its read back: 5.9 us, two launches; 4096 tokens likewise 20.3 us, floor 7.6 (12 of
-// them here: 33 instructions an element, a third of them the cosines and the rows' fixed
-// work, and 1.7 rounds of CTAs).
+// with its read back: 5.9 us, two launches; 4096 tokens likewise 19.4 us, floor 7.6; 32768
+// tokens 49.3 us here, floor 30.4 (bf16 48.0, 40.1), where four-chunk rows take 22 instructions an element
+// and one-chunk rows took 31.
 constexpr int kMaxTokens = 16;  // tokens a CTA takes at a time, at most
 template <bool PAGED, bool INT8, int CPL, bool PAIRED>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p) {
@@ -430,7 +430,10 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
           }
         }
       }
-      if (PAIRED && rotates && there) rotate_half(x[0], x[CPL - 1], cs + ti * np, gl * 8);
+      if (PAIRED && rotates && there)
+#pragma unroll
+        for (int c = 0; c < CPL / 2; ++c)
+          rotate_half(x[c], x[c + CPL / 2], cs + ti * np, (gl + c * p.lanes) * 8);
       if constexpr (INT8) {
         // The largest magnitude, then by its bits, whose order is that of the magnitudes, with
         // infinity and the NaNs above them: a row with any of those gets a NaN scale and zeros.
@@ -560,14 +563,20 @@ int check_cache_pointers(const CacheParams& p, bool paged, bool int8, bool has_v
 
 template <bool PAGED, bool INT8>
 int launch_write(CacheParams& p, int sms, cudaStream_t st) {
-  // two chunks a lane where tokens abound (fewer lanes share a row's fixed work: 4096 tokens
-  // x 8 heads x 128 written and read back, 28.8 -> 25.3 us), one for a step's few (more
-  // loads at once)
+  // Few rows: a chunk a lane, for more loads at once.  Many (20 an SM): two chunks, and int8
+  // four where the 16 tokens of a CTA still occupy it, as a row's fixed work is a lane's (8 heads x 128,
+  // int8 / bf16, us: 128 tokens 3.1 / 2.9, 3.4 / 2.8 with more chunks; 256 tokens 4.6 / 3.9 -> 3.5 /
+  // 2.8; 32768 tokens int8 56.7 with two, 49.4 with four, where bf16 takes 48.0 and 51.0)
   const int nchunk = p.D / 8;
-  const int cpl = nchunk > 64 ? 4 : nchunk > 32 || (nchunk > 1 && (long long)p.B * p.n >= 8LL * sms) ? 2 : 1;
+  const int rows = p.Hkv * (p.v_new ? 2 : 1), np = p.r.inv_freq ? p.r.rot / 2 : 0;
+  const bool many = (long long)p.B * p.n * rows >= 20LL * sms;
+  int cpl = nchunk > 64 ? 4 : nchunk > 32 || (nchunk > 1 && many) ? 2 : 1;
+  // no rotation, or pairs whose halves a lane with an even number of chunks holds both
+  bool paired = np == 0 || (!p.r.interleaved && p.r.offset == 0 && p.r.rot == p.D);
+  if (INT8 && paired && many && (nchunk == 16 || nchunk == 32) && rows * (nchunk / 4) * kMaxTokens >= kThreads) cpl = 4;
   p.lanes = 1;
   while (p.lanes * cpl < nchunk && p.lanes < 32) p.lanes *= 2;
-  const int rows = p.Hkv * (p.v_new ? 2 : 1), np = p.r.inv_freq ? p.r.rot / 2 : 0;
+  paired = paired && (cpl == 2 || (INT8 && cpl == 4)) && (np == 0 || p.lanes * cpl == nchunk);
   // enough tokens that every lane has a row, four rounds of them where tokens abound (the
   // cosines then take every thread), as long as the cosines fit
   const long long total = (long long)p.B * p.n;
@@ -580,8 +589,8 @@ int launch_write(CacheParams& p, int sms, cudaStream_t st) {
   const long long blocks = (total + p.tb - 1) / p.tb, cap = 8LL * sms;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const size_t smem = (size_t)np * 8 * (1 + p.tb);
-  // no rotation, or the halves of every pair are one lane's two chunks
-  const bool paired = cpl == 2 && (np == 0 || (!p.r.interleaved && np == 8 * p.lanes && p.r.offset == 0));
+  if constexpr (INT8)
+    if (paired && cpl == 4) return launch_dependent(kv_write_kernel<PAGED, INT8, 4, true>, grid, kThreads, smem, st, p);
   if (paired) return launch_dependent(kv_write_kernel<PAGED, INT8, 2, true>, grid, kThreads, smem, st, p);
   if (cpl == 1) return launch_dependent(kv_write_kernel<PAGED, INT8, 1, false>, grid, kThreads, smem, st, p);
   if (cpl == 2) return launch_dependent(kv_write_kernel<PAGED, INT8, 2, false>, grid, kThreads, smem, st, p);

@@ -316,6 +316,24 @@ def test_write_int8_special_rows():
     check_write(c, got, scales)
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("H,D,n", [(8, 128, 190), (4, 256, 400), (4, 192, 500), (12, 64, 150), (1, 256, 1700)])
+def test_write_many_rows_whole_heads(int8, H, D, n):
+    """Rows enough for two or four chunks a lane, whole heads rotated or none, rows with infinities and NaN among them."""
+    lens = [n + 3, n - 1]
+    c = write_case(D + n, 2, n, H, D, lens, n + 9, 0, int8)
+    w = freqs(D)
+    got, scales = run_write(c, w)
+    check_write(c, got, scales, w)
+    if int8:
+        c["new"] = [x.copy() for x in c["new"]]
+        for x in c["new"]:
+            x[0, ::37, 0, D - 1], x[1, ::41, H - 1, 3], x[1, 5] = 0x7F80, 0x7FC0, 0
+    got, scales = run_write(c)
+    check_write(c, got, scales)
+    assert binding.device_error() == 0
+
+
 def test_write_from_a_fused_projection():
     gen = torch.Generator(device="cuda").manual_seed(4)
     B, n, Hq, H, D = 2, 5, 4, 2, 64
