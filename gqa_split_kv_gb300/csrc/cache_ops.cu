@@ -38,6 +38,7 @@ struct RopeApplyParams {
   int H, D;
   long long xt, xh, ot, oh;  // strides in elements
   int copy;                  // out is not x: elements outside the rotated part are copied
+  int tb;                    // tokens a CTA takes at a time
 };
 
 template <typename T>
@@ -138,17 +139,17 @@ __device__ __forceinline__ void rotate_neighbours(float (&a)[V], const float2* c
   }
 }
 
-// One CTA a token at a time: its rot / 2 cosines and sines go to shared memory once
-// and serve every head.  VECTOR: all offsets and strides are whole 16-byte chunks; an
-// item is a chunk (interleaved: whole pairs; a copy) or the two chunks that hold the
-// halves of the same pairs.  Otherwise an item is one pair or one copied element.
+// A CTA takes one token at a time (MANY: tb tokens): their rot / 2 cosines and sines go
+// to shared memory once and serve every head.  VECTOR: all offsets and strides are whole
+// 16-byte chunks; an item is a chunk (interleaved: whole pairs; a copy) or the two chunks
+// that hold the halves of the same pairs.  Otherwise an item is one pair or one copied element.
 //
 // Bound by HBM (read and write once).  A thread's loads of the first U items go out
 // before the position is known: with them after the cosines, a token takes two memory
-// latencies and the sines in a row (4096 tokens x 32 heads x 128 bf16: 22.5 us, now 15.4;
-// floor 10.0).  fp32 gradients of 8192 tokens x 24 heads x 256, 64 elements of each turned:
-// 68.3 us, floor 60.1, 5.9 TB/s.  One token each of 64 sequences: 2.8 us, a launch.
-template <typename T, bool VECTOR>
+// latencies and the sines in a row (4096 tokens x 32 heads x 128 bf16, neighbours: 22.5 us, now
+// 14.8; floor 10.0).  fp32 gradients of 8192 tokens x 24 heads x 256, 64 elements of each
+// turned: 62.5 us, floor 60.1, 6.4 TB/s.  One token each of 64 sequences: 2.8 us, a launch.
+template <typename T, bool VECTOR, bool MANY>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p) {
   extern __shared__ __align__(16) uint8_t rope_smem[];
   const int np = p.r.rot / 2;
@@ -162,11 +163,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p)
   // items of one head: the rotated ones first, then the copies
   const int nrot = VECTOR && p.r.interleaved ? p.r.rot / V : np / V;
   const int ncopy = p.copy ? (p.D - p.r.rot) / V : 0;
-  const int per_head = nrot + ncopy, items = p.H * per_head;
+  const int per_head = nrot + ncopy, items = (MANY ? p.tb : 1) * p.H * per_head;
   const int lo = p.r.offset / V;  // copied items before the rotated part
-  // this thread's first item is the same of every token; kThreads items on is (dh, dk) on
-  const int h0 = threadIdx.x / per_head, k0 = threadIdx.x - h0 * per_head;
-  const int dh = kThreads / per_head, dk = kThreads - dh * per_head;
+  // this thread's first item is the same every time; kThreads items on is (di, dh, dk) on
+  const int ih0 = threadIdx.x / per_head, k0 = threadIdx.x - ih0 * per_head;
+  const int dih = kThreads / per_head, dk = kThreads - dih * per_head;
+  const int i0 = MANY ? ih0 / p.H : 0, h0 = ih0 - i0 * p.H;
+  const int di = MANY ? dih / p.H : 0, dh = dih - di * p.H;
+  const int ci0 = MANY ? threadIdx.x / np : 0, cj0 = threadIdx.x - ci0 * np;
+  const int dci = MANY ? kThreads / np : 0, dcj = kThreads - dci * np;
   const int second = VECTOR || !p.r.interleaved ? np : 1;  // from a pair's first half to its second
   const bool two = !(VECTOR && p.r.interleaved);           // the halves are loaded apart
   // an item's element (of the first of its two chunks or elements)
@@ -176,36 +181,55 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p)
     return (c < lo ? c : c + p.r.rot / V) * V;
   };
   using Item = typename std::conditional<VECTOR, uint4, T>::type;
-  for (long long t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    const int pos = __ldg(p.positions + t);
-    const T* x = static_cast<const T*>(p.x) + t * p.xt;
-    T* out = static_cast<T*>(p.out) + t * p.ot;
-    int h = h0, k = k0;
+  const int tb = MANY ? p.tb : 1;
+  for (long long t0 = (long long)blockIdx.x * tb; t0 < p.tokens; t0 += (long long)gridDim.x * tb) {
+    const int n = MANY ? (int)min((long long)tb, p.tokens - t0) : 1;
+    const int pos = MANY ? 0 : __ldg(p.positions + t0);
+    const T* x = static_cast<const T*>(p.x) + t0 * p.xt;
+    T* out = static_cast<T*>(p.out) + t0 * p.ot;
+    int i = i0, h = h0, k = k0;
     for (int e0 = 0; e0 < items; e0 += U * kThreads) {
       Item a[U], b[U];
-      int at[U];
+      int at[U], ti[U];
       bool rotates[U];
       long long oh[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        rotates[u] = k < nrot && h < p.H;
-        at[u] = h < p.H ? place(k) : -1;
-        oh[u] = h * p.oh;
-        if (h < p.H) {
-          const T* src = x + h * p.xh + at[u];
+        const bool there = MANY ? i < n : h < p.H;
+        rotates[u] = k < nrot && there;
+        at[u] = there ? place(k) : -1;
+        oh[u] = (MANY ? i * p.ot : 0) + h * p.oh;
+        ti[u] = i;
+        if (there) {
+          const T* src = x + (MANY ? i * p.xt : 0) + h * p.xh + at[u];
           a[u] = *reinterpret_cast<const Item*>(src);
           if (rotates[u] && two) b[u] = *reinterpret_cast<const Item*>(src + second);
         }
         k += dk;
         h += dh;
+        i += di;
         if (k >= per_head) {
           k -= per_head;
           ++h;
         }
+        if (MANY && h >= p.H) {
+          h -= p.H;
+          ++i;
+        }
       }
-      if (e0 == 0) {      // the token's cosines
-        __syncthreads();  // step is written; the last token's cosines are read
-        for (int j = threadIdx.x; j < np; j += kThreads) cs[j] = rope_cos_sin(step[j], pos, p.r);
+      if (e0 == 0) {      // the tokens' cosines
+        __syncthreads();  // step is written; the last tokens' cosines are read
+        if constexpr (MANY) {
+          for (int c = ci0, j = cj0; c < n; c += dci, j += dcj) {
+            if (j >= np) {
+              j -= np;
+              if (++c >= n) break;
+            }
+            cs[c * np + j] = rope_cos_sin(step[j], __ldg(p.positions + t0 + c), p.r);
+          }
+        } else {
+          for (int j = threadIdx.x; j < np; j += kThreads) cs[j] = rope_cos_sin(step[j], pos, p.r);
+        }
         __syncthreads();
       }
 #pragma unroll
@@ -215,18 +239,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p)
         if (rotates[u]) {
           if constexpr (VECTOR) {
             const int j = at[u] - p.r.offset;
+            const float2* w = cs + (MANY ? ti[u] * np : 0);
             float f[V], g[V];
             Chunk<T>::unpack(a[u], f);
             if (two) {
               Chunk<T>::unpack(b[u], g);
-              rotate_half(f, g, cs, j);
+              rotate_half(f, g, w, j);
               b[u] = Chunk<T>::pack(g);
             } else {
-              rotate_neighbours(f, cs, j / 2);
+              rotate_neighbours(f, w, j / 2);
             }
             a[u] = Chunk<T>::pack(f);
           } else {
-            const float2 w = cs[p.r.interleaved ? (at[u] - p.r.offset) / 2 : at[u] - p.r.offset];
+            const float2 w = cs[(MANY ? ti[u] * np : 0) + (p.r.interleaved ? (at[u] - p.r.offset) / 2 : at[u] - p.r.offset)];
             const float f = to_f32(a[u]), g = to_f32(b[u]);
             a[u] = from_f32<T>(f * w.x - g * w.y);
             b[u] = from_f32<T>(f * w.y + g * w.x);
@@ -240,16 +265,32 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p)
 }
 
 template <typename T>
-int launch_rope(const RopeApplyParams& p, int sms, cudaStream_t st) {
+int launch_rope(RopeApplyParams& p, int sms, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
   const int half = p.r.interleaved ? p.r.rot : p.r.rot / 2;
   const bool vec = aligned(p.x, 16) && aligned(p.out, 16) && p.D % V == 0 && p.r.offset % V == 0 && half % V == 0 &&
                    p.r.rot % V == 0 && p.xt % V == 0 && p.xh % V == 0 && p.ot % V == 0 && p.oh % V == 0;
-  const size_t smem = (size_t)(p.r.rot / 2 + 1) * 16;
-  const long long cap = 8LL * sms;  // 2048 threads an SM
-  const unsigned grid = (unsigned)(p.tokens < cap ? p.tokens : cap);
-  return vec ? launch_dependent(rope_kernel<T, true>, grid, kThreads, smem, st, p)
-             : launch_dependent(rope_kernel<T, false>, grid, kThreads, smem, st, p);
+  // As many tokens as give every thread its U items, while there are 4 CTAs an SM (32768
+  // tokens of one head of 64: 7.6 us, one at a time 36.6; 8 heads of 128: 29.5 and 55.2; one
+  // token's work is faster without the divisions and registers of several: 32 heads of 128
+  // neighbours, 4096 tokens, 14.8 us against 17.4)
+  const int np = p.r.rot / 2, v = vec ? V : 1;
+  const int items = p.H * ((vec && p.r.interleaved ? p.r.rot / v : np / v) + (p.copy ? (p.D - p.r.rot) / v : 0));
+  const long long room = kRopeSmem / (8 * np) - 2, even = p.tokens / (4 * sms);
+  long long tb = 2 * kThreads / items;
+  tb = tb > even ? even : tb;
+  tb = tb > room ? room : tb;
+  p.tb = tb < 1 ? 1 : (int)tb;
+  const size_t smem = (size_t)((np + 1) / 2 * 2 + p.tb * np) * 8;
+  // CTAs that go through several tokens: 16 an SM, 5 to 8 of them at once (the gradients above: 62.5
+  // us, 68.3 with 8)
+  const long long cap = (p.tb > 1 ? 8LL : 16LL) * sms, blocks = (p.tokens + p.tb - 1) / p.tb;
+  const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
+  if (p.tb > 1)
+    return vec ? launch_dependent(rope_kernel<T, true, true>, grid, kThreads, smem, st, p)
+               : launch_dependent(rope_kernel<T, false, true>, grid, kThreads, smem, st, p);
+  return vec ? launch_dependent(rope_kernel<T, true, false>, grid, kThreads, smem, st, p)
+             : launch_dependent(rope_kernel<T, false, false>, grid, kThreads, smem, st, p);
 }
 
 int rope_check(const double* inv_freq, int head_dim, int offset, int rot, int interleaved, float magnitude) {

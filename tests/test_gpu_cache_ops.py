@@ -128,6 +128,29 @@ def test_rope_empty_one_and_many_tokens():
             assert np.abs(y.double().cpu().numpy() - ref).max() < 1e-5 * 5
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,D,rot,offset", [(5000, 1, 64, 64, 0), (1301, 3, 40, 24, 8), (2000, 2, 10, 6, 3), (3001, 1, 3, 2, 1),
+                                              (4003, 7, 96, 96, 0), (1300, 1, 2048, 2048, 0), (2500, 2, 192, 64, 128)])
+def test_rope_many_tokens_of_few_heads(interleaved, dtype, T, H, D, rot, offset):
+    """Several tokens a CTA: their number not a multiple of a CTA's, strided, out of place and in place."""
+    rng = np.random.default_rng(T)
+    tdt = dict(bf16=torch.bfloat16, f32=torch.float32)[dtype]
+    wide = torch.from_numpy(rng.standard_normal((T, H + 1, D), dtype=np.float32)).to("cuda", tdt)
+    x = wide[:, :H]
+    pos = rng.integers(0, 1 << 20, T)
+    w = freqs(rot)
+    xh = x.double().cpu().numpy()
+    ref = oc.rotate(xh, pos, w, offset, interleaved)
+    far = 2 * np.abs(pos).max() * w.max() * 2.0 ** -52 * 2 * np.abs(xh).max()
+    bound = rope_bound(xh, ref, w, offset, interleaved, 1.0, torch.finfo(tdt).eps) + far
+    got = binding.rope_apply(x, dev_i32(pos), dev(w), offset=offset, interleaved=interleaved)
+    assert np.all(np.abs(got.double().cpu().numpy() - ref) <= bound)
+    last = wide[:, H].clone()
+    binding.rope_apply(x, dev_i32(pos), dev(w), offset=offset, interleaved=interleaved, out=x)
+    assert torch.equal(x, got) and torch.equal(wide[:, H], last)
+
+
 # ---------------------------------------------------------------- write and read
 
 def layout(rng, lens, cap, ps):
