@@ -46,9 +46,9 @@
 // guards every MMA, 45 cycles each, behind elect.sync 23, which at N <= 32 is less than the
 // tensor core takes (batch below: 57.8 -> 47.9 us).  Waits are bounded as in prefill_tc.cuh.
 //
-// Bound and measured (bf16, R = 512).  16 sequences up to 8192 tokens, 128 heads: 42.9
+// Bound and measured (bf16, R = 512).  16 sequences up to 8192 tokens, 128 heads: 42.1
 // us, where HBM needs 12.3 and the tensor cores 9.6; 64 sequences of 1 to 32768 tokens, 64
-// heads: 64.7 us, HBM 36.0; one sequence of 4096 tokens, 16 heads: 10.7 us.  A tile of 64
+// heads: 61.6 us, HBM 36.0; one sequence of 4096 tokens, 16 heads: 10.7 us.  A tile of 64
 // rows takes 1.85 us: the round through its two ring slots (load 1.5 us, S 0.6, softmax
 // 0.5, O 0.4, overlapping by units), not HBM (85 MB of it are read once, by the other row
 // tile from L2), with the tensor cores 35% busy.  Around the tiles: 5 us to the first
@@ -803,11 +803,13 @@ __global__ void __launch_bounds__(512, 1) latent_combine_kernel(const LatentComb
   // ---- short segments and empty sequences: CPI chunks of a row are a warp's work, 16 loads a
   // lane in flight.  Whole rows when there are about enough for every warp, else chunks: a
   // row's fixed work (divisions, shuffles) is an item's (2048 rows on 2432 warps, 5 pieces
-  // each: the call 42.9 us with whole rows, 46.7 with chunks).
+  // each: the call 42.1 us with whole rows, 45.9 with chunks).  Neighbouring rows, which have
+  // the same number of pieces, go to different CTAs: with them in one, a long sequence's few CTAs
+  // did most of the work (64 sequences of 1 to 32768 tokens: 66.6 us, now 61.6).
   auto merge_short = [&](auto cpi) {
     constexpr int CPI = decltype(cpi)::value, PARTS = NCH / CPI, KB = 16 / CPI;
     const unsigned items = (unsigned)p.B * p.rows * PARTS;
-    for (unsigned item = blockIdx.x * Cg::W + warp; item < items; item += gridDim.x * Cg::W) {
+    for (unsigned item = blockIdx.x + gridDim.x * warp; item < items; item += gridDim.x * Cg::W) {
       const int ch = item % PARTS * CPI, grow = item / PARTS;
       const int b = grow / p.rows, row = grow - b * p.rows;
       const int u = row / p.N, col = row - u * p.N;
