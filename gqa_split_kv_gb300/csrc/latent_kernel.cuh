@@ -89,7 +89,8 @@ struct LatentParams {
   unsigned long long timeout_ns;
 };
 
-// Line positions (16 tokens each) charged for a segment's fixed cost.
+// Line positions (16 tokens each) charged for a segment's fixed cost (64 sequences of 1 to
+// 32768 tokens: 69.3 us with 4, 61.5 with 8, 63.1 with 12; 16 sequences 43.3, 42.5, 42.1).
 constexpr int kLatentGap = 8;
 
 // The cut of the line into `ranges` equal ranges.
