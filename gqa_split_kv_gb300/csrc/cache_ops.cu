@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p)
   const int tb = MANY ? p.tb : 1;
   for (long long t0 = (long long)blockIdx.x * tb; t0 < p.tokens; t0 += (long long)gridDim.x * tb) {
     const int n = MANY ? (int)min((long long)tb, p.tokens - t0) : 1;
-    const int pos = MANY ? 0 : __ldg(p.positions + t0);
+    const int pos = MANY ? 0 : load_dependent(p.positions + t0);
     const T* x = static_cast<const T*>(p.x) + t0 * p.xt;
     T* out = static_cast<T*>(p.out) + t0 * p.ot;
     int i = i0, h = h0, k = k0;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeApplyParams p)
               j -= np;
               if (++c >= n) break;
             }
-            cs[c * np + j] = rope_cos_sin(step[j], __ldg(p.positions + t0 + c), p.r);
+            cs[c * np + j] = rope_cos_sin(step[j], load_dependent(p.positions + t0 + c), p.r);
           }
         } else {
           for (int j = threadIdx.x; j < np; j += kThreads) cs[j] = rope_cos_sin(step[j], pos, p.r);
@@ -337,7 +337,7 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
     in_slab = t;
   } else {
     const int col = t / p.slab;
-    const int page = __ldg(p.page_table + (size_t)b * p.max_pages + col);
+    const int page = load_dependent(p.page_table + (size_t)b * p.max_pages + col);
     if ((unsigned)page >= (unsigned)p.num_pages) {
       atomicOr(&g_error_word, 4u);
       return -1;
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
   // position of new token g = b n + i: L_b - n + i
   auto position = [&](unsigned g, int& b) -> long long {
     b = (int)(g / (unsigned)p.n);
-    const int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
+    const int L = p.seq_lens ? load_dependent(p.seq_lens + b) : p.cap;
     return (long long)L - p.n + (int)(g - (unsigned)b * (unsigned)p.n);
   };
   pdl_launch_dependents();
@@ -415,10 +415,10 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
         const int ch = gl + c * p.lanes;
         raw[c] = other[c] = make_uint4(0u, 0u, 0u, 0u);
         if (there && ch < nchunk) {
-          raw[c] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
+          raw[c] = load_dependent(reinterpret_cast<const uint4*>(src) + ch);
           const int at = ch * 8 - p.r.offset;  // within the rotated part
           if (!PAIRED && rotates && !p.r.interleaved && at >= 0 && at < p.r.rot)  // the other halves of these pairs
-            other[c] = __ldg(reinterpret_cast<const uint4*>(src + p.r.offset + (at >= np ? at - np : at + np)));
+            other[c] = load_dependent(reinterpret_cast<const uint4*>(src + p.r.offset + (at >= np ? at - np : at + np)));
         }
       }
       if (r0 == 0) {  // the tokens' places and cosines
@@ -536,12 +536,13 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) 
   const int b = blockIdx.x / nblk, i0 = (blockIdx.x - b * nblk) * p.tb;
   pdl_launch_dependents();
   pdl_wait_primary();
-  int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.cap;
+  int L = p.seq_lens ? load_dependent(p.seq_lens + b) : p.cap;
   L = min(L, p.cap);
-  const int start = p.starts ? __ldg(p.starts + b) : 0;
+  const int start = p.starts ? load_dependent(p.starts + b) : 0;
   constexpr int E = INT8 ? 16 : 8;  // elements of a 16-byte load
   const int per_row = p.Hkv * p.D / E, per_head = p.D / E;
   const int ntok = min(p.tb, p.n - i0);
+  const int tensors = p.v_out ? 2 : 1;
   for (int e = threadIdx.x; e < ntok * per_row; e += kThreads) {
     const int ti = e / per_row, c = e - ti * per_row;
     const long long t = (long long)start + i0 + ti;
@@ -551,15 +552,23 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) 
     const long long row = cache_row<PAGED>(p, b, (int)t, slab, in_slab);
     if (row < 0) continue;
     const size_t dst = ((size_t)b * p.n + i0 + ti) * per_row + c;
+    uint4 ws[2];
+    float ss[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {  // both tensors' loads before the first store
+      if (kv >= tensors) break;
+      ws[kv] = load_dependent(reinterpret_cast<const uint4*>(kv ? p.v : p.k) + row * per_row + c);
+      if (INT8) ss[kv] = load_dependent((kv ? p.vs : p.ks) + (slab * p.Hkv + c / per_head) * p.slab + in_slab);
+    }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
+      if (kv >= tensors) break;
       void* out = kv ? p.v_out : p.k_out;
-      if (kv && !out) break;
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(kv ? p.v : p.k) + row * per_row + c);
+      const uint4 w = ws[kv];
       if constexpr (!INT8) {
         reinterpret_cast<uint4*>(out)[dst] = w;
       } else {
-        const float s = __ldg((kv ? p.vs : p.ks) + (slab * p.Hkv + c / per_head) * p.slab + in_slab);
+        const float s = ss[kv];
         const uint32_t q[4] = {w.x, w.y, w.z, w.w};
         uint32_t o[8];
 #pragma unroll

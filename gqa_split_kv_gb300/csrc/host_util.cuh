@@ -85,7 +85,11 @@ bool overlap(const void* a, long long an, const void* b, long long bn) {
 
 // Launches kern as a programmatic dependent of what precedes it in the stream: its CTAs may
 // start while that drains, so every kernel launched here waits for it (griddepcontrol.wait)
-// before it touches memory.
+// before it touches memory that an earlier kernel may write or read, and reads such memory
+// by load_dependent or __ldcg, never through the read-only path.  One read comes before its
+// kernel's wait: latent_combine_kernel's of seq_lens, which its only predecessor,
+// latent_kernel, does not write, and whose writers are done because every CTA of latent_kernel
+// lets it start only after its own wait.
 template <typename P>
 int launch_dependent(void (*kern)(P), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const P& prm) {
   cudaLaunchAttribute attr[1];

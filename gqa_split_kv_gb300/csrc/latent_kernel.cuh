@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
               if (i < nbox) {
                 const int tok = t + i * rows;
                 const int col = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
-                page[i] = __ldg(p.page_table + (size_t)pc.b * p.max_pages + col);
+                page[i] = load_dependent(p.page_table + (size_t)pc.b * p.max_pages + col);
                 row0[i] = tok - col * p.page_size;
               }
             }
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
     const uint32_t st_off = (uint32_t)(st_row * 128 + (((2 * w + ((lane >> 3) & 1)) ^ (st_row & 7)) << 4));
     bool ok = true;
     while (take(piece)) {
-      const int L = max(0, min(p.seq_lens ? __ldg(p.seq_lens + pc.b) : p.max_len, p.max_len));
+      const int L = max(0, min(p.seq_lens ? load_dependent(p.seq_lens + pc.b) : p.max_len, p.max_len));
       float m[2 * NG], l[2 * NG];
 #pragma unroll
       for (int i = 0; i < 2 * NG; ++i) {

@@ -134,7 +134,7 @@ struct PrefillPiece {
     const int in_g = (int)(unit - gi * per_grp);
     const int bh = gi * p.grp + in_g % gsz;
     const int qb_ = p.nqb - 1 - in_g / gsz, b_ = bh / p.H;
-    int len = p.seq_lens ? __ldg(p.seq_lens + b_) : p.max_len;
+    int len = p.seq_lens ? load_dependent(p.seq_lens + b_) : p.max_len;
     len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
     const int rows = min(BQ, p.q_len - qb_ * BQ), first = len - p.q_len;
     const int end = max(0, min(len, first + qb_ * BQ + rows)), tiles = (end + BK - 1) / BK;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(256) latent_prefill_merge(const LatentPrefillP
   const int bh = unit / p.nqb, qb = unit - bh * p.nqb, b = bh / p.H, h = bh - b * p.H;
   pdl_wait_primary();
   pdl_launch_dependents();
-  int L = p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len;
+  int L = p.seq_lens ? load_dependent(p.seq_lens + b) : p.max_len;
   L = L < 0 ? 0 : (L > p.max_len ? p.max_len : L);
   const int q0 = qb * Gm::BQ, nq = min(Gm::BQ, p.q_len - q0);
   const int kv_end = max(0, min(L, L - p.q_len + q0 + nq));

@@ -31,6 +31,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace da {
 
 constexpr int kBlockTokens = 16;
@@ -68,10 +70,10 @@ struct Piece {
 // segment widths w_b (segment_width); P[B + 1] = the largest block count of one
 // sequence.  Run by the first nthreads threads of the block, which synchronise on
 // named barrier bar_id (bar_id 0 with every thread: __syncthreads).
-__device__ __forceinline__ void build_plan_arrays(const int* __restrict__ seq_lens, int B, int max_len, int gap,
+__device__ __forceinline__ void build_plan_arrays(const int* seq_lens, int B, int max_len, int gap,
                                                   int* lens, int* P, int bar_id, int nthreads) {
   for (int b = threadIdx.x; b < B; b += nthreads) {
-    int L = seq_lens ? __ldg(seq_lens + b) : max_len;
+    int L = seq_lens ? load_dependent(seq_lens + b) : max_len;
     L = L < 0 ? 0 : (L > max_len ? max_len : L);
     lens[b] = L;
   }

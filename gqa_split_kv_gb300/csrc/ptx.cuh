@@ -265,4 +265,13 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 
 __device__ __forceinline__ void pdl_wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Reads what a kernel before this one in the stream may have written, after the wait above.
+// An ordinary load, which the wait's memory clobber keeps below it.  __ldg is not for such
+// data: the read-only path wants memory that nothing writes while this grid lives, and a
+// dependent grid already lives while the kernel before it writes.
+template <typename T>
+__device__ __forceinline__ T load_dependent(const T* p) {
+  return *p;
+}
+
 }  // namespace da
