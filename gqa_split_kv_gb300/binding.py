@@ -117,6 +117,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "kv_read_paged": [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
         "kv_read_int8_contig": [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp],
         "kv_read_int8_paged": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
+        "kv_read_paged_filled": [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
+        "kv_read_int8_contig_filled": [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp],
+        "kv_read_int8_paged_filled": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp],
         "latent_attn_contig": [vp, vp, vp, i, i, i, i, i, f, vp, ll, vp, vp],
         "latent_attn_paged": [vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, ll, vp, vp],
         "latent_prefill_contig": [vp, vp, vp, vp, vp, i, i, i, i, i, ll, ll, ll, f, vp, ll, vp, vp],
@@ -537,26 +540,27 @@ def kv_write_int8_paged(k_new, v_new, k_pool_i8, v_pool_i8, k_scale_pool, v_scal
 
 
 def kv_read_paged(k_pool, v_pool, page_table, seq_lens, max_seq_len: int, n_tokens: int, starts=None, k_out=None,
-                  v_out=None, stream=None):
+                  v_out=None, stream=None, zero_rest: bool = False):
     """Tokens [starts[b], starts[b] + n_tokens) (starts int32 [B]; None: 0) of every sequence of a paged bf16 cache
-    as contiguous bf16 [B, n_tokens, Hkv, D]: (k_out, v_out), v_out None with v_pool None.  Rows past a sequence
-    are left as they were (zeros in outputs made here)."""
+    as contiguous bf16 [B, n_tokens, Hkv, D]: (k_out, v_out), v_out None with v_pool None.  Rows with no token (past a
+    sequence, before position 0, of a page outside the pool) are zeros in outputs made here; in a given output they are
+    left as they were, or zeros too with zero_rest."""
     return (_ext_module or _ext()).kv_read(k_pool, v_pool, None, None, page_table, seq_lens, max_seq_len, n_tokens,
-                                           starts, k_out, v_out, stream)
+                                           starts, k_out, v_out, stream, zero_rest)
 
 
 def kv_read_int8_contig(k_i8, v_i8, k_scale, v_scale, seq_lens, n_tokens: int, starts=None, k_out=None, v_out=None,
-                        stream=None):
+                        stream=None, zero_rest: bool = False):
     """kv_read_paged of a contiguous int8 cache (seq_lens may be None): value = int8 * scale, rounded to bf16."""
     return (_ext_module or _ext()).kv_read(k_i8, v_i8, _int8(k_scale), v_scale, None, seq_lens, 0, n_tokens, starts,
-                                           k_out, v_out, stream)
+                                           k_out, v_out, stream, zero_rest)
 
 
 def kv_read_int8_paged(k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, seq_lens, max_seq_len: int,
-                       n_tokens: int, starts=None, k_out=None, v_out=None, stream=None):
+                       n_tokens: int, starts=None, k_out=None, v_out=None, stream=None, zero_rest: bool = False):
     """kv_read_paged of an int8 cache: value = int8 * scale, rounded to bf16."""
     return (_ext_module or _ext()).kv_read(k_pool_i8, v_pool_i8, _int8(k_scale_pool), v_scale_pool, page_table, seq_lens,
-                                           max_seq_len, n_tokens, starts, k_out, v_out, stream)
+                                           max_seq_len, n_tokens, starts, k_out, v_out, stream, zero_rest)
 
 
 # ---------------------------------------------------------------- latent attention

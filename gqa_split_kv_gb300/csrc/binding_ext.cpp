@@ -55,6 +55,9 @@ struct Library {
   decltype(&::kv_read_paged) kv_read_paged = nullptr;
   decltype(&::kv_read_int8_contig) kv_read_int8_contig = nullptr;
   decltype(&::kv_read_int8_paged) kv_read_int8_paged = nullptr;
+  decltype(&::kv_read_paged_filled) kv_read_paged_filled = nullptr;
+  decltype(&::kv_read_int8_contig_filled) kv_read_int8_contig_filled = nullptr;
+  decltype(&::kv_read_int8_paged_filled) kv_read_int8_paged_filled = nullptr;
   decltype(&::latent_attn_contig) latent_attn_contig = nullptr;
   decltype(&::latent_attn_paged) latent_attn_paged = nullptr;
   decltype(&::latent_workspace_bytes) latent_workspace_bytes = nullptr;
@@ -356,9 +359,10 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
-// (k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, n_tokens, starts, k_out, v_out, stream)
+// (k, v, k_scale, v_scale, page_table, seq_lens, max_seq_len, n_tokens, starts, k_out, v_out, stream,
+//  zero_rest)
 PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  return guarded(nargs, 12, [&]() -> PyObject* {
+  return guarded(nargs, 13, [&]() -> PyObject* {
     const Tensor& k = ten(a[0], "k");
     const Tensor *v = opt(a[1], "v"), *ks = opt(a[2], "k_scale"), *vs = opt(a[3], "v_scale"),
                  *table = opt(a[4], "page_table"), *lens = opt(a[5], "seq_lens"), *starts = opt(a[8], "starts"),
@@ -376,26 +380,32 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     on_current(dev);
     Stream st(a[11], dev);
     const auto opts = k.options().dtype(at::kBFloat16);
-    const Tensor kt = ko ? *ko : at::zeros(dims(B, n, H, D), opts);
-    const Tensor vt = vo ? *vo : v ? at::zeros(dims(B, n, H, D), opts) : Tensor();
+    // outputs made here hold zeros where no token lies; a given one only when the caller asks for it
+    const bool fill = truth(a[12]) || (!ko && !vo);
+    auto make = [&] { return fill ? at::empty(dims(B, n, H, D), opts) : at::zeros(dims(B, n, H, D), opts); };
+    const Tensor kt = ko ? *ko : make();
+    const Tensor vt = vo ? *vo : v ? make() : Tensor();
     void* vp = v ? vt.data_ptr() : nullptr;
     const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k");
     if (!c.paged) {
       call("kv_read_int8_contig", [&] {
-        return g_lib.kv_read_int8_contig(ptr(k), ptr(v), ptr<float>(ks), ptr<float>(vs), ptr<int>(starts),
+        auto f = fill ? g_lib.kv_read_int8_contig_filled : g_lib.kv_read_int8_contig;
+        return f(ptr(k), ptr(v), ptr<float>(ks), ptr<float>(vs), ptr<int>(starts),
                                          ptr<int>(lens), B, n, H, D, slab, ptr(kt), vp, st.raw);
       });
     } else {
       const int cap = small(a[6], "max_seq_len");
       if (c.int8)
         call("kv_read_int8_paged", [&] {
-          return g_lib.kv_read_int8_paged(ptr(k), ptr(v), ptr<float>(ks), ptr<float>(vs), ptr<int>(table),
+          auto f = fill ? g_lib.kv_read_int8_paged_filled : g_lib.kv_read_int8_paged;
+          return f(ptr(k), ptr(v), ptr<float>(ks), ptr<float>(vs), ptr<int>(table),
                                           ptr<int>(starts), ptr<int>(lens), B, n, H, D, slab, cols, slabs, cap, ptr(kt),
                                           vp, st.raw);
         });
       else
         call("kv_read_paged", [&] {
-          return g_lib.kv_read_paged(ptr(k), ptr(v), ptr<int>(table), ptr<int>(starts), ptr<int>(lens), B, n, H, D,
+          auto f = fill ? g_lib.kv_read_paged_filled : g_lib.kv_read_paged;
+          return f(ptr(k), ptr(v), ptr<int>(table), ptr<int>(starts), ptr<int>(lens), B, n, H, D,
                                      slab, cols, slabs, cap, ptr(kt), vp, st.raw);
         });
     }
@@ -546,6 +556,9 @@ PyObject* open(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   FIND(kv_read_paged)
   FIND(kv_read_int8_contig)
   FIND(kv_read_int8_paged)
+  FIND(kv_read_paged_filled)
+  FIND(kv_read_int8_contig_filled)
+  FIND(kv_read_int8_paged_filled)
   FIND(latent_attn_contig)
   FIND(latent_attn_paged)
   FIND(latent_workspace_bytes)

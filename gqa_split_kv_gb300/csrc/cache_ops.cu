@@ -325,6 +325,7 @@ struct CacheParams {
   int max_pages, num_pages;
   int tb;                     // tokens a CTA takes at a time
   int lanes;                  // write: lanes a row (a power of two)
+  int fill;                   // read: rows with no token are written, as zeros
 };
 
 // The cache row (in tokens) of sequence b's position t, or -1 when its page is not in
@@ -527,10 +528,12 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
 }
 
 // A CTA reads tb consecutive tokens of one sequence, 16 bytes of the cache a thread and
-// step (int8: 32 bytes written).  Bound by HBM: 16 ragged sequences up to 8192 tokens, 8
-// heads x 128 from int8 pages, 71.6 us, floor 62.6 (5.9 TB/s); one sequence of 4096 tokens, 4
-// heads x 256: 5.9 us, floor 3.8.
-template <bool PAGED, bool INT8>
+// step (int8: 32 bytes written).  FILL: rows with no token are written too, as zeros.  Bound
+// by HBM: 16 ragged sequences up to 8192 tokens, 8 heads x 128 from int8 pages, 72.8 us, floor
+// 62.6 (5.8 TB/s), and filled 109.4 us, floor 102.5; one sequence of 4096 tokens, 4 heads x
+// 256: 6.0 us, floor 3.8.  The warps in flight hide the chain page, row, store: with two
+// items a thread the batch takes 84 us, with both tensors' loads before the first store 78.6.
+template <bool PAGED, bool INT8, bool FILL>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) {
   const int nblk = (p.n + p.tb - 1) / p.tb;
   const int b = blockIdx.x / nblk, i0 = (blockIdx.x - b * nblk) * p.tb;
@@ -546,29 +549,28 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) 
   for (int e = threadIdx.x; e < ntok * per_row; e += kThreads) {
     const int ti = e / per_row, c = e - ti * per_row;
     const long long t = (long long)start + i0 + ti;
-    if (t < 0 || t >= L) continue;
-    long long slab;
+    long long slab, row = -1;
     int in_slab;
-    const long long row = cache_row<PAGED>(p, b, (int)t, slab, in_slab);
-    if (row < 0) continue;
+    if (t >= 0 && t < L) row = cache_row<PAGED>(p, b, (int)t, slab, in_slab);
     const size_t dst = ((size_t)b * p.n + i0 + ti) * per_row + c;
-    uint4 ws[2];
-    float ss[2];
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {  // both tensors' loads before the first store
-      if (kv >= tensors) break;
-      ws[kv] = load_dependent(reinterpret_cast<const uint4*>(kv ? p.v : p.k) + row * per_row + c);
-      if (INT8) ss[kv] = load_dependent((kv ? p.vs : p.ks) + (slab * p.Hkv + c / per_head) * p.slab + in_slab);
+    if (row < 0) {
+      if (!FILL) continue;
+      for (int kv = 0; kv < tensors; ++kv) {
+        uint4* out = reinterpret_cast<uint4*>(kv ? p.v_out : p.k_out) + (INT8 ? 2 : 1) * dst;
+        out[0] = make_uint4(0u, 0u, 0u, 0u);
+        if (INT8) out[1] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
     }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       if (kv >= tensors) break;
-      void* out = kv ? p.v_out : p.k_out;
-      const uint4 w = ws[kv];
+      uint4* out = reinterpret_cast<uint4*>(kv ? p.v_out : p.k_out) + (INT8 ? 2 : 1) * dst;
+      const uint4 w = load_dependent(reinterpret_cast<const uint4*>(kv ? p.v : p.k) + row * per_row + c);
       if constexpr (!INT8) {
-        reinterpret_cast<uint4*>(out)[dst] = w;
+        out[0] = w;
       } else {
-        const float s = ss[kv];
+        const float s = load_dependent((kv ? p.vs : p.ks) + (slab * p.Hkv + c / per_head) * p.slab + in_slab);
         const uint32_t q[4] = {w.x, w.y, w.z, w.w};
         uint32_t o[8];
 #pragma unroll
@@ -576,9 +578,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) 
           o[2 * i] = pack_bf16x2((float)(int8_t)(q[i]) * s, (float)(int8_t)(q[i] >> 8) * s);
           o[2 * i + 1] = pack_bf16x2((float)(int8_t)(q[i] >> 16) * s, (float)(int8_t)(q[i] >> 24) * s);
         }
-        uint4* d = reinterpret_cast<uint4*>(out) + 2 * dst;
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        out[1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
   }
@@ -689,7 +690,15 @@ int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t
   const bool has_v = p.v_out != nullptr;
   if (!p.k_out || !aligned(p.k_out, 16) || !aligned(p.v_out, 16) || (!has_v && p.v)) return DA_ERR_INVALID_ARG;
   if (int e = check_cache_pointers(p, paged, int8, has_v)) return e;
-  if (p.cap == 0 || (paged && p.num_pages == 0)) return DA_OK;  // every row is past its sequence
+  if (p.cap == 0 || (paged && p.num_pages == 0)) {  // there is no token
+    const size_t bytes = (size_t)p.B * p.n * p.Hkv * p.D * 2;
+    if (p.fill && (cudaMemsetAsync(p.k_out, 0, bytes, st) != cudaSuccess ||
+                   (has_v && cudaMemsetAsync(p.v_out, 0, bytes, st) != cudaSuccess))) {
+      cudaGetLastError();
+      return DA_ERR_CUDA;
+    }
+    return DA_OK;
+  }
   {
     const long long on = (long long)p.B * p.n * p.Hkv * p.D * 2, cn = cache_bytes(p, paged, int8),
                     sn = scale_bytes(p, paged);
@@ -710,9 +719,14 @@ int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t
   p.tb = tb;
   const long long grid = (long long)p.B * ((p.n + p.tb - 1) / p.tb);
   if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
-  if (paged && int8) return launch_dependent(kv_read_kernel<true, true>, (unsigned)grid, kThreads, 0, st, p);
-  if (paged) return launch_dependent(kv_read_kernel<true, false>, (unsigned)grid, kThreads, 0, st, p);
-  return launch_dependent(kv_read_kernel<false, true>, (unsigned)grid, kThreads, 0, st, p);
+  auto launch = [&](auto in_pages, auto in_int8) {
+    constexpr bool P = decltype(in_pages)::value, I = decltype(in_int8)::value;
+    return p.fill ? launch_dependent(kv_read_kernel<P, I, true>, (unsigned)grid, kThreads, 0, st, p)
+                  : launch_dependent(kv_read_kernel<P, I, false>, (unsigned)grid, kThreads, 0, st, p);
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  return paged && int8 ? launch(yes, yes) : paged ? launch(yes, no) : launch(no, yes);
 }
 
 long long paged_cap(int page_size, int max_pages, int max_seq_len) {
@@ -825,7 +839,7 @@ CacheParams write_params(const void* k_new, const void* v_new, long long k_strid
 
 CacheParams read_params(const void* k, const void* v, const float* ks, const float* vs, const int* starts,
                         const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim, void* k_out,
-                        void* v_out) {
+                        void* v_out, bool fill) {
   CacheParams p = {};
   p.k = const_cast<void*>(k);
   p.v = const_cast<void*>(v);
@@ -839,6 +853,7 @@ CacheParams read_params(const void* k, const void* v, const float* ks, const flo
   p.D = head_dim;
   p.k_out = k_out;
   p.v_out = v_out;
+  p.fill = fill;
   return p;
 }
 
@@ -898,24 +913,43 @@ extern "C" int kv_write_int8_paged(const void* k_new, const void* v_new, long lo
                     reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+int read_contig_int8(const void* k_i8, const void* v_i8, const float* k_scale, const float* v_scale, const int* starts,
+                     const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim, int max_ctx,
+                     void* k_out, void* v_out, void* stream, bool fill) {
+  CacheParams p = read_params(k_i8, v_i8, k_scale, v_scale, starts, seq_lens, batch, n_tokens, num_kv_heads, head_dim,
+                              k_out, v_out, fill);
+  p.slab = max_ctx;
+  return read_call(false, true, p, max_ctx, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int read_paged(bool int8, const void* k, const void* v, const float* ks, const float* vs, const int* page_table,
+               const int* starts, const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
+               int page_size, int max_pages, int num_pages, int max_seq_len, void* k_out, void* v_out, void* stream,
+               bool fill) {
+  CacheParams p = read_params(k, v, ks, vs, starts, seq_lens, batch, n_tokens, num_kv_heads, head_dim, k_out, v_out,
+                              fill);
+  set_pages(p, page_table, page_size, max_pages, num_pages);
+  return read_call(true, int8, p, paged_cap(page_size, max_pages, max_seq_len), reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
 extern "C" int kv_read_int8_contig(const void* k_i8, const void* v_i8, const float* k_scale, const float* v_scale,
                                    const int* starts, const int* seq_lens, int batch, int n_tokens, int num_kv_heads,
                                    int head_dim, int max_ctx, void* k_out, void* v_out, void* stream) {
-  CacheParams p = read_params(k_i8, v_i8, k_scale, v_scale, starts, seq_lens, batch, n_tokens, num_kv_heads, head_dim,
-                              k_out, v_out);
-  p.slab = max_ctx;
-  return read_call(false, true, p, max_ctx, reinterpret_cast<cudaStream_t>(stream));
+  return read_contig_int8(k_i8, v_i8, k_scale, v_scale, starts, seq_lens, batch, n_tokens, num_kv_heads, head_dim,
+                          max_ctx, k_out, v_out, stream, false);
 }
 
 extern "C" int kv_read_paged(const void* k_pool, const void* v_pool, const int* page_table, const int* starts,
                              const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
                              int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
                              void* v_out, void* stream) {
-  CacheParams p = read_params(k_pool, v_pool, nullptr, nullptr, starts, seq_lens, batch, n_tokens, num_kv_heads,
-                              head_dim, k_out, v_out);
-  set_pages(p, page_table, page_size, max_pages_per_seq, num_pages);
-  return read_call(true, false, p, paged_cap(page_size, max_pages_per_seq, max_seq_len),
-                   reinterpret_cast<cudaStream_t>(stream));
+  return read_paged(false, k_pool, v_pool, nullptr, nullptr, page_table, starts, seq_lens, batch, n_tokens,
+                    num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out, v_out, stream,
+                    false);
 }
 
 extern "C" int kv_read_int8_paged(const void* k_pool_i8, const void* v_pool_i8, const float* k_scale_pool,
@@ -923,9 +957,33 @@ extern "C" int kv_read_int8_paged(const void* k_pool_i8, const void* v_pool_i8, 
                                   const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
                                   int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
                                   void* v_out, void* stream) {
-  CacheParams p = read_params(k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, starts, seq_lens, batch, n_tokens,
-                              num_kv_heads, head_dim, k_out, v_out);
-  set_pages(p, page_table, page_size, max_pages_per_seq, num_pages);
-  return read_call(true, true, p, paged_cap(page_size, max_pages_per_seq, max_seq_len),
-                   reinterpret_cast<cudaStream_t>(stream));
+  return read_paged(true, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, starts, seq_lens, batch,
+                    n_tokens, num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out, v_out,
+                    stream, false);
+}
+
+extern "C" int kv_read_int8_contig_filled(const void* k_i8, const void* v_i8, const float* k_scale, const float* v_scale,
+                                   const int* starts, const int* seq_lens, int batch, int n_tokens, int num_kv_heads,
+                                   int head_dim, int max_ctx, void* k_out, void* v_out, void* stream) {
+  return read_contig_int8(k_i8, v_i8, k_scale, v_scale, starts, seq_lens, batch, n_tokens, num_kv_heads, head_dim,
+                          max_ctx, k_out, v_out, stream, true);
+}
+
+extern "C" int kv_read_paged_filled(const void* k_pool, const void* v_pool, const int* page_table, const int* starts,
+                             const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
+                             int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
+                             void* v_out, void* stream) {
+  return read_paged(false, k_pool, v_pool, nullptr, nullptr, page_table, starts, seq_lens, batch, n_tokens,
+                    num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out, v_out, stream,
+                    true);
+}
+
+extern "C" int kv_read_int8_paged_filled(const void* k_pool_i8, const void* v_pool_i8, const float* k_scale_pool,
+                                  const float* v_scale_pool, const int* page_table, const int* starts,
+                                  const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
+                                  int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
+                                  void* v_out, void* stream) {
+  return read_paged(true, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, starts, seq_lens, batch,
+                    n_tokens, num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out, v_out,
+                    stream, true);
 }

@@ -450,6 +450,22 @@ int kv_read_int8_paged(const void* k_pool_i8, const void* v_pool_i8, const float
                        int num_pages, int max_seq_len, void* k_out, void* v_out, void* stream);
 
 /*
+ * kv_read_paged_filled / kv_read_int8_contig_filled / kv_read_int8_paged_filled — the same, but
+ * the outputs' rows that kv_read_* leaves as they were are zeros: every row is written.
+ */
+int kv_read_paged_filled(const void* k_pool, const void* v_pool, const int* page_table, const int* starts,
+                         const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim, int page_size,
+                         int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out, void* v_out, void* stream);
+int kv_read_int8_contig_filled(const void* k_i8, const void* v_i8, const float* k_scale, const float* v_scale,
+                               const int* starts, const int* seq_lens, int batch, int n_tokens, int num_kv_heads,
+                               int head_dim, int max_ctx, void* k_out, void* v_out, void* stream);
+int kv_read_int8_paged_filled(const void* k_pool_i8, const void* v_pool_i8, const float* k_scale_pool,
+                              const float* v_scale_pool, const int* page_table, const int* starts, const int* seq_lens,
+                              int batch, int n_tokens, int num_kv_heads, int head_dim, int page_size,
+                              int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out, void* v_out,
+                              void* stream);
+
+/*
  * latent_attn_contig / latent_attn_paged — attention over a cache of one shared latent
  * vector a token, in its absorbed form: the up-projections of keys and values are folded
  * into the queries and the output, so every head attends to the cached vector itself.

@@ -193,3 +193,15 @@ def test_binding_refuses_mismatched_tensors():
         binding.rope_inv_freq(8, scaling="sideways", device="cpu")
     with pytest.raises(binding.DecodeAttnError):
         binding.rope_inv_freq(7, device="cpu")
+
+
+@pytest.mark.parametrize("name", ["kv_read_paged", "kv_read_int8_contig", "kv_read_int8_paged"])
+def test_filled_reads_refuse_what_reads_refuse(clib, name):
+    f, g = getattr(clib, name), getattr(clib, name + "_filled")
+    scales = (SK, SV) if "int8" in name else ()
+    where = (16, 4, 8, 64) if "paged" in name else (64,)
+    table = (A,) if "paged" in name else ()
+    for B, n, D, ko, want in ((-1, 4, 64, A, 1), (2, -1, 64, A, 1), (2, 4, 20, A, 2), (2, 4, 64, None, 1),
+                              (2, 4, 64, K, 1), (0, 4, 64, A, 0), (2, 0, 64, A, 0)):
+        args = (K, V, *scales, *table, None, A, B, n, 2, D, *where, ko, A + (1 << 30), None)
+        assert f(*args) == g(*args) == want
