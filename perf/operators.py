@@ -249,16 +249,15 @@ def _own(s):
                                          starts=s["starts"], k_out=s["k_out"], v_out=s["v_out"])
         binding.kv_write_contig(s["k_new"], s["v_new"], s["k"], s["v"], s["lens"], **rope)
         return s["k"], s["v"]
-    if kind == "read":
+    if kind == "read":  # the whole output, whatever an earlier pass left in it
         n = s["k_out"].shape[1]
+        kw = dict(k_out=s["k_out"], v_out=s["v_out"], zero_rest=True)
         if c["int8"] and c["page"]:
             return binding.kv_read_int8_paged(s["k"], s["v"], s["k_scale"], s["v_scale"], s["table"], s["lens"],
-                                              c["max_len"], n, k_out=s["k_out"], v_out=s["v_out"])
+                                              c["max_len"], n, **kw)
         if c["int8"]:
-            return binding.kv_read_int8_contig(s["k"], s["v"], s["k_scale"], s["v_scale"], s["lens"], n,
-                                               k_out=s["k_out"], v_out=s["v_out"])
-        return binding.kv_read_paged(s["k"], s["v"], s["table"], s["lens"], c["max_len"], n, k_out=s["k_out"],
-                                     v_out=s["v_out"])
+            return binding.kv_read_int8_contig(s["k"], s["v"], s["k_scale"], s["v_scale"], s["lens"], n, **kw)
+        return binding.kv_read_paged(s["k"], s["v"], s["table"], s["lens"], c["max_len"], n, **kw)
     if kind == "latent":
         if c["page"]:
             return binding.latent_attn_paged(s["q"], s["cache"], s["table"], s["lens"], c["max_len"],
