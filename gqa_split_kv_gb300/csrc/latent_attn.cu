@@ -180,22 +180,20 @@ int latent_call(bool paged, const void* q, const void* cache, const int* page_ta
   }
 }
 
-// How a prefill's keys are cut: where all CTAs of two parts a block still run at once, into
-// as many parts as do, of 4 key tiles at least.  A second round of parts costs what the
-// cut saves: 128 blocks of up to 21 tiles (4 sequences, 16 heads, 500 new tokens) take
-// 51.2 us whole and 47 to 54 us in parts of 11 to 8, by the sequences' order.
-void prefill_parts(long long units, int max_ctx, int sms, int* parts, int* part_tiles) {
-  const long long tiles = ((long long)max_ctx + 127) / 128;
-  long long n = units > 0 ? sms / units : 1;
-  n = n > (tiles + 3) / 4 ? (tiles + 3) / 4 : n;
-  n = n < 1 ? 1 : n;
-  *parts = (int)n;
-  *part_tiles = n == 1 ? 0x7fffffff / 256 : (int)((tiles + n - 1) / n);
+// CTAs a query block: where all CTAs of two parts a block still run at once, as many as do,
+// up to the parts that the longest sequence there may be can have.  Blocks that see fewer
+// keys have fewer parts, and their other CTAs leave at once (8 heads, 200 new tokens after
+// 2800 keys: 22.4 us in a cache of that size and 24.2 in one of 131072; with parts sized by the
+// capacity 52.0 there).  A second round of parts cost what the cut saved: 128 blocks of up to 21
+// tiles (4 sequences, 16 heads, 500 new tokens) took 51.2 us whole and 47 to 54 in parts of 11
+// to 8, by the sequences' order, before CTAs took over waiting blocks.
+int prefill_parts(long long units, int max_ctx, int sms) {
+  const int tiles = max_ctx / 128 + (max_ctx % 128 != 0);
+  return units > 0 ? prefill_block_parts(tiles, (int)(sms / units)) : 1;
 }
 
 long long prefill_workspace(long long units, int max_ctx, int D, int sms) {
-  int parts, part_tiles;
-  prefill_parts(units, max_ctx, sms, &parts, &part_tiles);
+  const int parts = prefill_parts(units, max_ctx, sms);
   return parts == 1 ? 0 : units * parts * LatentPrefillGeo<128>::BQ * (D + 2) * 4;
 }
 
@@ -350,10 +348,9 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
   prm.timeout_ns = kWaitTimeoutNs;
   const long long units = nqb * batch * num_heads;
   prm.parts = 1;
-  prm.part_tiles = 0x7fffffff / 256;
   if (workspace) {
     if (workspace_bytes < prefill_workspace(units, max_ctx, head_dim, sms)) return DA_ERR_WORKSPACE;
-    prefill_parts(units, max_ctx, sms, &prm.parts, &prm.part_tiles);
+    prm.parts = prefill_parts(units, max_ctx, sms);
     prm.part_acc = static_cast<float*>(workspace);
     prm.part_ml = reinterpret_cast<float2*>(prm.part_acc + units * prm.parts * BQ * head_dim);
   }

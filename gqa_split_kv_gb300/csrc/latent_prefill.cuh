@@ -22,9 +22,9 @@
 // instead of 32 cycles an MMA.
 //
 // A few query blocks (a chunk after a long prefix, few heads) leave most SMs idle.  Then a
-// block's key tiles are cut into up to `parts` equal parts of at most `part_tiles`, each a
-// CTA's, which leaves (O, m, l) unnormalised in fp32; latent_prefill_merge joins them.  A
-// block of one part is written at once.
+// block's key tiles are cut into up to `parts` equal parts (prefill_cut.cuh), each a CTA's,
+// which leaves (O, m, l) unnormalised in fp32; latent_prefill_merge joins them.  A block of one
+// part is written at once.
 //
 // More blocks than SMs: a CTA that has issued its last loads asks for the index of one that
 // has not started (clusterlaunchcontrol) and goes on with it, so the next block's queries and
@@ -47,6 +47,7 @@
 #include <cstdint>
 
 #include "device_error.cuh"
+#include "prefill_cut.cuh"
 #include "ptx.cuh"
 #include "tc05.cuh"
 
@@ -61,7 +62,7 @@ struct LatentPrefillParams {
   const int* seq_lens;     // [B] or null (every sequence max_len tokens)
   float* part_acc;         // [unit][part][D][256]: parts' O (with more than one part)
   float2* part_ml;         // [unit][part][256], m in log2 units
-  int parts, part_tiles;   // parts a unit's keys may have, key tiles a part
+  int parts;               // CTAs a unit: parts that its keys may have
   int more;                // not every CTA runs at once: CTAs take over others' indices
   int B, q_len, H, nqb;
   int grp;                 // (sequence, head) units per launch group (their K/V fit in L2 together)
@@ -138,10 +139,9 @@ struct PrefillPiece {
     len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
     const int rows = min(BQ, p.q_len - qb_ * BQ), first = len - p.q_len;
     const int end = max(0, min(len, first + qb_ * BQ + rows)), tiles = (end + BK - 1) / BK;
-    // equal parts of at most part_tiles
-    const int nparts = max(1, (tiles + p.part_tiles - 1) / p.part_tiles);
-    const int from = part < nparts ? (int)((long long)tiles * part / nparts) : 0;
-    const int count = part < nparts ? (int)((long long)tiles * (part + 1) / nparts) - from : 0;
+    const int nparts = prefill_block_parts(tiles, p.parts);
+    const int from = part < nparts ? prefill_part_begin(tiles, part, nparts) : 0;
+    const int count = part < nparts ? prefill_part_begin(tiles, part + 1, nparts) - from : 0;
     const int end_a = max(0, min(len, first + qb_ * BQ + min(rows, BQ / 2)));
     b = b_;
     h = bh - b_ * p.H;
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(256) latent_prefill_merge(const LatentPrefillP
   L = L < 0 ? 0 : (L > p.max_len ? p.max_len : L);
   const int q0 = qb * Gm::BQ, nq = min(Gm::BQ, p.q_len - q0);
   const int kv_end = max(0, min(L, L - p.q_len + q0 + nq));
-  const int n = ((kv_end + Gm::BK - 1) / Gm::BK + p.part_tiles - 1) / p.part_tiles;
+  const int n = prefill_block_parts((kv_end + Gm::BK - 1) / Gm::BK, p.parts);
   if (n <= 1 || row >= nq) return;
   const float kNegInf = -__int_as_float(0x7f800000);
   const size_t slot0 = (size_t)unit * p.parts;

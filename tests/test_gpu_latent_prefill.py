@@ -198,3 +198,18 @@ def test_absorbed_and_expanded_agree():
         assert np.all(np.abs(exp[b].cpu().numpy() - ref) <= tol)
         assert np.all(np.abs(absd[b].cpu().numpy() - ref) <= tol)
     assert binding.device_error() == 0
+
+
+def test_the_capacity_does_not_change_how_keys_are_cut():
+    """3000 keys of a cache of that size and of a much larger one: the same parts, so the same bits."""
+    H, D, q_len, L, ctx = 8, 128, 200, 3000, 40000
+    c = make(14, [L], q_len, H, D, L)
+    first = run(c)
+    check(first, c, "parts")
+    far = [torch.full((1, ctx, *x.shape[2:]), float("nan"), dtype=torch.bfloat16, device="cuda") for x in
+           (c["k"], c["pe"], c["v"])]
+    for t, n in zip(far, ("k", "pe", "v")):
+        t[:, :L] = dev_bf16(c[n])
+    out = binding.latent_prefill_contig(dev_bf16(c["q"]), *far, dev_i32(c["lens"]), scale=c["scale"])
+    assert np.array_equal(host_bits(out), first)
+    assert binding.device_error() == 0
