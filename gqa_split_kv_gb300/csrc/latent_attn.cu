@@ -235,13 +235,14 @@ int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k
   if (int e = encode_map_t(&prm.tm_v, bf16, sw, v, 5, dims, strides, box_v)) return e;
   if (int e = encode_map_t(&prm.tm_pe, bf16, sw, k_rope, 3, dims_pe, strides_pe, box_pe)) return e;
   {
-    // launch groups of (b, h) units whose K/V fit in about 96 MB of L2 together: the longest
-    // query blocks of a group start first, so a second group's would start last (32 heads x
-    // 4096 tokens: 160 us in groups of 24, 142 in one)
-    const long long unit_bytes = 4LL * D * prm.max_len, units = (long long)prm.B * prm.H;
-    long long g = (96LL << 20) / unit_bytes;
-    g = g < 1 ? 1 : g;
-    prm.grp = (int)(g < units ? g : units);
+    // launch groups of (b, h) units whose K/V fit in L2 together: the longest query blocks of
+    // a group start first, so a second group's would start last (32 heads x 4096 tokens: 160 us
+    // in groups of 24, 142 in one).  Where the capacity would make several groups, the kernel
+    // takes the longest sequence's tokens instead (that prompt, other
+    // values, in a cache of 131072: 126 us, 157 in groups by the capacity; of its own size: 124)
+    const long long units = (long long)prm.B * prm.H;
+    prm.grp = prefill_group(prm.max_len, D, units);
+    prm.grp_by_length = prm.seq_lens && prm.grp < units;
   }
   const long long units = (long long)prm.nqb * prm.B * prm.H;
   if (units * prm.parts > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;

@@ -66,6 +66,7 @@ struct LatentPrefillParams {
   int more;                // not every CTA runs at once: CTAs take over others' indices
   int B, q_len, H, nqb;
   int grp;                 // (sequence, head) units per launch group (their K/V fit in L2 together)
+  int grp_by_length;       // that is by the capacity: the kernel takes the longest sequence's tokens
   int max_len;
   float scale_log2;
   unsigned long long timeout_ns;
@@ -92,7 +93,7 @@ struct LatentPrefillGeo {
                        BAR_FIN = BAR_ANSWER + 1, NBAR = BAR_FIN + 1;
   static constexpr int OFF_ANSWER = OFF_BAR + (NBAR + 1) / 2 * 16;  // to the request for a next index
   static constexpr int OFF_PIECE = OFF_ANSWER + 16;                 // this piece and the next
-  static constexpr int OFF_MISC = OFF_PIECE + 2 * 48;               // tensor memory base, abort flag
+  static constexpr int OFF_MISC = OFF_PIECE + 2 * 48;               // tensor memory base, abort flag, grp
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int TCOL_O = 2 * BK;             // S of tile t at t BK, O at TCOL_O + t D
   static constexpr uint32_t TMEM_COLS = 512;
@@ -114,14 +115,14 @@ __device__ __forceinline__ void latent_setmaxnreg_inc() {
 }
 
 // A CTA's work of one index: tiles [j0, j0 + n) of query block qb of (b, h).  Groups of grp
-// (b, h) pairs, latest query blocks (the longest) first; a unit's parts together.
+// (b, h) units, latest query blocks (the longest) first; a unit's parts together.
 struct PrefillPiece {
   int b, h, qb;
   int L, nq, base, kv_end;  // length, rows, position of query token 0, keys some row sees
   int j0, n, n_a;           // n_a: of the n tiles, those that query tile A's rows see some of
   int slot;                 // of the part; -1: the whole block
   int any;                  // 0: no part of this index; -1: no more pieces
-  __device__ __forceinline__ void set(const LatentPrefillParams& p, int index) volatile {
+  __device__ __forceinline__ void set(const LatentPrefillParams& p, int grp, int index) volatile {
     constexpr int BQ = 256, BK = 128;
     if (index < 0) {
       any = -1;
@@ -129,11 +130,11 @@ struct PrefillPiece {
     }
     const int part = index % p.parts, unit = index / p.parts;
     const int nbh = p.B * p.H;
-    const long long per_grp = (long long)p.nqb * p.grp;
+    const long long per_grp = (long long)p.nqb * grp;
     const int gi = (int)(unit / per_grp);
-    const int gsz = min(p.grp, nbh - gi * p.grp);
+    const int gsz = min(grp, nbh - gi * grp);
     const int in_g = (int)(unit - gi * per_grp);
-    const int bh = gi * p.grp + in_g % gsz;
+    const int bh = gi * grp + in_g % gsz;
     const int qb_ = p.nqb - 1 - in_g / gsz, b_ = bh / p.H;
     int len = p.seq_lens ? load_dependent(p.seq_lens + b_) : p.max_len;
     len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
@@ -231,7 +232,16 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
     tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  if (threadIdx.x == 64) reinterpret_cast<volatile PrefillPiece*>(smem + Gm::OFF_PIECE)->set(p, blockIdx.x);
+  int grp = p.grp;
+  if (p.grp_by_length && warp == 2) {
+    int longest = 0;
+    for (int b = lane; b < p.B; b += 32) longest = max(longest, load_dependent(p.seq_lens + b));
+    grp = prefill_group(min(__reduce_max_sync(0xffffffffu, longest), p.max_len), D, (long long)p.B * p.H);
+  }
+  if (threadIdx.x == 64) {
+    reinterpret_cast<volatile PrefillPiece*>(smem + Gm::OFF_PIECE)->set(p, grp, blockIdx.x);
+    *reinterpret_cast<int*>(smem + Gm::OFF_MISC + 8) = grp;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -301,7 +311,7 @@ __global__ void __launch_bounds__(LatentPrefillGeo<D>::NTHREADS, 1)
           waiting = false;
           if (k > 0 && !(ok = wait(Gm::BAR_READ + ((k + 1) & 1), (k - 1) >> 1))) break;
           ++k;
-          pieces[k & 1].set(p, next_index(answer));
+          pieces[k & 1].set(p, *reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 8), next_index(answer));
           fence_proxy_async_smem();  // the answer is read before another is asked for
           mbar_arrive(bar(Gm::BAR_NEXT + (k & 1)));
         } while (pieces[k & 1].any >= 0);

@@ -1,4 +1,5 @@
-// How a latent prefill's query block cuts its keys into parts.
+// How a latent prefill's query block cuts its keys into parts, and which (sequence, head)
+// units' blocks are launched together.
 #pragma once
 
 namespace da {
@@ -15,6 +16,13 @@ __host__ __device__ constexpr int prefill_block_parts(int tiles, int parts) {
 // The first of its tiles in part i, of nparts nearly equal ones.
 __host__ __device__ constexpr int prefill_part_begin(int tiles, int i, int nparts) {
   return (int)((long long)tiles * i / nparts);
+}
+
+// Units of a launch group: as many as have their K and V, of the longest sequence's tokens, in about
+// 96 MB of L2 together.
+__host__ __device__ constexpr int prefill_group(int longest, int D, long long units) {
+  const long long g = (96LL << 20) / (4LL * D * (longest < 1 ? 1 : longest));
+  return (int)(g < 1 ? 1 : g < units ? g : units);
 }
 
 }  // namespace da

@@ -213,3 +213,22 @@ def test_the_capacity_does_not_change_how_keys_are_cut():
     out = binding.latent_prefill_contig(dev_bf16(c["q"]), *far, dev_i32(c["lens"]), scale=c["scale"])
     assert np.array_equal(host_bits(out), first)
     assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("lens", [[300, 0, 513, 129, -7], [9000, 1, 2, 3, 4]])
+def test_launch_groups_by_the_longest_sequence(lens):
+    """A capacity that makes several launch groups: every block is still taken exactly once."""
+    H, D, q_len, ctx = 11, 128, 300, 8000
+    c = make(15, [max(min(L, ctx), 0) for L in lens], q_len, H, D, max(min(max(lens), ctx), 1))
+    first = run(c)
+    c["lens"] = np.asarray(lens, np.int32)
+    if max(lens) <= ctx:
+        check(first, c, "groups")
+    far = [torch.full((len(lens), ctx, *x.shape[2:]), float("nan"), dtype=torch.bfloat16, device="cuda") for x in
+           (c["k"], c["pe"], c["v"])]
+    for t, n in zip(far, ("k", "pe", "v")):
+        t[:, :c[n].shape[1]] = dev_bf16(c[n])
+    out = torch.full((len(lens), q_len, H, D), float("nan"), device="cuda", dtype=torch.bfloat16)
+    binding.latent_prefill_contig(dev_bf16(c["q"]), *far, dev_i32(c["lens"]), scale=c["scale"], out=out)
+    assert np.array_equal(host_bits(out), first)
+    assert binding.device_error() == 0

@@ -14,10 +14,13 @@ def cut(tmp_path_factory):
     src, out = d / "cut.cpp", d / "cut.so"
     src.write_text('#define __host__\n#define __device__\n#include "prefill_cut.cuh"\nextern "C" int block_parts(int t, int p) '
                    '{ return da::prefill_block_parts(t, p); }\nextern "C" int part_begin(int t, int i, int n) '
-                   '{ return da::prefill_part_begin(t, i, n); }\n')
+                   '{ return da::prefill_part_begin(t, i, n); }\nextern "C" int group(int longest, int D, long long units) '
+                   '{ return da::prefill_group(longest, D, units); }\n')
     subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-shared", "-fPIC", "-I" + CSRC, str(src), "-o", str(out)],
                    check=True)
-    return ctypes.CDLL(str(out))
+    lib = ctypes.CDLL(str(out))
+    lib.group.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_longlong]
+    return lib
 
 
 def test_never_more_parts_than_the_launch_has(cut):
@@ -37,3 +40,13 @@ def test_equal_parts_that_cover_the_block(cut):
             assert ends[0] == 0 and ends[-1] == tiles and max(size) - min(size) <= 1
             assert n == min(parts, -(-tiles // 4)) and min(size) >= 1
     assert cut.block_parts(24, 19) == 6 and cut.block_parts(1024, 19) == 19
+
+
+def test_launch_groups(cut):
+    g = cut.group
+    assert g(4096, 128, 32) == 32 and g(131072, 128, 32) == 1 and g(8192, 128, 32) == 24
+    for longest in (0, 1, 128, 3000, 2 ** 31 - 1):
+        for D in (64, 128):
+            for units in (1, 7, 1 << 20):
+                n = g(longest, D, units)
+                assert 1 <= n <= units and (n == 1 or n * 4 * D * max(longest, 1) <= 96 << 20)
