@@ -1,5 +1,6 @@
 """Builds libdecode_attn.so in-tree with nvcc for sm_103a, and the binding's CPython extension with the host compiler
-(no CMake; the units compile side by side)."""
+(no CMake; the units compile side by side).  The library needs nvcc and its host compiler alone; the extension needs the
+headers of Python and of an installed PyTorch, and is left out where there are none."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -17,6 +18,7 @@ LIB = os.path.join(PKG, "libdecode_attn.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("decode_attn.cu", "latent_attn.cu", "cache_ops.cu")]
 EXT = os.path.join(PKG, "_binding_ext" + sysconfig.get_config_var("EXT_SUFFIX"))
 EXT_SOURCE = os.path.join(CSRC, "binding_ext.cpp")
+EXT_STAMP = os.path.join(PKG, "_build", "binding_ext.torch")  # the PyTorch that EXT was compiled against
 HEADERS = [os.path.join(ROOT, "include", "decode_attn.h")] + [
     os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cuh", ".h"))
 ]
@@ -40,9 +42,34 @@ def link_command(out: str, objects) -> list:
             *objects]
 
 
+def torch_dir():
+    """The installed PyTorch's folder, or None (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def torch_tag():
+    """What tells one installed PyTorch from another."""
+    torch = torch_dir()
+    version = os.path.join(torch, "version.py")
+    return torch + "\n" + (open(version).read() if os.path.exists(version) else "")
+
+
+def ext_needs():
+    """Why the extension cannot be built here, or None."""
+    torch = torch_dir()
+    if torch is None:
+        return "PyTorch is not installed"
+    for header in (os.path.join(torch, "include", "ATen", "core", "Tensor.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return "no " + header
+    return None
+
+
 def ext_command(out: str) -> list:
-    """Compiles the binding's extension against the installed PyTorch (found without importing it)."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """Compiles the binding's extension against the installed PyTorch."""
+    torch = torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
@@ -52,38 +79,63 @@ def ext_command(out: str) -> list:
             "-ltorch_python", "-ldl"]
 
 
-def up_to_date() -> bool:
-    def newer(out, sources):
-        return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in sources)
-    return newer(LIB, SOURCES + HEADERS) and newer(EXT, [EXT_SOURCE, HEADERS[0]])
+def _newer(out, sources) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in sources)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, SOURCES + HEADERS)
+
+
+def ext_up_to_date() -> bool:
+    return (_newer(EXT, [EXT_SOURCE, HEADERS[0]]) and os.path.exists(EXT_STAMP) and
+            open(EXT_STAMP).read() == torch_tag())
 
 
 def _run(cmd: list):
     return subprocess.run(cmd, capture_output=True, text=True)
 
 
+def _install(made: str, out: str):
+    shutil.copy(made, out + ".tmp")
+    os.replace(out + ".tmp", out)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; returns its path."""
-    if not force and up_to_date():
+    """Compile what is older than its sources: the library, and the extension where it can be built (compiled against
+    another PyTorch counts as old).  Returns the library's path; a failing extension leaves the library in place."""
+    missing = ext_needs()
+    want_lib = force or not library_up_to_date()
+    want_ext = missing is None and (force or not ext_up_to_date())
+    if missing is not None:
+        print(f"the binding's extension is not built: {missing}")
+    if not want_lib and not want_ext:
         return LIB
-    with tempfile.TemporaryDirectory() as tmpdir:
-        objects = [os.path.join(tmpdir, os.path.basename(src) + ".o") for src in SOURCES]
-        ext = os.path.join(tmpdir, "ext.so")
-        commands = [*map(nvcc_command, objects, SOURCES), ext_command(ext)]
-        with concurrent.futures.ThreadPoolExecutor(len(commands)) as pool:
-            done = list(pool.map(_run, commands))
-        if all(res.returncode == 0 for res in done):
-            done.append(_run(link_command(os.path.join(tmpdir, "lib.so"), objects)))
-        if all(res.returncode == 0 for res in done):
-            for made, out in ((os.path.join(tmpdir, "lib.so"), LIB), (ext, EXT)):
-                shutil.copy(made, out + ".tmp")
-                os.replace(out + ".tmp", out)
-    for res in done:
+
+    def report(res):
         if verbose or res.returncode != 0:
             print(" ".join(res.args))
             print(res.stdout + res.stderr)
-    if any(res.returncode != 0 for res in done):
-        raise RuntimeError("nvcc failed building libdecode_attn.so")
+        return res.returncode == 0
+
+    with tempfile.TemporaryDirectory() as tmpdir:
+        objects = [os.path.join(tmpdir, os.path.basename(src) + ".o") for src in SOURCES] if want_lib else []
+        ext = os.path.join(tmpdir, "ext.so")
+        with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as pool:
+            ext_job = pool.submit(_run, ext_command(ext)) if want_ext else None
+            jobs = [pool.submit(_run, nvcc_command(out, src)) for out, src in zip(objects, SOURCES)]
+        if want_lib:
+            lib = os.path.join(tmpdir, "lib.so")
+            if not all([report(job.result()) for job in jobs]) or not report(_run(link_command(lib, objects))):
+                raise RuntimeError("nvcc failed building libdecode_attn.so")
+            _install(lib, LIB)
+        if ext_job:
+            if not report(ext_job.result()):
+                raise RuntimeError("the host compiler failed building the binding's extension")
+            _install(ext, EXT)
+            os.makedirs(os.path.dirname(EXT_STAMP), exist_ok=True)
+            with open(EXT_STAMP, "w") as f:
+                f.write(torch_tag())
     return LIB
 
 
