@@ -502,7 +502,10 @@ def rope_apply(x, positions, inv_freq, offset: int = 0, interleaved: bool = Fals
     """Rotary positions: x [T, H, D] or [B, T, H, D] (bf16, fp16 or fp32; tokens and heads may be strided),
     positions int32 [T] or [B, T], inv_freq float64 [rot / 2] (rope_inv_freq).  Elements [offset, offset + rot)
     of every head are rotated, pairs (j, j + rot / 2) or, interleaved, (2j, 2j + 1); with backward, the gradient
-    of that.  out: x itself (in place) or a tensor of x's shape.  Returns out."""
+    of that.  out: x itself (in place) or a tensor of x's shape.  Returns out.
+
+    Autograd does not record the call: what it returns is detached from x.  To train through it, call it in the
+    forward of a torch.autograd.Function and with backward=True in its backward."""
     return (_ext_module or _ext()).rope_apply(x, positions, inv_freq, offset, interleaved, magnitude, backward, out,
                                               stream)
 

@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -192,6 +193,18 @@ void call(const char* fn, F f) {
   if (st != DA_OK) throw Failed{fn, st};
 }
 
+// The call has written t (null: nothing): autograd notices where it had saved it.
+void written(const Tensor* t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
+// Autograd records none of these calls, so what it tracks cannot be written by one.
+void not_tracked(const Tensor* t, const char* name) {
+  if (t && t->requires_grad() && at::GradMode::is_enabled())
+    throw Bad(std::string(name) + ": it requires a gradient, and autograd does not record this call; write into a "
+              "detached tensor or under torch.no_grad()");
+}
+
 void need_library() {
   if (!g_lib.handle) throw std::runtime_error("the library is not open");
 }
@@ -244,6 +257,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* given = opt(a[7], "out");
     if (given && (given->scalar_type() != type || given->sizes() != shape || cuda_index(*given) != dev))
       mismatch(*given, "out", type, shape, dev, "");
+    not_tracked(given, "out");
     const int64_t xt = token_stride(x, "x", lead), ot = given ? token_stride(*given, "out", lead) : H * D;
     on_current(dev);
     Stream st(a[8], dev);
@@ -256,6 +270,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return g_lib.rope_apply(ptr(x), ptr(out), ptr<int>(positions), ptr<double>(w), positions.numel(), Hi, Di, off,
                               roti, il, mag, back, dtype, xt, xh, ot, oh, st.raw);
     });
+    written(given);
     return given ? same(a[7]) : THPVariable_Wrap(out);
   });
 }
@@ -327,6 +342,10 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       il = truth(a[11]);
       mag = real(a[12]);
     }
+    not_tracked(&k, "k");
+    not_tracked(v, "v");
+    not_tracked(ks, "k_scale");
+    not_tracked(vs, "v_scale");
     on_current(dev);
     Stream st(a[13], dev);
     const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k");
@@ -355,6 +374,7 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                                      il, mag, ptr(k), ptr(v), st.raw);
       });
     }
+    for (const Tensor* t : {&k, v, ks, vs}) written(t);
     Py_RETURN_NONE;
   });
 }
@@ -377,6 +397,8 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (ko) plain(*ko, "k_out", at::kBFloat16, dims(B, n, H, D), dev);
     if (!v && vo) throw Bad("v_out: no v to read");
     if (vo) plain(*vo, "v_out", at::kBFloat16, dims(B, n, H, D), dev);
+    not_tracked(ko, "k_out");
+    not_tracked(vo, "v_out");
     on_current(dev);
     Stream st(a[11], dev);
     const auto opts = k.options().dtype(at::kBFloat16);
@@ -409,6 +431,8 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                                      slab, cols, slabs, cap, ptr(kt), vp, st.raw);
         });
     }
+    written(ko);
+    written(vo);
     PyObject* kr = ko ? same(a[9]) : THPVariable_Wrap(kt);
     PyObject* vr = vo || !v ? same(a[10]) : THPVariable_Wrap(vt);
     PyObject* r = kr && vr ? PyTuple_Pack(2, kr, vr) : nullptr;
@@ -442,6 +466,7 @@ PyObject* latent_attn(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (ws && (!ws->is_contiguous() || cuda_index(*ws) != dev))
       throw Bad("workspace: expected a contiguous tensor on cuda:" + std::to_string(dev));
     const float scale = real(a[5]);
+    not_tracked(given, "out");
     on_current(dev);
     Stream st(a[8], dev);
     const Tensor out = given ? *given : at::empty(dims(B, n, H, R), q.options());
@@ -468,6 +493,7 @@ PyObject* latent_attn(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                                         ptr(out), st.raw);
       });
     }
+    written(given);
     return given ? same(a[7]) : THPVariable_Wrap(out);
   });
 }
@@ -510,6 +536,7 @@ PyObject* latent_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (given) plain(*given, "out", at::kBFloat16, dims(B, n, H, D), dev);
     const float scale = real(a[5]);
     const int ctxi = small(ctx, "k_nope");
+    not_tracked(given, "out");
     on_current(dev);
     Stream st(a[7], dev);
     const Tensor out = given ? *given : at::empty(dims(B, n, H, D), q.options());
@@ -522,6 +549,7 @@ PyObject* latent_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                                          ctxi, kst.first, kst.second, pst.first, scale,
                                          bytes > 0 ? ptr(work) : nullptr, bytes, ptr(out), st.raw);
     });
+    written(given);
     return given ? same(a[6]) : THPVariable_Wrap(out);
   });
 }

@@ -205,3 +205,19 @@ def test_filled_reads_refuse_what_reads_refuse(clib, name):
                               (2, 4, 64, K, 1), (0, 4, 64, A, 0), (2, 0, 64, A, 0)):
         args = (K, V, *scales, *table, None, A, B, n, 2, D, *where, ko, A + (1 << 30), None)
         assert f(*args) == g(*args) == want
+
+
+def test_outputs_that_autograd_tracks_are_refused():
+    torch = pytest.importorskip("torch")
+    from gqa_split_kv_gb300 import binding
+    x = torch.zeros(4, 2, 8, requires_grad=True)
+    pos, w = torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.float64)
+    for out in (x, x * 1):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            binding.rope_apply(x.detach(), pos, w, out=out)
+    with pytest.raises(ValueError, match="CUDA"):  # under no_grad only the device is wrong here
+        with torch.no_grad():
+            binding.rope_apply(x, pos, w, out=x)
+    k = torch.zeros(1, 4, 1, 8, dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(ValueError, match="k: it requires a gradient"):
+        binding.kv_write_contig(k.detach(), None, k, None)
