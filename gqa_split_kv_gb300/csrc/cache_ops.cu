@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
 // items a thread the batch takes 84 us, with both tensors' loads before the first store 78.6.
 template <bool PAGED, bool INT8, bool FILL>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheParams p) {
-  const int nblk = (p.n + p.tb - 1) / p.tb;
+  const int nblk = (int)(((long long)p.n + p.tb - 1) / p.tb);
   const int b = blockIdx.x / nblk, i0 = (blockIdx.x - b * nblk) * p.tb;
   pdl_launch_dependents();
   pdl_wait_primary();
@@ -595,10 +595,10 @@ int check_cache(const CacheParams& p, bool paged, bool int8, long long cap) {
 
 // Bytes of one tensor of the cache, and of its scales.
 long long cache_bytes(const CacheParams& p, bool paged, bool int8) {
-  return (long long)(paged ? p.num_pages : p.B) * p.slab * p.Hkv * p.D * (int8 ? 1 : 2);
+  return product(paged ? p.num_pages : p.B, p.slab, p.Hkv, p.D, int8 ? 1 : 2);
 }
 long long scale_bytes(const CacheParams& p, bool paged) {
-  return (long long)(paged ? p.num_pages : p.B) * p.slab * p.Hkv * 4;
+  return product(paged ? p.num_pages : p.B, p.slab, p.Hkv, 4);
 }
 
 int check_cache_pointers(const CacheParams& p, bool paged, bool int8, bool has_v) {
@@ -659,16 +659,16 @@ int write_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_
   const long long width = (long long)p.Hkv * p.D;
   const bool has_v = p.v_new != nullptr;
   if (!p.k_new || !aligned(p.k_new, 16) || !aligned(p.v_new, 16)) return DA_ERR_INVALID_ARG;
-  const long long far = 1LL << 40;  // strides whose products with the sizes stay in 64 bits
-  if (p.k_stride < width || p.k_stride % 8 || p.k_stride > far ||
-      (has_v && (p.v_stride < width || p.v_stride % 8 || p.v_stride > far)))
+  const long long far = 1LL << 40, new_tokens = (long long)p.B * p.n;
+  if (p.k_stride < width || p.k_stride % 8 || p.k_stride > far || !reachable(new_tokens, p.k_stride) ||
+      (has_v && (p.v_stride < width || p.v_stride % 8 || p.v_stride > far || !reachable(new_tokens, p.v_stride))))
     return DA_ERR_INVALID_ARG;
   if (!has_v && p.v) return DA_ERR_INVALID_ARG;
   if (int e = check_cache_pointers(p, paged, int8, has_v)) return e;
   {
     // nothing that is written may be read by the same call, nor written twice
-    const long long tokens = (long long)p.B * p.n - 1, kn = (tokens * p.k_stride + width) * 2,
-                    vn = (tokens * p.v_stride + width) * 2, cn = cache_bytes(p, paged, int8), sn = scale_bytes(p, paged);
+    const long long tokens = new_tokens - 1, kn = (tokens * p.k_stride + width) * 2,
+                    vn = has_v ? (tokens * p.v_stride + width) * 2 : 0, cn = cache_bytes(p, paged, int8), sn = scale_bytes(p, paged);
     const void* dst[4] = {p.k, p.v, p.ks, p.vs};
     const long long bytes[4] = {cn, cn, sn, sn};
     for (int i = 0; i < 4; ++i) {
@@ -700,7 +700,7 @@ int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t
     return DA_OK;
   }
   {
-    const long long on = (long long)p.B * p.n * p.Hkv * p.D * 2, cn = cache_bytes(p, paged, int8),
+    const long long on = product(p.B, p.n, p.Hkv, p.D, 2), cn = cache_bytes(p, paged, int8),
                     sn = scale_bytes(p, paged);
     const void *out[2] = {p.k_out, p.v_out}, *src[4] = {p.k, p.v, p.ks, p.vs};
     for (int i = 0; i < 2; ++i)
@@ -715,9 +715,10 @@ int read_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_t
   const int per_row = p.Hkv * p.D / (int8 ? 16 : 8);
   int tb = kThreads * 4 / per_row;
   tb = tb < 1 ? 1 : tb > 64 ? 64 : tb;
-  while (tb > 1 && tb * per_row > kThreads && (long long)p.B * ((p.n + tb - 1) / tb) < 8LL * sms) tb = (tb + 1) / 2;
+  auto blocks = [&](int t) { return p.B * (((long long)p.n + t - 1) / t); };
+  while (tb > 1 && tb * per_row > kThreads && blocks(tb) < 8LL * sms) tb = (tb + 1) / 2;
   p.tb = tb;
-  const long long grid = (long long)p.B * ((p.n + p.tb - 1) / p.tb);
+  const long long grid = blocks(tb);
   if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   auto launch = [&](auto in_pages, auto in_int8) {
     constexpr bool P = decltype(in_pages)::value, I = decltype(in_int8)::value;
@@ -777,10 +778,10 @@ extern "C" int rope_apply(const void* x, void* out, const int* positions, const 
   const int size = dtype == DA_F32 ? 4 : 2;
   if (!x || !out || !positions || !aligned(x, size) || !aligned(out, size) || !aligned(positions, 4))
     return DA_ERR_INVALID_ARG;
-  const long long far = 1LL << 40;  // strides whose products with the sizes stay in 64 bits
-  if (tokens > 0x7fffffffLL || x_token_stride < 0 || x_head_stride < 0 || x_token_stride > far ||
-      x_head_stride > far || out_token_stride < 0 || out_head_stride < 0 || out_token_stride > far ||
-      out_head_stride > far)
+  const long long far = 1LL << 40;
+  if (tokens > 0x7fffffffLL || x_token_stride > far || x_head_stride > far || out_token_stride > far ||
+      out_head_stride > far || !reachable(tokens, x_token_stride) || !reachable(num_heads, x_head_stride) ||
+      !reachable(tokens, out_token_stride) || !reachable(num_heads, out_head_stride))
     return DA_ERR_INVALID_ARG;
   if (!rows_apart(tokens, num_heads, head_dim, out_token_stride, out_head_stride)) return DA_ERR_INVALID_ARG;
   const bool same = x == out;

@@ -77,6 +77,20 @@ int encode_map_t(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle sw
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Whether a tensor can have n steps of this stride (in elements): 2^56 of them at most, more than any memory
+// holds, so that sums and byte counts of such extents stay in 64 bits.
+bool reachable(long long n, long long stride) {
+  return stride >= 0 && (stride == 0 || n <= (1LL << 56) / stride);
+}
+
+// The product of sizes that are not negative, at most 2^60.
+template <typename... T>
+long long product(T... n) {
+  long long p = 1;
+  for (long long x : {(long long)n...}) p = x == 0 || p == 0 ? 0 : p > (1LL << 60) / x ? 1LL << 60 : p * x;
+  return p;
+}
+
 // Whether [a, a + an) and [b, b + bn) share a byte (null pointers: no).
 bool overlap(const void* a, long long an, const void* b, long long bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);

@@ -111,18 +111,18 @@ int latent_call(bool paged, const void* q, const void* cache, const int* page_ta
   const int limit = R == 128 ? latent_batch_limit<128>(N) : R == 256 ? latent_batch_limit<256>(N)
                                                                      : latent_batch_limit<512>(N);
   if (B > limit) return DA_ERR_UNSUPPORTED;
-  int dev, sms, optin;
-  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
-  if (!workspace || workspace_bytes < latent_workspace(B, rows, R, sms)) return DA_ERR_WORKSPACE;
-  if (!aligned(workspace, 16)) return DA_ERR_INVALID_ARG;
   {
     // what is written overlaps nothing else of the call
-    const long long qn = (long long)B * rows * W * 2, on = (long long)B * rows * R * 2;
-    const long long cn = (paged ? (long long)num_pages * page_size : B * max_len) * W * 2;
+    const long long qn = product(B, rows, W, 2), on = product(B, rows, R, 2);
+    const long long cn = paged ? product(num_pages, page_size, W, 2) : product(B, max_len, W, 2);
     if (overlap(out, on, q, qn) || overlap(out, on, cache, cn) || overlap(out, on, workspace, workspace_bytes) ||
         overlap(workspace, workspace_bytes, q, qn) || overlap(workspace, workspace_bytes, cache, cn))
       return DA_ERR_INVALID_ARG;
   }
+  int dev, sms, optin;
+  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
+  if (!workspace || workspace_bytes < latent_workspace(B, rows, R, sms)) return DA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DA_ERR_INVALID_ARG;
 
   LatentParams prm;
   std::memset(&prm, 0, sizeof(prm));
@@ -318,14 +318,17 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
   }
   if (!k_nope || !k_rope || !v || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16))
     return DA_ERR_INVALID_ARG;
-  const long long far = 1LL << 40;  // strides whose products with the sizes stay in 64 bits
-  if (kv_head_stride > far || kv_token_stride > far || rope_token_stride > far) return DA_ERR_INVALID_ARG;
+  const long long far = 1LL << 40, cached = (long long)batch * max_ctx;
+  if (kv_head_stride > far || kv_token_stride > far || rope_token_stride > far || !reachable(num_heads, kv_head_stride) ||
+      !reachable(cached, kv_token_stride) || !reachable(cached, rope_token_stride))
+    return DA_ERR_INVALID_ARG;
   if (kv_head_stride < head_dim || kv_head_stride % 8 || kv_token_stride % 8 ||
       kv_token_stride < (num_heads - 1) * kv_head_stride + head_dim || rope_token_stride < 64 || rope_token_stride % 8)
     return DA_ERR_INVALID_ARG;
   {
-    const long long rows = (long long)batch * q_len * num_heads, on = rows * head_dim * 2, qn = rows * (head_dim + 64) * 2;
-    const long long tokens = (long long)batch * max_ctx - 1;
+    const long long on = product(batch, q_len, num_heads, head_dim, 2),
+                    qn = product(batch, q_len, num_heads, head_dim + 64, 2);
+    const long long tokens = cached - 1;
     const long long kn = (tokens * kv_token_stride + (num_heads - 1) * kv_head_stride + head_dim) * 2;
     const void* in[4] = {q, k_nope, v, k_rope};
     const long long bytes[4] = {qn, kn, kn, (tokens * rope_token_stride + 64) * 2};

@@ -221,3 +221,26 @@ def test_outputs_that_autograd_tracks_are_refused():
     k = torch.zeros(1, 4, 1, 8, dtype=torch.bfloat16, requires_grad=True)
     with pytest.raises(ValueError, match="k: it requires a gradient"):
         binding.kv_write_contig(k.detach(), None, k, None)
+
+
+FAR, MOST = 1 << 40, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("kw", [dict(xt=FAR), dict(ot=FAR), dict(xt=FAR, ot=FAR), dict(xt=1 << 33), dict(ot=1 << 33)])
+def test_rope_refuses_extents_past_64_bits(clib, kw):
+    """2^31 tokens 2^40 elements apart: no such tensor exists, and its size would not fit the overlap checks."""
+    assert rope(clib, **{**dict(T=MOST, xt=128, ot=128, out=A + (1 << 45)), **kw}) == 1
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("paged", [False, True])
+def test_cache_calls_refuse_extents_past_64_bits(clib, paged, int8):
+    far = dict(paged=paged, int8=int8, B=MOST, n=1, maxlen=64)
+    assert write(clib, **far, ks=FAR) == 1 and write(clib, **far, vs=1 << 32) == 1
+    # a cache whose bytes pass 2^64 still shares them with whatever lies behind its start
+    big = dict(paged=paged, int8=int8, H=1024, D=1024, ks=1 << 20, vs=1 << 20, ps=1 << 30, maxp=1, npages=MOST,
+               maxlen=MOST, B=2 if paged else MOST)
+    assert write(clib, **big, k_new=K + (1 << 30)) == 1 and write(clib, **big, v_new=V + (1 << 30)) == 1
+    if paged or int8:
+        del big["ks"], big["vs"]
+        assert read(clib, **big, n=1, ko=K + (1 << 30)) == 1 and read(clib, **big, n=1, vo=V + (1 << 30)) == 1

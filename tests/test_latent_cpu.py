@@ -151,3 +151,12 @@ def test_binding_refuses_mismatched_tensors():
             binding.latent_prefill_contig(*a, scale=1.0)
     with pytest.raises(binding.DecodeAttnError):
         binding.latent_max_batch(4, 100)
+
+
+def test_extents_past_64_bits_are_refused(clib):
+    most, far = 2 ** 31 - 1, 1 << 40
+    assert prefill(clib, B=1 << 20, ctx=most, ts=far) == 1 and prefill(clib, B=1 << 20, ctx=most, ps=far) == 1
+    assert prefill(clib, H=1 << 20, n=1, hs=far, ts=far) == 1
+    # pools whose bytes pass 2^64 still share them with whatever lies behind their start
+    big = dict(paged=True, B=1, ps=1 << 30, npages=most, maxp=1, maxlen=64)
+    assert attn(clib, **big, out=K + (1 << 43)) == 1 and attn(clib, **big, ws=K + (1 << 43)) == 1
