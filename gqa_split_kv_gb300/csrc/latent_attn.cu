@@ -308,6 +308,7 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
   const int BQ = LatentPrefillGeo<128>::BQ;
   const long long nqb = ((long long)q_len + BQ - 1) / BQ;
   if (nqb * batch > 0x7fffffffLL / num_heads) return DA_ERR_UNSUPPORTED;
+  if (max_ctx > 0x7fffffff - BQ) return DA_ERR_UNSUPPORTED;  // a token past the last tile still counts in 32 bits
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (max_ctx == 0) {
     if (cudaMemsetAsync(out, 0, (size_t)batch * q_len * num_heads * head_dim * 2, st) != cudaSuccess) {

@@ -521,7 +521,8 @@ int latent_max_batch(int q_len, int num_heads, int latent_dim);
  *  k_rope     bf16 [batch, max_ctx, 64] with rope_token_stride elements between tokens (a multiple
  *             of 8): the last 64 columns of a latent cache will do
  *  out        bf16 [batch, q_len, num_heads, head_dim]
- *  head_dim   64 or 128; seq_lens int32 [batch] clamped to [0, max_ctx], or NULL (max_ctx).
+ *  head_dim   64 or 128; seq_lens int32 [batch] clamped to [0, max_ctx], or NULL (max_ctx); max_ctx
+ *             below 2^31 - 256
  *  workspace  NULL, or latent_prefill_workspace_bytes(...) bytes, 16-byte aligned, of any content:
  *             with it, the keys of few query blocks are split over CTAs and joined in fp32.  Calls
  *             that share it must not overlap on the GPU (two captured graphs included).

@@ -154,9 +154,15 @@ def test_binding_refuses_mismatched_tensors():
 
 
 def test_extents_past_64_bits_are_refused(clib):
-    most, far = 2 ** 31 - 1, 1 << 40
-    assert prefill(clib, B=1 << 20, ctx=most, ts=far) == 1 and prefill(clib, B=1 << 20, ctx=most, ps=far) == 1
+    most, far, ctx = 2 ** 31 - 1, 1 << 40, 2 ** 31 - 512
+    assert prefill(clib, B=1 << 20, ctx=ctx, ts=far) == 1 and prefill(clib, B=1 << 20, ctx=ctx, ps=far) == 1
     assert prefill(clib, H=1 << 20, n=1, hs=far, ts=far) == 1
     # pools whose bytes pass 2^64 still share them with whatever lies behind their start
     big = dict(paged=True, B=1, ps=1 << 30, npages=most, maxp=1, maxlen=64)
     assert attn(clib, **big, out=K + (1 << 43)) == 1 and attn(clib, **big, ws=K + (1 << 43)) == 1
+
+
+@pytest.mark.parametrize("ctx", [2 ** 31 - 1, 2 ** 31 - 128])
+def test_prefill_refuses_lengths_whose_last_tile_passes_32_bits(clib, ctx):
+    """Keys, values and shared parts in one tensor of 64 columns would fit the card at 2^31 tokens."""
+    assert prefill(clib, B=1, H=1, D=64, ctx=ctx, ts=64, hs=64, ps=64, k=K, v=K, pe=K, out=A + (1 << 30)) == 2
