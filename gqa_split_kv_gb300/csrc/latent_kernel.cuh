@@ -93,6 +93,12 @@ struct LatentParams {
 // 32768 tokens: 69.3 us with 4, 61.5 with 8, 63.1 with 12; 16 sequences 43.3, 42.5, 42.1).
 constexpr int kLatentGap = 8;
 
+// Sequence b's length, before the plan clamps it.
+template <typename Params>
+__device__ __forceinline__ auto latent_length(const Params& p) {
+  return [&p](int b) { return p.seq_lens ? load_dependent(p.seq_lens + b) : p.max_len; };
+}
+
 // The cut of the line into `ranges` equal ranges.
 __device__ __forceinline__ Plan latent_plan(int B, int U, int ranges, const int* P) {
   Plan pl;
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(LatentGeo<R, N>::NTHREADS, 1) latent_kernel(co
     // this CTA's range of the line and its pieces
     int* lens = reinterpret_cast<int*>(smem + Gm::OFF_U);
     int* P = lens + p.B;
-    build_plan_arrays(p.seq_lens, p.B, p.max_len, kLatentGap, lens, P, 0, Gm::NTHREADS);
+    build_plan_arrays(latent_length(p), p.B, p.max_len, kLatentGap, lens, P, 0, Gm::NTHREADS);
     if (threadIdx.x == 0) {
       const Plan pl = latent_plan(p.B, p.U, p.ranges, P);
       const int r = blockIdx.x;
@@ -686,7 +692,7 @@ __global__ void __launch_bounds__(512, 1) latent_combine_kernel(const LatentComb
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float kNegInf = -__int_as_float(0x7f800000);
   pdl_launch_dependents();
-  build_plan_arrays(p.seq_lens, p.B, p.max_len, kLatentGap, lens, P, 0, Cg::NTHREADS);
+  build_plan_arrays(latent_length(p), p.B, p.max_len, kLatentGap, lens, P, 0, Cg::NTHREADS);
   const Plan pl = latent_plan(p.B, p.U, p.ranges, P);
   if (warp == 0) {
     int count = 0;
