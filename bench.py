@@ -70,8 +70,10 @@ def parse_args():
 
 # The sources each kind of workload runs (the ncu figures in profiles/ are tied to them).
 KERNEL_SOURCES = {
-    "decode": ("decode_attn.cu", "plan.cuh", "ptx.cuh", "split_kernel.cuh", "combine_kernel.cuh"),
-    "prefill": ("prefill_host.cuh", "prefill_kernel.cuh", "prefill_tc.cuh", "tc05.cuh", "ptx.cuh"),
+    "decode": ("decode_attn.cu", "plan.cuh", "ptx.cuh", "split_kernel.cuh", "combine_kernel.cuh", "device_error.cuh",
+               "host_util.cuh"),
+    "prefill": ("prefill_host.cuh", "prefill_kernel.cuh", "prefill_tc.cuh", "tc05.cuh", "ptx.cuh", "device_error.cuh",
+                "host_util.cuh"),
 }
 
 
