@@ -461,7 +461,8 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "plain", f
                   original_ctx: float = 4096, low_turns: float = 1.0, high_turns: float = 32.0, device=None):
     """Radians a position of each of the rot_dim / 2 rotated pairs: a float64 tensor on device (default: the
     current CUDA device) for rope_apply and kv_write_*.  scaling "plain", "linear", "base" or "by_parts"
-    (include/decode_attn.h, da_rope_scaling)."""
+    (include/decode_attn.h, da_rope_scaling; by_parts mixes linearly in a pair's turns: a model that does so in the
+    pair's index brings its own table, and its magnitude, as every scaling's, is an argument of the calls)."""
     import numpy as np
     import torch
     if scaling not in _ROPE_SCALING:

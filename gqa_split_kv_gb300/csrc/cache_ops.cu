@@ -363,9 +363,9 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
 // once.  The row's maximum is a shuffle over its lanes.  Bound by HBM for a chunk and by
 // latency for a step: the first rows' loads go out before the lengths, pages and cosines,
 // which are looked up once a token.  A decode step of 64 sequences (8 heads x 128, int8 pages)
-// with its read back: 5.9 us, two launches; 4096 tokens likewise 19.4 us, floor 7.6; 32768
-// tokens 49.3 us here, floor 30.4 (bf16 48.0, 40.1), where four-chunk rows take 22 instructions an element
-// and one-chunk rows took 31.
+// with its read back: 6.0 us, two launches; 4096 tokens likewise 20.2 us, floor 7.6; 32768
+// tokens 53.0 us here, floor 30.4 (bf16 48.0, 40.1), where four-chunk rows take 22 instructions
+// an element and one-chunk rows took 31.
 constexpr int kMaxTokens = 16;  // tokens a CTA takes at a time, at most
 template <bool PAGED, bool INT8, int CPL, bool PAIRED>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p) {
@@ -616,8 +616,8 @@ template <bool PAGED, bool INT8>
 int launch_write(CacheParams& p, int sms, cudaStream_t st) {
   // Few rows: a chunk a lane, for more loads at once.  Many (20 an SM): two chunks, and int8
   // four where the 16 tokens of a CTA still occupy it, as a row's fixed work is a lane's (8 heads x 128,
-  // int8 / bf16, us: 128 tokens 3.1 / 2.9, 3.4 / 2.8 with more chunks; 256 tokens 4.6 / 3.9 -> 3.5 /
-  // 2.8; 32768 tokens int8 56.7 with two, 49.4 with four, where bf16 takes 48.0 and 51.0)
+  // int8 / bf16, us: 128 tokens 3.2 / 2.9, 3.6 / 2.7 with more chunks; 256 tokens 4.4 / 3.4 -> 3.8 /
+  // 2.9; 32768 tokens int8 56.0 with two, 53.0 with four, where bf16 takes 48.0 and 51.0)
   const int nchunk = p.D / 8;
   const int rows = p.Hkv * (p.v_new ? 2 : 1), np = p.r.inv_freq ? p.r.rot / 2 : 0;
   const bool many = (long long)p.B * p.n * rows >= 20LL * sms;

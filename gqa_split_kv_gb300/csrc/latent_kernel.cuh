@@ -46,9 +46,9 @@
 // guards every MMA, 45 cycles each, behind elect.sync 23, which at N <= 32 is less than the
 // tensor core takes (batch below: 57.8 -> 47.9 us).  Waits are bounded as in prefill_tc.cuh.
 //
-// Bound and measured (bf16, R = 512).  16 sequences up to 8192 tokens, 128 heads: 42.1
+// Bound and measured (bf16, R = 512).  16 sequences up to 8192 tokens, 128 heads: 41.0
 // us, where HBM needs 12.3 and the tensor cores 9.6; 64 sequences of 1 to 32768 tokens, 64
-// heads: 61.6 us, HBM 36.0; one sequence of 4096 tokens, 16 heads: 10.7 us.  A tile of 64
+// heads: 61.6 us, HBM 36.0; one sequence of 4096 tokens, 16 heads: 10.8 us.  A tile of 64
 // rows takes 1.85 us: the round through its two ring slots (load 1.5 us, S 0.6, softmax
 // 0.5, O 0.4, overlapping by units), not HBM (85 MB of it are read once, by the other row
 // tile from L2), with the tensor cores 35% busy.  Around the tiles: 5 us to the first

@@ -4,10 +4,10 @@
 // Pair j of a head is turned by the angle p w_j (position p, w_j radians a position).
 // With f = frac(w_j / 2 pi) as a 64-bit fixed-point number F = f 2^64, the turn's
 // fraction is the wrapped integer product p F mod 2^64: whole turns fall off the top
-// by themselves and the error stays p 2^-53 f of a turn (the rounding of w_j / 2 pi)
-// at any 32-bit position, negative ones included.  Its upper 32 bits as a signed
-// number are half turns in [-1, 1), which sincospif takes in fp32: 2^-25 of a turn at
-// most, 2e-7 radians.  An fp32 product p w_j would be off by p w_j 2^-24: 0.06
+// by themselves and what stays is p w_j 2^-52 radians (the roundings of 1 / (2 pi) and of
+// its product with w_j, each 2^-53 of w_j / 2 pi turns a position) at any 32-bit position,
+// negative ones included.  Its upper 32 bits as a signed number are half turns in [-1, 1), which
+// sincospif takes in fp32: 2^-25 of a turn at most, 2e-7 radians.  An fp32 product p w_j would be off by p w_j 2^-24: 0.06
 // radians at position 2^20.
 #pragma once
 

@@ -355,12 +355,14 @@ typedef enum {
   DA_ROPE_BASE = 2,     /* base * factor^(rot_dim / (rot_dim - 2)): the slowest pair stretched by
                            factor, the fastest kept */
   DA_ROPE_BY_PARTS = 3  /* pairs of more than high_turns turns over original_ctx positions kept, of
-                           fewer than low_turns divided by factor, in between mixed linearly */
+                           fewer than low_turns divided by factor, in between mixed linearly in the
+                           turns.  A model that mixes linearly in the pair's index needs its own table. */
 } da_rope_scaling;
 
 /*
  * rope_inv_freq — the frequencies of a rotary embedding (host only, pure): writes
- * rot_dim / 2 values to inv_freq (HOST memory).  base > 1; factor >= 1 (unused when
+ * rot_dim / 2 values to inv_freq (HOST memory); the magnitude that goes with a scaling is
+ * the caller's.  base > 1; factor >= 1 (unused when
  * plain); original_ctx > 0 and 0 <= low_turns < high_turns (by parts only).
  */
 int rope_inv_freq(double* inv_freq, int rot_dim, double base, int scaling, double factor, double original_ctx,
@@ -548,9 +550,8 @@ const char* decode_status_string(int status);
  * decode_device_error — synchronise `stream`, then read and clear the device error
  * word of the current device.  *flags receives the word: bit 0 a kernel gave up on
  * a bounded wait, bit 1 a segment-counter update gave up, bit 2 a page-table entry
- * read by decode_attn_paged / decode_attn_multi_paged / decode_attn_int8_paged was
- * outside [0, num_pages)
- * (that box was read from page 0 instead, so the affected rows are wrong but no
+ * read by a paged attention call (decode_attn_*, prefill_attn_*, latent_attn_*) was outside
+ * [0, num_pages) (that box was read from page 0 instead, so the affected rows are wrong but no
  * copy leaves the pool; kv_write_* and kv_read_* skip such rows), bit 3 a token at or
  * past the cache's capacity that kv_write_* did not write.  Returns DA_OK when flags == 0, DA_ERR_TIMEOUT otherwise,
  * or DA_ERR_CUDA.
