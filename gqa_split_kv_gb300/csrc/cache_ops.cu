@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CacheParams p)
           raw[c] = load_dependent(reinterpret_cast<const uint4*>(src) + ch);
           const int at = ch * 8 - p.r.offset;  // within the rotated part
           if (!PAIRED && rotates && !p.r.interleaved && at >= 0 && at < p.r.rot)  // the other halves of these pairs
-            other[c] = load_dependent(reinterpret_cast<const uint4*>(src + p.r.offset + (at >= np ? at - np : at + np)));
+            other[c] =
+                load_dependent(reinterpret_cast<const uint4*>(src + p.r.offset + (at >= np ? at - np : at + np)));
         }
       }
       if (r0 == 0) {  // the tokens' places and cosines
@@ -668,7 +669,8 @@ int write_call(bool paged, bool int8, CacheParams& p, long long cap, cudaStream_
   {
     // nothing that is written may be read by the same call, nor written twice
     const long long tokens = new_tokens - 1, kn = (tokens * p.k_stride + width) * 2,
-                    vn = has_v ? (tokens * p.v_stride + width) * 2 : 0, cn = cache_bytes(p, paged, int8), sn = scale_bytes(p, paged);
+                    vn = has_v ? (tokens * p.v_stride + width) * 2 : 0, cn = cache_bytes(p, paged, int8),
+                    sn = scale_bytes(p, paged);
     const void* dst[4] = {p.k, p.v, p.ks, p.vs};
     const long long bytes[4] = {cn, cn, sn, sn};
     for (int i = 0; i < 4; ++i) {
@@ -959,32 +961,33 @@ extern "C" int kv_read_int8_paged(const void* k_pool_i8, const void* v_pool_i8, 
                                   int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
                                   void* v_out, void* stream) {
   return read_paged(true, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, starts, seq_lens, batch,
-                    n_tokens, num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out, v_out,
-                    stream, false);
+                    n_tokens, num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out,
+                    v_out, stream, false);
 }
 
-extern "C" int kv_read_int8_contig_filled(const void* k_i8, const void* v_i8, const float* k_scale, const float* v_scale,
-                                   const int* starts, const int* seq_lens, int batch, int n_tokens, int num_kv_heads,
-                                   int head_dim, int max_ctx, void* k_out, void* v_out, void* stream) {
+extern "C" int kv_read_int8_contig_filled(const void* k_i8, const void* v_i8, const float* k_scale,
+                                          const float* v_scale, const int* starts, const int* seq_lens, int batch,
+                                          int n_tokens, int num_kv_heads, int head_dim, int max_ctx, void* k_out,
+                                          void* v_out, void* stream) {
   return read_contig_int8(k_i8, v_i8, k_scale, v_scale, starts, seq_lens, batch, n_tokens, num_kv_heads, head_dim,
                           max_ctx, k_out, v_out, stream, true);
 }
 
 extern "C" int kv_read_paged_filled(const void* k_pool, const void* v_pool, const int* page_table, const int* starts,
-                             const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
-                             int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
-                             void* v_out, void* stream) {
+                                    const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
+                                    int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
+                                    void* v_out, void* stream) {
   return read_paged(false, k_pool, v_pool, nullptr, nullptr, page_table, starts, seq_lens, batch, n_tokens,
                     num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out, v_out, stream,
                     true);
 }
 
 extern "C" int kv_read_int8_paged_filled(const void* k_pool_i8, const void* v_pool_i8, const float* k_scale_pool,
-                                  const float* v_scale_pool, const int* page_table, const int* starts,
-                                  const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
-                                  int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, void* k_out,
-                                  void* v_out, void* stream) {
+                                         const float* v_scale_pool, const int* page_table, const int* starts,
+                                         const int* seq_lens, int batch, int n_tokens, int num_kv_heads, int head_dim,
+                                         int page_size, int max_pages_per_seq, int num_pages, int max_seq_len,
+                                         void* k_out, void* v_out, void* stream) {
   return read_paged(true, k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, page_table, starts, seq_lens, batch,
-                    n_tokens, num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out, v_out,
-                    stream, true);
+                    n_tokens, num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages, max_seq_len, k_out,
+                    v_out, stream, true);
 }

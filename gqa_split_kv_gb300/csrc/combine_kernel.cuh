@@ -73,7 +73,8 @@ __global__ void __maxnreg__(40) combine_kernel(const CombineParams p) {  // 512 
   Plan pl{};
   if (p.planned) {
     // seq_lens is not written by the split kernel: read it before waiting on it.
-    build_plan_arrays([&](int b) { return p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len; }, p.B, p.max_len, plan_gap_blocks(D), lens, P, 0, blockDim.x);
+    build_plan_arrays([&](int b) { return p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len; }, p.B, p.max_len,
+                      plan_gap_blocks(D), lens, P, 0, blockDim.x);
     pl = make_plan(p.B, p.U, p.S, plan_gap_blocks(D), P);
   }
   // A segment of n blocks meets at most (n - 1) / q + 2 ranges; when even the

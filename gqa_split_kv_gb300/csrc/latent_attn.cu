@@ -238,8 +238,8 @@ int launch_latent_prefill(LatentPrefillParams& prm, const void* q, const void* k
     // launch groups of (b, h) units whose K/V fit in L2 together: the longest query blocks of
     // a group start first, so a second group's would start last (32 heads x 4096 tokens: 160 us
     // in groups of 24, 142 in one).  Where the capacity would make several groups, the kernel
-    // takes the longest sequence's tokens instead (that prompt, other
-    // values, in a cache of 131072: 126 us, 157 in groups by the capacity; of its own size: 124)
+    // takes the longest sequence's tokens instead (that prompt in a cache of 131072: 126 us, 157
+    // in groups by the capacity; in a cache of its own size 124)
     const long long units = (long long)prm.B * prm.H;
     prm.grp = prefill_group(prm.max_len, D, units);
     prm.grp_by_length = prm.seq_lens && prm.grp < units;
@@ -320,8 +320,9 @@ extern "C" int latent_prefill_contig(const void* q, const void* k_nope, const vo
   if (!k_nope || !k_rope || !v || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16))
     return DA_ERR_INVALID_ARG;
   const long long far = 1LL << 40, cached = (long long)batch * max_ctx;
-  if (kv_head_stride > far || kv_token_stride > far || rope_token_stride > far || !reachable(num_heads, kv_head_stride) ||
-      !reachable(cached, kv_token_stride) || !reachable(cached, rope_token_stride))
+  if (kv_head_stride > far || kv_token_stride > far || rope_token_stride > far ||
+      !reachable(num_heads, kv_head_stride) || !reachable(cached, kv_token_stride) ||
+      !reachable(cached, rope_token_stride))
     return DA_ERR_INVALID_ARG;
   if (kv_head_stride < head_dim || kv_head_stride % 8 || kv_token_stride % 8 ||
       kv_token_stride < (num_heads - 1) * kv_head_stride + head_dim || rope_token_stride < 64 || rope_token_stride % 8)

@@ -1115,7 +1115,8 @@ __global__ void __launch_bounds__(SplitGeo<D, NGP, KV8, PAGED>::NTHREADS, 1)
     pdl_launch_dependents();
     named_bar_sync(4, kAll);
   } else {
-    build_plan_arrays([&](int b) { return p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len; }, p.B, p.max_len, plan_gap_blocks(D), lens, P, 2, kCons);
+    build_plan_arrays([&](int b) { return p.seq_lens ? __ldg(p.seq_lens + b) : p.max_len; }, p.B, p.max_len,
+                      plan_gap_blocks(D), lens, P, 2, kCons);
     pdl_launch_dependents();
     named_bar_sync(3, kAll);
     named_bar_arrive(4, kAll);
