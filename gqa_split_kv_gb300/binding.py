@@ -41,6 +41,24 @@ __all__ = [
     "latent_prefill_contig",
     "latent_workspace",
     "latent_max_batch",
+    "prefix_attn_contig",
+    "prefix_attn_paged",
+    "prefix_workspace",
+    "block_means_contig",
+    "block_means_paged",
+    "block_select",
+    "sparse_attn_contig",
+    "sparse_attn_paged",
+    "sparse_workspace",
+    "kv_weights_contig",
+    "kv_weights_paged",
+    "kv_weights_int8_contig",
+    "kv_weights_int8_paged",
+    "weights_workspace",
+    "kv_evict_contig",
+    "kv_evict_paged",
+    "kv_evict_int8_contig",
+    "kv_evict_int8_paged",
     "device_error",
     "selftest_bounded_wait",
     "counters_len",
@@ -126,6 +144,24 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "latent_prefill_workspace_bytes": [i, i, i, i, i, i],
         "latent_workspace_bytes": [i, i, i, i, i],
         "latent_max_batch": [i, i, i],
+        "prefix_attn_workspace_bytes": [i, i, i, i, i, i],
+        "prefix_attn_contig": [vp] * 6 + [i] * 7 + [f, vp, ll, vp, vp],
+        "prefix_attn_paged": [vp] * 4 + [i, vp, vp] + [i] * 9 + [f, vp, ll, vp, vp],
+        "block_means_contig": [vp, vp] + [i] * 7 + [vp, vp],
+        "block_means_paged": [vp] * 3 + [i] * 10 + [vp, vp],
+        "block_select": [vp] * 3 + [i] * 10 + [vp, vp],
+        "sparse_attn_workspace_bytes": [i, i],
+        "sparse_attn_contig": [vp] * 5 + [i] * 8 + [f, vp, ll, vp, vp],
+        "sparse_attn_paged": [vp] * 6 + [i] * 11 + [f, vp, ll, vp, vp],
+        "kv_weights_workspace_bytes": [i, i, i, i, i, i],
+        "kv_weights_contig": [vp] * 3 + [i] * 6 + [f, f, vp, vp, ll, vp, vp],
+        "kv_weights_paged": [vp] * 4 + [i] * 9 + [f, f, vp, vp, ll, vp, vp],
+        "kv_weights_int8_contig": [vp] * 4 + [i] * 6 + [f, f, vp, vp, ll, vp, vp],
+        "kv_weights_int8_paged": [vp] * 5 + [i] * 9 + [f, f, vp, vp, ll, vp, vp],
+        "kv_evict_contig": [vp] * 4 + [i] * 7 + [vp] * 3 + [i, vp, vp, vp],
+        "kv_evict_paged": [vp] * 5 + [i] * 10 + [vp] * 3 + [i, vp, vp, vp],
+        "kv_evict_int8_contig": [vp] * 6 + [i] * 7 + [vp] * 5 + [i, vp, vp, vp],
+        "kv_evict_int8_paged": [vp] * 7 + [i] * 10 + [vp] * 5 + [i, vp, vp, vp],
     }.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ll if name.endswith("_bytes") else i
@@ -610,6 +646,166 @@ def latent_prefill_contig(q, k_nope, k_rope, v, seq_lens=None, *, scale: float, 
     the halves of one expansion), k_rope bf16 [B, max_ctx, 64], shared by the heads (tokens may be strided, e.g. the
     last columns of a latent cache); seq_lens int32 [B] or None.  Returns out bf16 [B, q_len, H, D]."""
     return (_ext_module or _ext()).latent_prefill(q, k_nope, k_rope, v, seq_lens, scale, out, stream)
+
+
+# ---------------------------------------------------------------- attention over long caches
+
+def _workspace_of(name: str, *sizes):
+    import torch
+    n = getattr(load(), name)(*sizes, 0)
+    if n < 0:
+        raise DecodeAttnError(name, -n)
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def prefix_workspace(batch: int, q_len: int, num_q_heads: int, num_kv_heads: int, head_dim: int):
+    """A workspace for prefix_attn_* calls of this shape on the current CUDA device (uint8).  A program may keep one;
+    calls that share it must not overlap on the GPU."""
+    return _workspace_of("prefix_attn_workspace_bytes", batch, q_len, num_q_heads, num_kv_heads, head_dim)
+
+
+def prefix_attn_contig(q, k_prefix, v_prefix, k, v, seq_lens=None, *, scale: Optional[float] = None, workspace=None,
+                       out=None, stream=None):
+    """Attention of the last q_len tokens of sequences that begin with the same tokens, which are read once for the
+    batch: q bf16 [B, q_len, Hq, D] (D 64, 128 or 256), k_prefix/v_prefix bf16 [P, Hkv, D], k/v bf16
+    [B, max_ctx, Hkv, D] (row t - P holds a sequence's token t), seq_lens int32 [B] with the prefix, or None
+    (P + max_ctx each).  Query token i of sequence b sees its first seq_lens[b] - q_len + 1 + i tokens; one that sees
+    none gives zeros.  workspace: as made by prefix_workspace (None: made here).  Returns out like q."""
+    return (_ext_module or _ext()).prefix_attn(q, k_prefix, v_prefix, k, v, None, 0, None, seq_lens, 0, scale, workspace,
+                                               out, stream)
+
+
+def prefix_attn_paged(q, k_pool, v_pool, prefix_table, prefix_len: int, page_table, seq_lens, max_seq_len: int, *,
+                      scale: Optional[float] = None, workspace=None, out=None, stream=None):
+    """prefix_attn_contig over page pools [num_pages, page_size, Hkv, D]: prefix_table int32 [>= ceil(prefix_len /
+    page_size)], page_table int32 [B, max_pages] of whole sequences, of which the entries of the prefix's whole pages
+    are not read."""
+    return (_ext_module or _ext()).prefix_attn(q, None, None, k_pool, v_pool, prefix_table, prefix_len, page_table,
+                                               seq_lens, max_seq_len, scale, workspace, out, stream)
+
+
+def block_means_contig(k, seq_lens=None, block_size: int = 64, n_tokens: Optional[int] = None, *, out=None, stream=None):
+    """Mean keys of the blocks of block_size tokens that hold the last n_tokens of each sequence (None: all): k bf16
+    [B, max_ctx, Hkv, D], seq_lens int32 [B] or None.  out bf16 [B, Hkv, max_blocks, D], other blocks as they were
+    (None: made here, zeros).  Returns out."""
+    return (_ext_module or _ext()).block_means(k, None, seq_lens, 0, block_size, n_tokens, out, stream)
+
+
+def block_means_paged(k_pool, page_table, seq_lens, max_seq_len: int, block_size: int = 64,
+                      n_tokens: Optional[int] = None, *, out=None, stream=None):
+    """block_means_contig of a page pool [num_pages, page_size, Hkv, D]; page_table int32 [B, max_pages]."""
+    return (_ext_module or _ext()).block_means(k_pool, page_table, seq_lens, max_seq_len, block_size, n_tokens, out,
+                                               stream)
+
+
+def block_select(q, means, seq_lens, block_size: int, n_select: int, *, first: int = 1, recent: int = 1, out=None,
+                 stream=None):
+    """The n_select blocks that each of the last q_len tokens attends to, for every KV head: the first `first` and
+    the last `recent` of those up to its own, and of the others those with the largest max over the group's heads of
+    <q, mean> (as if computed exactly; ties: the lower block).  q bf16 [B, q_len, Hq, D], means as from block_means_*,
+    seq_lens int32 [B] or None.  Returns out int32 [B, q_len, Hkv, n_select], ascending, -1 behind the last."""
+    return (_ext_module or _ext()).block_select(q, means, seq_lens, block_size, n_select, first, recent, out, stream)
+
+
+def sparse_workspace(head_dim: int):
+    """A workspace for sparse_attn_* calls on the current CUDA device (uint8); calls that share it must not overlap
+    on the GPU."""
+    return _workspace_of("sparse_attn_workspace_bytes", head_dim)
+
+
+def sparse_attn_contig(q, k, v, blocks, seq_lens, block_size: int, *, scale: Optional[float] = None, workspace=None,
+                       out=None, stream=None):
+    """Attention of the last q_len tokens over listed blocks: q bf16 [B, q_len, Hq, D] (D 64, 128 or 256), k/v bf16
+    [B, max_ctx, Hkv, D], blocks int32 [B, q_len, Hkv, n_select] (block_select; a negative entry lists nothing, one
+    that is listed twice counts twice), seq_lens int32 [B] or None.  A token sees its blocks up to its own position;
+    one that sees nothing gives zeros.  workspace: as made by sparse_workspace (None: made here).  Returns out like q."""
+    return (_ext_module or _ext()).sparse_attn(q, k, v, blocks, None, seq_lens, 0, block_size, scale, workspace, out,
+                                               stream)
+
+
+def sparse_attn_paged(q, k_pool, v_pool, blocks, page_table, seq_lens, max_seq_len: int, block_size: int, *,
+                      scale: Optional[float] = None, workspace=None, out=None, stream=None):
+    """sparse_attn_contig over page pools [num_pages, page_size, Hkv, D]; page_table int32 [B, max_pages]."""
+    return (_ext_module or _ext()).sparse_attn(q, k_pool, v_pool, blocks, page_table, seq_lens, max_seq_len, block_size,
+                                               scale, workspace, out, stream)
+
+
+# ---------------------------------------------------------------- weights and eviction
+
+def weights_workspace(batch: int, q_len: int, num_q_heads: int, num_kv_heads: int, max_len: int):
+    """A workspace for kv_weights_* calls of this shape on the current CUDA device (uint8); max_len: max_ctx, or what
+    the page table and max_seq_len hold.  Calls that share it must not overlap on the GPU."""
+    return _workspace_of("kv_weights_workspace_bytes", batch, q_len, num_q_heads, num_kv_heads, max_len)
+
+
+def kv_weights_contig(q, k, weights, seq_lens=None, *, scale: Optional[float] = None, decay: float = 1.0, workspace=None,
+                      out=None, stream=None):
+    """The attention weight that the last q_len tokens give each cached token, added over them and the heads of its
+    group: out = decay * weights + that.  q bf16 [B, q_len, Hq, D] (D 64, 128 or 256, q_len * Hq / Hkv <= 1024), k bf16
+    [B, max_ctx, Hkv, D], weights fp32 [B, Hkv, max_ctx] or None (zeros), seq_lens int32 [B] or None.  out: None writes
+    weights in place, or a new tensor where that is None; entries past a sequence stay as they were.  workspace: as
+    made by weights_workspace (None: made here).  Returns what was written."""
+    return (_ext_module or _ext()).kv_weights(q, k, None, weights, None, seq_lens, 0, scale, decay, workspace, out, stream)
+
+
+def kv_weights_paged(q, k_pool, weights, page_table, seq_lens, max_seq_len: int, *, scale: Optional[float] = None,
+                     decay: float = 1.0, workspace=None, out=None, stream=None):
+    """kv_weights_contig over a page pool [num_pages, page_size, Hkv, D], weights fp32 [num_pages, Hkv, page_size].
+    Sequences may not share pages."""
+    return (_ext_module or _ext()).kv_weights(q, k_pool, None, weights, page_table, seq_lens, max_seq_len, scale, decay,
+                                              workspace, out, stream)
+
+
+def kv_weights_int8_contig(q, k_i8, k_scale, weights, seq_lens=None, *, scale: Optional[float] = None,
+                           decay: float = 1.0, workspace=None, out=None, stream=None):
+    """kv_weights_contig over an int8 cache [B, max_ctx, Hkv, D] with scales fp32 [B, Hkv, max_ctx]."""
+    return (_ext_module or _ext()).kv_weights(q, k_i8, _int8(k_scale), weights, None, seq_lens, 0, scale, decay, workspace,
+                                              out, stream)
+
+
+def kv_weights_int8_paged(q, k_pool_i8, k_scale_pool, weights, page_table, seq_lens, max_seq_len: int, *,
+                          scale: Optional[float] = None, decay: float = 1.0, workspace=None, out=None, stream=None):
+    """kv_weights_paged over an int8 pool with scale pools fp32 [num_pages, Hkv, page_size]."""
+    return (_ext_module or _ext()).kv_weights(q, k_pool_i8, _int8(k_scale_pool), weights, page_table, seq_lens, max_seq_len,
+                                              scale, decay, workspace, out, stream)
+
+
+def kv_evict_contig(k, v, weights, seq_lens, keep: int, *, first: int = 0, recent: int = 1, kept=None, new_lens=None,
+                    k_out=None, v_out=None, weights_out=None, stream=None):
+    """Cuts each sequence of a bf16 cache k/v [B, max_ctx, Hkv, D] (v may be None) down to `keep` tokens, KV head by
+    KV head: the first `first`, the last `recent`, and of the others those of the largest weights (fp32
+    [B, Hkv, max_ctx]; ties: the lower position).  They move together to positions 0, 1, ... in their order, and their
+    weights with them: in place, or to k_out, v_out [B, >= keep, Hkv, D] and weights_out [B, Hkv, >= keep]; weights
+    behind them become 0.  Returns (kept, new_lens): int32 [B, Hkv, keep], the old position of each, -1 behind the
+    last, and int32 [B], min(seq_lens, keep); seq_lens is not written."""
+    return (_ext_module or _ext()).kv_evict(k, v, None, None, weights, None, seq_lens, 0, keep, first, recent, kept,
+                                            new_lens, k_out, v_out, None, None, weights_out, stream)
+
+
+def kv_evict_paged(k_pool, v_pool, weights, page_table, seq_lens, max_seq_len: int, keep: int, *, first: int = 0,
+                   recent: int = 1, kept=None, new_lens=None, k_out=None, v_out=None, weights_out=None, stream=None):
+    """kv_evict_contig of page pools [num_pages, page_size, Hkv, D], weights fp32 [num_pages, Hkv, page_size]; the
+    outputs, if any, are contiguous.  In place, sequences may not share pages."""
+    return (_ext_module or _ext()).kv_evict(k_pool, v_pool, None, None, weights, page_table, seq_lens, max_seq_len, keep,
+                                            first, recent, kept, new_lens, k_out, v_out, None, None, weights_out, stream)
+
+
+def kv_evict_int8_contig(k_i8, v_i8, k_scale, v_scale, weights, seq_lens, keep: int, *, first: int = 0, recent: int = 1,
+                         kept=None, new_lens=None, k_out=None, v_out=None, k_scale_out=None, v_scale_out=None,
+                         weights_out=None, stream=None):
+    """kv_evict_contig of an int8 cache with scales fp32 [B, Hkv, max_ctx], which move along."""
+    return (_ext_module or _ext()).kv_evict(k_i8, v_i8, _int8(k_scale), v_scale, weights, None, seq_lens, 0, keep, first,
+                                            recent, kept, new_lens, k_out, v_out, k_scale_out, v_scale_out, weights_out,
+                                            stream)
+
+
+def kv_evict_int8_paged(k_pool_i8, v_pool_i8, k_scale_pool, v_scale_pool, weights, page_table, seq_lens,
+                        max_seq_len: int, keep: int, *, first: int = 0, recent: int = 1, kept=None, new_lens=None,
+                        k_out=None, v_out=None, k_scale_out=None, v_scale_out=None, weights_out=None, stream=None):
+    """kv_evict_paged of int8 pools with scale pools fp32 [num_pages, Hkv, page_size], which move along."""
+    return (_ext_module or _ext()).kv_evict(k_pool_i8, v_pool_i8, _int8(k_scale_pool), v_scale_pool, weights, page_table,
+                                            seq_lens, max_seq_len, keep, first, recent, kept, new_lens, k_out, v_out,
+                                            k_scale_out, v_scale_out, weights_out, stream)
 
 
 def selftest_bounded_wait(timeout_ns: int, stream=None) -> None:

@@ -15,7 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdecode_attn.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("decode_attn.cu", "latent_attn.cu", "cache_ops.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("decode_attn.cu", "latent_attn.cu", "cache_ops.cu", "prefix_attn.cu",
+                                                  "sparse_attn.cu", "evict.cu")]
 EXT = os.path.join(PKG, "_binding_ext" + sysconfig.get_config_var("EXT_SUFFIX"))
 EXT_SOURCE = os.path.join(CSRC, "binding_ext.cpp")
 EXT_STAMP = os.path.join(PKG, "_build", "binding_ext.torch")  # the PyTorch that EXT was compiled against

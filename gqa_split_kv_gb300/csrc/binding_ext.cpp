@@ -1,4 +1,4 @@
-// Argument marshalling of the cache and latent calls as a CPython extension: checks of
+// Argument marshalling of the cache, latent and long-cache calls as a CPython extension: checks of
 // tensors against one another, outputs and workspaces that the caller left out, and the C
 // ABI call.  A decode step's kernels take a few microseconds and so does a Python
 // function that looks at nine tensors (5 to 11 us here, against 0.5 us); nothing is
@@ -19,6 +19,7 @@
 
 #include <algorithm>
 #include <array>
+#include <cmath>
 #include <optional>
 #include <sstream>
 #include <stdexcept>
@@ -64,6 +65,24 @@ struct Library {
   decltype(&::latent_workspace_bytes) latent_workspace_bytes = nullptr;
   decltype(&::latent_prefill_contig) latent_prefill_contig = nullptr;
   decltype(&::latent_prefill_workspace_bytes) latent_prefill_workspace_bytes = nullptr;
+  decltype(&::prefix_attn_contig) prefix_attn_contig = nullptr;
+  decltype(&::prefix_attn_paged) prefix_attn_paged = nullptr;
+  decltype(&::prefix_attn_workspace_bytes) prefix_attn_workspace_bytes = nullptr;
+  decltype(&::block_means_contig) block_means_contig = nullptr;
+  decltype(&::block_means_paged) block_means_paged = nullptr;
+  decltype(&::block_select) block_select = nullptr;
+  decltype(&::sparse_attn_contig) sparse_attn_contig = nullptr;
+  decltype(&::sparse_attn_paged) sparse_attn_paged = nullptr;
+  decltype(&::sparse_attn_workspace_bytes) sparse_attn_workspace_bytes = nullptr;
+  decltype(&::kv_weights_contig) kv_weights_contig = nullptr;
+  decltype(&::kv_weights_paged) kv_weights_paged = nullptr;
+  decltype(&::kv_weights_int8_contig) kv_weights_int8_contig = nullptr;
+  decltype(&::kv_weights_int8_paged) kv_weights_int8_paged = nullptr;
+  decltype(&::kv_weights_workspace_bytes) kv_weights_workspace_bytes = nullptr;
+  decltype(&::kv_evict_contig) kv_evict_contig = nullptr;
+  decltype(&::kv_evict_paged) kv_evict_paged = nullptr;
+  decltype(&::kv_evict_int8_contig) kv_evict_int8_contig = nullptr;
+  decltype(&::kv_evict_int8_paged) kv_evict_int8_paged = nullptr;
 };
 Library g_lib;
 PyObject* g_error = nullptr;  // DecodeAttnError
@@ -554,6 +573,304 @@ PyObject* latent_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
+// ---------------------------------------------------------------- attention over long caches
+
+// A scale, or None: one over the root of the head's width.
+float scale_or(PyObject* o, int64_t D) { return o == Py_None ? (float)std::pow((double)D, -0.5) : real(o); }
+
+// A workspace that the caller gave, or one of these bytes (negative: an error) that is made here.
+struct Work {
+  Tensor own;
+  void* at;
+  long long size;
+  Work(const Tensor* given, long long bytes, const char* fn, const Tensor& like, int64_t dev) {
+    if (given) {
+      if (!given->is_contiguous() || cuda_index(*given) != dev)
+        throw Bad("workspace: expected a contiguous tensor on cuda:" + std::to_string(dev));
+      at = given->data_ptr();
+      size = (long long)given->nbytes();
+      return;
+    }
+    if (bytes < 0) throw Failed{fn, (int)-bytes};
+    own = at::empty(dims(bytes), like.options().dtype(at::kByte));
+    at = bytes ? own.data_ptr() : nullptr;
+    size = bytes;
+  }
+};
+
+// (q, k_prefix, v_prefix, k, v, prefix_table, prefix_len, page_table, seq_lens, max_seq_len, scale, workspace, out,
+//  stream)
+PyObject* prefix_attn(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 14, [&]() -> PyObject* {
+    const Tensor &q = ten(a[0], "q"), &k = ten(a[3], "k"), &v = ten(a[4], "v");
+    const Tensor *kp = opt(a[1], "k_prefix"), *vp = opt(a[2], "v_prefix"), *pt = opt(a[5], "prefix_table"),
+                 *table = opt(a[7], "page_table"), *lens = opt(a[8], "seq_lens"), *ws = opt(a[11], "workspace"),
+                 *given = opt(a[12], "out");
+    if (q.dim() != 4 || k.dim() != 4) throw Bad("q, k: expected 4 dims");
+    const int64_t dev = cuda_index(q);
+    const int B = small(q.size(0), "q"), n = small(q.size(1), "q"), Hq = small(q.size(2), "q"), D = small(q.size(3), "q"),
+              H = small(k.size(2), "k");
+    plain(q, "q", at::kBFloat16, dims(B, n, Hq, D), dev);
+    const Cache c = check_cache(k, &v, nullptr, nullptr, table, lens, B, H, D, dev);
+    if (given) plain(*given, "out", at::kBFloat16, dims(B, n, Hq, D), dev);
+    int P, cap = 0;
+    if (table) {
+      P = small(a[6], "prefix_len");
+      cap = small(a[9], "max_seq_len");
+      if (!pt) throw Bad("prefix_table: expected a tensor");
+      if (P < 0) throw Bad("prefix_len: negative");
+      const int64_t need = c.slab > 0 ? (P + c.slab - 1) / c.slab : 0;
+      if (pt->dim() != 1 || pt->size(0) < need)
+        throw Bad("prefix_table: expected one dim of at least " + std::to_string(need) + " pages");
+      plain(*pt, "prefix_table", at::kInt, dims(pt->size(0)), dev);
+    } else {
+      if (!kp || !vp) throw Bad("k_prefix, v_prefix: expected tensors");
+      P = kp->dim() == 3 ? small(kp->size(0), "k_prefix") : 0;
+      plain(*kp, "k_prefix", at::kBFloat16, dims(P, H, D), dev);
+      plain(*vp, "v_prefix", at::kBFloat16, dims(P, H, D), dev);
+    }
+    const float scale = scale_or(a[10], D);
+    not_tracked(given, "out");
+    on_current(dev);
+    Stream st(a[13], dev);
+    const Tensor out = given ? *given : at::empty(dims(B, n, Hq, D), q.options());
+    const char* fn = table ? "prefix_attn_paged" : "prefix_attn_contig";
+    const Work w(ws, ws ? 0 : g_lib.prefix_attn_workspace_bytes(B, n, Hq, H, D, 0), fn, q, dev);
+    const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k");
+    if (table)
+      call(fn, [&] {
+        return g_lib.prefix_attn_paged(ptr(q), ptr(k), ptr(v), ptr<int>(pt), P, ptr<int>(table), ptr<int>(lens), B, n, Hq,
+                                       H, D, slab, cols, slabs, cap, scale, w.at, w.size, ptr(out), st.raw);
+      });
+    else
+      call(fn, [&] {
+        return g_lib.prefix_attn_contig(ptr(q), ptr(kp), ptr(vp), ptr(k), ptr(v), ptr<int>(lens), B, n, Hq, H, D, P, slab,
+                                        scale, w.at, w.size, ptr(out), st.raw);
+      });
+    written(given);
+    return given ? same(a[12]) : THPVariable_Wrap(out);
+  });
+}
+
+// (k, page_table, seq_lens, max_seq_len, block_size, n_tokens, out, stream)
+PyObject* block_means(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 8, [&]() -> PyObject* {
+    const Tensor& k = ten(a[0], "k");
+    const Tensor *table = opt(a[1], "page_table"), *lens = opt(a[2], "seq_lens"), *given = opt(a[6], "out");
+    if (k.dim() != 4 || (table && table->dim() != 2)) throw Bad("k, page_table: expected 4 and 2 dims");
+    const int64_t dev = cuda_index(k);
+    const int B = small(table ? table->size(0) : k.size(0), "k"), H = small(k.size(2), "k"), D = small(k.size(3), "k"),
+              block = small(a[4], "block_size");
+    if (block <= 0) throw Bad("block_size: expected a positive number");
+    const Cache c = check_cache(k, nullptr, nullptr, nullptr, table, lens, B, H, D, dev);
+    const int cap = table ? small(a[3], "max_seq_len") : small(c.slab, "k");
+    const int64_t room = table ? std::min<int64_t>(std::max(cap, 0), c.cols * c.slab) : cap;
+    const int n = a[5] == Py_None ? small(room, "k") : small(a[5], "n_tokens");
+    const int64_t blocks = given && given->dim() == 4 ? given->size(2) : (room + block - 1) / block;
+    if (given) plain(*given, "out", at::kBFloat16, dims(B, H, blocks, D), dev);
+    not_tracked(given, "out");
+    on_current(dev);
+    Stream st(a[7], dev);
+    const Tensor out = given ? *given : at::zeros(dims(B, H, blocks, D), k.options());
+    const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k"),
+              nb = small(blocks, "out");
+    if (table)
+      call("block_means_paged", [&] {
+        return g_lib.block_means_paged(ptr(k), ptr<int>(table), ptr<int>(lens), B, n, H, D, slab, cols, slabs, cap, block,
+                                       nb, ptr(out), st.raw);
+      });
+    else
+      call("block_means_contig", [&] {
+        return g_lib.block_means_contig(ptr(k), ptr<int>(lens), B, n, H, D, slab, block, nb, ptr(out), st.raw);
+      });
+    written(given);
+    return given ? same(a[6]) : THPVariable_Wrap(out);
+  });
+}
+
+// (q, means, seq_lens, block_size, n_select, first, recent, out, stream)
+PyObject* block_select(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 9, [&]() -> PyObject* {
+    const Tensor &q = ten(a[0], "q"), &means = ten(a[1], "means");
+    const Tensor *lens = opt(a[2], "seq_lens"), *given = opt(a[7], "out");
+    if (q.dim() != 4 || means.dim() != 4) throw Bad("q, means: expected 4 dims");
+    const int64_t dev = cuda_index(q);
+    const int B = small(q.size(0), "q"), n = small(q.size(1), "q"), Hq = small(q.size(2), "q"), D = small(q.size(3), "q"),
+              H = small(means.size(1), "means"), blocks = small(means.size(2), "means"), block = small(a[3], "block_size"),
+              pick = small(a[4], "n_select"), first = small(a[5], "first"), recent = small(a[6], "recent");
+    plain(q, "q", at::kBFloat16, dims(B, n, Hq, D), dev);
+    plain(means, "means", at::kBFloat16, dims(B, H, blocks, D), dev);
+    if (lens) plain(*lens, "seq_lens", at::kInt, dims(B), dev);
+    if (pick < 0) throw Bad("n_select: negative");
+    if (given) plain(*given, "out", at::kInt, dims(B, n, H, pick), dev);
+    on_current(dev);
+    Stream st(a[8], dev);
+    const Tensor out = given ? *given : at::empty(dims(B, n, H, pick), q.options().dtype(at::kInt));
+    call("block_select", [&] {
+      return g_lib.block_select(ptr(q), ptr(means), ptr<int>(lens), B, n, Hq, H, D, block, blocks, pick, first, recent,
+                                ptr<int>(out), st.raw);
+    });
+    written(given);
+    return given ? same(a[7]) : THPVariable_Wrap(out);
+  });
+}
+
+// (q, k, v, blocks, page_table, seq_lens, max_seq_len, block_size, scale, workspace, out, stream)
+PyObject* sparse_attn(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 12, [&]() -> PyObject* {
+    const Tensor &q = ten(a[0], "q"), &k = ten(a[1], "k"), &v = ten(a[2], "v"), &blocks = ten(a[3], "blocks");
+    const Tensor *table = opt(a[4], "page_table"), *lens = opt(a[5], "seq_lens"), *ws = opt(a[9], "workspace"),
+                 *given = opt(a[10], "out");
+    if (q.dim() != 4 || k.dim() != 4 || blocks.dim() != 4) throw Bad("q, k, blocks: expected 4 dims");
+    const int64_t dev = cuda_index(q);
+    const int B = small(q.size(0), "q"), n = small(q.size(1), "q"), Hq = small(q.size(2), "q"), D = small(q.size(3), "q"),
+              H = small(k.size(2), "k"), pick = small(blocks.size(3), "blocks"), block = small(a[7], "block_size");
+    plain(q, "q", at::kBFloat16, dims(B, n, Hq, D), dev);
+    const Cache c = check_cache(k, &v, nullptr, nullptr, table, lens, B, H, D, dev);
+    plain(blocks, "blocks", at::kInt, dims(B, n, H, pick), dev);
+    if (given) plain(*given, "out", at::kBFloat16, dims(B, n, Hq, D), dev);
+    const float scale = scale_or(a[8], D);
+    not_tracked(given, "out");
+    on_current(dev);
+    Stream st(a[11], dev);
+    const Tensor out = given ? *given : at::empty(dims(B, n, Hq, D), q.options());
+    const char* fn = table ? "sparse_attn_paged" : "sparse_attn_contig";
+    const Work w(ws, ws ? 0 : g_lib.sparse_attn_workspace_bytes(D, 0), fn, q, dev);
+    const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k"),
+              cap = table ? small(a[6], "max_seq_len") : 0;
+    if (table)
+      call(fn, [&] {
+        return g_lib.sparse_attn_paged(ptr(q), ptr(k), ptr(v), ptr<int>(blocks), ptr<int>(table), ptr<int>(lens), B, n, Hq,
+                                       H, D, slab, cols, slabs, cap, block, pick, scale, w.at, w.size, ptr(out), st.raw);
+      });
+    else
+      call(fn, [&] {
+        return g_lib.sparse_attn_contig(ptr(q), ptr(k), ptr(v), ptr<int>(blocks), ptr<int>(lens), B, n, Hq, H, D, slab,
+                                        block, pick, scale, w.at, w.size, ptr(out), st.raw);
+      });
+    written(given);
+    return given ? same(a[10]) : THPVariable_Wrap(out);
+  });
+}
+
+// ---------------------------------------------------------------- weights and eviction
+
+// (q, k, k_scale, weights, page_table, seq_lens, max_seq_len, scale, decay, workspace, out, stream)
+PyObject* kv_weights(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 12, [&]() -> PyObject* {
+    const Tensor &q = ten(a[0], "q"), &k = ten(a[1], "k");
+    const Tensor *ks = opt(a[2], "k_scale"), *prior = opt(a[3], "weights"), *table = opt(a[4], "page_table"),
+                 *lens = opt(a[5], "seq_lens"), *ws = opt(a[9], "workspace"), *given = opt(a[10], "out");
+    if (q.dim() != 4 || k.dim() != 4) throw Bad("q, k: expected 4 dims");
+    const int64_t dev = cuda_index(q);
+    const int B = small(q.size(0), "q"), n = small(q.size(1), "q"), Hq = small(q.size(2), "q"), D = small(q.size(3), "q"),
+              H = small(k.size(2), "k");
+    plain(q, "q", at::kBFloat16, dims(B, n, Hq, D), dev);
+    const Cache c = check_cache(k, nullptr, ks, nullptr, table, lens, B, H, D, dev);
+    const auto shape = dims(c.slabs, H, c.slab);
+    if (prior) plain(*prior, "weights", at::kFloat, shape, dev);
+    if (given) plain(*given, "out", at::kFloat, shape, dev);
+    const Tensor* kept = given ? given : prior;  // where the sums go, unless they are made here
+    not_tracked(kept, given ? "out" : "weights");
+    const float scale = scale_or(a[7], D), decay = real(a[8]);
+    on_current(dev);
+    Stream st(a[11], dev);
+    const Tensor out = kept ? *kept : at::zeros(shape, q.options().dtype(at::kFloat));
+    const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k");
+    const int cap = table ? small(a[6], "max_seq_len") : slab;
+    const int64_t room = table ? std::min<int64_t>(std::max(cap, 0), c.cols * c.slab) : cap;
+    const char* fn = table ? (ks ? "kv_weights_int8_paged" : "kv_weights_paged")
+                           : (ks ? "kv_weights_int8_contig" : "kv_weights_contig");
+    const Work w(ws, ws ? 0 : g_lib.kv_weights_workspace_bytes(B, n, Hq, H, (int)room, 0), fn, q, dev);
+    const float* from = ptr<float>(prior);
+    call(fn, [&] {
+      if (table)
+        return ks ? g_lib.kv_weights_int8_paged(ptr(q), ptr(k), ptr<float>(ks), ptr<int>(table), ptr<int>(lens), B, n, Hq, H,
+                                                D, slab, cols, slabs, cap, scale, decay, from, w.at, w.size,
+                                                ptr<float>(out), st.raw)
+                  : g_lib.kv_weights_paged(ptr(q), ptr(k), ptr<int>(table), ptr<int>(lens), B, n, Hq, H, D, slab, cols, slabs,
+                                           cap, scale, decay, from, w.at, w.size, ptr<float>(out), st.raw);
+      return ks ? g_lib.kv_weights_int8_contig(ptr(q), ptr(k), ptr<float>(ks), ptr<int>(lens), B, n, Hq, H, D, slab, scale,
+                                               decay, from, w.at, w.size, ptr<float>(out), st.raw)
+                : g_lib.kv_weights_contig(ptr(q), ptr(k), ptr<int>(lens), B, n, Hq, H, D, slab, scale, decay, from, w.at,
+                                          w.size, ptr<float>(out), st.raw);
+    });
+    written(kept);
+    return given ? same(a[10]) : prior ? same(a[3]) : THPVariable_Wrap(out);
+  });
+}
+
+// (k, v, k_scale, v_scale, weights, page_table, seq_lens, max_seq_len, keep, first, recent, kept, new_lens, k_out,
+//  v_out, k_scale_out, v_scale_out, weights_out, stream)
+PyObject* kv_evict(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 19, [&]() -> PyObject* {
+    const Tensor &k = ten(a[0], "k"), &weights = ten(a[4], "weights");
+    const Tensor *v = opt(a[1], "v"), *ks = opt(a[2], "k_scale"), *vs = opt(a[3], "v_scale"),
+                 *table = opt(a[5], "page_table"), *lens = opt(a[6], "seq_lens"), *kept = opt(a[11], "kept"),
+                 *nl = opt(a[12], "new_lens"), *ko = opt(a[13], "k_out"), *vo = opt(a[14], "v_out"),
+                 *kso = opt(a[15], "k_scale_out"), *vso = opt(a[16], "v_scale_out"), *wo = opt(a[17], "weights_out");
+    if (k.dim() != 4 || (table && table->dim() != 2)) throw Bad("k, page_table: expected 4 and 2 dims");
+    const int64_t dev = cuda_index(k);
+    const int B = small(table ? table->size(0) : k.size(0), "k"), H = small(k.size(2), "k"), D = small(k.size(3), "k"),
+              keep = small(a[8], "keep"), first = small(a[9], "first"), recent = small(a[10], "recent");
+    const Cache c = check_cache(k, v, ks, vs, table, lens, B, H, D, dev);
+    plain(weights, "weights", at::kFloat, dims(c.slabs, H, c.slab), dev);
+    if (keep <= 0) throw Bad("keep: expected a positive number");
+    if (kept) plain(*kept, "kept", at::kInt, dims(B, H, keep), dev);
+    if (nl) plain(*nl, "new_lens", at::kInt, dims(B), dev);
+    int64_t room = 0;
+    const auto type = k.scalar_type();
+    if (ko) {
+      room = ko->dim() == 4 ? ko->size(1) : 0;
+      plain(*ko, "k_out", type, dims(B, room, H, D), dev);
+      if (!v != !vo) throw Bad("v_out: expected next to k_out, as v");
+      if (vo) plain(*vo, "v_out", type, dims(B, room, H, D), dev);
+      if (c.int8 && (!kso || !vs != !vso)) throw Bad("k_scale_out, v_scale_out: an int8 cache needs them");
+      if (room < keep) throw Bad("k_out: no room for the tokens that are kept");
+    } else if (vo || kso || vso || wo) {
+      throw Bad("k_out: expected with the other outputs");
+    }
+    if (kso) plain(*kso, "k_scale_out", at::kFloat, dims(B, H, room), dev);
+    if (vso) plain(*vso, "v_scale_out", at::kFloat, dims(B, H, room), dev);
+    if (wo) plain(*wo, "weights_out", at::kFloat, dims(B, H, room), dev);
+    const Tensor* moved[5] = {ko ? ko : &k, ko ? vo : v, ko ? kso : ks, ko ? vso : vs, ko ? wo : &weights};
+    for (const Tensor* t : moved) not_tracked(t, "an output");
+    on_current(dev);
+    Stream st(a[18], dev);
+    const auto ints = k.options().dtype(at::kInt);
+    const Tensor kt = kept ? *kept : at::empty(dims(B, H, keep), ints), nt = nl ? *nl : at::empty(dims(B), ints);
+    const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k"),
+              cap = table ? small(a[7], "max_seq_len") : 0, oc = small(room, "k_out");
+    const char* fn = table ? (c.int8 ? "kv_evict_int8_paged" : "kv_evict_paged")
+                           : (c.int8 ? "kv_evict_int8_contig" : "kv_evict_contig");
+    call(fn, [&] {
+      int *kd = ptr<int>(kt), *nd = ptr<int>(nt);
+      float* wd = ptr<float>(weights);
+      if (table)
+        return c.int8 ? g_lib.kv_evict_int8_paged(ptr(k), ptr(v), ptr<float>(ks), ptr<float>(vs), wd, ptr<int>(table),
+                                                  ptr<int>(lens), B, H, D, slab, cols, slabs, cap, keep, first, recent,
+                                                  ptr(ko), ptr(vo), ptr<float>(kso), ptr<float>(vso), ptr<float>(wo), oc, kd,
+                                                  nd, st.raw)
+                      : g_lib.kv_evict_paged(ptr(k), ptr(v), wd, ptr<int>(table), ptr<int>(lens), B, H, D, slab, cols, slabs,
+                                             cap, keep, first, recent, ptr(ko), ptr(vo), ptr<float>(wo), oc, kd, nd, st.raw);
+      return c.int8 ? g_lib.kv_evict_int8_contig(ptr(k), ptr(v), ptr<float>(ks), ptr<float>(vs), wd, ptr<int>(lens), B, H, D,
+                                                 slab, keep, first, recent, ptr(ko), ptr(vo), ptr<float>(kso),
+                                                 ptr<float>(vso), ptr<float>(wo), oc, kd, nd, st.raw)
+                    : g_lib.kv_evict_contig(ptr(k), ptr(v), wd, ptr<int>(lens), B, H, D, slab, keep, first, recent, ptr(ko),
+                                            ptr(vo), ptr<float>(wo), oc, kd, nd, st.raw);
+    });
+    for (const Tensor* t : moved) written(t);
+    written(kept);
+    written(nl);
+    PyObject* x = kept ? same(a[11]) : THPVariable_Wrap(kt);
+    PyObject* y = nl ? same(a[12]) : THPVariable_Wrap(nt);
+    PyObject* r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return r;
+  });
+}
+
 // ---------------------------------------------------------------- the library
 
 // (path, DecodeAttnError): the shared library whose entry points the calls above use.
@@ -592,6 +909,24 @@ PyObject* open(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   FIND(latent_workspace_bytes)
   FIND(latent_prefill_contig)
   FIND(latent_prefill_workspace_bytes)
+  FIND(prefix_attn_contig)
+  FIND(prefix_attn_paged)
+  FIND(prefix_attn_workspace_bytes)
+  FIND(block_means_contig)
+  FIND(block_means_paged)
+  FIND(block_select)
+  FIND(sparse_attn_contig)
+  FIND(sparse_attn_paged)
+  FIND(sparse_attn_workspace_bytes)
+  FIND(kv_weights_contig)
+  FIND(kv_weights_paged)
+  FIND(kv_weights_int8_contig)
+  FIND(kv_weights_int8_paged)
+  FIND(kv_weights_workspace_bytes)
+  FIND(kv_evict_contig)
+  FIND(kv_evict_paged)
+  FIND(kv_evict_int8_contig)
+  FIND(kv_evict_int8_paged)
 #undef FIND
   g_lib = l;
   Py_INCREF(a[1]);
@@ -600,8 +935,10 @@ PyObject* open(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {FAST(open),    FAST(rope_apply),  FAST(kv_write),       FAST(kv_read),
-                           FAST(latent_attn), FAST(latent_prefill), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {FAST(open),         FAST(rope_apply),  FAST(kv_write),     FAST(kv_read),
+                           FAST(latent_attn),  FAST(latent_prefill), FAST(prefix_attn), FAST(block_means),
+                           FAST(block_select), FAST(sparse_attn), FAST(kv_weights),   FAST(kv_evict),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding_ext", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,407 @@
+// Blocks of a cache: the mean key of each, and the selection of a query's blocks by its
+// scores with them.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "device_error.cuh"
+#include "ptx.cuh"
+#include "seg_kernel.cuh"
+
+namespace da {
+
+// ---------------------------------------------------------------- mean keys
+
+// mean_j = (1 / |j|) sum of the keys of block j's tokens below the length, in fp32, rounded
+// once to bf16.  Bytes bound it (a key read once, 1 / block of that written).  A CTA takes
+// one block and a share of its row: groups of threads, one 16-byte chunk a thread, take every
+// groups-th token each, and are added in order through shared memory.  A step's few blocks
+// are cut into shares so that the whole card loads them.
+struct MeansParams {
+  const __nv_bfloat16* k;
+  const int *page_table, *seq_lens;
+  __nv_bfloat16* means;  // [B, Hkv, max_blocks, D]
+  int B, n, Hkv, D, cap, ctx;
+  int page_size, max_pages, num_pages;
+  int block, max_blocks;
+  int touched;  // blocks a sequence, at most
+  int shares;   // CTAs a block; a share is at most kMeansThreads chunks
+};
+constexpr int kMeansThreads = 256;
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const __grid_constant__ MeansParams p) {
+  __shared__ float sums[kMeansThreads * 9];  // [group][chunk][8], a chunk 9 apart
+  pdl_wait_primary();
+  const int share = blockIdx.x % p.shares;
+  const long long bj = blockIdx.x / p.shares;
+  const int b = (int)(bj / p.touched);
+  const int L = seg_len(p.seq_lens, b, p.cap);
+  const int j = max(0, L - p.n) / p.block + (int)(bj % p.touched);
+  const long long t0 = (long long)j * p.block;
+  if (t0 >= L) return;
+  const int count = min(p.block, L - (int)t0);
+  const int chunks = p.Hkv * p.D / 8, per = (chunks + p.shares - 1) / p.shares;
+  const int c0 = share * per, here = min(per, chunks - c0);
+  if (here <= 0) return;
+  const int groups = kMeansThreads / here, g = threadIdx.x / here, c = threadIdx.x - g * here;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (g < groups) {
+#pragma unroll 8
+    for (int i = g; i < count; i += groups) {
+      const int t = (int)t0 + i;
+      size_t row;
+      if constexpr (PAGED) {
+        const int col = t / p.page_size;
+        int page = load_dependent(p.page_table + (size_t)b * p.max_pages + col);
+        if ((unsigned)page >= (unsigned)p.num_pages) {
+          atomicOr(&g_error_word, 4u);
+          page = 0;
+        }
+        row = (size_t)page * p.page_size + (t - col * p.page_size);
+      } else {
+        row = (size_t)b * p.ctx + t;
+      }
+      const uint4 w = load_dependent(reinterpret_cast<const uint4*>(p.k) + row * chunks + c0 + c);
+      s[0] += bf16lo_to_f32(w.x);
+      s[1] += bf16hi_to_f32(w.x);
+      s[2] += bf16lo_to_f32(w.y);
+      s[3] += bf16hi_to_f32(w.y);
+      s[4] += bf16lo_to_f32(w.z);
+      s[5] += bf16hi_to_f32(w.z);
+      s[6] += bf16lo_to_f32(w.w);
+      s[7] += bf16hi_to_f32(w.w);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[threadIdx.x * 9 + e] = s[e];
+  }
+  __syncthreads();
+  if (g > 0) return;
+  for (int o = 1; o < groups; ++o)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += sums[(o * here + c) * 9 + e];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = s[e] / (float)count;
+  const int at = (c0 + c) * 8, h = at / p.D, d = at - h * p.D;
+  *reinterpret_cast<uint4*>(p.means + (((size_t)b * p.Hkv + h) * p.max_blocks + j) * p.D + d) =
+      make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+}
+
+// ---------------------------------------------------------------- selection
+
+// For query token i of sequence b (position p = L - n + i) and KV head h, score_j =
+// max over the group's heads of <q, mean_j>, j = 0 .. p / block.  The first `first` blocks
+// and the last `recent` up to the token's own are taken, and of the others the best scores
+// until there are `pick` (ties: the lowest block).  Out: ascending, -1 behind.
+//
+// The selection is that of the exact scores.  The products run on the warp-level MMA in
+// fp32 (a mean is read once for all 16 rows: heads, and neighbouring tokens where a group
+// has few), whose sums are off by mu = D / 16 * 17 * 2^-23 |q| |mean| at most: bf16 products are
+// exact, and each of the D / 16 MMAs adds 17 terms, each cut off at 2^-23 of the largest at
+// worst.  Where the last block taken and the next differ by more than 2 mu, no block can be on
+// the wrong side.  Otherwise those within 2 mu of the border (hardly ever more than two) are
+// computed again in 64 bits and taken in that order.
+struct SelectParams {
+  const __nv_bfloat16 *q, *means;
+  const int* seq_lens;
+  int* out;  // [B, n, Hkv, pick]
+  int B, n, Hq, Hkv, G, cap;
+  int block, max_blocks, pick, first, recent;
+  int qt;       // query tokens a CTA (cluster)
+  int cluster;  // CTAs that share the blocks' scores
+};
+constexpr int kSelectThreads = 256;
+constexpr int kSelectTokens = 16;     // a CTA, at most
+constexpr int kSelectBlocks = 8192;
+
+// mu of a query whose largest square of a head's norm has these bits, among means likewise;
+// 2^-110 is for products below fp32's range.
+template <int D>
+__device__ __forceinline__ float select_slack(uint32_t q2, uint32_t mean2) {
+  return D / 16 * 17 * 1.1920929e-7f * sqrtf(__uint_as_float(q2)) * sqrtf(__uint_as_float(mean2)) + 7.7037198e-34f;
+}
+
+__device__ __forceinline__ float key_float(uint32_t k) {
+  if (k == 0u) return kNegInf;
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// atomicMax at shared-memory address a of the cluster's CTA 0.
+__device__ __forceinline__ void max_at_leader(uint32_t a, uint32_t v) {
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\tred.shared::cluster.max.u32 [r], %1;\n\t}" ::"r"(a),
+               "r"(v)
+               : "memory");
+}
+
+// The 64-bit scores and numbers of the blocks at the border, the queries' keys and bits.
+__host__ __device__ inline size_t select_smem(int qt, int max_blocks) {
+  const int words = (max_blocks + 31) / 32;
+  return (size_t)max_blocks * 8 + (size_t)qt * (max_blocks + words) * 4 + (size_t)max_blocks * 2 + 16;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_mean2, s_q2[16], s_border[16];  // bits of the largest squares of norms, keys
+  __shared__ int s_open[16], s_count, s_sum[kSelectThreads / 32];
+  const int words = (p.max_blocks + 31) / 32;
+  double* exact = reinterpret_cast<double*>(smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(exact + p.max_blocks);
+  uint32_t* bits = keys + (size_t)p.qt * p.max_blocks;
+  uint16_t* list = reinterpret_cast<uint16_t*>(bits + (size_t)p.qt * words);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
+
+  pdl_wait_primary();
+  const long long unit = blockIdx.x / p.cluster;
+  const int tiles = (p.n + p.qt - 1) / p.qt;
+  const int i0 = (int)(unit % tiles) * p.qt, h = (int)(unit / tiles % p.Hkv), b = (int)(unit / tiles / p.Hkv);
+  const int qn = min(p.qt, p.n - i0);  // query tokens here
+  const int L = seg_len(p.seq_lens, b, p.cap);
+  const int last = L - p.n + i0 + qn - 1;  // position of the last
+  const int blocks = last < 0 ? 0 : min(last / p.block + 1, p.max_blocks);
+  const __nv_bfloat16* means = p.means + ((size_t)b * p.Hkv + h) * p.max_blocks * D;
+
+  for (int e = threadIdx.x; e < qn * p.max_blocks; e += kSelectThreads) keys[e] = 0u;
+  for (int e = threadIdx.x; e < qn * words; e += kSelectThreads) bits[e] = 0u;
+  if (threadIdx.x < 16) s_q2[threadIdx.x] = 0u;
+  if (threadIdx.x == 0) {
+    s_mean2 = 0u;
+    s_count = 0;
+  }
+  if (p.cluster > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+
+  // scores: 16 query rows against 8 blocks a warp's step.  Element 32 c + 8 t + e of a row is
+  // thread t's of the quad, so that rows of both are read 16 bytes at a time; the order of a
+  // product's terms is free
+  const int rows = qn * p.G;
+  for (int r0 = 0; r0 < rows; r0 += 16) {
+    uint4 a[D / 32][2];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int row = r0 + lane / 4 + 8 * hf;
+      float q2 = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        a[c][hf] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows) {
+          const size_t token = (size_t)b * p.n + i0 + row / p.G;
+          a[c][hf] = load_dependent(
+              reinterpret_cast<const uint4*>(p.q + (token * p.Hq + h * p.G + row % p.G) * D) + 4 * c + lane % 4);
+        }
+        const uint32_t w[4] = {a[c][hf].x, a[c][hf].y, a[c][hf].z, a[c][hf].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          q2 = fmaf(bf16lo_to_f32(w[e]), bf16lo_to_f32(w[e]), q2);
+          q2 = fmaf(bf16hi_to_f32(w[e]), bf16hi_to_f32(w[e]), q2);
+        }
+      }
+      q2 += __shfl_xor_sync(0xffffffffu, q2, 1);
+      q2 += __shfl_xor_sync(0xffffffffu, q2, 2);
+      if (warp == 0 && lane % 4 == 0 && row < rows) atomicMax(&s_q2[row / p.G], __float_as_uint(q2));
+    }
+    float top2 = 0.f;
+    for (int nt = rank * (kSelectThreads / 32) + warp; nt * 8 < blocks; nt += p.cluster * (kSelectThreads / 32)) {
+      const int j = nt * 8 + lane / 4;
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, m2 = 0.f;
+      uint4 w[D / 32];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+        w[c] = j < blocks ? load_dependent(reinterpret_cast<const uint4*>(means + (size_t)j * D) + 4 * c + lane % 4)
+                          : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        mma_bf16_16816(s, a[c][0].x, a[c][1].x, a[c][0].y, a[c][1].y, w[c].x, w[c].y);
+        mma_bf16_16816(s, a[c][0].z, a[c][1].z, a[c][0].w, a[c][1].w, w[c].z, w[c].w);
+        const uint32_t e4[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          m2 = fmaf(bf16lo_to_f32(e4[e]), bf16lo_to_f32(e4[e]), m2);
+          m2 = fmaf(bf16hi_to_f32(e4[e]), bf16hi_to_f32(e4[e]), m2);
+        }
+      }
+      m2 += __shfl_xor_sync(0xffffffffu, m2, 1);
+      m2 += __shfl_xor_sync(0xffffffffu, m2, 2);
+      top2 = m2 != m2 ? -kNegInf : fmaxf(top2, m2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = r0 + lane / 4 + 8 * (e >> 1), col = nt * 8 + 2 * (lane % 4) + (e & 1);
+        if (row < rows && col < blocks)
+          max_at_leader(smem_u32(keys + (size_t)(row / p.G) * p.max_blocks + col), float_key(s[e]));
+      }
+    }
+    if (lane % 4 == 0 && top2 > 0.f) max_at_leader(smem_u32(&s_mean2), __float_as_uint(top2));
+  }
+  if (p.cluster > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (rank != 0) return;
+
+  // what query qi sees and must take
+  struct Want {
+    int visible, lo, hi, need;  // candidates [lo, hi), of which need are taken; need < 0: every visible block
+  };
+  auto want = [&](int qi) {
+    const int pos = L - p.n + i0 + qi;
+    Want w;
+    w.visible = pos < 0 ? 0 : min(pos / p.block + 1, p.max_blocks);
+    w.lo = min(p.first, w.visible);
+    w.hi = max(w.lo, w.visible - p.recent);
+    w.need = w.visible <= p.pick ? -1 : p.pick - (w.visible - (w.hi - w.lo));
+    return w;
+  };
+  auto take = [&](int qi, int j) { atomicOr(&bits[qi * words + (j >> 5)], 1u << (j & 31)); };
+
+  // the border of each query: the need-th largest key, by its bits from the top.  One query:
+  // the whole CTA counts; several: a warp each
+  const bool wide = qn == 1;
+  const int size = wide ? kSelectThreads : 32, me = wide ? (int)threadIdx.x : lane;
+  auto total = [&](int v) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (!wide) return v;
+    __syncthreads();
+    if (lane == 0) s_sum[warp] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kSelectThreads / 32; ++w) v += s_sum[w];
+    return v;
+  };
+  auto largest = [&](uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (!wide) return v;
+    __syncthreads();
+    if (lane == 0) s_sum[warp] = (int)v;
+    __syncthreads();
+    v = 0u;
+#pragma unroll
+    for (int w = 0; w < kSelectThreads / 32; ++w) v = max(v, (uint32_t)s_sum[w]);
+    return v;
+  };
+  for (int qi = wide ? 0 : warp; qi < qn; qi += wide ? 1 : kSelectThreads / 32) {
+    const Want w = want(qi);
+    const uint32_t* key = keys + (size_t)qi * p.max_blocks;
+    for (int j = me; j < w.visible; j += size)
+      if (w.need < 0 || j < w.lo || j >= w.hi) take(qi, j);
+    if (w.need <= 0) continue;
+    uint32_t border = 0u;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t at = border | 1u << bit;
+      int count = 0;
+      for (int j = w.lo + me; j < w.hi; j += size) count += key[j] >= at;
+      if (total(count) >= w.need) border = at;
+    }
+    uint32_t below = 0u;
+    int same = 0;
+    for (int j = w.lo + me; j < w.hi; j += size) {
+      if (key[j] < border) below = max(below, key[j]);
+      same += key[j] >= border;
+    }
+    below = largest(below);
+    const bool split = total(same) > w.need;  // equal keys on both sides
+    const float mu = select_slack<D>(s_q2[qi], s_mean2);
+    const bool sure = !split && key_float(border) - key_float(below) > 2.f * mu;
+    if (sure) {
+      for (int j = w.lo + me; j < w.hi; j += size)
+        if (key[j] >= border) take(qi, j);
+    } else if (me == 0) {
+      s_border[qi] = border;
+      s_open[atomicAdd(&s_count, 1)] = qi;
+    }
+  }
+  __syncthreads();
+
+  // queries whose border is too close to call
+  const int open = s_count;
+  for (int o = 0; o < open; ++o) {
+    const int qi = s_open[o];
+    const Want w = want(qi);
+    const uint32_t* key = keys + (size_t)qi * p.max_blocks;
+    const float border = key_float(s_border[qi]);
+    const float mu = select_slack<D>(s_q2[qi], s_mean2);
+    __syncthreads();
+    if (threadIdx.x == 0) s_count = 0;
+    __syncthreads();
+    int sure = 0;
+    for (int j = w.lo + threadIdx.x; j < w.hi; j += kSelectThreads) {
+      const float s = key_float(key[j]);
+      if (s > border + 2.f * mu) {
+        take(qi, j);
+        ++sure;
+      } else if (!(s < border - 2.f * mu)) {
+        list[atomicAdd(&s_count, 1)] = (uint16_t)j;
+      }
+    }
+    sure = __reduce_add_sync(0xffffffffu, sure);
+    if (lane == 0) s_sum[warp] = sure;
+    __syncthreads();
+    sure = 0;
+    for (int i = 0; i < kSelectThreads / 32; ++i) sure += s_sum[i];
+    const int count = s_count, left = w.need - sure;
+    const __nv_bfloat16* q = p.q + (((size_t)b * p.n + i0 + qi) * p.Hq + h * p.G) * D;
+    for (int c = warp; c < count; c += kSelectThreads / 32) {
+      const __nv_bfloat16* mean = means + (size_t)list[c] * D;
+      double best = (double)kNegInf;
+      for (int g = 0; g < p.G; ++g) {
+        double s = 0.0;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+          s = fma((double)__bfloat162float(load_dependent(q + g * D + d * 32 + lane)),
+                  (double)__bfloat162float(load_dependent(mean + d * 32 + lane)), s);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (s > best) best = s;
+      }
+      if (lane == 0) exact[c] = best;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < count; c += kSelectThreads) {
+      const double s = exact[c];
+      const int j = list[c];
+      int before = 0;
+      for (int i = 0; i < count; ++i) before += exact[i] > s || (exact[i] == s && list[i] < j);
+      if (before < left) take(qi, j);
+    }
+    __syncthreads();
+  }
+
+  // the numbers of the bits, ascending
+  for (int qi = warp; qi < qn; qi += kSelectThreads / 32) {
+    int* dst = p.out + (((size_t)b * p.n + i0 + qi) * p.Hkv + h) * p.pick;
+    int at = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      uint32_t w = w0 + lane < words ? bits[qi * words + w0 + lane] : 0u;
+      const int mine = __popc(w);
+      int sum = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      int k = at + sum - mine;
+      while (w) {
+        if (k < p.pick) dst[k] = (w0 + lane) * 32 + __ffs(w) - 1;
+        ++k;
+        w &= w - 1;
+      }
+      at += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    for (int k = at + lane; k < p.pick; k += 32) dst[k] = -1;
+  }
+}
+
+}  // namespace da

@@ -16,10 +16,15 @@
 #include "host_util.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
+#include "units.cuh"
 
 namespace da {
 
-int take_cache_error_word(unsigned int* flags) { return take_unit_error_word(flags); }
+// Of this unit and of those in units.cuh.
+int take_cache_error_word(unsigned int* flags) {
+  return take_unit_error_word(flags) || take_prefix_error_word(flags) || take_sparse_error_word(flags) ||
+         take_evict_error_word(flags);
+}
 
 namespace {
 

@@ -1,0 +1,167 @@
+// Entry points of attention behind a shared prefix (declared in include/decode_attn.h).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/decode_attn.h"
+#include "host_util.cuh"
+#include "seg_host.cuh"
+#include "seg_kernel.cuh"
+#include "units.cuh"
+
+namespace da {
+
+int take_prefix_error_word(unsigned int* flags) { return take_unit_error_word(flags); }
+
+namespace {
+
+// What a call of these sizes launches.
+struct PrefixShape {
+  int rt, rt_prefix, ctas;
+  long long slots, bytes;
+};
+
+int prefix_shape(int B, int n, int Hq, int Hkv, int D, int sms, PrefixShape* s) {
+  if (B < 0 || n < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return DA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128 && D != 256) return DA_ERR_UNSUPPORTED;
+  const int G = Hq / Hkv;
+  if (G > 64 || Hq > 65536 || product(B, n, Hq) > 0x7fffffffLL / 16) return DA_ERR_UNSUPPORTED;
+  s->rt = (int)(((long long)n * G + 15) / 16);
+  s->rt_prefix = (int)(((long long)B * n * G + 15) / 16);
+  s->ctas = seg_ctas(D, sms);
+  s->slots = (long long)Hkv * s->rt_prefix + (long long)B * Hkv * s->rt + s->ctas;
+  s->bytes = seg_partial_bytes(s->slots, D);
+  return DA_OK;
+}
+
+struct PrefixCall {
+  SegParams p;
+  bool paged;
+  int D;
+  void* workspace;
+  long long workspace_bytes;
+  long long cap;
+};
+
+template <int D>
+int launch_prefix(const PrefixCall& c, const PrefixShape& s, cudaStream_t st) {
+  const long long rows = (long long)c.p.B * c.p.n * c.p.Hq;
+  if (int e = c.paged ? launch_seg<D, true, kSegRange>(c.p, st) : launch_seg<D, false, kSegRange>(c.p, st)) return e;
+  return launch_dependent(seg_merge_prefix_kernel<D>, (unsigned)((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)),
+                          kMergeThreads, 0, st, c.p);
+}
+
+int prefix_call(PrefixCall& c, float scale, void* stream) {
+  SegParams& p = c.p;
+  PrefixShape s;
+  int dev, sms, optin;
+  if (int e = prefix_shape(p.B, p.n, p.Hq, p.Hkv, c.D, 1, &s)) return e;
+  if (p.base < 0 || c.cap < 0 || !std::isfinite(scale)) return DA_ERR_INVALID_ARG;
+  if (c.cap > 0x7fffffffLL - kTile) return DA_ERR_UNSUPPORTED;
+  if (c.paged && (p.page_size <= 0 || p.max_pages < 0 || p.num_pages < 0)) return DA_ERR_INVALID_ARG;
+  if (c.paged && p.page_size % 16) return DA_ERR_UNSUPPORTED;
+  if (p.B == 0 || p.n == 0) return DA_OK;
+  p.cap = (int)c.cap;
+  if (p.base > p.cap) p.base = p.cap;
+  p.G = p.Hq / p.Hkv;
+  if (!p.q || !p.out || !aligned(p.q, 16) || !aligned(p.out, 16) || !aligned(p.seq_lens, 4) || !aligned(p.k, 16) ||
+      !aligned(p.v, 16) || !aligned(p.kp, 16) || !aligned(p.vp, 16) || !aligned(p.page_table, 4) ||
+      !aligned(p.prefix_table, 4))
+    return DA_ERR_INVALID_ARG;
+  const long long on = product(p.B, p.n, p.Hq, c.D, 2), row = product(p.Hkv, c.D, 2);
+  const long long cn = c.paged ? product(p.num_pages, p.page_size, row) : product(p.B, p.ctx, row);
+  if (c.paged) {
+    if (!p.seq_lens || (p.max_pages > 0 && !p.page_table) || (p.base > 0 && !p.prefix_table) || (cn > 0 && (!p.k || !p.v)))
+      return DA_ERR_INVALID_ARG;
+    if (p.num_pages == 0) p.base = p.cap = 0;  // no token: zeros
+  } else if ((cn > 0 && (!p.k || !p.v)) || (p.base > 0 && (!p.kp || !p.vp))) {
+    return DA_ERR_INVALID_ARG;
+  }
+  const long long pn = c.paged ? 0 : product(p.base, row);
+  for (const void* src : {(const void*)p.k, (const void*)p.v})
+    if (overlap(p.out, on, src, cn)) return DA_ERR_INVALID_ARG;
+  if (overlap(p.out, on, p.q, on) || overlap(p.out, on, p.kp, pn) || overlap(p.out, on, p.vp, pn))
+    return DA_ERR_INVALID_ARG;
+  if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
+  if (int e = prefix_shape(p.B, p.n, p.Hq, p.Hkv, c.D, sms, &s)) return e;
+  if (!c.workspace || !aligned(c.workspace, 16) || c.workspace_bytes < s.bytes) return DA_ERR_WORKSPACE;
+  if (overlap(c.workspace, s.bytes, p.out, on)) return DA_ERR_INVALID_ARG;
+  p.rt = s.rt;
+  p.rt_prefix = s.rt_prefix;
+  p.ctas = s.ctas;
+  seg_partials(p, c.workspace, s.slots, c.D);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return c.D == 64 ? launch_prefix<64>(c, s, st) : c.D == 128 ? launch_prefix<128>(c, s, st) : launch_prefix<256>(c, s, st);
+}
+
+PrefixCall prefix_params(const void* q, const void* k, const void* v, const int* seq_lens, int batch, int q_len,
+                         int num_q_heads, int num_kv_heads, int head_dim, int prefix_len, void* workspace,
+                         long long workspace_bytes, void* out) {
+  PrefixCall c = {};
+  c.p.q = static_cast<const __nv_bfloat16*>(q);
+  c.p.k = static_cast<const __nv_bfloat16*>(k);
+  c.p.v = static_cast<const __nv_bfloat16*>(v);
+  c.p.seq_lens = seq_lens;
+  c.p.out = static_cast<__nv_bfloat16*>(out);
+  c.p.B = batch;
+  c.p.n = q_len;
+  c.p.Hq = num_q_heads;
+  c.p.Hkv = num_kv_heads;
+  c.p.base = prefix_len;
+  c.D = head_dim;
+  c.workspace = workspace;
+  c.workspace_bytes = workspace_bytes;
+  return c;
+}
+
+}  // namespace
+}  // namespace da
+
+using namespace da;
+
+extern "C" long long prefix_attn_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                                 int num_sms) {
+  int sms = num_sms;
+  if (sms <= 0) {
+    int dev, optin;
+    if (current_device(&dev) || device_info(dev, &sms, &optin)) return -DA_ERR_CUDA;
+  }
+  PrefixShape s;
+  if (int e = prefix_shape(batch, q_len, num_q_heads, num_kv_heads, head_dim, sms, &s)) return -e;
+  return s.bytes;
+}
+
+extern "C" int prefix_attn_contig(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                                  const int* seq_lens, int batch, int q_len, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int prefix_len, int max_ctx, float scale, void* workspace,
+                                  long long workspace_bytes, void* out, void* stream) {
+  if (max_ctx < 0 || prefix_len < 0) return DA_ERR_INVALID_ARG;
+  PrefixCall c = prefix_params(q, k, v, seq_lens, batch, q_len, num_q_heads, num_kv_heads, head_dim, prefix_len,
+                               workspace, workspace_bytes, out);
+  c.p.kp = static_cast<const __nv_bfloat16*>(k_prefix);
+  c.p.vp = static_cast<const __nv_bfloat16*>(v_prefix);
+  c.p.ctx = max_ctx;
+  c.cap = (long long)prefix_len + max_ctx;
+  return prefix_call(c, scale, stream);
+}
+
+extern "C" int prefix_attn_paged(const void* q, const void* k_pool, const void* v_pool, const int* prefix_table,
+                                 int prefix_len, const int* page_table, const int* seq_lens, int batch, int q_len,
+                                 int num_q_heads, int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq,
+                                 int num_pages, int max_seq_len, float scale, void* workspace,
+                                 long long workspace_bytes, void* out, void* stream) {
+  if (max_seq_len < 0) return DA_ERR_INVALID_ARG;
+  PrefixCall c = prefix_params(q, k_pool, v_pool, seq_lens, batch, q_len, num_q_heads, num_kv_heads, head_dim,
+                               prefix_len, workspace, workspace_bytes, out);
+  c.paged = true;
+  c.p.prefix_table = prefix_table;
+  c.p.page_table = page_table;
+  c.p.page_size = page_size;
+  c.p.max_pages = max_pages_per_seq;
+  c.p.num_pages = num_pages;
+  c.cap = capacity(page_size, max_pages_per_seq, max_seq_len);
+  return prefix_call(c, scale, stream);
+}

@@ -1,0 +1,54 @@
+// Host side of seg_kernel.cuh: grid, partials and launch.
+#pragma once
+
+#include <atomic>
+
+#include "host_util.cuh"
+#include "seg_kernel.cuh"
+
+namespace da {
+namespace {
+
+// CTAs of the seg kernels: as many as run at once.
+int seg_ctas(int D, int sms) { return sms * (D == 64 ? SegGeo<64>::PER_SM : D == 128 ? SegGeo<128>::PER_SM : SegGeo<256>::PER_SM); }
+
+long long seg_partial_bytes(long long slots, int D) { return slots * 16 * (D * 4ll + 8); }
+
+void seg_partials(SegParams& p, void* workspace, long long slots, int D) {
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + slots * 16 * D);
+}
+
+// Tokens that a paged cache of a sequence can hold (what the sizes allow, max_seq_len at most).
+long long capacity(int page_size, int max_pages, int max_seq_len) {
+  if (page_size <= 0 || max_pages < 0) return 0;
+  const long long room = (long long)max_pages * page_size;
+  return room < max_seq_len ? room : max_seq_len;
+}
+
+// Lets a kernel use this much shared memory, once a device.
+template <auto KERN>
+int allow_smem(size_t bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev;
+  if (current_device(&dev) || dev >= kMaxDevices) return DA_ERR_CUDA;
+  if (done.load(std::memory_order_relaxed) >> dev & 1) return DA_OK;
+  if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess ||
+      cudaFuncSetAttribute(KERN, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_CUDA;
+  }
+  done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return DA_OK;
+}
+
+template <int D, bool PAGED, int KIND>
+int launch_seg(const SegParams& p, cudaStream_t st) {
+  using Gm = SegGeo<D>;
+  if (int e = allow_smem<seg_kernel<D, PAGED, KIND>>(Gm::SMEM)) return e;
+  return launch_dependent(seg_kernel<D, PAGED, KIND>, (unsigned)p.ctas, Gm::THREADS, Gm::SMEM, st, p);
+}
+
+}  // namespace
+}  // namespace da

@@ -547,6 +547,159 @@ long long latent_prefill_workspace_bytes(int batch, int q_len, int num_heads, in
 const char* decode_status_string(int status);
 
 /*
+ * Attention behind a shared prefix.
+ *
+ * prefix_attn_contig / prefix_attn_paged — attention of the last q_len tokens of every
+ * sequence of a batch whose sequences begin with the same prefix_len tokens.  The prefix is
+ * read once for the whole batch, the rest of each sequence once for that sequence, and the
+ * two parts are joined by their softmax sums.  Query token i of sequence b (position L_b -
+ * q_len + i, L_b prefix included) attends to tokens 0 .. L_b - q_len + i, prefix and rest
+ * alike; one that sees none (a batch entry of length 0, say) gives zeros.  Query head h reads
+ * KV head h / G, G = num_q_heads / num_kv_heads <= 64.
+ *  q, out   bf16 [batch, q_len, num_q_heads, head_dim], token-major; head_dim 64, 128 or 256
+ *  k_prefix, v_prefix  contiguous: bf16 [prefix_len, num_kv_heads, head_dim]
+ *  k, v     contiguous: bf16 [batch, max_ctx, num_kv_heads, head_dim], row t - prefix_len holds token t;
+ *           paged: pools [num_pages, page_size, num_kv_heads, head_dim], page_size a multiple of 16
+ *  prefix_table  int32, the prefix's ceil(prefix_len / page_size) pages
+ *  page_table    int32 [batch, max_pages_per_seq] of the whole sequences: entry t / page_size is token t's
+ *           page for t >= prefix_len; the entries of the prefix's whole pages are not read, so the prefix
+ *           may end inside a page
+ *  seq_lens int32 [batch], clamped to [0, prefix_len + max_ctx], or to what the table and max_seq_len hold;
+ *           NULL (contiguous only): all prefix_len + max_ctx
+ *  workspace  prefix_attn_workspace_bytes(...) bytes, 16-byte aligned; contents need not be kept, calls that
+ *           share one must not overlap on the GPU.  num_sms <= 0: of the current device.
+ * Softmax in fp32, the weights rounded to bf16 for the product with V, fp32 sums, one rounding of the output.
+ * Pages outside [0, num_pages) set bit 2 of the device error word and read page 0 instead.  Outputs may not
+ * overlap inputs.
+ */
+long long prefix_attn_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                      int num_sms);
+int prefix_attn_contig(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                       const int* seq_lens, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                       int prefix_len, int max_ctx, float scale, void* workspace, long long workspace_bytes, void* out,
+                       void* stream);
+int prefix_attn_paged(const void* q, const void* k_pool, const void* v_pool, const int* prefix_table, int prefix_len,
+                      const int* page_table, const int* seq_lens, int batch, int q_len, int num_q_heads,
+                      int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq, int num_pages,
+                      int max_seq_len, float scale, void* workspace, long long workspace_bytes, void* out, void* stream);
+
+/*
+ * Attention over selected blocks.
+ *
+ * A sequence's cache is taken as blocks of block_size tokens (block j: tokens j block_size ..).
+ *
+ * block_means_contig / block_means_paged — the mean keys of the blocks that hold the last q_len
+ * tokens of each sequence (q_len >= the length: of all its blocks; after the keys are written):
+ * means[b, h, j] = the mean of the block's keys below the length, summed in fp32, rounded once.
+ * Other blocks' means stay as they were.
+ *  k        bf16 cache or pool as above; head_dim a multiple of 8
+ *  means    bf16 [batch, num_kv_heads, max_blocks, head_dim]; max_blocks * block_size must cover max_ctx (paged:
+ *           what the table and max_seq_len hold)
+ */
+int block_means_contig(const void* k, const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim,
+                       int max_ctx, int block_size, int max_blocks, void* means, void* stream);
+int block_means_paged(const void* k_pool, const int* page_table, const int* seq_lens, int batch, int q_len,
+                      int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq, int num_pages,
+                      int max_seq_len, int block_size, int max_blocks, void* means, void* stream);
+/*
+ * block_select — the blocks that each of the last q_len tokens attends to, for every KV head.  Token i of
+ * sequence b, at position p = L_b - q_len + i, sees blocks 0 .. p / block_size.  It takes the first `first` and
+ * the last `recent` (>= 1) of them, and of the others those with the largest max over the group's heads of
+ * <q, mean>, until it has n_select (>= first + recent) or all.  Scores are compared as if computed exactly (ties:
+ * the lower block; a head whose score is NaN counts as lowest).
+ *  q        bf16 [batch, q_len, num_q_heads, head_dim], head_dim 64, 128 or 256
+ *  means    as block_means writes them, max_blocks <= 8192; seq_lens is clamped to max_blocks * block_size (NULL:
+ *           that length)
+ *  out      int32 [batch, q_len, num_kv_heads, n_select], ascending, -1 behind the last
+ */
+int block_select(const void* q, const void* means, const int* seq_lens, int batch, int q_len, int num_q_heads,
+                 int num_kv_heads, int head_dim, int block_size, int max_blocks, int n_select, int first, int recent,
+                 int* out, void* stream);
+/*
+ * sparse_attn_contig / sparse_attn_paged — attention of the last q_len tokens over the listed blocks: query
+ * token i attends to the tokens of its blocks up to its own position.  An entry that is negative or past the
+ * position lists nothing, one that is listed twice counts twice, the order is free; a token whose blocks hold
+ * nothing gives zeros.
+ *  q, out, k, v, page_table, seq_lens, scale  as prefix_attn without a prefix
+ *  blocks   int32 [batch, q_len, num_kv_heads, n_select]; block_size a multiple of 16, of any relation to page_size
+ *  workspace  sparse_attn_workspace_bytes(head_dim, num_sms) bytes, 16-byte aligned
+ */
+long long sparse_attn_workspace_bytes(int head_dim, int num_sms);
+int sparse_attn_contig(const void* q, const void* k, const void* v, const int* blocks, const int* seq_lens, int batch,
+                       int q_len, int num_q_heads, int num_kv_heads, int head_dim, int max_ctx, int block_size,
+                       int n_select, float scale, void* workspace, long long workspace_bytes, void* out, void* stream);
+int sparse_attn_paged(const void* q, const void* k_pool, const void* v_pool, const int* blocks, const int* page_table,
+                      const int* seq_lens, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                      int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, int block_size, int n_select,
+                      float scale, void* workspace, long long workspace_bytes, void* out, void* stream);
+
+/*
+ * Weights and eviction.
+ *
+ * kv_weights_contig / kv_weights_paged / kv_weights_int8_* — what attention weight the last q_len tokens give
+ * each cached token: out[b, h, t] = decay * prior[b, h, t] + sum over the q_len tokens and the G heads of group h
+ * of softmax_t(scale <q, k>), causal as in prefix_attn without a prefix, for t < L_b; entries at and past L_b are
+ * neither read nor written.  Softmax and sums in fp32.
+ *  q        bf16 [batch, q_len, num_q_heads, head_dim], head_dim 64, 128 or 256, q_len * G <= 1024
+ *  k        bf16 or int8 cache or pool as for decode_attn_*; k_scale fp32 [batch, num_kv_heads, max_ctx] or
+ *           [num_pages, num_kv_heads, page_size]
+ *  prior, out  fp32, laid out like k_scale; prior may be out, or NULL (zeros), and may not overlap it otherwise
+ *  workspace  kv_weights_workspace_bytes(...) bytes, 16-byte aligned; max_len: max_ctx, or what the table and
+ *           max_seq_len hold
+ * Sequences may not share pages.  A page outside the pool is flagged (bit 2), read as page 0, and not written.
+ */
+long long kv_weights_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int max_len, int num_sms);
+int kv_weights_contig(const void* q, const void* k, const int* seq_lens, int batch, int q_len, int num_q_heads,
+                      int num_kv_heads, int head_dim, int max_ctx, float scale, float decay, const float* prior,
+                      void* workspace, long long workspace_bytes, float* out, void* stream);
+int kv_weights_paged(const void* q, const void* k_pool, const int* page_table, const int* seq_lens, int batch, int q_len,
+                     int num_q_heads, int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq,
+                     int num_pages, int max_seq_len, float scale, float decay, const float* prior, void* workspace,
+                     long long workspace_bytes, float* out, void* stream);
+int kv_weights_int8_contig(const void* q, const void* k_i8, const float* k_scale, const int* seq_lens, int batch,
+                           int q_len, int num_q_heads, int num_kv_heads, int head_dim, int max_ctx, float scale,
+                           float decay, const float* prior, void* workspace, long long workspace_bytes, float* out,
+                           void* stream);
+int kv_weights_int8_paged(const void* q, const void* k_pool_i8, const float* k_scale_pool, const int* page_table,
+                          const int* seq_lens, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                          int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, float scale, float decay,
+                          const float* prior, void* workspace, long long workspace_bytes, float* out, void* stream);
+/*
+ * kv_evict_contig / kv_evict_paged / kv_evict_int8_* — cuts each sequence down to `keep` tokens, KV head by KV
+ * head: of a sequence longer than that the first `first`, the last `recent`, and of the others those of the
+ * largest weights (ties: the lower position; NaN lowest, -0 as 0), first + recent <= keep; a shorter one keeps all.
+ * The kept tokens' keys, values, scales and weights move together to positions 0, 1, ... in their order.
+ * kept[b, h, i] is the old position of the token now at i, -1 behind the last; new_lens[b] = min(L_b, keep).
+ *  k, v, k_scale, v_scale  the cache or pools (v and v_scale may be NULL: keys only); head_dim * (2 or, int8, 1) a
+ *           multiple of 16 bytes, page_size any
+ *  weights  fp32, laid out like k_scale
+ *  seq_lens int32 [batch], clamped to the capacity; NULL (contiguous only): all max_ctx.  Not written.
+ *  k_out, v_out, k_scale_out, v_scale_out, weights_out  all NULL: the cache is compacted in place, and weights
+ *           [new_len, L_b) become 0.  Otherwise contiguous [batch, out_ctx, num_kv_heads, head_dim] and [batch,
+ *           num_kv_heads, out_ctx], out_ctx >= keep: rows past new_lens stay as they were, weights there
+ *           become 0.  weights_out may be NULL (not wanted) next to a k_out.
+ *  kept     int32 [batch, num_kv_heads, keep]; new_lens int32 [batch]
+ * In place, sequences may not share pages.  A page outside the pool is flagged (bit 2); rows from it are zeros,
+ * rows to it are not written.
+ */
+int kv_evict_contig(void* k, void* v, float* weights, const int* seq_lens, int batch, int num_kv_heads, int head_dim,
+                    int max_ctx, int keep, int first, int recent, void* k_out, void* v_out, float* weights_out,
+                    int out_ctx, int* kept, int* new_lens, void* stream);
+int kv_evict_paged(void* k_pool, void* v_pool, float* weights_pool, const int* page_table, const int* seq_lens,
+                   int batch, int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq, int num_pages,
+                   int max_seq_len, int keep, int first, int recent, void* k_out, void* v_out, float* weights_out,
+                   int out_ctx, int* kept, int* new_lens, void* stream);
+int kv_evict_int8_contig(void* k_i8, void* v_i8, float* k_scale, float* v_scale, float* weights, const int* seq_lens,
+                         int batch, int num_kv_heads, int head_dim, int max_ctx, int keep, int first, int recent,
+                         void* k_out, void* v_out, float* k_scale_out, float* v_scale_out, float* weights_out,
+                         int out_ctx, int* kept, int* new_lens, void* stream);
+int kv_evict_int8_paged(void* k_pool_i8, void* v_pool_i8, float* k_scale_pool, float* v_scale_pool, float* weights_pool,
+                        const int* page_table, const int* seq_lens, int batch, int num_kv_heads, int head_dim,
+                        int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, int keep, int first,
+                        int recent, void* k_out, void* v_out, float* k_scale_out, float* v_scale_out,
+                        float* weights_out, int out_ctx, int* kept, int* new_lens, void* stream);
+
+/*
  * decode_device_error — synchronise `stream`, then read and clear the device error
  * word of the current device.  *flags receives the word: bit 0 a kernel gave up on
  * a bounded wait, bit 1 a segment-counter update gave up, bit 2 a page-table entry
