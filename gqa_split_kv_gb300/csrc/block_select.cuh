@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const __gr
   const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
 
   pdl_wait_primary();
+  pdl_launch_dependents();
   const long long unit = blockIdx.x / p.cluster;
   const int tiles = (p.n + p.qt - 1) / p.qt;
   const int i0 = (int)(unit % tiles) * p.qt, h = (int)(unit / tiles % p.Hkv), b = (int)(unit / tiles / p.Hkv);

@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   __shared__ int s_warp[32], s_warp_eq[32], s_zero, s_digit, s_above;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait_primary();
+  pdl_launch_dependents();
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   const int L = seg_len(p.seq_lens, b, p.cap);
   int* kept = p.kept + (size_t)blockIdx.x * p.keep;

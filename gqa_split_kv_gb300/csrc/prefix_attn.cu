@@ -2,11 +2,13 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "../../include/decode_attn.h"
 #include "host_util.cuh"
+#include "prefix_tc.cuh"
 #include "seg_host.cuh"
 #include "seg_kernel.cuh"
 #include "units.cuh"
@@ -17,10 +19,15 @@ int take_prefix_error_word(unsigned int* flags) { return take_unit_error_word(fl
 
 namespace {
 
+template <int D>
+constexpr int tc_rows() { return PrefixTcGeo<D>::ROWS; }
+int tc_rows(int D) { return D == 64 ? tc_rows<64>() : D == 128 ? tc_rows<128>() : tc_rows<256>(); }
+
 // What a call of these sizes launches.
 struct PrefixShape {
-  int rt, rt_prefix, ctas;
-  long long slots, bytes;
+  int rt, rt_prefix, ctas;     // seg_kernel's
+  int splits, row_blocks;      // prefix_tc_kernel's: the most parts that a prefix's keys may have
+  long long slots, rows, tc_ml, bytes;  // tc_ml: bytes of the parts' (m, l)
 };
 
 int prefix_shape(int B, int n, int Hq, int Hkv, int D, int sms, PrefixShape* s) {
@@ -28,11 +35,17 @@ int prefix_shape(int B, int n, int Hq, int Hkv, int D, int sms, PrefixShape* s) 
   if (D != 64 && D != 128 && D != 256) return DA_ERR_UNSUPPORTED;
   const int G = Hq / Hkv;
   if (G > 64 || Hq > 65536 || product(B, n, Hq) > 0x7fffffffLL / 16) return DA_ERR_UNSUPPORTED;
+  s->rows = (long long)B * n * G;
   s->rt = (int)(((long long)n * G + 15) / 16);
-  s->rt_prefix = (int)(((long long)B * n * G + 15) / 16);
   s->ctas = seg_ctas(D, sms);
+  // up to 16 rows, the prefix goes through seg_kernel as one more unit a head
+  s->rt_prefix = s->rows <= 16 ? (s->rows > 0) : 0;
+  s->row_blocks = (int)((s->rows + tc_rows(D) - 1) / tc_rows(D));
+  const long long units = product(Hkv, s->row_blocks);
+  s->splits = s->rt_prefix || units == 0 ? 0 : units >= sms ? 1 : (int)(sms / units);
   s->slots = (long long)Hkv * s->rt_prefix + (long long)B * Hkv * s->rt + s->ctas;
-  s->bytes = seg_partial_bytes(s->slots, D);
+  s->tc_ml = (s->splits * product(Hkv, s->rows, 8) + 15) / 16 * 16;
+  s->bytes = seg_partial_bytes(s->slots, D) + s->tc_ml + s->splits * product(Hkv, s->rows, D * 4);
   return DA_OK;
 }
 
@@ -45,12 +58,77 @@ struct PrefixCall {
   long long cap;
 };
 
+// The prefix's part on the tensor cores.
 template <int D>
-int launch_prefix(const PrefixCall& c, const PrefixShape& s, cudaStream_t st) {
-  const long long rows = (long long)c.p.B * c.p.n * c.p.Hq;
-  if (int e = c.paged ? launch_seg<D, true, kSegRange>(c.p, st) : launch_seg<D, false, kSegRange>(c.p, st)) return e;
-  return launch_dependent(seg_merge_prefix_kernel<D>, (unsigned)((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)),
-                          kMergeThreads, 0, st, c.p);
+int launch_tc(const PrefixCall& c, const PrefixTcParams& base, cudaStream_t st) {
+  using Gm = PrefixTcGeo<D>;
+  if (int e = allow_smem<prefix_tc_kernel<D>>(Gm::SMEM)) return e;
+  if (Gm::NQT == 2) {
+    // the softmax warpgroups raise their registers out of what the launch gave the CTA; a build
+    // whose per-thread count is below the split would wait for ever, so it is refused
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, prefix_tc_kernel<D>) != cudaSuccess) {
+        cudaGetLastError();
+        return DA_ERR_CUDA;
+      }
+      regs.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) * Gm::NTHREADS < Gm::REG_POOL_NEEDED) return DA_ERR_UNSUPPORTED;
+  }
+  PrefixTcParams t = base;
+  const cuuint64_t row = (cuuint64_t)t.Hkv * D * 2;
+  const cuuint64_t rows = c.paged ? t.page_size : t.P, pages = c.paged ? t.num_pages : 1;
+  t.rk = 128;
+  if (c.paged)
+    while (t.page_size % t.rk) t.rk /= 2;
+  t.rv = t.rk < Gm::VKEYS ? t.rk : Gm::VKEYS;
+  const cuuint64_t dims[5] = {64, rows, D / 64, (cuuint64_t)t.Hkv, pages}, strides[4] = {row, 128, D * 2, row * rows};
+  const cuuint32_t box_k[5] = {64, (cuuint32_t)t.rk, 1, 1, 1}, box_v[5] = {64, (cuuint32_t)t.rv, 1, 1, 1};
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (int e = encode_map_t(&t.tm_k, bf16, sw, c.paged ? c.p.k : c.p.kp, 5, dims, strides, box_k)) return e;
+  if (int e = encode_map_t(&t.tm_v, bf16, sw, c.paged ? c.p.v : c.p.vp, 5, dims, strides, box_v)) return e;
+  const long long grid = product(t.row_blocks, t.splits, t.Hkv);
+  if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  return launch_dependent(prefix_tc_kernel<D>, (unsigned)grid, Gm::NTHREADS, Gm::SMEM, st, t);
+}
+
+template <int D>
+int launch_prefix(PrefixCall& c, const PrefixShape& s, cudaStream_t st) {
+  SegParams& p = c.p;
+  if (s.splits && p.base > 0) {
+    PrefixTcParams t = {};
+    t.q = p.q;
+    t.seq_lens = p.seq_lens;
+    t.prefix_table = c.paged ? p.prefix_table : nullptr;
+    t.o = const_cast<float*>(p.tc_o);
+    t.ml = const_cast<float2*>(p.tc_ml);
+    t.B = p.B;
+    t.n = p.n;
+    t.Hq = p.Hq;
+    t.Hkv = p.Hkv;
+    t.G = p.G;
+    t.P = p.base;
+    t.cap = p.cap;
+    t.page_size = p.page_size;
+    t.num_pages = p.num_pages;
+    t.row_blocks = s.row_blocks;
+    // as many parts as there is room for, of whole tiles and alike
+    const int tiles = (p.base + PrefixTcGeo<D>::BK - 1) / PrefixTcGeo<D>::BK;
+    const int each = (tiles + s.splits - 1) / s.splits;
+    t.splits = (tiles + each - 1) / each;
+    t.scale_log2 = p.scale_log2;
+    t.timeout_ns = kWaitTimeoutNs;
+    p.slabs = t.splits;
+    p.beside = 1;
+    if (int e = launch_tc<D>(c, t, st)) return e;
+  }
+  if (int e = c.paged ? launch_seg<D, true, kSegRange>(p, st) : launch_seg<D, false, kSegRange>(p, st)) return e;
+  return launch_dependent(seg_merge_prefix_kernel<D>,
+                          (unsigned)(((long long)p.B * p.n * p.Hq + kMergeThreads / 32 - 1) / (kMergeThreads / 32)),
+                          kMergeThreads, 0, st, p);
 }
 
 int prefix_call(PrefixCall& c, float scale, void* stream) {
@@ -92,6 +170,8 @@ int prefix_call(PrefixCall& c, float scale, void* stream) {
   p.rt_prefix = s.rt_prefix;
   p.ctas = s.ctas;
   seg_partials(p, c.workspace, s.slots, c.D);
+  p.tc_ml = p.part_ml + s.slots * 16;
+  p.tc_o = reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.tc_ml) + s.tc_ml);
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return c.D == 64 ? launch_prefix<64>(c, s, st) : c.D == 128 ? launch_prefix<128>(c, s, st) : launch_prefix<256>(c, s, st);

@@ -1,0 +1,463 @@
+// The shared prefix's part of prefix attention on the 5th-generation tensor cores: every
+// query row of the batch against the same keys and values, without a mask but for rows whose
+// sequence ends inside the prefix.
+//
+// The rows of a KV head are those of all B q_len tokens times its G query heads, so a batch
+// turns the prefix into two dense products,
+//   S = Q K^T,  O = 2^(S - m) V,
+// 4 D operations a (row, key) and D * 4 bytes a key once a block of rows: bound by the bytes
+// up to about 128 rows, then by the tensor cores and, beside them, one exponential a (row,
+// key).  The engine is that of latent_prefill.cuh: a CTA owns up to two tiles of 128 rows (one
+// at D = 256), whose rows are the lanes of tensor memory; each has a softmax warpgroup, one
+// thread a row; with two, the tensor cores run one tile's products while the other's softmax
+// works:
+//   P_A V_j, S_A = Q_A K_{j+1}^T, P_B V_j, S_B = Q_B K_{j+1}^T;
+// with one, S has two buffers and S_{j+1} is computed ahead of P_j V_j.  Tensor memory: two S
+// of 128 columns and the O (D columns each), 512 at D >= 128.  K and V come through one ring
+// of 16 KB granules (K: 128 keys x 64 elements; V: 16 KB / 2 D keys x D), each freed by its
+// last product.
+//
+// The key tiles are cut into `splits` parts so that parts x row blocks x heads fill the
+// card once; every part leaves (O, m, l) unnormalised in fp32 and seg_merge_prefix_kernel
+// joins them with the rests'.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "device_error.cuh"
+#include "ptx.cuh"
+#include "seg_kernel.cuh"
+#include "tc05.cuh"
+
+namespace da {
+
+struct PrefixTcParams {
+  CUtensorMap tm_k, tm_v;   // [pages][Hkv][D / 64][rows of a page][64]; boxes of rk, rv rows and 64 elements
+  const __nv_bfloat16* q;   // [B, n, Hq, D]
+  const int* seq_lens;      // or null: cap
+  const int* prefix_table;  // null: the prefix is one page
+  float* o;                 // [splits][Hkv][B n G][D]
+  float2* ml;               // [splits][Hkv][B n G]: m in log2 units, l
+  int B, n, Hq, Hkv, G;
+  int P, cap;
+  int page_size, num_pages;
+  int rk, rv;
+  int splits, row_blocks;
+  float scale_log2;
+  unsigned long long timeout_ns;
+};
+
+template <int D>
+struct PrefixTcGeo {
+  static constexpr int M = 128, BK = 128;
+  static constexpr int NQT = D <= 128 ? 2 : 1;  // query tiles a CTA
+  static constexpr int ROWS = NQT * M;
+  static constexpr int NSUB = D / 64;           // 64-element columns
+  static constexpr int GB = 16384;              // bytes a granule
+  static constexpr int VKEYS = GB / (2 * D);    // keys of a V granule
+  static constexpr int NKG = NSUB, NVG = BK / VKEYS, PER = NKG + NVG;
+  static constexpr int QT_BYTES = M * D * 2;
+  static constexpr int OFF_G = NQT * QT_BYTES;
+  static constexpr int NG_FIT = (227 * 1024 - 2048 - OFF_G) / GB;
+  static constexpr int NG = NG_FIT < 12 ? NG_FIT : 12;
+  static constexpr int OFF_BAR = OFF_G + NG * GB;
+  static constexpr int BAR_FULL = 0, BAR_EMPTY = NG, BAR_S = 2 * NG, BAR_P = BAR_S + 2, BAR_O = BAR_P + 2,
+                       BAR_FIN = BAR_O + 2, NBAR = BAR_FIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + (NBAR + 1) / 2 * 16;  // tensor memory base, abort flag
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr int TCOL_O = 2 * BK;  // S buffer i at i BK, O of tile t at TCOL_O + t D
+  static constexpr uint32_t TMEM_COLS = TCOL_O + NQT * D <= 256 ? 256u : 512u;
+  static constexpr int NTHREADS = 128 + 128 * NQT;
+  static constexpr int REG_LOW = 120, REG_HIGH = 192;  // after the split of the two-tile form
+  static constexpr int REG_POOL_NEEDED = 128 * REG_LOW + 128 * NQT * REG_HIGH;
+  static_assert(NG >= PER + (NQT == 1 ? 1 : NVG) && SMEM <= 227 * 1024, "the ring holds what the products hold at once");
+  static_assert(TCOL_O + NQT * D <= 512, "tensor memory");
+};
+
+template <int N>
+__device__ __forceinline__ void prefix_setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void prefix_setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D>
+__global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(const __grid_constant__ PrefixTcParams p) {
+  using Gm = PrefixTcGeo<D>;
+  constexpr int BK = Gm::BK, M = Gm::M, NQT = Gm::NQT;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  auto bar = [&](int i) -> uint32_t { return sbase + Gm::OFF_BAR + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Gm::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // work: the row blocks of a (head, part) side by side, as they read the same keys
+  const int rb = blockIdx.x % p.row_blocks, hs = blockIdx.x / p.row_blocks;
+  const int s = hs % p.splits, h = hs / p.splits;
+  const int T = (p.P + BK - 1) / BK;
+  const int j0 = (int)((long long)T * s / p.splits), ntiles = (int)((long long)T * (s + 1) / p.splits) - j0;
+  const int all_rows = p.B * p.n * p.G;
+  const int row0 = rb * Gm::ROWS, nrows = min(Gm::ROWS, all_rows - row0);
+  const int nqt = NQT == 2 && nrows > M ? 2 : 1;  // query tiles with rows
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Gm::NG; ++i) {
+      mbar_init(bar(Gm::BAR_FULL + i), 1);
+      mbar_init(bar(Gm::BAR_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Gm::BAR_S + i), 1);
+      mbar_init(bar(Gm::BAR_P + i), 4);  // one arrival a warp
+      mbar_init(bar(Gm::BAR_O + i), 1);
+    }
+    mbar_init(bar(Gm::BAR_FIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait_primary();
+  // the rests' kernel may start as soon as SMs are free: what it reads was written before this
+  // kernel's wait ended, and it waits for this kernel at its end
+  pdl_launch_dependents();
+  // query rows, [tile][D / 64][128][64] with the 128-byte swizzle, zeros past the last
+  for (int e = threadIdx.x; e < nqt * M * (D / 8); e += Gm::NTHREADS) {
+    const int rr = e / (D / 8), ch = e % (D / 8);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (rr < nrows) {
+      const int token = (row0 + rr) / p.G, g = row0 + rr - token * p.G;
+      v = load_dependent(reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + h * p.G + g) * D) + ch);
+    }
+    *reinterpret_cast<uint4*>(smem + (rr / M) * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(rr % M, ch % 8)) = v;
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MISC);
+  auto wait = [&](int i, int phase) { return wait_bounded(bar(i), (uint32_t)(phase & 1), abort_flag, p.timeout_ns); };
+  // granule g of this CTA's tile j: K columns 0 .. NKG - 1, then V
+  auto slot_of = [&](int j, int g) { return (j * Gm::PER + g) % Gm::NG; };
+  auto fill_of = [&](int j, int g) { return (j * Gm::PER + g) / Gm::NG; };
+  auto addr_of = [&](int j, int g) { return sbase + Gm::OFF_G + (uint32_t)(slot_of(j, g) * Gm::GB); };
+
+  if (warp < 4) {
+    if constexpr (NQT == 2) prefix_setmaxnreg_dec<Gm::REG_LOW>();
+    if (warp == 0) {
+      // ---- producer: granules in the order of the products; the lanes issue a granule's boxes
+      // side by side (a page of 16 tokens is 2 KB of each column).  Boxes wholly past the
+      // prefix are not loaded.
+      bool ok = true;
+      int last = -1;
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int t0 = (j0 + j) * BK;
+#pragma unroll 1
+        for (int g = 0; g < Gm::PER; ++g) {
+          const int fill = fill_of(j, g), slot = slot_of(j, g);
+          if (fill > 0 && !(ok = __all_sync(0xffffffffu, wait(Gm::BAR_EMPTY + slot, fill - 1)))) break;
+          const bool is_k = g < Gm::NKG;
+          const int rows = is_k ? p.rk : p.rv, keys = is_k ? BK : Gm::VKEYS;
+          const int t = is_k ? t0 : t0 + (g - Gm::NKG) * Gm::VKEYS;  // first key
+          const int live = min(keys, p.P - t), boxes = live > 0 ? (live + rows - 1) / rows : 0;  // a column
+          const int n = is_k ? boxes : boxes * Gm::NSUB;
+          const uint32_t full = bar(Gm::BAR_FULL + slot);
+          if (lane == 0) {
+            if (n > 0)
+              mbar_arrive_expect_tx(full, (uint32_t)(n * rows * 128));
+            else
+              mbar_arrive(full);
+          }
+          __syncwarp();
+          if (lane < n) {
+            const int sub = is_k ? g : lane / boxes, bx = is_k ? lane : lane - sub * boxes;
+            const int tok = t + bx * rows;
+            int page = 0, row = tok;
+            if (p.prefix_table) {
+              const int col = tok / p.page_size;
+              page = load_dependent(p.prefix_table + col);
+              if ((unsigned)page >= (unsigned)p.num_pages) {
+                atomicOr(&g_error_word, 4u);
+                page = 0;
+              }
+              row = tok - col * p.page_size;
+            }
+            const uint32_t dst = addr_of(j, g) + (uint32_t)((is_k ? 0 : sub * Gm::VKEYS * 128) + bx * rows * 128);
+            tma_load_5d(dst, is_k ? &p.tm_k : &p.tm_v, full, 0, row, sub, h, page);
+          }
+          last = j * Gm::PER + g;
+        }
+      }
+      if (*abort_flag && lane == 0) {  // copies in flight land before the CTA exits
+        const uint64_t at = globaltimer_ns();
+        for (int m = last; m >= 0 && m > last - Gm::NG; --m)
+          while (!mbar_try_wait(bar(Gm::BAR_FULL + m % Gm::NG), (uint32_t)((m / Gm::NG) & 1)) &&
+                 globaltimer_ns() - at < p.timeout_ns) {
+          }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- MMA issue (one lane); the warp zeroes V rows past the prefix
+      constexpr uint32_t id_s = tc_idesc_bf16(M, BK, false, false);
+      constexpr uint32_t id_o = tc_idesc_bf16(M, D, false, true);
+      auto wait_all = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)) != 0; };
+      auto landed = [&](int j, int g0, int g1) {
+        bool there = true;
+        for (int g = g0; g < g1; ++g) there = wait(Gm::BAR_FULL + slot_of(j, g), fill_of(j, g)) && there;
+        return __all_sync(0xffffffffu, there) != 0;
+      };
+      // one thread: S buffer sb = Q_t K_j^T; the granules are freed after the last query tile
+      auto issue_qk = [&](int t, int j, int sb) {
+#pragma unroll
+        for (int g = 0; g < Gm::NKG; ++g) {
+          const uint64_t da = tc_sdesc(sbase + t * Gm::QT_BYTES + g * (M * 128), 16, 1024, kTcSwizzle128B);
+          const uint64_t db = tc_sdesc(addr_of(j, g), 16, 1024, kTcSwizzle128B);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tc_mma_ss(tmem + sb * BK, da + 2 * i, db + 2 * i, id_s, g > 0 || i > 0);
+          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, g)));
+        }
+        tc_commit(bar(Gm::BAR_S + sb));
+      };
+      // one thread: O_t += P (S buffer sb) V_j
+      auto issue_pv = [&](int t, int j, int sb) {
+#pragma unroll
+        for (int g = 0; g < Gm::NVG; ++g) {
+          const uint64_t db = tc_sdesc(addr_of(j, Gm::NKG + g), Gm::VKEYS * 128, 1024, kTcSwizzle128B);
+#pragma unroll
+          for (int i = 0; i < Gm::VKEYS / 16; ++i)
+            tc_mma_ts(tmem + Gm::TCOL_O + t * D, tmem + sb * BK + 8 * (g * (Gm::VKEYS / 16) + i), db + i * 128, id_o,
+                      j > 0 || g > 0 || i > 0);
+          if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, Gm::NKG + g)));
+        }
+        // with two tiles O_t is waited for once, at the end; with one, every other P V completes the
+        // same barrier, so that a wait for either is never a phase behind
+        if (NQT == 1)
+          tc_commit(bar(Gm::BAR_O + (j & 1)));
+        else if (j + 1 == ntiles)
+          tc_commit(bar(Gm::BAR_O + t));
+      };
+      // V rows at or past the prefix may hold anything (0 * NaN would poison O): zero them
+      auto zero_tail = [&](int j) {
+        for (int g = 0; g < Gm::NVG; ++g) {
+          const int r0 = max(0, p.P - ((j0 + j) * BK + g * Gm::VKEYS));
+          uint8_t* vs = smem + Gm::OFF_G + slot_of(j, Gm::NKG + g) * Gm::GB;
+          for (int e = r0 * 8 + lane; e < Gm::VKEYS * 8; e += 32)
+            for (int c = 0; c < Gm::NSUB; ++c)
+              *reinterpret_cast<uint4*>(vs + c * (Gm::VKEYS * 128) + swz<128>(e / 8, e % 8)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      bool ok = ntiles > 0 && landed(0, 0, Gm::NKG);
+      const bool any = ok;
+      if (ok && elect_one()) {
+        tc_fence_after();
+        for (int t = 0; t < nqt; ++t) issue_qk(t, 0, t);
+      }
+      __syncwarp();
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const bool more = j + 1 < ntiles;
+        if constexpr (NQT == 2) {
+          if (!(ok = landed(j, Gm::NKG, Gm::PER))) break;
+          if ((j0 + j + 1) * BK > p.P) zero_tail(j);
+          if (!(ok = wait_all(Gm::BAR_P, j))) break;
+          if (elect_one()) {
+            tc_fence_after();
+            issue_pv(0, j, 0);
+          }
+          __syncwarp();
+          if (more) {
+            if (!(ok = landed(j + 1, 0, Gm::NKG))) break;
+            if (elect_one()) {
+              tc_fence_after();
+              issue_qk(0, j + 1, 0);
+            }
+            __syncwarp();
+          }
+          if (nqt == 2) {
+            if (!(ok = wait_all(Gm::BAR_P + 1, j))) break;
+            if (elect_one()) {
+              tc_fence_after();
+              issue_pv(1, j, 1);
+              if (more) issue_qk(1, j + 1, 1);
+            }
+            __syncwarp();
+          }
+        } else {
+          if (more) {
+            if (!(ok = landed(j + 1, 0, Gm::NKG))) break;
+            if (elect_one()) {
+              tc_fence_after();
+              issue_qk(0, j + 1, (j + 1) & 1);
+            }
+            __syncwarp();
+          }
+          if (!(ok = landed(j, Gm::NKG, Gm::PER))) break;
+          if ((j0 + j + 1) * BK > p.P) zero_tail(j);
+          if (!(ok = wait_all(Gm::BAR_P + (j & 1), j >> 1))) break;
+          if (elect_one()) {
+            tc_fence_after();
+            issue_pv(0, j, j & 1);
+          }
+          __syncwarp();
+        }
+      }
+      // before the tensor memory is freed, every MMA issued must have completed
+      if (any && elect_one()) {
+        tc_commit(bar(Gm::BAR_FIN));
+        const uint64_t at = globaltimer_ns();
+        while (!mbar_try_wait(bar(Gm::BAR_FIN), 0) && globaltimer_ns() - at < p.timeout_ns) {
+        }
+      }
+      __syncwarp();
+    }  // warps 2 and 3: idle
+  } else {
+    // ---- softmax of query tile qt and its partial: one thread per row (tensor memory lane)
+    if constexpr (NQT == 2) prefix_setmaxnreg_inc<Gm::REG_HIGH>();
+    const int qt = (warp >> 2) - 1;
+    const int row = qt * M + lane + 32 * (warp & 3);
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_addr = tmem + lane_addr + Gm::TCOL_O + qt * D;
+    const bool has_row = row < nrows;
+    int lim = p.P;  // keys this row sees
+    if (has_row) {
+      const int token = (row0 + row) / p.G, b = token / p.n;
+      lim = max(0, min(p.P, seg_len(p.seq_lens, b, p.cap) - p.n + 1 + (token - b * p.n)));
+    }
+    const int lim_first = __reduce_min_sync(0xffffffffu, lim);  // keys every row of the warp sees
+    const bool fold = p.scale_log2 > 0.f;  // a positive scale goes into the exponent's fma
+    const float sc = fold ? p.scale_log2 : 1.f;
+    float m = kNegInf, l = 0.f;
+    bool ok = qt < nqt;
+    for (int j = 0; j < ntiles && ok; ++j) {
+      const int sb = NQT == 2 ? qt : j & 1;
+      const uint32_t s_addr = tmem + lane_addr + sb * BK;
+      ok = __all_sync(0xffffffffu, wait(Gm::BAR_S + sb, NQT == 2 ? j : j >> 1));
+      if (!ok) break;
+      tc_fence_after();
+      float x[BK];
+      {
+        uint32_t r[BK];
+#pragma unroll
+        for (int c0 = 0; c0 < BK; c0 += 32) tmem_ld32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(r + c0));
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < BK; ++i) x[i] = __uint_as_float(r[i]);
+      }
+      if (!fold) {
+#pragma unroll
+        for (int i = 0; i < BK; ++i) x[i] *= p.scale_log2;
+      }
+      if ((j0 + j + 1) * BK > lim_first) {
+        const int left = lim - (j0 + j) * BK;
+#pragma unroll
+        for (int i = 0; i < BK; ++i) x[i] = i < left ? x[i] : kNegInf;
+      }
+      // P = exp2(x sc - mu) as bf16 pairs over the first half of the S buffer; the sum of the weights
+      auto weights = [&](float mu) {
+        float2 sk[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sk[k] = make_float2(0.f, 0.f);
+        const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
+#pragma unroll
+        for (int c0 = 0; c0 < BK / 2; c0 += 32) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 y = fma_f32x2(make_float2(x[2 * (c0 + i)], x[2 * (c0 + i) + 1]), sc2, mu2);
+            const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+            sk[i & 3] = add_f32x2(sk[i & 3], e);
+            pk[i] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st32(s_addr + c0, pk);
+        }
+        const float2 t = add_f32x2(add_f32x2(sk[0], sk[1]), add_f32x2(sk[2], sk[3]));
+        return t.x + t.y;
+      };
+      // The weights are first taken against the current m; only a row that has seen no key
+      // yet, or whose weights sum past 2^14, takes its maximum and raises m to it.  The stores
+      // in weights() are the whole warp's, so every call is warp-uniform.
+      const bool have = __any_sync(0xffffffffu, m != kNegInf);
+      float sum = 0.f;
+      if (have) sum = weights(m == kNegInf ? 0.f : m);
+      const bool need = m == kNegInf || !(sum <= 16384.f);
+      float mx = kNegInf;
+      if (need) {
+        float mk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mk[k] = x[k];
+#pragma unroll
+        for (int i = 8; i < BK; ++i) mk[i & 7] = fmaxf(mk[i & 7], x[i]);
+        mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
+        mx = fold ? mx * p.scale_log2 : mx;
+      }
+      const bool raise = need && mx > m;
+      const float m_new = raise ? mx : m;
+      const float alpha = raise && m != kNegInf ? exp2_approx(m - m_new) : raise ? 0.f : 1.f;
+      if (__any_sync(0xffffffffu, raise && m != kNegInf) && j > 0) {
+        // O holds the P V of the tiles before.  Two query tiles: S of tile j was issued after P V
+        // of tile j - 1, and its commit covers every MMA before it.  One: wait for that P V
+        if constexpr (NQT == 1) {
+          if (!(ok = __all_sync(0xffffffffu, wait(Gm::BAR_O + ((j - 1) & 1), (j - 1) >> 1)))) break;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c0, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st32(o_addr + c0, o);
+        }
+        tmem_st_wait();
+      }
+      m = m_new;
+      if (!have || __any_sync(0xffffffffu, raise)) sum = weights(m == kNegInf ? 0.f : m);
+      l = l * alpha + sum;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Gm::BAR_P + sb));
+    }
+    if (ok && ntiles > 0)
+      ok = __all_sync(0xffffffffu, NQT == 2 ? wait(Gm::BAR_O + qt, 0)
+                                            : wait(Gm::BAR_O + ((ntiles - 1) & 1), (ntiles - 1) >> 1));
+    if (qt < nqt) {
+      tc_fence_after();
+      const size_t at = ((size_t)s * p.Hkv + h) * all_rows + row0 + row;
+      if (has_row) p.ml[at] = make_float2(m, ok ? l : 0.f);
+#pragma unroll 1
+      for (int c0 = 0; c0 < D && ok && ntiles > 0; c0 += 32) {  // (l is 0 with no tile, and nothing else read)
+        uint32_t r[32];
+        tmem_ld32(o_addr + c0, r);
+        tmem_ld_wait();
+        if (has_row) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + c0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Gm::TMEM_COLS);
+  }
+}
+
+}  // namespace da

@@ -56,6 +56,7 @@ struct SegParams {
   int block, pick;
   int rt, rt_prefix;           // tiles of 16 query rows a sequence's KV head, and of the prefix's (0: none here)
   int ctas;                    // of seg_kernel: the plan's n
+  int beside;                  // the kernel before is the prefix's: seg_kernel runs beside it and waits for it at its end
   float scale_log2;
 };
 
@@ -271,10 +272,17 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
   const uint32_t ring_s = smem_u32(ring);
   volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * Gm::NSTAGE;
 
-  pdl_wait_primary();
+  // Beside the prefix's kernel there is nothing to wait for: it has written nothing that is read
+  // here, and lets this kernel start after its own wait for what came before.  The kernels after this
+  // one wait for this one alone, so it may not end before that one does.
+  if (!p.beside) pdl_wait_primary();
+  pdl_launch_dependents();
   const SegWalk<KIND> walk(p);
   long long x0, x1;
-  if (!walk.range(blockIdx.x, x0, x1)) return;
+  if (!walk.range(blockIdx.x, x0, x1)) {
+    if (p.beside) pdl_wait_primary();
+    return;
+  }
 
   // the load side: the unit and tile of the next copy, and where its rows lie (lanes 0 .. 15)
   int lj;
@@ -486,6 +494,7 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
     }
   }
   cp_async_wait<0>();
+  if (p.beside) pdl_wait_primary();
 }
 
 // One row's partials joined by a warp: pieces [0, count), piece(k) gives the index of its

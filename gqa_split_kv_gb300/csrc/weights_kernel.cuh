@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
   volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * Gm::NSTAGE;
 
   pdl_wait_primary();
+  pdl_launch_dependents();
   const SegWalk<kSegRange> walk(p);
   long long x0, x1;
   if (!walk.range(blockIdx.x, x0, x1)) return;
