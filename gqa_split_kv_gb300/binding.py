@@ -702,7 +702,7 @@ def block_select(q, means, seq_lens, block_size: int, n_select: int, *, first: i
                  stream=None):
     """The n_select blocks that each of the last q_len tokens attends to, for every KV head: the first `first` and
     the last `recent` of those up to its own, and of the others those with the largest max over the group's heads of
-    <q, mean> (as if computed exactly; ties: the lower block).  q bf16 [B, q_len, Hq, D], means as from block_means_*,
+    <q, mean> (compared to 2^-42 of |q| |mean|; ties: the lower block).  q bf16 [B, q_len, Hq, D], means as from block_means_*,
     seq_lens int32 [B] or None.  Returns out int32 [B, q_len, Hkv, n_select], ascending, -1 behind the last."""
     return (_ext_module or _ext()).block_select(q, means, seq_lens, block_size, n_select, first, recent, out, stream)
 

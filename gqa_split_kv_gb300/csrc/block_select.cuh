@@ -96,13 +96,14 @@ __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const __grid
 // and the last `recent` up to the token's own are taken, and of the others the best scores
 // until there are `pick` (ties: the lowest block).  Out: ascending, -1 behind.
 //
-// The selection is that of the exact scores.  The products run on the warp-level MMA in
+// The selection is that of the exact scores, as far as the last sentence says.  The products run on the warp-level MMA in
 // fp32 (a mean is read once for all 16 rows: heads, and neighbouring tokens where a group
 // has few), whose sums are off by mu = D / 16 * 17 * 2^-23 |q| |mean| at most: bf16 products are
 // exact, and each of the D / 16 MMAs adds 17 terms, each cut off at 2^-23 of the largest at
 // worst.  Where the last block taken and the next differ by more than 2 mu, no block can be on
 // the wrong side.  Otherwise those within 2 mu of the border (hardly ever more than two) are
-// computed again in 64 bits and taken in that order.
+// computed again, each sum with what its additions round off (to 2^-42 of |q| |mean|: the card
+// has few 64-bit units), and taken in that order.
 struct SelectParams {
   const __nv_bfloat16 *q, *means;
   const int* seq_lens;
@@ -115,6 +116,31 @@ struct SelectParams {
 constexpr int kSelectThreads = 256;
 constexpr int kSelectTokens = 16;     // a CTA, at most
 constexpr int kSelectBlocks = 8192;
+
+// The squares of 8 bf16 added up.
+__device__ __forceinline__ float square_sum(uint4 w, float s) {
+  const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(bf16lo_to_f32(e[i]), bf16lo_to_f32(e[i]), s);
+    s = fmaf(bf16hi_to_f32(e[i]), bf16hi_to_f32(e[i]), s);
+  }
+  return s;
+}
+
+// s += x, and into e what that rounded off: with t = s + x and v = t - s, exactly (s - (t - v)) + (x - v).
+__device__ __forceinline__ void add_exactly(float& s, float& e, float x) {
+  const float t = __fadd_rn(s, x), v = __fsub_rn(t, s);
+  e += __fadd_rn(__fsub_rn(s, __fsub_rn(t, v)), __fsub_rn(x, v));
+  s = t;
+}
+
+// float_key of a double: NaN lowest, -0 as 0.
+__device__ __forceinline__ unsigned long long double_key(double x) {
+  if (x != x) return 0ull;
+  const unsigned long long u = (unsigned long long)__double_as_longlong(x == 0.0 ? 0.0 : x);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
 
 // mu of a query whose largest square of a head's norm has these bits, among means likewise;
 // 2^-110 is for products below fp32's range.
@@ -146,36 +172,34 @@ __device__ __forceinline__ void max_at_leader(uint32_t a, uint32_t v) {
 // The 64-bit scores and numbers of the blocks at the border, the queries' keys and bits.
 __host__ __device__ inline size_t select_smem(int qt, int max_blocks) {
   const int words = (max_blocks + 31) / 32;
-  return (size_t)max_blocks * 8 + (size_t)qt * (max_blocks + words) * 4 + (size_t)max_blocks * 2 + 16;
+  return (size_t)max_blocks * 10 + (size_t)qt * (max_blocks + words + 256) * 4 + 16;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t s_mean2, s_q2[16], s_border[16];  // bits of the largest squares of norms, keys
-  __shared__ int s_open[16], s_count, s_sum[kSelectThreads / 32];
+  constexpr int WARPS = kSelectThreads / 32;
+  __shared__ uint32_t s_mean2, s_q2[kSelectTokens];  // bits of the largest squares of norms
+  __shared__ uint32_t s_prefix[kSelectTokens], s_low[kSelectTokens], s_below[kSelectTokens];
+  __shared__ int s_left[kSelectTokens], s_open[kSelectTokens], s_count, s_sure, s_busy;
   const int words = (p.max_blocks + 31) / 32;
-  double* exact = reinterpret_cast<double*>(smem);
+  unsigned long long* exact = reinterpret_cast<unsigned long long*>(smem);
   uint32_t* keys = reinterpret_cast<uint32_t*>(exact + p.max_blocks);
   uint32_t* bits = keys + (size_t)p.qt * p.max_blocks;
-  uint16_t* list = reinterpret_cast<uint16_t*>(bits + (size_t)p.qt * words);
+  int* hist = reinterpret_cast<int*>(bits + (size_t)p.qt * words);
+  uint16_t* list = reinterpret_cast<uint16_t*>(hist + p.qt * 256);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
 
-  pdl_wait_primary();
-  pdl_launch_dependents();
   const long long unit = blockIdx.x / p.cluster;
   const int tiles = (p.n + p.qt - 1) / p.qt;
   const int i0 = (int)(unit % tiles) * p.qt, h = (int)(unit / tiles % p.Hkv), b = (int)(unit / tiles / p.Hkv);
   const int qn = min(p.qt, p.n - i0);  // query tokens here
-  const int L = seg_len(p.seq_lens, b, p.cap);
-  const int last = L - p.n + i0 + qn - 1;  // position of the last
-  const int blocks = last < 0 ? 0 : min(last / p.block + 1, p.max_blocks);
+  const int rows = qn * p.G;
   const __nv_bfloat16* means = p.means + ((size_t)b * p.Hkv + h) * p.max_blocks * D;
-
   for (int e = threadIdx.x; e < qn * p.max_blocks; e += kSelectThreads) keys[e] = 0u;
   for (int e = threadIdx.x; e < qn * words; e += kSelectThreads) bits[e] = 0u;
-  if (threadIdx.x < 16) s_q2[threadIdx.x] = 0u;
+  if (threadIdx.x < kSelectTokens) s_q2[threadIdx.x] = 0u;
   if (threadIdx.x == 0) {
     s_mean2 = 0u;
     s_count = 0;
@@ -184,64 +208,68 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const __gr
     cluster_sync();
   else
     __syncthreads();
+  pdl_wait_primary();
+  pdl_launch_dependents();
 
   // scores: 16 query rows against 8 blocks a warp's step.  Element 32 c + 8 t + e of a row is
   // thread t's of the quad, so that rows of both are read 16 bytes at a time; the order of a
-  // product's terms is free
-  const int rows = qn * p.G;
+  // product's terms is free.  A step's means are loaded a step ahead, the first with the
+  // queries and the length (there are max_blocks rows, whatever the length)
+  const int step = p.cluster * WARPS, nt0 = rank * WARPS + warp;
+  auto load_means = [&](uint4 (&w)[D / 32], int nt, int limit) {
+    const int j = nt * 8 + lane / 4;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      w[c] = j < limit ? load_dependent(reinterpret_cast<const uint4*>(means + (size_t)j * D) + 4 * c + lane % 4)
+                       : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 w[D / 32];
+  load_means(w, nt0, p.max_blocks);
+  const int L = seg_len(p.seq_lens, b, p.cap);
+  const int last = L - p.n + i0 + qn - 1;  // position of the last
+  const int blocks = last < 0 ? 0 : min(last / p.block + 1, p.max_blocks);
   for (int r0 = 0; r0 < rows; r0 += 16) {
     uint4 a[D / 32][2];
+    int qi[2];  // the query token of this thread's two rows, -1: no row
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int row = r0 + lane / 4 + 8 * hf;
-      float q2 = 0.f;
+      qi[hf] = row < rows ? row / p.G : -1;
+      const size_t token = (size_t)b * p.n + i0 + qi[hf];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (token * p.Hq + h * p.G + row - qi[hf] * p.G) * D) + lane % 4;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        a[c][hf] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows) {
-          const size_t token = (size_t)b * p.n + i0 + row / p.G;
-          a[c][hf] = load_dependent(
-              reinterpret_cast<const uint4*>(p.q + (token * p.Hq + h * p.G + row % p.G) * D) + 4 * c + lane % 4);
-        }
-        const uint32_t w[4] = {a[c][hf].x, a[c][hf].y, a[c][hf].z, a[c][hf].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          q2 = fmaf(bf16lo_to_f32(w[e]), bf16lo_to_f32(w[e]), q2);
-          q2 = fmaf(bf16hi_to_f32(w[e]), bf16hi_to_f32(w[e]), q2);
-        }
-      }
-      q2 += __shfl_xor_sync(0xffffffffu, q2, 1);
-      q2 += __shfl_xor_sync(0xffffffffu, q2, 2);
-      if (warp == 0 && lane % 4 == 0 && row < rows) atomicMax(&s_q2[row / p.G], __float_as_uint(q2));
+      for (int c = 0; c < D / 32; ++c) a[c][hf] = qi[hf] >= 0 ? load_dependent(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
     }
-    float top2 = 0.f;
-    for (int nt = rank * (kSelectThreads / 32) + warp; nt * 8 < blocks; nt += p.cluster * (kSelectThreads / 32)) {
-      const int j = nt * 8 + lane / 4;
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, m2 = 0.f;
-      uint4 w[D / 32];
+    if (warp == 0) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        w[c] = j < blocks ? load_dependent(reinterpret_cast<const uint4*>(means + (size_t)j * D) + 4 * c + lane % 4)
-                          : make_uint4(0u, 0u, 0u, 0u);
+      for (int hf = 0; hf < 2; ++hf) {
+        float q2 = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) q2 = square_sum(a[c][hf], q2);
+        q2 += __shfl_xor_sync(0xffffffffu, q2, 1);
+        q2 += __shfl_xor_sync(0xffffffffu, q2, 2);
+        if (lane % 4 == 0 && qi[hf] >= 0) atomicMax(&s_q2[qi[hf]], __float_as_uint(q2));
+      }
+    }
+    if (r0 > 0) load_means(w, nt0, blocks);
+    float top2 = 0.f;
+    for (int nt = nt0; nt * 8 < blocks; nt += step) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, m2 = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         mma_bf16_16816(s, a[c][0].x, a[c][1].x, a[c][0].y, a[c][1].y, w[c].x, w[c].y);
         mma_bf16_16816(s, a[c][0].z, a[c][1].z, a[c][0].w, a[c][1].w, w[c].z, w[c].w);
-        const uint32_t e4[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          m2 = fmaf(bf16lo_to_f32(e4[e]), bf16lo_to_f32(e4[e]), m2);
-          m2 = fmaf(bf16hi_to_f32(e4[e]), bf16hi_to_f32(e4[e]), m2);
-        }
+        m2 = square_sum(w[c], m2);
       }
+      load_means(w, nt + step, blocks);
       m2 += __shfl_xor_sync(0xffffffffu, m2, 1);
       m2 += __shfl_xor_sync(0xffffffffu, m2, 2);
-      top2 = m2 != m2 ? -kNegInf : fmaxf(top2, m2);
+      if (nt * 8 + lane / 4 < blocks) top2 = m2 != m2 ? -kNegInf : fmaxf(top2, m2);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int row = r0 + lane / 4 + 8 * (e >> 1), col = nt * 8 + 2 * (lane % 4) + (e & 1);
-        if (row < rows && col < blocks)
-          max_at_leader(smem_u32(keys + (size_t)(row / p.G) * p.max_blocks + col), float_key(s[e]));
+        const int col = nt * 8 + 2 * (lane % 4) + (e & 1);
+        if (qi[e >> 1] >= 0 && col < blocks)
+          max_at_leader(smem_u32(keys + (size_t)qi[e >> 1] * p.max_blocks + col), float_key(s[e]));
       }
     }
     if (lane % 4 == 0 && top2 > 0.f) max_at_leader(smem_u32(&s_mean2), __float_as_uint(top2));
@@ -267,61 +295,103 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const __gr
   };
   auto take = [&](int qi, int j) { atomicOr(&bits[qi * words + (j >> 5)], 1u << (j & 31)); };
 
-  // the border of each query: the need-th largest key, by its bits from the top.  One query:
-  // the whole CTA counts; several: a warp each
-  const bool wide = qn == 1;
-  const int size = wide ? kSelectThreads : 32, me = wide ? (int)threadIdx.x : lane;
-  auto total = [&](int v) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    if (!wide) return v;
-    __syncthreads();
-    if (lane == 0) s_sum[warp] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int w = 0; w < kSelectThreads / 32; ++w) v += s_sum[w];
-    return v;
-  };
-  auto largest = [&](uint32_t v) {
-    v = __reduce_max_sync(0xffffffffu, v);
-    if (!wide) return v;
-    __syncthreads();
-    if (lane == 0) s_sum[warp] = (int)v;
-    __syncthreads();
-    v = 0u;
-#pragma unroll
-    for (int w = 0; w < kSelectThreads / 32; ++w) v = max(v, (uint32_t)s_sum[w]);
-    return v;
-  };
-  for (int qi = wide ? 0 : warp; qi < qn; qi += wide ? 1 : kSelectThreads / 32) {
-    const Want w = want(qi);
-    const uint32_t* key = keys + (size_t)qi * p.max_blocks;
-    for (int j = me; j < w.visible; j += size)
-      if (w.need < 0 || j < w.lo || j >= w.hi) take(qi, j);
-    if (w.need <= 0) continue;
-    uint32_t border = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t at = border | 1u << bit;
-      int count = 0;
-      for (int j = w.lo + me; j < w.hi; j += size) count += key[j] >= at;
-      if (total(count) >= w.need) border = at;
+  // The border of each query, 8 bits of the keys at a time from the top: how many keys have
+  // each value of the 8 bits (and the bits found so far), and in which value the need-th
+  // largest lies; done when all keys of that value are taken.  All queries go side by side, a
+  // group of `size` threads each.
+  const int size = kSelectThreads / (qn <= 1 ? 1 : qn <= 2 ? 2 : qn <= 4 ? 4 : qn <= 8 ? 8 : 16);
+  const int mine = threadIdx.x / size, me = threadIdx.x % size;
+  const Want my = mine < qn ? want(mine) : Want{0, 0, 0, 0};
+  const uint32_t* key = keys + (size_t)mine * p.max_blocks;
+  for (int j = me; j < my.visible; j += size)
+    if (my.need < 0 || j < my.lo || j >= my.hi) take(mine, j);
+  if (me == 0 && mine < qn) {
+    s_prefix[mine] = 0u;
+    s_left[mine] = my.need;
+    s_low[mine] = 0xffffffffu;
+    s_below[mine] = 0u;
+  }
+  for (int e = threadIdx.x; e < qn * 256; e += kSelectThreads) hist[e] = 0;
+  if (threadIdx.x == 0) s_busy = 0;
+  __syncthreads();
+  bool searching = my.need > 0;
+  int shift = 24;
+  for (; shift >= 0; shift -= 8) {
+    if (searching) {
+      const uint32_t prefix = s_prefix[mine];
+      for (int j = my.lo + me; j < my.hi; j += size)
+        if (shift == 24 || (key[j] ^ prefix) >> (shift + 8) == 0u) atomicAdd(&hist[mine * 256 + (key[j] >> shift & 255u)], 1);
     }
-    uint32_t below = 0u;
-    int same = 0;
-    for (int j = w.lo + me; j < w.hi; j += size) {
-      if (key[j] < border) below = max(below, key[j]);
-      same += key[j] >= border;
+    __syncthreads();
+    for (int qi = warp; qi < qn; qi += WARPS) {
+      const int left = s_left[qi];
+      if (left <= 0) continue;
+      // lane l has values 255 - 8 l .. 248 - 8 l
+      int c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = hist[qi * 256 + 255 - 8 * lane - i];
+        hist[qi * 256 + 255 - 8 * lane - i] = 0;
+        sum += c[i];
+      }
+      int at = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += up;
+      }
+      at -= sum;
+      if (at < left && at + sum >= left) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (at < left && at + c[i] >= left) {
+            s_prefix[qi] |= (uint32_t)(255 - 8 * lane - i) << shift;
+            // all keys of this value are taken (or it is one key): their lowest is the border
+            s_left[qi] = at + c[i] == left ? 0 : left - at;
+            if (at + c[i] != left) s_busy = 1;
+            break;
+          }
+          at += c[i];
+        }
+      }
+      __syncwarp();
     }
-    below = largest(below);
-    const bool split = total(same) > w.need;  // equal keys on both sides
-    const float mu = select_slack<D>(s_q2[qi], s_mean2);
-    const bool sure = !split && key_float(border) - key_float(below) > 2.f * mu;
-    if (sure) {
-      for (int j = w.lo + me; j < w.hi; j += size)
-        if (key[j] >= border) take(qi, j);
+    __syncthreads();
+    const bool busy = s_busy;
+    searching = searching && s_left[min(mine, qn - 1)] > 0;
+    __syncthreads();
+    if (threadIdx.x == 0) s_busy = 0;
+    if (!busy) break;
+  }
+  // the lowest key taken, and the largest below it; a query with something left has equal keys on both sides
+  if (my.need > 0) {
+    const uint32_t from = s_prefix[mine];  // bits not looked at are 0
+    uint32_t low = 0xffffffffu, below = 0u;
+    for (int j = my.lo + me; j < my.hi; j += size) {
+      const uint32_t k = key[j];
+      if (k >= from)
+        low = min(low, k);
+      else
+        below = max(below, k);
+    }
+    if (size >= 32) {  // a warp is of one group
+      low = __reduce_min_sync(0xffffffffu, low);
+      below = __reduce_max_sync(0xffffffffu, below);
+    }
+    if (size < 32 || lane == 0) {
+      atomicMin(&s_low[mine], low);
+      atomicMax(&s_below[mine], below);
+    }
+  }
+  __syncthreads();
+  if (my.need > 0) {
+    const float mu = select_slack<D>(s_q2[mine], s_mean2);
+    const uint32_t low = s_low[mine];
+    if (s_left[mine] <= 0 && key_float(low) - key_float(s_below[mine]) > 2.f * mu) {
+      for (int j = my.lo + me; j < my.hi; j += size)
+        if (key[j] >= low) take(mine, j);
     } else if (me == 0) {
-      s_border[qi] = border;
-      s_open[atomicAdd(&s_count, 1)] = qi;
+      s_open[atomicAdd(&s_count, 1)] = mine;
     }
   }
   __syncthreads();
@@ -332,46 +402,44 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const __gr
     const int qi = s_open[o];
     const Want w = want(qi);
     const uint32_t* key = keys + (size_t)qi * p.max_blocks;
-    const float border = key_float(s_border[qi]);
-    const float mu = select_slack<D>(s_q2[qi], s_mean2);
+    const float border = key_float(s_low[qi]), mu = select_slack<D>(s_q2[qi], s_mean2);
     __syncthreads();
-    if (threadIdx.x == 0) s_count = 0;
+    if (threadIdx.x == 0) s_count = s_sure = 0;
     __syncthreads();
-    int sure = 0;
     for (int j = w.lo + threadIdx.x; j < w.hi; j += kSelectThreads) {
       const float s = key_float(key[j]);
       if (s > border + 2.f * mu) {
         take(qi, j);
-        ++sure;
+        atomicAdd(&s_sure, 1);
       } else if (!(s < border - 2.f * mu)) {
-        list[atomicAdd(&s_count, 1)] = (uint16_t)j;
+        const int c = atomicAdd(&s_count, 1);
+        list[c] = (uint16_t)j;
+        exact[c] = 0ull;
       }
     }
-    sure = __reduce_add_sync(0xffffffffu, sure);
-    if (lane == 0) s_sum[warp] = sure;
     __syncthreads();
-    sure = 0;
-    for (int i = 0; i < kSelectThreads / 32; ++i) sure += s_sum[i];
-    const int count = s_count, left = w.need - sure;
+    // a warp a (candidate, head): the largest of the heads' scores, ordered by their bits
+    const int count = s_count, left = w.need - s_sure;
     const __nv_bfloat16* q = p.q + (((size_t)b * p.n + i0 + qi) * p.Hq + h * p.G) * D;
-    for (int c = warp; c < count; c += kSelectThreads / 32) {
+    for (int e = warp; e < count * p.G; e += WARPS) {
+      const int c = e / p.G, g = e - c * p.G;
       const __nv_bfloat16* mean = means + (size_t)list[c] * D;
-      double best = (double)kNegInf;
-      for (int g = 0; g < p.G; ++g) {
-        double s = 0.0;
+      float s = 0.f, e2 = 0.f;  // a sum and what its additions rounded off
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-          s = fma((double)__bfloat162float(load_dependent(q + g * D + d * 32 + lane)),
-                  (double)__bfloat162float(load_dependent(mean + d * 32 + lane)), s);
+      for (int d = 0; d < D / 32; ++d)
+        add_exactly(s, e2, __bfloat162float(load_dependent(q + g * D + d * 32 + lane)) *
+                               __bfloat162float(load_dependent(mean + d * 32 + lane)));
 #pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (s > best) best = s;
+      for (int d = 16; d; d >>= 1) {
+        const float os = __shfl_xor_sync(0xffffffffu, s, d), oe = __shfl_xor_sync(0xffffffffu, e2, d);
+        add_exactly(s, e2, os);
+        e2 += oe;
       }
-      if (lane == 0) exact[c] = best;
+      if (lane == 0) atomicMax(&exact[c], double_key((double)s + (double)(s - s == 0.f ? e2 : 0.f)));
     }
     __syncthreads();
     for (int c = threadIdx.x; c < count; c += kSelectThreads) {
-      const double s = exact[c];
+      const unsigned long long s = exact[c];
       const int j = list[c];
       int before = 0;
       for (int i = 0; i < count; ++i) before += exact[i] > s || (exact[i] == s && list[i] < j);

@@ -161,8 +161,19 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
       // prefix are not loaded.
       bool ok = true;
       int last = -1;
+      // lane l < 8: the page of the tile's keys from 16 l on, looked up a tile ahead
+      auto page_of = [&](int j) {
+        const int tok = (j0 + j) * BK + 16 * lane;
+        if (!p.prefix_table || lane >= BK / 16 || j >= ntiles || tok >= p.P) return 0;
+        const int page = load_dependent(p.prefix_table + tok / p.page_size);
+        if ((unsigned)page < (unsigned)p.num_pages) return page;
+        atomicOr(&g_error_word, 4u);
+        return 0;
+      };
+      int ahead = page_of(0);
       for (int j = 0; j < ntiles && ok; ++j) {
-        const int t0 = (j0 + j) * BK;
+        const int t0 = (j0 + j) * BK, pages = ahead;
+        ahead = page_of(j + 1);
 #pragma unroll 1
         for (int g = 0; g < Gm::PER; ++g) {
           const int fill = fill_of(j, g), slot = slot_of(j, g);
@@ -180,19 +191,11 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
               mbar_arrive(full);
           }
           __syncwarp();
+          const int sub = is_k ? g : lane / max(boxes, 1), bx = is_k ? lane : lane - sub * boxes;
+          const int tok = t + bx * rows;
+          const int page = __shfl_sync(0xffffffffu, pages, (tok - t0) / 16 & 31);
           if (lane < n) {
-            const int sub = is_k ? g : lane / boxes, bx = is_k ? lane : lane - sub * boxes;
-            const int tok = t + bx * rows;
-            int page = 0, row = tok;
-            if (p.prefix_table) {
-              const int col = tok / p.page_size;
-              page = load_dependent(p.prefix_table + col);
-              if ((unsigned)page >= (unsigned)p.num_pages) {
-                atomicOr(&g_error_word, 4u);
-                page = 0;
-              }
-              row = tok - col * p.page_size;
-            }
+            const int row = p.prefix_table ? tok % p.page_size : tok;
             const uint32_t dst = addr_of(j, g) + (uint32_t)((is_k ? 0 : sub * Gm::VKEYS * 128) + bx * rows * 128);
             tma_load_5d(dst, is_k ? &p.tm_k : &p.tm_v, full, 0, row, sub, h, page);
           }

@@ -235,7 +235,7 @@ extern "C" int block_select(const void* q, const void* means, const int* seq_len
   const long long units = product(batch, num_kv_heads, (q_len + p.qt - 1) / p.qt);
   // few queries over many blocks: the CTAs of a cluster share the scores, down to two steps a warp
   p.cluster = 1;
-  while (p.cluster < 8 && units * p.cluster * 2 <= 2LL * sms && max_blocks >= 2 * p.cluster * 2 * kSelectThreads / 32 * 8)
+  while (p.cluster < 8 && units * p.cluster * 2 <= 4LL * sms && max_blocks >= 2 * p.cluster * 2 * kSelectThreads / 32 * 8)
     p.cluster *= 2;
   if (units * p.cluster > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

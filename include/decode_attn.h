@@ -605,7 +605,7 @@ int block_means_paged(const void* k_pool, const int* page_table, const int* seq_
  * block_select — the blocks that each of the last q_len tokens attends to, for every KV head.  Token i of
  * sequence b, at position p = L_b - q_len + i, sees blocks 0 .. p / block_size.  It takes the first `first` and
  * the last `recent` (>= 1) of them, and of the others those with the largest max over the group's heads of
- * <q, mean>, until it has n_select (>= first + recent) or all.  Scores are compared as if computed exactly (ties:
+ * <q, mean>, until it has n_select (>= first + recent) or all.  Scores are compared to 2^-42 of |q| |mean| (ties:
  * the lower block; a head whose score is NaN counts as lowest).
  *  q        bf16 [batch, q_len, num_q_heads, head_dim], head_dim 64, 128 or 256
  *  means    as block_means writes them, max_blocks <= 8192; seq_lens is clamped to max_blocks * block_size (NULL:
