@@ -154,14 +154,6 @@ __device__ __forceinline__ float key_float(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // atomicMax at shared-memory address a of the cluster's CTA 0.
 __device__ __forceinline__ void max_at_leader(uint32_t a, uint32_t v) {
   asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\tred.shared::cluster.max.u32 [r], %1;\n\t}" ::"r"(a),

@@ -80,12 +80,14 @@ int launch_tc(const PrefixCall& c, const PrefixTcParams& base, cudaStream_t st) 
   PrefixTcParams t = base;
   const cuuint64_t row = (cuuint64_t)t.Hkv * D * 2;
   const cuuint64_t rows = c.paged ? t.page_size : t.P, pages = c.paged ? t.num_pages : 1;
-  t.rk = 128;
+  int rk = Gm::BK;
   if (c.paged)
-    while (t.page_size % t.rk) t.rk /= 2;
-  t.rv = t.rk < Gm::VKEYS ? t.rk : Gm::VKEYS;
+    while (t.page_size % rk) rk /= 2;
+  const int rv = rk < Gm::VKEYS ? rk : Gm::VKEYS;
+  for (t.rk_log2 = 0; 1 << t.rk_log2 < rk;) ++t.rk_log2;
+  for (t.rv_log2 = 0; 1 << t.rv_log2 < rv;) ++t.rv_log2;
   const cuuint64_t dims[5] = {64, rows, D / 64, (cuuint64_t)t.Hkv, pages}, strides[4] = {row, 128, D * 2, row * rows};
-  const cuuint32_t box_k[5] = {64, (cuuint32_t)t.rk, 1, 1, 1}, box_v[5] = {64, (cuuint32_t)t.rv, 1, 1, 1};
+  const cuuint32_t box_k[5] = {64, (cuuint32_t)rk, 1, 1, 1}, box_v[5] = {64, (cuuint32_t)rv, 1, 1, 1};
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (int e = encode_map_t(&t.tm_k, bf16, sw, c.paged ? c.p.k : c.p.kp, 5, dims, strides, box_k)) return e;

@@ -13,9 +13,12 @@
 // works:
 //   P_A V_j, S_A = Q_A K_{j+1}^T, P_B V_j, S_B = Q_B K_{j+1}^T;
 // with one, S has two buffers and S_{j+1} is computed ahead of P_j V_j.  Tensor memory: two S
-// of 128 columns and the O (D columns each), 512 at D >= 128.  K and V come through one ring
-// of 16 KB granules (K: 128 keys x 64 elements; V: 16 KB / 2 D keys x D), each freed by its
-// last product.
+// of 128 columns (64 at D = 256) and the O (D columns each).  K and V come through one ring
+// of 16 KB granules, each freed by its last product.  A tile is 128 keys, 64 at D = 256: a ring of
+// 160 KB holds one and a quarter of 128 keys there, and K_{j+1} next to V_j leaves hardly any of it
+// to loads in flight (4.7 us a tile of 128 keys).  Multicast of the keys to clusters of the row
+// blocks that share them did not help (2.0 -> 2.3 us a tile, D = 128): their loads are not
+// bound by L2's rate.
 //
 // The key tiles are cut into `splits` parts so that parts x row blocks x heads fill the
 // card once; every part leaves (O, m, l) unnormalised in fp32 and seg_merge_prefix_kernel
@@ -35,7 +38,7 @@
 namespace da {
 
 struct PrefixTcParams {
-  CUtensorMap tm_k, tm_v;   // [pages][Hkv][D / 64][rows of a page][64]; boxes of rk, rv rows and 64 elements
+  CUtensorMap tm_k, tm_v;   // [pages][Hkv][D / 64][rows of a page][64]; boxes of 2^rk_log2, 2^rv_log2 rows and 64 elements
   const __nv_bfloat16* q;   // [B, n, Hq, D]
   const int* seq_lens;      // or null: cap
   const int* prefix_table;  // null: the prefix is one page
@@ -44,7 +47,7 @@ struct PrefixTcParams {
   int B, n, Hq, Hkv, G;
   int P, cap;
   int page_size, num_pages;
-  int rk, rv;
+  int rk_log2, rv_log2;
   int splits, row_blocks;
   float scale_log2;
   unsigned long long timeout_ns;
@@ -52,13 +55,14 @@ struct PrefixTcParams {
 
 template <int D>
 struct PrefixTcGeo {
-  static constexpr int M = 128, BK = 128;
+  static constexpr int M = 128, BK = D == 256 ? 64 : 128;
   static constexpr int NQT = D <= 128 ? 2 : 1;  // query tiles a CTA
   static constexpr int ROWS = NQT * M;
   static constexpr int NSUB = D / 64;           // 64-element columns
   static constexpr int GB = 16384;              // bytes a granule
+  static constexpr int KSUB = GB / (BK * 128);  // 64-element columns of a K granule
   static constexpr int VKEYS = GB / (2 * D);    // keys of a V granule
-  static constexpr int NKG = NSUB, NVG = BK / VKEYS, PER = NKG + NVG;
+  static constexpr int NKG = NSUB / KSUB, NVG = BK / VKEYS, PER = NKG + NVG;
   static constexpr int QT_BYTES = M * D * 2;
   static constexpr int OFF_G = NQT * QT_BYTES;
   static constexpr int NG_FIT = (227 * 1024 - 2048 - OFF_G) / GB;
@@ -132,17 +136,6 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
   // the rests' kernel may start as soon as SMs are free: what it reads was written before this
   // kernel's wait ended, and it waits for this kernel at its end
   pdl_launch_dependents();
-  // query rows, [tile][D / 64][128][64] with the 128-byte swizzle, zeros past the last
-  for (int e = threadIdx.x; e < nqt * M * (D / 8); e += Gm::NTHREADS) {
-    const int rr = e / (D / 8), ch = e % (D / 8);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (rr < nrows) {
-      const int token = (row0 + rr) / p.G, g = row0 + rr - token * p.G;
-      v = load_dependent(reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + h * p.G + g) * D) + ch);
-    }
-    *reinterpret_cast<uint4*>(smem + (rr / M) * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(rr % M, ch % 8)) = v;
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -153,52 +146,91 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
   auto fill_of = [&](int j, int g) { return (j * Gm::PER + g) / Gm::NG; };
   auto addr_of = [&](int j, int g) { return sbase + Gm::OFF_G + (uint32_t)(slot_of(j, g) * Gm::GB); };
 
+  // query rows, [tile][D / 64][128][64] with the 128-byte swizzle, zeros past the last; by the warps
+  // that need them, while the first keys load, several loads of a thread in flight
+  auto stage_queries = [&](int me) {
+    constexpr int CH = D / 8, U = 8, N = 32 + 128 * NQT;
+    for (int e0 = me; e0 < nqt * M * CH; e0 += U * N) {
+      uint4 v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int rr = (e0 + i * N) / CH, ch = (e0 + i * N) % CH;
+        const int token = (row0 + rr) / p.G, g = row0 + rr - token * p.G;
+        v[i] = rr < nrows
+                   ? load_dependent(reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + h * p.G + g) * D) + ch)
+                   : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int rr = (e0 + i * N) / CH, ch = (e0 + i * N) % CH;
+        if (rr < nqt * M)
+          *reinterpret_cast<uint4*>(smem + (rr / M) * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(rr % M, ch % 8)) = v[i];
+      }
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(1, N);
+  };
+
   if (warp < 4) {
     if constexpr (NQT == 2) prefix_setmaxnreg_dec<Gm::REG_LOW>();
-    if (warp == 0) {
-      // ---- producer: granules in the order of the products; the lanes issue a granule's boxes
-      // side by side (a page of 16 tokens is 2 KB of each column).  Boxes wholly past the
-      // prefix are not loaded.
+    if (warp != 1) {
+      // ---- producers: granules in the order of the products, a granule's boxes dealt to the lanes
+      // of three warps (a page of 16 tokens is 2 KB of each column, and a warp issues its boxes one
+      // after another: 3.4 us a tile of 32 with one warp, 2.6 with three, D = 128).  Boxes wholly
+      // past the prefix are not loaded.  No warp falls a round of the ring behind: a granule is not
+      // full, and so not freed, without every warp's boxes.
+      const int pid = warp == 0 ? 0 : warp - 1;
       bool ok = true;
       int last = -1;
-      // lane l < 8: the page of the tile's keys from 16 l on, looked up a tile ahead
+      // lane l < BK / 16: the page of the tile's keys from 16 l on and their row in it, looked up a
+      // tile ahead
+      int row_ahead = 0;
       auto page_of = [&](int j) {
         const int tok = (j0 + j) * BK + 16 * lane;
+        row_ahead = tok;
         if (!p.prefix_table || lane >= BK / 16 || j >= ntiles || tok >= p.P) return 0;
-        const int page = load_dependent(p.prefix_table + tok / p.page_size);
+        const int col = tok / p.page_size;
+        row_ahead = tok - col * p.page_size;
+        const int page = load_dependent(p.prefix_table + col);
         if ((unsigned)page < (unsigned)p.num_pages) return page;
         atomicOr(&g_error_word, 4u);
         return 0;
       };
       int ahead = page_of(0);
       for (int j = 0; j < ntiles && ok; ++j) {
-        const int t0 = (j0 + j) * BK, pages = ahead;
+        const int t0 = (j0 + j) * BK, pages = ahead, page_rows = row_ahead;
         ahead = page_of(j + 1);
+        const bool whole = t0 + BK <= p.P;
 #pragma unroll 1
         for (int g = 0; g < Gm::PER; ++g) {
           const int fill = fill_of(j, g), slot = slot_of(j, g);
-          if (fill > 0 && !(ok = __all_sync(0xffffffffu, wait(Gm::BAR_EMPTY + slot, fill - 1)))) break;
           const bool is_k = g < Gm::NKG;
-          const int rows = is_k ? p.rk : p.rv, keys = is_k ? BK : Gm::VKEYS;
-          const int t = is_k ? t0 : t0 + (g - Gm::NKG) * Gm::VKEYS;  // first key
-          const int live = min(keys, p.P - t), boxes = live > 0 ? (live + rows - 1) / rows : 0;  // a column
-          const int n = is_k ? boxes : boxes * Gm::NSUB;
+          const int shift = is_k ? p.rk_log2 : p.rv_log2, keys = is_k ? BK : Gm::VKEYS;
+          const int first = is_k ? 0 : (g - Gm::NKG) * Gm::VKEYS;  // key of the tile
+          const int live = whole ? keys : max(0, min(keys, p.P - t0 - first));
+          const int boxes = (live + (1 << shift) - 1) >> shift;  // a column
+          const int box = 3 * lane + pid;
+          int sub = 0, bx = box;  // the column of the granule, and the box of it
+#pragma unroll
+          for (int c = 1; c < Gm::NSUB; ++c)
+            if (bx >= boxes && sub + 1 < (is_k ? Gm::KSUB : Gm::NSUB)) {
+              bx -= boxes;
+              ++sub;
+            }
+          const int at = (first >> 4) + (bx << shift >> 4);
+          const int page = __shfl_sync(0xffffffffu, pages, at & 31), row = __shfl_sync(0xffffffffu, page_rows, at & 31);
+          const int n = boxes * (is_k ? Gm::KSUB : Gm::NSUB);
+          if (fill > 0 && !(ok = __all_sync(0xffffffffu, wait(Gm::BAR_EMPTY + slot, fill - 1)))) break;
           const uint32_t full = bar(Gm::BAR_FULL + slot);
-          if (lane == 0) {
+          if (pid == 0 && lane == 0) {
             if (n > 0)
-              mbar_arrive_expect_tx(full, (uint32_t)(n * rows * 128));
+              mbar_arrive_expect_tx(full, (uint32_t)(n << shift) * 128u);
             else
               mbar_arrive(full);
           }
-          __syncwarp();
-          const int sub = is_k ? g : lane / max(boxes, 1), bx = is_k ? lane : lane - sub * boxes;
-          const int tok = t + bx * rows;
-          const int page = __shfl_sync(0xffffffffu, pages, (tok - t0) / 16 & 31);
-          if (lane < n) {
-            const int row = p.prefix_table ? tok % p.page_size : tok;
-            const uint32_t dst = addr_of(j, g) + (uint32_t)((is_k ? 0 : sub * Gm::VKEYS * 128) + bx * rows * 128);
-            tma_load_5d(dst, is_k ? &p.tm_k : &p.tm_v, full, 0, row, sub, h, page);
-          }
+          if (bx < boxes)
+            tma_load_5d(addr_of(j, g) + (uint32_t)(sub * keys * 128 + (bx << shift) * 128), is_k ? &p.tm_k : &p.tm_v, full, 0,
+                        row, is_k ? g * Gm::KSUB + sub : sub, h, page);
           last = j * Gm::PER + g;
         }
       }
@@ -210,8 +242,9 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
           }
       }
       __syncwarp();
-    } else if (warp == 1) {
+    } else {
       // ---- MMA issue (one lane); the warp zeroes V rows past the prefix
+      stage_queries(threadIdx.x - 32);
       constexpr uint32_t id_s = tc_idesc_bf16(M, BK, false, false);
       constexpr uint32_t id_o = tc_idesc_bf16(M, D, false, true);
       auto wait_all = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)) != 0; };
@@ -224,10 +257,12 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
       auto issue_qk = [&](int t, int j, int sb) {
 #pragma unroll
         for (int g = 0; g < Gm::NKG; ++g) {
-          const uint64_t da = tc_sdesc(sbase + t * Gm::QT_BYTES + g * (M * 128), 16, 1024, kTcSwizzle128B);
+          const uint64_t da = tc_sdesc(sbase + t * Gm::QT_BYTES + g * Gm::KSUB * (M * 128), 16, 1024, kTcSwizzle128B);
           const uint64_t db = tc_sdesc(addr_of(j, g), 16, 1024, kTcSwizzle128B);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tc_mma_ss(tmem + sb * BK, da + 2 * i, db + 2 * i, id_s, g > 0 || i > 0);
+          for (int i = 0; i < 4 * Gm::KSUB; ++i)
+            tc_mma_ss(tmem + sb * BK, da + (i / 4) * (M * 128 / 16) + 2 * (i % 4), db + (i / 4) * (BK * 128 / 16) + 2 * (i % 4),
+                      id_s, g > 0 || i > 0);
           if (t == nqt - 1) tc_commit(bar(Gm::BAR_EMPTY + slot_of(j, g)));
         }
         tc_commit(bar(Gm::BAR_S + sb));
@@ -325,10 +360,11 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
         }
       }
       __syncwarp();
-    }  // warps 2 and 3: idle
+    }
   } else {
     // ---- softmax of query tile qt and its partial: one thread per row (tensor memory lane)
     if constexpr (NQT == 2) prefix_setmaxnreg_inc<Gm::REG_HIGH>();
+    stage_queries(threadIdx.x - 96);
     const int qt = (warp >> 2) - 1;
     const int row = qt * M + lane + 32 * (warp & 3);
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;

@@ -43,6 +43,30 @@ int allow_smem(size_t bytes) {
   return DA_OK;
 }
 
+// launch_dependent in clusters of this many CTAs.
+template <typename P>
+int launch_clusters(void (*kern)(P), unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t st,
+                    const P& prm) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, prm) != cudaSuccess) {
+    cudaGetLastError();
+    return DA_ERR_CUDA;
+  }
+  return DA_OK;
+}
+
 template <int D, bool PAGED, int KIND>
 int launch_seg(const SegParams& p, cudaStream_t st) {
   using Gm = SegGeo<D>;

@@ -32,6 +32,8 @@ __device__ __forceinline__ uint32_t float_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr int kSegLens = 1024;  // lengths that a CTA copies to its shared memory
+
 enum SegKind { kSegRange = 0, kSegBlocks = 1 };
 
 struct SegParams {
@@ -60,6 +62,12 @@ struct SegParams {
   float scale_log2;
 };
 
+// A row where a unit's warps are joined: their factors, and its place in the output (-1: no row).
+struct FoldRow {
+  float f[4];
+  long long out;
+};
+
 template <int D>
 struct SegGeo {
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
@@ -68,11 +76,21 @@ struct SegGeo {
   static constexpr int NSTAGE = D == 64 ? 6 : 3;
   static constexpr int WARP_BYTES = NSTAGE * STAGE;
   static constexpr int OFF_ML = WARPS * WARP_BYTES;
-  static constexpr int OFF_MASK = OFF_ML + WARPS * 16 * 8;
-  static constexpr int SMEM = OFF_MASK + WARPS * NSTAGE * 4;
+  static constexpr int OFF_FOLD = OFF_ML + WARPS * 16 * 8;
+  static constexpr int OFF_MASK = OFF_FOLD + 16 * (int)sizeof(FoldRow);
+  static constexpr int OFF_LENS = OFF_MASK + WARPS * NSTAGE * 4;
+  static constexpr int SMEM = OFF_LENS + kSegLens * 4;
   static constexpr int PER_SM = D == 256 ? 1 : 2;
 };
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
@@ -85,6 +103,15 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ int seg_len(const int* lens, int b, int cap) {
   const int L = lens ? load_dependent(lens + b) : cap;
   return L < 0 ? 0 : L < cap ? L : cap;
+}
+
+// The lengths where a CTA reads them often: in its shared memory, if they fit.  The CTA executes it.
+template <int THREADS>
+__device__ __forceinline__ const int* seg_stage_lens(const SegParams& p, int* to) {
+  if (!p.seq_lens || p.B > kSegLens) return p.seq_lens;
+  for (int b = threadIdx.x; b < p.B; b += THREADS) to[b] = load_dependent(p.seq_lens + b);
+  __syncthreads();
+  return to;
 }
 
 // A unit: 16 query rows (from row 16 r of its rows) of KV head h, and its tokens.
@@ -100,17 +127,18 @@ struct SegUnit {
 template <int KIND>
 struct SegWalk {
   const SegParams& p;
+  const int* lens;  // seq_lens, or the CTA's copy
   long long all;  // tiles of the line
   int tp;         // tiles of a prefix unit
   int used;       // CTAs that have some
 
-  __device__ __forceinline__ explicit SegWalk(const SegParams& p_) : p(p_), all(0), tp(0), used(0) {
+  __device__ __forceinline__ SegWalk(const SegParams& p_, const int* lens_) : p(p_), lens(lens_), all(0), tp(0), used(0) {
     if constexpr (KIND == kSegBlocks) {
       tp = (p.pick * p.block + kTile - 1) / kTile;
       all = (long long)p.B * p.n * p.Hkv * p.rt * tp;
     } else {
       tp = p.rt_prefix ? (p.base + kTile - 1) / kTile : 0;
-      all = seg_sums(p.seq_lens, p.B, p.cap, p.base, 0).all * p.Hkv * p.rt + prefix_tiles();
+      all = seg_sums(lens, p.B, p.cap, p.base, 0).all * p.Hkv * p.rt + prefix_tiles();
     }
     used = seg_used(all, p.ctas);
   }
@@ -135,7 +163,7 @@ struct SegWalk {
     u.b = id / p.n;
     u.prefix = 0;
     u.tiles = tp;
-    u.len = seg_len(p.seq_lens, u.b, p.cap);
+    u.len = seg_len(lens, u.b, p.cap);
     u.end = max(0, u.len - p.n + 1 + u.i);
     return u;
   }
@@ -156,7 +184,7 @@ struct SegWalk {
     u.h = h;
     u.r = r;
     u.prefix = 0;
-    u.len = u.end = seg_len(p.seq_lens, b, p.cap);
+    u.len = u.end = seg_len(lens, b, p.cap);
     u.tiles = seg_tiles(u.end, p.cap, p.base);
     u.id = p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r;
     return u;
@@ -164,21 +192,23 @@ struct SegWalk {
   // The unit of tile x (x < all), j: the tile's place in it.  The warp executes it.
   __device__ __forceinline__ SegUnit at(long long x, int& j) const {
     if constexpr (KIND == kSegBlocks) {
-      j = (int)(x % tp);
-      return blocks_unit((int)(x / tp));
+      const int id = (int)seg_div(x, tp);
+      j = (int)(x - (long long)id * tp);
+      return blocks_unit(id);
     } else {
       const long long wp = prefix_tiles();
       if (x < wp) {
-        j = (int)(x % tp);
-        return prefix_unit((int)(x / tp));
+        const int id = (int)seg_div(x, tp);
+        j = (int)(x - (long long)id * tp);
+        return prefix_unit(id);
       }
       x -= wp;
       const int hr = p.Hkv * p.rt;
-      const SegAt f = seg_find(p.seq_lens, p.B, p.cap, p.base, x / hr);
-      const int tb = seg_tiles(seg_len(p.seq_lens, f.b, p.cap), p.cap, p.base);
+      const SegAt f = seg_find(lens, p.B, p.cap, p.base, seg_div(x, hr));
+      const int tb = seg_tiles(seg_len(lens, f.b, p.cap), p.cap, p.base);
       const long long in = x - f.start * hr;
-      const int w = (int)(in / tb);
-      j = (int)(in % tb);
+      const int w = (int)seg_div(in, tb);
+      j = (int)(in - (long long)w * tb);
       return range_unit(f.b, w / p.rt, w % p.rt);
     }
   }
@@ -242,7 +272,8 @@ __device__ __forceinline__ long long seg_row(const SegParams& p, const SegUnit& 
 // Row rr of a unit: its query token (over the batch), head in the group, and how many tokens
 // it sees; false past the unit's rows.
 template <int KIND>
-__device__ __forceinline__ bool seg_query(const SegParams& p, const SegUnit& u, int rr, int& token, int& g, int& lim) {
+__device__ __forceinline__ bool seg_query(const SegParams& p, const int* lens, const SegUnit& u, int rr, int& token, int& g,
+                                          int& lim) {
   const int row = u.r * 16 + rr;
   if constexpr (KIND == kSegBlocks) {
     token = u.b * p.n + u.i;
@@ -258,7 +289,7 @@ __device__ __forceinline__ bool seg_query(const SegParams& p, const SegUnit& u, 
       return false;
     }
     const int b = u.prefix ? i / p.n : u.b;
-    lim = (u.prefix ? seg_len(p.seq_lens, b, p.cap) : u.len) - p.n + 1 + (u.prefix ? i - b * p.n : i);
+    lim = (u.prefix ? seg_len(lens, b, p.cap) : u.len) - p.n + 1 + (u.prefix ? i - b * p.n : i);
     return true;
   }
 }
@@ -277,18 +308,33 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
   // one wait for this one alone, so it may not end before that one does.
   if (!p.beside) pdl_wait_primary();
   pdl_launch_dependents();
-  const SegWalk<KIND> walk(p);
+  const SegWalk<KIND> walk(p, seg_stage_lens<Gm::THREADS>(p, reinterpret_cast<int*>(smem + Gm::OFF_LENS)));
   long long x0, x1;
   if (!walk.range(blockIdx.x, x0, x1)) {
     if (p.beside) pdl_wait_primary();
     return;
   }
 
-  // the load side: the unit and tile of the next copy, and where its rows lie (lanes 0 .. 15)
+  // the load side: where the rows of the next copy lie (lanes 0 .. 15), and of the one after it;
+  // lu and lj are the unit and tile of the latter
   int lj;
   SegUnit lu = walk.at(x0, lj);
-  long long lx = x0;
-  long long off = lane < 16 ? seg_row<D, PAGED, KIND>(p, lu, lj * kTile + warp * 16 + lane) : -1;
+  const SegUnit u0 = lu;
+  const int start = lj;
+  long long lx = x0;  // the next copy's tile
+  auto look_up = [&]() {
+    return lane < 16 ? seg_row<D, PAGED, KIND>(p, lu, lj * kTile + warp * 16 + lane) : -1ll;
+  };
+  auto advance = [&](long long x) {  // to tile x, the one after lu's and lj's; none past the last
+    if (x >= x1) return;
+    if (++lj == lu.tiles) {
+      lu = walk.next(lu);
+      lj = 0;
+    }
+  };
+  long long off = look_up(), off_next = -1;
+  advance(x0 + 1);
+  if (x0 + 1 < x1) off_next = look_up();
   auto issue = [&](int stage) {
     if (lx < x1) {
       const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
@@ -296,7 +342,7 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
       if (live) {
         const uint32_t dst = ring_s + stage * Gm::STAGE;
         const __nv_bfloat16 *kb = p.k, *vb = p.v;
-        if (!PAGED && KIND == kSegRange && lu.prefix) {
+        if (!PAGED && KIND == kSegRange && lx < walk.prefix_tiles()) {
           kb = p.kp;
           vb = p.vp;
         }
@@ -313,19 +359,15 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
         }
       }
       ++lx;
-      if (lx < x1) {
-        if (++lj == lu.tiles) {
-          lu = walk.next(lu);
-          lj = 0;
-        }
-        off = lane < 16 ? seg_row<D, PAGED, KIND>(p, lu, lj * kTile + warp * 16 + lane) : -1;
-      }
+      off = off_next;
+      advance(lx + 1);
+      if (lx + 1 < x1) off_next = look_up();
     }
     cp_async_commit();
   };
 
-  int j;
-  SegUnit u = walk.at(x0, j);
+  int j = start;
+  SegUnit u = u0;
 #pragma unroll 1
   for (int s = 0; s < Gm::NSTAGE; ++s) issue(s);
 
@@ -343,7 +385,7 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         int token, g;
-        const bool is = seg_query<KIND>(p, u, lane / 4 + 8 * hf, token, g, lim[hf]);
+        const bool is = seg_query<KIND>(p, walk.lens, u, lane / 4 + 8 * hf, token, g, lim[hf]);
         const uint32_t* src =
             reinterpret_cast<const uint32_t*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D) + lane % 4;
 #pragma unroll
@@ -448,39 +490,57 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
       __syncthreads();
       const bool whole = KIND == kSegBlocks && last && j0 == 0;
       const size_t slot = KIND == kSegBlocks ? 2 * (size_t)blockIdx.x + (j0 == 0) : (size_t)u.id + blockIdx.x;
-      for (int e = threadIdx.x; e < 16 * (D / 4); e += Gm::THREADS) {
-        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+      // each row's factors of the warps' O, and where it goes
+      FoldRow* fold = reinterpret_cast<FoldRow*>(smem + Gm::OFF_FOLD);
+      if (threadIdx.x < 16) {
+        const int r = threadIdx.x;
         int token, g, unused;
-        if (!seg_query<KIND>(p, u, r, token, g, unused)) break;
-        float mw[Gm::WARPS], M = kNegInf, L = 0.f;
+        float mw[Gm::WARPS], lw[Gm::WARPS], M = kNegInf, L = 0.f;
 #pragma unroll
         for (int w = 0; w < Gm::WARPS; ++w) {
-          mw[w] = ml[w * 16 + r].x;
-          M = fmaxf(M, mw[w]);
+          const float2 y = ml[w * 16 + r];
+          mw[w] = y.x;
+          lw[w] = y.y;
+          M = fmaxf(M, y.x);
         }
+        FoldRow f;
+#pragma unroll
+        for (int w = 0; w < Gm::WARPS; ++w) {
+          // l = 0: saw nothing (scores of NaN alone leave m at -inf and l at NaN)
+          f.f[w] = lw[w] == 0.f ? 0.f : mw[w] == kNegInf ? 1.f : exp2_approx(mw[w] - M);
+          L += f.f[w] * lw[w];
+        }
+        f.out = seg_query<KIND>(p, walk.lens, u, r, token, g, unused) ? ((long long)token * p.Hq + u.h * p.G + g) * D : -1;
+        if (whole) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that saw nothing is zeros
+#pragma unroll
+          for (int w = 0; w < Gm::WARPS; ++w) f.f[w] *= inv;
+        } else if (f.out >= 0) {
+          p.part_ml[slot * 16 + r] = make_float2(M, L);
+        }
+        fold[r] = f;
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int e = threadIdx.x; e < 16 * (D / 4); e += Gm::THREADS) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        const FoldRow f = fold[r];
+        if (f.out < 0) break;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < Gm::WARPS; ++w) {
-          const float lw = ml[w * 16 + r].y;
-          if (lw == 0.f) continue;  // saw nothing (scores of NaN alone leave m at -inf and l at NaN)
-          const float f = mw[w] == kNegInf ? 1.f : exp2_approx(mw[w] - M);
-          L += f * lw;
           const float4 y = *reinterpret_cast<const float4*>(
               reinterpret_cast<const float*>(smem + w * Gm::WARP_BYTES + stage * Gm::STAGE) + r * D + (c ^ ((r & 3) << 3)));
-          a.x += f * y.x;
-          a.y += f * y.y;
-          a.z += f * y.z;
-          a.w += f * y.w;
+          if (f.f[w] == 0.f) continue;
+          a.x += f.f[w] * y.x;
+          a.y += f.f[w] * y.y;
+          a.z += f.f[w] * y.z;
+          a.w += f.f[w] * y.w;
         }
-        if (whole) {
-          const bool none = L == 0.f;  // a row that saw nothing is zeros
-          const float f = 1.f / L;
-          *reinterpret_cast<uint2*>(p.out + ((size_t)token * p.Hq + u.h * p.G + g) * D + c) =
-              none ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
-        } else {
+        if (whole)
+          *reinterpret_cast<uint2*>(p.out + f.out + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        else
           *reinterpret_cast<float4*>(p.part_o + (slot * 16 + r) * D + c) = a;
-          if (c == 0) p.part_ml[slot * 16 + r] = make_float2(M, L);
-        }
       }
       __syncthreads();
     }
@@ -497,7 +557,7 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
   if (p.beside) pdl_wait_primary();
 }
 
-// One row's partials joined by a warp: pieces [0, count), piece(k) gives the index of its
+// One row's partials joined by a warp: pieces [0, count), at(k, ml, o) gives the places of its
 // (m, l) and O.  Each lane ends with columns 4 lane + 128 k .. + 3 of O / l (D = 64: 2 lane, + 1).
 template <int D>
 struct SegRow {
@@ -509,46 +569,66 @@ struct SegRow {
     for (int i = 0; i < N; ++i) a[i] = 0.f;
   }
   template <typename F>
-  __device__ __forceinline__ void add(const float2* ml, const float* o, int count, F piece) {
+  __device__ __forceinline__ void add(int count, F at) {
     const int lane = threadIdx.x & 31;
-      for (int k0 = 0; k0 < count; k0 += 32) {
-      const int k = k0 + lane;
-      const float2 mine = k < count ? __ldcg(ml + piece(k)) : make_float2(kNegInf, 0.f);
-      float M = mine.x;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-      M = fmaxf(M, m);
-      const float mu = M == kNegInf ? 0.f : M;
-      const bool empty = mine.y == 0.f;
-      const float old = m == kNegInf ? 1.f : exp2_approx(m - mu);  // nothing yet, or NaN
-      const float w = empty ? 0.f : mine.x == kNegInf ? 1.f : exp2_approx(mine.x - mu);
-      m = M;
-      float s = empty ? 0.f : w * mine.y;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      l = l * old + s;
-#pragma unroll
-      for (int i = 0; i < N; ++i) a[i] *= old;
+    for (int k0 = 0; k0 < count; k0 += 32) {
+      const float2* ml = nullptr;
+      const float* o = nullptr;
+      if (k0 + lane < count) at(k0 + lane, ml, o);
+      const float2 mine = ml ? __ldcg(ml) : make_float2(kNegInf, 0.f);
       const int here = min(32, count - k0);
-      const unsigned some = __ballot_sync(0xffffffffu, !empty);
-#pragma unroll 4
-      for (int i = 0; i < here; ++i) {
-        const float f = __shfl_sync(0xffffffffu, w, i);
-        if (!((some >> i) & 1)) continue;
-        const float* src = o + (size_t)piece(k0 + i) * D;
-        if constexpr (D == 64) {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-          a[0] += f * y.x;
-          a[1] += f * y.y;
-        } else {
+      const unsigned long long from = reinterpret_cast<unsigned long long>(o);
+      // the loads do not wait for the weights: U pieces at a time
+      constexpr int U = 8;
+      float w = 0.f, old = 1.f;
+      for (int i0 = 0; i0 < here; i0 += U) {
+        float y[U][N];
 #pragma unroll
-          for (int c = 0; c < D / 128; ++c) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane + 32 * c);
-            a[4 * c] += f * y.x;
-            a[4 * c + 1] += f * y.y;
-            a[4 * c + 2] += f * y.z;
-            a[4 * c + 3] += f * y.w;
+        for (int i = 0; i < U; ++i) {
+          const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, from, i0 + i & 31));
+#pragma unroll
+          for (int c = 0; c < N; ++c) y[i][c] = 0.f;
+          if (i0 + i < here) {
+            if constexpr (D == 64) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+              y[i][0] = v.x;
+              y[i][1] = v.y;
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 128; ++c) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + lane + 32 * c);
+                y[i][4 * c] = v.x;
+                y[i][4 * c + 1] = v.y;
+                y[i][4 * c + 2] = v.z;
+                y[i][4 * c + 3] = v.w;
+              }
+            }
           }
+        }
+        if (i0 == 0) {
+          float M = mine.x;
+#pragma unroll
+          for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+          M = fmaxf(M, m);
+          const float mu = M == kNegInf ? 0.f : M;
+          const bool empty = mine.y == 0.f;
+          old = m == kNegInf ? 1.f : exp2_approx(m - mu);  // nothing yet, or NaN
+          w = empty ? 0.f : mine.x == kNegInf ? 1.f : exp2_approx(mine.x - mu);
+          m = M;
+          float s = empty ? 0.f : w * mine.y;
+#pragma unroll
+          for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+          l = l * old + s;
+#pragma unroll
+          for (int i = 0; i < N; ++i) a[i] *= old;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float f = __shfl_sync(0xffffffffu, w, i0 + i & 31);
+          const bool none = __shfl_sync(0xffffffffu, mine.y, i0 + i & 31) == 0.f;  // its O may be anything
+          if (none || i0 + i >= here) continue;
+#pragma unroll
+          for (int c = 0; c < N; ++c) a[c] += f * y[i][c];
         }
       }
     }
@@ -583,26 +663,31 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const _
   const long long tp = p.rt_prefix ? (p.base + kTile - 1) / kTile : 0, wp = (long long)p.Hkv * p.rt_prefix * tp;
   const long long W = wp + sums.all * p.Hkv * p.rt;
   const int used = seg_used(W, p.ctas);
+  // the prefix's pieces: parts of prefix_tc_kernel, or of the unit of seg_kernel with its row
+  const int head = token * p.G + g;  // among the rows of the head
+  int na = p.slabs, id0 = 0, c0 = 0;
+  if (!p.slabs && p.rt_prefix && tp > 0) {
+    id0 = h * p.rt_prefix + head / 16;
+    c0 = seg_owner(W, used, id0 * tp);
+    na = seg_owner(W, used, (id0 + 1) * tp - 1) - c0 + 1;
+  }
+  // the rest's
+  const int rr = i * p.G + g, r = rr / 16, t = seg_tiles(seg_len(p.seq_lens, b, p.cap), p.cap, p.base);
+  const long long a1 = wp + sums.before * p.Hkv * p.rt + (long long)(h * p.rt + r) * t;
+  const int id1 = p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r;
+  const int c1 = t ? seg_owner(W, used, a1) : 0, nb = t ? seg_owner(W, used, a1 + t - 1) - c1 + 1 : 0;
   SegRow<D> acc;
-  // pieces of the unit with tiles [a, a + t), for the row r of its 16
-  auto add_unit = [&](long long a, int t, int id, int r) {
-    if (t <= 0) return;
-    const int c0 = seg_owner(W, used, a), c1 = seg_owner(W, used, a + t - 1);
-    acc.add(p.part_ml, p.part_o, c1 - c0 + 1, [&](int k) { return ((long long)id + c0 + k) * 16 + r; });
-  };
-  if (p.slabs) {
-    const long long rows = (long long)p.B * p.n * p.G, mine = (long long)token * p.G + g;
-    acc.add(p.tc_ml, p.tc_o, p.slabs, [&](int k) { return ((long long)k * p.Hkv + h) * rows + mine; });
-  } else if (p.rt_prefix) {
-    const int rr = token * p.G + g, id = h * p.rt_prefix + rr / 16;
-    add_unit(id * tp, (int)tp, id, rr % 16);
-  }
-  {
-    const int rr = i * p.G + g, r = rr / 16;
-    const int t = seg_tiles(seg_len(p.seq_lens, b, p.cap), p.cap, p.base);
-    add_unit(wp + sums.before * p.Hkv * p.rt + (long long)(h * p.rt + r) * t, t,
-             p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r, rr % 16);
-  }
+  acc.add(na + nb, [&](int k, const float2*& ml, const float*& o) {
+    if (k < na && p.slabs) {
+      const long long at = ((long long)k * p.Hkv + h) * ((long long)p.B * p.n * p.G) + head;
+      ml = p.tc_ml + at;
+      o = p.tc_o + at * D;
+    } else {
+      const long long at = k < na ? ((long long)id0 + c0 + k) * 16 + head % 16 : ((long long)id1 + c1 + k - na) * 16 + rr % 16;
+      ml = p.part_ml + at;
+      o = p.part_o + at * D;
+    }
+  });
   acc.store(p.out + row * D);
 }
 
@@ -612,14 +697,18 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) seg_merge_blocks_kernel(const __grid_constant__ SegParams p) {
   pdl_wait_primary();
   const long long tp = (p.pick * p.block + kTile - 1) / kTile, W = (long long)p.B * p.n * p.Hkv * p.rt * tp;
-  const long long x = seg_start(W, p.ctas, blockIdx.x + 1), id = x / tp;
+  const long long x = seg_start(W, p.ctas, blockIdx.x + 1), id = seg_div(x, tp);
   if (x >= W || x == id * tp || seg_start(W, p.ctas, blockIdx.x) > id * tp) return;
   const int c0 = blockIdx.x, c1 = seg_owner(W, p.ctas, (id + 1) * tp - 1);
   const int r0 = (int)(id % p.rt) * 16, h = (int)(id / p.rt % p.Hkv);
   const long long token = id / p.rt / p.Hkv;
   for (int r = threadIdx.x >> 5; r < 16 && r0 + r < p.G; r += kMergeThreads / 32) {
     SegRow<D> acc;
-    acc.add(p.part_ml, p.part_o, c1 - c0 + 1, [&](int k) { return (2ll * (c0 + k) + (k == 0)) * 16 + r; });
+    acc.add(c1 - c0 + 1, [&](int k, const float2*& ml, const float*& o) {
+      const long long at = (2ll * (c0 + k) + (k == 0)) * 16 + r;
+      ml = p.part_ml + at;
+      o = p.part_o + at * D;
+    });
     acc.store(p.out + (token * p.Hq + h * p.G + r0 + r) * D);
   }
 }

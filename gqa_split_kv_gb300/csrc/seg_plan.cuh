@@ -13,19 +13,24 @@ namespace da {
 
 constexpr int kTile = 64;  // tokens
 
+// a / b of numbers that are not negative; most fit 32 bits, whose division is several times as fast.
+__host__ __device__ __forceinline__ long long seg_div(long long a, long long b) {
+  if (((unsigned long long)a | (unsigned long long)b) >> 32 == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
 // CTAs of a grid that have tiles.
 __host__ __device__ __forceinline__ int seg_used(long long W, int ctas) { return W < ctas ? (int)W : ctas; }
 // First tile of CTA c.
-__host__ __device__ __forceinline__ long long seg_start(long long W, int n, int c) { return W * c / n; }
+__host__ __device__ __forceinline__ long long seg_start(long long W, int n, int c) { return seg_div(W * c, n); }
 // The CTA that has tile x: the largest c with floor(c W / n) <= x.
 __host__ __device__ __forceinline__ int seg_owner(long long W, int n, long long x) {
-  return (int)(((x + 1) * n - 1) / W);
+  return (int)seg_div((x + 1) * n - 1, W);
 }
 
 // Tiles of the tokens [base, min(len, cap)).
 __host__ __device__ __forceinline__ int seg_tiles(int len, int cap, int base) {
   const int end = len < cap ? len : cap;
-  return end > base ? (int)(((long long)end - base + kTile - 1) / kTile) : 0;
+  return end > base ? (int)((unsigned)(end - base + kTile - 1) / kTile) : 0;
 }
 
 // Sums over the whole batch and over the sequences before b of their tiles; the warp

@@ -69,24 +69,7 @@ template <int D>
 int launch_select(const SelectParams& p, long long units, cudaStream_t st) {
   const size_t smem = select_smem(p.qt, p.max_blocks);
   if (int e = allow_smem<block_select_kernel<D>>(200 * 1024)) return e;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * p.cluster));
-  cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, block_select_kernel<D>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return DA_ERR_CUDA;
-  }
-  return DA_OK;
+  return launch_clusters(block_select_kernel<D>, (unsigned)(units * p.cluster), kSelectThreads, smem, p.cluster, st, p);
 }
 
 // Heads that a call of this family takes.

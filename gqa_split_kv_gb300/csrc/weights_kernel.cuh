@@ -34,7 +34,8 @@ struct ScoreGeo {
   static constexpr int WARP_BYTES = NSTAGE * STAGE;
   static constexpr int OFF_ML = WARPS * WARP_BYTES;
   static constexpr int OFF_MASK = OFF_ML + WARPS * 16 * 8;
-  static constexpr int SMEM = OFF_MASK + WARPS * NSTAGE * 4;
+  static constexpr int OFF_LENS = OFF_MASK + WARPS * NSTAGE * 4;
+  static constexpr int SMEM = OFF_LENS + kSegLens * 4;
   static constexpr int PER_SM = 2;
 };
 
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
 
   pdl_wait_primary();
   pdl_launch_dependents();
-  const SegWalk<kSegRange> walk(p);
+  const SegWalk<kSegRange> walk(p, seg_stage_lens<Gm::THREADS>(p, reinterpret_cast<int*>(smem + Gm::OFF_LENS)));
   long long x0, x1;
   if (!walk.range(blockIdx.x, x0, x1)) return;
 
@@ -134,8 +135,8 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
     cp_async_commit();
   };
 
-  int j;
-  SegUnit u = walk.at(x0, j);
+  int j = lj;
+  SegUnit u = lu;
 #pragma unroll 1
   for (int s = 0; s < Gm::NSTAGE; ++s) issue(s);
 
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         int token, g;
-        has[hf] = seg_query<kSegRange>(p, u, lane / 4 + 8 * hf, token, g, lim[hf]);
+        has[hf] = seg_query<kSegRange>(p, walk.lens, u, lane / 4 + 8 * hf, token, g, lim[hf]);
         const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D);
         // bf16: element 16 kk + 2 t (and + 8) is thread t's of the quad; int8: 64 c + 16 t + 4 s (and
         // + 2) for kk = 4 c + s, so that a thread's 16 bytes of a key hold its elements of 4 steps
