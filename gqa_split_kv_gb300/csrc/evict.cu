@@ -30,39 +30,60 @@ struct WeightsCall {
   long long workspace_bytes;
 };
 
+constexpr int kWindowRows = 128, kWeightRows = 1024;
+
 struct WeightsShape {
-  int rt, rows;
-  long long slots, tiles, bytes;
+  int rows;                       // of a KV head
+  long long slots, score, bytes;  // score: bytes of the scores
 };
 int weights_shape(int B, int n, int Hq, int Hkv, long long cap, int sms, WeightsShape* s) {
   if (B < 0 || n < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || cap < 0) return DA_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
-  if (G > 64 || Hq > 65536 || cap > 0x7fffffffLL - kTile || product(n, G) > kFinishRows ||
-      product(B, Hkv, (product(n, G) + 15) / 16) > 0x7fffffffLL)
+  if (G > 64 || Hq > 65536 || cap > 0x7fffffffLL - kTile || product(n, G) > kWeightRows || product(B, Hkv) > 0x3fffffffLL)
     return DA_ERR_UNSUPPORTED;
-  const int R = n * G;
-  s->rt = (R + 15) / 16;
-  s->rows = R < 16 ? R : 16;
-  s->slots = (long long)B * Hkv * s->rt + 2ll * sms;
-  s->tiles = product(B, Hkv, s->rt, (cap + kTile - 1) / kTile);
-  if (s->tiles > 1LL << 40) return DA_ERR_UNSUPPORTED;
-  s->bytes = s->slots * 16 * 8 + s->tiles * s->rows * kTile * 4;
+  s->rows = n * G;
+  s->slots = (long long)B * Hkv + 3ll * sms;
+  const long long tiles = product(B, Hkv, (cap + kTile - 1) / kTile);
+  if (tiles > 1LL << 40) return DA_ERR_UNSUPPORTED;
+  s->score = s->rows <= 16 ? tiles * s->rows * kTile * 4 : 0;
+  s->bytes = s->slots * (s->rows <= 16 ? 16 : kWindowRows) * 8 + s->score;
   return DA_OK;
 }
 
 template <int D, bool PAGED, bool INT8>
-int launch_scores(const WeightsParams& w, cudaStream_t st) {
-  using Gm = ScoreGeo<D, INT8>;
-  if (int e = allow_smem<weights_score_kernel<D, PAGED, INT8>>(Gm::SMEM)) return e;
-  return launch_dependent(weights_score_kernel<D, PAGED, INT8>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w);
+int launch_scores(WeightsParams w, int sms, cudaStream_t st) {
+  if (w.rows <= 16) {
+    using Gm = ScoreGeo<D, INT8, false>;
+    w.s.ctas = Gm::PER_SM * sms;
+    w.finish_ctas = 8 * sms;
+    if (int e = allow_smem<weights_score_kernel<D, PAGED, INT8>>(Gm::SMEM)) return e;
+    if (int e = launch_dependent(weights_score_kernel<D, PAGED, INT8>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
+      return e;
+    return launch_dependent(weights_finish_kernel<PAGED>, (unsigned)w.finish_ctas, kFinishThreads, 0, st, w);
+  }
+  using Gm = ScoreGeo<D, INT8, true>;
+  static_assert(Gm::ROWS == kWindowRows, "");
+  w.s.ctas = Gm::PER_SM * sms;
+  if (int e = allow_smem<weights_window_kernel<D, PAGED, INT8, false>>(Gm::SMEM)) return e;
+  if (int e = allow_smem<weights_window_kernel<D, PAGED, INT8, true>>(Gm::SMEM)) return e;
+  const int all = w.rows;
+  for (w.row0 = 0; w.row0 < all; w.row0 += kWindowRows) {
+    w.rows = all - w.row0 < kWindowRows ? all - w.row0 : kWindowRows;
+    if (w.row0 > 0) {  // added to what the windows before have written
+      w.prior = w.out;
+      w.decay = 1.f;
+    }
+    if (int e = launch_dependent(weights_window_kernel<D, PAGED, INT8, false>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
+      return e;
+    if (int e = launch_dependent(weights_window_kernel<D, PAGED, INT8, true>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
+      return e;
+  }
+  return DA_OK;
 }
 template <int D>
-int launch_weights(const WeightsCall& c, cudaStream_t st) {
-  if (int e = c.paged ? (c.int8 ? launch_scores<D, true, true>(c.w, st) : launch_scores<D, true, false>(c.w, st))
-                      : (c.int8 ? launch_scores<D, false, true>(c.w, st) : launch_scores<D, false, false>(c.w, st)))
-    return e;
-  return c.paged ? launch_dependent(weights_finish_kernel<true>, (unsigned)c.w.finish_ctas, kFinishThreads, 0, st, c.w)
-                 : launch_dependent(weights_finish_kernel<false>, (unsigned)c.w.finish_ctas, kFinishThreads, 0, st, c.w);
+int launch_weights(const WeightsCall& c, int sms, cudaStream_t st) {
+  return c.paged ? (c.int8 ? launch_scores<D, true, true>(c.w, sms, st) : launch_scores<D, true, false>(c.w, sms, st))
+                 : (c.int8 ? launch_scores<D, false, true>(c.w, sms, st) : launch_scores<D, false, false>(c.w, sms, st));
 }
 
 int weights_call(WeightsCall& c, float scale, void* stream) {
@@ -92,15 +113,15 @@ int weights_call(WeightsCall& c, float scale, void* stream) {
   if (!c.workspace || !aligned(c.workspace, 16) || c.workspace_bytes < s.bytes) return DA_ERR_WORKSPACE;
   for (const void* x : {(const void*)p.k, (const void*)p.q, (const void*)w.out, (const void*)w.prior, (const void*)w.k_scale})
     if (overlap(c.workspace, s.bytes, x, x == p.k ? kn : x == p.q ? qn : on)) return DA_ERR_INVALID_ARG;
-  p.rt = s.rt;
-  p.ctas = 2 * sms;
+  p.rt = 1;
   w.rows = s.rows;
-  w.finish_ctas = 4 * sms;
   p.part_ml = static_cast<float2*>(c.workspace);
   w.scores = reinterpret_cast<float*>(p.part_ml + s.slots * 16);
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return c.D == 64 ? launch_weights<64>(c, st) : c.D == 128 ? launch_weights<128>(c, st) : launch_weights<256>(c, st);
+  return c.D == 64    ? launch_weights<64>(c, sms, st)
+         : c.D == 128 ? launch_weights<128>(c, sms, st)
+                      : launch_weights<256>(c, sms, st);
 }
 
 WeightsCall weights_params(const void* q, const void* k, const float* k_scale, const int* page_table,
@@ -144,6 +165,8 @@ int weights_paged(WeightsCall c, bool int8, int page_size, int max_pages, int nu
 }
 
 // ---------------------------------------------------------------- eviction
+
+constexpr int kEvictKeys = 48 * 1024;  // 192 KB
 
 int evict_call(EvictParams& p, bool paged, bool int8, int head_dim, long long cap, void* stream) {
   if (p.B < 0 || p.Hkv <= 0 || head_dim <= 0 || cap < 0 || p.keep <= 0 || p.first < 0 || p.recent < 0 ||
@@ -211,8 +234,16 @@ int evict_call(EvictParams& p, bool paged, bool int8, int head_dim, long long ca
   const long long grid = (long long)units * (tensors * p.columns * p.parts + 1);
   if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (int e = paged ? launch_dependent(evict_select_kernel<true>, (unsigned)units, kEvictThreads, 0, st, p)
-                    : launch_dependent(evict_select_kernel<false>, (unsigned)units, kEvictThreads, 0, st, p))
+  // a cluster where there are SMs for it and 1024 weights a CTA
+  p.cluster = 1;
+  while (p.cluster < 8 && (long long)units * p.cluster * 2 <= 2LL * sms && p.cap >= p.cluster * 2 * 1024) p.cluster *= 2;
+  const int share = p.cap / p.cluster + 1;
+  p.keys = share < kEvictKeys ? share : kEvictKeys;
+  if (int e = paged ? allow_smem<evict_select_kernel<true>>(kEvictKeys * 4) : allow_smem<evict_select_kernel<false>>(kEvictKeys * 4))
+    return e;
+  const unsigned ctas = (unsigned)(units * p.cluster);
+  if (int e = paged ? launch_clusters(evict_select_kernel<true>, ctas, kEvictThreads, p.keys * 4, p.cluster, st, p)
+                    : launch_clusters(evict_select_kernel<false>, ctas, kEvictThreads, p.keys * 4, p.cluster, st, p))
     return e;
   return paged ? launch_dependent(evict_move_kernel<true>, (unsigned)grid, kMoveThreads, 0, st, p)
                : launch_dependent(evict_move_kernel<false>, (unsigned)grid, kMoveThreads, 0, st, p);

@@ -23,131 +23,192 @@ struct EvictParams {
   int keep, first, recent;
   int row_bytes;
   int in_place, out_ctx;
+  int cluster;  // CTAs that share a (sequence, head)'s weights
+  int keys;     // of them that a CTA's shared memory holds
   int parts;    // CTAs that share a (sequence, head, tensor)'s rows (in place: 1)
   int columns;  // CTAs that share its rows' bytes
 };
 
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 512;
 
-// The need-th largest of the candidates' keys is found 11, 11 and 10 bits at a time, by counting
-// the keys of each digit in shared memory (zeros, of which there may be very many, are counted
-// in registers); then every warp counts its own stretch of positions and, after one sum over
-// the warps, writes its kept ones in place.  The weights are read five times, from L1 but for
-// the first.
+// Adds at shared-memory address a of the cluster's CTA `rank`, or stores there.
+__device__ __forceinline__ void add_at(uint32_t a, int rank, int v) {
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\tred.shared::cluster.add.u32 [r], %2;\n\t}" ::"r"(a),
+               "r"(rank), "r"(v)
+               : "memory");
+}
+__device__ __forceinline__ void store_at(uint32_t a, int rank, int v) {
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\tst.shared::cluster.u32 [r], %2;\n\t}" ::"r"(a),
+               "r"(rank), "r"(v)
+               : "memory");
+}
+
+// The candidates are the positions [first, L - recent); a cluster's CTAs take a stretch of them
+// each, and keep its keys in shared memory (as long as they fit: `keys`).  The need-th largest key
+// is found 11, 11 and 10 bits at a time: each CTA counts its keys of each digit, CTA 0 adds the
+// counts up and finds the digit in which the need-th lies.  Zeros, of which there may be very
+// many, are counted in registers.  Then each warp counts what it keeps of its stretch, and after
+// one sum over the warps and one over the CTAs writes it in place.
+// Latency bounds it: one pass over the weights, 6 to 8 meetings of the cluster.
 template <bool PAGED>
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int hist[2048];
-  __shared__ int s_warp[32], s_warp_eq[32], s_zero, s_digit, s_above;
+  extern __shared__ uint32_t s_keys[];
+  constexpr int WARPS = kEvictThreads / 32;
+  __shared__ int hist[2048], total[2048];  // this CTA's counts; the cluster's (CTA 0)
+  __shared__ int s_warp[WARPS], s_warp_same[WARPS], s_zero, s_digit, s_above, s_done;
+  __shared__ int s_kept[8], s_same[8];  // of every CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
+  auto meet = [&]() {
+    if (p.cluster > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
+  for (int i = threadIdx.x; i < 2048; i += kEvictThreads) hist[i] = total[i] = 0;
+  if (threadIdx.x == 0) s_zero = 0;
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+  const int unit = blockIdx.x / p.cluster, b = unit / p.Hkv, h = unit % p.Hkv;
   const int L = seg_len(p.seq_lens, b, p.cap);
-  int* kept = p.kept + (size_t)blockIdx.x * p.keep;
-  if (h == 0 && threadIdx.x == 0) p.new_lens[b] = min(L, p.keep);
-  if (L <= p.keep) {
-    for (int i = threadIdx.x; i < p.keep; i += kEvictThreads) kept[i] = i < L ? i : -1;
+  int* kept = p.kept + (size_t)unit * p.keep;
+  if (rank == 0 && h == 0 && threadIdx.x == 0) p.new_lens[b] = min(L, p.keep);
+  if (L <= p.keep) {  // (all of the cluster)
+    for (int i = rank * kEvictThreads + threadIdx.x; i < p.keep; i += p.cluster * kEvictThreads) kept[i] = i < L ? i : -1;
     return;
   }
-  const int lo = p.first, hi = L - p.recent;  // candidates; L > keep >= first + recent
-  const int need = p.keep - p.first - p.recent;
-  auto key = [&](int t) {
-    const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.slab, p.num_pages, b, t);
+  const int hi = L - p.recent;                        // L > keep >= first + recent
+  const int need = p.keep - p.first - p.recent;       // of the candidates, which are more
+  const int share = (hi - p.first + p.cluster - 1) / p.cluster;
+  const int lo = min(hi, p.first + rank * share), count = min(hi, lo + share) - lo;
+  // forced ones
+  for (int i = rank * kEvictThreads + threadIdx.x; i < p.first + p.recent; i += p.cluster * kEvictThreads)
+    kept[i < p.first ? i : i + need] = i < p.first ? i : hi + i - p.first;
+  auto read = [&](int i) {
+    const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.slab, p.num_pages, b, lo + i);
     return float_key(load_dependent(p.weights + ((size_t)c.slab * p.Hkv + h) * p.slab + c.at));
   };
-  constexpr uint32_t kZero = 0x80000000u;  // of 0
-  uint32_t border = 0xffffffffu;           // nothing is above it
-  int left = 0;                            // of the border's keys that are kept
+  const int held = min(count, p.keys);
+#pragma unroll 8
+  for (int i = threadIdx.x; i < held; i += kEvictThreads) s_keys[i] = read(i);
+  auto key = [&](int i) { return i < held ? s_keys[i] : read(i); };
+  meet();
+
+  constexpr uint32_t kZero = 0x80000000u;  // the key of 0
+  uint32_t border = 0xffffffffu;           // keys above it are kept, and the first `left` of those that are it
+  int left = 0;
   if (need > 0) {
     uint32_t high = 0u;
     left = need;
+    bool done = false;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
+    for (int pass = 0; pass < 3 && !done; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-      for (int i = threadIdx.x; i < bins; i += kEvictThreads) hist[i] = 0;
-      if (threadIdx.x == 0) s_zero = 0;
-      __syncthreads();
+      const int known = pass == 1 ? 21 : 10;  // bits below the digits found so far
+      auto mine = [&](uint32_t k) { return pass == 0 || (k ^ high) >> known == 0u; };
       int zeros = 0;
 #pragma unroll 4
-      for (int t = lo + threadIdx.x; t < hi; t += kEvictThreads) {
-        const uint32_t k = key(t);
+      for (int i = threadIdx.x; i < count; i += kEvictThreads) {
+        const uint32_t k = key(i);
         if (k == kZero)
           ++zeros;
-        else if (pass == 0 || (k ^ high) >> (pass == 1 ? 21 : 10) == 0u)
+        else if (mine(k))
           atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
       }
-      if (pass > 0 && (kZero ^ high) >> (pass == 1 ? 21 : 10) != 0u) zeros = 0;
+      if (!mine(kZero)) zeros = 0;
       zeros = __reduce_add_sync(0xffffffffu, zeros);
-      if (lane == 0 && zeros) atomicAdd(&s_zero, zeros);
+      if (lane == 0 && zeros) atomicAdd(&hist[(kZero >> shift) & (bins - 1)], zeros);
       __syncthreads();
-      if (threadIdx.x == 0) hist[(kZero >> shift) & (bins - 1)] += s_zero;
-      __syncthreads();
-      // the digit in which the left-th from the top lies: two (one) bins a thread, from the top
-      const int per = bins / kEvictThreads;
-      int mine = 0;
-      for (int i = 0; i < per; ++i) mine += hist[bins - 1 - (threadIdx.x * per + i)];
-      int sum = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += up;
+      int* sums = hist;
+      if (p.cluster > 1) {
+        for (int i = threadIdx.x; i < bins; i += kEvictThreads) {
+          if (hist[i]) add_at(smem_u32(&total[i]), 0, hist[i]);
+          hist[i] = 0;
+        }
+        cluster_sync();
+        sums = total;
       }
-      if (lane == 31) s_warp[warp] = sum;
-      __syncthreads();
-      int before = sum - mine;
-      for (int w = 0; w < warp; ++w) before += s_warp[w];
-      if (before < left && before + mine >= left) {
+      if (rank == 0) {
+        // the digit in which the left-th from the top lies: 4 (2) bins a thread, from the top
+        const int per = bins / kEvictThreads;
+        int c[4], mine4 = 0;
         for (int i = 0; i < per; ++i) {
-          const int bin = bins - 1 - (threadIdx.x * per + i);
-          if (before + hist[bin] >= left) {
-            s_digit = bin;
-            s_above = before;
-            break;
+          c[i] = sums[bins - 1 - (threadIdx.x * per + i)];
+          sums[bins - 1 - (threadIdx.x * per + i)] = 0;
+          mine4 += c[i];
+        }
+        int sum = mine4;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += up;
+        }
+        if (lane == 31) s_warp[warp] = sum;
+        __syncthreads();
+        int before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0) + sum - mine4;
+        if (before < left && before + mine4 >= left) {
+          int i = 0;
+          while (before + c[i] < left) before += c[i++];
+          const int digit = bins - 1 - (threadIdx.x * per + i), all = before + c[i] == left;  // all of the digit's are kept
+          for (int r = 0; r < p.cluster; ++r) {
+            store_at(smem_u32(&s_digit), r, digit);
+            store_at(smem_u32(&s_above), r, before);
+            store_at(smem_u32(&s_done), r, all);
           }
-          before += hist[bin];
         }
       }
-      __syncthreads();
+      meet();
       high |= (uint32_t)s_digit << shift;
       left -= s_above;
-      __syncthreads();
+      done = s_done;
+      meet();
     }
-    border = high;
+    // where all keys of the last digit are kept, the border lies below the lowest they can be (which is
+    // not 0: as many candidates as are needed are not all of them)
+    border = done ? high - 1u : high;
+    if (done) left = 0;
   }
-  // every warp's stretch of [0, L), in whole steps of 32
-  const int steps = (L + 31) / 32, per = (steps + 31) / 32;
-  const int t0 = warp * per * 32, t1 = min(L, t0 + per * 32);
-  auto sure = [&](int t, uint32_t k) { return t < lo || t >= hi || k > border; };
+  // every warp's stretch, in whole steps of 32
+  const int steps = (count + 31) / 32, per = (steps + WARPS - 1) / WARPS;
+  const int i0 = warp * per * 32, i1 = min(count, i0 + per * 32);
   int above = 0, same = 0;
+  if (need > 0) {
 #pragma unroll 4
-  for (int t = t0 + lane; t < t1; t += 32) {
-    const uint32_t k = t >= lo && t < hi && need > 0 ? key(t) : 0u;
-    const bool in = sure(t, k);
-    above += in;
-    same += !in && need > 0 && k == border;
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const uint32_t k = key(i);
+      above += k > border;
+      same += k == border;
+    }
   }
   above = __reduce_add_sync(0xffffffffu, above);
   same = __reduce_add_sync(0xffffffffu, same);
   if (lane == 0) {
     s_warp[warp] = above;
-    s_warp_eq[warp] = same;
+    s_warp_same[warp] = same;
   }
   __syncthreads();
-  int at = 0, eq = 0;  // kept, and at the border, before this warp's stretch
-  for (int w = 0; w < warp; ++w) {
-    at += s_warp[w];
-    eq += s_warp_eq[w];
+  const int w_above = lane < WARPS ? s_warp[lane] : 0, w_same = lane < WARPS ? s_warp_same[lane] : 0;
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? w_above : 0), eq = __reduce_add_sync(0xffffffffu, lane < warp ? w_same : 0);
+  if (p.cluster > 1) {
+    const int all_above = __reduce_add_sync(0xffffffffu, w_above), all_same = __reduce_add_sync(0xffffffffu, w_same);
+    if (warp == 0 && lane < p.cluster) {
+      store_at(smem_u32(&s_kept[rank]), lane, all_above);
+      store_at(smem_u32(&s_same[rank]), lane, all_same);
+    }
+    cluster_sync();
+    at += __reduce_add_sync(0xffffffffu, lane < rank ? s_kept[lane & 7] : 0);
+    eq += __reduce_add_sync(0xffffffffu, lane < rank ? s_same[lane & 7] : 0);
   }
-  at += min(eq, left);
+  if (need == 0) return;
+  at += p.first + min(eq, left);
 #pragma unroll 1
-  for (int t = t0 + lane; t - lane < t1; t += 32) {
-    const bool is = t < t1;
-    const uint32_t k = is && t >= lo && t < hi && need > 0 ? key(t) : 0u;
-    const bool in = is && sure(t, k), tie = is && !in && need > 0 && k == border;
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const uint32_t k = i < i1 ? key(i) : 0u;
+    const bool in = i < i1 && k > border, tie = i < i1 && k == border;
     const unsigned ties = __ballot_sync(0xffffffffu, tie), below = (1u << lane) - 1u;
     const bool take = in || (tie && eq + __popc(ties & below) < left);
     const unsigned takes = __ballot_sync(0xffffffffu, take);
-    if (take) kept[at + __popc(takes & below)] = t;
+    if (take) kept[at + __popc(takes & below)] = lo + i;
     at += __popc(takes);
     eq += __popc(ties);
   }

@@ -1,13 +1,22 @@
 // The attention weight that new tokens give each cached token, summed over them and over the
 // heads of a group.  A softmax needs its whole row's maximum and sum before the first weight
-// is known, so there are two kernels:
-//   scores    reads every key once, 16 query rows at a time on the warp-level MMA, writes the
-//             scores (64 fp32 a row and tile, a sixteenth of a bf16 key's bytes a row) and
-//             each piece's (m, l);
-//   finish    joins a sequence's (m, l), reads the scores, adds the rows' weights in their
-//             order and writes decay * prior + sum.
-// Both go along a line of tiles (seg_plan.cuh), of (sequence, KV head, 16 rows) and of (sequence,
-// KV head).  A key's bytes bound it: what decode reads without the values.
+// is known, so there are two kernels, on the warp-level MMA with 16 query rows to a tile:
+//
+// up to 16 rows (decode):
+//   weights_score_kernel   reads every key once, writes the scores (64 fp32 a row and tile, a
+//                          sixteenth of a bf16 key's bytes a row) and each piece's (m, l);
+//   weights_finish_kernel  joins a sequence's (m, l), reads the scores, adds the rows' weights
+//                          in their order and writes decay * prior + sum.
+// A key's bytes bound it: what decode reads without the values.
+//
+// more rows (a window of a prompt), 128 at a time:
+//   weights_window_kernel  twice: once for each piece's (m, l), once for the sums, with the scores
+//                          computed again, as writing and reading 128 fp32 a key costs more than its
+//                          own 128 or 256 bytes and 2 D products a row.  A key is widened to MMA
+//                          fragments once for all rows, whose queries lie in shared memory.
+// Bound by the MMAs (2 x 2 D operations a row and key) and two exponentials a row and key.
+//
+// All go along a line of tiles (seg_plan.cuh) of (sequence, KV head).
 #pragma once
 
 #include "seg_kernel.cuh"
@@ -15,28 +24,31 @@
 namespace da {
 
 struct WeightsParams {
-  SegParams s;  // k: bf16 or int8; base = rt_prefix = 0
+  SegParams s;  // k: bf16 or int8; base = rt_prefix = 0, rt = 1
   const float* k_scale;
   const float* prior;
   float* out;
-  float* scores;  // [tile of the line][rows of a unit, 16 at most][64]
-  int rows;       // that number
+  float* scores;  // [tile of the line][rows][64]
+  int rows;       // query rows of a KV head, or of this window
+  int row0;       // the window's first
   int finish_ctas;
   float decay;
 };
 
-template <int D, bool INT8>
+template <int D, bool INT8, bool WINDOW>
 struct ScoreGeo {
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
   static constexpr int ROWB = D * (INT8 ? 1 : 2);
   static constexpr int STAGE = 16 * ROWB + (INT8 ? 64 : 0);  // keys of 16 tokens, and their scales
-  static constexpr int NSTAGE = ROWB == 512 ? 3 : 6;  // two CTAs an SM either way
+  static constexpr int NSTAGE = WINDOW ? (ROWB == 512 ? 2 : 4) : ROWB == 512 ? 3 : 6;
   static constexpr int WARP_BYTES = NSTAGE * STAGE;
-  static constexpr int OFF_ML = WARPS * WARP_BYTES;
-  static constexpr int OFF_MASK = OFF_ML + WARPS * 16 * 8;
+  static constexpr int ROWS = WINDOW ? 128 : 16;  // query rows of a unit
+  static constexpr int OFF_Q = WARPS * WARP_BYTES;  // a window's queries, [128][D]
+  static constexpr int OFF_ML = OFF_Q + (WINDOW ? ROWS * D * 2 : 0);
+  static constexpr int OFF_MASK = OFF_ML + WARPS * ROWS * 8;
   static constexpr int OFF_LENS = OFF_MASK + WARPS * NSTAGE * 4;
   static constexpr int SMEM = OFF_LENS + kSegLens * 4;
-  static constexpr int PER_SM = 2;
+  static constexpr int PER_SM = WINDOW ? (D == 256 ? 1 : INT8 || D == 64 ? 3 : 2) : 2;
 };
 
 // Where a token's row lies: its page (or sequence) and place in it.
@@ -73,15 +85,132 @@ __device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
+// A warp's ring of keys: 16 tokens of every tile of the CTA's, looked up a tile ahead.
+template <int D, bool PAGED, bool INT8, bool WINDOW>
+struct KeyRing {
+  using Gm = ScoreGeo<D, INT8, WINDOW>;
+  static constexpr int CH = Gm::ROWB / 16;  // chunks a row
+  const WeightsParams& wp;
+  const SegWalk<kSegRange>& walk;
+  uint32_t at;  // of the ring in shared memory
+  volatile uint32_t* masks;
+  SegUnit u;
+  int j;
+  long long x, x1, off, soff;
+
+  __device__ __forceinline__ KeyRing(const WeightsParams& wp_, const SegWalk<kSegRange>& walk_, uint32_t at_,
+                                     volatile uint32_t* masks_, long long x0, long long x1_)
+      : wp(wp_), walk(walk_), at(at_), masks(masks_), x(x0), x1(x1_) {
+    u = walk.at(x0, j);
+    look_up();
+  }
+  // int8: rows 2 p and 2 p + 1 of a quarter warp's read in different halves of 128 bytes
+  static __device__ __forceinline__ int chunk(int row, int c) {
+    return INT8 ? c ^ ((row & 1) << 2) % CH : c ^ (row & 7);
+  }
+  __device__ __forceinline__ void look_up() {
+    const SegParams& p = wp.s;
+    const int lane = threadIdx.x & 31, t = j * kTile + (threadIdx.x >> 5) * 16 + lane;
+    off = -1;
+    soff = 0;
+    if (lane < 16 && t < u.end) {
+      const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
+      const int slab_rows = PAGED ? p.page_size : p.ctx;
+      off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)Gm::ROWB;
+      soff = (c.slab * p.Hkv + u.h) * slab_rows + c.at;
+    }
+  }
+  __device__ __forceinline__ void issue(int stage) {
+    if (x < x1) {
+      const int lane = threadIdx.x & 31;
+      const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
+      if (lane == 0) masks[stage] = live;
+      if (live) {
+        const uint8_t* keys = reinterpret_cast<const uint8_t*>(wp.s.k);
+        const uint32_t dst = at + stage * Gm::STAGE;
+        constexpr int RPP = 32 / (CH < 32 ? CH : 32);
+        const int c = lane % CH, r0 = lane / CH;
+#pragma unroll
+        for (int r = 0; r < 16; r += RPP) {
+          const int row = r + r0;
+          const long long o = __shfl_sync(0xffffffffu, off, row);
+          cp_async16(dst + row * Gm::ROWB + (chunk(row, c) << 4), keys + (o < 0 ? 0 : o) + c * 16, o >= 0);
+        }
+        if (INT8 && off >= 0) cp_async4(dst + 16 * Gm::ROWB + lane * 4, wp.k_scale + soff);
+      }
+      ++x;
+      if (x < x1) {
+        if (++j == u.tiles) {
+          u = walk.next(u);
+          j = 0;
+        }
+        look_up();
+      }
+    }
+    cp_async_commit();
+  }
+  // The B fragments of 8 tokens from token 8 nt of a stage, step kk of 16 elements in b[kk], and
+  // the scales of this thread's two.  bf16: element 16 kk + 2 t (and + 8) is thread t's of the
+  // quad; int8: 64 c + 16 t + 4 s (and + 2) for kk = 4 c + s, so that a thread's 16 bytes of a key
+  // hold its elements of 4 steps.
+  __device__ __forceinline__ void fragments(int stage, int nt, uint32_t (&b)[D / 16][2], float2& scale) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t kst = at + stage * Gm::STAGE;
+    if constexpr (INT8) {
+      const int row = nt * 8 + lane / 4;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t e[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
+                     : "r"(kst + row * Gm::ROWB + chunk(row, 4 * c + lane % 4) * 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          b[4 * c + i][0] = int8x2_to_bf16x2<0>(e[i]);
+          b[4 * c + i][1] = int8x2_to_bf16x2<1>(e[i]);
+        }
+      }
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(scale.x), "=f"(scale.y)
+                   : "r"(kst + 16 * Gm::ROWB + (nt * 8 + 2 * (lane % 4)) * 4));
+    } else {
+      scale = make_float2(1.f, 1.f);
+      const int mrow = lane & 7, mi = lane >> 3;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; kk += 2) {
+        // matrices: steps kk and kk + 1, low and high half
+        const int row = nt * 8 + mrow, c = 2 * kk + mi;
+        ldsm_x4(kst + row * Gm::ROWB + (chunk(row, c) << 4), b[kk][0], b[kk][1], b[kk + 1][0], b[kk + 1][1]);
+      }
+    }
+  }
+  // The words of a query row (32-bit index) that go with them for step kk: first and second half.
+  static __device__ __forceinline__ int query_word(int kk, int t) { return INT8 ? 32 * (kk / 4) + 8 * t + 2 * (kk % 4) : 8 * kk + t; }
+  static constexpr int kQueryHalf = INT8 ? 1 : 4;
+};
+
+// Joins the warps' (m, l) of a row.
+template <int WARPS, int ROWS>
+__device__ __forceinline__ float2 join_warps(const float2* ml, int row) {
+  float M = kNegInf, L = 0.f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml[w * ROWS + row].x);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float2 y = ml[w * ROWS + row];
+    if (y.y != 0.f) L += y.x == kNegInf ? y.y : exp2_approx(y.x - M) * y.y;
+  }
+  return make_float2(M, L);
+}
+
 template <int D, bool PAGED, bool INT8>
-__global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>::PER_SM)
+__global__ void __launch_bounds__(ScoreGeo<D, INT8, false>::THREADS, ScoreGeo<D, INT8, false>::PER_SM)
     weights_score_kernel(const __grid_constant__ WeightsParams wp) {
-  using Gm = ScoreGeo<D, INT8>;
+  using Gm = ScoreGeo<D, INT8, false>;
+  using Ring = KeyRing<D, PAGED, INT8, false>;
   const SegParams& p = wp.s;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ring = smem + warp * Gm::WARP_BYTES;
-  const uint32_t ring_s = smem_u32(ring);
   volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * Gm::NSTAGE;
 
   pdl_wait_primary();
@@ -89,56 +218,11 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
   const SegWalk<kSegRange> walk(p, seg_stage_lens<Gm::THREADS>(p, reinterpret_cast<int*>(smem + Gm::OFF_LENS)));
   long long x0, x1;
   if (!walk.range(blockIdx.x, x0, x1)) return;
-
-  const uint8_t* keys = reinterpret_cast<const uint8_t*>(p.k);
-  const int slab_rows = PAGED ? p.page_size : p.ctx;
-  int lj;
-  SegUnit lu = walk.at(x0, lj);
-  long long lx = x0, off = -1, soff = 0;
-  auto look_up = [&]() {
-    off = -1;
-    const int t = lj * kTile + warp * 16 + lane;
-    if (lane < 16 && t < lu.end) {
-      const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, lu.b, t);
-      off = ((c.slab * slab_rows + c.at) * p.Hkv + lu.h) * (long long)Gm::ROWB;
-      soff = (c.slab * p.Hkv + lu.h) * slab_rows + c.at;
-    }
-  };
-  look_up();
-  auto issue = [&](int stage) {
-    if (lx < x1) {
-      const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
-      if (lane == 0) masks[stage] = live;
-      if (live) {
-        const uint32_t dst = ring_s + stage * Gm::STAGE;
-        constexpr int CH = Gm::ROWB / 16, RPP = 32 / (CH < 32 ? CH : 32);
-        const int c = lane % CH, r0 = lane / CH;
-#pragma unroll
-        for (int r = 0; r < 16; r += RPP) {
-          const int row = r + r0;
-          const long long o = __shfl_sync(0xffffffffu, off, row);
-          // int8: rows 2 p and 2 p + 1 of a quarter warp's read in different halves of 128 bytes
-          const int at = INT8 ? c ^ ((row & 1) << 2) % CH : c ^ (row & 7);
-          cp_async16(dst + row * Gm::ROWB + (at << 4), keys + (o < 0 ? 0 : o) + c * 16, o >= 0);
-        }
-        if (INT8 && off >= 0) cp_async4(dst + 16 * Gm::ROWB + lane * 4, wp.k_scale + soff);
-      }
-      ++lx;
-      if (lx < x1) {
-        if (++lj == lu.tiles) {
-          lu = walk.next(lu);
-          lj = 0;
-        }
-        look_up();
-      }
-    }
-    cp_async_commit();
-  };
-
-  int j = lj;
-  SegUnit u = lu;
+  Ring ring(wp, walk, smem_u32(smem + warp * Gm::WARP_BYTES), masks, x0, x1);
+  SegUnit u = ring.u;
+  int j = ring.j;
 #pragma unroll 1
-  for (int s = 0; s < Gm::NSTAGE; ++s) issue(s);
+  for (int s = 0; s < Gm::NSTAGE; ++s) ring.issue(s);
 
   uint32_t qa[D / 16][4];
   float m[2], l[2];
@@ -154,13 +238,11 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
         int token, g;
         has[hf] = seg_query<kSegRange>(p, walk.lens, u, lane / 4 + 8 * hf, token, g, lim[hf]);
         const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D);
-        // bf16: element 16 kk + 2 t (and + 8) is thread t's of the quad; int8: 64 c + 16 t + 4 s (and
-        // + 2) for kk = 4 c + s, so that a thread's 16 bytes of a key hold its elements of 4 steps
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const int w = INT8 ? 32 * (kk / 4) + 8 * (lane % 4) + 2 * (kk % 4) : 8 * kk + lane % 4;
+          const int w = Ring::query_word(kk, lane % 4);
           qa[kk][hf] = has[hf] ? load_dependent(src + w) : 0u;
-          qa[kk][2 + hf] = has[hf] ? load_dependent(src + w + (INT8 ? 1 : 4)) : 0u;
+          qa[kk][2 + hf] = has[hf] ? load_dependent(src + w + Ring::kQueryHalf) : 0u;
         }
         m[hf] = kNegInf;
         l[hf] = 0.f;
@@ -170,50 +252,24 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
     __syncwarp();
     const uint32_t live = masks[stage];
     if (live) {
-      const uint32_t kst = ring_s + stage * Gm::STAGE;
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      float ks[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
-      if constexpr (INT8) {
-        constexpr int CH = Gm::ROWB / 16;
-        const uint8_t* kp = ring + stage * Gm::STAGE;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int row = nt * 8 + lane / 4;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const int ch = (4 * c + lane % 4) ^ ((row & 1) << 2) % CH;
-            const uint4 w = *reinterpret_cast<const uint4*>(kp + row * Gm::ROWB + ch * 16);
-            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_bf16_16816(s[nt], qa[4 * c + i][0], qa[4 * c + i][1], qa[4 * c + i][2], qa[4 * c + i][3],
-                             int8x2_to_bf16x2<0>(e[i]), int8x2_to_bf16x2<1>(e[i]));
-          }
-          const float2 sc = *reinterpret_cast<const float2*>(kp + 16 * Gm::ROWB + (nt * 8 + 2 * (lane % 4)) * 4);
-          ks[nt][0] = sc.x;
-          ks[nt][1] = sc.y;
-        }
-      } else {
-        const int mrow = lane & 7, mi = lane >> 3;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t r0, r1, r2, r3;
-          const int row = (mi >> 1) * 8 + mrow, c = 2 * kk + (mi & 1);
-          ldsm_x4(kst + row * Gm::ROWB + ((c ^ mrow) << 4), r0, r1, r2, r3);
-          mma_bf16_16816(s[0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], r0, r1);
-          mma_bf16_16816(s[1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], r2, r3);
-        }
-      }
       float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < 2; ++nt) {
+        uint32_t b[D / 16][2];
+        float2 ks;
+        ring.fragments(stage, nt, b, ks);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_16816(s[nt], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[kk][0], b[kk][1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int col = nt * 8 + 2 * (lane % 4) + (e & 1);
           const bool see = ((live >> col) & 1) && j * kTile + warp * 16 + col < lim[e >> 1];
-          s[nt][e] = see ? s[nt][e] * ks[nt][e & 1] * p.scale_log2 : kNegInf;
+          s[nt][e] = see ? s[nt][e] * (e & 1 ? ks.y : ks.x) * p.scale_log2 : kNegInf;
           mx[e >> 1] = fmaxf(mx[e >> 1], s[nt][e]);
         }
+      }
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
@@ -242,20 +298,11 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
         if (lane % 4 == 0) ml[warp * 16 + lane / 4 + 8 * hf] = make_float2(m[hf], l[hf]);
       }
       __syncthreads();
-      if (threadIdx.x < 16) {
-        float M = kNegInf, L = 0.f;
-#pragma unroll
-        for (int w = 0; w < Gm::WARPS; ++w) M = fmaxf(M, ml[w * 16 + threadIdx.x].x);
-#pragma unroll
-        for (int w = 0; w < Gm::WARPS; ++w) {
-          const float2 y = ml[w * 16 + threadIdx.x];
-          if (y.y != 0.f) L += y.x == kNegInf ? y.y : exp2_approx(y.x - M) * y.y;
-        }
-        p.part_ml[((size_t)u.id + blockIdx.x) * 16 + threadIdx.x] = make_float2(M, L);
-      }
+      if (threadIdx.x < 16)
+        p.part_ml[((size_t)u.id + blockIdx.x) * 16 + threadIdx.x] = join_warps<Gm::WARPS, 16>(ml, threadIdx.x);
       __syncthreads();
     }
-    issue(stage);
+    ring.issue(stage);
     stage = stage + 1 == Gm::NSTAGE ? 0 : stage + 1;
     ++j;
     if (last && x + 1 < x1) {
@@ -267,66 +314,281 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
   cp_async_wait<0>();
 }
 
-constexpr int kFinishThreads = 256, kFinishRows = 1024;
+// (m, l) of row r of a unit from its pieces, [slot][stride] of them; the warp executes it.
+__device__ __forceinline__ float2 join_pieces(const float2* ml, long long slot, int pieces, int stride, int r) {
+  const int lane = threadIdx.x & 31;
+  float M = kNegInf, L = 0.f;
+  for (int k = lane; k < pieces; k += 32) {
+    const float2 y = __ldcg(ml + (slot + k) * stride + r);
+    if (y.y == 0.f) continue;
+    const float to = fmaxf(M, y.x);
+    L = (M == kNegInf ? L : L * exp2_approx(M - to)) + (y.x == kNegInf ? y.y : y.y * exp2_approx(y.x - to));
+    M = to;
+  }
+  float top = M;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  L = M == kNegInf ? L : L * exp2_approx(M - top);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  return make_float2(top, L);
+}
+// What a weight is made with: 2^(x - .x) * .y; a row that saw nothing gives nothing.
+__device__ __forceinline__ float2 weight_factors(float2 ml) {
+  return make_float2(ml.x == kNegInf ? 0.f : ml.x, ml.y == 0.f ? 0.f : 1.f / ml.y);
+}
+
+// Rows [row0, row0 + rows) of every unit, at most 128.  SUMS: out = decay * prior + their
+// weights; else their pieces' (m, l), [slot][128].
+template <int D, bool PAGED, bool INT8, bool SUMS>
+__global__ void __launch_bounds__(ScoreGeo<D, INT8, true>::THREADS, ScoreGeo<D, INT8, true>::PER_SM)
+    weights_window_kernel(const __grid_constant__ WeightsParams wp) {
+  using Gm = ScoreGeo<D, INT8, true>;
+  using Ring = KeyRing<D, PAGED, INT8, true>;
+  constexpr int RT = Gm::ROWS / 16;  // row tiles
+  const SegParams& p = wp.s;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * Gm::NSTAGE;
+  float2* ml = reinterpret_cast<float2*>(smem + Gm::OFF_ML);
+
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const SegWalk<kSegRange> walk(p, seg_stage_lens<Gm::THREADS>(p, reinterpret_cast<int*>(smem + Gm::OFF_LENS)));
+  long long x0, x1;
+  if (!walk.range(blockIdx.x, x0, x1)) return;
+  Ring ring(wp, walk, smem_u32(smem + warp * Gm::WARP_BYTES), masks, x0, x1);
+  SegUnit u = ring.u;
+  int j = ring.j;
+#pragma unroll 1
+  for (int s = 0; s < Gm::NSTAGE; ++s) ring.issue(s);
+
+  const int tiles = (wp.rows + 15) / 16;  // row tiles with rows
+  // queries, [128][D], 16-byte chunks of a row exchanged so that the reads of a fragment meet different banks
+  uint4* qs = reinterpret_cast<uint4*>(smem + Gm::OFF_Q);
+  auto query_chunk = [](int row, int c) { return row * (D / 8) + (INT8 ? c ^ (row & 1) : c ^ (row & 7)); };
+  float m[RT][2], l[RT][2];
+  bool fresh = true;
+  int stage = 0;
+  for (long long x = x0; x < x1; ++x) {
+    if (fresh) {
+      fresh = false;
+      __syncthreads();
+      constexpr int U = 8;
+      for (int e0 = threadIdx.x; e0 < tiles * 16 * (D / 8); e0 += U * Gm::THREADS) {
+        uint4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int in = (e0 + i * Gm::THREADS) / (D / 8), c = (e0 + i * Gm::THREADS) % (D / 8), row = wp.row0 + in;
+          const int token = u.b * p.n + row / p.G, g = row % p.G;
+          v[i] = in < wp.rows ? load_dependent(reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D) + c)
+                              : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int in = (e0 + i * Gm::THREADS) / (D / 8), c = (e0 + i * Gm::THREADS) % (D / 8);
+          if (in < tiles * 16) qs[query_chunk(in, c)] = v[i];
+        }
+      }
+      if constexpr (SUMS) {
+        const SegSums sums = seg_sums(walk.lens, p.B, p.cap, 0, u.b);
+        const long long a = sums.before * p.Hkv + (long long)u.h * u.tiles;
+        const int c0 = seg_owner(walk.all, walk.used, a), c1 = seg_owner(walk.all, walk.used, a + u.tiles - 1);
+        for (int r = warp; r < tiles * 16; r += Gm::WARPS) {
+          const float2 f = weight_factors(join_pieces(p.part_ml, (long long)u.id + c0, c1 - c0 + 1, Gm::ROWS, r));
+          if (lane == 0) ml[r] = r < wp.rows ? f : make_float2(0.f, 0.f);  // no weight of rows that are not
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          m[r][hf] = kNegInf;
+          l[r][hf] = 0.f;
+        }
+      __syncthreads();
+    }
+    cp_async_wait<Gm::NSTAGE - 1>();
+    __syncwarp();
+    const uint32_t live = masks[stage];
+    const int t0 = j * kTile + warp * 16;
+    if (live) {
+      // both halves of the 16 tokens against a row tile at a time: a query fragment is read once for two
+      // products, and two chains of them run side by side
+      uint32_t b[2][D / 16][2];
+      float2 ks[2], sum[2];
+      bool on[2][2];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        ring.fragments(stage, nt, b[nt], ks[nt]);
+        ks[nt].x *= p.scale_log2;
+        ks[nt].y *= p.scale_log2;
+        on[nt][0] = (live >> (nt * 8 + 2 * (lane % 4))) & 1;
+        on[nt][1] = (live >> (nt * 8 + 2 * (lane % 4) + 1)) & 1;
+        sum[nt] = make_float2(0.f, 0.f);
+      }
+      const bool edge = t0 + 16 > u.len - p.n + 1;  // a token that not every row sees
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (r >= tiles) break;
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        if constexpr (INT8) {
+          // 16 elements of each of the thread's two rows: four steps
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t w[2][8];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint4 v = qs[query_chunk(r * 16 + lane / 4 + 8 * hf, 8 * c + 2 * (lane % 4) + i)];
+                w[hf][4 * i] = v.x;
+                w[hf][4 * i + 1] = v.y;
+                w[hf][4 * i + 2] = v.z;
+                w[hf][4 * i + 3] = v.w;
+              }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+                mma_bf16_16816(s[nt], w[0][2 * i], w[1][2 * i], w[0][2 * i + 1], w[1][2 * i + 1], b[nt][4 * c + i][0],
+                               b[nt][4 * c + i][1]);
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t a0, a1, a2, a3;  // rows 0 .. 7 and 8 .. 15 of the first 8 elements, then of the second
+            ldsm_x4(smem_u32(qs + query_chunk(r * 16 + (lane & 15), 2 * kk + (lane >> 4))), a0, a1, a2, a3);
+            mma_bf16_16816(s[0], a0, a1, a2, a3, b[0][kk][0], b[0][kk][1]);
+            mma_bf16_16816(s[1], a0, a1, a2, a3, b[1][kk][0], b[1][kk][1]);
+          }
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float y[2][2];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            y[nt][0] = on[nt][0] ? s[nt][2 * hf] * ks[nt].x : kNegInf;
+            y[nt][1] = on[nt][1] ? s[nt][2 * hf + 1] * ks[nt].y : kNegInf;
+          }
+          if (edge) {
+            const int left = u.len - p.n + 1 + (wp.row0 + r * 16 + lane / 4 + 8 * hf) / p.G - t0 - 2 * (lane % 4);
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              y[nt][0] = nt * 8 < left ? y[nt][0] : kNegInf;
+              y[nt][1] = nt * 8 + 1 < left ? y[nt][1] : kNegInf;
+            }
+          }
+          if constexpr (SUMS) {
+            const float2 f = ml[r * 16 + lane / 4 + 8 * hf];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              sum[nt].x = fmaf(exp2_approx(y[nt][0] - f.x), f.y, sum[nt].x);
+              sum[nt].y = fmaf(exp2_approx(y[nt][1] - f.x), f.y, sum[nt].y);
+            }
+          } else {
+            const float top = fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[1][0], y[1][1]));
+            if (top > m[r][hf]) {
+              l[r][hf] *= exp2_approx(m[r][hf] - top);
+              m[r][hf] = top;
+            }
+            const float mu = m[r][hf] == kNegInf ? 0.f : m[r][hf];
+            l[r][hf] += (exp2_approx(y[0][0] - mu) + exp2_approx(y[0][1] - mu)) +
+                        (exp2_approx(y[1][0] - mu) + exp2_approx(y[1][1] - mu));
+          }
+        }
+      }
+      if constexpr (SUMS) {
+        // the rows' sum: over the 8 lanes of a column, which hold 16 rows
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            sum[nt].x += __shfl_xor_sync(0xffffffffu, sum[nt].x, d);
+            sum[nt].y += __shfl_xor_sync(0xffffffffu, sum[nt].y, d);
+          }
+        // lane 4 k + c writes token 2 c + (k & 1) of half k / 2
+        const int k = lane / 4, t = t0 + (k >> 1) * 8 + 2 * (lane % 4) + (k & 1);
+        if (k < 4 && t < u.end) {
+          const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
+          if (c.good) {
+            const size_t o = ((size_t)c.slab * p.Hkv + u.h) * (PAGED ? p.page_size : p.ctx) + c.at;
+            const float w = k == 0 ? sum[0].x : k == 1 ? sum[0].y : k == 2 ? sum[1].x : sum[1].y;
+            wp.out[o] = wp.prior ? fmaf(wp.decay, load_dependent(wp.prior + o), w) : w;
+          }
+        }
+      }
+    }
+    const bool last = j + 1 == u.tiles;
+    if (!SUMS && (last || x + 1 == x1)) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          // the quad's four
+          float M = m[r][hf];
+          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+          float L = l[r][hf] == 0.f ? 0.f : m[r][hf] == kNegInf ? l[r][hf] : l[r][hf] * exp2_approx(m[r][hf] - M);
+          L += __shfl_xor_sync(0xffffffffu, L, 1);
+          L += __shfl_xor_sync(0xffffffffu, L, 2);
+          if (lane % 4 == 0) ml[warp * Gm::ROWS + r * 16 + lane / 4 + 8 * hf] = make_float2(M, L);
+        }
+      __syncthreads();
+      for (int r = threadIdx.x; r < tiles * 16; r += Gm::THREADS)
+        p.part_ml[((size_t)u.id + blockIdx.x) * Gm::ROWS + r] = join_warps<Gm::WARPS, Gm::ROWS>(ml, r);
+      __syncthreads();
+    }
+    ring.issue(stage);
+    stage = stage + 1 == Gm::NSTAGE ? 0 : stage + 1;
+    ++j;
+    if (last && x + 1 < x1) {
+      u = walk.next(u);
+      j = 0;
+      fresh = true;
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// A thread a token: it adds the rows in their order, 256 tokens of a sequence's KV head at a time.
+constexpr int kFinishThreads = 256;
 
 template <bool PAGED>
 __global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const __grid_constant__ WeightsParams wp) {
   const SegParams& p = wp.s;
-  __shared__ float2 row_ml[kFinishRows];  // m and 1 / l
-  __shared__ float sums[kFinishThreads];
+  __shared__ float2 row[16];
   pdl_wait_primary();
   const long long all = seg_sums(p.seq_lens, p.B, p.cap, 0, 0).all;  // tiles of the batch
-  const long long W = all * p.Hkv * p.rt, F = all * p.Hkv;
-  const long long f0 = seg_start(F, wp.finish_ctas, blockIdx.x), f1 = seg_start(F, wp.finish_ctas, blockIdx.x + 1);
-  const int rows = p.n * p.G, used = seg_used(W, p.ctas);
-  long long f = f0;
-  while (f < f1) {  // a sequence's KV head at a time
-    const SegAt s = seg_find(p.seq_lens, p.B, p.cap, 0, f / p.Hkv);
+  const long long W = all * p.Hkv;
+  const int used = seg_used(W, p.ctas), ctas = seg_used(W, wp.finish_ctas);
+  if ((int)blockIdx.x >= ctas) return;
+  const long long f1 = seg_start(W, ctas, blockIdx.x + 1);
+  long long f = seg_start(W, ctas, blockIdx.x);
+  while (f < f1) {
+    const SegAt s = seg_find(p.seq_lens, p.B, p.cap, 0, seg_div(f, p.Hkv));
     const int L = seg_len(p.seq_lens, s.b, p.cap), tiles = seg_tiles(L, p.cap, 0);
-    const int h = (int)((f - s.start * p.Hkv) / tiles), j0 = (int)((f - s.start * p.Hkv) % tiles);
+    const int h = (int)seg_div(f - s.start * p.Hkv, tiles), j0 = (int)(f - s.start * p.Hkv - (long long)h * tiles);
     const int j1 = (int)min((long long)tiles, j0 + (f1 - f));
-    const long long line = s.start * p.Hkv * p.rt + (long long)h * p.rt * tiles;  // its first tile among the scores
+    const long long line = s.start * p.Hkv + (long long)h * tiles;  // its first tile among the scores
+    const int c0 = seg_owner(W, used, line), c1 = seg_owner(W, used, line + tiles - 1);
     __syncthreads();
-    for (int r = threadIdx.x; r < rows; r += kFinishThreads) {
-      const long long a = line + (long long)(r / 16) * tiles;
-      const int c0 = seg_owner(W, used, a), c1 = seg_owner(W, used, a + tiles - 1);
-      const float2* ml = p.part_ml + ((size_t)(s.b * p.Hkv + h) * p.rt + r / 16 + c0) * 16 + r % 16;
-      float M = kNegInf, sum = 0.f;
-#pragma unroll 4
-      for (int k = 0; k <= c1 - c0; ++k) {
-        const float2 y = __ldcg(ml + (size_t)k * 16);
-        if (y.y == 0.f) continue;
-        const float to = fmaxf(M, y.x);
-        sum = (M == kNegInf ? sum : sum * exp2_approx(M - to)) + (y.x == kNegInf ? y.y : y.y * exp2_approx(y.x - to));
-        M = to;
-      }
-      row_ml[r] = make_float2(M == kNegInf ? 0.f : M, sum == 0.f ? 0.f : 1.f / sum);
+    for (int r = threadIdx.x >> 5; r < wp.rows; r += kFinishThreads / 32) {
+      const float2 y = weight_factors(join_pieces(p.part_ml, (long long)(s.b * p.Hkv + h) + c0, c1 - c0 + 1, 16, r));
+      if ((threadIdx.x & 31) == 0) row[r] = y;
     }
     __syncthreads();
-    const int at = threadIdx.x % kTile, part = threadIdx.x / kTile;
-    constexpr int PARTS = kFinishThreads / kTile;
-    for (int j = j0; j < j1; ++j) {
-      const int t = j * kTile + at;
+    for (int j = j0 + threadIdx.x / kTile; j < j1; j += kFinishThreads / kTile) {
+      const int t = j * kTile + threadIdx.x % kTile;
+      if (t >= L) continue;
+      const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, s.b, t);
+      const size_t o = ((size_t)c.slab * p.Hkv + h) * (PAGED ? p.page_size : p.ctx) + c.at;
+      const float before = wp.prior && c.good ? load_dependent(wp.prior + o) : 0.f;
+      const float* x = wp.scores + (size_t)(line + j) * wp.rows * kTile + threadIdx.x % kTile;
       float w = 0.f;
-      if (t < L) {
-#pragma unroll 4
-        for (int r = part; r < rows; r += PARTS) {
-          const float x = __ldcg(wp.scores + ((size_t)(line + (long long)(r / 16) * tiles + j) * wp.rows + r % 16) * kTile + at);
-          w += exp2_approx(x - row_ml[r].x) * row_ml[r].y;
-        }
-      }
-      sums[threadIdx.x] = w;
-      __syncthreads();
-      if (part == 0 && t < L) {
-#pragma unroll
-        for (int k = 1; k < PARTS; ++k) w += sums[k * kTile + at];
-        const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, s.b, t);
-        if (c.good) {
-          const size_t o = ((size_t)c.slab * p.Hkv + h) * (PAGED ? p.page_size : p.ctx) + c.at;
-          wp.out[o] = wp.prior ? fmaf(wp.decay, load_dependent(wp.prior + o), w) : w;
-        }
-      }
-      __syncthreads();
+#pragma unroll 8
+      for (int r = 0; r < wp.rows; ++r) w = fmaf(exp2_approx(__ldcg(x + r * kTile) - row[r].x), row[r].y, w);
+      if (c.good) wp.out[o] = wp.prior ? fmaf(wp.decay, before, w) : w;
     }
     f += j1 - j0;
   }
