@@ -114,6 +114,7 @@ int weights_call(WeightsCall& c, float scale, void* stream) {
   for (const void* x : {(const void*)p.k, (const void*)p.q, (const void*)w.out, (const void*)w.prior, (const void*)w.k_scale})
     if (overlap(c.workspace, s.bytes, x, x == p.k ? kn : x == p.q ? qn : on)) return DA_ERR_INVALID_ARG;
   p.rt = 1;
+  p.ru = 16;
   w.rows = s.rows;
   p.part_ml = static_cast<float2*>(c.workspace);
   w.scores = reinterpret_cast<float*>(p.part_ml + s.slots * 16);

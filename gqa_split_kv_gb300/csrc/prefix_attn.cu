@@ -25,7 +25,7 @@ int tc_rows(int D) { return D == 64 ? tc_rows<64>() : D == 128 ? tc_rows<128>() 
 
 // What a call of these sizes launches.
 struct PrefixShape {
-  int rt, rt_prefix, ctas;     // seg_kernel's
+  int ru, rt, rt_prefix, ctas;  // seg_kernel's
   int splits, row_blocks;      // prefix_tc_kernel's: the most parts that a prefix's keys may have
   long long slots, rows, tc_ml, bytes;  // tc_ml: bytes of the parts' (m, l)
 };
@@ -36,16 +36,17 @@ int prefix_shape(int B, int n, int Hq, int Hkv, int D, int sms, PrefixShape* s) 
   const int G = Hq / Hkv;
   if (G > 64 || Hq > 65536 || product(B, n, Hq) > 0x7fffffffLL / 16) return DA_ERR_UNSUPPORTED;
   s->rows = (long long)B * n * G;
-  s->rt = (int)(((long long)n * G + 15) / 16);
-  s->ctas = seg_ctas(D, sms);
-  // up to 16 rows, the prefix goes through seg_kernel as one more unit a head
-  s->rt_prefix = s->rows <= 16 ? (s->rows > 0) : 0;
+  s->ru = seg_unit_rows((long long)n * G, D);
+  s->rt = (int)(((long long)n * G + s->ru - 1) / s->ru);
+  s->ctas = seg_ctas(s->ru, D, sms);
+  // few rows: the prefix goes through seg_kernel, as one or two more units a head
+  s->rt_prefix = s->rows <= 16 ? (int)((s->rows + s->ru - 1) / s->ru) : 0;
   s->row_blocks = (int)((s->rows + tc_rows(D) - 1) / tc_rows(D));
   const long long units = product(Hkv, s->row_blocks);
   s->splits = s->rt_prefix || units == 0 ? 0 : units >= sms ? 1 : (int)(sms / units);
   s->slots = (long long)Hkv * s->rt_prefix + (long long)B * Hkv * s->rt + s->ctas;
   s->tc_ml = (s->splits * product(Hkv, s->rows, 8) + 15) / 16 * 16;
-  s->bytes = seg_partial_bytes(s->slots, D) + s->tc_ml + s->splits * product(Hkv, s->rows, D * 4);
+  s->bytes = seg_partial_bytes(s->slots, s->ru, D) + s->tc_ml + s->splits * product(Hkv, s->rows, D * 4);
   return DA_OK;
 }
 
@@ -171,8 +172,9 @@ int prefix_call(PrefixCall& c, float scale, void* stream) {
   p.rt = s.rt;
   p.rt_prefix = s.rt_prefix;
   p.ctas = s.ctas;
+  p.ru = s.ru;
   seg_partials(p, c.workspace, s.slots, c.D);
-  p.tc_ml = p.part_ml + s.slots * 16;
+  p.tc_ml = p.part_ml + s.slots * s.ru;
   p.tc_o = reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.tc_ml) + s.tc_ml);
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -9,14 +9,22 @@
 namespace da {
 namespace {
 
-// CTAs of the seg kernels: as many as run at once.
-int seg_ctas(int D, int sms) { return sms * (D == 64 ? SegGeo<64>::PER_SM : D == 128 ? SegGeo<128>::PER_SM : SegGeo<256>::PER_SM); }
+// Query rows of a unit, of `rows` a KV head: 8 where that is all or, at D = 256, where 16 would leave an SM one CTA's
+// registers; else 16, which read a key and value once.
+int seg_unit_rows(long long rows, int D) { return rows <= 8 || D == 256 ? 8 : 16; }
 
-long long seg_partial_bytes(long long slots, int D) { return slots * 16 * (D * 4ll + 8); }
+// CTAs of seg_kernel: as many as run at once.
+int seg_ctas(int ru, int D, int sms) {
+  const int per_sm = ru == 8 ? (D == 64 ? SegGeo<64, 1>::PER_SM : D == 128 ? SegGeo<128, 1>::PER_SM : SegGeo<256, 1>::PER_SM)
+                             : (D == 64 ? SegGeo<64, 2>::PER_SM : SegGeo<128, 2>::PER_SM);
+  return sms * per_sm;
+}
+
+long long seg_partial_bytes(long long slots, int ru, int D) { return slots * ru * (D * 4ll + 8); }
 
 void seg_partials(SegParams& p, void* workspace, long long slots, int D) {
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + slots * 16 * D);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + slots * p.ru * D);
 }
 
 // Tokens that a paged cache of a sequence can hold (what the sizes allow, max_seq_len at most).
@@ -67,11 +75,17 @@ int launch_clusters(void (*kern)(P), unsigned grid, unsigned threads, size_t sme
   return DA_OK;
 }
 
+template <int D, bool PAGED, int KIND, int NT>
+int launch_seg_nt(const SegParams& p, cudaStream_t st) {
+  using Gm = SegGeo<D, NT>;
+  if (int e = allow_smem<seg_kernel<D, PAGED, KIND, NT>>(Gm::SMEM)) return e;
+  return launch_dependent(seg_kernel<D, PAGED, KIND, NT>, (unsigned)p.ctas, Gm::THREADS, Gm::SMEM, st, p);
+}
 template <int D, bool PAGED, int KIND>
 int launch_seg(const SegParams& p, cudaStream_t st) {
-  using Gm = SegGeo<D>;
-  if (int e = allow_smem<seg_kernel<D, PAGED, KIND>>(Gm::SMEM)) return e;
-  return launch_dependent(seg_kernel<D, PAGED, KIND>, (unsigned)p.ctas, Gm::THREADS, Gm::SMEM, st, p);
+  if constexpr (D != 256)
+    if (p.ru == 16) return launch_seg_nt<D, PAGED, KIND, 2>(p, st);
+  return launch_seg_nt<D, PAGED, KIND, 1>(p, st);
 }
 
 }  // namespace

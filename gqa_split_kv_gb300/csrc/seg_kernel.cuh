@@ -1,12 +1,20 @@
 // Attention of query rows over lists of cached tokens, for few rows a KV head: the tokens
 // [base, L) of a sequence, the first base tokens that a batch shares, or the blocks that
-// were selected for a query.  16 rows at a time on the warp-level MMA, as the tokens' bytes
-// bound it: a CTA reads each key and value once for its 16 rows.
+// were selected for a query.  The tokens' bytes should bound it, so a CTA reads each key and
+// value once for its 8 or 16 rows.
+//
+// The warp-level MMA of this card gives 256 products a cycle and SM (a 16 x 8 x 16 step every
+// 32 cycles a scheduler, measured), a sixteenth of tcgen05's, and would bound it first if its 16
+// rows were the queries, of which a group has 4 to 8.  So the tokens are its 16 rows and the
+// queries its 8 columns:
+//     S^T = K Q^T (16 tokens x 8 rows),   O^T += V^T P^T (D x 8 rows),
+// D / 8 steps for 16 tokens and 8 rows, 1 KB of keys and values a 1024 / D steps; P^T is S^T's
+// accumulator, transposed 8 x 8 at a time.
 //
 // The 4 warps of a CTA take 16 tokens each of every tile of 64 and run on their own, with
-// no barrier between them: a warp looks up where its tokens lie one tile ahead, copies
-// their rows into its own ring (cp.async; rows that do not exist are zeros there), and keeps
-// a running maximum m, sum l and output O of its tokens,
+// no barrier between them: a warp looks up where its tokens lie two tiles ahead, copies
+// their rows into its own ring (cp.async; rows that do not exist are zeros there), keys and
+// values of 16 tokens in turn, and keeps a running maximum m, sum l and output O of its tokens,
 //     O = sum_t 2^(s_t - m) v_t,   l = sum_t 2^(s_t - m),   s_t = scale log2(e) <q, k_t>.
 // Where a unit ends (seg_plan.cuh) the warps' four (m, l, O) are joined through shared memory
 // and written as one partial, or as the output where the CTA had the whole unit.  m is only
@@ -32,7 +40,7 @@ __device__ __forceinline__ uint32_t float_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSegLens = 1024;  // lengths that a CTA copies to its shared memory
+constexpr int kSegLens = 512;  // lengths that a CTA copies to its shared memory
 
 enum SegKind { kSegRange = 0, kSegBlocks = 1 };
 
@@ -44,9 +52,9 @@ struct SegParams {
   const int *page_table, *prefix_table;
   const int* blocks;           // [B, n, Hkv, pick]
   __nv_bfloat16* out;          // like q
-  float* part_o;               // [slots][16][D]; slots: seg_plan.cuh's, of blocks 2 c + 1 for the piece of CTA c that
+  float* part_o;               // [slots][ru][D]; slots: seg_plan.cuh's, of blocks 2 c + 1 for the piece of CTA c that
                                // starts a unit, 2 c for one that goes on with it
-  float2* part_ml;             // [slots][16]: m, l
+  float2* part_ml;             // [slots][ru]: m, l
   const float* tc_o;           // [slabs][Hkv][B n G][D]: the prefix's partials, where another kernel made them
   const float2* tc_ml;
   int slabs;
@@ -56,7 +64,8 @@ struct SegParams {
   int ctx;
   int page_size, max_pages, num_pages;
   int block, pick;
-  int rt, rt_prefix;           // tiles of 16 query rows a sequence's KV head, and of the prefix's (0: none here)
+  int ru;                      // query rows of a unit: 8 or 16
+  int rt, rt_prefix;           // units a sequence's KV head (rows over ru), and of the prefix's (0: none here)
   int ctas;                    // of seg_kernel: the plan's n
   int beside;                  // the kernel before is the prefix's: seg_kernel runs beside it and waits for it at its end
   float scale_log2;
@@ -68,19 +77,20 @@ struct FoldRow {
   long long out;
 };
 
-template <int D>
+template <int D, int NT>
 struct SegGeo {
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
+  static constexpr int ROWS = 8 * NT;           // query rows of a unit
   static constexpr int ROWB = 2 * D;            // a row of K or V
-  static constexpr int STAGE = 2 * 16 * ROWB;   // 16 tokens of both; also 16 rows of O in fp32
-  static constexpr int NSTAGE = D == 64 ? 6 : 3;
-  static constexpr int WARP_BYTES = NSTAGE * STAGE;
+  static constexpr int GRAN = 16 * ROWB;        // 16 tokens of one of them; also 8 rows of O in fp32
+  static constexpr int NG = D == 64 ? 5 : 3;    // of them in a warp's ring
+  static constexpr int WARP_BYTES = NG * GRAN;
   static constexpr int OFF_ML = WARPS * WARP_BYTES;
-  static constexpr int OFF_FOLD = OFF_ML + WARPS * 16 * 8;
-  static constexpr int OFF_MASK = OFF_FOLD + 16 * (int)sizeof(FoldRow);
-  static constexpr int OFF_LENS = OFF_MASK + WARPS * NSTAGE * 4;
+  static constexpr int OFF_FOLD = OFF_ML + WARPS * ROWS * 8;
+  static constexpr int OFF_MASK = OFF_FOLD + ROWS * (int)sizeof(FoldRow);
+  static constexpr int OFF_LENS = OFF_MASK + WARPS * 4 * 4;
   static constexpr int SMEM = OFF_LENS + kSegLens * 4;
-  static constexpr int PER_SM = D == 256 ? 1 : 2;
+  static constexpr int PER_SM = D == 256 ? 2 : NT == 1 ? 4 : 3;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -114,7 +124,7 @@ __device__ __forceinline__ const int* seg_stage_lens(const SegParams& p, int* to
   return to;
 }
 
-// A unit: 16 query rows (from row 16 r of its rows) of KV head h, and its tokens.
+// A unit: ru query rows (from row ru r of its rows) of KV head h, and its tokens.
 struct SegUnit {
   int b, i, h, r;
   int prefix;  // rows of the whole batch, over the shared prefix
@@ -274,7 +284,7 @@ __device__ __forceinline__ long long seg_row(const SegParams& p, const SegUnit& 
 template <int KIND>
 __device__ __forceinline__ bool seg_query(const SegParams& p, const int* lens, const SegUnit& u, int rr, int& token, int& g,
                                           int& lim) {
-  const int row = u.r * 16 + rr;
+  const int row = u.r * p.ru + rr;
   if constexpr (KIND == kSegBlocks) {
     token = u.b * p.n + u.i;
     g = row;
@@ -294,14 +304,22 @@ __device__ __forceinline__ bool seg_query(const SegParams& p, const int* lens, c
   }
 }
 
-template <int D, bool PAGED, int KIND>
-__global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_kernel(const __grid_constant__ SegParams p) {
-  using Gm = SegGeo<D>;
+// An 8 x 8 matrix of 16-bit elements, lane l holding row l / 4, columns 2 (l % 4) and the next: its transpose.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, bool PAGED, int KIND, int NT>
+__global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
+    seg_kernel(const __grid_constant__ SegParams p) {
+  using Gm = SegGeo<D, NT>;
+  constexpr int NG = Gm::NG;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ring = smem + warp * Gm::WARP_BYTES;
-  const uint32_t ring_s = smem_u32(ring);
-  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * Gm::NSTAGE;
+  const uint32_t ring_s = smem_u32(smem + warp * Gm::WARP_BYTES);
+  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * 4;
 
   // Beside the prefix's kernel there is nothing to wait for: it has written nothing that is read
   // here, and lets this kernel start after its own wait for what came before.  The kernels after this
@@ -315,53 +333,56 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
     return;
   }
 
-  // the load side: where the rows of the next copy lie (lanes 0 .. 15), and of the one after it;
-  // lu and lj are the unit and tile of the latter
+  // the load side: where the rows of the next tile to copy lie (lanes 0 .. 15), and of the one after
+  // it; lu and lj are the unit and tile of the latter
   int lj;
   SegUnit lu = walk.at(x0, lj);
   const SegUnit u0 = lu;
   const int start = lj;
-  long long lx = x0;  // the next copy's tile
+  long long lx = x0;
+  long long off, off_next = -1;
   auto look_up = [&]() {
     return lane < 16 ? seg_row<D, PAGED, KIND>(p, lu, lj * kTile + warp * 16 + lane) : -1ll;
   };
-  auto advance = [&](long long x) {  // to tile x, the one after lu's and lj's; none past the last
-    if (x >= x1) return;
-    if (++lj == lu.tiles) {
-      lu = walk.next(lu);
-      lj = 0;
-    }
-  };
-  long long off = look_up(), off_next = -1;
-  advance(x0 + 1);
-  if (x0 + 1 < x1) off_next = look_up();
-  auto issue = [&](int stage) {
+  off = look_up();
+  int ls = 0;       // the next granule's slot
+  bool lv = false;  // it is of values
+  bool ahead = false;  // off_next holds the tile after lx
+  auto issue = [&]() {
     if (lx < x1) {
-      const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
-      if (lane == 0) masks[stage] = live;
-      if (live) {
-        const uint32_t dst = ring_s + stage * Gm::STAGE;
-        const __nv_bfloat16 *kb = p.k, *vb = p.v;
-        if (!PAGED && KIND == kSegRange && lx < walk.prefix_tiles()) {
-          kb = p.kp;
-          vb = p.vp;
+      if (!ahead) {  // (once a tile, with its keys)
+        ahead = true;
+        off_next = -1;
+        if (lx + 1 < x1) {
+          if (++lj == lu.tiles) {
+            lu = walk.next(lu);
+            lj = 0;
+          }
+          off_next = look_up();
         }
+      }
+      const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
+      if (!lv && lane == 0) masks[(int)(lx & 3)] = live;
+      if (live) {
+        const uint32_t dst = ring_s + ls * Gm::GRAN;
+        const __nv_bfloat16* from = lv ? p.v : p.k;
+        if (!PAGED && KIND == kSegRange && lx < walk.prefix_tiles()) from = lv ? p.vp : p.kp;
         constexpr int CH = D / 8, RPP = 32 / (CH < 32 ? CH : 32);  // chunks a row, rows a pass
         const int c = lane % CH, r0 = lane / CH;
 #pragma unroll
         for (int r = 0; r < 16; r += RPP) {
           const int row = r + r0;
           const long long o = __shfl_sync(0xffffffffu, off, row);
-          const size_t e = (size_t)(o < 0 ? 0 : o) + c * 8;
-          const uint32_t d = dst + row * Gm::ROWB + ((c ^ (row & 7)) << 4);
-          cp_async16(d, kb + e, o >= 0);
-          cp_async16(d + 16 * Gm::ROWB, vb + e, o >= 0);
+          cp_async16(dst + row * Gm::ROWB + ((c ^ (row & 7)) << 4), from + (o < 0 ? 0 : o) + c * 8, o >= 0);
         }
       }
-      ++lx;
-      off = off_next;
-      advance(lx + 1);
-      if (lx + 1 < x1) off_next = look_up();
+      if (lv) {
+        ++lx;
+        off = off_next;
+        ahead = false;
+      }
+      lv = !lv;
+      ls = ls + 1 == NG ? 0 : ls + 1;
     }
     cp_async_commit();
   };
@@ -369,136 +390,168 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
   int j = start;
   SegUnit u = u0;
 #pragma unroll 1
-  for (int s = 0; s < Gm::NSTAGE; ++s) issue(s);
+  for (int s = 0; s < NG; ++s) issue();
 
-  uint32_t qa[D / 16][4];
-  float o[D / 8][4];
-  float m[2], l[2];
-  int lim[2];
+  // column n of an MMA is the unit's row 8 nt + n; this lane's columns are 2 (lane % 4) and the next
+  uint32_t qb[NT][D / 16][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+  int lim[NT][2];
   int j0 = j;
   bool fresh = true;
-  int stage = 0;
+  int slot_at = 0;  // of the granule that is read next
   for (long long x = x0; x < x1; ++x) {
     if (fresh) {  // a new unit: its queries
       fresh = false;
       j0 = j;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        int token, g;
-        const bool is = seg_query<KIND>(p, walk.lens, u, lane / 4 + 8 * hf, token, g, lim[hf]);
+      for (int nt = 0; nt < NT; ++nt) {
+        int token, g, unused;
+        const bool is = seg_query<KIND>(p, walk.lens, u, 8 * nt + lane / 4, token, g, unused);
         const uint32_t* src =
             reinterpret_cast<const uint32_t*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D) + lane % 4;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          qa[kk][hf] = is ? load_dependent(src + 8 * kk) : 0u;
-          qa[kk][2 + hf] = is ? load_dependent(src + 8 * kk + 4) : 0u;
+          qb[nt][kk][0] = is ? load_dependent(src + 8 * kk) : 0u;
+          qb[nt][kk][1] = is ? load_dependent(src + 8 * kk + 4) : 0u;
+          o[nt][kk][0] = o[nt][kk][1] = o[nt][kk][2] = o[nt][kk][3] = 0.f;
         }
-        m[hf] = kNegInf;
-        l[hf] = 0.f;
-      }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] = kNegInf;
+          l[nt][e] = 0.f;
+          if (KIND == kSegRange) seg_query<KIND>(p, walk.lens, u, 8 * nt + 2 * (lane % 4) + e, token, g, lim[nt][e]);
+        }
+      }
     }
-    cp_async_wait<Gm::NSTAGE - 1>();
+    const bool last = j + 1 == u.tiles, join = last || x + 1 == x1;
+    const uint32_t kst = ring_s + slot_at * Gm::GRAN;
+    const int k_slot = slot_at;
+    slot_at = slot_at + 1 == NG ? 0 : slot_at + 1;
+    cp_async_wait<NG - 1>();
     __syncwarp();
-    const uint32_t live = masks[stage];
+    const uint32_t live = masks[(int)(x & 3)];
+    const int mrow = lane & 7, mi = lane >> 3;
+    uint32_t pb[NT][2];
     if (live) {
-      const uint32_t kst = ring_s + stage * Gm::STAGE, vst = kst + 16 * Gm::ROWB;
-      const int mrow = lane & 7, mi = lane >> 3;
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t r0, r1, r2, r3;
-        const int row = (mi >> 1) * 8 + mrow, c = 2 * kk + (mi & 1);
-        ldsm_x4(kst + row * Gm::ROWB + ((c ^ mrow) << 4), r0, r1, r2, r3);
-        mma_bf16_16816(s[0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], r0, r1);
-        mma_bf16_16816(s[1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], r2, r3);
+        uint32_t a0, a1, a2, a3;  // tokens 0 .. 7 and 8 .. 15 of the first 8 elements, then of the second
+        const int row = lane & 15, c = 2 * kk + (lane >> 4);
+        ldsm_x4(kst + row * Gm::ROWB + ((c ^ mrow) << 4), a0, a1, a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[nt], a0, a1, a2, a3, qb[nt][kk][0], qb[nt][kk][1]);
       }
-      const int t0 = (KIND == kSegRange && !u.prefix ? p.base : 0) + j * kTile + warp * 16;
-      float mx[2] = {kNegInf, kNegInf};
+      const int t0 = (KIND == kSegRange && !u.prefix ? p.base : 0) + j * kTile + warp * 16 + lane / 4;
+      float mx[NT][2];
+      bool any = false;
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = nt * 8 + 2 * (lane % 4) + (e & 1);
-          bool see = (live >> col) & 1;
-          if (KIND == kSegRange) see = see && t0 + col < lim[e >> 1];
-          s[nt][e] = see ? s[nt][e] * p.scale_log2 : kNegInf;
-          mx[e >> 1] = fmaxf(mx[e >> 1], s[nt][e]);
-        }
-      float mu[2];
-      bool raise[2];
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
-        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
-        raise[hf] = mx[hf] > m[hf] + 8.f;
-      }
-      if (__any_sync(0xffffffffu, raise[0] || raise[1])) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float to = raise[hf] ? mx[hf] : m[hf];
-          const float alpha = raise[hf] ? exp2_approx(m[hf] - to) : 1.f;  // 0 from -inf
-          m[hf] = to;
-          l[hf] *= alpha;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][2 * hf] *= alpha;
-            o[i][2 * hf + 1] *= alpha;
+          for (int hf = 0; hf < 2; ++hf) {
+            bool see = (live >> (lane / 4 + 8 * hf)) & 1;
+            if (KIND == kSegRange) see = see && t0 + 8 * hf < lim[nt][e];
+            s[nt][2 * hf + e] = see ? s[nt][2 * hf + e] * p.scale_log2 : kNegInf;
           }
+          float t = fmaxf(s[nt][e], s[nt][2 + e]);
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          mx[nt][e] = t;
+          any = any || t > m[nt][e] + 8.f;
         }
+      if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool raise = mx[nt][e] > m[nt][e] + 8.f;
+            const float to = raise ? mx[nt][e] : m[nt][e];
+            const float alpha = raise ? exp2_approx(m[nt][e] - to) : 1.f;  // 0 from -inf
+            m[nt][e] = to;
+            l[nt][e] *= alpha;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[nt][i][e] *= alpha;
+              o[nt][i][2 + e] *= alpha;
+            }
+          }
       }
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        mu[hf] = m[hf] == kNegInf ? 0.f : m[hf];
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          s[nt][2 * hf] = exp2_approx(s[nt][2 * hf] - mu[hf]);
-          s[nt][2 * hf + 1] = exp2_approx(s[nt][2 * hf + 1] - mu[hf]);
-          l[hf] += s[nt][2 * hf] + s[nt][2 * hf + 1];
+        for (int e = 0; e < 2; ++e) {
+          const float mu = m[nt][e] == kNegInf ? 0.f : m[nt][e];
+          s[nt][e] = exp2_approx(s[nt][e] - mu);
+          s[nt][2 + e] = exp2_approx(s[nt][2 + e] - mu);
+          l[nt][e] += s[nt][e] + s[nt][2 + e];
         }
-      }
-      // the weights go into the product as bf16 (2^-9 of each, against the output's own 2^-9)
-      const uint32_t a0 = pack_bf16x2(s[0][0], s[0][1]), a1 = pack_bf16x2(s[0][2], s[0][3]),
-                     a2 = pack_bf16x2(s[1][0], s[1][1]), a3 = pack_bf16x2(s[1][2], s[1][3]);
-#pragma unroll
-      for (int nn = 0; nn < D / 16; ++nn) {
-        uint32_t r0, r1, r2, r3;
-        const int row = (mi & 1) * 8 + mrow, c = 2 * nn + (mi >> 1);
-        ldsm_x4_t(vst + row * Gm::ROWB + ((c ^ mrow) << 4), r0, r1, r2, r3);
-        mma_bf16_16816(o[2 * nn], a0, a1, a2, a3, r0, r1);
-        mma_bf16_16816(o[2 * nn + 1], a0, a1, a2, a3, r2, r3);
+        // the weights go into the product as bf16 (2^-8 of each at most, as the output's own rounding)
+        pb[nt][0] = transpose8x8(pack_bf16x2(s[nt][0], s[nt][1]));
+        pb[nt][1] = transpose8x8(pack_bf16x2(s[nt][2], s[nt][3]));
       }
     }
-    const bool last = j + 1 == u.tiles;
-    if (last || x + 1 == x1) {
-      // join the warps: each leaves its O in the ring slot that it has just read
+    // the keys' place is free, unless the warps are joined now
+    __syncwarp();
+    if (!join) issue();
+    const uint32_t vst = ring_s + slot_at * Gm::GRAN;
+    const int v_slot = slot_at;
+    slot_at = slot_at + 1 == NG ? 0 : slot_at + 1;
+    if (join)
+      cp_async_wait<NG - 2>();
+    else
+      cp_async_wait<NG - 1>();
+    __syncwarp();
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t a0, a1, a2, a3;  // elements 0 .. 7 and 8 .. 15 of tokens 0 .. 7, then of 8 .. 15
+        const int row = (mi >> 1) * 8 + mrow, c = 2 * i + (mi & 1);
+        ldsm_x4_t(vst + row * Gm::ROWB + ((c ^ mrow) << 4), a0, a1, a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[nt][i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+    __syncwarp();
+    if (join) {
+      // join the warps: each leaves 8 rows of its O in the places of the values (and the keys) that it has read
       float2* ml = reinterpret_cast<float2*>(smem + Gm::OFF_ML);
-      __syncwarp();
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-        const int r = lane / 4 + 8 * hf;
-        if (lane % 4 == 0) ml[warp * 16 + r] = make_float2(m[hf], l[hf]);
-        float* dst = reinterpret_cast<float*>(ring + stage * Gm::STAGE) + r * D;
+      for (int nt = 0; nt < NT; ++nt) {
+        float* dst = reinterpret_cast<float*>(smem + warp * Gm::WARP_BYTES + (nt == 0 ? v_slot : k_slot) * Gm::GRAN);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<float2*>(dst + ((8 * i + 2 * (lane % 4)) ^ ((r & 3) << 3))) =
-              make_float2(o[i][2 * hf], o[i][2 * hf + 1]);
+        for (int e = 0; e < 2; ++e) {
+          float t = l[nt][e];
+          t += __shfl_xor_sync(0xffffffffu, t, 4);
+          t += __shfl_xor_sync(0xffffffffu, t, 8);
+          t += __shfl_xor_sync(0xffffffffu, t, 16);
+          const int n = 2 * (lane % 4) + e;
+          if (lane < 4) ml[warp * Gm::ROWS + 8 * nt + n] = make_float2(m[nt][e], t);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int d = 16 * i + lane / 4;
+            dst[n * D + (d ^ ((lane % 4) << 3))] = o[nt][i][e];
+            dst[n * D + ((d + 8) ^ ((lane % 4) << 3))] = o[nt][i][2 + e];
+          }
+        }
       }
       __syncthreads();
       const bool whole = KIND == kSegBlocks && last && j0 == 0;
       const size_t slot = KIND == kSegBlocks ? 2 * (size_t)blockIdx.x + (j0 == 0) : (size_t)u.id + blockIdx.x;
       // each row's factors of the warps' O, and where it goes
       FoldRow* fold = reinterpret_cast<FoldRow*>(smem + Gm::OFF_FOLD);
-      if (threadIdx.x < 16) {
+      if (threadIdx.x < Gm::ROWS) {
         const int r = threadIdx.x;
         int token, g, unused;
         float mw[Gm::WARPS], lw[Gm::WARPS], M = kNegInf, L = 0.f;
 #pragma unroll
         for (int w = 0; w < Gm::WARPS; ++w) {
-          const float2 y = ml[w * 16 + r];
+          const float2 y = ml[w * Gm::ROWS + r];
           mw[w] = y.x;
           lw[w] = y.y;
           M = fmaxf(M, y.x);
@@ -516,21 +569,22 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
 #pragma unroll
           for (int w = 0; w < Gm::WARPS; ++w) f.f[w] *= inv;
         } else if (f.out >= 0) {
-          p.part_ml[slot * 16 + r] = make_float2(M, L);
+          p.part_ml[slot * Gm::ROWS + r] = make_float2(M, L);
         }
         fold[r] = f;
       }
       __syncthreads();
-#pragma unroll 4
-      for (int e = threadIdx.x; e < 16 * (D / 4); e += Gm::THREADS) {
-        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+#pragma unroll 2
+      for (int e = threadIdx.x; e < Gm::ROWS * (D / 4); e += Gm::THREADS) {
+        const int r = e / (D / 4), n = r % 8, c = (e % (D / 4)) * 4;
         const FoldRow f = fold[r];
         if (f.out < 0) break;
+        const uint8_t* from = smem + (r < 8 ? v_slot : k_slot) * Gm::GRAN;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < Gm::WARPS; ++w) {
-          const float4 y = *reinterpret_cast<const float4*>(
-              reinterpret_cast<const float*>(smem + w * Gm::WARP_BYTES + stage * Gm::STAGE) + r * D + (c ^ ((r & 3) << 3)));
+          const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(from + w * Gm::WARP_BYTES) +
+                                                            n * D + (c ^ ((n >> 1) << 3)));
           if (f.f[w] == 0.f) continue;
           a.x += f.f[w] * y.x;
           a.y += f.f[w] * y.y;
@@ -540,12 +594,12 @@ __global__ void __launch_bounds__(SegGeo<D>::THREADS, SegGeo<D>::PER_SM) seg_ker
         if (whole)
           *reinterpret_cast<uint2*>(p.out + f.out + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
         else
-          *reinterpret_cast<float4*>(p.part_o + (slot * 16 + r) * D + c) = a;
+          *reinterpret_cast<float4*>(p.part_o + (slot * Gm::ROWS + r) * D + c) = a;
       }
       __syncthreads();
+      issue();
     }
-    issue(stage);
-    stage = stage + 1 == Gm::NSTAGE ? 0 : stage + 1;
+    issue();
     ++j;
     if (last && x + 1 < x1) {
       u = walk.next(u);
@@ -667,12 +721,12 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const _
   const int head = token * p.G + g;  // among the rows of the head
   int na = p.slabs, id0 = 0, c0 = 0;
   if (!p.slabs && p.rt_prefix && tp > 0) {
-    id0 = h * p.rt_prefix + head / 16;
+    id0 = h * p.rt_prefix + head / p.ru;
     c0 = seg_owner(W, used, id0 * tp);
     na = seg_owner(W, used, (id0 + 1) * tp - 1) - c0 + 1;
   }
   // the rest's
-  const int rr = i * p.G + g, r = rr / 16, t = seg_tiles(seg_len(p.seq_lens, b, p.cap), p.cap, p.base);
+  const int rr = i * p.G + g, r = rr / p.ru, t = seg_tiles(seg_len(p.seq_lens, b, p.cap), p.cap, p.base);
   const long long a1 = wp + sums.before * p.Hkv * p.rt + (long long)(h * p.rt + r) * t;
   const int id1 = p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r;
   const int c1 = t ? seg_owner(W, used, a1) : 0, nb = t ? seg_owner(W, used, a1 + t - 1) - c1 + 1 : 0;
@@ -683,7 +737,7 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const _
       ml = p.tc_ml + at;
       o = p.tc_o + at * D;
     } else {
-      const long long at = k < na ? ((long long)id0 + c0 + k) * 16 + head % 16 : ((long long)id1 + c1 + k - na) * 16 + rr % 16;
+      const long long at = k < na ? ((long long)id0 + c0 + k) * p.ru + head % p.ru : ((long long)id1 + c1 + k - na) * p.ru + rr % p.ru;
       ml = p.part_ml + at;
       o = p.part_o + at * D;
     }
@@ -700,12 +754,12 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_blocks_kernel(const _
   const long long x = seg_start(W, p.ctas, blockIdx.x + 1), id = seg_div(x, tp);
   if (x >= W || x == id * tp || seg_start(W, p.ctas, blockIdx.x) > id * tp) return;
   const int c0 = blockIdx.x, c1 = seg_owner(W, p.ctas, (id + 1) * tp - 1);
-  const int r0 = (int)(id % p.rt) * 16, h = (int)(id / p.rt % p.Hkv);
+  const int r0 = (int)(id % p.rt) * p.ru, h = (int)(id / p.rt % p.Hkv);
   const long long token = id / p.rt / p.Hkv;
-  for (int r = threadIdx.x >> 5; r < 16 && r0 + r < p.G; r += kMergeThreads / 32) {
+  for (int r = threadIdx.x >> 5; r < p.ru && r0 + r < p.G; r += kMergeThreads / 32) {
     SegRow<D> acc;
     acc.add(c1 - c0 + 1, [&](int k, const float2*& ml, const float*& o) {
-      const long long at = (2ll * (c0 + k) + (k == 0)) * 16 + r;
+      const long long at = (2ll * (c0 + k) + (k == 0)) * p.ru + r;
       ml = p.part_ml + at;
       o = p.part_o + at * D;
     });

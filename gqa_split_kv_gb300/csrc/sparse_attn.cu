@@ -82,7 +82,11 @@ int check_heads(int B, int n, int Hq, int Hkv, int D) {
 
 // ---------------------------------------------------------------- attention
 
-long long sparse_bytes(int D, int sms) { return seg_partial_bytes(2ll * seg_ctas(D, sms), D); }
+long long sparse_bytes(int D, int sms) {
+  const long long few = seg_partial_bytes(2ll * seg_ctas(8, D, sms), 8, D);
+  const long long many = D == 256 ? 0 : seg_partial_bytes(2ll * seg_ctas(16, D, sms), 16, D);
+  return few > many ? few : many;
+}
 
 struct SparseCall {
   SegParams p;
@@ -125,10 +129,11 @@ int sparse_call(SparseCall& c, float scale, cudaStream_t st) {
   const long long need = sparse_bytes(c.D, sms);
   if (!c.workspace || !aligned(c.workspace, 16) || c.workspace_bytes < need) return DA_ERR_WORKSPACE;
   if (overlap(c.workspace, need, p.out, on)) return DA_ERR_INVALID_ARG;
-  p.rt = (p.G + 15) / 16;
+  p.ru = seg_unit_rows(p.G, c.D);
+  p.rt = (p.G + p.ru - 1) / p.ru;
   const long long units = product(p.B, p.n, p.Hkv, p.rt), tiles = units * ((p.pick * p.block + kTile - 1) / kTile);
   if (units > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
-  p.ctas = (int)(tiles < seg_ctas(c.D, sms) ? tiles : seg_ctas(c.D, sms));
+  p.ctas = (int)(tiles < seg_ctas(p.ru, c.D, sms) ? tiles : seg_ctas(p.ru, c.D, sms));
   seg_partials(p, c.workspace, 2ll * p.ctas, c.D);
   p.scale_log2 = scale * 1.4426950408889634f;
   return c.D == 64 ? launch_sparse<64>(c, st) : c.D == 128 ? launch_sparse<128>(c, st) : launch_sparse<256>(c, st);
