@@ -29,12 +29,14 @@ struct MeansParams {
   int touched;  // blocks a sequence, at most
   int shares;   // CTAs a block; a share is at most kMeansThreads chunks
 };
-constexpr int kMeansThreads = 256;
+constexpr int kMeansThreads = 256, kMeansTokens = 256;
 
 template <bool PAGED>
 __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const __grid_constant__ MeansParams p) {
-  __shared__ float sums[kMeansThreads * 9];  // [group][chunk][8], a chunk 9 apart
+  __shared__ float sums[kMeansThreads * 9];     // [group][chunk][8], a chunk 9 apart
+  __shared__ unsigned s_row[kMeansTokens];      // where the block's tokens lie, 256 at a time
   pdl_wait_primary();
+  pdl_launch_dependents();
   const int share = blockIdx.x % p.shares;
   const long long bj = blockIdx.x / p.shares;
   const int b = (int)(bj / p.touched);
@@ -47,36 +49,48 @@ __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const __grid
   const int c0 = share * per, here = min(per, chunks - c0);
   if (here <= 0) return;
   const int groups = kMeansThreads / here, g = threadIdx.x / here, c = threadIdx.x - g * here;
+  const uint4* keys = reinterpret_cast<const uint4*>(p.k) + (PAGED ? 0 : ((size_t)b * p.ctx + t0) * chunks) + c0 + c;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (g < groups) {
-#pragma unroll 8
-    for (int i = g; i < count; i += groups) {
-      const int t = (int)t0 + i;
-      size_t row;
-      if constexpr (PAGED) {
-        const int col = t / p.page_size;
+  for (int i0 = 0; i0 < count; i0 += kMeansTokens) {
+    const int n = min(kMeansTokens, count - i0);
+    if constexpr (PAGED) {
+      __syncthreads();
+      if (threadIdx.x < n) {
+        const int t = (int)t0 + i0 + threadIdx.x, col = t / p.page_size;
         int page = load_dependent(p.page_table + (size_t)b * p.max_pages + col);
         if ((unsigned)page >= (unsigned)p.num_pages) {
           atomicOr(&g_error_word, 4u);
           page = 0;
         }
-        row = (size_t)page * p.page_size + (t - col * p.page_size);
-      } else {
-        row = (size_t)b * p.ctx + t;
+        s_row[threadIdx.x] = (unsigned)(page * (long long)p.page_size + (t - col * p.page_size));
       }
-      const uint4 w = load_dependent(reinterpret_cast<const uint4*>(p.k) + row * chunks + c0 + c);
-      s[0] += bf16lo_to_f32(w.x);
-      s[1] += bf16hi_to_f32(w.x);
-      s[2] += bf16lo_to_f32(w.y);
-      s[3] += bf16hi_to_f32(w.y);
-      s[4] += bf16lo_to_f32(w.z);
-      s[5] += bf16hi_to_f32(w.z);
-      s[6] += bf16lo_to_f32(w.w);
-      s[7] += bf16hi_to_f32(w.w);
+      __syncthreads();
     }
+    if (g >= groups) continue;
+    constexpr int U = 8;  // loads of a thread in flight
+    for (int i = g; i < n; i += U * groups) {
+      uint4 w[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int at = i + k * groups;
+        w[k] = at < n ? load_dependent(keys + (size_t)(PAGED ? s_row[at] : i0 + at) * chunks) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        s[0] += bf16lo_to_f32(w[k].x);
+        s[1] += bf16hi_to_f32(w[k].x);
+        s[2] += bf16lo_to_f32(w[k].y);
+        s[3] += bf16hi_to_f32(w[k].y);
+        s[4] += bf16lo_to_f32(w[k].z);
+        s[5] += bf16hi_to_f32(w[k].z);
+        s[6] += bf16lo_to_f32(w[k].w);
+        s[7] += bf16hi_to_f32(w[k].w);
+      }
+    }
+  }
+  if (g < groups)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[threadIdx.x * 9 + e] = s[e];
-  }
   __syncthreads();
   if (g > 0) return;
   for (int o = 1; o < groups; ++o)

@@ -24,7 +24,7 @@ int means_call(MeansParams& p, bool paged, long long cap, cudaStream_t st) {
     return DA_ERR_INVALID_ARG;
   if (p.D % 8 || p.D > 1024 || p.Hkv > 1024 || cap > 0x7fffffffLL - p.block) return DA_ERR_UNSUPPORTED;
   if (paged && (p.page_size <= 0 || p.max_pages < 0 || p.num_pages < 0)) return DA_ERR_INVALID_ARG;
-  if (p.block > 65536) return DA_ERR_UNSUPPORTED;
+  if (p.block > 65536 || (paged && product(p.num_pages, p.page_size) > 0xffffffffLL)) return DA_ERR_UNSUPPORTED;
   // tokens past the last block have no mean
   if (cap > (long long)p.max_blocks * p.block) return DA_ERR_INVALID_ARG;
   if (p.B == 0 || p.n == 0 || cap == 0 || (paged && p.num_pages == 0)) return DA_OK;
