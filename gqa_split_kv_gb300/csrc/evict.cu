@@ -232,7 +232,7 @@ int evict_call(EvictParams& p, bool paged, bool int8, int head_dim, long long ca
     while (p.parts < 64 && (long long)units * tensors * p.parts < 8LL * sms && p.keep / (2 * p.parts) * chunks >= kMoveThreads)
       p.parts *= 2;
   }
-  const long long grid = (long long)units * (tensors * p.columns * p.parts + 1);
+  const long long grid = (long long)units * (tensors * p.columns * p.parts + 3);
   if (grid > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // a cluster where there are SMs for it and 1024 weights a CTA

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   extern __shared__ uint32_t s_keys[];
   constexpr int WARPS = kEvictThreads / 32;
   __shared__ int hist[2048], total[2048];  // this CTA's counts; the cluster's (CTA 0)
-  __shared__ int s_warp[WARPS], s_warp_same[WARPS], s_zero, s_digit, s_above, s_done;
+  __shared__ int s_warp[WARPS], s_warp_same[WARPS], s_digit[3], s_above[3], s_done[3];
   __shared__ int s_kept[8], s_same[8];  // of every CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
@@ -66,7 +66,6 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
       __syncthreads();
   };
   for (int i = threadIdx.x; i < 2048; i += kEvictThreads) hist[i] = total[i] = 0;
-  if (threadIdx.x == 0) s_zero = 0;
   pdl_wait_primary();
   pdl_launch_dependents();
   const int unit = blockIdx.x / p.cluster, b = unit / p.Hkv, h = unit % p.Hkv;
@@ -151,17 +150,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
           while (before + c[i] < left) before += c[i++];
           const int digit = bins - 1 - (threadIdx.x * per + i), all = before + c[i] == left;  // all of the digit's are kept
           for (int r = 0; r < p.cluster; ++r) {
-            store_at(smem_u32(&s_digit), r, digit);
-            store_at(smem_u32(&s_above), r, before);
-            store_at(smem_u32(&s_done), r, all);
+            store_at(smem_u32(&s_digit[pass]), r, digit);
+            store_at(smem_u32(&s_above[pass]), r, before);
+            store_at(smem_u32(&s_done[pass]), r, all);
           }
         }
       }
       meet();
-      high |= (uint32_t)s_digit << shift;
-      left -= s_above;
-      done = s_done;
-      meet();
+      high |= (uint32_t)s_digit[pass] << shift;
+      left -= s_above[pass];
+      done = s_done[pass];
     }
     // where all keys of the last digit are kept, the border lies below the lowest they can be (which is
     // not 0: as many candidates as are needed are not all of them)
@@ -216,16 +214,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
 
 constexpr int kMoveThreads = 256;
 
-// A CTA moves the rows' columns [c0, c1) of one (sequence, head, tensor), or the scales and
+// A CTA moves the rows' columns [c0, c1) of one (sequence, head, tensor), or the scales or the
 // weights of one (sequence, head).  In place it goes forward in steps: a row moves to its own
 // place or a lower one, so a step's sources lie at or past its targets and past every earlier
-// step's; all of a step are loaded before the first is stored.  Byte traffic bounds it: 16 bytes
-// a thread, 4 of them in flight.
+// step's; all of a step are loaded before the first is stored.  Byte traffic bounds it, and for
+// few rows the chain of kept position, page and row: 16 bytes a thread, 8 of them in flight.
 template <bool PAGED>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p) {
-  constexpr int U = 4;
+  constexpr int U = 8;
   pdl_wait_primary();
-  const int tensors = p.v ? 2 : 1, rolls = tensors * p.columns * p.parts + 1;
+  const int tensors = p.v ? 2 : 1, copies = tensors * p.columns * p.parts, rolls = copies + 3;
   const int unit = blockIdx.x / rolls, role = blockIdx.x % rolls;
   const int b = unit / p.Hkv, h = unit % p.Hkv;
   const int L = seg_len(p.seq_lens, b, p.cap), len = min(L, p.keep);
@@ -242,7 +240,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   };
   const int to_slab = p.in_place ? p.slab : p.out_ctx;
 
-  if (role < rolls - 1) {
+  if (role < copies) {
     const int part = role % p.parts, column = role / p.parts % p.columns;
     const bool is_v = role / p.parts / p.columns;
     const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v : p.k);
@@ -284,10 +282,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     return;
   }
   // numbers: a thread a token
-  for (int a = 0; a < 3; ++a) {
-    const float* src = a == 0 ? p.ks : a == 1 ? p.vs : p.weights;
-    float* dst = a == 0 ? p.ks_out : a == 1 ? p.vs_out : p.weights_out;
-    if (!src || !dst) continue;
+  {
+    const int a = role - copies;
+    const float* src = a == 0 ? p.weights : a == 1 ? p.ks : p.vs;
+    float* dst = a == 0 ? p.weights_out : a == 1 ? p.ks_out : p.vs_out;
+    if (!src || !dst) return;
     for (int i0 = 0; i0 < len; i0 += kMoveThreads * U) {
       float w[U];
       int t[U];
@@ -311,7 +310,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
           if (good) dst[((size_t)d.slab * p.Hkv + h) * to_slab + d.at] = w[k];
         }
     }
-    if (a < 2) continue;
+    if (a > 0) return;
     __syncthreads();
     for (int t = len + threadIdx.x; t < (p.in_place ? L : p.out_ctx); t += kMoveThreads) {
       bool good;
