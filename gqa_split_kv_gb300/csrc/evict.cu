@@ -12,6 +12,7 @@
 #include "seg_host.cuh"
 #include "units.cuh"
 #include "weights_kernel.cuh"
+#include "weights_tc.cuh"
 
 namespace da {
 
@@ -42,7 +43,7 @@ int weights_shape(int B, int n, int Hq, int Hkv, long long cap, int sms, Weights
   if (G > 64 || Hq > 65536 || cap > 0x7fffffffLL - kTile || product(n, G) > kWeightRows || product(B, Hkv) > 0x3fffffffLL)
     return DA_ERR_UNSUPPORTED;
   s->rows = n * G;
-  s->slots = (long long)B * Hkv + 3ll * sms;
+  s->slots = (long long)B * Hkv + 2ll * sms;
   const long long tiles = product(B, Hkv, (cap + kTile - 1) / kTile);
   if (tiles > 1LL << 40) return DA_ERR_UNSUPPORTED;
   s->score = s->rows <= 16 ? tiles * s->rows * kTile * 4 : 0;
@@ -53,7 +54,7 @@ int weights_shape(int B, int n, int Hq, int Hkv, long long cap, int sms, Weights
 template <int D, bool PAGED, bool INT8>
 int launch_scores(WeightsParams w, int sms, cudaStream_t st) {
   if (w.rows <= 16) {
-    using Gm = ScoreGeo<D, INT8, false>;
+    using Gm = ScoreGeo<D, INT8>;
     w.s.ctas = Gm::PER_SM * sms;
     w.finish_ctas = 8 * sms;
     if (int e = allow_smem<weights_score_kernel<D, PAGED, INT8>>(Gm::SMEM)) return e;
@@ -61,11 +62,12 @@ int launch_scores(WeightsParams w, int sms, cudaStream_t st) {
       return e;
     return launch_dependent(weights_finish_kernel<PAGED>, (unsigned)w.finish_ctas, kFinishThreads, 0, st, w);
   }
-  using Gm = ScoreGeo<D, INT8, true>;
+  using Gm = WeightsTcGeo<D>;
   static_assert(Gm::ROWS == kWindowRows, "");
   w.s.ctas = Gm::PER_SM * sms;
-  if (int e = allow_smem<weights_window_kernel<D, PAGED, INT8, false>>(Gm::SMEM)) return e;
-  if (int e = allow_smem<weights_window_kernel<D, PAGED, INT8, true>>(Gm::SMEM)) return e;
+  w.timeout_ns = kWaitTimeoutNs;
+  if (int e = allow_smem<weights_tc_kernel<D, PAGED, INT8, false>>(Gm::SMEM)) return e;
+  if (int e = allow_smem<weights_tc_kernel<D, PAGED, INT8, true>>(Gm::SMEM)) return e;
   const int all = w.rows;
   for (w.row0 = 0; w.row0 < all; w.row0 += kWindowRows) {
     w.rows = all - w.row0 < kWindowRows ? all - w.row0 : kWindowRows;
@@ -73,9 +75,9 @@ int launch_scores(WeightsParams w, int sms, cudaStream_t st) {
       w.prior = w.out;
       w.decay = 1.f;
     }
-    if (int e = launch_dependent(weights_window_kernel<D, PAGED, INT8, false>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
+    if (int e = launch_dependent(weights_tc_kernel<D, PAGED, INT8, false>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
       return e;
-    if (int e = launch_dependent(weights_window_kernel<D, PAGED, INT8, true>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
+    if (int e = launch_dependent(weights_tc_kernel<D, PAGED, INT8, true>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
       return e;
   }
   return DA_OK;

@@ -128,17 +128,19 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
   }
+  // Tensor memory is taken after the wait and before the next kernel may start: none waits for another
+  // while it holds some that the other still has to take.
+  pdl_wait_primary();
   if (warp == 1) {
     tmem_alloc(sbase + Gm::OFF_MISC, Gm::TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait_primary();
-  // the rests' kernel may start as soon as SMs are free: what it reads was written before this
-  // kernel's wait ended, and it waits for this kernel at its end
-  pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // the rests' kernel may start as soon as SMs are free: what it reads was written before this
+  // kernel's wait ended, and it waits for this kernel at its end
+  pdl_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MISC);
   auto wait = [&](int i, int phase) { return wait_bounded(bar(i), (uint32_t)(phase & 1), abort_flag, p.timeout_ns); };
   // granule g of this CTA's tile j: K columns 0 .. NKG - 1, then V

@@ -1,20 +1,15 @@
 // The attention weight that new tokens give each cached token, summed over them and over the
 // heads of a group.  A softmax needs its whole row's maximum and sum before the first weight
-// is known, so there are two kernels, on the warp-level MMA with 16 query rows to a tile:
+// is known, so there are two kernels:
 //
 // up to 16 rows (decode):
-//   weights_score_kernel   reads every key once, writes the scores (64 fp32 a row and tile, a
+//   weights_score_kernel   reads every key once (warp-level MMA), writes the scores (64 fp32 a row and tile, a
 //                          sixteenth of a bf16 key's bytes a row) and each piece's (m, l);
 //   weights_finish_kernel  joins a sequence's (m, l), reads the scores, adds the rows' weights
 //                          in their order and writes decay * prior + sum.
 // A key's bytes bound it: what decode reads without the values.
 //
-// more rows (a window of a prompt), 128 at a time:
-//   weights_window_kernel  twice: once for each piece's (m, l), once for the sums, with the scores
-//                          computed again, as writing and reading 128 fp32 a key costs more than its
-//                          own 128 or 256 bytes and 2 D products a row.  A key is widened to MMA
-//                          fragments once for all rows, whose queries lie in shared memory.
-// Bound by the MMAs (2 x 2 D operations a row and key) and two exponentials a row and key.
+// more rows (a window of a prompt): weights_tc.cuh, 128 at a time.
 //
 // All go along a line of tiles (seg_plan.cuh) of (sequence, KV head).
 #pragma once
@@ -33,22 +28,22 @@ struct WeightsParams {
   int row0;       // the window's first
   int finish_ctas;
   float decay;
+  unsigned long long timeout_ns;
 };
 
-template <int D, bool INT8, bool WINDOW>
+template <int D, bool INT8>
 struct ScoreGeo {
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
   static constexpr int ROWB = D * (INT8 ? 1 : 2);
   static constexpr int STAGE = 16 * ROWB + (INT8 ? 64 : 0);  // keys of 16 tokens, and their scales
-  static constexpr int NSTAGE = WINDOW ? (ROWB == 512 ? 2 : 4) : ROWB == 512 ? 3 : 6;
+  static constexpr int NSTAGE = ROWB == 512 ? 3 : 6;  // two CTAs an SM either way
   static constexpr int WARP_BYTES = NSTAGE * STAGE;
-  static constexpr int ROWS = WINDOW ? 128 : 16;  // query rows of a unit
-  static constexpr int OFF_Q = WARPS * WARP_BYTES;  // a window's queries, [128][D]
-  static constexpr int OFF_ML = OFF_Q + (WINDOW ? ROWS * D * 2 : 0);
+  static constexpr int ROWS = 16;  // query rows of a unit
+  static constexpr int OFF_ML = WARPS * WARP_BYTES;
   static constexpr int OFF_MASK = OFF_ML + WARPS * ROWS * 8;
   static constexpr int OFF_LENS = OFF_MASK + WARPS * NSTAGE * 4;
   static constexpr int SMEM = OFF_LENS + kSegLens * 4;
-  static constexpr int PER_SM = WINDOW ? (D == 256 ? 1 : INT8 || D == 64 ? 3 : 2) : 2;
+  static constexpr int PER_SM = 2;
 };
 
 // Where a token's row lies: its page (or sequence) and place in it.
@@ -86,9 +81,9 @@ __device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t w) {
 }
 
 // A warp's ring of keys: 16 tokens of every tile of the CTA's, looked up a tile ahead.
-template <int D, bool PAGED, bool INT8, bool WINDOW>
+template <int D, bool PAGED, bool INT8>
 struct KeyRing {
-  using Gm = ScoreGeo<D, INT8, WINDOW>;
+  using Gm = ScoreGeo<D, INT8>;
   static constexpr int CH = Gm::ROWB / 16;  // chunks a row
   const WeightsParams& wp;
   const SegWalk<kSegRange>& walk;
@@ -204,10 +199,10 @@ __device__ __forceinline__ float2 join_warps(const float2* ml, int row) {
 }
 
 template <int D, bool PAGED, bool INT8>
-__global__ void __launch_bounds__(ScoreGeo<D, INT8, false>::THREADS, ScoreGeo<D, INT8, false>::PER_SM)
+__global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>::PER_SM)
     weights_score_kernel(const __grid_constant__ WeightsParams wp) {
-  using Gm = ScoreGeo<D, INT8, false>;
-  using Ring = KeyRing<D, PAGED, INT8, false>;
+  using Gm = ScoreGeo<D, INT8>;
+  using Ring = KeyRing<D, PAGED, INT8>;
   const SegParams& p = wp.s;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -336,219 +331,6 @@ __device__ __forceinline__ float2 join_pieces(const float2* ml, long long slot, 
 // What a weight is made with: 2^(x - .x) * .y; a row that saw nothing gives nothing.
 __device__ __forceinline__ float2 weight_factors(float2 ml) {
   return make_float2(ml.x == kNegInf ? 0.f : ml.x, ml.y == 0.f ? 0.f : 1.f / ml.y);
-}
-
-// Rows [row0, row0 + rows) of every unit, at most 128.  SUMS: out = decay * prior + their
-// weights; else their pieces' (m, l), [slot][128].
-template <int D, bool PAGED, bool INT8, bool SUMS>
-__global__ void __launch_bounds__(ScoreGeo<D, INT8, true>::THREADS, ScoreGeo<D, INT8, true>::PER_SM)
-    weights_window_kernel(const __grid_constant__ WeightsParams wp) {
-  using Gm = ScoreGeo<D, INT8, true>;
-  using Ring = KeyRing<D, PAGED, INT8, true>;
-  constexpr int RT = Gm::ROWS / 16;  // row tiles
-  const SegParams& p = wp.s;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * Gm::NSTAGE;
-  float2* ml = reinterpret_cast<float2*>(smem + Gm::OFF_ML);
-
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const SegWalk<kSegRange> walk(p, seg_stage_lens<Gm::THREADS>(p, reinterpret_cast<int*>(smem + Gm::OFF_LENS)));
-  long long x0, x1;
-  if (!walk.range(blockIdx.x, x0, x1)) return;
-  Ring ring(wp, walk, smem_u32(smem + warp * Gm::WARP_BYTES), masks, x0, x1);
-  SegUnit u = ring.u;
-  int j = ring.j;
-#pragma unroll 1
-  for (int s = 0; s < Gm::NSTAGE; ++s) ring.issue(s);
-
-  const int tiles = (wp.rows + 15) / 16;  // row tiles with rows
-  // queries, [128][D], 16-byte chunks of a row exchanged so that the reads of a fragment meet different banks
-  uint4* qs = reinterpret_cast<uint4*>(smem + Gm::OFF_Q);
-  auto query_chunk = [](int row, int c) { return row * (D / 8) + (INT8 ? c ^ (row & 1) : c ^ (row & 7)); };
-  float m[RT][2], l[RT][2];
-  bool fresh = true;
-  int stage = 0;
-  for (long long x = x0; x < x1; ++x) {
-    if (fresh) {
-      fresh = false;
-      __syncthreads();
-      constexpr int U = 8;
-      for (int e0 = threadIdx.x; e0 < tiles * 16 * (D / 8); e0 += U * Gm::THREADS) {
-        uint4 v[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int in = (e0 + i * Gm::THREADS) / (D / 8), c = (e0 + i * Gm::THREADS) % (D / 8), row = wp.row0 + in;
-          const int token = u.b * p.n + row / p.G, g = row % p.G;
-          v[i] = in < wp.rows ? load_dependent(reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D) + c)
-                              : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int in = (e0 + i * Gm::THREADS) / (D / 8), c = (e0 + i * Gm::THREADS) % (D / 8);
-          if (in < tiles * 16) qs[query_chunk(in, c)] = v[i];
-        }
-      }
-      if constexpr (SUMS) {
-        const SegSums sums = seg_sums(walk.lens, p.B, p.cap, 0, u.b);
-        const long long a = sums.before * p.Hkv + (long long)u.h * u.tiles;
-        const int c0 = seg_owner(walk.all, walk.used, a), c1 = seg_owner(walk.all, walk.used, a + u.tiles - 1);
-        for (int r = warp; r < tiles * 16; r += Gm::WARPS) {
-          const float2 f = weight_factors(join_pieces(p.part_ml, (long long)u.id + c0, c1 - c0 + 1, Gm::ROWS, r));
-          if (lane == 0) ml[r] = r < wp.rows ? f : make_float2(0.f, 0.f);  // no weight of rows that are not
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          m[r][hf] = kNegInf;
-          l[r][hf] = 0.f;
-        }
-      __syncthreads();
-    }
-    cp_async_wait<Gm::NSTAGE - 1>();
-    __syncwarp();
-    const uint32_t live = masks[stage];
-    const int t0 = j * kTile + warp * 16;
-    if (live) {
-      // both halves of the 16 tokens against a row tile at a time: a query fragment is read once for two
-      // products, and two chains of them run side by side
-      uint32_t b[2][D / 16][2];
-      float2 ks[2], sum[2];
-      bool on[2][2];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        ring.fragments(stage, nt, b[nt], ks[nt]);
-        ks[nt].x *= p.scale_log2;
-        ks[nt].y *= p.scale_log2;
-        on[nt][0] = (live >> (nt * 8 + 2 * (lane % 4))) & 1;
-        on[nt][1] = (live >> (nt * 8 + 2 * (lane % 4) + 1)) & 1;
-        sum[nt] = make_float2(0.f, 0.f);
-      }
-      const bool edge = t0 + 16 > u.len - p.n + 1;  // a token that not every row sees
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (r >= tiles) break;
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        if constexpr (INT8) {
-          // 16 elements of each of the thread's two rows: four steps
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t w[2][8];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint4 v = qs[query_chunk(r * 16 + lane / 4 + 8 * hf, 8 * c + 2 * (lane % 4) + i)];
-                w[hf][4 * i] = v.x;
-                w[hf][4 * i + 1] = v.y;
-                w[hf][4 * i + 2] = v.z;
-                w[hf][4 * i + 3] = v.w;
-              }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int nt = 0; nt < 2; ++nt)
-                mma_bf16_16816(s[nt], w[0][2 * i], w[1][2 * i], w[0][2 * i + 1], w[1][2 * i + 1], b[nt][4 * c + i][0],
-                               b[nt][4 * c + i][1]);
-          }
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t a0, a1, a2, a3;  // rows 0 .. 7 and 8 .. 15 of the first 8 elements, then of the second
-            ldsm_x4(smem_u32(qs + query_chunk(r * 16 + (lane & 15), 2 * kk + (lane >> 4))), a0, a1, a2, a3);
-            mma_bf16_16816(s[0], a0, a1, a2, a3, b[0][kk][0], b[0][kk][1]);
-            mma_bf16_16816(s[1], a0, a1, a2, a3, b[1][kk][0], b[1][kk][1]);
-          }
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float y[2][2];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            y[nt][0] = on[nt][0] ? s[nt][2 * hf] * ks[nt].x : kNegInf;
-            y[nt][1] = on[nt][1] ? s[nt][2 * hf + 1] * ks[nt].y : kNegInf;
-          }
-          if (edge) {
-            const int left = u.len - p.n + 1 + (wp.row0 + r * 16 + lane / 4 + 8 * hf) / p.G - t0 - 2 * (lane % 4);
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              y[nt][0] = nt * 8 < left ? y[nt][0] : kNegInf;
-              y[nt][1] = nt * 8 + 1 < left ? y[nt][1] : kNegInf;
-            }
-          }
-          if constexpr (SUMS) {
-            const float2 f = ml[r * 16 + lane / 4 + 8 * hf];
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              sum[nt].x = fmaf(exp2_approx(y[nt][0] - f.x), f.y, sum[nt].x);
-              sum[nt].y = fmaf(exp2_approx(y[nt][1] - f.x), f.y, sum[nt].y);
-            }
-          } else {
-            const float top = fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[1][0], y[1][1]));
-            if (top > m[r][hf]) {
-              l[r][hf] *= exp2_approx(m[r][hf] - top);
-              m[r][hf] = top;
-            }
-            const float mu = m[r][hf] == kNegInf ? 0.f : m[r][hf];
-            l[r][hf] += (exp2_approx(y[0][0] - mu) + exp2_approx(y[0][1] - mu)) +
-                        (exp2_approx(y[1][0] - mu) + exp2_approx(y[1][1] - mu));
-          }
-        }
-      }
-      if constexpr (SUMS) {
-        // the rows' sum: over the 8 lanes of a column, which hold 16 rows
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            sum[nt].x += __shfl_xor_sync(0xffffffffu, sum[nt].x, d);
-            sum[nt].y += __shfl_xor_sync(0xffffffffu, sum[nt].y, d);
-          }
-        // lane 4 k + c writes token 2 c + (k & 1) of half k / 2
-        const int k = lane / 4, t = t0 + (k >> 1) * 8 + 2 * (lane % 4) + (k & 1);
-        if (k < 4 && t < u.end) {
-          const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
-          if (c.good) {
-            const size_t o = ((size_t)c.slab * p.Hkv + u.h) * (PAGED ? p.page_size : p.ctx) + c.at;
-            const float w = k == 0 ? sum[0].x : k == 1 ? sum[0].y : k == 2 ? sum[1].x : sum[1].y;
-            wp.out[o] = wp.prior ? fmaf(wp.decay, load_dependent(wp.prior + o), w) : w;
-          }
-        }
-      }
-    }
-    const bool last = j + 1 == u.tiles;
-    if (!SUMS && (last || x + 1 == x1)) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          // the quad's four
-          float M = m[r][hf];
-          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
-          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
-          float L = l[r][hf] == 0.f ? 0.f : m[r][hf] == kNegInf ? l[r][hf] : l[r][hf] * exp2_approx(m[r][hf] - M);
-          L += __shfl_xor_sync(0xffffffffu, L, 1);
-          L += __shfl_xor_sync(0xffffffffu, L, 2);
-          if (lane % 4 == 0) ml[warp * Gm::ROWS + r * 16 + lane / 4 + 8 * hf] = make_float2(M, L);
-        }
-      __syncthreads();
-      for (int r = threadIdx.x; r < tiles * 16; r += Gm::THREADS)
-        p.part_ml[((size_t)u.id + blockIdx.x) * Gm::ROWS + r] = join_warps<Gm::WARPS, Gm::ROWS>(ml, r);
-      __syncthreads();
-    }
-    ring.issue(stage);
-    stage = stage + 1 == Gm::NSTAGE ? 0 : stage + 1;
-    ++j;
-    if (last && x + 1 < x1) {
-      u = walk.next(u);
-      j = 0;
-      fresh = true;
-    }
-  }
-  cp_async_wait<0>();
 }
 
 // A thread a token: it adds the rows in their order, 256 tokens of a sequence's KV head at a time.
