@@ -128,7 +128,10 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
           }
         }
         // no weight of rows that are not
-        reinterpret_cast<float2*>(smem + Gm::OFF_F)[r] = r < wp.rows ? weight_factors(make_float2(M, L)) : make_float2(0.f, 0.f);
+        const float2 f = r < wp.rows ? weight_factors(make_float2(M, L)) : make_float2(0.f, 0.f);
+        float* to = reinterpret_cast<float*>(smem + Gm::OFF_F) + (r / 2) * 4 + r % 2;  // -m of two rows, then their 1 / l
+        to[0] = -f.x;
+        to[2] = f.y;
       }
       fence_proxy_async_smem();
       __syncthreads();
@@ -139,29 +142,35 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
       const int me = threadIdx.x;
       long long* offs = reinterpret_cast<long long*>(smem + Gm::OFF_OFF);
       constexpr int ROWB = D * (INT8 ? 1 : 2), CH = ROWB / 16;
-      auto look_up = [&](int k) {
-        if (k >= n) return;
+      long long next_off = -1;
+      float next_scale = 0.f;
+      auto look_up = [&](int k) {  // starts the loads; their results are stored later
+        next_off = -1;
+        next_scale = 0.f;
         const int t = t0 + k * Gm::KEYS + me;
-        long long off = -1;
-        float scale = 0.f;
         if (t < t1) {
           const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
           const int slab_rows = PAGED ? p.page_size : p.ctx;
-          off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)ROWB;
-          scale = p.scale_log2;
-          if (INT8) scale *= load_dependent(wp.k_scale + (c.slab * p.Hkv + u.h) * slab_rows + c.at);
+          next_off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)ROWB;
+          next_scale = 1.f;
+          if (INT8) next_scale = load_dependent(wp.k_scale + (c.slab * p.Hkv + u.h) * slab_rows + c.at);
         }
-        offs[((it + k) & 1) * Gm::KEYS + me] = off;
-        reinterpret_cast<float*>(smem + Gm::OFF_KS)[((it + k) & 7) * Gm::KEYS + me] = scale;
+      };
+      // The place of a tile's scales was last read for the tile eight before, long done: the products of tile
+      // at - 2, which are waited for below, began after the readers of tile at - 4.
+      auto keep = [&](int k) {
+        offs[((it + k) & 1) * Gm::KEYS + me] = next_off;
+        reinterpret_cast<float*>(smem + Gm::OFF_KS)[((it + k) & 7) * Gm::KEYS + me] = next_scale * p.scale_log2;
       };
       look_up(0);
+      keep(0);
       // (after a wait that gave up, the threads go on without waits, so that all meet at the barrier)
       for (int k = 0; k < n; ++k) {
         const int at = it + k, buf = at & 1;
         named_bar_sync(1, 128);
         const long long* off = offs + buf * Gm::KEYS;
         uint8_t* dst = smem + Gm::OFF_K + buf * Gm::TILE;
-        constexpr int U = CH < 16 ? CH : 16;
+        constexpr int U = CH < 8 ? CH : Gm::PER_SM == 2 ? 8 : 16;  // loads of a thread in flight
         for (int e0 = 0; e0 < Gm::KEYS * CH; e0 += U * 128) {
           uint4 v[U];
 #pragma unroll
@@ -171,6 +180,7 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
             v[i] = o >= 0 ? load_dependent(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p.k) + o) + c)
                           : make_uint4(0u, 0u, 0u, 0u);
           }
+          if (e0 == 0) look_up(k + 1);
           if (e0 == 0 && at >= 2) ok = ok && wait(Gm::BAR_KE + buf, (at >> 1) - 1);
 #pragma unroll
           for (int i = 0; i < U; ++i) {
@@ -191,11 +201,9 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
             }
           }
         }
-        // the place of the next tile's scales was last read for tile at - 7, long done: the products of tile
-        // at - 2, which were waited for above, began after the readers of tile at - 4
-        look_up(k + 1);
         fence_proxy_async_smem();
         mbar_arrive(bar(Gm::BAR_KF + buf));
+        keep(k + 1);
       }
     } else if (warp == 8) {
       // ---- products
@@ -259,19 +267,20 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
           float y[32];
           if constexpr (SUMS) {
             const float4* f = reinterpret_cast<const float4*>(smem + Gm::OFF_F) + c0 / 2;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 mine2 = make_float2(mine, mine);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float4 g = f[i];
-              float a = fmaf(__uint_as_float(r[2 * i]), mine, -g.x), b = fmaf(__uint_as_float(r[2 * i + 1]), mine, -g.z);
+              float2 y = fma_f32x2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), mine2,
+                                   make_float2(g.x, g.y));
               if (edge) {
-                a = c0 + 2 * i >= from ? a : kNegInf;
-                b = c0 + 2 * i + 1 >= from ? b : kNegInf;
+                y.x = c0 + 2 * i >= from ? y.x : kNegInf;
+                y.y = c0 + 2 * i + 1 >= from ? y.y : kNegInf;
               }
-              acc[2 * (i & 1)] = fmaf(exp2_approx(a), g.y, acc[2 * (i & 1)]);
-              acc[2 * (i & 1) + 1] = fmaf(exp2_approx(b), g.w, acc[2 * (i & 1) + 1]);
+              acc[i & 1] = fma_f32x2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(g.z, g.w), acc[i & 1]);
             }
-            w += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            w += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           } else {
             const float4* s4 = reinterpret_cast<const float4*>(ks + c0);
             float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
@@ -279,10 +288,16 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
             for (int i = 0; i < 8; ++i) {
               float4 g = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
               if constexpr (INT8) g = s4[i];
-              const float z[4] = {g.x, g.y, g.z, g.w};
+              const float2 lo = fma_f32x2(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), make_float2(g.x, g.y),
+                                          make_float2(0.f, 0.f));
+              const float2 hi = fma_f32x2(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
+                                          make_float2(g.z, g.w), make_float2(0.f, 0.f));
+              y[4 * i] = lo.x;
+              y[4 * i + 1] = lo.y;
+              y[4 * i + 2] = hi.x;
+              y[4 * i + 3] = hi.y;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                y[4 * i + e] = __uint_as_float(r[4 * i + e]) * z[e];
                 if (edge) y[4 * i + e] = c0 + 4 * i + e < end ? y[4 * i + e] : kNegInf;
                 top[e] = fmaxf(top[e], y[4 * i + e]);
               }
@@ -293,10 +308,14 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
               m = to;
             }
             const float mu = m == kNegInf ? 0.f : m;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 mu2 = make_float2(-mu, -mu);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i & 3] += exp2_approx(y[i] - mu);
-            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            for (int i = 0; i < 16; ++i) {
+              const float2 z = add_f32x2(make_float2(y[2 * i], y[2 * i + 1]), mu2);
+              acc[i & 1] = add_f32x2(acc[i & 1], make_float2(exp2_approx(z.x), exp2_approx(z.y)));
+            }
+            l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           }
         }
         tc_fence_before();
