@@ -49,7 +49,6 @@ __all__ = [
     "block_select",
     "sparse_attn_contig",
     "sparse_attn_paged",
-    "sparse_workspace",
     "kv_weights_contig",
     "kv_weights_paged",
     "kv_weights_int8_contig",
@@ -150,9 +149,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "block_means_contig": [vp, vp] + [i] * 7 + [vp, vp],
         "block_means_paged": [vp] * 3 + [i] * 10 + [vp, vp],
         "block_select": [vp] * 3 + [i] * 10 + [vp, vp],
-        "sparse_attn_workspace_bytes": [i, i],
-        "sparse_attn_contig": [vp] * 5 + [i] * 8 + [f, vp, ll, vp, vp],
-        "sparse_attn_paged": [vp] * 6 + [i] * 11 + [f, vp, ll, vp, vp],
+        "sparse_attn_contig": [vp] * 5 + [i] * 8 + [f, vp, vp],
+        "sparse_attn_paged": [vp] * 6 + [i] * 11 + [f, vp, vp],
         "kv_weights_workspace_bytes": [i, i, i, i, i, i],
         "kv_weights_contig": [vp] * 3 + [i] * 6 + [f, f, vp, vp, ll, vp, vp],
         "kv_weights_paged": [vp] * 4 + [i] * 9 + [f, f, vp, vp, ll, vp, vp],
@@ -707,27 +705,20 @@ def block_select(q, means, seq_lens, block_size: int, n_select: int, *, first: i
     return (_ext_module or _ext()).block_select(q, means, seq_lens, block_size, n_select, first, recent, out, stream)
 
 
-def sparse_workspace(head_dim: int):
-    """A workspace for sparse_attn_* calls on the current CUDA device (uint8); calls that share it must not overlap
-    on the GPU."""
-    return _workspace_of("sparse_attn_workspace_bytes", head_dim)
-
-
-def sparse_attn_contig(q, k, v, blocks, seq_lens, block_size: int, *, scale: Optional[float] = None, workspace=None,
-                       out=None, stream=None):
+def sparse_attn_contig(q, k, v, blocks, seq_lens, block_size: int, *, scale: Optional[float] = None, out=None,
+                       stream=None):
     """Attention of the last q_len tokens over listed blocks: q bf16 [B, q_len, Hq, D] (D 64, 128 or 256), k/v bf16
     [B, max_ctx, Hkv, D], blocks int32 [B, q_len, Hkv, n_select] (block_select; a negative entry lists nothing, one
     that is listed twice counts twice), seq_lens int32 [B] or None.  A token sees its blocks up to its own position;
-    one that sees nothing gives zeros.  workspace: as made by sparse_workspace (None: made here).  Returns out like q."""
-    return (_ext_module or _ext()).sparse_attn(q, k, v, blocks, None, seq_lens, 0, block_size, scale, workspace, out,
-                                               stream)
+    one that sees nothing gives zeros.  Returns out like q."""
+    return (_ext_module or _ext()).sparse_attn(q, k, v, blocks, None, seq_lens, 0, block_size, scale, out, stream)
 
 
 def sparse_attn_paged(q, k_pool, v_pool, blocks, page_table, seq_lens, max_seq_len: int, block_size: int, *,
-                      scale: Optional[float] = None, workspace=None, out=None, stream=None):
+                      scale: Optional[float] = None, out=None, stream=None):
     """sparse_attn_contig over page pools [num_pages, page_size, Hkv, D]; page_table int32 [B, max_pages]."""
     return (_ext_module or _ext()).sparse_attn(q, k_pool, v_pool, blocks, page_table, seq_lens, max_seq_len, block_size,
-                                               scale, workspace, out, stream)
+                                               scale, out, stream)
 
 
 # ---------------------------------------------------------------- weights and eviction

@@ -73,7 +73,6 @@ struct Library {
   decltype(&::block_select) block_select = nullptr;
   decltype(&::sparse_attn_contig) sparse_attn_contig = nullptr;
   decltype(&::sparse_attn_paged) sparse_attn_paged = nullptr;
-  decltype(&::sparse_attn_workspace_bytes) sparse_attn_workspace_bytes = nullptr;
   decltype(&::kv_weights_contig) kv_weights_contig = nullptr;
   decltype(&::kv_weights_paged) kv_weights_paged = nullptr;
   decltype(&::kv_weights_int8_contig) kv_weights_int8_contig = nullptr;
@@ -715,12 +714,11 @@ PyObject* block_select(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
-// (q, k, v, blocks, page_table, seq_lens, max_seq_len, block_size, scale, workspace, out, stream)
+// (q, k, v, blocks, page_table, seq_lens, max_seq_len, block_size, scale, out, stream)
 PyObject* sparse_attn(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  return guarded(nargs, 12, [&]() -> PyObject* {
+  return guarded(nargs, 11, [&]() -> PyObject* {
     const Tensor &q = ten(a[0], "q"), &k = ten(a[1], "k"), &v = ten(a[2], "v"), &blocks = ten(a[3], "blocks");
-    const Tensor *table = opt(a[4], "page_table"), *lens = opt(a[5], "seq_lens"), *ws = opt(a[9], "workspace"),
-                 *given = opt(a[10], "out");
+    const Tensor *table = opt(a[4], "page_table"), *lens = opt(a[5], "seq_lens"), *given = opt(a[9], "out");
     if (q.dim() != 4 || k.dim() != 4 || blocks.dim() != 4) throw Bad("q, k, blocks: expected 4 dims");
     const int64_t dev = cuda_index(q);
     const int B = small(q.size(0), "q"), n = small(q.size(1), "q"), Hq = small(q.size(2), "q"), D = small(q.size(3), "q"),
@@ -732,24 +730,23 @@ PyObject* sparse_attn(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const float scale = scale_or(a[8], D);
     not_tracked(given, "out");
     on_current(dev);
-    Stream st(a[11], dev);
+    Stream st(a[10], dev);
     const Tensor out = given ? *given : at::empty(dims(B, n, Hq, D), q.options());
     const char* fn = table ? "sparse_attn_paged" : "sparse_attn_contig";
-    const Work w(ws, ws ? 0 : g_lib.sparse_attn_workspace_bytes(D, 0), fn, q, dev);
     const int slab = small(c.slab, "k"), cols = small(c.cols, "page_table"), slabs = small(c.slabs, "k"),
               cap = table ? small(a[6], "max_seq_len") : 0;
     if (table)
       call(fn, [&] {
         return g_lib.sparse_attn_paged(ptr(q), ptr(k), ptr(v), ptr<int>(blocks), ptr<int>(table), ptr<int>(lens), B, n, Hq,
-                                       H, D, slab, cols, slabs, cap, block, pick, scale, w.at, w.size, ptr(out), st.raw);
+                                       H, D, slab, cols, slabs, cap, block, pick, scale, ptr(out), st.raw);
       });
     else
       call(fn, [&] {
         return g_lib.sparse_attn_contig(ptr(q), ptr(k), ptr(v), ptr<int>(blocks), ptr<int>(lens), B, n, Hq, H, D, slab,
-                                        block, pick, scale, w.at, w.size, ptr(out), st.raw);
+                                        block, pick, scale, ptr(out), st.raw);
       });
     written(given);
-    return given ? same(a[10]) : THPVariable_Wrap(out);
+    return given ? same(a[9]) : THPVariable_Wrap(out);
   });
 }
 
@@ -917,7 +914,6 @@ PyObject* open(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   FIND(block_select)
   FIND(sparse_attn_contig)
   FIND(sparse_attn_paged)
-  FIND(sparse_attn_workspace_bytes)
   FIND(kv_weights_contig)
   FIND(kv_weights_paged)
   FIND(kv_weights_int8_contig)

@@ -77,8 +77,10 @@ int launch_clusters(void (*kern)(P), unsigned grid, unsigned threads, size_t sme
 
 template <int D, bool PAGED, int KIND, int NT>
 int launch_seg_nt(const SegParams& p, cudaStream_t st) {
-  using Gm = SegGeo<D, NT>;
+  using Gm = SegGeo<D, NT, KIND>;
   if (int e = allow_smem<seg_kernel<D, PAGED, KIND, NT>>(Gm::SMEM)) return e;
+  if (KIND == kSegBlocks)
+    return launch_clusters(seg_kernel<D, PAGED, KIND, NT>, (unsigned)p.ctas, Gm::THREADS, Gm::SMEM, p.cluster, st, p);
   return launch_dependent(seg_kernel<D, PAGED, KIND, NT>, (unsigned)p.ctas, Gm::THREADS, Gm::SMEM, st, p);
 }
 template <int D, bool PAGED, int KIND>

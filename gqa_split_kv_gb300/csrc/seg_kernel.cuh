@@ -16,9 +16,13 @@
 // their rows into its own ring (cp.async; rows that do not exist are zeros there), keys and
 // values of 16 tokens in turn, and keeps a running maximum m, sum l and output O of its tokens,
 //     O = sum_t 2^(s_t - m) v_t,   l = sum_t 2^(s_t - m),   s_t = scale log2(e) <q, k_t>.
-// Where a unit ends (seg_plan.cuh) the warps' four (m, l, O) are joined through shared memory
-// and written as one partial, or as the output where the CTA had the whole unit.  m is only
-// raised when a score passes it by more than 8; it cancels in O / l.
+// Where a unit ends the warps' four (m, l, O) are joined through shared memory.  m is only raised
+// when a score passes it by more than 8; it cancels in O / l.
+//
+// Ranges are ragged: their tiles are cut evenly over the CTAs (seg_plan.cuh), each piece is
+// written as a partial, and a merge kernel joins them, with the prefix's.  Blocks units all
+// have as many tiles: a cluster of 1 to 8 CTAs takes a unit, each CTA its share of the tiles, and
+// joins it through distributed shared memory.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -52,8 +56,7 @@ struct SegParams {
   const int *page_table, *prefix_table;
   const int* blocks;           // [B, n, Hkv, pick]
   __nv_bfloat16* out;          // like q
-  float* part_o;               // [slots][ru][D]; slots: seg_plan.cuh's, of blocks 2 c + 1 for the piece of CTA c that
-                               // starts a unit, 2 c for one that goes on with it
+  float* part_o;               // [slots][ru][D] (seg_plan.cuh; ranges only)
   float2* part_ml;             // [slots][ru]: m, l
   const float* tc_o;           // [slabs][Hkv][B n G][D]: the prefix's partials, where another kernel made them
   const float2* tc_ml;
@@ -66,7 +69,8 @@ struct SegParams {
   int block, pick;
   int ru;                      // query rows of a unit: 8 or 16
   int rt, rt_prefix;           // units a sequence's KV head (rows over ru), and of the prefix's (0: none here)
-  int ctas;                    // of seg_kernel: the plan's n
+  int ctas;                    // of seg_kernel; ranges: the plan's n
+  int cluster;                 // CTAs that share a blocks unit
   int beside;                  // the kernel before is the prefix's: seg_kernel runs beside it and waits for it at its end
   float scale_log2;
 };
@@ -77,7 +81,7 @@ struct FoldRow {
   long long out;
 };
 
-template <int D, int NT>
+template <int D, int NT, int KIND = kSegRange>
 struct SegGeo {
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
   static constexpr int ROWS = 8 * NT;           // query rows of a unit
@@ -89,7 +93,8 @@ struct SegGeo {
   static constexpr int OFF_FOLD = OFF_ML + WARPS * ROWS * 8;
   static constexpr int OFF_MASK = OFF_FOLD + ROWS * (int)sizeof(FoldRow);
   static constexpr int OFF_LENS = OFF_MASK + WARPS * 4 * 4;
-  static constexpr int SMEM = OFF_LENS + kSegLens * 4;
+  static constexpr int OFF_RES = OFF_LENS + kSegLens * 4;  // blocks: this CTA's (m, l) and O, for the cluster
+  static constexpr int SMEM = OFF_RES + (KIND == kSegBlocks ? ROWS * (8 + D * 4) : 0);
   static constexpr int PER_SM = D == 256 ? 2 : NT == 1 ? 4 : 3;
 };
 
@@ -97,6 +102,28 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
+}
+// A word or four at shared-memory address a of the cluster's CTA `rank`.
+template <typename T>
+__device__ __forceinline__ T load_at(uint32_t a, int rank);
+template <>
+__device__ __forceinline__ float2 load_at<float2>(uint32_t a, int rank) {
+  float2 v;
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [r];\n\t}"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(a), "r"(rank)
+               : "memory");
+  return v;
+}
+template <>
+__device__ __forceinline__ float4 load_at<float4>(uint32_t a, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(a), "r"(rank)
+      : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -139,27 +166,43 @@ struct SegWalk {
   const SegParams& p;
   const int* lens;  // seq_lens, or the CTA's copy
   long long all;  // tiles of the line
-  int tp;         // tiles of a prefix unit
+  int tp;         // tiles of a prefix unit, or of a blocks unit
   int used;       // CTAs that have some
+  int lo, hi;     // blocks: this CTA's tiles of a unit
+  int units;      // blocks
 
-  __device__ __forceinline__ SegWalk(const SegParams& p_, const int* lens_) : p(p_), lens(lens_), all(0), tp(0), used(0) {
+  __device__ __forceinline__ SegWalk(const SegParams& p_, const int* lens_)
+      : p(p_), lens(lens_), all(0), tp(0), used(0), lo(0), hi(0), units(0) {
     if constexpr (KIND == kSegBlocks) {
       tp = (p.pick * p.block + kTile - 1) / kTile;
-      all = (long long)p.B * p.n * p.Hkv * p.rt * tp;
+      const int rank = blockIdx.x % p.cluster;
+      lo = tp * rank / p.cluster;
+      hi = tp * (rank + 1) / p.cluster;
+      units = p.B * p.n * p.Hkv * p.rt;
     } else {
       tp = p.rt_prefix ? (p.base + kTile - 1) / kTile : 0;
       all = seg_sums(lens, p.B, p.cap, p.base, 0).all * p.Hkv * p.rt + prefix_tiles();
+      used = seg_used(all, p.ctas);
     }
-    used = seg_used(all, p.ctas);
   }
-  // The tiles [x0, x1) of a CTA; none past those used.
+  // The tiles [x0, x1) of a CTA, of ranges in the line; false if there are none.
   __device__ __forceinline__ bool range(int c, long long& x0, long long& x1) const {
-    if (c >= used) return false;
-    x0 = seg_start(all, used, c);
-    x1 = seg_start(all, used, c + 1);
-    return true;
+    if constexpr (KIND == kSegBlocks) {
+      const int first = c / p.cluster, step = p.ctas / p.cluster;
+      x0 = 0;
+      x1 = first < units ? (long long)((units - first + step - 1) / step) * (hi - lo) : 0;
+      return x1 > 0;
+    } else {
+      if (c >= used) return false;
+      x0 = seg_start(all, used, c);
+      x1 = seg_start(all, used, c + 1);
+      return true;
+    }
   }
   __device__ __forceinline__ long long prefix_tiles() const { return (long long)p.Hkv * p.rt_prefix * tp; }
+  // Of this CTA: the first tile of a unit that it starts, and the end of its tiles.
+  __device__ __forceinline__ int first_tile() const { return KIND == kSegBlocks ? lo : 0; }
+  __device__ __forceinline__ int end_tile(const SegUnit& u) const { return KIND == kSegBlocks ? hi : u.tiles; }
 
   // A blocks unit by number.
   __device__ __forceinline__ SegUnit blocks_unit(int id) const {
@@ -199,12 +242,11 @@ struct SegWalk {
     u.id = p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r;
     return u;
   }
-  // The unit of tile x (x < all), j: the tile's place in it.  The warp executes it.
+  // The unit of tile x (x < all; blocks: the CTA's first), j: the tile's place in it.  The warp executes it.
   __device__ __forceinline__ SegUnit at(long long x, int& j) const {
     if constexpr (KIND == kSegBlocks) {
-      const int id = (int)seg_div(x, tp);
-      j = (int)(x - (long long)id * tp);
-      return blocks_unit(id);
+      j = lo;
+      return blocks_unit((int)blockIdx.x / p.cluster);
     } else {
       const long long wp = prefix_tiles();
       if (x < wp) {
@@ -225,7 +267,7 @@ struct SegWalk {
   // The next unit that has tiles; there is one.
   __device__ __forceinline__ SegUnit next(const SegUnit& u) const {
     if constexpr (KIND == kSegBlocks) {
-      return blocks_unit(u.id + 1);
+      return blocks_unit(u.id + p.ctas / p.cluster);
     } else {
       int b = u.b, h = u.h, r = u.r + 1;
       if (u.prefix) {
@@ -312,9 +354,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 template <int D, bool PAGED, int KIND, int NT>
-__global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
+__global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KIND>::PER_SM)
     seg_kernel(const __grid_constant__ SegParams p) {
-  using Gm = SegGeo<D, NT>;
+  using Gm = SegGeo<D, NT, KIND>;
   constexpr int NG = Gm::NG;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -354,9 +396,9 @@ __global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
         ahead = true;
         off_next = -1;
         if (lx + 1 < x1) {
-          if (++lj == lu.tiles) {
+          if (++lj == walk.end_tile(lu)) {
             lu = walk.next(lu);
-            lj = 0;
+            lj = walk.first_tile();
           }
           off_next = look_up();
         }
@@ -397,13 +439,11 @@ __global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];
   int lim[NT][2];
-  int j0 = j;
   bool fresh = true;
   int slot_at = 0;  // of the granule that is read next
   for (long long x = x0; x < x1; ++x) {
     if (fresh) {  // a new unit: its queries
       fresh = false;
-      j0 = j;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         int token, g, unused;
@@ -424,7 +464,7 @@ __global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
         }
       }
     }
-    const bool last = j + 1 == u.tiles, join = last || x + 1 == x1;
+    const bool last = j + 1 == walk.end_tile(u), join = last || x + 1 == x1;
     const uint32_t kst = ring_s + slot_at * Gm::GRAN;
     const int k_slot = slot_at;
     slot_at = slot_at + 1 == NG ? 0 : slot_at + 1;
@@ -541,8 +581,10 @@ __global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
         }
       }
       __syncthreads();
-      const bool whole = KIND == kSegBlocks && last && j0 == 0;
-      const size_t slot = KIND == kSegBlocks ? 2 * (size_t)blockIdx.x + (j0 == 0) : (size_t)u.id + blockIdx.x;
+      const bool whole = KIND == kSegBlocks && p.cluster == 1;
+      const size_t slot = (size_t)u.id + blockIdx.x;
+      float2* res_ml = reinterpret_cast<float2*>(smem + Gm::OFF_RES);  // blocks shared by a cluster
+      float* res_o = reinterpret_cast<float*>(smem + Gm::OFF_RES + Gm::ROWS * 8);
       // each row's factors of the warps' O, and where it goes
       FoldRow* fold = reinterpret_cast<FoldRow*>(smem + Gm::OFF_FOLD);
       if (threadIdx.x < Gm::ROWS) {
@@ -568,6 +610,8 @@ __global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
           const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that saw nothing is zeros
 #pragma unroll
           for (int w = 0; w < Gm::WARPS; ++w) f.f[w] *= inv;
+        } else if (KIND == kSegBlocks) {
+          res_ml[r] = make_float2(M, L);
         } else if (f.out >= 0) {
           p.part_ml[slot * Gm::ROWS + r] = make_float2(M, L);
         }
@@ -593,17 +637,52 @@ __global__ void __launch_bounds__(SegGeo<D, NT>::THREADS, SegGeo<D, NT>::PER_SM)
         }
         if (whole)
           *reinterpret_cast<uint2*>(p.out + f.out + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        else if (KIND == kSegBlocks)
+          *reinterpret_cast<float4*>(res_o + r * D + c) = a;
         else
           *reinterpret_cast<float4*>(p.part_o + (slot * Gm::ROWS + r) * D + c) = a;
       }
-      __syncthreads();
+      if (KIND == kSegBlocks && p.cluster > 1) {
+        // the cluster's CTAs join a share of the rows' elements each
+        cluster_sync();
+        const int rank = blockIdx.x % p.cluster, all = Gm::ROWS * (D / 4);
+        for (int e = all * rank / p.cluster + threadIdx.x; e < all * (rank + 1) / p.cluster; e += Gm::THREADS) {
+          const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+          const long long to = fold[r].out;
+          if (to < 0) break;
+          float2 y[8];
+          float M = kNegInf, L = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            y[k] = k < p.cluster ? load_at<float2>(smem_u32(res_ml + r), k) : make_float2(kNegInf, 0.f);
+            M = fmaxf(M, y[k].x);
+          }
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (y[k].y == 0.f) continue;
+            const float w = y[k].x == kNegInf ? 1.f : exp2_approx(y[k].x - M);
+            const float4 z = load_at<float4>(smem_u32(res_o + r * D + c), k);
+            L += w * y[k].y;
+            a.x += w * z.x;
+            a.y += w * z.y;
+            a.z += w * z.z;
+            a.w += w * z.w;
+          }
+          const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that saw nothing is zeros
+          *reinterpret_cast<uint2*>(p.out + to + c) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        }
+        cluster_sync();  // no CTA writes its own again, or leaves, before all have read it
+      } else {
+        __syncthreads();
+      }
       issue();
     }
     issue();
     ++j;
     if (last && x + 1 < x1) {
       u = walk.next(u);
-      j = 0;
+      j = walk.first_tile();
       fresh = true;
     }
   }
@@ -705,12 +784,16 @@ struct SegRow {
 
 constexpr int kMergeThreads = 256;
 
-// Joins the prefix's and the rests' partials: a warp a row of the output.
+// Joins the prefix's and the rests' partials: a warp a row of the output.  The lengths are read
+// before the wait: the kernels that wrote them were done before seg_kernel, and prefix_tc_kernel
+// before it, let anything start.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const __grid_constant__ SegParams p) {
-  pdl_wait_primary();
   const long long row = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  if (row >= (long long)p.B * p.n * p.Hq) return;
+  if (row >= (long long)p.B * p.n * p.Hq) {
+    pdl_wait_primary();
+    return;
+  }
   const int hq = (int)(row % p.Hq), token = (int)(row / p.Hq);
   const int b = token / p.n, i = token - b * p.n, h = hq / p.G, g = hq - h * p.G;
   const SegSums sums = seg_sums(p.seq_lens, p.B, p.cap, p.base, b);
@@ -730,6 +813,7 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const _
   const long long a1 = wp + sums.before * p.Hkv * p.rt + (long long)(h * p.rt + r) * t;
   const int id1 = p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r;
   const int c1 = t ? seg_owner(W, used, a1) : 0, nb = t ? seg_owner(W, used, a1 + t - 1) - c1 + 1 : 0;
+  pdl_wait_primary();
   SegRow<D> acc;
   acc.add(na + nb, [&](int k, const float2*& ml, const float*& o) {
     if (k < na && p.slabs) {
@@ -743,28 +827,6 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const _
     }
   });
   acc.store(p.out + row * D);
-}
-
-// Joins the partials of the blocks units that were cut: CTA c looks at the start of CTA c + 1's
-// tiles, and joins that unit if it is cut there first.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) seg_merge_blocks_kernel(const __grid_constant__ SegParams p) {
-  pdl_wait_primary();
-  const long long tp = (p.pick * p.block + kTile - 1) / kTile, W = (long long)p.B * p.n * p.Hkv * p.rt * tp;
-  const long long x = seg_start(W, p.ctas, blockIdx.x + 1), id = seg_div(x, tp);
-  if (x >= W || x == id * tp || seg_start(W, p.ctas, blockIdx.x) > id * tp) return;
-  const int c0 = blockIdx.x, c1 = seg_owner(W, p.ctas, (id + 1) * tp - 1);
-  const int r0 = (int)(id % p.rt) * p.ru, h = (int)(id / p.rt % p.Hkv);
-  const long long token = id / p.rt / p.Hkv;
-  for (int r = threadIdx.x >> 5; r < p.ru && r0 + r < p.G; r += kMergeThreads / 32) {
-    SegRow<D> acc;
-    acc.add(c1 - c0 + 1, [&](int k, const float2*& ml, const float*& o) {
-      const long long at = (2ll * (c0 + k) + (k == 0)) * p.ru + r;
-      ml = p.part_ml + at;
-      o = p.part_o + at * D;
-    });
-    acc.store(p.out + (token * p.Hq + h * p.G + r0 + r) * D);
-  }
 }
 
 }  // namespace da

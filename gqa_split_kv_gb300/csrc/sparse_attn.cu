@@ -82,26 +82,16 @@ int check_heads(int B, int n, int Hq, int Hkv, int D) {
 
 // ---------------------------------------------------------------- attention
 
-long long sparse_bytes(int D, int sms) {
-  const long long few = seg_partial_bytes(2ll * seg_ctas(8, D, sms), 8, D);
-  const long long many = D == 256 ? 0 : seg_partial_bytes(2ll * seg_ctas(16, D, sms), 16, D);
-  return few > many ? few : many;
-}
-
 struct SparseCall {
   SegParams p;
   bool paged;
   int D;
   long long cap;
-  void* workspace;
-  long long workspace_bytes;
 };
 
 template <int D>
 int launch_sparse(const SparseCall& c, cudaStream_t st) {
-  if (int e = c.paged ? launch_seg<D, true, kSegBlocks>(c.p, st) : launch_seg<D, false, kSegBlocks>(c.p, st)) return e;
-  if (c.p.ctas == 1) return DA_OK;
-  return launch_dependent(seg_merge_blocks_kernel<D>, (unsigned)c.p.ctas - 1, kMergeThreads, 0, st, c.p);
+  return c.paged ? launch_seg<D, true, kSegBlocks>(c.p, st) : launch_seg<D, false, kSegBlocks>(c.p, st);
 }
 
 int sparse_call(SparseCall& c, float scale, cudaStream_t st) {
@@ -126,22 +116,27 @@ int sparse_call(SparseCall& c, float scale, cudaStream_t st) {
     return DA_ERR_INVALID_ARG;
   int dev, sms, optin;
   if (current_device(&dev) || device_info(dev, &sms, &optin)) return DA_ERR_CUDA;
-  const long long need = sparse_bytes(c.D, sms);
-  if (!c.workspace || !aligned(c.workspace, 16) || c.workspace_bytes < need) return DA_ERR_WORKSPACE;
-  if (overlap(c.workspace, need, p.out, on)) return DA_ERR_INVALID_ARG;
   p.ru = seg_unit_rows(p.G, c.D);
   p.rt = (p.G + p.ru - 1) / p.ru;
-  const long long units = product(p.B, p.n, p.Hkv, p.rt), tiles = units * ((p.pick * p.block + kTile - 1) / kTile);
+  const long long units = product(p.B, p.n, p.Hkv, p.rt), room = seg_ctas(p.ru, c.D, sms);
   if (units > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
-  p.ctas = (int)(tiles < seg_ctas(p.ru, c.D, sms) ? tiles : seg_ctas(p.ru, c.D, sms));
-  seg_partials(p, c.workspace, 2ll * p.ctas, c.D);
+  // CTAs a unit: as many as make the rounds over the card shortest, a unit's fixed work counting as 2 tiles
+  const long long tiles = (p.pick * p.block + kTile - 1) / kTile;
+  long long best = 0;
+  for (int k = 1; k <= 8 && k <= tiles; k *= 2) {
+    const long long at_once = room / k, cost = (units + at_once - 1) / at_once * ((tiles + k - 1) / k + 2);
+    if (k > 1 && cost >= best) continue;
+    best = cost;
+    p.cluster = k;
+    p.ctas = (int)((units < at_once ? units : at_once) * k);
+  }
   p.scale_log2 = scale * 1.4426950408889634f;
   return c.D == 64 ? launch_sparse<64>(c, st) : c.D == 128 ? launch_sparse<128>(c, st) : launch_sparse<256>(c, st);
 }
 
 SparseCall sparse_params(const void* q, const void* k, const void* v, const int* blocks, const int* seq_lens, int batch,
                          int q_len, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int n_select,
-                         void* workspace, long long workspace_bytes, void* out) {
+                         void* out) {
   SparseCall c = {};
   c.p.q = static_cast<const __nv_bfloat16*>(q);
   c.p.k = static_cast<const __nv_bfloat16*>(k);
@@ -156,8 +151,6 @@ SparseCall sparse_params(const void* q, const void* k, const void* v, const int*
   c.p.block = block_size;
   c.p.pick = n_select;
   c.D = head_dim;
-  c.workspace = workspace;
-  c.workspace_bytes = workspace_bytes;
   return c;
 }
 
@@ -232,22 +225,11 @@ extern "C" int block_select(const void* q, const void* means, const int* seq_len
                            : launch_select<256>(p, units, st);
 }
 
-extern "C" long long sparse_attn_workspace_bytes(int head_dim, int num_sms) {
-  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return -DA_ERR_UNSUPPORTED;
-  int sms = num_sms;
-  if (sms <= 0) {
-    int dev, optin;
-    if (current_device(&dev) || device_info(dev, &sms, &optin)) return -DA_ERR_CUDA;
-  }
-  return sparse_bytes(head_dim, sms);
-}
-
 extern "C" int sparse_attn_contig(const void* q, const void* k, const void* v, const int* blocks, const int* seq_lens,
                                   int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim, int max_ctx,
-                                  int block_size, int n_select, float scale, void* workspace, long long workspace_bytes,
-                                  void* out, void* stream) {
+                                  int block_size, int n_select, float scale, void* out, void* stream) {
   SparseCall c = sparse_params(q, k, v, blocks, seq_lens, batch, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
-                               n_select, workspace, workspace_bytes, out);
+                               n_select, out);
   c.p.ctx = max_ctx;
   c.cap = max_ctx;
   return sparse_call(c, scale, reinterpret_cast<cudaStream_t>(stream));
@@ -256,11 +238,11 @@ extern "C" int sparse_attn_contig(const void* q, const void* k, const void* v, c
 extern "C" int sparse_attn_paged(const void* q, const void* k_pool, const void* v_pool, const int* blocks,
                                  const int* page_table, const int* seq_lens, int batch, int q_len, int num_q_heads,
                                  int num_kv_heads, int head_dim, int page_size, int max_pages_per_seq, int num_pages,
-                                 int max_seq_len, int block_size, int n_select, float scale, void* workspace,
-                                 long long workspace_bytes, void* out, void* stream) {
+                                 int max_seq_len, int block_size, int n_select, float scale, void* out,
+                                 void* stream) {
   if (max_seq_len < 0) return DA_ERR_INVALID_ARG;
   SparseCall c = sparse_params(q, k_pool, v_pool, blocks, seq_lens, batch, q_len, num_q_heads, num_kv_heads, head_dim,
-                               block_size, n_select, workspace, workspace_bytes, out);
+                               block_size, n_select, out);
   c.paged = true;
   c.p.page_table = page_table;
   c.p.page_size = page_size;

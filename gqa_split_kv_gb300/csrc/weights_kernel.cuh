@@ -334,38 +334,58 @@ __device__ __forceinline__ float2 weight_factors(float2 ml) {
 }
 
 // A thread a token: it adds the rows in their order, 256 tokens of a sequence's KV head at a time.
+// The plan, the pages and the priors come before the wait: nothing that weights_score_kernel
+// writes is among them, and the kernels before that one were done when it let this one start.
 constexpr int kFinishThreads = 256;
 
 template <bool PAGED>
 __global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const __grid_constant__ WeightsParams wp) {
   const SegParams& p = wp.s;
   __shared__ float2 row[16];
-  pdl_wait_primary();
-  const long long all = seg_sums(p.seq_lens, p.B, p.cap, 0, 0).all;  // tiles of the batch
+  __shared__ int s_lens[kSegLens];
+  const int* lens = seg_stage_lens<kFinishThreads>(p, s_lens);
+  const long long all = seg_sums(lens, p.B, p.cap, 0, 0).all;  // tiles of the batch
   const long long W = all * p.Hkv;
   const int used = seg_used(W, p.ctas), ctas = seg_used(W, wp.finish_ctas);
-  if ((int)blockIdx.x >= ctas) return;
-  const long long f1 = seg_start(W, ctas, blockIdx.x + 1);
-  long long f = seg_start(W, ctas, blockIdx.x);
+  long long f = 0, f1 = 0;
+  if ((int)blockIdx.x < ctas) {
+    f = seg_start(W, ctas, blockIdx.x);
+    f1 = seg_start(W, ctas, blockIdx.x + 1);
+  }
+  bool waited = false;
   while (f < f1) {
-    const SegAt s = seg_find(p.seq_lens, p.B, p.cap, 0, seg_div(f, p.Hkv));
-    const int L = seg_len(p.seq_lens, s.b, p.cap), tiles = seg_tiles(L, p.cap, 0);
+    const SegAt s = seg_find(lens, p.B, p.cap, 0, seg_div(f, p.Hkv));
+    const int L = seg_len(lens, s.b, p.cap), tiles = seg_tiles(L, p.cap, 0);
     const int h = (int)seg_div(f - s.start * p.Hkv, tiles), j0 = (int)(f - s.start * p.Hkv - (long long)h * tiles);
     const int j1 = (int)min((long long)tiles, j0 + (f1 - f));
     const long long line = s.start * p.Hkv + (long long)h * tiles;  // its first tile among the scores
     const int c0 = seg_owner(W, used, line), c1 = seg_owner(W, used, line + tiles - 1);
-    __syncthreads();
-    for (int r = threadIdx.x >> 5; r < wp.rows; r += kFinishThreads / 32) {
-      const float2 y = weight_factors(join_pieces(p.part_ml, (long long)(s.b * p.Hkv + h) + c0, c1 - c0 + 1, 16, r));
-      if ((threadIdx.x & 31) == 0) row[r] = y;
-    }
-    __syncthreads();
-    for (int j = j0 + threadIdx.x / kTile; j < j1; j += kFinishThreads / kTile) {
-      const int t = j * kTile + threadIdx.x % kTile;
-      if (t >= L) continue;
-      const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, s.b, t);
-      const size_t o = ((size_t)c.slab * p.Hkv + h) * (PAGED ? p.page_size : p.ctx) + c.at;
-      const float before = wp.prior && c.good ? load_dependent(wp.prior + o) : 0.f;
+    bool fresh = true;
+    for (int ja = j0; ja < j1; ja += kFinishThreads / kTile) {
+      const int j = ja + threadIdx.x / kTile, t = j * kTile + threadIdx.x % kTile;
+      const bool mine = j < j1 && t < L;
+      Cell c = {0, 0, false};
+      size_t o = 0;
+      float before = 0.f;
+      if (mine) {
+        c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, s.b, t);
+        o = ((size_t)c.slab * p.Hkv + h) * (PAGED ? p.page_size : p.ctx) + c.at;
+        if (wp.prior && c.good) before = load_dependent(wp.prior + o);
+      }
+      if (!waited) {
+        waited = true;
+        pdl_wait_primary();
+      }
+      if (fresh) {
+        fresh = false;
+        __syncthreads();
+        for (int r = threadIdx.x >> 5; r < wp.rows; r += kFinishThreads / 32) {
+          const float2 y = weight_factors(join_pieces(p.part_ml, (long long)(s.b * p.Hkv + h) + c0, c1 - c0 + 1, 16, r));
+          if ((threadIdx.x & 31) == 0) row[r] = y;
+        }
+        __syncthreads();
+      }
+      if (!mine) continue;
       const float* x = wp.scores + (size_t)(line + j) * wp.rows * kTile + threadIdx.x % kTile;
       float w = 0.f;
 #pragma unroll 8
@@ -374,6 +394,7 @@ __global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const __
     }
     f += j1 - j0;
   }
+  if (!waited) pdl_wait_primary();
 }
 
 }  // namespace da

@@ -622,16 +622,14 @@ int block_select(const void* q, const void* means, const int* seq_lens, int batc
  * nothing gives zeros.
  *  q, out, k, v, page_table, seq_lens, scale  as prefix_attn without a prefix
  *  blocks   int32 [batch, q_len, num_kv_heads, n_select]; block_size a multiple of 16, of any relation to page_size
- *  workspace  sparse_attn_workspace_bytes(head_dim, num_sms) bytes, 16-byte aligned
  */
-long long sparse_attn_workspace_bytes(int head_dim, int num_sms);
 int sparse_attn_contig(const void* q, const void* k, const void* v, const int* blocks, const int* seq_lens, int batch,
                        int q_len, int num_q_heads, int num_kv_heads, int head_dim, int max_ctx, int block_size,
-                       int n_select, float scale, void* workspace, long long workspace_bytes, void* out, void* stream);
+                       int n_select, float scale, void* out, void* stream);
 int sparse_attn_paged(const void* q, const void* k_pool, const void* v_pool, const int* blocks, const int* page_table,
                       const int* seq_lens, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
                       int page_size, int max_pages_per_seq, int num_pages, int max_seq_len, int block_size, int n_select,
-                      float scale, void* workspace, long long workspace_bytes, void* out, void* stream);
+                      float scale, void* out, void* stream);
 
 /*
  * Weights and eviction.

@@ -168,14 +168,14 @@ def test_all_blocks_equal_decode():
 
 def test_captured_and_replayed():
     c = Cache(4, [3000, 2000, 2500], 3100, 2, 128, 16)
-    q, ws = randn(c.gen, 3, 1, 16, 128), binding.sparse_workspace(128)
+    q = randn(c.gen, 3, 1, 16, 128)
     means, out = means_of(c, 64), torch.empty_like(q)
     blocks = binding.block_select(q, means, c.seq_lens, 64, 12)
 
     def step():
         means_of(c, 64, 1, means)
         binding.block_select(q, means, c.seq_lens, 64, 12, out=blocks)
-        listed(c, q, blocks, 64, workspace=ws, out=out)
+        listed(c, q, blocks, 64, out=out)
 
     step()
     torch.cuda.synchronize()
@@ -185,7 +185,6 @@ def test_captured_and_replayed():
     for cut in (1, 500, 0):
         c.seq_lens.copy_(lens_of(3000 - cut, 2000, 2500 - cut))
         q.copy_(torch.randn(q.shape, device="cuda", generator=c.gen))
-        ws.fill_(0xFF)
         graph.replay()
         got = out.clone(), blocks.clone()
         step()

@@ -147,12 +147,11 @@ def test_sparse_refusals(clib):
     assert select(B=0) == 0
 
     def sparse(q=A, k=A + BIG, v=A + 2 * BIG, blocks=A, B=1, n=1, Hq=8, Hkv=2, D=64, ctx=128, block=64, pick=2, scale=F,
-               ws=A + 3 * BIG, size=BIG, out=A + 4 * BIG):
-        return clib.sparse_attn_contig(q, k, v, blocks, None, B, n, Hq, Hkv, D, ctx, block, pick, scale, ws, size, out, None)
+               out=A + 4 * BIG):
+        return clib.sparse_attn_contig(q, k, v, blocks, None, B, n, Hq, Hkv, D, ctx, block, pick, scale, out, None)
     assert sparse(pick=0) == sparse(block=0) == sparse(blocks=None) == sparse(blocks=A + 2) == sparse(scale=float("inf")) == 1
     assert sparse(out=A) == sparse(out=A + BIG) == sparse(k=None) == sparse(Hq=9) == sparse(ctx=-1) == 1
     assert sparse(block=24) == sparse(D=80) == sparse(pick=2 ** 26, block=64) == 2
-    assert clib.sparse_attn_workspace_bytes(128, 152) > 0 and clib.sparse_attn_workspace_bytes(100, 152) == -2
 
 
 def test_weights_refusals(clib):
