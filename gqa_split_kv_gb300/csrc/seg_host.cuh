@@ -35,7 +35,7 @@ long long capacity(int page_size, int max_pages, int max_seq_len) {
 }
 
 // Lets a kernel use this much shared memory, once a device.
-template <auto KERN>
+template <auto KERN, bool CLUSTERS_OF_16 = false>
 int allow_smem(size_t bytes) {
   static std::atomic<unsigned long long> done{0};
   int dev;
@@ -43,7 +43,8 @@ int allow_smem(size_t bytes) {
   if (done.load(std::memory_order_relaxed) >> dev & 1) return DA_OK;
   if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess ||
       cudaFuncSetAttribute(KERN, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
-          cudaSuccess) {
+          cudaSuccess ||
+      (CLUSTERS_OF_16 && cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
     cudaGetLastError();
     return DA_ERR_CUDA;
   }
@@ -78,7 +79,7 @@ int launch_clusters(void (*kern)(P), unsigned grid, unsigned threads, size_t sme
 template <int D, bool PAGED, int KIND, int NT>
 int launch_seg_nt(const SegParams& p, cudaStream_t st) {
   using Gm = SegGeo<D, NT, KIND>;
-  if (int e = allow_smem<seg_kernel<D, PAGED, KIND, NT>>(Gm::SMEM)) return e;
+  if (int e = allow_smem<seg_kernel<D, PAGED, KIND, NT>, KIND == kSegBlocks>(Gm::SMEM)) return e;
   if (KIND == kSegBlocks)
     return launch_clusters(seg_kernel<D, PAGED, KIND, NT>, (unsigned)p.ctas, Gm::THREADS, Gm::SMEM, p.cluster, st, p);
   return launch_dependent(seg_kernel<D, PAGED, KIND, NT>, (unsigned)p.ctas, Gm::THREADS, Gm::SMEM, st, p);

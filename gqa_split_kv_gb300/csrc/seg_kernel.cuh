@@ -44,6 +44,7 @@ __device__ __forceinline__ uint32_t float_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr int kSegCluster = 16;  // CTAs that may share a blocks unit
 constexpr int kSegLens = 512;  // lengths that a CTA copies to its shared memory
 
 enum SegKind { kSegRange = 0, kSegBlocks = 1 };
@@ -650,16 +651,16 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
           const int r = e / (D / 4), c = (e % (D / 4)) * 4;
           const long long to = fold[r].out;
           if (to < 0) break;
-          float2 y[8];
+          float2 y[kSegCluster];
           float M = kNegInf, L = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < kSegCluster; ++k) {
             y[k] = k < p.cluster ? load_at<float2>(smem_u32(res_ml + r), k) : make_float2(kNegInf, 0.f);
             M = fmaxf(M, y[k].x);
           }
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < kSegCluster; ++k) {
             if (y[k].y == 0.f) continue;
             const float w = y[k].x == kNegInf ? 1.f : exp2_approx(y[k].x - M);
             const float4 z = load_at<float4>(smem_u32(res_o + r * D + c), k);

@@ -123,7 +123,7 @@ int sparse_call(SparseCall& c, float scale, cudaStream_t st) {
   // CTAs a unit: as many as make the rounds over the card shortest, a unit's fixed work counting as 2 tiles
   const long long tiles = (p.pick * p.block + kTile - 1) / kTile;
   long long best = 0;
-  for (int k = 1; k <= 8 && k <= tiles; k *= 2) {
+  for (int k = 1; k <= kSegCluster && k <= tiles; k *= 2) {
     const long long at_once = room / k, cost = (units + at_once - 1) / at_once * ((tiles + k - 1) / k + 2);
     if (k > 1 && cost >= best) continue;
     best = cost;
