@@ -12,9 +12,10 @@
 // accumulator, transposed 8 x 8 at a time.
 //
 // The 4 warps of a CTA take 16 tokens each of every tile of 64 and run on their own, with
-// no barrier between them: a warp looks up where its tokens lie two tiles ahead, copies
-// their rows into its own ring (cp.async; rows that do not exist are zeros there), keys and
-// values of 16 tokens in turn, and keeps a running maximum m, sum l and output O of its tokens,
+// no barrier between them: a warp looks up where its 16 tokens lie two tiles ahead (they start at a
+// multiple of 16 and pages hold whole 16s, so their rows are equally far apart: one look-up and an
+// addition a row; a look-up a row made half of the instructions), copies their rows into its own ring
+// (cp.async; rows that do not exist are zeros there), keys and values in turn, and keeps a running maximum m, sum l and output O of its tokens,
 //     O = sum_t 2^(s_t - m) v_t,   l = sum_t 2^(s_t - m),   s_t = scale log2(e) <q, k_t>.
 // Where a unit ends the warps' four (m, l, O) are joined through shared memory.  m is only raised
 // when a score passes it by more than 8; it cancels in O / l.
@@ -63,7 +64,7 @@ struct SegParams {
   const float2* tc_ml;
   int slabs;
   int B, n, Hq, Hkv, G;
-  int base;                    // tokens of the shared prefix
+  int base;                    // tokens of the shared prefix; the rests' tiles start at the multiple of 16 below
   int cap;                     // longest sequence
   int ctx;
   int page_size, max_pages, num_pages;
@@ -92,8 +93,7 @@ struct SegGeo {
   static constexpr int WARP_BYTES = NG * GRAN;
   static constexpr int OFF_ML = WARPS * WARP_BYTES;
   static constexpr int OFF_FOLD = OFF_ML + WARPS * ROWS * 8;
-  static constexpr int OFF_MASK = OFF_FOLD + ROWS * (int)sizeof(FoldRow);
-  static constexpr int OFF_LENS = OFF_MASK + WARPS * 4 * 4;
+  static constexpr int OFF_LENS = OFF_FOLD + ROWS * (int)sizeof(FoldRow);
   static constexpr int OFF_RES = OFF_LENS + kSegLens * 4;  // blocks: this CTA's (m, l) and O, for the cluster
   static constexpr int SMEM = OFF_RES + (KIND == kSegBlocks ? ROWS * (8 + D * 4) : 0);
   static constexpr int PER_SM = D == 256 ? 2 : NT == 1 ? 4 : 3;
@@ -129,6 +129,7 @@ __device__ __forceinline__ float4 load_at<float4>(uint32_t a, int rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Copies 16 bytes, or writes as many zeros and reads nothing.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
@@ -182,7 +183,7 @@ struct SegWalk {
       units = p.B * p.n * p.Hkv * p.rt;
     } else {
       tp = p.rt_prefix ? (p.base + kTile - 1) / kTile : 0;
-      all = seg_sums(lens, p.B, p.cap, p.base, 0).all * p.Hkv * p.rt + prefix_tiles();
+      all = seg_sums(lens, p.B, p.cap, p.base & ~15, 0).all * p.Hkv * p.rt + prefix_tiles();
       used = seg_used(all, p.ctas);
     }
   }
@@ -239,7 +240,7 @@ struct SegWalk {
     u.r = r;
     u.prefix = 0;
     u.len = u.end = seg_len(lens, b, p.cap);
-    u.tiles = seg_tiles(u.end, p.cap, p.base);
+    u.tiles = seg_tiles(u.end, p.cap, p.base & ~15);
     u.id = p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r;
     return u;
   }
@@ -257,8 +258,8 @@ struct SegWalk {
       }
       x -= wp;
       const int hr = p.Hkv * p.rt;
-      const SegAt f = seg_find(lens, p.B, p.cap, p.base, seg_div(x, hr));
-      const int tb = seg_tiles(seg_len(lens, f.b, p.cap), p.cap, p.base);
+      const SegAt f = seg_find(lens, p.B, p.cap, p.base & ~15, seg_div(x, hr));
+      const int tb = seg_tiles(seg_len(lens, f.b, p.cap), p.cap, p.base & ~15);
       const long long in = x - f.start * hr;
       const int w = (int)seg_div(in, tb);
       j = (int)(in - (long long)w * tb);
@@ -293,32 +294,40 @@ struct SegWalk {
   }
 };
 
-// Element offset of a token's row of head h in the cache (or the prefix's), -1 where there
-// is none.  A page outside the pool is flagged and page 0 read instead.
+// 16 tokens: the element offset of the first one's row of head h in the cache (or the prefix's), the rest
+// Hkv D apart, and which of them there are (bit i: token i).  A page outside the pool is flagged and
+// page 0 read instead.  The same in every lane.
+struct SegGroup {
+  long long off;
+  uint32_t live;
+};
 template <int D, bool PAGED, int KIND>
-__device__ __forceinline__ long long seg_row(const SegParams& p, const SegUnit& u, int at) {
-  int t;  // the token
+__device__ __forceinline__ SegGroup seg_group(const SegParams& p, const SegUnit& u, int at) {
+  int t;  // the first token
   if constexpr (KIND == kSegBlocks) {
     const int e = at / p.block;
-    if (e >= p.pick) return -1;
+    if (e >= p.pick) return {0, 0u};
     const int id = load_dependent(p.blocks + (((size_t)u.b * p.n + u.i) * p.Hkv + u.h) * p.pick + e);
-    if (id < 0 || id > (u.end - 1) / p.block) return -1;
+    if (id < 0 || id > (u.end - 1) / p.block) return {0, 0u};
     t = id * p.block + (at - e * p.block);
   } else {
-    t = at + (u.prefix ? 0 : p.base);
+    t = at + (u.prefix ? 0 : p.base & ~15);
   }
-  if (t >= u.end) return -1;
+  const int n = u.end - t;
+  if (n <= 0) return {0, 0u};
+  uint32_t live = n < 16 ? (1u << n) - 1u : 0xffffu;
+  if (KIND == kSegRange && !u.prefix && t < p.base) live &= 0xffffu << (p.base - t);
   if constexpr (PAGED) {
     const int col = t / p.page_size;
-    int page = load_dependent(u.prefix ? p.prefix_table + col : p.page_table + (size_t)u.b * p.max_pages + col);
+    int page = live ? load_dependent(u.prefix ? p.prefix_table + col : p.page_table + (size_t)u.b * p.max_pages + col) : 0;
     if ((unsigned)page >= (unsigned)p.num_pages) {
       atomicOr(&g_error_word, 4u);
       page = 0;
     }
-    return (((long long)page * p.page_size + (t - col * p.page_size)) * p.Hkv + u.h) * D;
+    return {(((long long)page * p.page_size + (t - col * p.page_size)) * p.Hkv + u.h) * D, live};
   } else {
     const long long row = u.prefix ? t : (long long)u.b * p.ctx + (t - p.base);
-    return (row * p.Hkv + u.h) * D;
+    return {(row * p.Hkv + u.h) * D, live};
   }
 }
 
@@ -362,7 +371,6 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring_s = smem_u32(smem + warp * Gm::WARP_BYTES);
-  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * 4;
 
   // Beside the prefix's kernel there is nothing to wait for: it has written nothing that is read
   // here, and lets this kernel start after its own wait for what came before.  The kernels after this
@@ -376,52 +384,60 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
     return;
   }
 
-  // the load side: where the rows of the next tile to copy lie (lanes 0 .. 15), and of the one after
-  // it; lu and lj are the unit and tile of the latter
+  // the load side: where this warp's tokens of the next tile to copy lie, and of the one after it; lu
+  // and lj are the unit and tile of the latter
   int lj;
   SegUnit lu = walk.at(x0, lj);
   const SegUnit u0 = lu;
   const int start = lj;
   long long lx = x0;
-  long long off, off_next = -1;
-  auto look_up = [&]() {
-    return lane < 16 ? seg_row<D, PAGED, KIND>(p, lu, lj * kTile + warp * 16 + lane) : -1ll;
-  };
-  off = look_up();
-  int ls = 0;       // the next granule's slot
-  bool lv = false;  // it is of values
-  bool ahead = false;  // off_next holds the tile after lx
+  auto look_up = [&]() { return seg_group<D, PAGED, KIND>(p, lu, lj * kTile + warp * 16); };
+  SegGroup now = look_up(), then = {0, 0u};
+  unsigned long long lives = 0ull;  // of the last four tiles, tile x in bits 16 (x % 4) on
+  int ls = 0;          // the next granule's slot
+  bool lv = false;     // it is of values
+  bool ahead = false;  // `then` is of the tile after lx
+  const int row_step = p.Hkv * D;
   auto issue = [&]() {
     if (lx < x1) {
       if (!ahead) {  // (once a tile, with its keys)
         ahead = true;
-        off_next = -1;
+        then.live = 0u;
         if (lx + 1 < x1) {
           if (++lj == walk.end_tile(lu)) {
             lu = walk.next(lu);
             lj = walk.first_tile();
           }
-          off_next = look_up();
+          then = look_up();
         }
+        const int at = 16 * (int)(lx & 3);
+        lives = (lives & ~(0xffffull << at)) | (unsigned long long)now.live << at;
       }
-      const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
-      if (!lv && lane == 0) masks[(int)(lx & 3)] = live;
-      if (live) {
-        const uint32_t dst = ring_s + ls * Gm::GRAN;
+      if (now.live) {
         const __nv_bfloat16* from = lv ? p.v : p.k;
         if (!PAGED && KIND == kSegRange && lx < walk.prefix_tiles()) from = lv ? p.vp : p.kp;
         constexpr int CH = D / 8, RPP = 32 / (CH < 32 ? CH : 32);  // chunks a row, rows a pass
         const int c = lane % CH, r0 = lane / CH;
+        const __nv_bfloat16* src = from + now.off + r0 * row_step + c * 8;
+        const uint32_t dst = ring_s + ls * Gm::GRAN + r0 * Gm::ROWB;
+        if (now.live == 0xffffu) {
 #pragma unroll
-        for (int r = 0; r < 16; r += RPP) {
-          const int row = r + r0;
-          const long long o = __shfl_sync(0xffffffffu, off, row);
-          cp_async16(dst + row * Gm::ROWB + ((c ^ (row & 7)) << 4), from + (o < 0 ? 0 : o) + c * 8, o >= 0);
+          for (int r = 0; r < 16; r += RPP) {
+            cp_async16(dst + r * Gm::ROWB + ((c ^ ((r + r0) & 7)) << 4), src, true);
+            src += RPP * row_step;
+          }
+        } else {
+#pragma unroll 1
+          for (int r = 0; r < 16; r += RPP) {
+            const bool is = (now.live >> (r + r0)) & 1;
+            cp_async16(dst + r * Gm::ROWB + ((c ^ ((r + r0) & 7)) << 4), is ? src : from, is);
+            src += RPP * row_step;
+          }
         }
       }
       if (lv) {
         ++lx;
-        off = off_next;
+        now = then;
         ahead = false;
       }
       lv = !lv;
@@ -471,7 +487,7 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
     slot_at = slot_at + 1 == NG ? 0 : slot_at + 1;
     cp_async_wait<NG - 1>();
     __syncwarp();
-    const uint32_t live = masks[(int)(x & 3)];
+    const uint32_t live = (uint32_t)(lives >> (16 * (int)(x & 3))) & 0xffffu;
     const int mrow = lane & 7, mi = lane >> 3;
     uint32_t pb[NT][2];
     if (live) {
@@ -486,7 +502,7 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[nt], a0, a1, a2, a3, qb[nt][kk][0], qb[nt][kk][1]);
       }
-      const int t0 = (KIND == kSegRange && !u.prefix ? p.base : 0) + j * kTile + warp * 16 + lane / 4;
+      const int t0 = (KIND == kSegRange && !u.prefix ? p.base & ~15 : 0) + j * kTile + warp * 16 + lane / 4;
       float mx[NT][2];
       bool any = false;
 #pragma unroll
@@ -797,7 +813,7 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const _
   }
   const int hq = (int)(row % p.Hq), token = (int)(row / p.Hq);
   const int b = token / p.n, i = token - b * p.n, h = hq / p.G, g = hq - h * p.G;
-  const SegSums sums = seg_sums(p.seq_lens, p.B, p.cap, p.base, b);
+  const SegSums sums = seg_sums(p.seq_lens, p.B, p.cap, p.base & ~15, b);
   const long long tp = p.rt_prefix ? (p.base + kTile - 1) / kTile : 0, wp = (long long)p.Hkv * p.rt_prefix * tp;
   const long long W = wp + sums.all * p.Hkv * p.rt;
   const int used = seg_used(W, p.ctas);
@@ -810,7 +826,7 @@ __global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const _
     na = seg_owner(W, used, (id0 + 1) * tp - 1) - c0 + 1;
   }
   // the rest's
-  const int rr = i * p.G + g, r = rr / p.ru, t = seg_tiles(seg_len(p.seq_lens, b, p.cap), p.cap, p.base);
+  const int rr = i * p.G + g, r = rr / p.ru, t = seg_tiles(seg_len(p.seq_lens, b, p.cap), p.cap, p.base & ~15);
   const long long a1 = wp + sums.before * p.Hkv * p.rt + (long long)(h * p.rt + r) * t;
   const int id1 = p.Hkv * p.rt_prefix + (b * p.Hkv + h) * p.rt + r;
   const int c1 = t ? seg_owner(W, used, a1) : 0, nb = t ? seg_owner(W, used, a1 + t - 1) - c1 + 1 : 0;

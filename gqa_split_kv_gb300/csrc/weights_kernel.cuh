@@ -40,8 +40,7 @@ struct ScoreGeo {
   static constexpr int WARP_BYTES = NSTAGE * STAGE;
   static constexpr int ROWS = 16;  // query rows of a unit
   static constexpr int OFF_ML = WARPS * WARP_BYTES;
-  static constexpr int OFF_MASK = OFF_ML + WARPS * ROWS * 8;
-  static constexpr int OFF_LENS = OFF_MASK + WARPS * NSTAGE * 4;
+  static constexpr int OFF_LENS = OFF_ML + WARPS * ROWS * 8;
   static constexpr int SMEM = OFF_LENS + kSegLens * 4;
   static constexpr int PER_SM = 2;
 };
@@ -88,50 +87,67 @@ struct KeyRing {
   const WeightsParams& wp;
   const SegWalk<kSegRange>& walk;
   uint32_t at;  // of the ring in shared memory
-  volatile uint32_t* masks;
   SegUnit u;
   int j;
-  long long x, x1, off, soff;
+  long long x, x1;
+  unsigned long long lives0, lives1;  // which of the 16 tokens there are, of the last eight tiles: tile x in bits 16 (x % 4) on
+  long long off, soff;          // of the first one's key and scale
+  uint32_t live;
 
-  __device__ __forceinline__ KeyRing(const WeightsParams& wp_, const SegWalk<kSegRange>& walk_, uint32_t at_,
-                                     volatile uint32_t* masks_, long long x0, long long x1_)
-      : wp(wp_), walk(walk_), at(at_), masks(masks_), x(x0), x1(x1_) {
+  __device__ __forceinline__ KeyRing(const WeightsParams& wp_, const SegWalk<kSegRange>& walk_, uint32_t at_, long long x0,
+                                     long long x1_)
+      : wp(wp_), walk(walk_), at(at_), x(x0), x1(x1_), lives0(0ull), lives1(0ull) {
     u = walk.at(x0, j);
     look_up();
+  }
+  __device__ __forceinline__ uint32_t live_of(long long tile) const {
+    const int k = (int)(tile & 7);
+    return (uint32_t)((k < 4 ? lives0 : lives1) >> (16 * (k & 3))) & 0xffffu;
   }
   // int8: rows 2 p and 2 p + 1 of a quarter warp's read in different halves of 128 bytes
   static __device__ __forceinline__ int chunk(int row, int c) {
     return INT8 ? c ^ ((row & 1) << 2) % CH : c ^ (row & 7);
   }
+  // (16 tokens from a multiple of 16 on lie in one page)
   __device__ __forceinline__ void look_up() {
     const SegParams& p = wp.s;
-    const int lane = threadIdx.x & 31, t = j * kTile + (threadIdx.x >> 5) * 16 + lane;
-    off = -1;
-    soff = 0;
-    if (lane < 16 && t < u.end) {
-      const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
-      const int slab_rows = PAGED ? p.page_size : p.ctx;
-      off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)Gm::ROWB;
-      soff = (c.slab * p.Hkv + u.h) * slab_rows + c.at;
-    }
+    const int t = j * kTile + (threadIdx.x >> 5) * 16, n = u.end - t;
+    live = n <= 0 ? 0u : n < 16 ? (1u << n) - 1u : 0xffffu;
+    if (!live) return;
+    const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
+    const int slab_rows = PAGED ? p.page_size : p.ctx;
+    off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)Gm::ROWB;
+    soff = (c.slab * p.Hkv + u.h) * slab_rows + c.at;
   }
   __device__ __forceinline__ void issue(int stage) {
     if (x < x1) {
-      const int lane = threadIdx.x & 31;
-      const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
-      if (lane == 0) masks[stage] = live;
+      const int lane = threadIdx.x & 31, k = (int)(x & 7), bit = 16 * (k & 3);
+      const unsigned long long others = ~(0xffffull << bit), mine = (unsigned long long)live << bit;
+      if (k < 4)
+        lives0 = (lives0 & others) | mine;
+      else
+        lives1 = (lives1 & others) | mine;
       if (live) {
         const uint8_t* keys = reinterpret_cast<const uint8_t*>(wp.s.k);
-        const uint32_t dst = at + stage * Gm::STAGE;
         constexpr int RPP = 32 / (CH < 32 ? CH : 32);
-        const int c = lane % CH, r0 = lane / CH;
+        const int c = lane % CH, r0 = lane / CH, step = wp.s.Hkv * Gm::ROWB;
+        const uint8_t* src = keys + off + r0 * step + c * 16;
+        const uint32_t dst = at + stage * Gm::STAGE + r0 * Gm::ROWB;
+        if (live == 0xffffu) {
 #pragma unroll
-        for (int r = 0; r < 16; r += RPP) {
-          const int row = r + r0;
-          const long long o = __shfl_sync(0xffffffffu, off, row);
-          cp_async16(dst + row * Gm::ROWB + (chunk(row, c) << 4), keys + (o < 0 ? 0 : o) + c * 16, o >= 0);
+          for (int r = 0; r < 16; r += RPP) {
+            cp_async16(dst + r * Gm::ROWB + (chunk(r + r0, c) << 4), src, true);
+            src += RPP * step;
+          }
+        } else {
+#pragma unroll 1
+          for (int r = 0; r < 16; r += RPP) {
+            const bool is = (live >> (r + r0)) & 1;
+            cp_async16(dst + r * Gm::ROWB + (chunk(r + r0, c) << 4), is ? src : keys, is);
+            src += RPP * step;
+          }
         }
-        if (INT8 && off >= 0) cp_async4(dst + 16 * Gm::ROWB + lane * 4, wp.k_scale + soff);
+        if (INT8 && lane < 16 && (live >> lane) & 1) cp_async4(at + stage * Gm::STAGE + 16 * Gm::ROWB + lane * 4, wp.k_scale + soff + lane);
       }
       ++x;
       if (x < x1) {
@@ -206,14 +222,13 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
   const SegParams& p = wp.s;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + Gm::OFF_MASK) + warp * Gm::NSTAGE;
 
   pdl_wait_primary();
   pdl_launch_dependents();
   const SegWalk<kSegRange> walk(p, seg_stage_lens<Gm::THREADS>(p, reinterpret_cast<int*>(smem + Gm::OFF_LENS)));
   long long x0, x1;
   if (!walk.range(blockIdx.x, x0, x1)) return;
-  Ring ring(wp, walk, smem_u32(smem + warp * Gm::WARP_BYTES), masks, x0, x1);
+  Ring ring(wp, walk, smem_u32(smem + warp * Gm::WARP_BYTES), x0, x1);
   SegUnit u = ring.u;
   int j = ring.j;
 #pragma unroll 1
@@ -245,7 +260,7 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
     }
     cp_async_wait<Gm::NSTAGE - 1>();
     __syncwarp();
-    const uint32_t live = masks[stage];
+    const uint32_t live = ring.live_of(x);
     if (live) {
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       float mx[2] = {kNegInf, kNegInf};
