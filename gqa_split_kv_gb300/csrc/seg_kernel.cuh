@@ -89,14 +89,14 @@ struct SegGeo {
   static constexpr int ROWS = 8 * NT;           // query rows of a unit
   static constexpr int ROWB = 2 * D;            // a row of K or V
   static constexpr int GRAN = 16 * ROWB;        // 16 tokens of one of them; also 8 rows of O in fp32
-  static constexpr int NG = D == 64 ? 5 : 3;    // of them in a warp's ring
+  static constexpr int NG = D == 64 ? 5 : D == 256 ? 2 : 3;  // of them in a warp's ring
   static constexpr int WARP_BYTES = NG * GRAN;
   static constexpr int OFF_ML = WARPS * WARP_BYTES;
   static constexpr int OFF_FOLD = OFF_ML + WARPS * ROWS * 8;
   static constexpr int OFF_LENS = OFF_FOLD + ROWS * (int)sizeof(FoldRow);
   static constexpr int OFF_RES = OFF_LENS + kSegLens * 4;  // blocks: this CTA's (m, l) and O, for the cluster
   static constexpr int SMEM = OFF_RES + (KIND == kSegBlocks ? ROWS * (8 + D * 4) : 0);
-  static constexpr int PER_SM = D == 256 ? 2 : NT == 1 ? 4 : 3;
+  static constexpr int PER_SM = D == 256 ? 3 : NT == 1 ? 4 : 3;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
