@@ -127,7 +127,7 @@ struct SelectParams {
   int qt;       // query tokens a CTA (cluster)
   int cluster;  // CTAs that share the blocks' scores
 };
-constexpr int kSelectThreads = 256;
+constexpr int kSelectThreads = 256;   // a CTA; 128 where there are many queries of few blocks
 constexpr int kSelectTokens = 16;     // a CTA, at most
 constexpr int kSelectBlocks = 8192;
 
@@ -181,12 +181,13 @@ __host__ __device__ inline size_t select_smem(int qt, int max_blocks) {
   return (size_t)max_blocks * 10 + (size_t)qt * (max_blocks + words + 256) * 4 + 16;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const __grid_constant__ SelectParams p) {
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) block_select_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int WARPS = kSelectThreads / 32;
+  constexpr int WARPS = THREADS / 32;
   __shared__ uint32_t s_mean2, s_q2[kSelectTokens];  // bits of the largest squares of norms
-  __shared__ uint32_t s_prefix[kSelectTokens], s_low[kSelectTokens], s_below[kSelectTokens];
+  __shared__ uint32_t s_base[kSelectTokens], s_top[kSelectTokens], s_low[kSelectTokens], s_below[kSelectTokens];
+  __shared__ int s_shift[kSelectTokens];
   __shared__ int s_left[kSelectTokens], s_open[kSelectTokens], s_count, s_sure, s_busy;
   const int words = (p.max_blocks + 31) / 32;
   unsigned long long* exact = reinterpret_cast<unsigned long long*>(smem);
@@ -203,8 +204,8 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
   const int qn = min(p.qt, p.n - i0);  // query tokens here
   const int rows = qn * p.G;
   const __nv_bfloat16* means = p.means + ((size_t)b * p.Hkv + h) * p.max_blocks * D;
-  for (int e = threadIdx.x; e < qn * p.max_blocks; e += kSelectThreads) keys[e] = 0u;
-  for (int e = threadIdx.x; e < qn * words; e += kSelectThreads) bits[e] = 0u;
+  for (int e = threadIdx.x; e < qn * p.max_blocks; e += THREADS) keys[e] = 0u;
+  for (int e = threadIdx.x; e < qn * words; e += THREADS) bits[e] = 0u;
   if (threadIdx.x < kSelectTokens) s_q2[threadIdx.x] = 0u;
   if (threadIdx.x == 0) {
     s_mean2 = 0u;
@@ -301,38 +302,61 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
   };
   auto take = [&](int qi, int j) { atomicOr(&bits[qi * words + (j >> 5)], 1u << (j & 31)); };
 
-  // The border of each query, 8 bits of the keys at a time from the top: how many keys have
-  // each value of the 8 bits (and the bits found so far), and in which value the need-th
-  // largest lies; done when all keys of that value are taken.  All queries go side by side, a
-  // group of `size` threads each.
-  const int size = kSelectThreads / (qn <= 1 ? 1 : qn <= 2 ? 2 : qn <= 4 ? 4 : qn <= 8 ? 8 : 16);
+  // The border of each query: the keys' range is cut into up to 256 equal bins, whose keys are counted;
+  // the bin in which the need-th largest lies is the next range, until all keys of that bin are taken
+  // (scores spread, so twice as a rule; four times at most).  All queries go side by side, a group of
+  // `size` threads each.
+  const int size = THREADS / (qn <= 1 ? 1 : qn <= 2 ? 2 : qn <= 4 ? 4 : qn <= 8 ? 8 : 16);
   const int mine = threadIdx.x / size, me = threadIdx.x % size;
   const Want my = mine < qn ? want(mine) : Want{0, 0, 0, 0};
   const uint32_t* key = keys + (size_t)mine * p.max_blocks;
   for (int j = me; j < my.visible; j += size)
     if (my.need < 0 || j < my.lo || j >= my.hi) take(mine, j);
+  // the least and the largest number that a group brings, into two words
+  auto extremes = [&](uint32_t least, uint32_t most, uint32_t* to_least, uint32_t* to_most) {
+    if (size >= 32) {  // a warp is of one group
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+    }
+    if (size < 32 || lane == 0) {
+      atomicMin(to_least, least);
+      atomicMax(to_most, most);
+    }
+  };
   if (me == 0 && mine < qn) {
-    s_prefix[mine] = 0u;
+    s_base[mine] = s_low[mine] = 0xffffffffu;
+    s_top[mine] = s_below[mine] = 0u;
     s_left[mine] = my.need;
-    s_low[mine] = 0xffffffffu;
-    s_below[mine] = 0u;
   }
-  for (int e = threadIdx.x; e < qn * 256; e += kSelectThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < qn * 256; e += THREADS) hist[e] = 0;
   if (threadIdx.x == 0) s_busy = 0;
   __syncthreads();
+  if (my.need > 0) {
+    uint32_t least = 0xffffffffu, most = 0u;
+    for (int j = my.lo + me; j < my.hi; j += size) {
+      least = min(least, key[j]);
+      most = max(most, key[j]);
+    }
+    extremes(least, most, &s_base[mine], &s_top[mine]);
+  }
+  __syncthreads();
   bool searching = my.need > 0;
-  int shift = 24;
-  for (; shift >= 0; shift -= 8) {
+  int shift = searching ? max(0, 24 - __clz((int)(s_top[mine] - s_base[mine]))) : 0;
+  uint32_t bins = 256u;  // of the range
+  for (;;) {
     if (searching) {
-      const uint32_t prefix = s_prefix[mine];
-      for (int j = my.lo + me; j < my.hi; j += size)
-        if (shift == 24 || (key[j] ^ prefix) >> (shift + 8) == 0u) atomicAdd(&hist[mine * 256 + (key[j] >> shift & 255u)], 1);
+      const uint32_t base = s_base[mine];
+      if (me == 0) s_shift[mine] = shift;
+      for (int j = my.lo + me; j < my.hi; j += size) {
+        const uint32_t bin = (key[j] - base) >> shift;
+        if (key[j] >= base && bin < bins) atomicAdd(&hist[mine * 256 + bin], 1);
+      }
     }
     __syncthreads();
     for (int qi = warp; qi < qn; qi += WARPS) {
       const int left = s_left[qi];
       if (left <= 0) continue;
-      // lane l has values 255 - 8 l .. 248 - 8 l
+      // lane l has bins 255 - 8 l .. 248 - 8 l
       int c[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -351,10 +375,11 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (at < left && at + c[i] >= left) {
-            s_prefix[qi] |= (uint32_t)(255 - 8 * lane - i) << shift;
-            // all keys of this value are taken (or it is one key): their lowest is the border
-            s_left[qi] = at + c[i] == left ? 0 : left - at;
-            if (at + c[i] != left) s_busy = 1;
+            s_base[qi] += (uint32_t)(255 - 8 * lane - i) << s_shift[qi];
+            // all keys of this bin are taken: their lowest is the border; one value: some of equal keys are not
+            const bool all = at + c[i] == left;
+            s_left[qi] = all ? 0 : s_shift[qi] == 0 ? -(left - at) : left - at;
+            if (!all && s_shift[qi] > 0) s_busy = 1;
             break;
           }
           at += c[i];
@@ -365,13 +390,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
     __syncthreads();
     const bool busy = s_busy;
     searching = searching && s_left[min(mine, qn - 1)] > 0;
+    bins = shift >= 8 ? 256u : 1u << shift;
+    shift = max(0, shift - 8);
     __syncthreads();
     if (threadIdx.x == 0) s_busy = 0;
     if (!busy) break;
   }
   // the lowest key taken, and the largest below it; a query with something left has equal keys on both sides
   if (my.need > 0) {
-    const uint32_t from = s_prefix[mine];  // bits not looked at are 0
+    const uint32_t from = s_base[mine];
     uint32_t low = 0xffffffffu, below = 0u;
     for (int j = my.lo + me; j < my.hi; j += size) {
       const uint32_t k = key[j];
@@ -380,20 +407,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
       else
         below = max(below, k);
     }
-    if (size >= 32) {  // a warp is of one group
-      low = __reduce_min_sync(0xffffffffu, low);
-      below = __reduce_max_sync(0xffffffffu, below);
-    }
-    if (size < 32 || lane == 0) {
-      atomicMin(&s_low[mine], low);
-      atomicMax(&s_below[mine], below);
-    }
+    extremes(low, below, &s_low[mine], &s_below[mine]);
   }
   __syncthreads();
   if (my.need > 0) {
     const float mu = select_slack<D>(s_q2[mine], s_mean2);
     const uint32_t low = s_low[mine];
-    if (s_left[mine] <= 0 && key_float(low) - key_float(s_below[mine]) > 2.f * mu) {
+    if (s_left[mine] == 0 && key_float(low) - key_float(s_below[mine]) > 2.f * mu) {
       for (int j = my.lo + me; j < my.hi; j += size)
         if (key[j] >= low) take(mine, j);
     } else if (me == 0) {
@@ -412,7 +432,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
     __syncthreads();
     if (threadIdx.x == 0) s_count = s_sure = 0;
     __syncthreads();
-    for (int j = w.lo + threadIdx.x; j < w.hi; j += kSelectThreads) {
+    for (int j = w.lo + threadIdx.x; j < w.hi; j += THREADS) {
       const float s = key_float(key[j]);
       if (s > border + 2.f * mu) {
         take(qi, j);
@@ -424,27 +444,37 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
       }
     }
     __syncthreads();
-    // a warp a (candidate, head): the largest of the heads' scores, ordered by their bits
+    // half a warp a (candidate, head): the largest of the heads' scores, ordered by their bits
     const int count = s_count, left = w.need - s_sure;
     const __nv_bfloat16* q = p.q + (((size_t)b * p.n + i0 + qi) * p.Hq + h * p.G) * D;
-    for (int e = warp; e < count * p.G; e += WARPS) {
-      const int c = e / p.G, g = e - c * p.G;
-      const __nv_bfloat16* mean = means + (size_t)list[c] * D;
+    const int half = lane >> 4, hl = lane & 15;
+    for (int e0 = 2 * warp; e0 < count * p.G; e0 += 2 * WARPS) {
+      const int e = min(e0 + half, count * p.G - 1), c = e / p.G, g = e - c * p.G;
+      const uint4* a = reinterpret_cast<const uint4*>(q + g * D) + hl;
+      const uint4* m = reinterpret_cast<const uint4*>(means + (size_t)list[c] * D) + hl;
       float s = 0.f, e2 = 0.f;  // a sum and what its additions rounded off
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-        add_exactly(s, e2, __bfloat162float(load_dependent(q + g * D + d * 32 + lane)) *
-                               __bfloat162float(load_dependent(mean + d * 32 + lane)));
+      for (int d = 0; d < (D + 127) / 128; ++d) {
+        if (D >= 128 || hl < D / 8) {
+          const uint4 x = load_dependent(a + 16 * d), y = load_dependent(m + 16 * d);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int d = 16; d; d >>= 1) {
+          for (int i = 0; i < 4; ++i) {
+            add_exactly(s, e2, bf16lo_to_f32(xs[i]) * bf16lo_to_f32(ys[i]));
+            add_exactly(s, e2, bf16hi_to_f32(xs[i]) * bf16hi_to_f32(ys[i]));
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 8; d; d >>= 1) {
         const float os = __shfl_xor_sync(0xffffffffu, s, d), oe = __shfl_xor_sync(0xffffffffu, e2, d);
         add_exactly(s, e2, os);
         e2 += oe;
       }
-      if (lane == 0) atomicMax(&exact[c], double_key((double)s + (double)(s - s == 0.f ? e2 : 0.f)));
+      if (hl == 0) atomicMax(&exact[c], double_key((double)s + (double)(s - s == 0.f ? e2 : 0.f)));
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < count; c += kSelectThreads) {
+    for (int c = threadIdx.x; c < count; c += THREADS) {
       const unsigned long long s = exact[c];
       const int j = list[c];
       int before = 0;
@@ -455,7 +485,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) block_select_kernel(const _
   }
 
   // the numbers of the bits, ascending
-  for (int qi = warp; qi < qn; qi += kSelectThreads / 32) {
+  for (int qi = warp; qi < qn; qi += THREADS / 32) {
     int* dst = p.out + (((size_t)b * p.n + i0 + qi) * p.Hkv + h) * p.pick;
     int at = 0;
     for (int w0 = 0; w0 < words; w0 += 32) {

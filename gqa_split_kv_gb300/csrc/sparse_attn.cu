@@ -65,11 +65,18 @@ MeansParams means_params(const void* k, const int* seq_lens, int batch, int q_le
 
 // ---------------------------------------------------------------- selection
 
+template <int D, int THREADS>
+int launch_select_by(const SelectParams& p, long long units, cudaStream_t st) {
+  if (int e = allow_smem<block_select_kernel<D, THREADS>>(200 * 1024)) return e;
+  return launch_clusters(block_select_kernel<D, THREADS>, (unsigned)(units * p.cluster), THREADS,
+                         select_smem(p.qt, p.max_blocks), p.cluster, st, p);
+}
 template <int D>
-int launch_select(const SelectParams& p, long long units, cudaStream_t st) {
-  const size_t smem = select_smem(p.qt, p.max_blocks);
-  if (int e = allow_smem<block_select_kernel<D>>(200 * 1024)) return e;
-  return launch_clusters(block_select_kernel<D>, (unsigned)(units * p.cluster), kSelectThreads, smem, p.cluster, st, p);
+int launch_select(const SelectParams& p, long long units, int sms, cudaStream_t st) {
+  // a CTA's time is its chain of steps; with several rounds of CTAs and no more than 4 steps of 8 blocks a warp,
+  // twice as many small ones run at once
+  if (units > 2LL * sms && p.max_blocks <= 4 * 8 * 4) return launch_select_by<D, kSelectThreads / 2>(p, units, st);
+  return launch_select_by<D, kSelectThreads>(p, units, st);
 }
 
 // Heads that a call of this family takes.
@@ -220,9 +227,9 @@ extern "C" int block_select(const void* q, const void* means, const int* seq_len
     p.cluster *= 2;
   if (units * p.cluster > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return head_dim == 64    ? launch_select<64>(p, units, st)
-         : head_dim == 128 ? launch_select<128>(p, units, st)
-                           : launch_select<256>(p, units, st);
+  return head_dim == 64    ? launch_select<64>(p, units, sms, st)
+         : head_dim == 128 ? launch_select<128>(p, units, sms, st)
+                           : launch_select<256>(p, units, sms, st);
 }
 
 extern "C" int sparse_attn_contig(const void* q, const void* k, const void* v, const int* blocks, const int* seq_lens,
