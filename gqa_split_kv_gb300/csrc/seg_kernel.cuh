@@ -805,7 +805,7 @@ constexpr int kMergeThreads = 256;
 // before the wait: the kernels that wrote them were done before seg_kernel, and prefix_tc_kernel
 // before it, let anything start.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) seg_merge_prefix_kernel(const __grid_constant__ SegParams p) {
+__global__ void __launch_bounds__(kMergeThreads, D == 256 ? 2 : 4) seg_merge_prefix_kernel(const __grid_constant__ SegParams p) {
   const long long row = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
   if (row >= (long long)p.B * p.n * p.Hq) {
     pdl_wait_primary();
