@@ -218,10 +218,10 @@ constexpr int kMoveThreads = 256;
 // weights of one (sequence, head).  In place it goes forward in steps: a row moves to its own
 // place or a lower one, so a step's sources lie at or past its targets and past every earlier
 // step's; all of a step are loaded before the first is stored.  Byte traffic bounds it, and for
-// few rows the chain of kept position, page and row: 16 bytes a thread, 8 of them in flight.
+// few rows the chain of kept position, page and row: 16 bytes a thread, 4 of them in flight.
 template <bool PAGED>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p) {
-  constexpr int U = 8;
+  constexpr int U = 4;
   pdl_wait_primary();
   const int tensors = p.v ? 2 : 1, copies = tensors * p.columns * p.parts, rolls = copies + 3;
   const int unit = blockIdx.x / rolls, role = blockIdx.x % rolls;

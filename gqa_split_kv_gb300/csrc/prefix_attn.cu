@@ -128,7 +128,10 @@ int launch_prefix(PrefixCall& c, const PrefixShape& s, cudaStream_t st) {
     p.beside = 1;
     if (int e = launch_tc<D>(c, t, st)) return e;
   }
-  if (int e = c.paged ? launch_seg<D, true, kSegRange>(p, st) : launch_seg<D, false, kSegRange>(p, st)) return e;
+  const bool edges = p.n > 1 || p.rt_prefix > 0;
+  if (int e = c.paged ? (edges ? launch_seg<D, true, kSegEdges>(p, st) : launch_seg<D, true, kSegRange>(p, st))
+                      : (edges ? launch_seg<D, false, kSegEdges>(p, st) : launch_seg<D, false, kSegRange>(p, st)))
+    return e;
   return launch_dependent(seg_merge_prefix_kernel<D>,
                           (unsigned)(((long long)p.B * p.n * p.Hq + kMergeThreads / 32 - 1) / (kMergeThreads / 32)),
                           kMergeThreads, 0, st, p);

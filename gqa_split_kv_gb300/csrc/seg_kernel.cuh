@@ -48,7 +48,9 @@ __device__ __forceinline__ uint32_t float_key(float f) {
 constexpr int kSegCluster = 16;  // CTAs that may share a blocks unit
 constexpr int kSegLens = 512;  // lengths that a CTA copies to its shared memory
 
-enum SegKind { kSegRange = 0, kSegBlocks = 1 };
+// Ranges of one new token each (every row of a unit sees all of its tokens), of several or of a whole batch's
+// prefix (a row may see fewer), and blocks.
+enum SegKind { kSegRange = 0, kSegBlocks = 1, kSegEdges = 2 };
 
 struct SegParams {
   const __nv_bfloat16* q;      // [B, n, Hq, D]
@@ -95,7 +97,8 @@ struct SegGeo {
   static constexpr int OFF_FOLD = OFF_ML + WARPS * ROWS * 8;
   static constexpr int OFF_LENS = OFF_FOLD + ROWS * (int)sizeof(FoldRow);
   static constexpr int OFF_RES = OFF_LENS + kSegLens * 4;  // blocks: this CTA's (m, l) and O, for the cluster
-  static constexpr int SMEM = OFF_RES + (KIND == kSegBlocks ? ROWS * (8 + D * 4) : 0);
+  static constexpr int OFF_ODD = OFF_RES;                  // edges: see there
+  static constexpr int SMEM = OFF_RES + (KIND == kSegBlocks ? ROWS * (8 + D * 4) : KIND == kSegEdges ? 4 + ROWS * (D + 4) : 0);
   static constexpr int PER_SM = D == 256 ? 3 : NT == 1 ? 4 : 3;
 };
 
@@ -316,7 +319,7 @@ __device__ __forceinline__ SegGroup seg_group(const SegParams& p, const SegUnit&
   const int n = u.end - t;
   if (n <= 0) return {0, 0u};
   uint32_t live = n < 16 ? (1u << n) - 1u : 0xffffu;
-  if (KIND == kSegRange && !u.prefix && t < p.base) live &= 0xffffu << (p.base - t);
+  if (KIND != kSegBlocks && !u.prefix && t < p.base) live &= 0xffffu << (p.base - t);
   if constexpr (PAGED) {
     const int col = t / p.page_size;
     int page = live ? load_dependent(u.prefix ? p.prefix_table + col : p.page_table + (size_t)u.b * p.max_pages + col) : 0;
@@ -354,6 +357,12 @@ __device__ __forceinline__ bool seg_query(const SegParams& p, const int* lens, c
     lim = (u.prefix ? seg_len(lens, b, p.cap) : u.len) - p.n + 1 + (u.prefix ? i - b * p.n : i);
     return true;
   }
+}
+
+// The sum of values that are not finite: infinities of one sign, else NaN; 0 of none.
+__device__ __forceinline__ float odd_value(uint32_t marks) {
+  marks &= 7u;
+  return marks == 0u ? 0.f : marks == 1u ? -kNegInf : marks == 2u ? kNegInf : __int_as_float(0x7fffffff);
 }
 
 // An 8 x 8 matrix of 16-bit elements, lane l holding row l / 4, columns 2 (l % 4) and the next: its transpose.
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
       }
       if (now.live) {
         const __nv_bfloat16* from = lv ? p.v : p.k;
-        if (!PAGED && KIND == kSegRange && lx < walk.prefix_tiles()) from = lv ? p.vp : p.kp;
+        if (!PAGED && KIND != kSegBlocks && lx < walk.prefix_tiles()) from = lv ? p.vp : p.kp;
         constexpr int CH = D / 8, RPP = 32 / (CH < 32 ? CH : 32);  // chunks a row, rows a pass
         const int c = lane % CH, r0 = lane / CH;
         const __nv_bfloat16* src = from + now.off + r0 * row_step + c * 8;
@@ -452,10 +461,18 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
   for (int s = 0; s < NG; ++s) issue();
 
   // column n of an MMA is the unit's row 8 nt + n; this lane's columns are 2 (lane % 4) and the next
+  // values that are not finite, where not every row sees them: whether there are any in this unit, then 8 bits a
+  // (row, element); and the tokens that each row sees
+  uint32_t* odd_values = reinterpret_cast<uint32_t*>(smem + Gm::OFF_ODD);
+  int* row_lims = reinterpret_cast<int*>(smem + Gm::OFF_ODD) + 1 + Gm::ROWS * D / 4;
+  if constexpr (KIND == kSegEdges)
+    for (int e = threadIdx.x; e < 1 + Gm::ROWS * D / 4; e += Gm::THREADS) odd_values[e] = 0u;
+
   uint32_t qb[NT][D / 16][2];
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];
   int lim[NT][2];
+  int some_see = 0;  // tokens that every row sees which sees any
   bool fresh = true;
   int slot_at = 0;  // of the granule that is read next
   for (long long x = x0; x < x1; ++x) {
@@ -477,8 +494,26 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
         for (int e = 0; e < 2; ++e) {
           m[nt][e] = kNegInf;
           l[nt][e] = 0.f;
-          if (KIND == kSegRange) seg_query<KIND>(p, walk.lens, u, 8 * nt + 2 * (lane % 4) + e, token, g, lim[nt][e]);
+          if (KIND == kSegEdges && !seg_query<KIND>(p, walk.lens, u, 8 * nt + 2 * (lane % 4) + e, token, g, lim[nt][e]))
+            lim[nt][e] = 0x7fffffff;  // no row
         }
+      }
+      if constexpr (KIND == kSegEdges) {
+        int seen = 0x7fffffff;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (lim[nt][e] > 0) seen = min(seen, lim[nt][e]);
+        if (warp == 0 && lane < 4) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            row_lims[8 * nt + 2 * lane] = lim[nt][0];
+            row_lims[8 * nt + 2 * lane + 1] = lim[nt][1];
+          }
+        }
+        __syncthreads();
+        some_see = __reduce_min_sync(0xffffffffu, seen);
       }
     }
     const bool last = j + 1 == walk.end_tile(u), join = last || x + 1 == x1;
@@ -490,6 +525,7 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
     const uint32_t live = (uint32_t)(lives >> (16 * (int)(x & 3))) & 0xffffu;
     const int mrow = lane & 7, mi = lane >> 3;
     uint32_t pb[NT][2];
+    const int g0 = (KIND != kSegBlocks && !u.prefix ? p.base & ~15 : 0) + j * kTile + warp * 16;  // the warp's first token
     if (live) {
       float s[NT][4];
 #pragma unroll
@@ -502,7 +538,7 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[nt], a0, a1, a2, a3, qb[nt][kk][0], qb[nt][kk][1]);
       }
-      const int t0 = (KIND == kSegRange && !u.prefix ? p.base & ~15 : 0) + j * kTile + warp * 16 + lane / 4;
+      const int t0 = g0 + lane / 4;
       float mx[NT][2];
       bool any = false;
 #pragma unroll
@@ -512,7 +548,7 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             bool see = (live >> (lane / 4 + 8 * hf)) & 1;
-            if (KIND == kSegRange) see = see && t0 + 8 * hf < lim[nt][e];
+            if (KIND == kSegEdges) see = see && t0 + 8 * hf < lim[nt][e];
             s[nt][2 * hf + e] = see ? s[nt][2 * hf + e] * p.scale_log2 : kNegInf;
           }
           float t = fmaxf(s[nt][e], s[nt][2 + e]);
@@ -564,6 +600,38 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
     else
       cp_async_wait<NG - 1>();
     __syncwarp();
+    if (KIND == kSegEdges && live && g0 + 16 > some_see) {
+      // Tokens that some rows see and others do not: a weight of 0 times an infinity or NaN would reach the
+      // others.  Such values leave the products, and the rows that see them are marked.
+      uint32_t odd = 0u;  // an exponent of ones carries into the bit above it
+#pragma unroll
+      for (int c = 0; c < 16 * D / 8; c += 32) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(vst + (c + lane) * 16));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) odd |= (w[k] & 0x7f807f80u) + 0x00800080u;
+      }
+      const bool any = __any_sync(0xffffffffu, odd & 0x80008000u);
+#pragma unroll 1
+      for (int c = lane; any && c < 16 * D / 8; c += 32) {
+        const int t = c / (D / 8), d0 = ((c % (D / 8)) ^ (t & 7)) * 8;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          uint16_t* at = reinterpret_cast<uint16_t*>(smem + warp * Gm::WARP_BYTES + v_slot * Gm::GRAN + c * 16) + k;
+          const uint32_t v = *at;
+          if ((v & 0x7f80u) != 0x7f80u) continue;
+          *at = 0;
+          if (!((live >> t) & 1)) continue;
+          odd_values[0] = 1u;
+          const uint32_t mark = v & 0x7fu ? 4u : v >> 15 ? 2u : 1u;  // NaN, -inf, inf
+          for (int n = 0; n < Gm::ROWS; ++n)
+            if (g0 + t < row_lims[n]) atomicOr(&odd_values[1 + (n * D + d0 + k) / 4], mark << 8 * (k & 3));
+        }
+      }
+      __syncwarp();
+    }
     if (live) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -652,6 +720,13 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
           a.z += f.f[w] * y.z;
           a.w += f.f[w] * y.w;
         }
+        if (KIND == kSegEdges && odd_values[0]) {
+          const uint32_t marks = odd_values[1 + (r * D + c) / 4];
+          a.x += odd_value(marks);
+          a.y += odd_value(marks >> 8);
+          a.z += odd_value(marks >> 16);
+          a.w += odd_value(marks >> 24);
+        }
         if (whole)
           *reinterpret_cast<uint2*>(p.out + f.out + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
         else if (KIND == kSegBlocks)
@@ -691,6 +766,11 @@ __global__ void __launch_bounds__(SegGeo<D, NT, KIND>::THREADS, SegGeo<D, NT, KI
         }
         cluster_sync();  // no CTA writes its own again, or leaves, before all have read it
       } else {
+        __syncthreads();
+      }
+      if (KIND == kSegEdges && odd_values[0]) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < 1 + Gm::ROWS * D / 4; e += Gm::THREADS) odd_values[e] = 0u;
         __syncthreads();
       }
       issue();

@@ -98,6 +98,24 @@ def test_scales(scale):
     s.check(s.run(scale=scale), scale)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 8, 4), (128, 8, 2), (256, 12, 2), (128, 20, 1)])
+@pytest.mark.parametrize("B", [1, 9])
+def test_values_that_a_row_does_not_see_do_not_reach_it(D, Hq, Hkv, B):
+    """Infinities and NaN in the keys and values of new tokens: only the tokens from them on are touched."""
+    n, P = 5, 70
+    lens = [P + 3 + 17 * b + n for b in range(B)]
+    s = Shared(D + B, P, lens, n, Hq, Hkv, D)
+    clean = s.run()
+    for x, bad in ((s.c.v, float("inf")), (s.c.v, float("nan")), (s.c.k, float("nan"))):
+        keep = x.clone()
+        for b, L in enumerate(lens):
+            x[b, L - P - 2, :, 3:9] = bad  # the last token but one
+        out = s.run()
+        assert torch.equal(out[:, :n - 2], clean[:, :n - 2])
+        assert not torch.isfinite(out[:, n - 2:]).all(-1).any()
+        x.copy_(keep)
+
+
 def test_no_prefix_and_no_rest():
     s = Shared(6, 0, [5, 300], 2, 4, 2, 64)
     s.check(s.run())
