@@ -40,7 +40,7 @@ struct WeightsShape {
 int weights_shape(int B, int n, int Hq, int Hkv, long long cap, int sms, WeightsShape* s) {
   if (B < 0 || n < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || cap < 0) return DA_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
-  if (G > 64 || Hq > 65536 || cap > 0x7fffffffLL - kTile || product(n, G) > kWeightRows || product(B, Hkv) > 0x3fffffffLL)
+  if (G > 64 || Hq > 65536 || cap > kMostTokens || product(n, G) > kWeightRows || product(B, Hkv) > 0x3fffffffLL)
     return DA_ERR_UNSUPPORTED;
   s->rows = n * G;
   s->slots = (long long)B * Hkv + 2ll * sms;
@@ -177,7 +177,8 @@ int evict_call(EvictParams& p, bool paged, bool int8, int head_dim, long long ca
     return DA_ERR_INVALID_ARG;
   if (paged && (p.slab <= 0 || p.max_pages < 0 || p.num_pages < 0)) return DA_ERR_INVALID_ARG;
   p.row_bytes = head_dim * (int8 ? 1 : 2);
-  if (head_dim > 1024 || p.Hkv > 1024 || p.row_bytes % 16 || cap > 0x7fffffffLL - 1024 ||
+  if (head_dim > 1024 || p.Hkv > 1024 || p.row_bytes % 16 || cap > kMostTokens - 4096 || p.keep > kMostTokens - 4096 ||
+      p.out_ctx > kMostTokens ||
       product(p.B, p.Hkv) > 0x7fffffffLL / 1024)
     return DA_ERR_UNSUPPORTED;
   p.in_place = !p.k_out && !p.v_out && !p.ks_out && !p.vs_out && !p.weights_out;
@@ -231,7 +232,7 @@ int evict_call(EvictParams& p, bool paged, bool int8, int head_dim, long long ca
     while (chunks % (2 * p.columns) == 0 && chunks / p.columns >= 4 && (long long)units * tensors * p.columns < 4LL * sms)
       p.columns *= 2;
   } else {
-    while (p.parts < 64 && (long long)units * tensors * p.parts < 8LL * sms && p.keep / (2 * p.parts) * chunks >= kMoveThreads)
+    while (p.parts < 64 && (long long)units * tensors * p.parts < 8LL * sms && (long long)p.keep / (2 * p.parts) * chunks >= kMoveThreads)
       p.parts *= 2;
   }
   const long long grid = (long long)units * (tensors * p.columns * p.parts + 3);

@@ -143,7 +143,7 @@ int prefix_call(PrefixCall& c, float scale, void* stream) {
   int dev, sms, optin;
   if (int e = prefix_shape(p.B, p.n, p.Hq, p.Hkv, c.D, 1, &s)) return e;
   if (p.base < 0 || c.cap < 0 || !std::isfinite(scale)) return DA_ERR_INVALID_ARG;
-  if (c.cap > 0x7fffffffLL - kTile) return DA_ERR_UNSUPPORTED;
+  if (c.cap > kMostTokens) return DA_ERR_UNSUPPORTED;
   if (c.paged && (p.page_size <= 0 || p.max_pages < 0 || p.num_pages < 0)) return DA_ERR_INVALID_ARG;
   if (c.paged && p.page_size % 16) return DA_ERR_UNSUPPORTED;
   if (p.B == 0 || p.n == 0) return DA_OK;

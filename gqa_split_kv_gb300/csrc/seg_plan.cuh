@@ -2,9 +2,10 @@
 // head and 16 of its query rows, say) of whole tiles of 64 tokens; the tiles of all units
 // stand in one line, and CTA c of n takes [c W / n, (c + 1) W / n) of its W tiles (n at most
 // W, so that each has some).  So every CTA has the same number of tiles, whatever the lengths,
-// and a unit is cut only where a CTA's range ends in it: its pieces are those of consecutive CTAs.  A CTA's share of a unit is a piece; piece (unit u, CTA c) has slot
-// u + c of the partials: along the line u or c grows from one piece to the next, so no two
-// share a slot, and units + n slots hold them all.
+// and a unit
+// is cut only where a CTA's range ends in it: its pieces are those of consecutive CTAs.  Piece (unit u,
+// CTA c) has slot u + c of the partials: along the line u or c grows from one piece to the next, so no
+// two share a slot, and units + n slots hold them all.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -12,6 +13,7 @@
 namespace da {
 
 constexpr int kTile = 64;  // tokens
+constexpr long long kMostTokens = 0x7fffffffLL - 1024;  // of a sequence: tiles and strides past the last fit 32 bits
 
 // a / b of numbers that are not negative; most fit 32 bits, whose division is several times as fast.
 __host__ __device__ __forceinline__ long long seg_div(long long a, long long b) {

@@ -22,7 +22,7 @@ namespace {
 int means_call(MeansParams& p, bool paged, long long cap, cudaStream_t st) {
   if (p.B < 0 || p.n < 0 || p.Hkv <= 0 || p.D <= 0 || cap < 0 || p.block <= 0 || p.max_blocks < 0)
     return DA_ERR_INVALID_ARG;
-  if (p.D % 8 || p.D > 1024 || p.Hkv > 1024 || cap > 0x7fffffffLL - p.block) return DA_ERR_UNSUPPORTED;
+  if (p.D % 8 || p.D > 1024 || p.Hkv > 1024 || cap > kMostTokens - p.block) return DA_ERR_UNSUPPORTED;
   if (paged && (p.page_size <= 0 || p.max_pages < 0 || p.num_pages < 0)) return DA_ERR_INVALID_ARG;
   if (p.block > 65536 || (paged && product(p.num_pages, p.page_size) > 0xffffffffLL)) return DA_ERR_UNSUPPORTED;
   // tokens past the last block have no mean
@@ -106,8 +106,8 @@ int sparse_call(SparseCall& c, float scale, cudaStream_t st) {
   if (int e = check_heads(p.B, p.n, p.Hq, p.Hkv, c.D)) return e;
   if (c.cap < 0 || p.pick <= 0 || p.block <= 0 || !std::isfinite(scale)) return DA_ERR_INVALID_ARG;
   if (c.paged && (p.page_size <= 0 || p.max_pages < 0 || p.num_pages < 0)) return DA_ERR_INVALID_ARG;
-  if (p.block % 16 || p.block > 65536 || (long long)p.pick * p.block > 0x7fffffffLL - kTile ||
-      c.cap > 0x7fffffffLL - p.block || (c.paged && p.page_size % 16))
+  if (p.block % 16 || p.block > 65536 || (long long)p.pick * p.block > kMostTokens ||
+      c.cap > kMostTokens - p.block || (c.paged && p.page_size % 16))
     return DA_ERR_UNSUPPORTED;
   if (p.B == 0 || p.n == 0) return DA_OK;
   p.cap = c.paged && p.num_pages == 0 ? 0 : (int)c.cap;
@@ -191,7 +191,7 @@ extern "C" int block_select(const void* q, const void* means, const int* seq_len
   if (int e = check_heads(batch, q_len, num_q_heads, num_kv_heads, head_dim)) return e;
   if (block_size <= 0 || max_blocks < 0 || n_select <= 0 || first < 0 || recent < 1 || (long long)first + recent > n_select)
     return DA_ERR_INVALID_ARG;
-  if (block_size > 65536 || max_blocks > kSelectBlocks) return DA_ERR_UNSUPPORTED;
+  if (block_size > 65536 || max_blocks > kSelectBlocks || n_select > kMostTokens) return DA_ERR_UNSUPPORTED;
   if (batch == 0 || q_len == 0) return DA_OK;
   const long long qn = product(batch, q_len, num_q_heads, head_dim, 2), mn = product(batch, num_kv_heads, max_blocks, head_dim, 2),
                   on = product(batch, q_len, num_kv_heads, n_select, 4);

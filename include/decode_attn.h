@@ -569,6 +569,9 @@ const char* decode_status_string(int status);
  *  workspace  prefix_attn_workspace_bytes(...) bytes, 16-byte aligned; contents need not be kept, calls that
  *           share one must not overlap on the GPU.  num_sms <= 0: of the current device.
  * Softmax in fp32, the weights rounded to bf16 for the product with V, fp32 sums, one rounding of the output.
+ * What lies past a sequence's end may hold anything, and no row's infinities or NaN reach another's, but for one
+ * case: with more than 16 query rows a KV head (batch * q_len * G), values of the prefix that are not finite reach
+ * every row, those of sequences that end before them too.
  * Pages outside [0, num_pages) set bit 2 of the device error word and read page 0 instead.  Outputs may not
  * overlap inputs.
  */
@@ -594,7 +597,7 @@ int prefix_attn_paged(const void* q, const void* k_pool, const void* v_pool, con
  * Other blocks' means stay as they were.
  *  k        bf16 cache or pool as above; head_dim a multiple of 8
  *  means    bf16 [batch, num_kv_heads, max_blocks, head_dim]; max_blocks * block_size must cover max_ctx (paged:
- *           what the table and max_seq_len hold)
+ *           what the table and max_seq_len hold); block_size <= 65536; a pool of less than 2^32 tokens
  */
 int block_means_contig(const void* k, const int* seq_lens, int batch, int q_len, int num_kv_heads, int head_dim,
                        int max_ctx, int block_size, int max_blocks, void* means, void* stream);
@@ -639,7 +642,7 @@ int sparse_attn_paged(const void* q, const void* k_pool, const void* v_pool, con
  * of softmax_t(scale <q, k>), causal as in prefix_attn without a prefix, for t < L_b; entries at and past L_b are
  * neither read nor written.  Softmax and sums in fp32.
  *  q        bf16 [batch, q_len, num_q_heads, head_dim], head_dim 64, 128 or 256, q_len * G <= 1024
- *  k        bf16 or int8 cache or pool as for decode_attn_*; k_scale fp32 [batch, num_kv_heads, max_ctx] or
+ *  k        bf16 or int8 cache or pool as for decode_attn_*, page_size a multiple of 16; k_scale fp32 [batch, num_kv_heads, max_ctx] or
  *           [num_pages, num_kv_heads, page_size]
  *  prior, out  fp32, laid out like k_scale; prior may be out, or NULL (zeros), and may not overlap it otherwise
  *  workspace  kv_weights_workspace_bytes(...) bytes, 16-byte aligned; max_len: max_ctx, or what the table and

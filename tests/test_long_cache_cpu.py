@@ -184,3 +184,15 @@ def test_evict_refusals(clib):
                                      None, 0, A + 6 * BIG, A + 7 * BIG, None) == 1
     assert clib.kv_evict_paged(A, A + BIG, A + 2 * BIG, None, A, 1, 2, 64, 16, 4, 9, 64, 8, 1, 1, None, None, None, 0,
                                A + 6 * BIG, A + 7 * BIG, None) == 1
+
+
+def test_sizes_whose_loops_would_pass_32_bits(clib):
+    most = 2 ** 31 - 1
+    assert prefix_contig(clib, ctx=most - 600) == prefix_contig(clib, P=most - 600, ctx=0) == 2
+    assert clib.kv_weights_contig(A, A + BIG, None, 1, 1, 8, 2, 64, most - 600, F, 1.0, None, A, BIG, A + 2 * BIG, None) == 2
+    assert clib.block_select(A, A + BIG, None, 1, 1, 8, 2, 64, 64, 9, most, 1, 1, A + 2 * BIG, None) == 2
+    assert clib.sparse_attn_contig(A, A + BIG, A + 2 * BIG, A, None, 1, 1, 8, 2, 64, most - 600, 64, 2, F, A + 4 * BIG, None) == 2
+    out = (A + 6 * BIG, A + 7 * BIG, None)
+    assert clib.kv_evict_contig(A, A + BIG, A + 2 * BIG, None, 1, 2, 64, 64, most, 1, 1, None, None, None, 0, *out) == 2
+    assert clib.kv_evict_contig(A, A + BIG, A + 2 * BIG, None, 1, 2, 64, 64, 8, 1, 1, A + 3 * BIG, A + 4 * BIG, None, most,
+                                *out) == 2
