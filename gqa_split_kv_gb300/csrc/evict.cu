@@ -43,25 +43,28 @@ int weights_shape(int B, int n, int Hq, int Hkv, long long cap, int sms, Weights
   if (G > 64 || Hq > 65536 || cap > kMostTokens || product(n, G) > kWeightRows || product(B, Hkv) > 0x3fffffffLL)
     return DA_ERR_UNSUPPORTED;
   s->rows = n * G;
-  s->slots = (long long)B * Hkv + 2ll * sms;
+  s->slots = (long long)B * Hkv + 4ll * sms;  // 4 CTAs an SM at most
   const long long tiles = product(B, Hkv, (cap + kTile - 1) / kTile);
   if (tiles > 1LL << 40) return DA_ERR_UNSUPPORTED;
-  s->score = s->rows <= 16 ? tiles * s->rows * kTile * 4 : 0;
+  s->score = s->rows <= 16 ? tiles * score_rows(s->rows) * kTile * 4 : 0;
   s->bytes = s->slots * (s->rows <= 16 ? 16 : kWindowRows) * 8 + s->score;
   return DA_OK;
 }
 
+template <int D, bool PAGED, bool INT8, int NT>
+int launch_few(WeightsParams w, int sms, cudaStream_t st) {
+  using Gm = ScoreGeo<D, INT8, NT>;
+  w.s.ctas = Gm::PER_SM * sms;
+  w.finish_ctas = 8 * sms;
+  if (int e = allow_smem<weights_score_kernel<D, PAGED, INT8, NT>>(Gm::SMEM)) return e;
+  if (int e = launch_dependent(weights_score_kernel<D, PAGED, INT8, NT>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
+    return e;
+  return launch_dependent(weights_finish_kernel<PAGED>, (unsigned)w.finish_ctas, kFinishThreads, 0, st, w);
+}
 template <int D, bool PAGED, bool INT8>
 int launch_scores(WeightsParams w, int sms, cudaStream_t st) {
-  if (w.rows <= 16) {
-    using Gm = ScoreGeo<D, INT8>;
-    w.s.ctas = Gm::PER_SM * sms;
-    w.finish_ctas = 8 * sms;
-    if (int e = allow_smem<weights_score_kernel<D, PAGED, INT8>>(Gm::SMEM)) return e;
-    if (int e = launch_dependent(weights_score_kernel<D, PAGED, INT8>, (unsigned)w.s.ctas, Gm::THREADS, Gm::SMEM, st, w))
-      return e;
-    return launch_dependent(weights_finish_kernel<PAGED>, (unsigned)w.finish_ctas, kFinishThreads, 0, st, w);
-  }
+  if (w.rows <= 8) return launch_few<D, PAGED, INT8, 1>(w, sms, st);
+  if (w.rows <= 16) return launch_few<D, PAGED, INT8, 2>(w, sms, st);
   using Gm = WeightsTcGeo<D>;
   static_assert(Gm::ROWS == kWindowRows, "");
   w.s.ctas = Gm::PER_SM * sms;

@@ -23,7 +23,7 @@ struct WeightsParams {
   const float* k_scale;
   const float* prior;
   float* out;
-  float* scores;  // [tile of the line][rows][64]
+  float* scores;  // [tile of the line][64][score_rows(rows)]
   int rows;       // query rows of a KV head, or of this window
   int row0;       // the window's first
   int finish_ctas;
@@ -31,18 +31,22 @@ struct WeightsParams {
   unsigned long long timeout_ns;
 };
 
-template <int D, bool INT8>
+// Rows of a token's scores in memory: whole 16 bytes.
+__host__ __device__ constexpr int score_rows(int rows) { return (rows + 3) & ~3; }
+
+template <int D, bool INT8, int NT>
 struct ScoreGeo {
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
+  static constexpr int ROWS = 8 * NT;           // query rows of a unit
   static constexpr int ROWB = D * (INT8 ? 1 : 2);
   static constexpr int STAGE = 16 * ROWB + (INT8 ? 64 : 0);  // keys of 16 tokens, and their scales
-  static constexpr int NSTAGE = ROWB == 512 ? 3 : 6;  // two CTAs an SM either way
+  // 150 KB and more of keys in flight an SM, by as many warps as their registers allow
+  static constexpr int PER_SM = D == 256 ? 2 : 4;
+  static constexpr int NSTAGE = ROWB == 512 ? 3 : ROWB == 256 ? (PER_SM == 2 ? 6 : 3) : 6;
   static constexpr int WARP_BYTES = NSTAGE * STAGE;
-  static constexpr int ROWS = 16;  // query rows of a unit
   static constexpr int OFF_ML = WARPS * WARP_BYTES;
   static constexpr int OFF_LENS = OFF_ML + WARPS * ROWS * 8;
   static constexpr int SMEM = OFF_LENS + kSegLens * 4;
-  static constexpr int PER_SM = 2;
 };
 
 // Where a token's row lies: its page (or sequence) and place in it.
@@ -80,9 +84,9 @@ __device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t w) {
 }
 
 // A warp's ring of keys: 16 tokens of every tile of the CTA's, looked up a tile ahead.
-template <int D, bool PAGED, bool INT8>
+template <int D, bool PAGED, bool INT8, int NT>
 struct KeyRing {
-  using Gm = ScoreGeo<D, INT8>;
+  using Gm = ScoreGeo<D, INT8, NT>;
   static constexpr int CH = Gm::ROWB / 16;  // chunks a row
   const WeightsParams& wp;
   const SegWalk<kSegRange>& walk;
@@ -160,39 +164,35 @@ struct KeyRing {
     }
     cp_async_commit();
   }
-  // The B fragments of 8 tokens from token 8 nt of a stage, step kk of 16 elements in b[kk], and
-  // the scales of this thread's two.  bf16: element 16 kk + 2 t (and + 8) is thread t's of the
-  // quad; int8: 64 c + 16 t + 4 s (and + 2) for kk = 4 c + s, so that a thread's 16 bytes of a key
-  // hold its elements of 4 steps.
-  __device__ __forceinline__ void fragments(int stage, int nt, uint32_t (&b)[D / 16][2], float2& scale) const {
-    const int lane = threadIdx.x & 31;
-    const uint32_t kst = at + stage * Gm::STAGE;
+  // Step kk's fragment of a stage's 16 tokens: 0 .. 7 and 8 .. 15 in its first half of the elements, then
+  // in its second.  bf16: element 16 kk + 2 t (and + 8) is thread t's of the quad; int8: 64 c + 16 t + 4 s
+  // (and + 2) for kk = 4 c + s, so that a thread's 16 bytes of a key hold its elements of 4 steps, [c][row half].
+  static constexpr int kHeld = INT8 ? D / 64 : 1;
+  __device__ __forceinline__ void hold(int stage, uint32_t (&e)[kHeld][2][4]) const {
     if constexpr (INT8) {
-      const int row = nt * 8 + lane / 4;
+      const int lane = threadIdx.x & 31;
+      const uint32_t kst = at + stage * Gm::STAGE;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t e[4];
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
-                     : "r"(kst + row * Gm::ROWB + chunk(row, 4 * c + lane % 4) * 16));
+      for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          b[4 * c + i][0] = int8x2_to_bf16x2<0>(e[i]);
-          b[4 * c + i][1] = int8x2_to_bf16x2<1>(e[i]);
+        for (int hf = 0; hf < 2; ++hf) {
+          const int row = hf * 8 + lane / 4;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(e[c][hf][0]), "=r"(e[c][hf][1]), "=r"(e[c][hf][2]), "=r"(e[c][hf][3])
+                       : "r"(kst + row * Gm::ROWB + chunk(row, 4 * c + lane % 4) * 16));
         }
-      }
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(scale.x), "=f"(scale.y)
-                   : "r"(kst + 16 * Gm::ROWB + (nt * 8 + 2 * (lane % 4)) * 4));
-    } else {
-      scale = make_float2(1.f, 1.f);
-      const int mrow = lane & 7, mi = lane >> 3;
+    }
+  }
+  __device__ __forceinline__ void fragment(int stage, int kk, const uint32_t (&e)[kHeld][2][4], uint32_t (&a)[4]) const {
+    if constexpr (INT8) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; kk += 2) {
-        // matrices: steps kk and kk + 1, low and high half
-        const int row = nt * 8 + mrow, c = 2 * kk + mi;
-        ldsm_x4(kst + row * Gm::ROWB + (chunk(row, c) << 4), b[kk][0], b[kk][1], b[kk + 1][0], b[kk + 1][1]);
+      for (int hf = 0; hf < 2; ++hf) {
+        a[hf] = int8x2_to_bf16x2<0>(e[kk / 4][hf][kk % 4]);
+        a[2 + hf] = int8x2_to_bf16x2<1>(e[kk / 4][hf][kk % 4]);
       }
+    } else {
+      const int lane = threadIdx.x & 31, row = lane & 15, c = 2 * kk + (lane >> 4);
+      ldsm_x4(at + stage * Gm::STAGE + row * Gm::ROWB + (chunk(row, c) << 4), a[0], a[1], a[2], a[3]);
     }
   }
   // The words of a query row (32-bit index) that go with them for step kk: first and second half.
@@ -214,11 +214,13 @@ __device__ __forceinline__ float2 join_warps(const float2* ml, int row) {
   return make_float2(M, L);
 }
 
-template <int D, bool PAGED, bool INT8>
-__global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>::PER_SM)
+// The tokens are the MMA's 16 rows and the queries its 8 columns, as in seg_kernel.  A lane keeps a
+// maximum and a sum of its own tokens; the lanes are joined where a unit ends.
+template <int D, bool PAGED, bool INT8, int NT>
+__global__ void __launch_bounds__(ScoreGeo<D, INT8, NT>::THREADS, ScoreGeo<D, INT8, NT>::PER_SM)
     weights_score_kernel(const __grid_constant__ WeightsParams wp) {
-  using Gm = ScoreGeo<D, INT8>;
-  using Ring = KeyRing<D, PAGED, INT8>;
+  using Gm = ScoreGeo<D, INT8, NT>;
+  using Ring = KeyRing<D, PAGED, INT8, NT>;
   const SegParams& p = wp.s;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -234,82 +236,98 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8>::THREADS, ScoreGeo<D, INT8>:
 #pragma unroll 1
   for (int s = 0; s < Gm::NSTAGE; ++s) ring.issue(s);
 
-  uint32_t qa[D / 16][4];
-  float m[2], l[2];
-  int lim[2];
-  bool has[2];
+  // column n of an MMA is row 8 nt + n; this lane's columns are 2 (lane % 4) and the next
+  uint32_t qb[NT][D / 16][2];
+  float m[NT][2], l[NT][2];
+  int lim[NT][2];
+  const int padded = score_rows(wp.rows);
   bool fresh = true;
   int stage = 0;
   for (long long x = x0; x < x1; ++x) {
     if (fresh) {
       fresh = false;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        int token, g;
-        has[hf] = seg_query<kSegRange>(p, walk.lens, u, lane / 4 + 8 * hf, token, g, lim[hf]);
+      for (int nt = 0; nt < NT; ++nt) {
+        int token, g, unused;
+        const bool is = seg_query<kSegRange>(p, walk.lens, u, 8 * nt + lane / 4, token, g, unused);
         const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int w = Ring::query_word(kk, lane % 4);
-          qa[kk][hf] = has[hf] ? load_dependent(src + w) : 0u;
-          qa[kk][2 + hf] = has[hf] ? load_dependent(src + w + Ring::kQueryHalf) : 0u;
+          qb[nt][kk][0] = is ? load_dependent(src + w) : 0u;
+          qb[nt][kk][1] = is ? load_dependent(src + w + Ring::kQueryHalf) : 0u;
         }
-        m[hf] = kNegInf;
-        l[hf] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          seg_query<kSegRange>(p, walk.lens, u, 8 * nt + 2 * (lane % 4) + e, token, g, lim[nt][e]);  // 0: no row
+          m[nt][e] = kNegInf;
+          l[nt][e] = 0.f;
+        }
       }
     }
     cp_async_wait<Gm::NSTAGE - 1>();
     __syncwarp();
     const uint32_t live = ring.live_of(x);
     if (live) {
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      float mx[2] = {kNegInf, kNegInf};
+      float s[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        uint32_t b[D / 16][2];
-        float2 ks;
-        ring.fragments(stage, nt, b, ks);
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      uint32_t held[Ring::kHeld][2][4];
+      ring.hold(stage, held);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_16816(s[nt], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[kk][0], b[kk][1]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t a[4];
+        ring.fragment(stage, kk, held, a);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = nt * 8 + 2 * (lane % 4) + (e & 1);
-          const bool see = ((live >> col) & 1) && j * kTile + warp * 16 + col < lim[e >> 1];
-          s[nt][e] = see ? s[nt][e] * (e & 1 ? ks.y : ks.x) * p.scale_log2 : kNegInf;
-          mx[e >> 1] = fmaxf(mx[e >> 1], s[nt][e]);
-        }
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[nt], a[0], a[1], a[2], a[3], qb[nt][kk][0], qb[nt][kk][1]);
       }
+      float* to = wp.scores + ((size_t)x * kTile + warp * 16 + lane / 4) * padded + 2 * (lane % 4);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
-        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
-        if (mx[hf] > m[hf]) {
-          l[hf] *= exp2_approx(m[hf] - mx[hf]);
-          m[hf] = mx[hf];
-        }
-        const float mu = m[hf] == kNegInf ? 0.f : m[hf];
+        float f = p.scale_log2;
+        if (INT8) f *= *reinterpret_cast<const float*>(smem + warp * Gm::WARP_BYTES + stage * Gm::STAGE + 16 * Gm::ROWB +
+                                                       (lane / 4 + 8 * hf) * 4);
+        const int t = j * kTile + warp * 16 + lane / 4 + 8 * hf;
+        const bool is = (live >> (lane / 4 + 8 * hf)) & 1;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          l[hf] += exp2_approx(s[nt][2 * hf] - mu) + exp2_approx(s[nt][2 * hf + 1] - mu);
-          if (has[hf])
-            *reinterpret_cast<float2*>(wp.scores + ((size_t)x * wp.rows + lane / 4 + 8 * hf) * kTile + warp * 16 + nt * 8 +
-                                       2 * (lane % 4)) = make_float2(s[nt][2 * hf], s[nt][2 * hf + 1]);
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s[nt][2 * hf + e] = is && t < lim[nt][e] ? s[nt][2 * hf + e] * f : kNegInf;
+          if (8 * nt + 2 * (lane % 4) < padded)
+            *reinterpret_cast<float2*>(to + 8 * hf * padded + 8 * nt) = make_float2(s[nt][2 * hf], s[nt][2 * hf + 1]);
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mx = fmaxf(s[nt][e], s[nt][2 + e]);
+          if (mx > m[nt][e]) {
+            l[nt][e] *= exp2_approx(m[nt][e] - mx);
+            m[nt][e] = mx;
+          }
+          const float mu = m[nt][e] == kNegInf ? 0.f : m[nt][e];
+          l[nt][e] += exp2_approx(s[nt][e] - mu) + exp2_approx(s[nt][2 + e] - mu);
+        }
     }
     const bool last = j + 1 == u.tiles;
     if (last || x + 1 == x1) {
       float2* ml = reinterpret_cast<float2*>(smem + Gm::OFF_ML);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-        if (lane % 4 == 0) ml[warp * 16 + lane / 4 + 8 * hf] = make_float2(m[hf], l[hf]);
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = m[nt][e];
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          float sum = m[nt][e] == kNegInf ? l[nt][e] : l[nt][e] * exp2_approx(m[nt][e] - top);  // 0, or NaN
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          if (lane < 4) ml[warp * Gm::ROWS + 8 * nt + 2 * lane + e] = make_float2(top, sum);
+        }
       __syncthreads();
-      if (threadIdx.x < 16)
-        p.part_ml[((size_t)u.id + blockIdx.x) * 16 + threadIdx.x] = join_warps<Gm::WARPS, 16>(ml, threadIdx.x);
+      if (threadIdx.x < Gm::ROWS)
+        p.part_ml[((size_t)u.id + blockIdx.x) * 16 + threadIdx.x] = join_warps<Gm::WARPS, Gm::ROWS>(ml, threadIdx.x);
       __syncthreads();
     }
     ring.issue(stage);
@@ -394,17 +412,25 @@ __global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const __
       if (fresh) {
         fresh = false;
         __syncthreads();
-        for (int r = threadIdx.x >> 5; r < wp.rows; r += kFinishThreads / 32) {
-          const float2 y = weight_factors(join_pieces(p.part_ml, (long long)(s.b * p.Hkv + h) + c0, c1 - c0 + 1, 16, r));
+        for (int r = threadIdx.x >> 5; r < 16; r += kFinishThreads / 32) {
+          float2 y = make_float2(0.f, 0.f);
+          if (r < wp.rows) y = weight_factors(join_pieces(p.part_ml, (long long)(s.b * p.Hkv + h) + c0, c1 - c0 + 1, 16, r));
           if ((threadIdx.x & 31) == 0) row[r] = y;
         }
         __syncthreads();
       }
       if (!mine) continue;
-      const float* x = wp.scores + (size_t)(line + j) * wp.rows * kTile + threadIdx.x % kTile;
+      const float4* x = reinterpret_cast<const float4*>(wp.scores + ((size_t)(line + j) * kTile + threadIdx.x % kTile) *
+                                                                        score_rows(wp.rows));
       float w = 0.f;
-#pragma unroll 8
-      for (int r = 0; r < wp.rows; ++r) w = fmaf(exp2_approx(__ldcg(x + r * kTile) - row[r].x), row[r].y, w);
+#pragma unroll 2
+      for (int r = 0; r < wp.rows; r += 4) {  // (rows past the last: score -inf, factor 0)
+        const float4 y = __ldcg(x + r / 4);
+        w = fmaf(exp2_approx(y.x - row[r].x), row[r].y, w);
+        w = fmaf(exp2_approx(y.y - row[r + 1].x), row[r + 1].y, w);
+        w = fmaf(exp2_approx(y.z - row[r + 2].x), row[r + 2].y, w);
+        w = fmaf(exp2_approx(y.w - row[r + 3].x), row[r + 3].y, w);
+      }
       if (c.good) wp.out[o] = wp.prior ? fmaf(wp.decay, before, w) : w;
     }
     f += j1 - j0;
