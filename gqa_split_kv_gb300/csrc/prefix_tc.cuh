@@ -149,26 +149,18 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
   auto addr_of = [&](int j, int g) { return sbase + Gm::OFF_G + (uint32_t)(slot_of(j, g) * Gm::GB); };
 
   // query rows, [tile][D / 64][128][64] with the 128-byte swizzle, zeros past the last; by the warps
-  // that need them, while the first keys load, several loads of a thread in flight
+  // that need them, while the first keys load, all copies in flight at once
   auto stage_queries = [&](int me) {
-    constexpr int CH = D / 8, U = 8, N = 32 + 128 * NQT;
-    for (int e0 = me; e0 < nqt * M * CH; e0 += U * N) {
-      uint4 v[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int rr = (e0 + i * N) / CH, ch = (e0 + i * N) % CH;
-        const int token = (row0 + rr) / p.G, g = row0 + rr - token * p.G;
-        v[i] = rr < nrows
-                   ? load_dependent(reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + h * p.G + g) * D) + ch)
-                   : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int rr = (e0 + i * N) / CH, ch = (e0 + i * N) % CH;
-        if (rr < nqt * M)
-          *reinterpret_cast<uint4*>(smem + (rr / M) * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(rr % M, ch % 8)) = v[i];
-      }
+    constexpr int CH = D / 8, N = 32 + 128 * NQT;
+#pragma unroll 4
+    for (int e = me; e < nqt * M * CH; e += N) {
+      const int rr = e / CH, ch = e % CH, token = (row0 + rr) / p.G, g = row0 + rr - token * p.G;
+      const bool is = rr < nrows;
+      cp_async16(sbase + (rr / M) * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(rr % M, ch % 8),
+                 is ? p.q + ((size_t)token * p.Hq + h * p.G + g) * D + ch * 8 : p.q, is);
     }
+    cp_async_commit();
+    cp_async_wait<0>();
     fence_proxy_async_smem();
     named_bar_sync(1, N);
   };
