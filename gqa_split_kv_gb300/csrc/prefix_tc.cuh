@@ -151,13 +151,23 @@ __global__ void __launch_bounds__(PrefixTcGeo<D>::NTHREADS, 1) prefix_tc_kernel(
   // query rows, [tile][D / 64][128][64] with the 128-byte swizzle, zeros past the last; by the warps
   // that need them, while the first keys load, all copies in flight at once
   auto stage_queries = [&](int me) {
-    constexpr int CH = D / 8, N = 32 + 128 * NQT;
+    constexpr int CH = D / 8, N = 32 + 128 * NQT, STEP = N / CH;  // a thread's chunk of every STEP-th row
+    static_assert(N % CH == 0, "");
+    const int ch = me % CH, more = STEP / p.G, step_g = STEP - more * p.G;
+    const uint32_t column = sbase + (ch / 8) * (M * 128);
+    int token = (row0 + me / CH) / p.G, g = row0 + me / CH - token * p.G;
+    const __nv_bfloat16* from = p.q + (size_t)h * p.G * D + ch * 8;
 #pragma unroll 4
-    for (int e = me; e < nqt * M * CH; e += N) {
-      const int rr = e / CH, ch = e % CH, token = (row0 + rr) / p.G, g = row0 + rr - token * p.G;
+    for (int rr = me / CH; rr < nqt * M; rr += STEP) {
       const bool is = rr < nrows;
-      cp_async16(sbase + (rr / M) * Gm::QT_BYTES + (ch / 8) * (M * 128) + swz<128>(rr % M, ch % 8),
-                 is ? p.q + ((size_t)token * p.Hq + h * p.G + g) * D + ch * 8 : p.q, is);
+      cp_async16(column + (rr / M) * Gm::QT_BYTES + swz<128>(rr % M, ch % 8),
+                 is ? from + ((size_t)token * p.Hq + g) * D : p.q, is);
+      token += more;
+      g += step_g;
+      if (g >= p.G) {
+        g -= p.G;
+        ++token;
+      }
     }
     cp_async_commit();
     cp_async_wait<0>();
