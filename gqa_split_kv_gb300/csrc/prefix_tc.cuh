@@ -14,9 +14,11 @@
 //   P_A V_j, S_A = Q_A K_{j+1}^T, P_B V_j, S_B = Q_B K_{j+1}^T;
 // with one, S has two buffers and S_{j+1} is computed ahead of P_j V_j.  Tensor memory: two S
 // of 128 columns (64 at D = 256) and the O (D columns each).  K and V come through one ring
-// of 16 KB granules, each freed by its last product.  A tile is 128 keys, 64 at D = 256: a ring of
-// 160 KB holds one and a quarter of 128 keys there, and K_{j+1} next to V_j leaves hardly any of it
-// to loads in flight (4.7 us a tile of 128 keys).  Multicast of the keys to clusters of the row
+// of granules, a tile's keys or values each, freed by their last product (16 KB ones at D >= 128 cost the
+// producers one more chain of wait, look-up and boxes a 16 KB: 62.6 us a call of 64 x (16384 + <= 2048)
+// tokens, 64/8 heads of 128, instead of 60.1; 52.9 instead of 48.8 at 16 x 4 rows of 24/4 heads of 256 after
+// 8192).  A tile is 128 keys, 64 at D = 256: a ring of 160 KB holds one and a quarter of 128 keys there, and
+// K_{j+1} next to V_j leaves hardly any of it to loads in flight.  Multicast of the keys to clusters of the row
 // blocks that share them did not help (2.0 -> 2.3 us a tile, D = 128): their loads are not
 // bound by L2's rate.
 //
@@ -59,7 +61,7 @@ struct PrefixTcGeo {
   static constexpr int NQT = D <= 128 ? 2 : 1;  // query tiles a CTA
   static constexpr int ROWS = NQT * M;
   static constexpr int NSUB = D / 64;           // 64-element columns
-  static constexpr int GB = 16384;              // bytes a granule
+  static constexpr int GB = D >= 128 ? 32768 : 16384;  // bytes a granule
   static constexpr int KSUB = GB / (BK * 128);  // 64-element columns of a K granule
   static constexpr int VKEYS = GB / (2 * D);    // keys of a V granule
   static constexpr int NKG = NSUB / KSUB, NVG = BK / VKEYS, PER = NKG + NVG;
