@@ -95,7 +95,7 @@ struct KeyRing {
   int j;
   long long x, x1;
   unsigned long long lives0, lives1;  // which of the 16 tokens there are, of the last eight tiles: tile x in bits 16 (x % 4) on
-  long long off, soff;          // of the first one's key and scale
+  int slab, row, h;  // the first one's page (not checked yet) or sequence, place in it, and head
   uint32_t live;
 
   __device__ __forceinline__ KeyRing(const WeightsParams& wp_, const SegWalk<kSegRange>& walk_, uint32_t at_, long long x0,
@@ -112,16 +112,19 @@ struct KeyRing {
   static __device__ __forceinline__ int chunk(int row, int c) {
     return INT8 ? c ^ ((row & 1) << 2) % CH : c ^ (row & 7);
   }
-  // (16 tokens from a multiple of 16 on lie in one page)
+  // Starts the load of the page (16 tokens from a multiple of 16 on lie in one), which issue() uses a tile later.
   __device__ __forceinline__ void look_up() {
     const SegParams& p = wp.s;
     const int t = j * kTile + (threadIdx.x >> 5) * 16, n = u.end - t;
     live = n <= 0 ? 0u : n < 16 ? (1u << n) - 1u : 0xffffu;
-    if (!live) return;
-    const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
-    const int slab_rows = PAGED ? p.page_size : p.ctx;
-    off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)Gm::ROWB;
-    soff = (c.slab * p.Hkv + u.h) * slab_rows + c.at;
+    h = u.h;
+    slab = u.b;
+    row = t;
+    if (PAGED && live) {
+      const int col = t / p.page_size;
+      row = t - col * p.page_size;
+      slab = load_dependent(p.page_table + (size_t)u.b * p.max_pages + col);
+    }
   }
   __device__ __forceinline__ void issue(int stage) {
     if (x < x1) {
@@ -132,6 +135,13 @@ struct KeyRing {
       else
         lives1 = (lives1 & others) | mine;
       if (live) {
+        if (PAGED && (unsigned)slab >= (unsigned)wp.s.num_pages) {
+          atomicOr(&g_error_word, 4u);
+          slab = 0;
+        }
+        const int slab_rows = PAGED ? wp.s.page_size : wp.s.ctx;
+        const long long off = (((long long)slab * slab_rows + row) * wp.s.Hkv + h) * Gm::ROWB,
+                        soff = ((long long)slab * wp.s.Hkv + h) * slab_rows + row;
         const uint8_t* keys = reinterpret_cast<const uint8_t*>(wp.s.k);
         constexpr int RPP = 32 / (CH < 32 ? CH : 32);
         const int c = lane % CH, r0 = lane / CH, step = wp.s.Hkv * Gm::ROWB;
