@@ -87,24 +87,52 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
     const int tiles64 = (int)min((long long)(u.tiles - j), x1 - x);
     const int t0 = j * kTile, t1 = min(u.end, (j + tiles64) * kTile);
     const int n = (t1 - t0 + Gm::KEYS - 1) / Gm::KEYS;
+    // warps 0 to 3: a thread a token of tile k
+    long long* offs = reinterpret_cast<long long*>(smem + Gm::OFF_OFF);
+    constexpr int ROWB = D * (INT8 ? 1 : 2), CH = ROWB / 16;
+    long long next_off = -1;
+    float next_scale = 0.f;
+    auto look_up = [&](int k) {  // starts the loads; their results are stored later
+      next_off = -1;
+      next_scale = 0.f;
+      const int t = t0 + k * Gm::KEYS + threadIdx.x;
+      if (t < t1) {
+        const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
+        const int slab_rows = PAGED ? p.page_size : p.ctx;
+        next_off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)ROWB;
+        next_scale = 1.f;
+        if (INT8) next_scale = load_dependent(wp.k_scale + (c.slab * p.Hkv + u.h) * slab_rows + c.at);
+      }
+    };
+    // The place of a tile's scales was last read for the tile eight before, long done: the products of tile
+    // at - 2, which are waited for below, began after the readers of tile at - 4.
+    auto keep = [&](int k) {
+      offs[((it + k) & 1) * Gm::KEYS + threadIdx.x] = next_off;
+      reinterpret_cast<float*>(smem + Gm::OFF_KS)[((it + k) & 7) * Gm::KEYS + threadIdx.x] = next_scale * p.scale_log2;
+    };
     // its queries (the products of the last unit's are done: every thread has seen their results)
     {
-      constexpr int U = 8;
-      for (int e0 = threadIdx.x; e0 < Gm::ROWS * (D / 8); e0 += U * Gm::THREADS) {
-        uint4 v[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int in = (e0 + i * Gm::THREADS) / (D / 8), c = (e0 + i * Gm::THREADS) % (D / 8), row = wp.row0 + in;
-          const int token = u.b * p.n + row / p.G, g = row % p.G;
-          v[i] = in < wp.rows
-                     ? load_dependent(reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + u.h * p.G + g) * D) + c)
-                     : make_uint4(0u, 0u, 0u, 0u);
+      constexpr int QCH = D / 8, STEP = Gm::THREADS / QCH;  // a thread's chunk of every STEP-th row
+      static_assert(Gm::THREADS % QCH == 0, "");
+      const int c = threadIdx.x % QCH, more = STEP / p.G, step_g = STEP - more * p.G;
+      const uint32_t column = sbase + (c / 8) * 16384;
+      int in = threadIdx.x / QCH, token = (wp.row0 + in) / p.G, g = wp.row0 + in - token * p.G;
+      const __nv_bfloat16* from = p.q + ((size_t)u.b * p.n * p.Hq + (size_t)u.h * p.G) * D + c * 8;
+#pragma unroll 4
+      for (; in < Gm::ROWS; in += STEP) {
+        const bool is = in < wp.rows;
+        cp_async16(column + swz<128>(in, c % 8), is ? from + ((size_t)token * p.Hq + g) * D : p.q, is);
+        token += more;
+        g += step_g;
+        if (g >= p.G) {
+          g -= p.G;
+          ++token;
         }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int in = (e0 + i * Gm::THREADS) / (D / 8), c = (e0 + i * Gm::THREADS) % (D / 8);
-          if (in < Gm::ROWS) *reinterpret_cast<uint4*>(smem + (c / 8) * 16384 + swz<128>(in, c % 8)) = v[i];
-        }
+      }
+      cp_async_commit();
+      if (warp < 4) {
+        look_up(0);
+        keep(0);
       }
       if (SUMS && warp >= 4 && warp < 8) {
         // a thread a row: its (m, l) over all pieces of the unit
@@ -133,6 +161,7 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
         to[0] = -f.x;
         to[2] = f.y;
       }
+      cp_async_wait<0>();
       fence_proxy_async_smem();
       __syncthreads();
     }
@@ -140,30 +169,6 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
     if (warp < 4) {
       // ---- keys
       const int me = threadIdx.x;
-      long long* offs = reinterpret_cast<long long*>(smem + Gm::OFF_OFF);
-      constexpr int ROWB = D * (INT8 ? 1 : 2), CH = ROWB / 16;
-      long long next_off = -1;
-      float next_scale = 0.f;
-      auto look_up = [&](int k) {  // starts the loads; their results are stored later
-        next_off = -1;
-        next_scale = 0.f;
-        const int t = t0 + k * Gm::KEYS + me;
-        if (t < t1) {
-          const Cell c = token_cell<PAGED>(p.page_table, p.max_pages, p.page_size, p.num_pages, u.b, t);
-          const int slab_rows = PAGED ? p.page_size : p.ctx;
-          next_off = ((c.slab * slab_rows + c.at) * p.Hkv + u.h) * (long long)ROWB;
-          next_scale = 1.f;
-          if (INT8) next_scale = load_dependent(wp.k_scale + (c.slab * p.Hkv + u.h) * slab_rows + c.at);
-        }
-      };
-      // The place of a tile's scales was last read for the tile eight before, long done: the products of tile
-      // at - 2, which are waited for below, began after the readers of tile at - 4.
-      auto keep = [&](int k) {
-        offs[((it + k) & 1) * Gm::KEYS + me] = next_off;
-        reinterpret_cast<float*>(smem + Gm::OFF_KS)[((it + k) & 7) * Gm::KEYS + me] = next_scale * p.scale_log2;
-      };
-      look_up(0);
-      keep(0);
       // (after a wait that gave up, the threads go on without waits, so that all meet at the barrier)
       for (int k = 0; k < n; ++k) {
         const int at = it + k, buf = at & 1;
