@@ -269,7 +269,6 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
           uint32_t r[32];
           tmem_ld32(tmem + lane_addr + buf * 128 + c0, r);
           tmem_ld_wait();
-          float y[32];
           if constexpr (SUMS) {
             const float4* f = reinterpret_cast<const float4*>(smem + Gm::OFF_F) + c0 / 2;
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -288,39 +287,49 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
             w += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           } else {
             const float4* s4 = reinterpret_cast<const float4*>(ks + c0);
-            float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            float2 y[16];  // the scores times their scales (into the exponents' fma they need more registers than there are)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float4 g = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
               if constexpr (INT8) g = s4[i];
-              const float2 lo = fma_f32x2(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), make_float2(g.x, g.y),
-                                          make_float2(0.f, 0.f));
-              const float2 hi = fma_f32x2(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
-                                          make_float2(g.z, g.w), make_float2(0.f, 0.f));
-              y[4 * i] = lo.x;
-              y[4 * i + 1] = lo.y;
-              y[4 * i + 2] = hi.x;
-              y[4 * i + 3] = hi.y;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (edge) y[4 * i + e] = c0 + 4 * i + e < end ? y[4 * i + e] : kNegInf;
-                top[e] = fmaxf(top[e], y[4 * i + e]);
+              const float2 zero = make_float2(0.f, 0.f);
+              y[2 * i] = fma_f32x2(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), make_float2(g.x, g.y), zero);
+              y[2 * i + 1] =
+                  fma_f32x2(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), make_float2(g.z, g.w), zero);
+              if (edge) {
+                const int left = end - c0 - 4 * i;
+                y[2 * i].x = left > 0 ? y[2 * i].x : kNegInf;
+                y[2 * i].y = left > 1 ? y[2 * i].y : kNegInf;
+                y[2 * i + 1].x = left > 2 ? y[2 * i + 1].x : kNegInf;
+                y[2 * i + 1].y = left > 3 ? y[2 * i + 1].y : kNegInf;
               }
             }
-            const float to = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-            if (to > m) {
-              l *= exp2_approx(m - to);
-              m = to;
-            }
-            const float mu = m == kNegInf ? 0.f : m;
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float2 mu2 = make_float2(-mu, -mu);
+            auto total = [&]() {
+              const float mu = m == kNegInf ? 0.f : m;
+              const float2 mu2 = make_float2(-mu, -mu);
+              float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 z = add_f32x2(make_float2(y[2 * i], y[2 * i + 1]), mu2);
-              acc[i & 1] = add_f32x2(acc[i & 1], make_float2(exp2_approx(z.x), exp2_approx(z.y)));
+              for (int i = 0; i < 16; ++i) {
+                const float2 z = add_f32x2(y[i], mu2);
+                acc[i & 1] = add_f32x2(acc[i & 1], make_float2(exp2_approx(z.x), exp2_approx(z.y)));
+              }
+              return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            };
+            // against the m so far; a row that has seen no key yet, or whose weights sum past 2^14, raises it (the
+            // maximum of every 32 first: 53.7 us instead of 51.6 for 32 tokens x 32 heads over 32768 int8 keys)
+            float sum = total();
+            if (m == kNegInf || !(sum <= 16384.f)) {
+              float2 top = make_float2(m, m);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) top = make_float2(fmaxf(top.x, y[i].x), fmaxf(top.y, y[i].y));
+              const float to = fmaxf(top.x, top.y);
+              if (to > m) {
+                l *= exp2_approx(m - to);
+                m = to;
+              }
+              sum = total();
             }
-            l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            l += sum;
           }
         }
         tc_fence_before();
