@@ -142,18 +142,19 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
         const int c0 = seg_owner(walk.all, walk.used, a), c1 = seg_owner(walk.all, walk.used, a + u.tiles - 1);
         const float2* ml = p.part_ml + ((long long)u.id + c0) * Gm::ROWS + r;
         float M = kNegInf, L = 0.f;
-        constexpr int U2 = 16;
+        constexpr int U2 = 20;
         for (int k0 = 0; k0 <= c1 - c0; k0 += U2) {
           float2 y[U2];
 #pragma unroll
           for (int k = 0; k < U2; ++k) y[k] = k0 + k <= c1 - c0 ? __ldcg(ml + (size_t)(k0 + k) * Gm::ROWS) : make_float2(kNegInf, 0.f);
+          float top = M, sum = 0.f;  // (one piece after another, each with its exponentials, made a chain of 2 us)
 #pragma unroll
-          for (int k = 0; k < U2; ++k) {
-            if (y[k].y == 0.f) continue;
-            const float to = fmaxf(M, y[k].x);
-            L = (M == kNegInf ? L : L * exp2_approx(M - to)) + (y[k].x == kNegInf ? y[k].y : y[k].y * exp2_approx(y[k].x - to));
-            M = to;
-          }
+          for (int k = 0; k < U2; ++k) top = fmaxf(top, y[k].y == 0.f ? kNegInf : y[k].x);
+#pragma unroll
+          for (int k = 0; k < U2; ++k)
+            sum += y[k].y == 0.f ? 0.f : y[k].x == kNegInf ? y[k].y : y[k].y * exp2_approx(y[k].x - top);
+          L = (M == kNegInf ? L : L * exp2_approx(M - top)) + sum;
+          M = top;
         }
         // no weight of rows that are not
         const float2 f = r < wp.rows ? weight_factors(make_float2(M, L)) : make_float2(0.f, 0.f);
