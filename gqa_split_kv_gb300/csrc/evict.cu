@@ -243,7 +243,8 @@ int evict_call(EvictParams& p, bool paged, bool int8, int head_dim, long long ca
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // a cluster where there are SMs for it and 1024 weights a CTA
   p.cluster = 1;
-  while (p.cluster < 8 && (long long)units * p.cluster * 2 <= 4LL * sms && p.cap >= p.cluster * 2 * 1024) p.cluster *= 2;
+  while (p.cluster < 8 && (long long)units * p.cluster * 2 <= 4LL * sms && p.cap >= p.cluster * 2 * 1024)
+    p.cluster *= 2;
   const int share = p.cap / p.cluster + 1;
   p.keys = share < kEvictKeys ? share : kEvictKeys;
   if (int e = paged ? allow_smem<evict_select_kernel<true>>(kEvictKeys * 4) : allow_smem<evict_select_kernel<false>>(kEvictKeys * 4))
