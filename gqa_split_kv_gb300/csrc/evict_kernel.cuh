@@ -251,6 +251,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int chunks = p.row_bytes / 16 / p.columns;  // of a row, here
     const int rows = kMoveThreads / chunks;           // a pass
     const int c = threadIdx.x % chunks, r = threadIdx.x / chunks;
+    // a row's place: its page's (sequence's) and, in it, its own
+    const long long head = (long long)h * p.row_bytes + (column * chunks + c) * 16, row_step = (long long)p.Hkv * p.row_bytes;
+    const long long src_slab = row_step * p.slab, dst_slab = row_step * to_slab;
     const long long i_begin = (long long)len * part / p.parts, i_end = (long long)len * (part + 1) / p.parts;
     for (long long i0 = i_begin; i0 < i_end; i0 += rows * U) {
       uint4 w[U];
@@ -268,8 +271,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
           bool good;
           const Cell s = from(t[k], good);
           if (good)
-            w[k] = load_dependent(reinterpret_cast<const uint4*>(
-                src + ((s.slab * p.slab + s.at) * p.Hkv + h) * (long long)p.row_bytes) + column * chunks + c);
+            w[k] = load_dependent(reinterpret_cast<const uint4*>(src + s.slab * src_slab + s.at * row_step + head));
         }
       if (p.in_place) __syncthreads();
 #pragma unroll
@@ -278,8 +280,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
           bool good;
           const Cell d = to((int)(i0 + k * rows + r), good);
           if (good)
-            *(reinterpret_cast<uint4*>(dst + ((d.slab * to_slab + d.at) * p.Hkv + h) * (long long)p.row_bytes) +
-              column * chunks + c) = w[k];
+            *reinterpret_cast<uint4*>(dst + d.slab * dst_slab + d.at * row_step + head) = w[k];
         }
     }
     return;

@@ -59,7 +59,8 @@ struct Cell {
 template <bool PAGED>
 __device__ __forceinline__ Cell token_cell(const int* table, int max_pages, int page_size, int num_pages, int b, int t) {
   if constexpr (PAGED) {
-    const int col = t / page_size;
+    // (a shift where it can be one: a division is a score of instructions)
+    const int col = (page_size & (page_size - 1)) == 0 ? t >> (31 - __clz(page_size)) : (int)((unsigned)t / (unsigned)page_size);
     const int page = load_dependent(table + (size_t)b * max_pages + col);
     const bool good = (unsigned)page < (unsigned)num_pages;
     if (!good) atomicOr(&g_error_word, 4u);
