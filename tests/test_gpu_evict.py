@@ -75,6 +75,31 @@ def test_weights_of_long_sequences(int8):
     assert abs(float(total) - 1024) < 1024 * 2.0 ** -12
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3, 5, 7, 9, 11, 15, 17, 33])
+def test_weights_of_any_number_of_rows(rows, D, int8):
+    c = Cache(rows, [130, 0, 1, 513], 600, 2, D, 16, names="k", int8=int8)
+    q = randn(c.gen, 4, 1, 2 * rows, D)
+    check_weights(c, q, c.numbers_back(weigh(c, q, None)), None)
+
+
+@pytest.mark.parametrize("page", [0, 32])
+@pytest.mark.parametrize("n,Hq,D", [(1, 8, 128), (2, 16, 256), (40, 8, 64), (40, 8, 128), (20, 10, 256)])
+def test_weights_of_growing_scores(n, Hq, D, page):
+    """The largest score comes late and the sums pass every limit of a running maximum on the way."""
+    c = Cache(n, [3000, 900, 2048], 3000, 2, D, page, names="k")
+    grow = torch.linspace(0.1, 9, 3000, device="cuda")
+    c.k.mul_(grow.view(1, 3000, 1, 1))
+    if page:
+        for b, L in enumerate(c.lens):
+            for t in range(0, L, page):
+                c.kp[int(c.table[b, t // page]), :min(page, L - t)] = c.k[b, t:min(t + page, L)]
+    q = randn(c.gen, 3, n, Hq, D) * 3
+    got = weigh(c, q, None)
+    check_weights(c, q, c.numbers_back(got) if page else got, None)
+
+
 def numbers(c, seed, kind):
     gen = torch.Generator(device="cuda").manual_seed(seed)
     w = torch.rand(c.B, c.H, c.cap, generator=gen, device="cuda") ** 6

@@ -92,6 +92,16 @@ def test_many_rows(page, B, n, Hq, Hkv, D, P):
     assert binding.device_error() == 0
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(1, 8, 2, 128), (5, 24, 2, 256), (9, 8, 1, 64), (9, 16, 1, 128)])
+def test_growing_scores(n, Hq, Hkv, D):
+    """Scores that grow along the prefix and the rests: running maxima are raised again and again."""
+    P = 1500
+    s = Shared(D, P, [P + 300, P + 20, P, 700, 0], n, Hq, Hkv, D, rest=300)
+    s.kp.mul_(torch.linspace(0.1, 9, P, device="cuda").view(P, 1, 1))
+    s.c.k.mul_(torch.linspace(9, 12, 300, device="cuda").view(1, 300, 1, 1))
+    s.check(s.run())
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 def test_scales(scale):
     s = Shared(5, 90, [91, 140], 1, 8, 2, 128)
