@@ -23,6 +23,8 @@ template <int D>
 constexpr int tc_rows() { return PrefixTcGeo<D>::ROWS; }
 int tc_rows(int D) { return D == 64 ? tc_rows<64>() : D == 128 ? tc_rows<128>() : tc_rows<256>(); }
 
+constexpr int kFewRows = 64;  // of a KV head: those that may read the prefix in seg_kernel
+
 // What a call of these sizes launches.
 struct PrefixShape {
   int ru, rt, rt_prefix, ctas;  // seg_kernel's
@@ -39,11 +41,11 @@ int prefix_shape(int B, int n, int Hq, int Hkv, int D, int sms, PrefixShape* s) 
   s->ru = seg_unit_rows((long long)n * G, D);
   s->rt = (int)(((long long)n * G + s->ru - 1) / s->ru);
   s->ctas = seg_ctas(s->ru, D, sms);
-  // few rows: the prefix goes through seg_kernel, as one or two more units a head
-  s->rt_prefix = s->rows <= 16 ? (int)((s->rows + s->ru - 1) / s->ru) : 0;
+  // few rows: the prefix may go through seg_kernel, as more units of a head
+  s->rt_prefix = s->rows <= kFewRows ? (int)((s->rows + s->ru - 1) / s->ru) : 0;
   s->row_blocks = (int)((s->rows + tc_rows(D) - 1) / tc_rows(D));
   const long long units = product(Hkv, s->row_blocks);
-  s->splits = s->rt_prefix || units == 0 ? 0 : units >= sms ? 1 : (int)(sms / units);
+  s->splits = s->rows <= 16 || units == 0 ? 0 : units >= sms ? 1 : (int)(sms / units);
   s->slots = (long long)Hkv * s->rt_prefix + (long long)B * Hkv * s->rt + s->ctas;
   s->tc_ml = (s->splits * product(Hkv, s->rows, 8) + 15) / 16 * 16;
   s->bytes = seg_partial_bytes(s->slots, s->ru, D) + s->tc_ml + s->splits * product(Hkv, s->rows, D * 4);
@@ -98,10 +100,18 @@ int launch_tc(const PrefixCall& c, const PrefixTcParams& base, cudaStream_t st) 
   return launch_dependent(prefix_tc_kernel<D>, (unsigned)grid, Gm::NTHREADS, Gm::SMEM, st, t);
 }
 
+// Whether the prefix goes through seg_kernel: up to 16 rows, and up to 64 where its tiles of 64 tokens and 8 or 16 rows
+// are at most half as many as the CTAs, so that the call takes one kernel less: 32 rows of 8 heads of 128 after 200 tokens
+// 10.7 -> 9.5 us, after 512 (256 tiles of 608 CTAs) 11.0 -> 10.4; after 1024 (512) it would be 11.7 -> 12.1.
+bool prefix_through_seg(const PrefixShape& s, int Hkv, int P) {
+  return s.rows <= 16 || (s.rt_prefix && product(Hkv, s.rt_prefix, (P + kTile - 1) / kTile) * 2 <= s.ctas);
+}
+
 template <int D>
-int launch_prefix(PrefixCall& c, const PrefixShape& s, cudaStream_t st) {
+int launch_prefix(PrefixCall& c, const PrefixShape& s, int sms, cudaStream_t st) {
   SegParams& p = c.p;
-  if (s.splits && p.base > 0) {
+  if (!prefix_through_seg(s, p.Hkv, p.base)) p.rt_prefix = 0;
+  if (!p.rt_prefix && p.base > 0) {
     PrefixTcParams t = {};
     t.q = p.q;
     t.seq_lens = p.seq_lens;
@@ -118,9 +128,19 @@ int launch_prefix(PrefixCall& c, const PrefixShape& s, cudaStream_t st) {
     t.page_size = p.page_size;
     t.num_pages = p.num_pages;
     t.row_blocks = s.row_blocks;
-    // as many parts as there is room for, of whole tiles and alike
+    // As many parts as there is room for, of whole tiles and alike.  A CTA of the prefix's takes an SM for itself: where the
+    // rests can be no more than fill half of the SMs, those stay free for them, if that makes the parts no more than 3
+    // times 128 keys longer (a second turn of starts costs as much).  8 x (P + <= 256) tokens, 64/8 heads of 128: P = 2048
+    // 18.6 -> 13.3 us, 8192 23.3 -> 19.8, while 32768 would be 38.4 -> 44.3; 24/4 heads of 256, 2048: 22.8 -> 14.1.
     const int tiles = (p.base + PrefixTcGeo<D>::BK - 1) / PrefixTcGeo<D>::BK;
-    const int each = (tiles + s.splits - 1) / s.splits;
+    const long long rests = product(p.B, p.Hkv, p.rt, seg_tiles(p.cap, p.cap, p.base & ~15));
+    const long long beside = ((rests < s.ctas ? rests : s.ctas) + s.ctas / sms - 1) / (s.ctas / sms);
+    const long long room = (sms - beside) / product(s.row_blocks, p.Hkv);  // parts next to the rests
+    int each = (tiles + s.splits - 1) / s.splits;
+    if (beside <= sms / 2 && room >= 1 && room < s.splits) {
+      const int longer = (int)((tiles + room - 1) / room);
+      if ((longer - each) * PrefixTcGeo<D>::BK <= 3 * 128) each = longer;
+    }
     t.splits = (tiles + each - 1) / each;
     t.scale_log2 = p.scale_log2;
     t.timeout_ns = kWaitTimeoutNs;
@@ -181,7 +201,9 @@ int prefix_call(PrefixCall& c, float scale, void* stream) {
   p.tc_o = reinterpret_cast<const float*>(reinterpret_cast<const char*>(p.tc_ml) + s.tc_ml);
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return c.D == 64 ? launch_prefix<64>(c, s, st) : c.D == 128 ? launch_prefix<128>(c, s, st) : launch_prefix<256>(c, s, st);
+  return c.D == 64    ? launch_prefix<64>(c, s, sms, st)
+         : c.D == 128 ? launch_prefix<128>(c, s, sms, st)
+                      : launch_prefix<256>(c, s, sms, st);
 }
 
 PrefixCall prefix_params(const void* q, const void* k, const void* v, const int* seq_lens, int batch, int q_len,
