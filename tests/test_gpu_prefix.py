@@ -92,6 +92,18 @@ def test_many_rows(page, B, n, Hq, Hkv, D, P):
     assert binding.device_error() == 0
 
 
+@pytest.mark.parametrize("page", [0, 48])
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,P", [(8, 1, 64, 8, 128, 2300), (8, 1, 24, 4, 256, 2300), (3, 5, 8, 2, 64, 5000),
+                                            (8, 1, 32, 8, 128, 300), (5, 3, 8, 2, 256, 130), (3, 5, 16, 4, 64, 512)])
+def test_short_rests(page, B, n, Hq, Hkv, D, P):
+    """Prefixes that share the card with their rests, and ones that few rows read like rests."""
+    lens = [P + n + 9 * b for b in range(B)]
+    lens[-1], lens[0] = P // 2, P
+    s = Shared(B, P, lens, n, Hq, Hkv, D, page)
+    s.check(s.run())
+    assert binding.device_error() == 0
+
+
 @pytest.mark.parametrize("n,Hq,Hkv,D", [(1, 8, 2, 128), (5, 24, 2, 256), (9, 8, 1, 64), (9, 16, 1, 128)])
 def test_growing_scores(n, Hq, Hkv, D):
     """Scores that grow along the prefix and the rests: running maxima are raised again and again."""
