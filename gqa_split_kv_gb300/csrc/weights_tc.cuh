@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
         const float* ks = reinterpret_cast<const float*>(smem + Gm::OFF_KS) + (at & 7) * Gm::KEYS;
         const int end = min(t1, SUMS ? t1 : lim) - first;  // keys of the tile that the row sees
         const float mine = SUMS ? ks[me] : 0.f;
-        // SUMS: the first row that sees the token
-        const int from = SUMS ? (t - (u.len - p.n)) * p.G - wp.row0 : 0;
+        // SUMS: the first row that sees the token (an early one's product with G could pass 32 bits below 0)
+        const int from = SUMS ? max(t - (u.len - p.n), 0) * p.G - wp.row0 : 0;
         const bool edge = SUMS ? __any_sync(0xffffffffu, from > 0) : __any_sync(0xffffffffu, end < Gm::KEYS);
         float w = 0.f;
 #pragma unroll 1
