@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(ScoreGeo<D, INT8, NT>::THREADS, ScoreGeo<D, IN
         p.part_ml[((size_t)u.id + blockIdx.x) * 16 + threadIdx.x] = join_warps<Gm::WARPS, Gm::ROWS>(ml, threadIdx.x);
       __syncthreads();
     }
+    __syncwarp();  // every lane has read its tokens' scales: their place is filled again
     ring.issue(stage);
     stage = stage + 1 == Gm::NSTAGE ? 0 : stage + 1;
     ++j;

@@ -1,4 +1,5 @@
-"""Attention weights over lengths whose products pass 32 bits."""
+"""Attention weights over lengths whose products pass 32 bits, and with scales that differ from token to token."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -6,7 +7,21 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
+from long_cache_helpers import Cache, f64, randn, score_error  # noqa: E402
+from oracle import long_cache as ol  # noqa: E402
 from gqa_split_kv_gb300 import binding  # noqa: E402
+
+
+def check(got, q, k, scale, finite):
+    """The weights of one sequence; tolerance: twice a score's error, taken of the finite scores, and the sums'."""
+    with np.errstate(invalid="ignore"):
+        want = ol.weights(f64(q), k, scale)
+    rows = q.shape[0] * q.shape[1] // k.shape[1]
+    tol = want * (2 * score_error(f64(q), finite, scale, q.shape[-1]) + (rows + 64) * 2.0 ** -24) + rows * 1e-37
+    got = f64(got)
+    assert (np.isnan(got) == np.isnan(want)).all(), np.argwhere(np.isnan(got) != np.isnan(want))[:5]
+    assert not (np.abs(got - want) > tol).any()
+    return want
 
 
 def test_lengths_whose_products_with_the_group_pass_32_bits():
@@ -19,4 +34,24 @@ def test_lengths_whose_products_with_the_group_pass_32_bits():
     w = binding.kv_weights_int8_contig(q, k, scale, None)
     off = (w.double() * (L / G) - 1).abs().max().item()
     assert off <= 400 * 2.0 ** -24, off
+    assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("D,G,n", [(64, 4, 1), (128, 8, 1), (128, 4, 3), (256, 6, 2)])
+def test_every_token_has_its_own_scale(D, G, n, page):
+    """Scales of neighbouring tokens 64 times apart, over many rounds of the ring of keys: a scale of another token
+    shows."""
+    lens = [6000, 1, 333, 4097]
+    c = Cache(D + G, lens, 6000, 2, D, page, names="k", int8=True)
+    far = torch.where(torch.arange(6000, device="cuda") % 2 == 0, 2.0 ** -12, 2.0 ** -6)
+    s = (torch.rand(4, 2, 6000, generator=c.gen, device="cuda") + 0.5) * far
+    c.put_numbers("ks", s)
+    q = randn(c.gen, 4, n, 2 * G, D)
+    if page:
+        got = c.numbers_back(binding.kv_weights_int8_paged(q, c.kp, c.ksp, None, c.table, c.seq_lens, c.cap))
+    else:
+        got = binding.kv_weights_int8_contig(q, c.k, c.ks, None, c.seq_lens)
+    for b, L in enumerate(lens):
+        check(got[b, :, :L], q[b], c.values("k", b), D ** -0.5, c.values("k", b))
     assert binding.device_error() == 0
