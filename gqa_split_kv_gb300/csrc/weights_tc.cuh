@@ -110,7 +110,9 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
       offs[((it + k) & 1) * Gm::KEYS + threadIdx.x] = next_off;
       reinterpret_cast<float*>(smem + Gm::OFF_KS)[((it + k) & 7) * Gm::KEYS + threadIdx.x] = next_scale * p.scale_log2;
     };
-    // its queries (the products of the last unit's are done: every thread has seen their results)
+    // Its queries (the products of the last unit's are done: every thread has seen their results).  Rows past the last one
+    // are the last one again, with its m and a factor of 0: zeros there would be NaN against an infinite key, which that
+    // row may well score -inf, and a NaN of its own is in the sum anyway.
     {
       constexpr int QCH = D / 8, STEP = Gm::THREADS / QCH;  // a thread's chunk of every STEP-th row
       static_assert(Gm::THREADS % QCH == 0, "");
@@ -118,10 +120,11 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
       const uint32_t column = sbase + (c / 8) * 16384;
       int in = threadIdx.x / QCH, token = (wp.row0 + in) / p.G, g = wp.row0 + in - token * p.G;
       const __nv_bfloat16* from = p.q + ((size_t)u.b * p.n * p.Hq + (size_t)u.h * p.G) * D + c * 8;
+      const int last = wp.row0 + wp.rows - 1, last_token = last / p.G;
+      const __nv_bfloat16* again = from + ((size_t)last_token * p.Hq + (last - last_token * p.G)) * D;
 #pragma unroll 4
       for (; in < Gm::ROWS; in += STEP) {
-        const bool is = in < wp.rows;
-        cp_async16(column + swz<128>(in, c % 8), is ? from + ((size_t)token * p.Hq + g) * D : p.q, is);
+        cp_async16(column + swz<128>(in, c % 8), in < wp.rows ? from + ((size_t)token * p.Hq + g) * D : again, true);
         token += more;
         g += step_g;
         if (g >= p.G) {
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
         const SegSums sums = seg_sums(walk.lens, p.B, p.cap, 0, u.b);
         const long long a = sums.before * p.Hkv + (long long)u.h * u.tiles;
         const int c0 = seg_owner(walk.all, walk.used, a), c1 = seg_owner(walk.all, walk.used, a + u.tiles - 1);
-        const float2* ml = p.part_ml + ((long long)u.id + c0) * Gm::ROWS + r;
+        const float2* ml = p.part_ml + ((long long)u.id + c0) * Gm::ROWS + min(r, wp.rows - 1);
         float M = kNegInf, L = 0.f;
         constexpr int U2 = 20;
         for (int k0 = 0; k0 <= c1 - c0; k0 += U2) {
@@ -157,8 +160,8 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
           L = (M == kNegInf ? L : L * exp2_approx(M - top)) + sum;
           M = top;
         }
-        // no weight of rows that are not
-        const float2 f = r < wp.rows ? weight_factors(make_float2(M, L)) : make_float2(0.f, 0.f);
+        float2 f = weight_factors(make_float2(M, L));
+        if (r >= wp.rows) f.y = 0.f;
         float* to = reinterpret_cast<float*>(smem + Gm::OFF_F) + (r / 2) * 4 + r % 2;  // -m of two rows, then their 1 / l
         to[0] = -f.x;
         to[2] = f.y;

@@ -1,4 +1,5 @@
-"""Attention weights over lengths whose products pass 32 bits, and with scales that differ from token to token."""
+"""Attention weights where scores are not finite, over lengths whose products pass 32 bits, and with scales that differ from
+token to token."""
 import numpy as np
 import pytest
 
@@ -12,6 +13,19 @@ from oracle import long_cache as ol  # noqa: E402
 from gqa_split_kv_gb300 import binding  # noqa: E402
 
 
+def weigh(c, q):
+    if c.page:
+        return c.numbers_back(binding.kv_weights_paged(q, c.kp, None, c.table, c.seq_lens, c.cap))
+    return binding.kv_weights_contig(q, c.k, None, c.seq_lens)
+
+
+def put(c, b, t, h, d, x):
+    """Element d of token t's key becomes x, in the cache and in its pool."""
+    c.k[b, t, h, d] = x
+    if c.page:
+        c.kp[int(c.table[b, t // c.page]), t % c.page, h, d] = x
+
+
 def check(got, q, k, scale, finite):
     """The weights of one sequence; tolerance: twice a score's error, taken of the finite scores, and the sums'."""
     with np.errstate(invalid="ignore"):
@@ -22,6 +36,28 @@ def check(got, q, k, scale, finite):
     assert (np.isnan(got) == np.isnan(want)).all(), np.argwhere(np.isnan(got) != np.isnan(want))[:5]
     assert not (np.abs(got - want) > tol).any()
     return want
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("D,rows", [(64, 3), (128, 13), (64, 17), (128, 33), (256, 40), (128, 96), (128, 145)])
+def test_a_score_of_minus_infinity_is_a_weight_of_zero(D, rows, page):
+    """An infinite key that every row scores -inf: its weight is 0 and the others' are what they are without it."""
+    c = Cache(D + rows, [300, 77], 300, 2, D, page, names="k")
+    q = randn(c.gen, 2, 1, 2 * rows if rows <= 64 else 2, D)
+    if rows > 64:  # more rows than a group may have heads: several tokens
+        q = randn(c.gen, 2, rows, 2, D)
+    q[..., 5] = -q[..., 5].abs() - 0.5
+    clean = [c.values("k", b) for b in range(2)]
+    for b, t in ((0, 130), (1, 7)):
+        for h in range(2):
+            put(c, b, t, h, 5, float("inf"))
+    got = weigh(c, q)
+    for b, (L, t) in enumerate(((300, 130), (77, 7))):
+        if q.shape[1] > L:  # (the first tokens see nothing)
+            continue
+        want = check(got[b, :, :L], q[b], c.values("k", b), D ** -0.5, clean[b])
+        assert (want[:, t] == 0).all() and np.isfinite(want).all()
+    assert binding.device_error() == 0
 
 
 def test_lengths_whose_products_with_the_group_pass_32_bits():
