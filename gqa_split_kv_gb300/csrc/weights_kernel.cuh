@@ -439,14 +439,17 @@ __global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const __
       if (!mine) continue;
       const float4* x = reinterpret_cast<const float4*>(wp.scores + ((size_t)(line + j) * kTile + threadIdx.x % kTile) *
                                                                         score_rows(wp.rows));
+      // The rows that see the token are those from `from` on (rows past the last: score -inf, factor 0); the others' scores are
+      // -inf, but a row's factor may be NaN.
+      const int from = max(t - (L - p.n), 0) * p.G;
       float w = 0.f;
 #pragma unroll 2
-      for (int r = 0; r < wp.rows; r += 4) {  // (rows past the last: score -inf, factor 0)
+      for (int r = from & ~3; r < wp.rows; r += 4) {
         const float4 y = __ldcg(x + r / 4);
-        w = fmaf(exp2_approx(y.x - row[r].x), row[r].y, w);
-        w = fmaf(exp2_approx(y.y - row[r + 1].x), row[r + 1].y, w);
-        w = fmaf(exp2_approx(y.z - row[r + 2].x), row[r + 2].y, w);
-        w = fmaf(exp2_approx(y.w - row[r + 3].x), row[r + 3].y, w);
+        w = fmaf(exp2_approx(y.x - row[r].x), r >= from ? row[r].y : 0.f, w);
+        w = fmaf(exp2_approx(y.y - row[r + 1].x), r + 1 >= from ? row[r + 1].y : 0.f, w);
+        w = fmaf(exp2_approx(y.z - row[r + 2].x), r + 2 >= from ? row[r + 2].y : 0.f, w);
+        w = fmaf(exp2_approx(y.w - row[r + 3].x), row[r + 3].y, w);  // (from is less than r + 4)
       }
       if (c.good) wp.out[o] = wp.prior ? fmaf(wp.decay, before, w) : w;
     }

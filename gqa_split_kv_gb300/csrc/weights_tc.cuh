@@ -283,11 +283,13 @@ __global__ void __launch_bounds__(WeightsTcGeo<D>::THREADS, WeightsTcGeo<D>::PER
               const float4 g = f[i];
               float2 y = fma_f32x2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), mine2,
                                    make_float2(g.x, g.y));
-              if (edge) {
-                y.x = c0 + 2 * i >= from ? y.x : kNegInf;
-                y.y = c0 + 2 * i + 1 >= from ? y.y : kNegInf;
+              float2 part = make_float2(g.z, g.w);
+              if (edge) {  // a row that does not see the token gives it nothing, not even its NaN
+                const bool a = c0 + 2 * i >= from, b = c0 + 2 * i + 1 >= from;
+                y = make_float2(a ? y.x : kNegInf, b ? y.y : kNegInf);
+                part = make_float2(a ? part.x : 0.f, b ? part.y : 0.f);
               }
-              acc[i & 1] = fma_f32x2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(g.z, g.w), acc[i & 1]);
+              acc[i & 1] = fma_f32x2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), part, acc[i & 1]);
             }
             w += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           } else {

@@ -1,5 +1,5 @@
-"""Attention weights where scores are not finite, over lengths whose products pass 32 bits, and with scales that differ from
-token to token."""
+"""Attention weights where scores are not finite, where rows see different tokens, over lengths whose products pass 32 bits,
+and with scales that differ from token to token."""
 import numpy as np
 import pytest
 
@@ -57,6 +57,27 @@ def test_a_score_of_minus_infinity_is_a_weight_of_zero(D, rows, page):
             continue
         want = check(got[b, :, :L], q[b], c.values("k", b), D ** -0.5, clean[b])
         assert (want[:, t] == 0).all() and np.isfinite(want).all()
+    assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("page", [0, 32])
+@pytest.mark.parametrize("n,G,D", [(2, 1, 64), (3, 4, 128), (5, 3, 256), (3, 8, 64), (7, 7, 128), (40, 4, 128), (20, 5, 256)])
+def test_a_row_that_is_not_finite_reaches_the_tokens_it_sees(n, G, D, page):
+    """The last token but one scores its own key +inf with one head, so that row is NaN; the last token's rows score that
+    key -inf.  The last key is seen by the last token alone, and its weight is finite."""
+    lens = [n + 90, 200]
+    c = Cache(n + G + D, lens, 200, 2, D, page, names="k")
+    q = randn(c.gen, 2, n, 2 * G, D)
+    q[..., 5] = -q[..., 5].abs() - 0.5
+    q[:, n - 2, ::G, 5] = 1.0
+    clean = [c.values("k", b) for b in range(2)]
+    for b, L in enumerate(lens):
+        for h in range(2):
+            put(c, b, L - 2, h, 5, float("inf"))
+    got = weigh(c, q)
+    for b, L in enumerate(lens):
+        want = check(got[b, :, :L], q[b], c.values("k", b), D ** -0.5, clean[b])
+        assert np.isnan(want[:, :L - 1]).all() and (want[:, L - 1] > 0).all()
     assert binding.device_error() == 0
 
 
