@@ -191,9 +191,11 @@ int evict_call(EvictParams& p, bool paged, bool int8, int head_dim, long long ca
   if (!p.kept || !p.new_lens || !aligned(p.kept, 4) || !aligned(p.new_lens, 4) || !aligned(p.seq_lens, 4) ||
       !aligned(p.page_table, 4) || (paged && (!p.seq_lens || (p.max_pages > 0 && !p.page_table))))
     return DA_ERR_INVALID_ARG;
+  // (a cache without a token may have no memory: only the outputs have to be whole then)
   if (rows && (!p.k || !p.weights || (int8 && (!p.ks || !p.v != !p.vs)))) return DA_ERR_INVALID_ARG;
   if (!int8 && (p.ks || p.vs || p.ks_out || p.vs_out)) return DA_ERR_INVALID_ARG;
-  if (!p.in_place && (!p.k_out || !p.v != !p.v_out || p.out_ctx < p.keep || (int8 && (!p.ks_out || !p.vs != !p.vs_out))))
+  if (!p.in_place && (!p.k_out || (rows && !p.v != !p.v_out) || p.out_ctx < p.keep ||
+                      (int8 && (!p.ks_out || !p.v_out != !p.vs_out))))
     return DA_ERR_INVALID_ARG;
   for (const void* x : {p.k, p.v, p.k_out, p.v_out})
     if (!aligned(x, 16)) return DA_ERR_INVALID_ARG;

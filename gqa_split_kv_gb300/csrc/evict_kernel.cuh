@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int a = role - copies;
     const float* src = a == 0 ? p.weights : a == 1 ? p.ks : p.vs;
     float* dst = a == 0 ? p.weights_out : a == 1 ? p.ks_out : p.vs_out;
-    if (!src || !dst) return;
+    if (!dst || (!src && len > 0)) return;
     for (int i0 = 0; i0 < len; i0 += kMoveThreads * U) {
       float w[U];
       int t[U];
