@@ -1,4 +1,5 @@
-"""Eviction at its edges: caches without a token."""
+"""Eviction and weights at their edges: pages outside the pool, and caches without a token."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -6,8 +7,98 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
-from long_cache_helpers import lens_of  # noqa: E402
+from long_cache_helpers import Cache, f64, lens_of, randn, score_error  # noqa: E402
+from oracle import long_cache as ol  # noqa: E402
 from gqa_split_kv_gb300 import binding  # noqa: E402
+
+
+def with_bad_page(int8, names, column=2):
+    """Two sequences of 90 and 80 tokens in pages of 16; the first one's page of tokens 32 .. 47 lies outside the pool.
+    Every cell of the pools is finite.  Returns the cache and the page that it had."""
+    c = Cache(12, [90, 80], 96, 2, 64, 16, names=names, int8=int8)
+    c.put_numbers("w", torch.rand(2, 2, 96, generator=c.gen, device="cuda"))
+    for x in ("kp", "vp", "ksp", "vsp", "wp"):
+        if hasattr(c, x) and getattr(c, x).is_floating_point():
+            getattr(c, x).nan_to_num_(7.0)
+    lost = int(c.table[0, column])
+    c.table[0, column] = 10 ** 6
+    return c, lost
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_weights_do_not_write_for_a_page_outside_the_pool(int8, n):
+    c, lost = with_bad_page(int8, "k")
+    q = randn(c.gen, 2, n, 4, 64)
+    before = c.wp.clone()
+    if int8:
+        binding.kv_weights_int8_paged(q, c.kp, c.ksp, c.wp, c.table, c.seq_lens, c.cap)
+    else:
+        binding.kv_weights_paged(q, c.kp, c.wp, c.table, c.seq_lens, c.cap)
+    assert binding.device_error() == 4
+    live = torch.zeros_like(c.wp, dtype=torch.bool)
+    for b, t0, t1, page in c.places():
+        if page != 10 ** 6:
+            live[page, :, :t1 - t0] = True
+    assert not live[lost].any()
+    assert torch.equal(c.wp[~live], before[~live])
+    assert (c.wp[live] >= before[live]).all()
+    k = c.values("k", 1)  # the other sequence is what it is without the bad page
+    w = ol.weights(f64(q[1]), k, 0.125)
+    tol = w * (2 * score_error(f64(q[1]), k, 0.125, 64) + (2 * n + 64) * 2.0 ** -24)
+    for t0 in range(0, 80, 16):
+        page = int(c.table[1, t0 // 16])
+        got = f64(c.wp[page]) - f64(before[page])
+        assert (np.abs(got - w[:, t0:t0 + 16]) <= tol[:, t0:t0 + 16] + 2.0 ** -23 * (w[:, t0:t0 + 16] + 1)).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("column", [0, 2, 4])
+def test_eviction_with_a_page_outside_the_pool(int8, in_place, column):
+    """Rows from it are zeros, rows to it are not written, and the other sequence is cut as ever."""
+    keep, first, recent = 40, 2, 8
+    c, lost = with_bad_page(int8, "kv", column)
+    names = ("k", "v", "ks", "vs", "w") if int8 else ("k", "v", "w")
+    pools = [getattr(c, x + "p") for x in names]
+    before = [p.clone() for p in pools]
+    out = {}
+    if not in_place:
+        out = dict(k_out=torch.full((2, keep, 2, 64), 3, device="cuda").to(c.k.dtype))
+        out["v_out"] = out["k_out"].clone()
+        if int8:
+            out["k_scale_out"], out["v_scale_out"] = (torch.full((2, 2, keep), 5.0, device="cuda") for _ in "kv")
+        out["weights_out"] = torch.full((2, 2, keep), 5.0, device="cuda")
+    fn = binding.kv_evict_int8_paged if int8 else binding.kv_evict_paged
+    kept, new_lens = fn(*pools, c.table, c.seq_lens, c.cap, keep, first=first, recent=recent, **out)
+    assert binding.device_error() == 4
+    assert new_lens.tolist() == [keep, keep]
+    bad = 10 ** 6
+    place = lambda b, t: (int(c.table[b, t // 16]), t % 16)  # noqa: E731
+    want = [p.clone() for p in before]  # in place: what each pool has to hold
+    for b, L in enumerate((90, 80)):
+        for h in range(2):
+            at = kept[b, h].cpu().numpy()
+            assert (np.diff(at) > 0).all() and at[0] >= 0 and at[-1] == L - 1
+            if b == 1:
+                w = [float(before[-1][place(1, t)[0], h, place(1, t)[1]]) for t in range(L)]
+                assert (at == ol.evict(np.array(w), keep, first, recent)).all()
+            for x, p in enumerate(before):
+                cell = lambda q, page, row: q[page, row, h] if q.dim() == 4 else q[page, h, row]  # noqa: E731
+                for i, t in enumerate(at):
+                    page, row = place(b, int(t))
+                    value = torch.zeros_like(cell(p, 0, 0)) if page == bad else cell(p, page, row)
+                    if not in_place:
+                        y = list(out.values())[x]
+                        assert torch.equal(y[b, i, h] if y.dim() == 4 else y[b, h, i], value), (b, h, x, i, t)
+                    elif place(b, i)[0] != bad and t != i:
+                        cell(want[x], *place(b, i)).copy_(value)
+                if in_place and x == len(before) - 1:
+                    for t in range(keep, L):
+                        if place(b, t)[0] != bad:
+                            cell(want[x], *place(b, t)).zero_()
+    for p, y in zip(pools, want if in_place else before):
+        assert torch.equal(p, y)
 
 
 @pytest.mark.parametrize("paged", [False, True])
