@@ -5,6 +5,8 @@
 // The rows of a KV head are those of all B q_len tokens times its G query heads, so a batch
 // turns the prefix into two dense products,
 //   S = Q K^T,  O = 2^(S - m) V,
+// (a weight of 0 times a value that is not finite is NaN: rows that do not see all of the prefix and come out so are
+// computed by themselves in seg_merge_prefix_kernel)
 // 4 D operations a (row, key) and D * 4 bytes a key once a block of rows: bound by the bytes
 // up to about 128 rows, then by the tensor cores and, beside them, one exponential a (row,
 // key).  The engine is that of latent_prefill.cuh: a CTA owns up to two tiles of 128 rows (one

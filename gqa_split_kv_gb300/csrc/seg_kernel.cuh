@@ -888,6 +888,67 @@ struct SegRow {
 
 constexpr int kMergeThreads = 256;
 
+// On the tensor cores a value of the prefix meets every row, with a weight of 0 where the row's sequence ends before it; if it
+// is not finite, that is NaN.  A row that sees a part of the prefix alone is computed here by itself, by its warp: 32 tokens
+// at a time, a lane the score of one and then its columns of the sum.  False for other rows.  (Not inlined: it is rare.)
+template <int D>
+__device__ __noinline__ bool seg_row_of_prefix(const SegParams& p, long long row) {
+  const int lane = threadIdx.x & 31, row_step = p.Hkv * D;
+  const int hq = (int)(row % p.Hq), token = (int)(row / p.Hq), h = hq / p.G, b = token / p.n;
+  const int seen = seg_len(p.seq_lens, b, p.cap) - p.n + 1 + (token - b * p.n);
+  if (seen <= 0 || seen >= p.base) return false;
+  SegRow<D> acc;
+  const __nv_bfloat16 *keys = p.prefix_table ? p.k : p.kp, *values = p.prefix_table ? p.v : p.vp;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + ((size_t)token * p.Hq + hq) * D);
+#pragma unroll 1
+  for (int t0 = 0; t0 < seen; t0 += 32) {
+    const int t = t0 + lane;
+    long long at = t;
+    float s = kNegInf;
+    if (t < seen) {
+      if (p.prefix_table) {
+        const int col = t / p.page_size, page = load_dependent(p.prefix_table + col);
+        at = ((unsigned)page < (unsigned)p.num_pages ? (long long)page : 0ll) * p.page_size + (t - col * p.page_size);
+      }
+      const uint32_t* k = reinterpret_cast<const uint32_t*>(keys + at * row_step + h * D);
+      s = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D / 2; ++c) {
+        const uint32_t x = load_dependent(q + c), y = load_dependent(k + c);
+        s = fmaf(bf16lo_to_f32(x), bf16lo_to_f32(y), s);
+        s = fmaf(bf16hi_to_f32(x), bf16hi_to_f32(y), s);
+      }
+      s *= p.scale_log2;
+    }
+    float top = fmaxf(acc.m, s);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float mu = top == kNegInf ? 0.f : top, old = acc.m == kNegInf ? 1.f : exp2_approx(acc.m - mu);
+    const float w = exp2_approx(s - mu);
+    float sum = w;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    acc.m = top;
+    acc.l = acc.l * old + sum;
+#pragma unroll
+    for (int c = 0; c < SegRow<D>::N; ++c) acc.a[c] *= old;
+#pragma unroll 1
+    for (int i = 0; i < min(32, seen - t0); ++i) {
+      const float f = __shfl_sync(0xffffffffu, w, i);
+      const __nv_bfloat16* v = values + __shfl_sync(0xffffffffu, at, i) * row_step + h * D;
+#pragma unroll
+      for (int c = 0; c < SegRow<D>::N / 2; ++c) {
+        // columns as SegRow has them
+        const uint32_t y = load_dependent(reinterpret_cast<const uint32_t*>(v) + (D == 64 ? lane : 2 * lane + 64 * (c / 2) + c % 2));
+        acc.a[2 * c] += f * bf16lo_to_f32(y);
+        acc.a[2 * c + 1] += f * bf16hi_to_f32(y);
+      }
+    }
+  }
+  acc.store(p.out + row * D);
+  return true;
+}
+
 // Joins the prefix's and the rests' partials: a warp a row of the output, the loads of 8 pieces in flight.  33 MB for 64
 // x 64 heads of 128: 8 us behind the rests' kernel.  The lengths are read
 // before the wait: the kernels that wrote them were done before seg_kernel, and prefix_tc_kernel
@@ -932,6 +993,12 @@ __global__ void __launch_bounds__(kMergeThreads, D == 256 ? 2 : 4) seg_merge_pre
       o = p.part_o + at * D;
     }
   });
+  if (p.slabs) {
+    bool odd = false;
+#pragma unroll
+    for (int c = 0; c < SegRow<D>::N; ++c) odd = odd || !(acc.a[c] - acc.a[c] == 0.f);
+    if (__any_sync(0xffffffffu, odd) && seg_row_of_prefix<D>(p, row)) return;
+  }
   acc.store(p.out + row * D);
 }
 

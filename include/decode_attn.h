@@ -569,9 +569,8 @@ const char* decode_status_string(int status);
  *  workspace  prefix_attn_workspace_bytes(...) bytes, 16-byte aligned; contents need not be kept, calls that
  *           share one must not overlap on the GPU.  num_sms <= 0: of the current device.
  * Softmax in fp32, the weights rounded to bf16 for the product with V, fp32 sums, one rounding of the output.
- * What lies past a sequence's end may hold anything, and no row's infinities or NaN reach another's, but for one
- * case: with more than 16 query rows a KV head (batch * q_len * G), values of the prefix that are not finite reach
- * every row, those of sequences that end before them too.
+ * What lies past a sequence's end may hold anything, and infinities and NaN, of the prefix too, reach only the rows
+ * that see them.
  * Pages outside [0, num_pages) set bit 2 of the device error word and read page 0 instead.  Outputs may not
  * overlap inputs.
  */
