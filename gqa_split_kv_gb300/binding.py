@@ -549,7 +549,8 @@ def kv_write_contig(k_new, v_new, k, v, seq_lens=None, inv_freq=None, offset: in
                     magnitude: float = 1.0, stream=None):
     """Writes the last q_len tokens of every sequence, k_new/v_new bf16 [B, q_len, Hkv, D], into the bf16 cache k/v
     [B, max_ctx, Hkv, D]; seq_lens int32 [B] (with the new tokens) or None.  inv_freq: rotate the keys at their
-    positions first (rope_apply).  v_new and v may both be None (keys only)."""
+    positions first (rope_apply; not in a cache that kv_evict_* has cut, where places are no positions).  v_new and v may
+    both be None (keys only)."""
     (_ext_module or _ext()).kv_write(k_new, v_new, k, v, None, None, None, seq_lens, 0, inv_freq, offset, interleaved,
                                      magnitude, stream)
 
@@ -768,7 +769,10 @@ def kv_evict_contig(k, v, weights, seq_lens, keep: int, *, first: int = 0, recen
     [B, Hkv, max_ctx]; ties: the lower position).  They move together to positions 0, 1, ... in their order, and their
     weights with them: in place, or to k_out, v_out [B, >= keep, Hkv, D] and weights_out [B, Hkv, >= keep]; weights
     behind them become 0.  Returns (kept, new_lens): int32 [B, Hkv, keep], the old position of each, -1 behind the
-    last, and int32 [B], min(seq_lens, keep); seq_lens is not written."""
+    last, and int32 [B], min(seq_lens, keep); seq_lens is not written.
+
+    Afterwards a token's place is no longer its position: rotate new keys and queries by rope_apply with positions that
+    the program counts, and write the keys by kv_write_* without inv_freq (with it they are rotated by their places)."""
     return (_ext_module or _ext()).kv_evict(k, v, None, None, weights, None, seq_lens, 0, keep, first, recent, kept,
                                             new_lens, k_out, v_out, None, None, weights_out, stream)
 

@@ -399,7 +399,7 @@ int rope_apply(const void* x, void* out, const int* positions, const double* inv
  *                head_dim: a slice of a fused projection will do); 16-byte aligned
  *  inv_freq      NULL, or the frequencies by which keys are rotated first, as in rope_apply,
  *                at their positions (rot_offset a multiple of 8, rot_dim of 16); in fp32,
- *                without a rounding in between
+ *                without a rounding in between (not for a cache that kv_evict_* has cut: see there)
  *  v_new, v      both NULL: only keys are written (a latent cache, num_kv_heads 1)
  *  bf16 caches   as decode_attn_contig / _paged read them (latent_attn_*: num_kv_heads 1,
  *                head_dim latent_dim + 64); head_dim a multiple of 8 up to 1024
@@ -681,6 +681,10 @@ int kv_weights_int8_paged(const void* q, const void* k_pool_i8, const float* k_s
  *  kept     int32 [batch, num_kv_heads, keep]; new_lens int32 [batch]
  * In place, sequences may not share pages.  A page outside the pool is flagged (bit 2); rows from it are zeros,
  * rows to it are not written.
+ * After an eviction a token's place in the cache is no longer its position in the sequence, and the places of a
+ * position differ from KV head to KV head.  Kept keys keep the rotation that they were written with, while kv_write_*
+ * with inv_freq rotates a new key by its place: turn new keys and queries by rope_apply, with the positions that the
+ * program counts, and write with inv_freq NULL.  Block means of the cache are to be made again.
  */
 int kv_evict_contig(void* k, void* v, float* weights, const int* seq_lens, int batch, int num_kv_heads, int head_dim,
                     int max_ctx, int keep, int first, int recent, void* k_out, void* v_out, float* weights_out,
