@@ -123,3 +123,21 @@ def test_a_cache_without_a_token(paged, int8):
         if x != "weights_out":
             assert torch.equal(out[x], old[x])
     assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("B,L,keep", [(1, 500_000, 300_000), (1, 500_000, 700), (330, 50_000, 900)])
+def test_more_weights_than_shared_memory_holds(B, L, keep):
+    """One sequence whose share of a cluster's CTA is more than its shared memory, and many of a CTA each."""
+    gen = torch.Generator(device="cuda").manual_seed(L)
+    k = torch.arange(L, device="cuda", dtype=torch.int32).view(1, L, 1, 1).expand(B, L, 1, 4).contiguous().view(torch.bfloat16)
+    w = (torch.rand(B, 1, L, generator=gen, device="cuda") * 5000).floor()  # with ties
+    before = w.clone()
+    kept, new_lens = binding.kv_evict_contig(k, None, w, None, keep, first=3, recent=50)
+    assert new_lens.tolist() == [keep] * B
+    for b in sorted({0, B // 2, B - 1}):
+        want = ol.evict(f64(before[b, 0]), keep, 3, 50)
+        assert (kept[b, 0].cpu().numpy() == want).all()
+        at = torch.from_numpy(want).cuda()
+        assert torch.equal(k[b, :keep, 0].view(torch.int32), at.to(torch.int32)[:, None].expand(keep, 4))
+        assert torch.equal(w[b, 0, :keep], before[b, 0, at]) and not w[b, 0, keep:].any()
+    assert binding.device_error() == 0
