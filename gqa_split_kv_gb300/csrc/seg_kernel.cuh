@@ -890,16 +890,16 @@ constexpr int kMergeThreads = 256;
 
 // On the tensor cores a value of the prefix meets every row, with a weight of 0 where the row's sequence ends before it; if it
 // is not finite, that is NaN.  A row that sees a part of the prefix alone is computed here by itself, by its warp: 32 tokens
-// at a time, a lane the score of one and then its columns of the sum.  False for other rows.  (Not inlined: it is rare.)
+// at a time, a lane the score of one and then its columns of the sum; 0.2 us a token.  (Not inlined: it is rare.)
 template <int D>
-__device__ __noinline__ bool seg_row_of_prefix(const SegParams& p, long long row) {
+__device__ __noinline__ void seg_row_of_prefix(const SegParams& p, long long row) {
   const int lane = threadIdx.x & 31, row_step = p.Hkv * D;
   const int hq = (int)(row % p.Hq), token = (int)(row / p.Hq), h = hq / p.G, b = token / p.n;
   const int seen = seg_len(p.seq_lens, b, p.cap) - p.n + 1 + (token - b * p.n);
-  if (seen <= 0 || seen >= p.base) return false;
+  if (seen <= 0 || seen >= p.base) return;
   SegRow<D> acc;
   const __nv_bfloat16 *keys = p.prefix_table ? p.k : p.kp, *values = p.prefix_table ? p.v : p.vp;
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + ((size_t)token * p.Hq + hq) * D);
+  const uint4* q = reinterpret_cast<const uint4*>(p.q + ((size_t)token * p.Hq + hq) * D);
 #pragma unroll 1
   for (int t0 = 0; t0 < seen; t0 += 32) {
     const int t = t0 + lane;
@@ -910,13 +910,17 @@ __device__ __noinline__ bool seg_row_of_prefix(const SegParams& p, long long row
         const int col = t / p.page_size, page = load_dependent(p.prefix_table + col);
         at = ((unsigned)page < (unsigned)p.num_pages ? (long long)page : 0ll) * p.page_size + (t - col * p.page_size);
       }
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(keys + at * row_step + h * D);
+      const uint4* k = reinterpret_cast<const uint4*>(keys + at * row_step + h * D);
       s = 0.f;
 #pragma unroll 4
-      for (int c = 0; c < D / 2; ++c) {
-        const uint32_t x = load_dependent(q + c), y = load_dependent(k + c);
-        s = fmaf(bf16lo_to_f32(x), bf16lo_to_f32(y), s);
-        s = fmaf(bf16hi_to_f32(x), bf16hi_to_f32(y), s);
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = load_dependent(q + c), y = load_dependent(k + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s = fmaf(bf16lo_to_f32(xs[i]), bf16lo_to_f32(ys[i]), s);
+          s = fmaf(bf16hi_to_f32(xs[i]), bf16hi_to_f32(ys[i]), s);
+        }
       }
       s *= p.scale_log2;
     }
@@ -932,7 +936,7 @@ __device__ __noinline__ bool seg_row_of_prefix(const SegParams& p, long long row
     acc.l = acc.l * old + sum;
 #pragma unroll
     for (int c = 0; c < SegRow<D>::N; ++c) acc.a[c] *= old;
-#pragma unroll 1
+#pragma unroll 8
     for (int i = 0; i < min(32, seen - t0); ++i) {
       const float f = __shfl_sync(0xffffffffu, w, i);
       const __nv_bfloat16* v = values + __shfl_sync(0xffffffffu, at, i) * row_step + h * D;
@@ -946,7 +950,6 @@ __device__ __noinline__ bool seg_row_of_prefix(const SegParams& p, long long row
     }
   }
   acc.store(p.out + row * D);
-  return true;
 }
 
 // Joins the prefix's and the rests' partials: a warp a row of the output, the loads of 8 pieces in flight.  33 MB for 64
@@ -993,13 +996,13 @@ __global__ void __launch_bounds__(kMergeThreads, D == 256 ? 2 : 4) seg_merge_pre
       o = p.part_o + at * D;
     }
   });
+  acc.store(p.out + row * D);
   if (p.slabs) {
     bool odd = false;
 #pragma unroll
     for (int c = 0; c < SegRow<D>::N; ++c) odd = odd || !(acc.a[c] - acc.a[c] == 0.f);
-    if (__any_sync(0xffffffffu, odd) && seg_row_of_prefix<D>(p, row)) return;
+    if (__any_sync(0xffffffffu, odd)) seg_row_of_prefix<D>(p, row);
   }
-  acc.store(p.out + row * D);
 }
 
 }  // namespace da
