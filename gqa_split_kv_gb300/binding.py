@@ -669,7 +669,8 @@ def prefix_attn_contig(q, k_prefix, v_prefix, k, v, seq_lens=None, *, scale: Opt
     batch: q bf16 [B, q_len, Hq, D] (D 64, 128 or 256), k_prefix/v_prefix bf16 [P, Hkv, D], k/v bf16
     [B, max_ctx, Hkv, D] (row t - P holds a sequence's token t), seq_lens int32 [B] with the prefix, or None
     (P + max_ctx each).  Query token i of sequence b sees its first seq_lens[b] - q_len + 1 + i tokens; one that sees
-    none gives zeros.  workspace: as made by prefix_workspace (None: made here).  Returns out like q."""
+    none gives zeros.  workspace: as made by prefix_workspace (None: made here).  Returns out like q.  For new prompts of
+    more than about 100 tokens a sequence prefill_attn_* over whole sequences is faster."""
     return (_ext_module or _ext()).prefix_attn(q, k_prefix, v_prefix, k, v, None, 0, None, seq_lens, 0, scale, workspace,
                                                out, stream)
 
@@ -726,7 +727,8 @@ def sparse_attn_paged(q, k_pool, v_pool, blocks, page_table, seq_lens, max_seq_l
 
 def weights_workspace(batch: int, q_len: int, num_q_heads: int, num_kv_heads: int, max_len: int):
     """A workspace for kv_weights_* calls of this shape on the current CUDA device (uint8); max_len: max_ctx, or what
-    the page table and max_seq_len hold.  Calls that share it must not overlap on the GPU."""
+    the page table and max_seq_len hold, and with up to 16 query rows a KV head its size grows with that.  Calls that share
+    it must not overlap on the GPU."""
     return _workspace_of("kv_weights_workspace_bytes", batch, q_len, num_q_heads, num_kv_heads, max_len)
 
 

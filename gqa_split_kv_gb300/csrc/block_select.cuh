@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kMeansThreads) block_means_kernel(const __grid
 // worst.  Where the last block taken and the next differ by more than 2 mu, no block can be on
 // the wrong side.  Otherwise those within 2 mu of the border (hardly ever more than two) are
 // computed again, each sum with what its additions round off (to 2^-42 of |q| |mean|: the card
-// has few 64-bit units), and taken in that order.
+// has few 64-bit units), and taken in that order, which compares them pairwise: 512 equal scores take 0.15 ms instead of
+// 8 us, 8192 of them 14 ms instead of 26 us.
 // Latency bounds it: a mean is 1 / block of its keys, but bins, borders and bits are steps of 0.5 to 1 us that follow one
 // another.  16 tokens of 64/8 heads of 128 over up to 512 blocks: 21 us by itself, 11 MB; 500 tokens of 24/4 heads
 // of 256 over 128 blocks: 31.

@@ -100,10 +100,13 @@ bool overlap(const void* a, long long an, const void* b, long long bn) {
 // Launches kern as a programmatic dependent of what precedes it in the stream: its CTAs may
 // start while that drains, so every kernel launched here waits for it (griddepcontrol.wait)
 // before it touches memory that an earlier kernel may write or read, and reads such memory
-// by load_dependent or __ldcg, never through the read-only path.  One read comes before its
-// kernel's wait: latent_combine_kernel's of seq_lens, which its only predecessor,
-// latent_kernel, does not write, and whose writers are done because every CTA of latent_kernel
-// lets it start only after its own wait.
+// by load_dependent or __ldcg, never through the read-only path.  Some touch memory earlier, where their only
+// predecessor lets them start after its own wait (so all kernels before that one are done) and does not write
+// what they read, nor use what they write:
+//   latent_combine_kernel, seg_merge_prefix_kernel  read seq_lens,
+//   weights_finish_kernel  reads lengths, page table and priors,
+//   seg_kernel beside prefix_tc_kernel  reads all of its inputs and writes its own partials; it waits at its end, as
+//     the kernel behind it waits for it alone.
 template <typename P>
 int launch_dependent(void (*kern)(P), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const P& prm) {
   cudaLaunchAttribute attr[1];

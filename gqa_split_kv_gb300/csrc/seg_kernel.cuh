@@ -1,6 +1,7 @@
 // Attention of query rows over lists of cached tokens, for few rows a KV head: the tokens
 // [base, L) of a sequence, the first base tokens that a batch shares, or the blocks that
-// were selected for a query.  The tokens' bytes should bound it, so a CTA reads each key and
+// were selected for a query.  (A unit of a sequence's rows goes along all of its tokens, those that none of its rows sees
+// among them: for new prompts it is slow.)  The tokens' bytes should bound it, so a CTA reads each key and
 // value once for its 8 or 16 rows.
 //
 // The warp-level MMA of this card gives 256 products a cycle and SM (a 16 x 8 x 16 step every

@@ -569,6 +569,9 @@ const char* decode_status_string(int status);
  *  workspace  prefix_attn_workspace_bytes(...) bytes, 16-byte aligned; contents need not be kept, calls that
  *           share one must not overlap on the GPU.  num_sms <= 0: of the current device.
  * Softmax in fp32, the weights rounded to bf16 for the product with V, fp32 sums, one rounding of the output.
+ * Made for few new tokens a sequence: their own tokens are read once for every 8 or 16 query rows, so prompts of more
+ * than about 100 tokens are faster as whole sequences in prefill_attn_* (8 x 128 tokens behind 2048, 32/8 heads of 128:
+ * 107 us against 43; 8 x 64 behind 8192: 91 against 131).
  * What lies past a sequence's end may hold anything, and infinities and NaN, of the prefix too, reach only the rows
  * that see them.
  * Pages outside [0, num_pages) set bit 2 of the device error word and read page 0 instead.  Outputs may not
@@ -608,7 +611,9 @@ int block_means_paged(const void* k_pool, const int* page_table, const int* seq_
  * sequence b, at position p = L_b - q_len + i, sees blocks 0 .. p / block_size.  It takes the first `first` and
  * the last `recent` (>= 1) of them, and of the others those with the largest max over the group's heads of
  * <q, mean>, until it has n_select (>= first + recent) or all.  Scores are compared to 2^-42 of |q| |mean| (ties:
- * the lower block; a head whose score is NaN counts as lowest).
+ * the lower block; a head whose score is NaN counts as lowest).  Blocks whose scores lie within fp32's error of the
+ * last one taken are compared pairwise: a few as a rule, but a cache of many equal means takes long (512 of them 0.15
+ * ms, 8192 14 ms).
  *  q        bf16 [batch, q_len, num_q_heads, head_dim], head_dim 64, 128 or 256
  *  means    as block_means writes them, max_blocks <= 8192; seq_lens is clamped to max_blocks * block_size (NULL:
  *           that length)
@@ -645,7 +650,9 @@ int sparse_attn_paged(const void* q, const void* k_pool, const void* v_pool, con
  *           [num_pages, num_kv_heads, page_size]
  *  prior, out  fp32, laid out like k_scale; prior may be out, or NULL (zeros), and may not overlap it otherwise
  *  workspace  kv_weights_workspace_bytes(...) bytes, 16-byte aligned; max_len: max_ctx, or what the table and
- *           max_seq_len hold
+ *           max_seq_len hold.  With up to 16 rows a KV head (q_len * G) it holds their scores over the whole
+ *           capacity, whatever the lengths: batch * num_kv_heads * max_len * 4 bytes a row (rows rounded up to 4's),
+ *           2.1 GB for 64 sequences of 8 heads and 8 rows that can grow to 131072 tokens.
  * Sequences may not share pages.  A page outside the pool is flagged (bit 2), read as page 0, and not written.
  */
 long long kv_weights_workspace_bytes(int batch, int q_len, int num_q_heads, int num_kv_heads, int max_len, int num_sms);
@@ -707,9 +714,10 @@ int kv_evict_int8_paged(void* k_pool_i8, void* v_pool_i8, float* k_scale_pool, f
  * decode_device_error — synchronise `stream`, then read and clear the device error
  * word of the current device.  *flags receives the word: bit 0 a kernel gave up on
  * a bounded wait, bit 1 a segment-counter update gave up, bit 2 a page-table entry
- * read by a paged attention call (decode_attn_*, prefill_attn_*, latent_attn_*) was outside
- * [0, num_pages) (that box was read from page 0 instead, so the affected rows are wrong but no
- * copy leaves the pool; kv_write_* and kv_read_* skip such rows), bit 3 a token at or
+ * read by a paged attention call (decode_attn_*, prefill_attn_*, latent_attn_*, prefix_attn_*, sparse_attn_*) or by
+ * block_means_* or kv_weights_* was outside [0, num_pages) (those tokens were read from page 0 instead, so the affected
+ * results are wrong but no copy leaves the pool; kv_write_* and kv_read_* skip such rows, kv_weights_* writes nothing
+ * for them, kv_evict_* takes zeros from them and writes none), bit 3 a token at or
  * past the cache's capacity that kv_write_* did not write.  Returns DA_OK when flags == 0, DA_ERR_TIMEOUT otherwise,
  * or DA_ERR_CUDA.
  */
