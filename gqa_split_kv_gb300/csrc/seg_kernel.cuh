@@ -27,9 +27,9 @@
 // have as many tiles: a cluster of 1 to 16 CTAs takes a unit, each CTA its share of the tiles, and
 // joins it through distributed shared memory.
 //
-// Measured: 64 of 64 tokens of 16 sequences, 64/8 heads of 128, pages of 32: 258 MB in 55 us by itself (4.7 TB/s); 16
-// of 64 for each of 500 tokens, 24/4 heads of 256: 2.1 GB through L2 in 200 us, next to 113 of MMAs; the rests of 64
-// sequences behind a prefix (71 MB): 15 us after a start of 4.
+// Measured: 64 of 64 tokens of 16 sequences, 64/8 heads of 128, pages of 32: 258 MB in 52 us by itself (63% of HBM's rate:
+// its loads' latency); 16 of 64 for each of 500 tokens, 24/4 heads of 256: 2.1 GB through L2 in 200 us, next to 113 of MMAs;
+// the rests of 64 sequences behind a prefix (71 MB): 15 us after a start of 4.
 #pragma once
 
 #include <cuda_bf16.h>

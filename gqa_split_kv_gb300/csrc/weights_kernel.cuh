@@ -7,7 +7,7 @@
 //                          sixty-fourth of a 128-wide bf16 key a row) and each piece's (m, l);
 //   weights_finish_kernel  joins a sequence's (m, l), reads the scores, adds the rows' weights
 //                          in their order and writes decay * prior + sum.
-// A key's bytes bound it: what decode reads without the values.  16 x <= 8192 tokens, 32/8 heads of 128 (139 MB): 37.8 us
+// A key's bytes bound it: what decode reads without the values.  16 x <= 8192 tokens, 32/8 heads of 128 (139 MB): 38.0 us
 // for both, 29 of them the first; with the queries as the MMA's rows it was 49.4.
 //
 // more rows (a window of a prompt): weights_tc.cuh, 128 at a time.

@@ -6,8 +6,8 @@
 // The scores are computed twice: writing and reading 128 fp32 a key costs more than its 128 to 512
 // bytes.  2 x 2 D operations a (row, key) on tcgen05 and two exponentials: 32 tokens x 32 heads over
 // 32768 keys are 9 us of operations and 15 of exponentials (warp-level MMAs, at 256 products a
-// cycle and SM, take 58 us a pass); measured, 50.4 for both.  Both operands lie K-major in shared memory, so that the two
-// passes differ in which is A.
+// cycle and SM, take 58 us a pass); measured, 49.4 for both.  Latency bounds them: a CTA has about seven tiles a pass, 3.7 us each,
+// with one tile's loads in flight.  Both operands lie K-major in shared memory, so that the two passes differ in which is A.
 //
 // Warps 0 to 3 bring the keys: they look a tile's tokens up, load them, widen int8, and store
 // them with the swizzle of the products, two tiles of 128 tokens deep; warp 8 issues the products
